@@ -98,16 +98,22 @@ enum {
   SPEC_ROW_BAD_PARENT = 4,      /* tree: parent[0] != -1 or not 0 <= parent[i] < i */
   SPEC_ROW_EMPTY = 5,           /* a logit row that is -inf everywhere */
   SPEC_ROW_TIMEOUT = 6,         /* a bounded on-device wait gave up (see below) */
-  SPEC_ROW_BAD_TEMPERATURE = 7  /* temperature used and not finite and > 0 */
+  SPEC_ROW_BAD_TEMPERATURE = 7, /* temperature used and not finite and > 0 */
+  SPEC_ROW_BAD_SLOT = 8         /* KV cache: a length, start or count outside the row's slots */
 };
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* Logits are SPEC_F32 or SPEC_BF16; the cache and attention calls also use
+ * the other two. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2, SPEC_E4M3 = 3 } spec_dtype;
 typedef enum { SPEC_STOCHASTIC = 0, SPEC_GREEDY = 1 } spec_mode;
 
 /* Limits checked by the entry points. */
 #define SPEC_MAX_K 1023          /* drafts per chain */
 #define SPEC_MAX_TREE_NODES 1024 /* nodes per tree, root included */
 #define SPEC_MAX_V 262144        /* vocabulary size */
+#define SPEC_MAX_HEAD_DIM 128    /* KV cache and attention: head size, a multiple of 16 */
+#define SPEC_MAX_HEADS 1024      /* KV cache and attention: heads per token */
+#define SPEC_MAX_TOP 64          /* spec_token_logprobs: alternatives per position */
 
 /* ------------------------------------------------------------------ chain */
 
@@ -439,6 +445,139 @@ spec_status spec_adaptive_tree_policy(const spec_adaptive_params *params, int32_
                                       const int32_t *accepted_len, const int32_t *depth,
                                       const float *draft_top1, double *ema, int32_t *zero_run,
                                       int32_t *shape, void *stream);
+
+/* ---------------------------------------------- the verify pass's KV cache */
+
+/*
+ * A KV cache: `rows` rows of `slots` token slots in two planes (keys, values).
+ * The entry of (row b, slot s) starts at k (or v) + b*row_stride + s*tok_stride
+ * bytes and is spec_kv_entry_bytes(heads, head_dim, dtype) long:
+ *   SPEC_BF16, SPEC_F16: heads x head_dim numbers, rounded to nearest even;
+ *   SPEC_E4M3: heads x head_dim e4m3 codes, then one scale byte x per head
+ *     (the scale is 2^(x-127); x = 255 stands for NaN), then zeros to a
+ *     multiple of 16 bytes.  A number is its code times its head's scale.
+ * These are the layouts spec_kv_compact_tree moves: with plane 0 the keys and
+ * plane 1 the values, an entry carries its scales along.
+ * k and v must be 16-byte aligned and the strides non-negative multiples of
+ * 16 (else SPEC_ERR_ALIGN), tok_stride at least one entry; entries must not
+ * overlap.  head_dim is a multiple of 16 up to SPEC_MAX_HEAD_DIM, heads is
+ * 1..SPEC_MAX_HEADS, rows <= 65535, slots < 2^31 (else SPEC_ERR_SHAPE).
+ */
+typedef struct {
+  int32_t rows;
+  int32_t heads;       /* KV heads */
+  int32_t head_dim;
+  int32_t dtype;       /* SPEC_BF16, SPEC_F16 or SPEC_E4M3 */
+  int64_t slots;
+  int64_t row_stride;  /* bytes */
+  int64_t tok_stride;  /* bytes */
+  void *k, *v;         /* device */
+} spec_kv_cache;
+
+/* Bytes of one token's entry in one plane; 0 on invalid arguments. */
+size_t spec_kv_entry_bytes(int32_t heads, int32_t head_dim, int32_t dtype);
+
+/*
+ * spec_kv_append -- write the keys and values of newly fed tokens into the
+ * cache ("Speculative Decoding: Draft, Verify, and Correct", 'Verify several
+ * proposed tokens in one target pass': the pass feeds the last token and the
+ * drafts; their entries are kept or rewound afterwards).  Token i of row b goes to slot kv_len[b] + i, the slots
+ * spec_kv_compact_tree and spec_rollback_lengths expect.
+ *
+ * With cache dtype SPEC_E4M3 each head vector x gets the smallest power-of-two
+ * scale s = 2^(c-127), c >= 1, with max|x| / s <= 448, and codes that round
+ * x / s to nearest even; the division is exact, so every stored number is
+ * within 2^-4 relative (2^-10 s absolute below 2^-6 s) of x.  A vector with a
+ * NaN or an infinity gets c = 255 and zero codes: all of it reads back as NaN.
+ *
+ * k, v: [rows, N, heads, head_dim] of src_dtype (SPEC_F32, SPEC_BF16 or
+ * SPEC_F16), with strides in elements for row, token and head and a dense
+ * last dimension; aligned to 16 bytes they are read in 16-byte pieces, else
+ * element by element.  count [rows] (NULL: N for every row) is how many of the
+ * N tokens row b has.  row_status [rows] (optional): SPEC_ROW_BAD_SLOT where
+ * kv_len[b] < 0, count[b] is outside [0, N] or kv_len[b] + count[b] > slots;
+ * such a row is left untouched.  One launch, no workspace.
+ */
+typedef struct {
+  spec_kv_cache cache;
+  int32_t N;               /* tokens per row, >= 0 */
+  int32_t src_dtype;
+  const void *k, *v;       /* device */
+  int64_t k_stride[3];     /* elements: row, token, head */
+  int64_t v_stride[3];
+  const int32_t *kv_len;   /* [rows] device: first slot written */
+  const int32_t *count;    /* [rows] device, or NULL */
+} spec_kv_append_args;
+
+spec_status spec_kv_append(const spec_kv_append_args *args, int32_t *row_status, void *stream);
+
+/*
+ * spec_kv_read -- read cache entries back as dense numbers: k_out, v_out
+ * [rows, T, heads, head_dim] of out_dtype (SPEC_F32, SPEC_BF16 or SPEC_F16;
+ * 16-byte aligned).  Entry t of row b is slot start[b] + t (start NULL: 0) for
+ * t < length[b], and zero from there to T.  Values are exact in fp32, then
+ * rounded once to out_dtype.  row_status [rows] (optional): SPEC_ROW_BAD_SLOT
+ * where start[b] < 0, length[b] is outside [0, T] or start[b] + length[b] >
+ * slots; such a row reads as zeros.  One launch, no workspace.
+ */
+typedef struct {
+  spec_kv_cache cache;
+  int32_t T;
+  int32_t out_dtype;
+  void *k_out, *v_out;     /* device */
+  const int32_t *start;    /* [rows] device, or NULL */
+  const int32_t *length;   /* [rows] device */
+} spec_kv_read_args;
+
+spec_status spec_kv_read(const spec_kv_read_args *args, int32_t *row_status, void *stream);
+
+/*
+ * spec_token_logprobs -- what a serving call reports beside the emitted
+ * tokens: under x = logits / T_b, at every position j of row b with a token
+ * asked for (tokens[b,j] >= 0), in nats,
+ *   logprob = x[token] - lse,  lse = ln sum_v exp(x_v),
+ *   entropy = lse - sum_v p_v x_v  (a -inf logit adds nothing),
+ *   top_ids, top_logprobs: the m tokens of largest logit, ties to the lower
+ *     id, in that order, and their log probabilities.
+ * A position whose token is -1 (spec_verify_chain's filler) is skipped: its
+ * logits are not read, its floats are NaN and its ids -1.  tokens NULL: every
+ * position is computed and logprob is not written.  The laws are the full
+ * temperature-scaled ones, before any truncation.
+ *
+ * logits [B, npos, V], consecutive positions row_stride elements apart
+ * (>= V).  1 <= npos, 0 <= m <= min(V, SPEC_MAX_TOP) (m = 0: the top outputs
+ * may be NULL).  status [B, npos]: SPEC_ROW_* per position (NONFINITE: a NaN
+ * or +inf logit; EMPTY: no finite logit; BAD_TOKEN: outside [-1, V);
+ * BAD_TEMPERATURE); a flagged position's floats are NaN and its ids -1.
+ * B * npos < 2^31 / 64.  Workspace: spec_token_logprobs_workspace_size bytes;
+ * nothing in it is kept between calls.  Two kernels: one pass over the logits
+ * that also keeps the largest of every 32 (bf16) or 16 (fp32) of them, then
+ * one CTA per position.
+ */
+typedef struct {
+  int32_t B, npos, V;
+  int32_t dtype;             /* SPEC_BF16 or SPEC_F32 */
+  int32_t m;
+  int32_t pad;
+  int64_t row_stride;        /* elements between positions */
+  const void *logits;
+  const int32_t *tokens;     /* [B, npos] or NULL */
+  const float *temperature;  /* [B] or NULL = 1 */
+} spec_logprobs_args;
+
+typedef struct {
+  float *logprob;            /* [B, npos] */
+  float *entropy;            /* [B, npos] */
+  int32_t *top_ids;          /* [B, npos, m] */
+  float *top_logprobs;       /* [B, npos, m] */
+  int32_t *status;           /* [B, npos] */
+} spec_logprobs_out;
+
+/* Bytes of workspace (any dtype, any m).  0 on invalid sizes. */
+size_t spec_token_logprobs_workspace_size(int32_t B, int32_t npos, int32_t V);
+
+spec_status spec_token_logprobs(const spec_logprobs_args *args, const spec_logprobs_out *out,
+                                void *ws, size_t ws_bytes, void *stream);
 
 /* Zero-fill a workspace on `stream` (a cudaMemsetAsync).  Optional: the
  * verify calls do not need a zeroed workspace. */

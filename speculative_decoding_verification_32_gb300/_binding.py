@@ -14,10 +14,10 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16, SPEC_E4M3 = 0, 1, 2, 3
 SPEC_STOCHASTIC, SPEC_GREEDY = 0, 1
 ROW_STATUS = {0: "OK", 1: "NONFINITE", 2: "BAD_TOKEN", 3: "BAD_UNIFORM", 4: "BAD_PARENT",
-              5: "EMPTY", 6: "TIMEOUT", 7: "BAD_TEMPERATURE"}
+              5: "EMPTY", 6: "TIMEOUT", 7: "BAD_TEMPERATURE", 8: "BAD_SLOT"}
 
 _c = ctypes
 _P = _c.c_void_p
@@ -61,6 +61,34 @@ class SpecAdaptiveParams(_c.Structure):
     _fields_ = [("alpha", _c.c_double), ("divisor", _c.c_double), ("ema0", _c.c_double),
                 ("shallow", _c.c_int32 * 3), ("deep", _c.c_int32 * 3), ("start", _c.c_int32 * 3),
                 ("breaker", _c.c_int32)]
+
+
+class SpecKvCache(_c.Structure):
+    _fields_ = [("rows", _c.c_int32), ("heads", _c.c_int32), ("head_dim", _c.c_int32),
+                ("dtype", _c.c_int32), ("slots", _c.c_int64), ("row_stride", _c.c_int64),
+                ("tok_stride", _c.c_int64), ("k", _P), ("v", _P)]
+
+
+class SpecKvAppendArgs(_c.Structure):
+    _fields_ = [("cache", SpecKvCache), ("N", _c.c_int32), ("src_dtype", _c.c_int32), ("k", _P),
+                ("v", _P), ("k_stride", _c.c_int64 * 3), ("v_stride", _c.c_int64 * 3),
+                ("kv_len", _P), ("count", _P)]
+
+
+class SpecKvReadArgs(_c.Structure):
+    _fields_ = [("cache", SpecKvCache), ("T", _c.c_int32), ("out_dtype", _c.c_int32),
+                ("k_out", _P), ("v_out", _P), ("start", _P), ("length", _P)]
+
+
+class SpecLogprobsArgs(_c.Structure):
+    _fields_ = [("B", _c.c_int32), ("npos", _c.c_int32), ("V", _c.c_int32), ("dtype", _c.c_int32),
+                ("m", _c.c_int32), ("pad", _c.c_int32), ("row_stride", _c.c_int64),
+                ("logits", _P), ("tokens", _P), ("temperature", _P)]
+
+
+class SpecLogprobsOut(_c.Structure):
+    _fields_ = [("logprob", _P), ("entropy", _P), ("top_ids", _P), ("top_logprobs", _P),
+                ("status", _P)]
 
 
 class SpecError(RuntimeError):
@@ -116,6 +144,17 @@ def _bind(L):
     L.spec_adaptive_tree_policy.restype = _c.c_int
     L.spec_rollback_lengths.argtypes = [i32, i32, _P, _P, _P, _P, i32, _P, _P, _P, _P]
     L.spec_rollback_lengths.restype = _c.c_int
+    L.spec_kv_entry_bytes.argtypes = [i32, i32, i32]
+    L.spec_kv_entry_bytes.restype = sz
+    L.spec_kv_append.argtypes = [_c.POINTER(SpecKvAppendArgs), _P, _P]
+    L.spec_kv_append.restype = _c.c_int
+    L.spec_kv_read.argtypes = [_c.POINTER(SpecKvReadArgs), _P, _P]
+    L.spec_kv_read.restype = _c.c_int
+    L.spec_token_logprobs_workspace_size.argtypes = [i32, i32, i32]
+    L.spec_token_logprobs_workspace_size.restype = sz
+    L.spec_token_logprobs.argtypes = [_c.POINTER(SpecLogprobsArgs), _c.POINTER(SpecLogprobsOut),
+                                      _P, sz, _P]
+    L.spec_token_logprobs.restype = _c.c_int
     L.spec_workspace_init.argtypes = [_P, sz, _P]
     L.spec_workspace_init.restype = _c.c_int
     L.spec_status_string.argtypes = [_c.c_int]
@@ -363,6 +402,198 @@ def spec_adaptive_tree_policy(accepted_len, depth, draft_top1, ema, zero_run, al
                                            _ptr(draft_top1), _ptr(ema), _ptr(zero_run),
                                            _ptr(shape), sp))
     return shape
+
+
+class _On:
+    """The stream of one call of the cache, attention and log-probability
+    operators.  With an explicit stream, tensors made inside `with` come from
+    that stream's pool, and use() tells the allocator that the stream reads
+    or writes tensors of another's, so none is handed out again too early.
+    scratch() is a workspace of these calls' own: the verify calls keep a
+    header and stamped records in theirs."""
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.given = stream
+        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
+        self.ptr = _P(self.stream.cuda_stream)
+        self._ctx = None
+
+    def __enter__(self):
+        if self.given is not None:
+            self._ctx = torch.cuda.stream(self.given)
+            self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+    def use(self, *tensors):
+        if self.given is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+    def scratch(self, nbytes):
+        return workspace(self.device, nbytes, ("scratch", self.stream.cuda_stream))
+
+
+_KV_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+
+
+def _kv_dtype(dtype, name):
+    if dtype not in _KV_DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return _KV_DTYPES[dtype]
+
+
+def spec_kv_entry_bytes(heads, head_dim, dtype=torch.uint8):
+    """Bytes of one token's entry in one plane of a cache (see spec_kv_cache in
+    include/specverify.h): dtype torch.uint8 (e4m3 codes and scale bytes),
+    torch.bfloat16 or torch.float16."""
+    code = SPEC_E4M3 if dtype == torch.uint8 else _kv_dtype(dtype, "dtype")
+    n = lib().spec_kv_entry_bytes(int(heads), int(head_dim), code)
+    if n == 0:
+        raise ValueError(f"no cache entry of {heads} heads of {head_dim} in {dtype}")
+    return n
+
+
+def _kv_cache(cache, heads, head_dim, dev, name):
+    """The C descriptor of a cache tensor: [2, rows, slots, heads, head_dim]
+    bfloat16 / float16, or [2, rows, slots, entry bytes] uint8 (e4m3)."""
+    if not isinstance(cache, torch.Tensor) or cache.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    e4m3 = cache.dtype == torch.uint8
+    if not e4m3 and cache.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be bfloat16, float16 or uint8 (e4m3 entries), got {cache.dtype}")
+    entry = spec_kv_entry_bytes(heads, head_dim, cache.dtype)
+    want = (entry,) if e4m3 else (heads, head_dim)
+    if cache.dim() != 3 + len(want) or cache.shape[0] != 2 or tuple(cache.shape[3:]) != want:
+        raise ValueError(f"{name} must be [2, rows, slots, {', '.join(map(str, want))}], "
+                         f"got {tuple(cache.shape)}")
+    if any(cache.stride(3 + i) != s and cache.shape[3 + i] != 1
+           for i, s in enumerate((1,) if e4m3 else (head_dim, 1))):
+        raise ValueError(f"{name}: one token's entry must be contiguous")
+    e = cache.element_size()
+    return SpecKvCache(cache.shape[1], heads, head_dim,
+                       SPEC_E4M3 if e4m3 else _kv_dtype(cache.dtype, name), cache.shape[2],
+                       cache.stride(1) * e, cache.stride(2) * e, _P(cache.data_ptr()),
+                       _P(cache.data_ptr() + cache.stride(0) * e))
+
+
+def _rows_i32(t, name, dev, n):
+    _req(t, name, dev, torch.int32)
+    if t is not None and tuple(t.shape) != (n,):
+        raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+    return t
+
+
+def spec_kv_append(cache, k, v, kv_len, count=None, stream=None):
+    """Write the keys and values of newly fed tokens into the KV cache (see
+    spec_kv_append in include/specverify.h): token i of row b goes to slot
+    kv_len[b] + i.
+
+    cache [2, B, S, heads, D] (bfloat16 / float16) or [2, B, S, entry bytes]
+    uint8 (e4m3 codes and power-of-two scales); k, v [B, N, heads, D]
+    (float32, bfloat16 or float16, any strides with a dense last dimension);
+    kv_len [B] int32; count [B] int32 or None (all N tokens).  Returns
+    row_status [B] int32.
+    """
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a [B, N, heads, head_dim] tensor")
+    dev = k.device
+    if not isinstance(v, torch.Tensor) or v.device != dev or v.shape != k.shape:
+        raise ValueError(f"v must be a tensor like k, on {dev}")
+    if v.dtype != k.dtype:
+        raise TypeError(f"v must be {k.dtype}, got {v.dtype}")
+    B, N, heads, D = k.shape
+    for t, n in ((k, "k"), (v, "v")):
+        if t.stride(3) != 1 and D > 1:
+            raise ValueError(f"{n}: the last dimension must be dense")
+    c = _kv_cache(cache, heads, D, dev, "cache")
+    if c.rows != B:
+        raise ValueError(f"cache has {c.rows} rows, k has {B}")
+    _rows_i32(kv_len, "kv_len", dev, B)
+    _rows_i32(count, "count", dev, B)
+    i64x3 = _c.c_int64 * 3
+    a = SpecKvAppendArgs(c, N, _kv_dtype(k.dtype, "k"), _ptr(k), _ptr(v), i64x3(*k.stride()[:3]),
+                         i64x3(*v.stride()[:3]), _ptr(kv_len), _ptr(count))
+    with _On(dev, stream) as on:
+        on.use(cache, k, v, kv_len, count)
+        status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
+        _check(lib().spec_kv_append(_c.byref(a), _ptr(status), on.ptr))
+    return status
+
+
+def spec_kv_read(cache, length, T, heads=None, head_dim=None, start=None, dtype=torch.bfloat16,
+                 stream=None):
+    """Read cache entries back as dense numbers (see spec_kv_read in
+    include/specverify.h): entry t < length[b] of row b is slot start[b] + t
+    (start None: 0); zeros from there to T.  heads and head_dim are needed for
+    a uint8 (e4m3) cache.  Returns (k [B, T, heads, D], v, row_status [B])."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() < 4:
+        raise ValueError("cache must be a [2, rows, slots, ...] tensor")
+    dev = cache.device
+    if cache.dtype != torch.uint8:
+        heads, head_dim = cache.shape[3:5] if cache.dim() == 5 else (heads, head_dim)
+    if heads is None or head_dim is None:
+        raise ValueError("heads and head_dim are needed for a uint8 cache")
+    c = _kv_cache(cache, int(heads), int(head_dim), dev, "cache")
+    B = c.rows
+    _rows_i32(length, "length", dev, B)
+    _rows_i32(start, "start", dev, B)
+    code = _kv_dtype(dtype, "dtype")
+    with _On(dev, stream) as on:
+        on.use(cache, length, start)
+        k = torch.empty(B, T, heads, head_dim, dtype=dtype, device=dev)
+        v = torch.empty_like(k)
+        status = (torch.empty if T else torch.zeros)(B, dtype=torch.int32, device=dev)
+        a = SpecKvReadArgs(c, int(T), code, _ptr(k), _ptr(v), _ptr(start), _ptr(length))
+        _check(lib().spec_kv_read(_c.byref(a), _ptr(status), on.ptr))
+    return k, v, status
+
+
+def spec_token_logprobs(logits, tokens=None, temperature=None, m=0, stream=None):
+    """Log probabilities of given tokens, entropy and the top m alternatives
+    (see spec_token_logprobs in include/specverify.h).
+
+    logits [B, npos, V] (bfloat16 or float32; positions may be spaced wider
+    than V); tokens [B, npos] int32 (-1: skip the position) or None (no given
+    tokens); temperature [B] float32 or None.  Returns a dict: logprob and
+    entropy [B, npos] float32 (logprob only with tokens), top_ids [B, npos, m]
+    int32, top_logprobs [B, npos, m] float32, status [B, npos] int32.
+    """
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+        raise ValueError("logits must be a [B, npos, V] tensor")
+    dev = logits.device
+    B, npos, V = logits.shape
+    dt = _dtype_code(logits)
+    pitch = logits.stride(1) if npos > 1 else logits.stride(0) if B > 1 else V
+    if (V > 1 and logits.stride(2) != 1) or (B > 1 and logits.stride(0) != npos * pitch):
+        raise ValueError("logits: positions must be evenly spaced with a dense last dimension")
+    _req(tokens, "tokens", dev, torch.int32)
+    if tokens is not None and tuple(tokens.shape) != (B, npos):
+        raise ValueError(f"tokens must be [{B}, {npos}], got {tuple(tokens.shape)}")
+    _req(temperature, "temperature", dev, torch.float32)
+    if temperature is not None and tuple(temperature.shape) != (B,):
+        raise ValueError(f"temperature must be [{B}], got {tuple(temperature.shape)}")
+    L = lib()
+    with _On(dev, stream) as on:
+        on.use(logits, tokens, temperature)
+        out = dict(entropy=torch.empty(B, npos, dtype=torch.float32, device=dev),
+                   status=torch.empty(B, npos, dtype=torch.int32, device=dev),
+                   top_ids=torch.empty(B, npos, m, dtype=torch.int32, device=dev),
+                   top_logprobs=torch.empty(B, npos, m, dtype=torch.float32, device=dev))
+        if tokens is not None:
+            out["logprob"] = torch.empty(B, npos, dtype=torch.float32, device=dev)
+        a = SpecLogprobsArgs(B, npos, V, dt, int(m), 0, pitch, _ptr(logits), _ptr(tokens),
+                             _ptr(temperature))
+        o = SpecLogprobsOut(_ptr(out.get("logprob")), _ptr(out["entropy"]), _ptr(out["top_ids"]),
+                            _ptr(out["top_logprobs"]), _ptr(out["status"]))
+        ws = on.scratch(L.spec_token_logprobs_workspace_size(B, npos, V))
+        _check(L.spec_token_logprobs(_c.byref(a), _c.byref(o), _ptr(ws), ws.numel(), on.ptr))
+    return out
 
 
 def set_wait_timeout_ns(ns):

@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libspecverify.so")
 VARIANTS = {None: (BUILD, LIB, []),
             "bounds": (os.path.join(HERE, "_build_bounds"),
                        os.path.join(HERE, "libspecverify_bounds.so"), ["-DSV_BOUNDS"])}
-SOURCES = ["api.cu", "chain_stochastic.cu", "greedy.cu", "rollback.cu", "kv_policy.cu"]
+SOURCES = ["api.cu", "chain_stochastic.cu", "greedy.cu", "rollback.cu", "kv_policy.cu",
+           "kv_cache.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

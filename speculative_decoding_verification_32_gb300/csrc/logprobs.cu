@@ -1,0 +1,418 @@
+// logprobs.cu -- log probabilities of given tokens, entropy and the top
+// alternatives (spec_token_logprobs).
+//
+// With y_v = (l_v - M) log2(e) / T, M the largest logit, S = sum 2^y_v and
+// U = sum y_v 2^y_v:
+//   log p(v) = ln 2 (y_v - log2 S),   entropy = ln 2 (log2 S - U / S).
+// (max, S, U) of two parts join by shifting to the larger max, so one pass
+// over the logits is enough; its HBM read is what bounds the call.
+//
+//  logprobs_stream_kernel -- one CTA per slice of 256 x 4 16-byte vectors of a
+//    position: every thread loads its four vectors at once (64 KB in flight
+//    on an SM at 4 CTAs), takes the largest of its 32 bf16 or 16 fp32 logits,
+//    its own S and U against that, and the CTA joins the threads'.  The
+//    thread maxima are kept as 16-bit order keys (1/32 of the bf16 traffic):
+//  logprobs_pick_kernel -- one CTA per position joins the slices' records and
+//    finds the top m without reading the logits again: the m-th largest of
+//    the chunk keys is a lower bound of the m-th largest logit's key, so only
+//    the few chunks that reach it are looked at.  Positions where that leaves
+//    too many (masses of equal logits) are searched whole.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "specverify.h"
+
+namespace sv {
+namespace {
+
+constexpr int kLpThreads = 256;
+constexpr int kLpVecs = 4;  // 16-byte vectors per thread
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.442695040888963407f;
+// 2^-200 is zero in fp32: stands in for the y of a masked logit, so that y 2^y is 0 and not NaN
+constexpr float kFloorY = -200.f;
+constexpr int kLpChunks = 1024;  // candidate chunks the pick kernel lists
+constexpr int kLpCands = 1024;   // candidate logits it ranks
+
+struct LpPart {
+  float m, s, u;
+  uint32_t flags;
+};
+
+struct LpParams {
+  const void *logits;
+  const int32_t *tokens;
+  const float *temperature;
+  float *logprob, *entropy, *top_logprobs;
+  int32_t *top_ids, *status;
+  LpPart *part;          // [rows * nslices]
+  unsigned short *cmax;  // [rows * nslices * kLpThreads]
+  long long row_stride;
+  int rows, npos, V, m, slice, nslices;
+};
+
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);  // -0 counts as +0
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float from_key(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float logit_at(const void *row, int v) {
+  if (BF16) return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const unsigned short *>(row) + v)) << 16);
+  return __ldg(static_cast<const float *>(row) + v);
+}
+
+// (m, s, u) <- (m, s, u) joined with (m2, s2, u2); sc = log2(e) / T
+__device__ __forceinline__ void join(float &m, float &s, float &u, float m2, float s2, float u2, float sc) {
+  const float M = fmaxf(m, m2);
+  if (M == -INFINITY) return;
+  const float d1 = fmaxf((m - M) * sc, kFloorY), d2 = fmaxf((m2 - M) * sc, kFloorY);
+  const float f1 = ex2(d1), f2 = ex2(d2);
+  u = f1 * (u + d1 * s) + f2 * (u2 + d2 * s2);
+  s = f1 * s + f2 * s2;
+  m = M;
+}
+
+__device__ __forceinline__ float row_scale(const LpParams &P, int r, uint32_t &flags) {
+  const float T = P.temperature ? __ldg(P.temperature + r / P.npos) : 1.f;
+  if (!(T > 0.f) || isinf(T)) {
+    flags |= F_BAD_TEMPERATURE;
+    return 1.f;
+  }
+  return kLog2e / T;
+}
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kLpThreads) logprobs_stream_kernel(const __grid_constant__ LpParams P) {
+  constexpr int E = BF16 ? 8 : 4;
+  const int r = blockIdx.y * 32768 + blockIdx.z, sl = blockIdx.x, tid = threadIdx.x;
+  if (r >= P.rows) return;
+  if (P.tokens && __ldg(P.tokens + r) == -1) return;
+  uint32_t flags = 0;
+  const float sc = row_scale(P, r, flags);
+  const size_t esz = BF16 ? 2 : 4;
+  const char *row = static_cast<const char *>(P.logits) + static_cast<size_t>(r) * P.row_stride * esz;
+  const int v0 = sl * P.slice;
+  float x[kLpVecs * E];
+  if constexpr (VEC) {
+    const uint64_t pol = l2_policy_evict_first();
+    uint4 w[kLpVecs];
+#pragma unroll
+    for (int i = 0; i < kLpVecs; ++i) {
+      const int v = v0 + (i * kLpThreads + tid) * E;
+      // V is a multiple of E here: a vector is inside or outside as a whole
+      w[i] = BF16 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
+                  : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+      if (v < P.V) w[i] = ld_stream_u4(row + static_cast<size_t>(v) * esz, pol);
+    }
+#pragma unroll
+    for (int i = 0; i < kLpVecs; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (BF16) {
+          x[i * E + 2 * j] = bf16_lo(u[j]);
+          x[i * E + 2 * j + 1] = bf16_hi(u[j]);
+        } else {
+          x[i * E + j] = __uint_as_float(u[j]);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kLpVecs; ++i)
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int v = v0 + (i * kLpThreads + tid) * E + j;
+        x[i * E + j] = v < P.V ? logit_at<BF16>(row, v) : -INFINITY;
+      }
+  }
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < kLpVecs * E; ++i) m = fmax_nan(m, x[i]);
+  if (!(m < INFINITY)) flags |= F_NONFINITE;  // NaN or +inf
+  float s = 0.f, u = 0.f;
+  if (m > -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < kLpVecs * E; ++i) {
+      const float y = fmaxf((x[i] - m) * sc, kFloorY);
+      const float e = ex2(y);
+      s += e;
+      u = fmaf(y, e, u);
+    }
+  }
+  const size_t item = static_cast<size_t>(r) * P.nslices + sl;
+  if (P.m > 0) P.cmax[item * kLpThreads + tid] = static_cast<unsigned short>(order_key(m) >> 16);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    join(m, s, u, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, s, o),
+         __shfl_xor_sync(FULL_MASK, u, o), sc);
+  flags = __reduce_or_sync(FULL_MASK, flags);
+  __shared__ LpPart sh[kLpThreads / 32];
+  if (tid % 32 == 0) sh[tid / 32] = LpPart{m, s, u, flags};
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kLpThreads / 32; ++w) {
+      join(m, s, u, sh[w].m, sh[w].s, sh[w].u, sc);
+      flags |= sh[w].flags;
+    }
+    P.part[item] = LpPart{m, s, u, flags};
+  }
+}
+
+// Sum over the CTA of one int per thread (all threads get it).
+__device__ __forceinline__ int block_sum(int v, int *sh) {
+  v = __reduce_add_sync(FULL_MASK, v);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
+  __syncthreads();
+  int t = 0;
+#pragma unroll
+  for (int w = 0; w < kLpThreads / 32; ++w) t += sh[w];
+  return t;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_constant__ LpParams P) {
+  constexpr int E = BF16 ? 8 : 4;
+  constexpr int kChunk = kLpVecs * E;
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  __shared__ LpPart sh[kLpThreads / 32];
+  __shared__ int red[kLpThreads / 32];
+  __shared__ int n_chunks, n_cands;
+  __shared__ int chunk[kLpChunks];
+  __shared__ unsigned long long cand[kLpCands];
+  const int tok = P.tokens ? __ldg(P.tokens + r) : -1;
+  const bool skip = P.tokens && tok == -1;
+  uint32_t flags = 0;
+  const float sc = row_scale(P, r, flags);
+  if (P.tokens && (tok < -1 || tok >= P.V)) flags |= F_BAD_TOKEN;
+  const size_t esz = BF16 ? 2 : 4;
+  const char *row = static_cast<const char *>(P.logits) + static_cast<size_t>(r) * P.row_stride * esz;
+  float xt = 0.f;  // the given token's logit
+  if (tok >= 0 && tok < P.V) xt = logit_at<BF16>(row, tok);
+  if (tid == 0) n_chunks = n_cands = 0;
+  grid_dependency_wait();
+  if (skip) {
+    for (int i = tid; i < P.m; i += kLpThreads) {
+      P.top_ids[static_cast<size_t>(r) * P.m + i] = -1;
+      P.top_logprobs[static_cast<size_t>(r) * P.m + i] = NAN;
+    }
+    if (tid == 0) {
+      P.logprob[r] = NAN;
+      P.entropy[r] = NAN;
+      P.status[r] = 0;
+    }
+    return;
+  }
+  // the slices' records
+  float m = -INFINITY, s = 0.f, u = 0.f;
+  for (int i = tid; i < P.nslices; i += kLpThreads) {
+    const LpPart p = P.part[static_cast<size_t>(r) * P.nslices + i];
+    join(m, s, u, p.m, p.s, p.u, sc);
+    flags |= p.flags;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    join(m, s, u, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, s, o),
+         __shfl_xor_sync(FULL_MASK, u, o), sc);
+  flags = __reduce_or_sync(FULL_MASK, flags);
+  if (lane == 0) sh[warp] = LpPart{m, s, u, flags};
+  __syncthreads();
+  m = sh[0].m, s = sh[0].s, u = sh[0].u, flags = sh[0].flags;
+  for (int w = 1; w < kLpThreads / 32; ++w) {
+    join(m, s, u, sh[w].m, sh[w].s, sh[w].u, sc);
+    flags |= sh[w].flags;
+  }
+  if (m == -INFINITY && !(flags & F_NONFINITE)) flags |= F_EMPTY;
+  const float lgs = log2f(s);
+  const bool bad = flags != 0;
+  if (tid == 0) {
+    if (P.tokens) P.logprob[r] = bad ? NAN : kLn2 * ((xt - m) * sc - lgs);
+    P.entropy[r] = bad ? NAN : fmaxf(0.f, kLn2 * (lgs - u / s));
+    P.status[r] = lowest_code(flags);
+  }
+  if (P.m == 0) return;
+  int32_t *ids = P.top_ids + static_cast<size_t>(r) * P.m;
+  float *lps = P.top_logprobs + static_cast<size_t>(r) * P.m;
+  if (bad) {
+    for (int i = tid; i < P.m; i += kLpThreads) {
+      ids[i] = -1;
+      lps[i] = NAN;
+    }
+    return;
+  }
+  // The chunk keys' m-th largest: bit by bit, the largest t that at least m
+  // keys reach.  If the position has fewer than m chunks, t = 0: every
+  // chunk is looked at.
+  const int nkeys = P.nslices * kLpThreads;
+  const unsigned short *ck = P.cmax + static_cast<size_t>(r) * nkeys;
+  unsigned t16 = 0;
+  for (int bit = 15; bit >= 0; --bit) {
+    const unsigned t = t16 | (1u << bit);
+    int c = 0;
+    for (int i = tid; i < nkeys; i += kLpThreads) c += ck[i] >= t;
+    if (block_sum(c, red) >= P.m) t16 = t;
+  }
+  for (int i = tid; i < nkeys; i += kLpThreads)
+    if (ck[i] >= t16) {
+      const int at = atomicAdd(&n_chunks, 1);
+      if (at < kLpChunks) chunk[at] = i;
+    }
+  __syncthreads();
+  const int nc = n_chunks;
+  if (nc <= kLpChunks) {
+    for (int i = tid; i < nc * kChunk; i += kLpThreads) {
+      const int c = chunk[i / kChunk], e = i % kChunk;
+      const int v = (c / kLpThreads) * P.slice + ((e / E) * kLpThreads + c % kLpThreads) * E + e % E;
+      if (v >= P.V) continue;
+      const uint32_t k = order_key(logit_at<BF16>(row, v));
+      if ((k >> 16) < t16) continue;
+      const int at = atomicAdd(&n_cands, 1);
+      if (at < kLpCands) cand[at] = static_cast<unsigned long long>(k) << 32 | (0xffffffffu - v);
+    }
+  }
+  __syncthreads();
+  int n = n_cands;
+  if (nc > kLpChunks || n > kLpCands) {
+    // Whole-position search: the m-th largest key exactly, bit by bit, then
+    // everything above it (fewer than m) and the first of the equal ones.
+    uint32_t t = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t tt = t | (1u << bit);
+      int c = 0;
+      for (int v = tid; v < P.V; v += kLpThreads) c += order_key(logit_at<BF16>(row, v)) >= tt;
+      if (block_sum(c, red) >= P.m) t = tt;
+    }
+    if (tid == 0) n_cands = 0;
+    __syncthreads();
+    for (int v = tid; v < P.V; v += kLpThreads) {
+      const uint32_t k = order_key(logit_at<BF16>(row, v));
+      if (k > t) cand[atomicAdd(&n_cands, 1)] = static_cast<unsigned long long>(k) << 32 | (0xffffffffu - v);
+    }
+    __syncthreads();
+    const int above = n_cands;
+    int have = above;  // the same in every thread
+    for (int v0 = 0; v0 < P.V && have < P.m; v0 += kLpThreads) {
+      const int v = v0 + tid;
+      const bool hit = v < P.V && order_key(logit_at<BF16>(row, v)) == t;
+      const unsigned ball = __ballot_sync(FULL_MASK, hit);
+      __syncthreads();
+      if (lane == 0) red[warp] = __popc(ball);
+      __syncthreads();
+      int at = have, all = 0;
+      for (int w = 0; w < kLpThreads / 32; ++w) {
+        if (w < warp) at += red[w];
+        all += red[w];
+      }
+      at += __popc(ball & ((1u << lane) - 1));
+      if (hit && at < P.m) cand[at] = static_cast<unsigned long long>(t) << 32 | (0xffffffffu - v);
+      have += all;
+    }
+    __syncthreads();
+    n = min(have, P.m);
+  }
+  // rank by counting: keys are unique (the id is part of them)
+  for (int i = tid; i < n; i += kLpThreads) {
+    const unsigned long long k = cand[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += cand[j] > k;
+    if (rank < P.m) {
+      ids[rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k));
+      lps[rank] = kLn2 * ((from_key(static_cast<uint32_t>(k >> 32)) - m) * sc - lgs);
+    }
+  }
+}
+
+int lp_slice(bool bf16) { return kLpThreads * kLpVecs * (bf16 ? 8 : 4); }
+size_t lp_round(size_t x) { return (x + 255) / 256 * 256; }
+bool lp_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+bool lp_sizes(int32_t B, int32_t npos, int32_t V) {
+  return B >= 0 && npos >= 1 && V >= 1 && V <= SPEC_MAX_V && static_cast<long long>(B) * npos < 0x7fffffffLL / 64;
+}
+
+template <bool BF16>
+cudaError_t launch_logprobs(const LpParams &p, bool vec, cudaStream_t s) {
+  // rows over y and z (65535 at most in each)
+  const dim3 grid(p.nslices, (p.rows + 32767) / 32768, p.rows < 32768 ? p.rows : 32768);
+  if (vec)
+    logprobs_stream_kernel<BF16, true><<<grid, kLpThreads, 0, s>>>(p);
+  else
+    logprobs_stream_kernel<BF16, false><<<grid, kLpThreads, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.rows);
+  cfg.blockDim = dim3(kLpThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, logprobs_pick_kernel<BF16>, p);
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+size_t spec_token_logprobs_workspace_size(int32_t B, int32_t npos, int32_t V) {
+  if (!lp_sizes(B, npos, V)) return 0;
+  const size_t items = static_cast<size_t>(B) * npos * ((V + lp_slice(false) - 1) / lp_slice(false));
+  return lp_round(items * sizeof(LpPart)) + lp_round(items * kLpThreads * 2) + 256;
+}
+
+spec_status spec_token_logprobs(const spec_logprobs_args *a, const spec_logprobs_out *o, void *ws,
+                                size_t ws_bytes, void *stream) {
+  if (!a || !o) return SPEC_ERR_NULL;
+  if (!lp_sizes(a->B, a->npos, a->V)) return SPEC_ERR_SHAPE;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
+  if (a->m < 0 || a->m > SPEC_MAX_TOP || a->m > a->V || a->row_stride < a->V) return SPEC_ERR_ARG;
+  if (a->B == 0) return SPEC_OK;
+  if (!a->logits || !o->entropy || !o->status || (a->tokens && !o->logprob) ||
+      (a->m > 0 && (!o->top_ids || !o->top_logprobs)))
+    return SPEC_ERR_NULL;
+  const bool bf16 = a->dtype == SPEC_BF16;
+  const int esz = bf16 ? 2 : 4;
+  if (!lp_aligned(a->logits, esz)) return SPEC_ERR_ALIGN;
+  const void *w4[] = {a->tokens, a->temperature, o->logprob, o->entropy, o->top_ids, o->top_logprobs, o->status};
+  for (const void *q : w4)
+    if (!lp_aligned(q, 4)) return SPEC_ERR_ALIGN;
+  if (!ws || !lp_aligned(ws, 256) || ws_bytes < spec_token_logprobs_workspace_size(a->B, a->npos, a->V))
+    return SPEC_ERR_WORKSPACE;
+  LpParams p = {};
+  p.logits = a->logits;
+  p.tokens = a->tokens;
+  p.temperature = a->temperature;
+  p.logprob = o->logprob;
+  p.entropy = o->entropy;
+  p.top_ids = o->top_ids;
+  p.top_logprobs = o->top_logprobs;
+  p.status = o->status;
+  p.row_stride = a->row_stride;
+  p.rows = a->B * a->npos;
+  p.npos = a->npos;
+  p.V = a->V;
+  p.m = a->m;
+  p.slice = lp_slice(bf16);
+  p.nslices = (a->V + p.slice - 1) / p.slice;
+  p.part = static_cast<LpPart *>(ws);
+  p.cmax = reinterpret_cast<unsigned short *>(static_cast<char *>(ws) +
+                                              lp_round(static_cast<size_t>(p.rows) * p.nslices * sizeof(LpPart)));
+  const bool vec = lp_aligned(a->logits, 16) && (a->row_stride * esz) % 16 == 0 && (static_cast<long long>(a->V) * esz) % 16 == 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = bf16 ? launch_logprobs<true>(p, vec, s) : launch_logprobs<false>(p, vec, s);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // extern "C"
