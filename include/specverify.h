@@ -532,6 +532,67 @@ typedef struct {
 spec_status spec_kv_read(const spec_kv_read_args *args, int32_t *row_status, void *stream);
 
 /*
+ * spec_prefix_attention -- the verify pass's attention ("Speculative Decoding:
+ * Draft, Verify, and Correct", 'Verify several proposed tokens in one target
+ * pass'; "Speculative Decoding: How a Small Model Speeds Up a Big One",
+ * 'Beyond Two Models: The EAGLE Line': a draft tree in one pass under a tree
+ * mask) for rows that share a long prefix, whose keys and values are stored
+ * and read once for all of them.
+ *
+ * Query i of row b (i < count[b], count NULL: N) is the token whose entry
+ * spec_kv_append wrote at slot kv_len[b] + i.  Its head h reads KV head
+ * g = h / (q_heads / heads) and sees
+ *   - prefix entries 0 .. prefix_len - 1 (row 0 of `prefix`),
+ *   - its row's slots 0 .. kv_len[b] - 1,
+ *   - of the pass's own tokens, slots kv_len[b] + j: j <= i for a chain
+ *     (parent NULL), or node i and its ancestors for a tree (parent [rows, N]
+ *     as in spec_verify_tree: parent[b,0] = -1, 0 <= parent[b,i] < i).
+ * Over the keys it sees, x_t = scale * q . k_t, and
+ *   out = sum_t softmax(x)_t v_t,   lse = ln sum_t exp(x_t).
+ * Nothing else is read into the result: slots past the row's last token and
+ * tokens a query does not see may hold anything, NaN included.
+ *
+ * q: [rows, N, q_heads, head_dim] of q_dtype (SPEC_BF16 or SPEC_F16) with
+ * strides in elements for row, token and head and a dense last dimension;
+ * q_heads is a multiple of cache.heads.  The cache has q_dtype or SPEC_E4M3;
+ * `prefix` has the cache's heads, head_dim and dtype, at least one row and
+ * prefix_len slots (prefix_len 0: `prefix` is ignored).  out [rows, N,
+ * q_heads, head_dim] of q_dtype and lse [rows, N, q_heads] fp32 (optional) are
+ * dense, 16-byte aligned.  N <= SPEC_MAX_TREE_NODES,
+ * rows * N * q_heads < 2^31 / 256.
+ *
+ * row_status [rows] (optional): SPEC_ROW_BAD_SLOT (kv_len[b] < 0, count[b]
+ * outside [0, N], kv_len[b] + count[b] > slots) or SPEC_ROW_BAD_PARENT; such a
+ * row, and a query i >= count[b], gets zeros and lse = -inf.
+ *
+ * Sums, maxima and softmax statistics are fp32; the softmax weights are
+ * rounded once to the cache's 16-bit type (fp16 for SPEC_E4M3) for the product
+ * with v.  Results do not depend on timing: every sum has a fixed order.
+ * Workspace: spec_prefix_attention_workspace_size(args) bytes, no contents
+ * kept between calls.
+ */
+typedef struct {
+  spec_kv_cache cache;     /* the rows' own entries */
+  spec_kv_cache prefix;    /* the shared entries (row 0) */
+  int64_t prefix_len;
+  int32_t N;               /* queries per row */
+  int32_t q_heads;
+  int32_t q_dtype;
+  float scale;             /* finite */
+  const void *q;
+  int64_t q_stride[3];     /* elements: row, token, head */
+  const int32_t *kv_len;   /* [rows] device: own entries before this pass */
+  const int32_t *count;    /* [rows] device, or NULL */
+  const int32_t *parent;   /* [rows, N] device, or NULL (a chain) */
+} spec_attention_args;
+
+/* Bytes of workspace; 0 on invalid sizes or types (pointers are not looked at). */
+size_t spec_prefix_attention_workspace_size(const spec_attention_args *args);
+
+spec_status spec_prefix_attention(const spec_attention_args *args, void *out, float *lse,
+                                  int32_t *row_status, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * spec_token_logprobs -- what a serving call reports beside the emitted
  * tokens: under x = logits / T_b, at every position j of row b with a token
  * asked for (tokens[b,j] >= 0), in nats,

@@ -7,5 +7,5 @@ from ._binding import (ROW_STATUS, SPEC_BF16, SPEC_E4M3, SPEC_F16, SPEC_F32,  # 
                        SPEC_GREEDY, SPEC_STOCHASTIC, SpecError, debug_force_wait_timeout,
                        get_wait_timeout_ns, lib, set_wait_timeout_ns, spec_adaptive_tree_policy,
                        spec_drift_residuals, spec_kv_append, spec_kv_compact_tree,
-                       spec_kv_entry_bytes, spec_kv_read, spec_rollback_lengths,
-                       spec_token_logprobs, spec_verify_chain, spec_verify_tree)
+                       spec_kv_entry_bytes, spec_kv_read, spec_prefix_attention,
+                       spec_rollback_lengths, spec_token_logprobs, spec_verify_chain, spec_verify_tree)

@@ -80,6 +80,13 @@ class SpecKvReadArgs(_c.Structure):
                 ("k_out", _P), ("v_out", _P), ("start", _P), ("length", _P)]
 
 
+class SpecAttentionArgs(_c.Structure):
+    _fields_ = [("cache", SpecKvCache), ("prefix", SpecKvCache), ("prefix_len", _c.c_int64),
+                ("N", _c.c_int32), ("q_heads", _c.c_int32), ("q_dtype", _c.c_int32),
+                ("scale", _c.c_float), ("q", _P), ("q_stride", _c.c_int64 * 3),
+                ("kv_len", _P), ("count", _P), ("parent", _P)]
+
+
 class SpecLogprobsArgs(_c.Structure):
     _fields_ = [("B", _c.c_int32), ("npos", _c.c_int32), ("V", _c.c_int32), ("dtype", _c.c_int32),
                 ("m", _c.c_int32), ("pad", _c.c_int32), ("row_stride", _c.c_int64),
@@ -150,6 +157,10 @@ def _bind(L):
     L.spec_kv_append.restype = _c.c_int
     L.spec_kv_read.argtypes = [_c.POINTER(SpecKvReadArgs), _P, _P]
     L.spec_kv_read.restype = _c.c_int
+    L.spec_prefix_attention_workspace_size.argtypes = [_c.POINTER(SpecAttentionArgs)]
+    L.spec_prefix_attention_workspace_size.restype = sz
+    L.spec_prefix_attention.argtypes = [_c.POINTER(SpecAttentionArgs), _P, _P, _P, _P, sz, _P]
+    L.spec_prefix_attention.restype = _c.c_int
     L.spec_token_logprobs_workspace_size.argtypes = [i32, i32, i32]
     L.spec_token_logprobs_workspace_size.restype = sz
     L.spec_token_logprobs.argtypes = [_c.POINTER(SpecLogprobsArgs), _c.POINTER(SpecLogprobsOut),
@@ -552,6 +563,62 @@ def spec_kv_read(cache, length, T, heads=None, head_dim=None, start=None, dtype=
         a = SpecKvReadArgs(c, int(T), code, _ptr(k), _ptr(v), _ptr(start), _ptr(length))
         _check(lib().spec_kv_read(_c.byref(a), _ptr(status), on.ptr))
     return k, v, status
+
+
+def spec_prefix_attention(q, cache, kv_len, prefix=None, prefix_len=None, parent=None, count=None,
+                          scale=None, kv_heads=None, stream=None):
+    """The verify pass's attention over a shared prefix and each row's own cache
+    (see spec_prefix_attention in include/specverify.h).
+
+    q [B, N, q_heads, D] (bfloat16 or float16, any strides with a dense last
+    dimension): the pass's tokens, already appended at slots kv_len[b] + i of
+    cache [2, B, S, kv_heads, D] (q's dtype) or [2, B, S, entry bytes] uint8
+    (kv_heads needed); prefix: a cache tensor whose row 0 holds the shared
+    entries, the first prefix_len of them used (None: all); parent [B, N]
+    int32 for draft trees (None: chains); count [B] int32 queries per row
+    (None: N); scale: 1/sqrt(D) if None.  Returns (out like q, dense; lse
+    [B, N, q_heads] float32; row_status [B] int32).
+    """
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, N, q_heads, head_dim] tensor")
+    dev = q.device
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
+    B, N, heads, D = q.shape
+    if q.stride(3) != 1 and D > 1:
+        raise ValueError("q: the last dimension must be dense")
+    if kv_heads is None:
+        if not isinstance(cache, torch.Tensor) or cache.dim() != 5:
+            raise ValueError("kv_heads is needed for a uint8 cache")
+        kv_heads = cache.shape[3]
+    c = _kv_cache(cache, kv_heads, D, dev, "cache")
+    if c.rows != B:
+        raise ValueError(f"cache has {c.rows} rows, q has {B}")
+    if prefix is not None:
+        pc = _kv_cache(prefix, kv_heads, D, dev, "prefix")
+        P = pc.slots if prefix_len is None else int(prefix_len)
+    else:
+        if prefix_len:
+            raise ValueError("prefix_len without a prefix")
+        pc, P = SpecKvCache(), 0
+    _rows_i32(kv_len, "kv_len", dev, B)
+    _rows_i32(count, "count", dev, B)
+    _req(parent, "parent", dev, torch.int32)
+    if parent is not None and tuple(parent.shape) != (B, N):
+        raise ValueError(f"parent must be [{B}, {N}], got {tuple(parent.shape)}")
+    a = SpecAttentionArgs(c, pc, P, N, heads, _KV_DTYPES[q.dtype],
+                          D ** -0.5 if scale is None else float(scale), _ptr(q),
+                          (_c.c_int64 * 3)(*q.stride()[:3]), _ptr(kv_len), _ptr(count), _ptr(parent))
+    L = lib()
+    with _On(dev, stream) as on:
+        on.use(q, cache, kv_len, prefix, parent, count)
+        out = torch.empty(B, N, heads, D, dtype=q.dtype, device=dev)
+        lse = torch.empty(B, N, heads, dtype=torch.float32, device=dev)
+        status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
+        ws = on.scratch(L.spec_prefix_attention_workspace_size(_c.byref(a)))
+        _check(L.spec_prefix_attention(_c.byref(a), _ptr(out), _ptr(lse), _ptr(status), _ptr(ws),
+                                       ws.numel(), on.ptr))
+    return out, lse, status
 
 
 def spec_token_logprobs(logits, tokens=None, temperature=None, m=0, stream=None):

@@ -1,0 +1,151 @@
+// attention.cuh -- parameters and small device helpers shared by the kernels
+// of spec_prefix_attention.
+//
+// For a query row (row b, token i, query head h) let x_t = scale log2(e) q.k_t
+// be its base-2 scores and v_t = 2^e_t c_t the values of token t (e_t = 0 and
+// c_t = v_t in a 16-bit cache; in an e4m3 cache c_t are the codes and 2^e_t the
+// scale).  A part of the keys is summed up as
+//   m = max_t (x_t + e_t),  O = sum_t 2^(x_t + e_t - m) c_t,  z = log2 sum_t 2^x_t,
+// so the weights of the codes never exceed 1, whatever the scales, and the
+// query's answer over several parts is
+//   Z = log2 sum 2^z,  out = sum 2^(m - Z) O,  lse = ln 2 Z.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kv_layout.cuh"
+#include "specverify.h"
+
+namespace sv {
+
+struct AttnParams {
+  // caches
+  const unsigned char *k, *v;    // own entries
+  const unsigned char *pk, *pv;  // prefix entries
+  long long row_stride, tok_stride, ptok_stride, slots;
+  int P;  // prefix length
+  // queries
+  const void *q;
+  long long qs[3];
+  float scale;  // times log2(e)
+  int B, N, Hq, H, G, D;
+  const int32_t *kv_len, *count;
+  // tree: words of 32 ancestor bits per query (node i's own bit among them)
+  // and each row's query count (negative: bad row), from the mask kernel
+  const uint32_t *anc;
+  const int32_t *rowinfo;
+  int W;
+  // partial sums: slot s of output row r has O at part[(s * rows + r) * D] and
+  // (m, z) at ml[s * rows + r]; z = -inf: an empty part, O not written
+  float *part;
+  float2 *ml;
+  int rows;         // B * N * Hq
+  int psplits, pchunk;  // prefix parts (slots 0 .. psplits - 1) and tokens in each
+  int osplits;          // own parts (slots psplits ..)
+  int min_chunk;        // smallest own part (tokens)
+  // outputs
+  void *out;
+  float *lse;
+  int32_t *row_status;
+  int qbf16;
+  uint64_t wait_limit_ns;
+};
+
+constexpr int kRowBadSlot = -1, kRowBadParent = -2;
+
+// Queries of row b; negative if the row cannot be used.
+__device__ __forceinline__ int row_queries(const AttnParams &P, int b) {
+  if (P.rowinfo) return __ldg(P.rowinfo + b);
+  const int n = __ldg(P.kv_len + b), c = P.count ? __ldg(P.count + b) : P.N;
+  if (n < 0 || c < 0 || c > P.N || static_cast<long long>(n) + c > P.slots) return kRowBadSlot;
+  return c;
+}
+
+// The own part `split` covers of a row's len entries: equal parts, rounded up
+// to 64 tokens.
+__device__ __forceinline__ void own_range(const AttnParams &P, int len, int split, int &t0, int &t1) {
+  int chunk = (len + P.osplits - 1) / P.osplits;
+  chunk = max(P.min_chunk, (chunk + 63) / 64 * 64);
+  const long long a = static_cast<long long>(split) * chunk;
+  t0 = static_cast<int>(min(a, static_cast<long long>(len)));
+  t1 = static_cast<int>(min(a + chunk, static_cast<long long>(len)));
+}
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8)
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// two floats rounded to a pair of the 16-bit type, lo in the low half
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// two e4m3 codes (the low 16 bits) as a pair of fp16: exact
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// Exponent of a scale byte as a float.
+__device__ __forceinline__ float scale_exponent(uint32_t c) {
+  return c == 255u ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(c) - 127);
+}
+// sum_t 2^(x_t - m) is kept as l 2^-E, E the largest scale exponent met so far
+// (at least kMinExponent), so that it stays in range for all scales; a token
+// whose scale is more than 2^kExponentSpan below the largest counts with that
+// span and takes the rest of the factor on its weight.
+constexpr float kMinExponent = -60.f;
+constexpr float kExponentSpan = 60.f;
+
+// Host launchers.
+cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool prefix_too, cudaStream_t s);
+
+}  // namespace sv

@@ -1,0 +1,900 @@
+// prefix_attention.cu -- the verify pass's attention over a shared prefix and
+// each row's own cache (spec_prefix_attention): the entry point, the tree
+// mask, the kernel for few query rows and the join of the parts.
+//
+//  attn_mask_kernel -- draft trees only: checks each row's parents and turns
+//    them into ancestor bits, one thread per node walking to the root.
+//  attn_rows_kernel -- 16 or 32 query rows (the query heads of one KV head and
+//    the tokens of one row; for the prefix, of all rows) against a range of
+//    tokens.  Bound by the cache's bytes, so what matters is bytes in flight:
+//    each warp streams its own blocks of 16 tokens through its own ring of
+//    asynchronous copies and never waits for another warp; the warps' sums
+//    join once at the end.  e4m3 codes are turned into fp16 in registers on
+//    the way to the tensor cores (exact), scales go into the scores and the
+//    weights.
+//  attn_join_kernel -- one warp per query row adds up the parts.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "attention.cuh"
+#include "internal.h"
+
+namespace sv {
+namespace {
+
+constexpr int kSms = 152;           // parts are sized for this many SMs
+constexpr int kRowWarps = 4;        // warps of attn_rows_kernel, each with its own ring
+constexpr int kRowThreads = 32 * kRowWarps;
+constexpr int kRowStages = 4;
+constexpr int kBlk = 16;            // tokens per block
+constexpr int kMaskThreads = 256;
+constexpr int kJoinThreads = 256;
+
+// ---------------------------------------------------------------- tree mask
+__global__ void __launch_bounds__(kMaskThreads) attn_mask_kernel(const int32_t *parent, const int32_t *kv_len,
+                                                                 const int32_t *count, long long slots, int N, int W,
+                                                                 uint32_t *anc, int32_t *rowinfo) {
+  __shared__ int par[SPEC_MAX_TREE_NODES];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int n = kv_len[b], c = count ? count[b] : N;
+  const bool slot_ok = n >= 0 && c >= 0 && c <= N && static_cast<long long>(n) + c <= slots;
+  const int used = max(0, min(c, N));
+  bool ok = true;
+  for (int i = tid; i < used; i += kMaskThreads) {
+    const int p = parent[static_cast<size_t>(b) * N + i];
+    par[i] = p;
+    ok = ok && (i == 0 ? p == -1 : p >= 0 && p < i);
+  }
+  ok = __syncthreads_and(ok);
+  if (tid == 0) rowinfo[b] = !ok ? kRowBadParent : !slot_ok ? kRowBadSlot : c;
+  if (!ok || !slot_ok) return;
+  for (int i = tid; i < used; i += kMaskThreads) {
+    uint32_t *row = anc + (static_cast<size_t>(b) * N + i) * W;
+    int w = W - 1, j = i;
+    uint32_t bits = 0;
+    while (j >= 0) {  // indexes fall strictly on the way up
+      while (w > (j >> 5)) {
+        row[w--] = bits;
+        bits = 0;
+      }
+      bits |= 1u << (j & 31);
+      j = par[j];
+    }
+    row[w] = bits;  // w == 0: the root is in word 0
+  }
+}
+
+// ------------------------------------------------------------- row kernel
+template <int CT, int DP, int MT>
+struct RowCfg {
+  static constexpr bool E4 = CT == SPEC_E4M3;
+  static constexpr int kEsz = E4 ? 1 : 2;
+  static constexpr int kPitch = DP * kEsz + 16;             // bytes of one token in a ring slot
+  static constexpr int kPlane = kBlk * kPitch;              // K or V of a block
+  static constexpr int kScales = E4 ? 2 * kBlk * 4 : 0;     // scale words, K then V
+  static constexpr int kStage = 2 * kPlane + kScales;
+  static constexpr int kQPitch = DP * 2 + 16;
+  static constexpr int kM = 16 * MT;
+  static constexpr int kRing = kRowWarps * kRowStages * kStage;
+  static constexpr int kMerge = kRowWarps * kM * (DP + 2) * 4;  // the warps' sums, after the loop
+  static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kSmem = kBody + kM * kQPitch + kM * 4;
+};
+
+// Item: prefix items first (KV head, block of kM rows of all rows' queries,
+// part), then own items (row, KV head, block, part).
+template <int CT, int DP, int MT>
+__global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_constant__ AttnParams P, int pitems,
+                                                                int pblocks, int oblocks) {
+  using C = RowCfg<CT, DP, MT>;
+  constexpr bool E4 = C::E4;
+  constexpr bool BF = CT == SPEC_BF16;
+  constexpr int kSteps = DP / 16, kNt = DP / 8;
+  extern __shared__ __align__(16) unsigned char smem[];
+  unsigned char *const qsm = smem + C::kBody;
+  float *const qfac = reinterpret_cast<float *>(qsm + C::kM * C::kQPitch);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int quad = lane / 4, j4 = lane % 4;
+
+  // --- the item
+  int item = blockIdx.x;
+  const bool pre = item < pitems;
+  if (!pre) item -= pitems;
+  int b = 0, g, blk, split;
+  if (pre) {
+    split = item % P.psplits;
+    item /= P.psplits;
+    blk = item % pblocks;
+    g = item / pblocks;
+  } else {
+    split = item % P.osplits;
+    item /= P.osplits;
+    blk = item % oblocks;
+    item /= oblocks;
+    g = item % P.H;
+    b = item / P.H;
+  }
+  const int r0 = blk * C::kM;              // first query row of the block
+  const int nrows = (pre ? P.B : 1) * P.N * P.G;
+  const int slot = pre ? split : P.psplits + split;
+  int t0, t1, len0 = 0;                    // tokens; own slots below len0 are seen by every query
+  const unsigned char *kb, *vb;
+  long long ts;
+  int bad_or_count = 0;
+  if (pre) {
+    t0 = split * P.pchunk;
+    t1 = min(P.P, t0 + P.pchunk);
+    kb = P.pk, vb = P.pv, ts = P.ptok_stride;
+  } else {
+    bad_or_count = row_queries(P, b);
+    len0 = __ldg(P.kv_len + b);
+    if (bad_or_count <= 0)
+      t0 = t1 = 0;
+    else
+      own_range(P, len0 + bad_or_count, split, t0, t1);
+    kb = P.k + b * P.row_stride, vb = P.v + b * P.row_stride, ts = P.tok_stride;
+  }
+  // query row rr of the block -> its token's flat index (b * N + i) and head; false if it has no use
+  auto decode = [&](int rr, int &qi, int &h) -> bool {
+    const int r = r0 + rr;
+    if (r >= nrows) return false;
+    const int t = r / P.G;
+    h = g * P.G + (r - t * P.G);
+    if (pre) {
+      qi = t;
+      const int rb = t / P.N;
+      return t - rb * P.N < row_queries(P, rb);
+    }
+    qi = b * P.N + t;
+    return t < bad_or_count;
+  };
+  if (t0 >= t1) {  // nothing here (an empty part, or a row that cannot be used)
+    for (int rr = tid; rr < C::kM; rr += kRowThreads) {
+      const int r = r0 + rr;
+      if (r >= nrows) break;
+      const int t = r / P.G;
+      const long long orow = (static_cast<long long>(pre ? 0 : b) * P.N + t) * P.Hq + g * P.G + (r - t * P.G);
+      P.ml[static_cast<long long>(slot) * P.rows + orow] = make_float2(-INFINITY, -INFINITY);
+    }
+    return;
+  }
+
+  // --- this warp's ring of token blocks
+  const uint32_t ring = smem_u32(smem) + warp * kRowStages * C::kStage;
+  const int nblk = (t1 - t0 + kBlk - 1) / kBlk;
+  const int pieces = P.D * C::kEsz / 16;  // 16-byte pieces of a head vector
+  const long long head_off = static_cast<long long>(g) * P.D * C::kEsz;
+  const long long scale_off = static_cast<long long>(P.H) * P.D + (g & ~3);
+  if (P.D < DP) {  // the columns past the head vector stay zero: no copy writes them
+    for (int i = lane; i < kRowStages * C::kStage / 16; i += 32)
+      *reinterpret_cast<uint4 *>(smem + warp * kRowStages * C::kStage + i * 16) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+  auto issue = [&](int blkno, int st) {
+    if (blkno < nblk) {
+      const int tb = t0 + blkno * kBlk;
+      const uint32_t base = ring + st * C::kStage;
+      for (int i = lane; i < kBlk * pieces; i += 32) {
+        const int tk = i / pieces, pc = i - tk * pieces;
+        const bool on = tb + tk < t1;
+        const long long off = static_cast<long long>(on ? tb + tk : t0) * ts + head_off + pc * 16;
+        cp_async16_zfill(base + tk * C::kPitch + pc * 16, kb + off, on);
+        cp_async16_zfill(base + C::kPlane + tk * C::kPitch + pc * 16, vb + off, on);
+      }
+      if constexpr (E4) {
+        const int tk = lane % kBlk;
+        const bool on = tb + tk < t1;
+        const long long off = static_cast<long long>(on ? tb + tk : t0) * ts + scale_off;
+        cp_async4_zfill(base + 2 * C::kPlane + lane * 4, (lane < kBlk ? kb : vb) + off, on);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kRowStages - 1; ++s) issue(warp + s * kRowWarps, s);
+
+  // --- queries into shared memory, a warp per row; fp16 for an e4m3 cache: a
+  // row far outside fp16's range is brought into it by a power of two
+  for (int rr = warp; rr < C::kM; rr += kRowWarps) {
+    int qi, h;
+    const bool on = decode(rr, qi, h);
+    float x[DP / 32];
+#pragma unroll
+    for (int i = 0; i < DP / 32; ++i) x[i] = 0.f;
+    if (on) {
+      const int qb = qi / P.N, qt = qi - qb * P.N;
+      const long long off = qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2];
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) {
+        const int d = i * 32 + lane;
+        if (d < P.D)
+          x[i] = P.qbf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(P.q)[off + d])
+                         : __half2float(static_cast<const __half *>(P.q)[off + d]);
+      }
+    }
+    float fac = 1.f;
+    if constexpr (E4) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) a = max(a, __float_as_uint(x[i]) & 0x7fffffffu);
+      a = __reduce_max_sync(FULL_MASK, a);
+      const int e = static_cast<int>(a >> 23) - 127;  // magnitude's exponent
+      if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
+        const int up = max(-126, min(126, -e));
+        const float by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+        fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) x[i] *= by;
+      }
+    }
+    if (lane == 0) qfac[rr] = fac;
+#pragma unroll
+    for (int i = 0; i < DP / 32; ++i) {
+      unsigned short u;
+      if constexpr (BF)
+        u = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
+      else
+        u = __half_as_ushort(__float2half_rn(x[i]));
+      *reinterpret_cast<unsigned short *>(qsm + rr * C::kQPitch + (i * 32 + lane) * 2) = u;
+    }
+  }
+  __syncthreads();
+
+  // Fragments.  The contraction over d may run in any order as long as Q and
+  // K agree: for codes a thread takes DP/4 consecutive d (a few 16-byte
+  // reads), for 16-bit entries the order ldmatrix gives.
+  uint32_t qf[MT][kSteps][4];
+  float rf[MT][2];
+  bool scaled = false;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int rr = mt * 16 + hf * 8 + quad;
+      rf[mt][hf] = qfac[rr];
+      scaled = scaled || rf[mt][hf] != 1.f;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int d0 = E4 ? j4 * (DP / 4) + s * 4 : s * 16 + j4 * 2;
+        const int d1 = E4 ? d0 + 2 : d0 + 8;
+        qf[mt][s][hf] = *reinterpret_cast<const uint32_t *>(qsm + rr * C::kQPitch + d0 * 2);
+        qf[mt][s][2 + hf] = *reinterpret_cast<const uint32_t *>(qsm + rr * C::kQPitch + d1 * 2);
+      }
+    }
+  }
+  scaled = __any_sync(FULL_MASK, scaled);
+  // each thread's rows, for the mask of the pass's own tokens
+  int qtok[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = r0 + mt * 16 + hf * 8 + quad;
+      qtok[mt][hf] = min(r / P.G, P.N - 1);
+    }
+
+  float o[MT][kNt][4];
+  float mx[MT][2], l[MT][2];
+  float E = kMinExponent;  // l counts in units of 2^(mx - E), E the largest scale exponent so far
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    mx[mt][0] = mx[mt][1] = -INFINITY;
+    l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < kNt; ++n)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[mt][n][c] = 0.f;
+  }
+
+  int st = 0;
+  for (int blkno = warp; blkno < nblk; blkno += kRowWarps) {
+    issue(blkno + (kRowStages - 1) * kRowWarps, (st + kRowStages - 1) % kRowStages);
+    cp_async_wait<kRowStages - 1>();
+    __syncwarp();
+    const uint32_t kst = ring + st * C::kStage, vst = kst + C::kPlane;
+    const int tb = t0 + blkno * kBlk;
+    // --- scores: token nt * 8 + 2 j4 + {0, 1} of rows quad and quad + 8
+    float s4[MT][2][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s4[mt][n][c] = 0.f;
+    if constexpr (E4) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const uint32_t at = kst + (n * 8 + quad) * C::kPitch + j4 * (DP / 4);
+#pragma unroll
+        for (int s0 = 0; s0 < kSteps; s0 += 4) {
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(at + s0 * 4)
+                       : "memory");
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t b0 = e4m3x2_to_f16x2(w[s]), b1 = e4m3x2_to_f16x2_hi(w[s]);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mma16816<false>(s4[mt][n], qf[mt][s0 + s], b0, b1);
+          }
+        }
+      }
+    } else {
+      // matrices: (tokens 0-7, d 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
+      const uint32_t at = kst + ((lane / 16) * 8 + lane % 8) * C::kPitch + ((lane / 8) % 2) * 16;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint32_t kf[4];
+        ldmatrix_x4(kf, at + s * 32);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816<BF>(s4[mt][0], qf[mt][s], kf[0], kf[1]);
+          mma16816<BF>(s4[mt][1], qf[mt][s], kf[2], kf[3]);
+        }
+      }
+    }
+    // --- to base-2 exponents of the weights
+    float a4[2][2], e4[2][2], inv[2][2], f4[2][2];
+    bool small = false;
+    float dE = 0.f;
+    if constexpr (E4) {
+      int top = -127;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int tk = n * 8 + 2 * j4 + c;
+          uint32_t kw, vw;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(kst + 2 * C::kPlane + tk * 4) : "memory");
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(kst + 2 * C::kPlane + (kBlk + tk) * 4) : "memory");
+          a4[n][c] = P.scale * e4m3_scale(kw >> (8 * (g & 3)) & 255u);
+          const uint32_t vc = vw >> (8 * (g & 3)) & 255u;
+          e4[n][c] = scale_exponent(vc);
+          if (vc != 255u) top = max(top, static_cast<int>(vc) - 127);
+        }
+      const float En = fmaxf(E, static_cast<float>(__reduce_max_sync(FULL_MASK, top)));
+      dE = En - E;
+      E = En;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float e = e4[n][c];
+          e4[n][c] = e < E - kExponentSpan ? E - kExponentSpan : e;
+          f4[n][c] = e < E - kExponentSpan ? ex2(e - e4[n][c]) : 1.f;
+          small = small || e < E - kExponentSpan;
+          inv[n][c] = ex2(E - e4[n][c]);
+        }
+      small = __any_sync(FULL_MASK, small);
+      if (scaled) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s4[mt][n][c] *= rf[mt][c >> 1];
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s4[mt][n][c] = fmaf(s4[mt][n][c], a4[n][c & 1], e4[n][c & 1]);
+    } else {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s4[mt][n][c] *= P.scale;
+    }
+    // --- masks: the range's end, and the pass's own tokens
+    const bool masked = tb + kBlk > t1 || (!pre && tb + kBlk > len0);
+    if (masked) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int t = tb + n * 8 + 2 * j4 + (c & 1);
+            bool see = t < t1;
+            const int jn = t - len0;
+            if (see && !pre && jn >= 0) {
+              const int qi = qtok[mt][c >> 1];
+              see = P.anc ? (__ldg(P.anc + (static_cast<size_t>(b) * P.N + qi) * P.W + (jn >> 5)) >> (jn & 31)) & 1 : jn <= qi;
+            }
+            if (!see) s4[mt][n][c] = -INFINITY;
+          }
+    }
+    // --- softmax
+    uint32_t pf[MT][4];
+    bool moved = false;
+    float al[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float t = fmaxf(fmaxf(s4[mt][0][2 * hf], s4[mt][0][2 * hf + 1]), fmaxf(s4[mt][1][2 * hf], s4[mt][1][2 * hf + 1]));
+        t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 1));
+        t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 2));
+        const float mn = fmaxf(mx[mt][hf], t);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        al[mt][hf] = ex2(mx[mt][hf] - ref);
+        moved = moved || mn != mx[mt][hf];
+        float add = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float &x = s4[mt][n][2 * hf + c];
+            x = ex2(x - ref);
+            if constexpr (E4) {
+              // 0 * NaN: a token that is not seen adds nothing, whatever its scale
+              add += x == 0.f ? 0.f : x * inv[n][c];
+            } else {
+              add += x;
+            }
+          }
+        const float ll = E4 && dE != 0.f ? ex2(mx[mt][hf] - ref + dE) : al[mt][hf];
+        mx[mt][hf] = mn;
+        l[mt][hf] = fmaf(l[mt][hf], ll, add);
+      }
+    if constexpr (E4) {
+      if (small) {  // the rest of the factor of scales that far below the largest
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              s4[mt][n][c] *= f4[n][c];
+              s4[mt][n][2 + c] *= f4[n][c];
+            }
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      pf[mt][0] = pack16<BF>(s4[mt][0][0], s4[mt][0][1]);
+      pf[mt][1] = pack16<BF>(s4[mt][0][2], s4[mt][0][3]);
+      pf[mt][2] = pack16<BF>(s4[mt][1][0], s4[mt][1][1]);
+      pf[mt][3] = pack16<BF>(s4[mt][1][2], s4[mt][1][3]);
+    }
+    if (__any_sync(FULL_MASK, moved)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+          o[mt][n][0] *= al[mt][0];
+          o[mt][n][1] *= al[mt][0];
+          o[mt][n][2] *= al[mt][1];
+          o[mt][n][3] *= al[mt][1];
+        }
+    }
+    // --- a value that is not finite in a block that some query may not see:
+    // zero times it would be NaN.  Such elements are added by hand to the
+    // queries that see them and set to zero for the product.
+    if (masked) {
+      bool odd = false;
+      const int per = P.D * C::kEsz / 4;  // words of a head vector
+      auto clean = [&](uint32_t w) -> uint32_t {  // w without its non-finite elements
+        uint32_t r = w;
+        if constexpr (E4) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if ((w >> (8 * c) & 127u) == 127u) r &= ~(255u << (8 * c));
+        } else {
+          constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
+          if ((w & top) == top) r &= 0xffff0000u;
+          if ((w >> 16 & top) == top) r &= 0x0000ffffu;
+        }
+        return r;
+      };
+      for (int i = lane; i < kBlk * per; i += 32) {
+        const int tk = i / per;
+        uint32_t w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(vst + tk * C::kPitch + (i - tk * per) * 4) : "memory");
+        odd = odd || clean(w) != w;
+      }
+      if (__any_sync(FULL_MASK, odd)) {
+        for (int tk = 0; tk < kBlk; ++tk) {
+          const int src = (lane & ~3) | (tk % 8) / 2;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                if (n == tk / 8 && c == tk % 2) w0 = s4[mt][n][c], w1 = s4[mt][n][2 + c];
+            w0 = __shfl_sync(FULL_MASK, w0, src);
+            w1 = __shfl_sync(FULL_MASK, w1, src);
+#pragma unroll
+            for (int n = 0; n < kNt; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int d = E4 ? (2 * j4 + c) * kNt + n : n * 8 + 2 * j4 + c;
+                float val;
+                const unsigned char *at = smem + warp * kRowStages * C::kStage + st * C::kStage + C::kPlane + tk * C::kPitch + d * C::kEsz;
+                if constexpr (E4)
+                  val = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16x2(*at))));
+                else if constexpr (BF)
+                  val = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(at));
+                else
+                  val = __half2float(*reinterpret_cast<const __half *>(at));
+                if (isfinite(val)) continue;
+                if (w0 != 0.f) o[mt][n][c] = fmaf(w0, val, o[mt][n][c]);
+                if (w1 != 0.f) o[mt][n][2 + c] = fmaf(w1, val, o[mt][n][2 + c]);
+              }
+          }
+        }
+        __syncwarp();
+        for (int i = lane; i < kBlk * per; i += 32) {
+          const int tk = i / per;
+          const uint32_t at = vst + tk * C::kPitch + (i - tk * per) * 4;
+          uint32_t w;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(clean(w)) : "memory");
+        }
+        __syncwarp();
+      }
+    }
+    // --- weights times values
+    if constexpr (E4) {
+      // tokens 2 j4, 2 j4 + 1, 8 + 2 j4, 9 + 2 j4 of columns quad * kNt + n
+#pragma unroll
+      for (int n0 = 0; n0 < kNt; n0 += 8) {
+        uint32_t w[4][2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                       : "=r"(w[t][0]), "=r"(w[t][1])
+                       : "r"(vst + ((t / 2) * 8 + 2 * j4 + t % 2) * C::kPitch + quad * kNt + n0)
+                       : "memory");
+#pragma unroll
+        for (int n = 0; n < 8; n += 2) {
+          // bytes n, n + 1 of two tokens: (t0 n, t1 n, t0 n+1, t1 n+1)
+          const uint32_t sel = n % 4 == 0 ? 0x5140u : 0x7362u;
+          const uint32_t lo = __byte_perm(w[0][n / 4], w[1][n / 4], sel);
+          const uint32_t hi = __byte_perm(w[2][n / 4], w[3][n / 4], sel);
+          const uint32_t b0 = e4m3x2_to_f16x2(lo), b1 = e4m3x2_to_f16x2(hi);
+          const uint32_t c0 = e4m3x2_to_f16x2_hi(lo), c1 = e4m3x2_to_f16x2_hi(hi);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816<false>(o[mt][n0 + n], pf[mt], b0, b1);
+            mma16816<false>(o[mt][n0 + n + 1], pf[mt], c0, c1);
+          }
+        }
+      }
+    } else {
+      // matrices: (tokens 0-7, d 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+      const uint32_t at = vst + (lane % 16) * C::kPitch + (lane / 16) * 16;
+#pragma unroll
+      for (int n = 0; n < kNt; n += 2) {
+        uint32_t vf[4];
+        ldmatrix_x4_trans(vf, at + n * 16);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816<BF>(o[mt][n], pf[mt], vf[0], vf[1]);
+          mma16816<BF>(o[mt][n + 1], pf[mt], vf[2], vf[3]);
+        }
+      }
+    }
+    __syncwarp();
+    st = (st + 1) % kRowStages;
+  }
+
+  // --- join the warps: everyone leaves its sums in the ring's memory
+  cp_async_wait_all();
+  __syncthreads();
+  float *const om = reinterpret_cast<float *>(smem);                  // [warp][row][DP]
+  float *const mm = om + kRowWarps * C::kM * DP;                      // [warp][row]
+  float *const lm = mm + kRowWarps * C::kM;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int rr = mt * 16 + hf * 8 + quad;
+      float t = l[mt][hf];
+      t += __shfl_xor_sync(FULL_MASK, t, 1);
+      t += __shfl_xor_sync(FULL_MASK, t, 2);
+      if (j4 == 0) {
+        mm[warp * C::kM + rr] = mx[mt][hf];
+        lm[warp * C::kM + rr] = t == 0.f ? -INFINITY : mx[mt][hf] + log2f(t) - (E4 ? E : 0.f);
+      }
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int d = E4 ? (2 * j4 + c) * kNt + n : n * 8 + 2 * j4 + c;
+          om[(warp * C::kM + rr) * DP + d] = o[mt][n][2 * hf + c];
+        }
+    }
+  __syncthreads();
+  for (int rr = warp; rr < C::kM; rr += kRowWarps) {
+    int qi, h;
+    const bool on = decode(rr, qi, h);
+    if (r0 + rr >= nrows) break;
+    if (!on) {  // no such query: an empty part
+      const int r = r0 + rr, t = r / P.G;
+      qi = (pre ? 0 : b * P.N) + t;
+      h = g * P.G + (r - t * P.G);
+    }
+    const long long orow = static_cast<long long>(qi) * P.Hq + h;
+    float M = -INFINITY, Z = -INFINITY, S = 0.f, w[kRowWarps];
+#pragma unroll
+    for (int k = 0; k < kRowWarps; ++k) {
+      M = fmaxf(M, mm[k * C::kM + rr]);
+      Z = fmaxf(Z, lm[k * C::kM + rr]);
+    }
+    const float ref = M == -INFINITY ? 0.f : M, zref = Z == -INFINITY ? 0.f : Z;
+#pragma unroll
+    for (int k = 0; k < kRowWarps; ++k) {
+      w[k] = ex2(mm[k * C::kM + rr] - ref);
+      S += ex2(lm[k * C::kM + rr] - zref);
+    }
+    const bool some = on && S != 0.f;
+    if (lane == 0)
+      P.ml[static_cast<long long>(slot) * P.rows + orow] = some ? make_float2(M, zref + log2f(S)) : make_float2(-INFINITY, -INFINITY);
+    if (!some) continue;
+    float *to = P.part + (static_cast<long long>(slot) * P.rows + orow) * P.D;
+    for (int d = lane; d < P.D; d += 32) {
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < kRowWarps; ++k) x = fmaf(w[k], om[(k * C::kM + rr) * DP + d], x);
+      to[d] = x;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- join
+// One warp per output row: the weights of the parts, then their sum.
+template <bool BF>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams P) {
+  grid_dependency_wait();
+  const int lane = threadIdx.x % 32;
+  const long long r = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
+  if (r >= P.rows) return;
+  const int nslots = P.psplits + P.osplits;
+  const int b = static_cast<int>(r / (static_cast<long long>(P.N) * P.Hq));
+  const int n = row_queries(P, b);
+  if (P.row_status && r == static_cast<long long>(b) * P.N * P.Hq && lane == 0)
+    P.row_status[b] = n >= 0 ? 0 : n == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
+  const bool on = static_cast<int>(r / P.Hq) - b * P.N < n;
+  float Z = -INFINITY;
+  if (on)
+    for (int s = lane; s < nslots; s += 32) Z = fmaxf(Z, P.ml[static_cast<long long>(s) * P.rows + r].y);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) Z = fmaxf(Z, __shfl_xor_sync(FULL_MASK, Z, o));
+  const float zref = Z == -INFINITY ? 0.f : Z;
+  float S = 0.f;
+  if (on)
+    for (int s = lane; s < nslots; s += 32) S += ex2(P.ml[static_cast<long long>(s) * P.rows + r].y - zref);
+  S = warp_sum(S);
+  const float z = S == 0.f ? -INFINITY : zref + log2f(S);
+  float acc[SPEC_MAX_HEAD_DIM / 32] = {0.f, 0.f, 0.f, 0.f};
+  if (S != 0.f)
+    for (int s0 = 0; s0 < nslots; s0 += 32) {
+      float2 ml = make_float2(-INFINITY, -INFINITY);
+      if (s0 + lane < nslots) ml = P.ml[static_cast<long long>(s0 + lane) * P.rows + r];
+      const float wl = ex2(ml.x - z);
+      const int top = min(32, nslots - s0);
+      for (int k = 0; k < top; ++k) {
+        const float w = __shfl_sync(FULL_MASK, wl, k);
+        if (__shfl_sync(FULL_MASK, ml.y, k) == -INFINITY) continue;  // an empty part left no sum
+        const float *from = P.part + (static_cast<long long>(s0 + k) * P.rows + r) * P.D;
+#pragma unroll
+        for (int i = 0; i < SPEC_MAX_HEAD_DIM / 32; ++i) {
+          const int d = i * 32 + lane;
+          if (d < P.D) acc[i] = fmaf(w, from[d], acc[i]);
+        }
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < SPEC_MAX_HEAD_DIM / 32; ++i) {
+    const int d = i * 32 + lane;
+    if (d < P.D) {
+      if constexpr (BF)
+        static_cast<__nv_bfloat16 *>(P.out)[r * P.D + d] = __float2bfloat16_rn(acc[i]);
+      else
+        static_cast<__half *>(P.out)[r * P.D + d] = __float2half_rn(acc[i]);
+    }
+  }
+  if (lane == 0 && P.lse) P.lse[r] = 0.693147180559945309f * z;
+}
+
+// -------------------------------------------------------------------- host
+template <int CT, int DP, int MT>
+cudaError_t launch_rows(const AttnParams &p, bool with_prefix, cudaStream_t s) {
+  using C = RowCfg<CT, DP, MT>;
+  const int pblocks = static_cast<int>((static_cast<long long>(p.B) * p.N * p.G + C::kM - 1) / C::kM);
+  const int oblocks = (p.N * p.G + C::kM - 1) / C::kM;
+  const long long pitems = with_prefix ? static_cast<long long>(p.H) * pblocks * p.psplits : 0;
+  const long long items = pitems + static_cast<long long>(p.B) * p.H * oblocks * p.osplits;
+  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<CT, DP, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  attn_rows_kernel<CT, DP, MT><<<static_cast<unsigned>(items), kRowThreads, C::kSmem, s>>>(p, static_cast<int>(pitems), pblocks, oblocks);
+  return cudaGetLastError();
+}
+
+template <int CT>
+cudaError_t launch_rows_d(const AttnParams &p, bool with_prefix, cudaStream_t s) {
+  const bool two = p.N * p.G > 16 || (with_prefix && static_cast<long long>(p.B) * p.N * p.G > 16);
+  if (p.D <= 64) return two ? launch_rows<CT, 64, 2>(p, with_prefix, s) : launch_rows<CT, 64, 1>(p, with_prefix, s);
+  return two ? launch_rows<CT, 128, 2>(p, with_prefix, s) : launch_rows<CT, 128, 1>(p, with_prefix, s);
+}
+
+struct AttnPlan {
+  int psplits, pchunk, osplits, W;
+  size_t rows, anc_at, info_at, ml_at, part_at, bytes;
+};
+
+size_t at_round(size_t x) { return (x + 255) / 256 * 256; }
+bool at_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Sizes and types (no pointers).
+spec_status check_attention(const spec_attention_args *a) {
+  const spec_kv_cache &c = a->cache;
+  if (a->q_dtype != SPEC_BF16 && a->q_dtype != SPEC_F16) return SPEC_ERR_DTYPE;
+  if (c.dtype != SPEC_E4M3 && c.dtype != a->q_dtype) return SPEC_ERR_DTYPE;
+  spec_status st = check_kv_cache(c);
+  if (st != SPEC_OK) return st;
+  if (a->prefix_len < 0 || a->prefix_len > 0x7fffffffLL - 4096) return SPEC_ERR_SHAPE;
+  if (a->prefix_len > 0) {
+    if (a->prefix.dtype != c.dtype) return SPEC_ERR_DTYPE;
+    st = check_kv_cache(a->prefix);
+    if (st != SPEC_OK) return st;
+    if (a->prefix.heads != c.heads || a->prefix.head_dim != c.head_dim || a->prefix.rows < 1 ||
+        a->prefix.slots < a->prefix_len)
+      return SPEC_ERR_SHAPE;
+  }
+  if (a->N < 0 || a->N > SPEC_MAX_TREE_NODES || a->q_heads < 1 || a->q_heads % c.heads) return SPEC_ERR_SHAPE;
+  if (static_cast<long long>(c.rows) * a->N >= 0x7fffffffLL / 256 / a->q_heads) return SPEC_ERR_SHAPE;
+  if (c.slots > 0x7fffffffLL - 4096) return SPEC_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i)
+    if (a->q_stride[i] < 0) return SPEC_ERR_SHAPE;
+  if (!std::isfinite(a->scale)) return SPEC_ERR_ARG;
+  return SPEC_OK;
+}
+
+// How the keys are cut into parts: enough items for two per SM, no part
+// under 64 tokens, and no more parts than 64.
+AttnPlan plan_attention(const spec_attention_args *a) {
+  AttnPlan p = {};
+  const spec_kv_cache &c = a->cache;
+  const long long G = a->q_heads / c.heads;
+  const long long q = static_cast<long long>(c.rows) * a->N;
+  p.rows = static_cast<size_t>(q) * a->q_heads;
+  auto parts = [](long long blocks, long long tokens) {
+    const long long want = (2 * kSms + blocks - 1) / blocks;
+    return static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 64})));
+  };
+  if (a->prefix_len > 0) {
+    const long long blocks = c.heads * ((q * G + 31) / 32);
+    p.psplits = parts(blocks, a->prefix_len);
+    p.pchunk = static_cast<int>(((a->prefix_len + p.psplits - 1) / p.psplits + 63) / 64 * 64);
+    p.psplits = static_cast<int>((a->prefix_len + p.pchunk - 1) / p.pchunk);
+  }
+  p.osplits = parts(c.rows * c.heads * ((a->N * G + 31) / 32), c.slots);
+  p.W = (a->N + 31) / 32;
+  size_t at = 0;
+  p.anc_at = at;
+  at += at_round(static_cast<size_t>(q) * p.W * 4);
+  p.info_at = at;
+  at += at_round(static_cast<size_t>(c.rows) * 4);
+  p.ml_at = at;
+  const size_t slots = static_cast<size_t>(p.psplits) + p.osplits;
+  at += at_round(slots * p.rows * sizeof(float2));
+  p.part_at = at;
+  at += at_round(slots * p.rows * c.head_dim * 4);
+  p.bytes = at + 256;
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool with_prefix, cudaStream_t s) {
+  if (ctype == SPEC_E4M3) return launch_rows_d<SPEC_E4M3>(p, with_prefix, s);
+  if (ctype == SPEC_BF16) return launch_rows_d<SPEC_BF16>(p, with_prefix, s);
+  return launch_rows_d<SPEC_F16>(p, with_prefix, s);
+}
+
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+size_t spec_prefix_attention_workspace_size(const spec_attention_args *a) {
+  if (!a) return 0;
+  spec_attention_args t = *a;  // sizes and types only
+  t.cache.k = t.cache.v = t.prefix.k = t.prefix.v = nullptr;
+  if (check_attention(&t) != SPEC_OK) return 0;
+  if (a->cache.rows == 0 || a->N == 0) return 256;
+  return plan_attention(a).bytes;
+}
+
+spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float *lse, int32_t *row_status,
+                                  void *ws, size_t ws_bytes, void *stream) {
+  if (!a) return SPEC_ERR_NULL;
+  const spec_status st = check_attention(a);
+  if (st != SPEC_OK) return st;
+  const spec_kv_cache &c = a->cache;
+  if (!at_aligned(a->q, 2) || !at_aligned(out, 16) || !at_aligned(lse, 16) || !at_aligned(row_status, 4) ||
+      !at_aligned(a->kv_len, 4) || !at_aligned(a->count, 4) || !at_aligned(a->parent, 4))
+    return SPEC_ERR_ALIGN;
+  if (c.rows == 0 || a->N == 0) return SPEC_OK;
+  if (!a->q || !out || !a->kv_len || ((!c.k || !c.v) && c.slots > 0) ||
+      (a->prefix_len > 0 && (!a->prefix.k || !a->prefix.v)))
+    return SPEC_ERR_NULL;
+  const AttnPlan plan = plan_attention(a);
+  if (!ws || !at_aligned(ws, 256) || ws_bytes < plan.bytes) return SPEC_ERR_WORKSPACE;
+  char *w = static_cast<char *>(ws);
+  AttnParams p = {};
+  p.k = static_cast<const unsigned char *>(c.k);
+  p.v = static_cast<const unsigned char *>(c.v);
+  p.row_stride = c.row_stride;
+  p.tok_stride = c.tok_stride;
+  p.slots = c.slots;
+  p.P = static_cast<int>(a->prefix_len);
+  if (p.P) {
+    p.pk = static_cast<const unsigned char *>(a->prefix.k);
+    p.pv = static_cast<const unsigned char *>(a->prefix.v);
+    p.ptok_stride = a->prefix.tok_stride;
+  }
+  p.q = a->q;
+  for (int i = 0; i < 3; ++i) p.qs[i] = a->q_stride[i];
+  p.scale = a->scale * 1.442695040888963407f;
+  p.B = c.rows;
+  p.N = a->N;
+  p.Hq = a->q_heads;
+  p.H = c.heads;
+  p.G = a->q_heads / c.heads;
+  p.D = c.head_dim;
+  p.kv_len = a->kv_len;
+  p.count = a->count;
+  p.W = plan.W;
+  p.ml = reinterpret_cast<float2 *>(w + plan.ml_at);
+  p.part = reinterpret_cast<float *>(w + plan.part_at);
+  p.rows = static_cast<int>(plan.rows);
+  p.psplits = plan.psplits;
+  p.pchunk = plan.pchunk;
+  p.osplits = plan.osplits;
+  p.min_chunk = 64;
+  p.out = out;
+  p.lse = lse;
+  p.row_status = row_status;
+  p.qbf16 = a->q_dtype == SPEC_BF16;
+  p.wait_limit_ns = spec_get_wait_timeout_ns();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->parent) {
+    uint32_t *anc = reinterpret_cast<uint32_t *>(w + plan.anc_at);
+    int32_t *info = reinterpret_cast<int32_t *>(w + plan.info_at);
+    attn_mask_kernel<<<p.B, kMaskThreads, 0, s>>>(a->parent, a->kv_len, a->count, c.slots, p.N, p.W, anc, info);
+    if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+    p.anc = anc;
+    p.rowinfo = info;
+  }
+  if (launch_attn_rows(p, c.dtype, p.P > 0, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = p.qbf16 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true>, p)
+                                : cudaLaunchKernelEx(&cfg, attn_join_kernel<false>, p);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -140,3 +140,37 @@ def test_binding_refusals(L):
         sv.spec_token_logprobs(torch.zeros(3, 5, 7), torch.zeros(3, 4, dtype=torch.int32))
     with pytest.raises(ValueError):
         sv.spec_kv_entry_bytes(8, 100)
+
+
+def attention(L, c=None, pc=None, P_len=64, N=3, q_heads=16, q_dtype=BF16, scale=0.1, q=P, qs=(6000, 2000, 128),
+              kv_len=P, count=None, parent=None, out=P, lse=P, status=P, ws=P, ws_bytes=1 << 40):
+    from speculative_decoding_verification_32_gb300._binding import SpecAttentionArgs
+    a = SpecAttentionArgs(cache(**(c or {})), cache(**dict(dict(rows=1), **(pc or {}))), P_len, N, q_heads, q_dtype,
+                          scale, ptr(q), (ctypes.c_int64 * 3)(*qs), ptr(kv_len), ptr(count), ptr(parent))
+    return L.spec_prefix_attention(ctypes.byref(a), ptr(out), ptr(lse), ptr(status), ptr(ws), ws_bytes, None), a
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q_dtype=F32), DTYPE), (dict(q_dtype=E4M3), DTYPE), (dict(c=dict(dtype=F16, tok=2048)), DTYPE),
+    (dict(pc=dict(dtype=BF16, tok=2048)), DTYPE), (dict(c=dict(rows=-1)), SHAPE), (dict(pc=dict(rows=0)), SHAPE),
+    (dict(P_len=-1), SHAPE), (dict(P_len=65), SHAPE), (dict(pc=dict(heads=4)), SHAPE), (dict(N=-1), SHAPE),
+    (dict(N=1025), SHAPE), (dict(q_heads=12), SHAPE), (dict(q_heads=0), SHAPE), (dict(q_heads=8 << 20), SHAPE),
+    (dict(qs=(0, -1, 0)), SHAPE), (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG),
+    (dict(c=dict(k=P + 8)), ALIGN), (dict(pc=dict(v=P + 8)), ALIGN), (dict(out=P + 8), ALIGN),
+    (dict(q=P + 1), ALIGN), (dict(kv_len=P + 2), ALIGN), (dict(parent=P + 2), ALIGN), (dict(count=P + 1), ALIGN),
+    (dict(q=0), NULL), (dict(out=0), NULL), (dict(kv_len=0), NULL), (dict(c=dict(v=0)), NULL),
+    (dict(pc=dict(k=0)), NULL), (dict(ws=0), WORKSPACE), (dict(ws=P + 16), WORKSPACE), (dict(ws_bytes=4096), WORKSPACE),
+    (dict(c=dict(rows=0)), OK), (dict(N=0), OK)])
+def test_attention_refusals(L, kw, want):
+    assert attention(L, **kw)[0] == want
+
+
+def test_attention_workspace_size(L):
+    """Sizes only: pointers may be anything; more queries, heads or parts need more."""
+    def size(**kw):
+        return L.spec_prefix_attention_workspace_size(ctypes.byref(attention(L, **kw)[1]))
+    base = size(ws=0)
+    assert base >= 2 * 3 * 16 * (128 + 2) * 4 * 2  # two parts at least of 96 output rows
+    assert size(ws=0, N=6) > base and size(ws=0, q_heads=32) > base
+    assert size(ws=0, q_dtype=F32) == 0 and size(ws=0, N=1025) == 0
+    assert L.spec_prefix_attention_workspace_size(None) == 0
