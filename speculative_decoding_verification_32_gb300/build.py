@@ -23,7 +23,8 @@ VARIANTS = {None: (BUILD, LIB, []),
             "bounds": (os.path.join(HERE, "_build_bounds"),
                        os.path.join(HERE, "libspecverify_bounds.so"), ["-DSV_BOUNDS"])}
 SOURCES = ["api.cu", "chain_stochastic.cu", "greedy.cu", "rollback.cu", "kv_policy.cu",
-           "kv_cache.cu", "logprobs.cu", "prefix_attention.cu"]
+           "kv_cache.cu", "logprobs.cu", "prefix_attention.cu",
+           "prefix_attention_tile.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

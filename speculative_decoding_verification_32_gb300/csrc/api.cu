@@ -279,6 +279,8 @@ spec_status setup_stochastic(const spec_chain_args *a, void *ws, size_t ws_bytes
 
 }  // namespace
 
+bool sv::force_wait_timeout() { return g_force_timeout.load() != 0; }
+
 extern "C" {
 
 size_t spec_verify_chain_workspace_size(int32_t B, int32_t K, int32_t V) {

@@ -44,16 +44,21 @@ struct AttnParams {
   int rows;         // B * N * Hq
   int psplits, pchunk;  // prefix parts (slots 0 .. psplits - 1) and tokens in each
   int osplits;          // own parts (slots psplits ..)
-  int min_chunk;        // smallest own part (tokens)
+  int chunk;            // own parts are multiples of this many tokens
+  int oblk;             // query rows per own item
+  int32_t *oflag;       // per own item: a value that is not finite was left out of its sums
   // outputs
   void *out;
   float *lse;
   int32_t *row_status;
   int qbf16;
   uint64_t wait_limit_ns;
+  int force_timeout;
 };
 
 constexpr int kRowBadSlot = -1, kRowBadParent = -2;
+// z of a part whose kernel gave up waiting (no arithmetic makes this NaN)
+constexpr uint32_t kTimeoutBits = 0x7fc0deadu;
 
 // Queries of row b; negative if the row cannot be used.
 __device__ __forceinline__ int row_queries(const AttnParams &P, int b) {
@@ -64,10 +69,10 @@ __device__ __forceinline__ int row_queries(const AttnParams &P, int b) {
 }
 
 // The own part `split` covers of a row's len entries: equal parts, rounded up
-// to 64 tokens.
+// to P.chunk tokens.
 __device__ __forceinline__ void own_range(const AttnParams &P, int len, int split, int &t0, int &t1) {
   int chunk = (len + P.osplits - 1) / P.osplits;
-  chunk = max(P.min_chunk, (chunk + 63) / 64 * 64);
+  chunk = (chunk + P.chunk - 1) / P.chunk * P.chunk;
   const long long a = static_cast<long long>(split) * chunk;
   t0 = static_cast<int>(min(a, static_cast<long long>(len)));
   t1 = static_cast<int>(min(a + chunk, static_cast<long long>(len)));
@@ -146,6 +151,9 @@ constexpr float kMinExponent = -60.f;
 constexpr float kExponentSpan = 60.f;
 
 // Host launchers.
-cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool prefix_too, cudaStream_t s);
+// attn_rows_kernel over the own entries (own) and the prefix (prefix) ...
+cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool own, bool prefix, cudaStream_t s);
+// ... and attn_tile_kernel over one of the two.
+cudaError_t launch_attn_tile(const AttnParams &p, int ctype, bool prefix, cudaStream_t s);
 
 }  // namespace sv

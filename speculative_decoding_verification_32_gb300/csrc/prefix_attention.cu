@@ -4,6 +4,7 @@
 //
 //  attn_mask_kernel -- draft trees only: checks each row's parents and turns
 //    them into ancestor bits, one thread per node walking to the root.
+//  attn_tile_kernel (prefix_attention_tile.cu) -- many query rows.
 //  attn_rows_kernel -- 16 or 32 query rows (the query heads of one KV head and
 //    the tokens of one row; for the prefix, of all rows) against a range of
 //    tokens.  Bound by the cache's bytes, so what matters is bytes in flight:
@@ -153,7 +154,10 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
     qi = b * P.N + t;
     return t < bad_or_count;
   };
+  if (!pre && split == 0 && blk == 0 && g == 0 && tid == 0 && P.row_status)
+    P.row_status[b] = bad_or_count >= 0 ? 0 : bad_or_count == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
   if (t0 >= t1) {  // nothing here (an empty part, or a row that cannot be used)
+    if (!pre && tid == 0) P.oflag[blockIdx.x - pitems] = 0;
     for (int rr = tid; rr < C::kM; rr += kRowThreads) {
       const int r = r0 + rr;
       if (r >= nrows) break;
@@ -291,6 +295,7 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
       for (int c = 0; c < 4; ++c) o[mt][n][c] = 0.f;
   }
 
+  bool odd = false;
   int st = 0;
   for (int blkno = warp; blkno < nblk; blkno += kRowWarps) {
     issue(blkno + (kRowStages - 1) * kRowWarps, (st + kRowStages - 1) % kRowStages);
@@ -477,13 +482,18 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
           o[mt][n][3] *= al[mt][1];
         }
     }
-    // --- a value that is not finite in a block that some query may not see:
-    // zero times it would be NaN.  Such elements are added by hand to the
-    // queries that see them and set to zero for the product.
-    if (masked) {
-      bool odd = false;
+    // --- values of the pass's own tokens that are not finite: a query that
+    // does not see them would get 0 * NaN.  They are taken out here and put
+    // into the answers of the queries that see them when the parts are joined.
+    if (masked && !pre) {
       const int per = P.D * C::kEsz / 4;  // words of a head vector
-      auto clean = [&](uint32_t w) -> uint32_t {  // w without its non-finite elements
+      bool bad = false;
+      for (int i = lane; i < kBlk * per; i += 32) {
+        const int tk = i / per;
+        if (tb + tk < len0) continue;
+        const uint32_t at = vst + tk * C::kPitch + (i - tk * per) * 4;
+        uint32_t w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
         uint32_t r = w;
         if constexpr (E4) {
 #pragma unroll
@@ -494,56 +504,13 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
           if ((w & top) == top) r &= 0xffff0000u;
           if ((w >> 16 & top) == top) r &= 0x0000ffffu;
         }
-        return r;
-      };
-      for (int i = lane; i < kBlk * per; i += 32) {
-        const int tk = i / per;
-        uint32_t w;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(vst + tk * C::kPitch + (i - tk * per) * 4) : "memory");
-        odd = odd || clean(w) != w;
-      }
-      if (__any_sync(FULL_MASK, odd)) {
-        for (int tk = 0; tk < kBlk; ++tk) {
-          const int src = (lane & ~3) | (tk % 8) / 2;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float w0 = 0.f, w1 = 0.f;
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-                if (n == tk / 8 && c == tk % 2) w0 = s4[mt][n][c], w1 = s4[mt][n][2 + c];
-            w0 = __shfl_sync(FULL_MASK, w0, src);
-            w1 = __shfl_sync(FULL_MASK, w1, src);
-#pragma unroll
-            for (int n = 0; n < kNt; ++n)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const int d = E4 ? (2 * j4 + c) * kNt + n : n * 8 + 2 * j4 + c;
-                float val;
-                const unsigned char *at = smem + warp * kRowStages * C::kStage + st * C::kStage + C::kPlane + tk * C::kPitch + d * C::kEsz;
-                if constexpr (E4)
-                  val = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16x2(*at))));
-                else if constexpr (BF)
-                  val = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(at));
-                else
-                  val = __half2float(*reinterpret_cast<const __half *>(at));
-                if (isfinite(val)) continue;
-                if (w0 != 0.f) o[mt][n][c] = fmaf(w0, val, o[mt][n][c]);
-                if (w1 != 0.f) o[mt][n][2 + c] = fmaf(w1, val, o[mt][n][2 + c]);
-              }
-          }
+        if (r != w) {
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(r) : "memory");
+          bad = true;
         }
-        __syncwarp();
-        for (int i = lane; i < kBlk * per; i += 32) {
-          const int tk = i / per;
-          const uint32_t at = vst + tk * C::kPitch + (i - tk * per) * 4;
-          uint32_t w;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(clean(w)) : "memory");
-        }
-        __syncwarp();
       }
+      odd = __any_sync(FULL_MASK, bad) || odd;
+      __syncwarp();
     }
     // --- weights times values
     if constexpr (E4) {
@@ -592,7 +559,8 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
 
   // --- join the warps: everyone leaves its sums in the ring's memory
   cp_async_wait_all();
-  __syncthreads();
+  odd = __syncthreads_or(odd);
+  if (!pre && tid == 0) P.oflag[blockIdx.x - pitems] = odd;
   float *const om = reinterpret_cast<float *>(smem);                  // [warp][row][DP]
   float *const mm = om + kRowWarps * C::kM * DP;                      // [warp][row]
   float *const lm = mm + kRowWarps * C::kM;
@@ -655,7 +623,7 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
 
 // ------------------------------------------------------------------- join
 // One warp per output row: the weights of the parts, then their sum.
-template <bool BF>
+template <bool BF, bool E4>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams P) {
   grid_dependency_wait();
   const int lane = threadIdx.x % 32;
@@ -664,17 +632,23 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   const int nslots = P.psplits + P.osplits;
   const int b = static_cast<int>(r / (static_cast<long long>(P.N) * P.Hq));
   const int n = row_queries(P, b);
-  if (P.row_status && r == static_cast<long long>(b) * P.N * P.Hq && lane == 0)
-    P.row_status[b] = n >= 0 ? 0 : n == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
-  const bool on = static_cast<int>(r / P.Hq) - b * P.N < n;
+  const int qt = static_cast<int>(r / P.Hq) - b * P.N, h = static_cast<int>(r % P.Hq);
+  const bool on = qt < n;
   float Z = -INFINITY;
+  bool gone = false;  // a part's kernel gave up: the row is flagged and its answer left empty
   if (on)
-    for (int s = lane; s < nslots; s += 32) Z = fmaxf(Z, P.ml[static_cast<long long>(s) * P.rows + r].y);
+    for (int s = lane; s < nslots; s += 32) {
+      const float z = P.ml[static_cast<long long>(s) * P.rows + r].y;
+      gone = gone || __float_as_uint(z) == kTimeoutBits;
+      Z = fmaxf(Z, z);
+    }
+  gone = __any_sync(FULL_MASK, gone);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) Z = fmaxf(Z, __shfl_xor_sync(FULL_MASK, Z, o));
   const float zref = Z == -INFINITY ? 0.f : Z;
   float S = 0.f;
-  if (on)
+  if (gone && lane == 0 && P.row_status) P.row_status[b] = SPEC_ROW_TIMEOUT;
+  if (on && !gone)
     for (int s = lane; s < nslots; s += 32) S += ex2(P.ml[static_cast<long long>(s) * P.rows + r].y - zref);
   S = warp_sum(S);
   const float z = S == 0.f ? -INFINITY : zref + log2f(S);
@@ -696,6 +670,34 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         }
       }
     }
+  // values that are not finite, of the pass's tokens that this query sees
+  if (S != 0.f) {
+    const int g = h / P.G, blocks = (P.N * P.G + P.oblk - 1) / P.oblk;
+    const int32_t *flag = P.oflag + ((static_cast<long long>(b) * P.H + g) * blocks + (qt * P.G + h % P.G) / P.oblk) * P.osplits;
+    bool odd = false;
+    for (int s = lane; s < P.osplits; s += 32) odd = odd || flag[s];
+    if (__any_sync(FULL_MASK, odd)) {
+      const int len0 = P.kv_len[b];
+      for (int j = 0; j < n; ++j) {
+        const bool see = P.anc ? P.anc[(static_cast<size_t>(b) * P.N + qt) * P.W + (j >> 5)] >> (j & 31) & 1u : j <= qt;
+        if (!see) continue;
+        const unsigned char *const e = P.v + b * P.row_stride + static_cast<long long>(len0 + j) * P.tok_stride;
+#pragma unroll
+        for (int i = 0; i < SPEC_MAX_HEAD_DIM / 32; ++i) {
+          const int d = i * 32 + lane;
+          if (d >= P.D) continue;
+          float val;
+          if constexpr (E4)
+            val = e[P.H * P.D + g] == 255 || (e[g * P.D + d] & 127) == 127 ? __uint_as_float(0x7fc00000u) : 0.f;
+          else if (BF)
+            val = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(e)[g * P.D + d]);
+          else
+            val = __half2float(reinterpret_cast<const __half *>(e)[g * P.D + d]);
+          if (!isfinite(val)) acc[i] += val;
+        }
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < SPEC_MAX_HEAD_DIM / 32; ++i) {
     const int d = i * 32 + lane;
@@ -711,12 +713,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 
 // -------------------------------------------------------------------- host
 template <int CT, int DP, int MT>
-cudaError_t launch_rows(const AttnParams &p, bool with_prefix, cudaStream_t s) {
+cudaError_t launch_rows(const AttnParams &p, bool own, bool prefix, cudaStream_t s) {
   using C = RowCfg<CT, DP, MT>;
   const int pblocks = static_cast<int>((static_cast<long long>(p.B) * p.N * p.G + C::kM - 1) / C::kM);
   const int oblocks = (p.N * p.G + C::kM - 1) / C::kM;
-  const long long pitems = with_prefix ? static_cast<long long>(p.H) * pblocks * p.psplits : 0;
-  const long long items = pitems + static_cast<long long>(p.B) * p.H * oblocks * p.osplits;
+  const long long pitems = prefix ? static_cast<long long>(p.H) * pblocks * p.psplits : 0;
+  const long long items = pitems + (own ? static_cast<long long>(p.B) * p.H * oblocks * p.osplits : 0);
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<CT, DP, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
@@ -724,16 +726,22 @@ cudaError_t launch_rows(const AttnParams &p, bool with_prefix, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// 16 query rows an item where no item would use more (half the sums and
+// registers), else 32.
+bool two_row_tiles(int B, int N, int G, bool prefix) { return N * G > 16 || (prefix && static_cast<long long>(B) * N * G > 16); }
+
 template <int CT>
-cudaError_t launch_rows_d(const AttnParams &p, bool with_prefix, cudaStream_t s) {
-  const bool two = p.N * p.G > 16 || (with_prefix && static_cast<long long>(p.B) * p.N * p.G > 16);
-  if (p.D <= 64) return two ? launch_rows<CT, 64, 2>(p, with_prefix, s) : launch_rows<CT, 64, 1>(p, with_prefix, s);
-  return two ? launch_rows<CT, 128, 2>(p, with_prefix, s) : launch_rows<CT, 128, 1>(p, with_prefix, s);
+cudaError_t launch_rows_d(const AttnParams &p, bool own, bool prefix, cudaStream_t s) {
+  const bool two = two_row_tiles(p.B, p.N, p.G, prefix);
+  if (p.D <= 64) return two ? launch_rows<CT, 64, 2>(p, own, prefix, s) : launch_rows<CT, 64, 1>(p, own, prefix, s);
+  return two ? launch_rows<CT, 128, 2>(p, own, prefix, s) : launch_rows<CT, 128, 1>(p, own, prefix, s);
 }
 
 struct AttnPlan {
   int psplits, pchunk, osplits, W;
-  size_t rows, anc_at, info_at, ml_at, part_at, bytes;
+  bool ptile, otile;  // attn_tile_kernel for the prefix, for the own entries
+  int oblk;           // query rows per own item
+  size_t rows, anc_at, info_at, flag_at, ml_at, part_at, bytes;
 };
 
 size_t at_round(size_t x) { return (x + 255) / 256 * 256; }
@@ -764,31 +772,51 @@ spec_status check_attention(const spec_attention_args *a) {
   return SPEC_OK;
 }
 
-// How the keys are cut into parts: enough items for two per SM, no part
-// under 64 tokens, and no more parts than 64.
+// Which kernel, and how the keys are cut into parts.
 AttnPlan plan_attention(const spec_attention_args *a) {
   AttnPlan p = {};
   const spec_kv_cache &c = a->cache;
   const long long G = a->q_heads / c.heads;
   const long long q = static_cast<long long>(c.rows) * a->N;
   p.rows = static_cast<size_t>(q) * a->q_heads;
-  auto parts = [](long long blocks, long long tokens) {
+  // more than 32 query rows per KV head would read the keys again for each 32
+  p.ptile = q * G > 32;
+  p.otile = a->N * G > 32;
+  // rows kernel: enough items for two per SM, no part under 64 tokens
+  auto row_parts = [](long long blocks, long long tokens) {
     const long long want = (2 * kSms + blocks - 1) / blocks;
     return static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 64})));
   };
+  // tile kernel (one item per SM at a time): the fewest rounds of items times
+  // their blocks of 128 tokens, an item's start and end counting as three
+  auto tile_parts = [](long long blocks, long long tokens) {
+    const long long n = (tokens + 127) / 128;
+    long long best = -1;
+    int parts = 1;
+    for (long long s = 1; s <= std::min<long long>(n, 64); ++s) {
+      const long long cost = (blocks * s + kSms - 1) / kSms * ((n + s - 1) / s + 3);
+      if (best < 0 || cost < best) best = cost, parts = static_cast<int>(s);
+    }
+    return parts;
+  };
   if (a->prefix_len > 0) {
-    const long long blocks = c.heads * ((q * G + 31) / 32);
-    p.psplits = parts(blocks, a->prefix_len);
-    p.pchunk = static_cast<int>(((a->prefix_len + p.psplits - 1) / p.psplits + 63) / 64 * 64);
+    p.psplits = p.ptile ? tile_parts(c.heads * ((q * G + 255) / 256), a->prefix_len)
+                        : row_parts(c.heads * ((q * G + 31) / 32), a->prefix_len);
+    const int unit = p.ptile ? 128 : 64;
+    p.pchunk = static_cast<int>(((a->prefix_len + p.psplits - 1) / p.psplits + unit - 1) / unit * unit);
     p.psplits = static_cast<int>((a->prefix_len + p.pchunk - 1) / p.pchunk);
   }
-  p.osplits = parts(c.rows * c.heads * ((a->N * G + 31) / 32), c.slots);
+  p.oblk = p.otile ? 256 : two_row_tiles(c.rows, a->N, static_cast<int>(G), a->prefix_len > 0 && !p.ptile) ? 32 : 16;
+  const long long oblocks = (a->N * G + p.oblk - 1) / p.oblk;
+  p.osplits = p.otile ? tile_parts(c.rows * c.heads * oblocks, c.slots) : row_parts(c.rows * c.heads * oblocks, c.slots);
   p.W = (a->N + 31) / 32;
   size_t at = 0;
   p.anc_at = at;
   at += at_round(static_cast<size_t>(q) * p.W * 4);
   p.info_at = at;
   at += at_round(static_cast<size_t>(c.rows) * 4);
+  p.flag_at = at;
+  at += at_round(static_cast<size_t>(c.rows) * c.heads * oblocks * p.osplits * 4);
   p.ml_at = at;
   const size_t slots = static_cast<size_t>(p.psplits) + p.osplits;
   at += at_round(slots * p.rows * sizeof(float2));
@@ -800,10 +828,10 @@ AttnPlan plan_attention(const spec_attention_args *a) {
 
 }  // namespace
 
-cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool with_prefix, cudaStream_t s) {
-  if (ctype == SPEC_E4M3) return launch_rows_d<SPEC_E4M3>(p, with_prefix, s);
-  if (ctype == SPEC_BF16) return launch_rows_d<SPEC_BF16>(p, with_prefix, s);
-  return launch_rows_d<SPEC_F16>(p, with_prefix, s);
+cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool own, bool prefix, cudaStream_t s) {
+  if (ctype == SPEC_E4M3) return launch_rows_d<SPEC_E4M3>(p, own, prefix, s);
+  if (ctype == SPEC_BF16) return launch_rows_d<SPEC_BF16>(p, own, prefix, s);
+  return launch_rows_d<SPEC_F16>(p, own, prefix, s);
 }
 
 }  // namespace sv
@@ -867,12 +895,15 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   p.psplits = plan.psplits;
   p.pchunk = plan.pchunk;
   p.osplits = plan.osplits;
-  p.min_chunk = 64;
+  p.chunk = plan.otile ? 128 : 64;
+  p.oblk = plan.oblk;
+  p.oflag = reinterpret_cast<int32_t *>(w + plan.flag_at);
   p.out = out;
   p.lse = lse;
   p.row_status = row_status;
   p.qbf16 = a->q_dtype == SPEC_BF16;
   p.wait_limit_ns = spec_get_wait_timeout_ns();
+  p.force_timeout = force_wait_timeout();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->parent) {
     uint32_t *anc = reinterpret_cast<uint32_t *>(w + plan.anc_at);
@@ -882,7 +913,12 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
     p.anc = anc;
     p.rowinfo = info;
   }
-  if (launch_attn_rows(p, c.dtype, p.P > 0, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  const bool prefix = p.P > 0;
+  if (prefix && plan.ptile && launch_attn_tile(p, c.dtype, true, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (plan.otile && launch_attn_tile(p, c.dtype, false, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  if ((!plan.otile || (prefix && !plan.ptile)) &&
+      launch_attn_rows(p, c.dtype, !plan.otile, prefix && !plan.ptile, s) != cudaSuccess)
+    return SPEC_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
   cfg.blockDim = dim3(kJoinThreads);
@@ -892,8 +928,11 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = p.qbf16 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true>, p)
-                                : cudaLaunchKernelEx(&cfg, attn_join_kernel<false>, p);
+  const bool e4 = c.dtype == SPEC_E4M3;
+  const cudaError_t e = p.qbf16 ? (e4 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true, true>, p)
+                                      : cudaLaunchKernelEx(&cfg, attn_join_kernel<true, false>, p))
+                                : (e4 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<false, true>, p)
+                                      : cudaLaunchKernelEx(&cfg, attn_join_kernel<false, false>, p));
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

@@ -1,0 +1,708 @@
+// prefix_attention_tile.cu -- spec_prefix_attention for many query rows:
+// two tiles of 128 query rows of one KV head against a range of tokens, on
+// the 5th-generation tensor cores.
+//
+// For 256 rows the two products cost 4 * 256 * D operations per token and head,
+// about as long on the tensor cores as the softmax's exponentials between
+// them, while the cache's bytes come mostly from L2 (every block of 256 rows
+// reads the same prefix).  So the kernel is laid out to keep the tensor cores
+// fed while the softmax runs:
+//   - a CTA holds two row tiles A and B.  One thread issues, for each block of
+//     128 tokens, W V and then the next Q K^T of tile A, then those of tile B;
+//     while the tensor cores work on one tile, a warpgroup does the other's
+//     softmax;
+//   - scores, weights and sums stay in tensor memory (scores of A and B at
+//     columns 0 and 128, sums at 256 and 384); the weights take the place of
+//     the scores and are the product's left operand from there;
+//   - a thread owns a row, so its softmax needs no exchange.  The sums are
+//     rescaled only when a row's maximum has grown by more than 2^8 since
+//     the last time: weights up to 2^8 are as exact as weights up to 1;
+//   - four warps bring keys and values into shared memory, two buffers each:
+//     16-bit entries by asynchronous copies, e4m3 codes through registers as
+//     fp16 numbers relative to the block's largest scale (exact for scales
+//     down to 2^-15 of it, off by at most 2^-25 of it below), so that the
+//     block's scale is one factor on the scores and one on the sums.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attention.cuh"
+#include "internal.h"
+
+namespace sv {
+namespace {
+
+constexpr int kTok = 128;          // tokens per block
+constexpr int kTileThreads = 512;  // softmax A, softmax B, producers, tensor-core issue
+constexpr int kProducers = 128;
+constexpr float kLazy = 8.f;       // log2 of the growth a row's maximum may make before its sums follow
+// registers per thread of the roles: 2 x 184 + 104 + 40 = 4 x 128, what the block is launched with
+constexpr int kRegsSoftmax = 184, kRegsProduce = 104, kRegsIssue = 40;
+
+template <int DP>
+struct TileCfg {
+  static constexpr int kOp = kTok * DP * 2;  // an operand tile: 128 rows, 64-column panels of 16 KB
+  static constexpr int kQ = 0;               // tiles A and B
+  static constexpr int kK = 2 * kOp;         // two buffers
+  static constexpr int kV = 4 * kOp;         // two buffers
+  static constexpr int kCtrl = 6 * kOp;
+  static constexpr int kSmem = kCtrl + 4096 + 1024;  // + control block + alignment
+};
+
+struct Ctrl {
+  uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
+  uint64_t sfull[2], pfull[2], done[2], drain;
+  uint32_t tmem;
+  int abort;
+  int odd;
+  int pad;
+  float ksc[2];             // per buffer: the block's scale of the keys
+  float vex[2], vtop[2];    // the values' exponent, and the largest so far
+  uint32_t red[2][4];       // producers' reductions
+  float qfac[256];
+};
+static_assert(sizeof(Ctrl) <= 4096, "control block");
+
+// ------------------------------------------------------------ tcgen05 wrappers
+__device__ __forceinline__ void tc_alloc(uint32_t *dst) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tc_dealloc(uint32_t tmem) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D (tensor memory) = A (shared) B (shared) [+ D]
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+// D (tensor memory) = A (tensor memory) B (shared) [+ D]
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+// 32 columns of this thread's lane
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle: rows of 128 bytes in
+// groups of 8 (1024 bytes).  A tile of rows x 64 columns is one panel; for an
+// operand whose 64-column direction is the product's M or N (the values), the
+// leading offset is the distance of two panels.
+__device__ __forceinline__ uint64_t op_desc(uint32_t addr, uint32_t panel) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | static_cast<uint64_t>(panel >> 4) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// Instruction descriptor: fp32 sums, 16-bit operands, M = 128.
+__device__ __forceinline__ uint32_t inst_desc(bool bf16, int n, bool b_cols) {
+  const uint32_t f = bf16 ? 1u : 0u;
+  return 1u << 4 | f << 7 | f << 10 | (b_cols ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void producer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Bounded wait that also ends when another role has given up.
+__device__ __forceinline__ bool wait_for(Ctrl *c, uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity, 10000)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity, 10000)) return true;
+    if (*reinterpret_cast<volatile int *>(&c->abort)) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *reinterpret_cast<volatile int *>(&c->abort) = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+__device__ __forceinline__ void st_global_v8(float *p, const uint32_t *r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Item: prefix (PRE): KV head, block of 256 rows of all rows' queries, part;
+// own: row, KV head, block of 256 of the row's queries, part.
+template <int CT, int DP, bool PRE>
+__global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid_constant__ AttnParams P, int blocks) {
+  using C = TileCfg<DP>;
+  constexpr bool E4 = CT == SPEC_E4M3, BF = CT == SPEC_BF16;
+  extern __shared__ unsigned char raw[];
+  unsigned char *const smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Ctrl *const c = reinterpret_cast<Ctrl *>(smem + C::kCtrl);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, role = tid / 128;
+
+  // --- the item
+  int item = blockIdx.x;
+  const int nsplit = PRE ? P.psplits : P.osplits;
+  const int split = item % nsplit;
+  item /= nsplit;
+  const int blk = item % blocks;
+  item /= blocks;
+  const int g = PRE ? item : item % P.H;
+  const int b = PRE ? 0 : item / P.H;
+  const int r0 = blk * 256;
+  const int nrows = (PRE ? P.B : 1) * P.N * P.G;
+  const int slot = PRE ? split : P.psplits + split;
+  int t0, t1, len0 = 0x7fffffff, cnt = 0;
+  if constexpr (PRE) {
+    t0 = split * P.pchunk;
+    t1 = min(P.P, t0 + P.pchunk);
+  } else {
+    cnt = row_queries(P, b);
+    len0 = __ldg(P.kv_len + b);
+    if (split == 0 && blk == 0 && g == 0 && tid == 0 && P.row_status)
+      P.row_status[b] = cnt >= 0 ? 0 : cnt == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
+    if (cnt <= 0)
+      t0 = t1 = 0;
+    else
+      own_range(P, len0 + cnt, split, t0, t1);
+  }
+  const unsigned char *const kb = PRE ? P.pk : P.k + b * P.row_stride;
+  const unsigned char *const vb = PRE ? P.pv : P.v + b * P.row_stride;
+  const long long ts = PRE ? P.ptok_stride : P.tok_stride;
+  const int n = (t1 - t0 + kTok - 1) / kTok;        // blocks of tokens
+  const int tiles = nrows - r0 > 128 ? 2 : 1;       // row tiles in use
+  // query row rr of the block -> its token (flat index) and head; false if it has no use
+  auto decode = [&](int rr, int &qi, int &h) -> bool {
+    const int r = r0 + rr;
+    if (r >= nrows) return false;
+    const int t = r / P.G;
+    h = g * P.G + (r - t * P.G);
+    if constexpr (PRE) {
+      qi = t;
+      const int rb = t / P.N;
+      return t - rb * P.N < row_queries(P, rb);
+    } else {
+      qi = b * P.N + t;
+      return t < cnt;
+    }
+  };
+  if (n == 0) {  // nothing here (an empty part, or a row that cannot be used)
+    if (tid < 256 && r0 + tid < nrows) {
+      int qi, h;
+      decode(tid, qi, h);
+      P.ml[static_cast<long long>(slot) * P.rows + static_cast<long long>(qi) * P.Hq + h] = make_float2(-INFINITY, -INFINITY);
+    }
+    if (!PRE && tid == 0) P.oflag[blockIdx.x] = 0;
+    return;
+  }
+
+  // --- set up: barriers, tensor memory, queries
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c->kfull[i], kProducers);
+      mbar_init(&c->vfull[i], kProducers);
+      mbar_init(&c->kfree[i], 1);
+      mbar_init(&c->vfree[i], 1);
+      mbar_init(&c->sfull[i], 1);
+      mbar_init(&c->pfull[i], 128);
+      mbar_init(&c->done[i], 1);
+    }
+    mbar_init(&c->drain, 1);
+    c->abort = 0;
+    c->odd = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) tc_alloc(&c->tmem);
+  {
+    // DP/8 lanes per row, 16 bytes of the operand each; fp16 for an e4m3
+    // cache: a row far outside fp16's range is brought into it by a power of
+    // two.  A negative scale turns the queries' sign.
+    constexpr int L = DP / 8;
+    const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
+    for (int i = tid; i < 256 * L; i += kTileThreads) {
+      const int rr = i / L, pc = i % L;
+      int qi = 0, h = 0;
+      const bool on = decode(rr, qi, h) && pc * 8 < P.D;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (on) {
+        const int qb = qi / P.N, qt = qi - qb * P.N;
+        const unsigned short *q = static_cast<const unsigned short *>(P.q) + qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2] + pc * 8;
+        if (vec) {
+          u = __ldg(reinterpret_cast<const uint4 *>(q));
+        } else {
+          u.x = q[0] | static_cast<uint32_t>(q[1]) << 16;
+          u.y = q[2] | static_cast<uint32_t>(q[3]) << 16;
+          u.z = q[4] | static_cast<uint32_t>(q[5]) << 16;
+          u.w = q[6] | static_cast<uint32_t>(q[7]) << 16;
+        }
+      }
+      if (E4 && P.qbf16) {
+        float x[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y), bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
+        uint32_t a = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
+        float fac = 1.f, by = 1.f;
+        const int e = static_cast<int>(a >> 23) - 127;
+        if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
+          const int up = max(-126, min(126, -e));
+          by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+          fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
+        u = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
+                       pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
+        if (pc == 0) c->qfac[rr] = fac;
+      } else if (pc == 0) {
+        c->qfac[rr] = 1.f;
+      }
+      if (P.scale < 0.f) u.x ^= 0x80008000u, u.y ^= 0x80008000u, u.z ^= 0x80008000u, u.w ^= 0x80008000u;
+      *reinterpret_cast<uint4 *>(smem + C::kQ + (rr / 128) * C::kOp + (pc / 8) * 16384 + (rr % 128) * 128 + (((pc % 8) ^ (rr & 7)) << 4)) = u;
+    }
+  }
+  fence_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem;
+  const uint64_t limit = P.wait_limit_ns;
+
+  if (role == 2) {
+    // ------------------------------------------------------------ producers
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProduce));
+    const int pt = tid - 256;
+    bool live = true;
+    if constexpr (!E4) {
+      constexpr int L = DP / 8, kPer = L;  // 16-byte pieces per row; pieces per thread and operand tile
+      constexpr int kStep = kProducers / L;
+      const int pc = pt % L, row0 = pt / L;
+      const bool col = pc * 8 < P.D;
+      const uint32_t dst0 = smem_u32(smem) + (pc / 8) * 16384 + row0 * 128 + (((pc % 8) ^ (row0 & 7)) << 4);
+      const long long src0 = static_cast<long long>(g) * P.D * 2 + pc * 16;
+      // item 2k: keys of block k, item 2k + 1: its values
+      auto issue = [&](int it) {
+        if (it < 2 * n && live) {
+          const int k = it >> 1, s = k & 1;
+          uint64_t *const fr = it & 1 ? &c->vfree[s] : &c->kfree[s];
+          if (k >= 2) live = wait_for(c, fr, ((k >> 1) - 1) & 1, limit);
+          if (live) {
+            const unsigned char *const src = (it & 1 ? vb : kb) + src0;
+            const uint32_t dst = dst0 + (it & 1 ? C::kV : C::kK) + s * C::kOp;
+            const int tb = t0 + k * kTok;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+              const int t = tb + row0 + i * kStep;
+              const bool on = col && t < t1;
+              cp_async16_zfill(dst + i * kStep * 128, src + static_cast<long long>(on ? t : t0) * ts - (on ? 0 : pc * 16), on);
+            }
+          }
+        }
+        cp_async_commit();
+      };
+      issue(0);
+      issue(1);
+      for (int it = 0; it < 2 * n; ++it) {
+        issue(it + 2);
+        cp_async_wait<2>();
+        const int k = it >> 1, s = k & 1;
+        if (!PRE && (it & 1) && live) {
+          // values of the pass's own tokens that are not finite: a query that
+          // does not see them would get 0 * NaN.  They are taken out here and
+          // put into the answers of the queries that see them when the parts
+          // are joined.
+          const int tb = t0 + k * kTok;
+          if (tb + kTok > len0) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+              const int t = tb + row0 + i * kStep;
+              if (t < len0 || t >= t1) continue;
+              const uint32_t at = dst0 + C::kV + s * C::kOp + i * kStep * 128;
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+              bool odd = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
+                if ((w[e] & top) == top) w[e] &= 0xffff0000u, odd = true;
+                if ((w[e] >> 16 & top) == top) w[e] &= 0x0000ffffu, odd = true;
+              }
+              if (odd) {
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+                c->odd = 1;
+              }
+            }
+          }
+        }
+        fence_async_smem();
+        if (!(P.force_timeout && it == 0)) mbar_arrive(it & 1 ? &c->vfull[s] : &c->kfull[s]);
+      }
+      cp_async_wait_all();
+    } else {
+      constexpr int L = DP / 16, kPer = L;  // 16-code pieces per row; pieces per thread and operand tile
+      constexpr int kStep = kProducers / L;
+      const int pc = pt % L, row0 = pt / L;
+      const bool col = pc * 16 < P.D;
+      const long long src0 = static_cast<long long>(g) * P.D + (col ? pc * 16 : 0);
+      const long long sc0 = static_cast<long long>(P.H) * P.D + g;
+      uint4 w[kPer], wn[kPer];
+      uint32_t sc[kPer], scn[kPer];
+      auto fetch = [&](int it, uint4 (&x)[kPer], uint32_t (&y)[kPer]) {
+        const int tb = t0 + (it >> 1) * kTok;
+        const unsigned char *const base = it & 1 ? vb : kb;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int t = tb + row0 + i * kStep;
+          x[i] = make_uint4(0, 0, 0, 0);
+          y[i] = 0;
+          if (t < t1) {
+            const unsigned char *const e = base + static_cast<long long>(t) * ts;
+            if (col) x[i] = __ldg(reinterpret_cast<const uint4 *>(e + src0));
+            y[i] = __ldg(e + sc0);
+          }
+        }
+      };
+      float E = kMinExponent, kscale = 1.f;
+      fetch(0, w, sc);
+      for (int it = 0; it < 2 * n; ++it) {
+        if (it + 1 < 2 * n) fetch(it + 1, wn, scn);
+        const int k = it >> 1, s = k & 1;
+        const bool val = it & 1;
+        // the block's largest scale
+        uint32_t top = 1;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (sc[i] != 255u) top = max(top, sc[i]);
+        top = __reduce_max_sync(FULL_MASK, top);
+        if (lane == 0) c->red[it & 1][warp & 3] = top;
+        producer_sync();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, c->red[it & 1][i]);
+        float ex = static_cast<float>(static_cast<int>(top) - 127);
+        if (val) {
+          E = fmaxf(E, ex);
+          ex = fmaxf(ex, E - kExponentSpan);
+        }
+        const int ref = static_cast<int>(ex) + 127;
+        if (k >= 2 && live) live = wait_for(c, val ? &c->vfree[s] : &c->kfree[s], ((k >> 1) - 1) & 1, limit);
+        if (live) {
+          unsigned char *const dst = smem + (val ? C::kV : C::kK) + s * C::kOp + (pc / 4) * 16384;
+          const int tb = t0 + k * kTok;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int row = row0 + i * kStep;
+            // 2^(scale - block's scale) as fp16: exact down to 2^-24, zero below
+            const int d = static_cast<int>(sc[i]) - ref;
+            const uint32_t f = sc[i] == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+            const __half2 f2 = __halves2half2(__ushort_as_half(static_cast<unsigned short>(f)), __ushort_as_half(static_cast<unsigned short>(f)));
+            const uint32_t cw[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t lo = e4m3x2_to_f16x2(cw[e]), hi = e4m3x2_to_f16x2_hi(cw[e]);
+              const __half2 l2 = __hmul2(*reinterpret_cast<const __half2 *>(&lo), f2);
+              const __half2 h2 = __hmul2(*reinterpret_cast<const __half2 *>(&hi), f2);
+              o[2 * e] = *reinterpret_cast<const uint32_t *>(&l2);
+              o[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&h2);
+            }
+            if (!PRE && val && tb + row >= len0) {  // as for 16-bit entries
+              bool odd = false;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if ((o[e] & 0x7c00u) == 0x7c00u) o[e] &= 0xffff0000u, odd = true;
+                if ((o[e] >> 16 & 0x7c00u) == 0x7c00u) o[e] &= 0x0000ffffu, odd = true;
+              }
+              if (odd) c->odd = 1;
+            }
+            // the two 16-byte halves, the upper panel's lanes in the other
+            // order: eight lanes then cover all banks
+            const int ch = (pc % 4) * 2, first = pc / 4;
+            unsigned char *const at = dst + row * 128;
+            const uint4 h0 = make_uint4(o[0], o[1], o[2], o[3]), h1 = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4 *>(at + (((ch + first) ^ (row & 7)) << 4)) = first ? h1 : h0;
+            *reinterpret_cast<uint4 *>(at + (((ch + 1 - first) ^ (row & 7)) << 4)) = first ? h0 : h1;
+          }
+          // the keys' scale goes with the values' exponents: the softmax waits
+          // for the values' buffer, which it holds until it is done
+          if (!val) kscale = e4m3_scale(top);
+          if (val && pt == 0) {
+            c->ksc[s] = kscale;
+            c->vex[s] = ex;
+            c->vtop[s] = E;
+          }
+        }
+        fence_async_smem();
+        if (!(P.force_timeout && it == 0)) mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          w[i] = wn[i];
+          sc[i] = scn[i];
+        }
+      }
+    }
+  } else if (role == 3) {
+    // ------------------------------------------------- tensor-core issue
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 12 && lane == 0) {
+      const uint32_t qk = inst_desc(BF, kTok, false), wv = inst_desc(BF, DP, true);
+      const uint32_t base = smem_u32(smem);
+      auto scores = [&](int tile, int k) {
+        const uint32_t q = base + C::kQ + tile * C::kOp, kk = base + C::kK + (k & 1) * C::kOp;
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+          const uint32_t off = (d / 4) * 16384 + (d % 4) * 32;
+          tc_mma_ss(tmem + tile * 128, op_desc(q + off, 16), op_desc(kk + off, 16), qk, d > 0);
+        }
+        tc_commit(&c->sfull[tile]);
+      };
+      auto values = [&](int tile, int k) {
+        const uint32_t vv = base + C::kV + (k & 1) * C::kOp;
+#pragma unroll
+        for (int j = 0; j < kTok / 16; ++j)
+          tc_mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + j * 8, op_desc(vv + j * 2048, 16384), wv, k > 0 || j > 0);
+      };
+      bool live = wait_for(c, &c->kfull[0], 0, limit);
+      if (live) {
+        tc_fence_after();
+        for (int t = 0; t < tiles; ++t) scores(t, 0);
+        tc_commit(&c->kfree[0]);
+      }
+      for (int k = 0; k < n && live; ++k) {
+        for (int t = 0; t < tiles && live; ++t) {
+          live = wait_for(c, &c->pfull[t], k & 1, limit);
+          if (live && t == 0) live = wait_for(c, &c->vfull[k & 1], (k >> 1) & 1, limit);
+          if (!live) break;
+          tc_fence_after();
+          values(t, k);
+          if (k + 1 < n) {
+            if (t == 0) live = wait_for(c, &c->kfull[(k + 1) & 1], ((k + 1) >> 1) & 1, limit);
+            if (!live) break;
+            tc_fence_after();
+            scores(t, k + 1);
+          } else {
+            tc_commit(&c->done[t]);
+          }
+        }
+        if (live) {
+          tc_commit(&c->vfree[k & 1]);
+          if (k + 1 < n) tc_commit(&c->kfree[(k + 1) & 1]);
+        }
+      }
+      if (!live) {  // let what was issued end before tensor memory is given back
+        tc_commit(&c->drain);
+        mbar_wait_bounded(&c->drain, 0, limit);
+      }
+    }
+  } else {
+    // --------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int tile = role;
+    if (tile < tiles) {
+      const int rr = tid;  // row of the block (tile * 128 + lane of tensor memory)
+      int qi = 0, h = 0;
+      const bool on = decode(rr, qi, h);
+      const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+      const uint32_t s_addr = lane_addr + tile * 128, o_addr = lane_addr + 256 + tile * 128;
+      const float base_sc = fabsf(P.scale) * (E4 ? c->qfac[rr] : 1.f);
+      const int my = PRE ? 0 : min((r0 + rr) / P.G, P.N - 1);  // the row's token
+      const uint32_t *const anc = PRE || !P.anc ? nullptr : P.anc + (static_cast<size_t>(b) * P.N + my) * P.W;
+      float m = -INFINITY, l = 0.f, E = E4 ? kMinExponent : 0.f;
+      bool live = true;
+      for (int k = 0; k < n; ++k) {
+        live = wait_for(c, &c->sfull[tile], k & 1, limit);
+        float ex = 0.f, sc = base_sc, grow = 0.f;
+        if constexpr (E4) {
+          if (live) live = wait_for(c, &c->vfull[k & 1], (k >> 1) & 1, limit);
+          sc *= c->ksc[k & 1];
+          ex = c->vex[k & 1];
+          const float En = c->vtop[k & 1];
+          grow = En - E;
+          E = En;
+        }
+        sc = fmaxf(sc, 1e-37f);  // not zero: a token that is not seen has the score -inf
+        live = __all_sync(FULL_MASK, live);
+        if (!live) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tc_ld32(s[q], s_addr + q * 32);
+        tc_wait_ld();
+        const int tb = t0 + k * kTok;
+        if (tb + kTok > t1 || (!PRE && tb + kTok > len0)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int tq = tb + q * 32;
+            uint32_t bits;  // tokens tq .. tq + 31 this row sees
+            if (PRE || !anc) {
+              const int see = (PRE ? t1 : min(t1, len0 + my + 1)) - tq;
+              bits = see >= 32 ? 0xffffffffu : see <= 0 ? 0u : (1u << see) - 1u;
+            } else {
+              const int j = tq - len0;  // first token's index among the pass's own
+              if (j <= -32) {
+                bits = 0xffffffffu;
+              } else if (j < 0) {
+                bits = ((1u << -j) - 1u) | __ldg(anc) << -j;
+              } else {
+                const int wd = j >> 5;
+                const uint32_t lo = wd < P.W ? __ldg(anc + wd) : 0u, hi = wd + 1 < P.W ? __ldg(anc + wd + 1) : 0u;
+                bits = __funnelshift_r(lo, hi, j & 31);
+              }
+              const int in = t1 - tq;
+              if (in < 32) bits &= in <= 0 ? 0u : (1u << in) - 1u;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(bits >> j & 1)) s[q][j] = 0xff800000u;
+          }
+        }
+        float mq[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mq[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+          for (int j = 1; j < 31; j += 2) mq[q] = max3(mq[q], __uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1]));
+          mq[q] = fmaxf(mq[q], __uint_as_float(s[q][31]));
+        }
+        const float top = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        const float mt = top == -INFINITY ? -INFINITY : fmaf(top, sc, ex);
+        float al = 1.f;
+        const float old = m;
+        if (mt > m + kLazy || m == -INFINITY) {
+          al = mt == -INFINITY ? 1.f : ex2(m - mt);
+          m = mt;
+        }
+        if (k > 0 && __any_sync(FULL_MASK, al != 1.f)) {
+#pragma unroll
+          for (int q = 0; q < DP / 32; ++q) {
+            uint32_t o[32];
+            tc_ld32(o, o_addr + q * 32);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+            tc_st32(o_addr + q * 32, o);
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float2 sc2 = make_float2(sc, sc), off2 = make_float2(ex - ref, ex - ref);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = ffma2(make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), sc2, off2);
+            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+            sum[j & 1] = fadd2(sum[j & 1], p);
+            pk[j] = pack16<BF>(p.x, p.y);
+          }
+          tc_st16(s_addr + q * 16, pk);
+        }
+        const float add = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        if constexpr (E4) {
+          // l counts in units of 2^(m - E)
+          const float ll = grow != 0.f ? (old == -INFINITY ? 0.f : ex2(old - m + grow)) : al;
+          l = fmaf(l, ll, add * ex2(E - ex));
+        } else {
+          l = fmaf(l, al, add);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&c->pfull[tile]);
+      }
+      if (live) live = __all_sync(FULL_MASK, wait_for(c, &c->done[tile], 0, limit));
+      const long long orow = static_cast<long long>(qi) * P.Hq + h;
+      const bool have = r0 + rr < nrows;
+      if (!live) {
+        if (have) P.ml[static_cast<long long>(slot) * P.rows + orow] = make_float2(-INFINITY, __uint_as_float(kTimeoutBits));
+      } else {
+        tc_fence_after();
+        const float z = l == 0.f ? -INFINITY : m + log2f(l) - E;
+        const bool some = on && l != 0.f;
+        if (have) P.ml[static_cast<long long>(slot) * P.rows + orow] = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
+        float *const to = P.part + (static_cast<long long>(slot) * P.rows + orow) * P.D;
+#pragma unroll
+        for (int q = 0; q < DP / 32; ++q) {
+          uint32_t o[32];
+          tc_ld32(o, o_addr + q * 32);
+          tc_wait_ld();
+          if (some) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              if (q * 32 + j < P.D) st_global_v8(to + q * 32 + j, o + j);
+          }
+        }
+        tc_fence_before();
+      }
+    }
+  }
+  __syncthreads();
+  if (!PRE && tid == 0) P.oflag[blockIdx.x] = c->odd;
+  if (warp == 12) {
+    __syncwarp();
+    tc_fence_after();
+    tc_dealloc(tmem);
+  }
+}
+
+template <int CT, int DP, bool PRE>
+cudaError_t launch(const AttnParams &p, cudaStream_t s) {
+  using C = TileCfg<DP>;
+  const int blocks = static_cast<int>(((PRE ? static_cast<long long>(p.B) : 1LL) * p.N * p.G + 255) / 256);
+  const long long items = PRE ? static_cast<long long>(p.H) * blocks * p.psplits : static_cast<long long>(p.B) * p.H * blocks * p.osplits;
+  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<CT, DP, PRE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  attn_tile_kernel<CT, DP, PRE><<<static_cast<unsigned>(items), kTileThreads, C::kSmem, s>>>(p, blocks);
+  return cudaGetLastError();
+}
+
+template <int CT>
+cudaError_t launch_d(const AttnParams &p, bool prefix, cudaStream_t s) {
+  if (p.D <= 64) return prefix ? launch<CT, 64, true>(p, s) : launch<CT, 64, false>(p, s);
+  return prefix ? launch<CT, 128, true>(p, s) : launch<CT, 128, false>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tile(const AttnParams &p, int ctype, bool prefix, cudaStream_t s) {
+  if (ctype == SPEC_E4M3) return launch_d<SPEC_E4M3>(p, prefix, s);
+  if (ctype == SPEC_BF16) return launch_d<SPEC_BF16>(p, prefix, s);
+  return launch_d<SPEC_F16>(p, prefix, s);
+}
+
+}  // namespace sv

@@ -346,3 +346,50 @@ def test_on_another_stream_and_in_a_graph(sv):
     p.qx = p.q.cpu().double().numpy()
     want, _ = p.check()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kind,qt", KINDS)
+@pytest.mark.parametrize("B,N,Hq,H,D,P,lens,tree", [
+    (43, 3, 8, 2, 128, 1000, list(range(0, 129, 3)), False),   # three blocks of 256 rows, a ragged last one
+    (16, 2, 8, 1, 64, 4097, [0] * 16, False),                  # exactly one block; one token in the last block of tokens
+    (2, 33, 16, 2, 128, 128, [127, 128], True),                # trees over block borders
+    (1, 200, 8, 1, 64, 0, [300], True),                        # 1600 rows of one tree
+    (2, 64, 8, 2, 96, 500, [64, 1], False),
+    (40, 1, 16, 2, 48, 256, [5] * 40, False),
+])
+def test_many_query_rows(sv, kind, qt, B, N, Hq, H, D, P, lens, tree):
+    Problem(sv, B, N, Hq, H, D, P, lens, kind, qt, tree, seed=B + N).check(rows=sorted({0, B // 2, B - 1}))
+
+
+@pytest.mark.parametrize("kind,qt", KINDS)
+def test_prefix_weights_far_apart(sv, kind, qt):
+    """Scores that grow along the prefix (the sums have to follow) and large queries; a negative and a zero scale."""
+    p = Problem(sv, 24, 2, 8, 2, 128, 3000, [10] * 24, kind, qt, seed=77, qsize=8.0)
+    p.check(rows=[0, 23])
+    for scale in (-0.05, 0.0):
+        p.scale = scale
+        call = p.call
+        p.call = lambda **kw: call(scale=scale, **kw)
+        p.check(rows=[3])
+        p.call = call
+
+
+def test_a_wait_that_runs_out_is_reported(sv):
+    """The tile kernel's waits are bounded: with one arrival withheld its rows report a timeout."""
+    import torch
+    limit = sv.get_wait_timeout_ns()
+    for kind in ("bfloat16", "uint8"):
+        p = Problem(sv, 24, 2, 8, 2, 128, 300, [10] * 24, kind, "bfloat16", seed=78)
+        out0, lse0 = p.check(rows=[0])
+        try:
+            sv.set_wait_timeout_ns(2_000_000)
+            sv.debug_force_wait_timeout(True)
+            out, lse, st = p.call()
+            torch.cuda.synchronize()
+        finally:
+            sv.debug_force_wait_timeout(False)
+            sv.set_wait_timeout_ns(limit)
+        assert st.tolist() == [6] * 24
+        assert float(out.abs().max()) == 0.0 and bool((lse == float("-inf")).all())
+        out, lse, st = p.call()
+        assert st.tolist() == [0] * 24 and torch.equal(out, out0) and torch.equal(lse, lse0)
