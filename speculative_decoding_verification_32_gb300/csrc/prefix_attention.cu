@@ -29,9 +29,8 @@ namespace sv {
 namespace {
 
 constexpr int kSms = 152;           // parts are sized for this many SMs
-constexpr int kRowWarps = 4;        // warps of attn_rows_kernel, each with its own ring
+constexpr int kRowWarps = 8;        // warps of attn_rows_kernel, each with its own ring
 constexpr int kRowThreads = 32 * kRowWarps;
-constexpr int kRowStages = 4;
 constexpr int kBlk = 16;            // tokens per block
 constexpr int kMaskThreads = 256;
 constexpr int kJoinThreads = 256;
@@ -75,13 +74,14 @@ template <int CT, int DP, int MT>
 struct RowCfg {
   static constexpr bool E4 = CT == SPEC_E4M3;
   static constexpr int kEsz = E4 ? 1 : 2;
+  static constexpr int kStages = E4 ? 4 : 3;                // 24 KB and 26 KB a warp at most
   static constexpr int kPitch = DP * kEsz + 16;             // bytes of one token in a ring slot
   static constexpr int kPlane = kBlk * kPitch;              // K or V of a block
   static constexpr int kScales = E4 ? 2 * kBlk * 4 : 0;     // scale words, K then V
   static constexpr int kStage = 2 * kPlane + kScales;
   static constexpr int kQPitch = DP * 2 + 16;
   static constexpr int kM = 16 * MT;
-  static constexpr int kRing = kRowWarps * kRowStages * kStage;
+  static constexpr int kRing = kRowWarps * kStages * kStage;
   static constexpr int kMerge = kRowWarps * kM * (DP + 2) * 4;  // the warps' sums, after the loop
   static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
   static constexpr int kSmem = kBody + kM * kQPitch + kM * 4;
@@ -140,111 +140,129 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
       own_range(P, len0 + bad_or_count, split, t0, t1);
     kb = P.k + b * P.row_stride, vb = P.v + b * P.row_stride, ts = P.tok_stride;
   }
-  // query row rr of the block -> its token's flat index (b * N + i) and head; false if it has no use
-  auto decode = [&](int rr, int &qi, int &h) -> bool {
-    const int r = r0 + rr;
-    if (r >= nrows) return false;
-    const int t = r / P.G;
-    h = g * P.G + (r - t * P.G);
-    if (pre) {
-      qi = t;
-      const int rb = t / P.N;
-      return t - rb * P.N < row_queries(P, rb);
+  // Lane i of every warp knows query row i of the block (kM <= 32): its output
+  // row (-1 past the last), whether there is such a query, where it is.
+  int my_row = -1, my_tok = 0;
+  bool my_use = false;
+  long long my_q = 0;
+  {
+    const int r = r0 + lane;
+    if (lane < C::kM && r < nrows) {
+      const int t = r / P.G, h = g * P.G + (r - t * P.G);
+      const int qb = pre ? t / P.N : b, qt = pre ? t - qb * P.N : t;
+      my_row = (qb * P.N + qt) * P.Hq + h;
+      my_tok = qt;
+      my_use = qt < (pre ? row_queries(P, qb) : bad_or_count);
+      my_q = qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2];
     }
-    qi = b * P.N + t;
-    return t < bad_or_count;
-  };
+  }
   if (!pre && split == 0 && blk == 0 && g == 0 && tid == 0 && P.row_status)
     P.row_status[b] = bad_or_count >= 0 ? 0 : bad_or_count == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
   if (t0 >= t1) {  // nothing here (an empty part, or a row that cannot be used)
     if (!pre && tid == 0) P.oflag[blockIdx.x - pitems] = 0;
-    for (int rr = tid; rr < C::kM; rr += kRowThreads) {
-      const int r = r0 + rr;
-      if (r >= nrows) break;
-      const int t = r / P.G;
-      const long long orow = (static_cast<long long>(pre ? 0 : b) * P.N + t) * P.Hq + g * P.G + (r - t * P.G);
-      P.ml[static_cast<long long>(slot) * P.rows + orow] = make_float2(-INFINITY, -INFINITY);
-    }
+    if (warp == 0 && my_row >= 0) P.ml[static_cast<long long>(slot) * P.rows + my_row] = make_float2(-INFINITY, -INFINITY);
     return;
   }
 
   // --- this warp's ring of token blocks
-  const uint32_t ring = smem_u32(smem) + warp * kRowStages * C::kStage;
+  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage;
   const int nblk = (t1 - t0 + kBlk - 1) / kBlk;
-  const int pieces = P.D * C::kEsz / 16;  // 16-byte pieces of a head vector
-  const long long head_off = static_cast<long long>(g) * P.D * C::kEsz;
-  const long long scale_off = static_cast<long long>(P.H) * P.D + (g & ~3);
+  // lanes over a token's 16-byte pieces, then over tokens; pointers advance
+  constexpr int L = DP * C::kEsz / 16, kPer = kBlk * L / 32, kStep = 32 / L;
+  const int pc = lane % L, row0 = lane / L;
+  const bool col = pc * 16 < P.D * C::kEsz;
+  const long long first = static_cast<long long>(t0 + warp * kBlk + row0) * ts +
+                          static_cast<long long>(g) * P.D * C::kEsz + (col ? pc * 16 : 0);
+  const unsigned char *kp = kb + first, *vp = vb + first;
+  const long long step = ts * kStep, jump = ts * (kRowWarps * kBlk);
+  const unsigned char *sp = nullptr;  // scale words: lanes 0-15 the keys', 16-31 the values'
+  if constexpr (E4)
+    sp = (lane < kBlk ? kb : vb) + static_cast<long long>(t0 + warp * kBlk + lane % kBlk) * ts + static_cast<long long>(P.H) * P.D + (g & ~3);
   if (P.D < DP) {  // the columns past the head vector stay zero: no copy writes them
-    for (int i = lane; i < kRowStages * C::kStage / 16; i += 32)
-      *reinterpret_cast<uint4 *>(smem + warp * kRowStages * C::kStage + i * 16) = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < C::kStages * C::kStage / 16; i += 32)
+      *reinterpret_cast<uint4 *>(smem + warp * C::kStages * C::kStage + i * 16) = make_uint4(0, 0, 0, 0);
     __syncwarp();
   }
   auto issue = [&](int blkno, int st) {
     if (blkno < nblk) {
-      const int tb = t0 + blkno * kBlk;
-      const uint32_t base = ring + st * C::kStage;
-      for (int i = lane; i < kBlk * pieces; i += 32) {
-        const int tk = i / pieces, pc = i - tk * pieces;
-        const bool on = tb + tk < t1;
-        const long long off = static_cast<long long>(on ? tb + tk : t0) * ts + head_off + pc * 16;
-        cp_async16_zfill(base + tk * C::kPitch + pc * 16, kb + off, on);
-        cp_async16_zfill(base + C::kPlane + tk * C::kPitch + pc * 16, vb + off, on);
+      const uint32_t base = ring + st * C::kStage + row0 * C::kPitch + pc * 16;
+      const int left = t1 - (t0 + blkno * kBlk);
+      if (col) {
+        const unsigned char *k = kp, *v = vp;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const bool on = row0 + i * kStep < left;
+          cp_async16_zfill(base + i * kStep * C::kPitch, on ? k : kb, on);
+          cp_async16_zfill(base + C::kPlane + i * kStep * C::kPitch, on ? v : vb, on);
+          k += step;
+          v += step;
+        }
       }
+      kp += jump;
+      vp += jump;
       if constexpr (E4) {
-        const int tk = lane % kBlk;
-        const bool on = tb + tk < t1;
-        const long long off = static_cast<long long>(on ? tb + tk : t0) * ts + scale_off;
-        cp_async4_zfill(base + 2 * C::kPlane + lane * 4, (lane < kBlk ? kb : vb) + off, on);
+        const bool on = lane % kBlk < left;
+        cp_async4_zfill(ring + st * C::kStage + 2 * C::kPlane + lane * 4, on ? sp : kb, on);
+        sp += jump;
       }
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < kRowStages - 1; ++s) issue(warp + s * kRowWarps, s);
+  for (int s = 0; s < C::kStages - 1; ++s) issue(warp + s * kRowWarps, s);
 
-  // --- queries into shared memory, a warp per row; fp16 for an e4m3 cache: a
-  // row far outside fp16's range is brought into it by a power of two
-  for (int rr = warp; rr < C::kM; rr += kRowWarps) {
-    int qi, h;
-    const bool on = decode(rr, qi, h);
-    float x[DP / 32];
+  // --- queries into shared memory; fp16 for an e4m3 cache: a row far outside
+  // fp16's range is brought into it by a power of two
+  {
+    constexpr int QL = DP / 8, kRows = 32 / QL;  // lanes per row, rows per pass
+    constexpr int kPass = C::kM / (kRowWarps * kRows) > 0 ? C::kM / (kRowWarps * kRows) : 1;
+    const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
+    const int qc = lane % QL;
+    uint4 u[kPass];
 #pragma unroll
-    for (int i = 0; i < DP / 32; ++i) x[i] = 0.f;
-    if (on) {
-      const int qb = qi / P.N, qt = qi - qb * P.N;
-      const long long off = qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2];
-#pragma unroll
-      for (int i = 0; i < DP / 32; ++i) {
-        const int d = i * 32 + lane;
-        if (d < P.D)
-          x[i] = P.qbf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(P.q)[off + d])
-                         : __half2float(static_cast<const __half *>(P.q)[off + d]);
+    for (int i = 0; i < kPass; ++i) {
+      const int rr = (i * kRowWarps + warp) * kRows + lane / QL;
+      const bool use = __shfl_sync(FULL_MASK, my_use, rr & 31);
+      const long long off = __shfl_sync(FULL_MASK, my_q, rr & 31);
+      u[i] = make_uint4(0, 0, 0, 0);
+      if (rr < C::kM && use && qc * 8 < P.D) {
+        const unsigned short *q = static_cast<const unsigned short *>(P.q) + off + qc * 8;
+        if (vec) {
+          u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
+        } else {
+          u[i].x = q[0] | static_cast<uint32_t>(q[1]) << 16;
+          u[i].y = q[2] | static_cast<uint32_t>(q[3]) << 16;
+          u[i].z = q[4] | static_cast<uint32_t>(q[5]) << 16;
+          u[i].w = q[6] | static_cast<uint32_t>(q[7]) << 16;
+        }
       }
     }
-    float fac = 1.f;
-    if constexpr (E4) {
-      uint32_t a = 0;
 #pragma unroll
-      for (int i = 0; i < DP / 32; ++i) a = max(a, __float_as_uint(x[i]) & 0x7fffffffu);
-      a = __reduce_max_sync(FULL_MASK, a);
-      const int e = static_cast<int>(a >> 23) - 127;  // magnitude's exponent
-      if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
-        const int up = max(-126, min(126, -e));
-        const float by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-        fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+    for (int i = 0; i < kPass; ++i) {
+      const int rr = (i * kRowWarps + warp) * kRows + lane / QL;
+      float fac = 1.f;
+      if (E4 && P.qbf16) {
+        const float x[8] = {bf16_lo(u[i].x), bf16_hi(u[i].x), bf16_lo(u[i].y), bf16_hi(u[i].y),
+                            bf16_lo(u[i].z), bf16_hi(u[i].z), bf16_lo(u[i].w), bf16_hi(u[i].w)};
+        uint32_t a = 0;
 #pragma unroll
-        for (int i = 0; i < DP / 32; ++i) x[i] *= by;
+        for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = QL / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
+        float by = 1.f;
+        const int e = static_cast<int>(a >> 23) - 127;
+        if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
+          const int up = max(-126, min(126, -e));
+          by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+          fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
+        u[i] = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
+                          pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
       }
-    }
-    if (lane == 0) qfac[rr] = fac;
-#pragma unroll
-    for (int i = 0; i < DP / 32; ++i) {
-      unsigned short u;
-      if constexpr (BF)
-        u = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
-      else
-        u = __half_as_ushort(__float2half_rn(x[i]));
-      *reinterpret_cast<unsigned short *>(qsm + rr * C::kQPitch + (i * 32 + lane) * 2) = u;
+      if (rr < C::kM) {
+        if (qc == 0) qfac[rr] = fac;
+        *reinterpret_cast<uint4 *>(qsm + rr * C::kQPitch + qc * 16) = u[i];
+      }
     }
   }
   __syncthreads();
@@ -298,8 +316,8 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
   bool odd = false;
   int st = 0;
   for (int blkno = warp; blkno < nblk; blkno += kRowWarps) {
-    issue(blkno + (kRowStages - 1) * kRowWarps, (st + kRowStages - 1) % kRowStages);
-    cp_async_wait<kRowStages - 1>();
+    issue(blkno + (C::kStages - 1) * kRowWarps, (st + C::kStages - 1) % C::kStages);
+    cp_async_wait<C::kStages - 1>();
     __syncwarp();
     const uint32_t kst = ring + st * C::kStage, vst = kst + C::kPlane;
     const int tb = t0 + blkno * kBlk;
@@ -554,7 +572,7 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
       }
     }
     __syncwarp();
-    st = (st + 1) % kRowStages;
+    st = (st + 1) % C::kStages;
   }
 
   // --- join the warps: everyone leaves its sums in the ring's memory
@@ -585,16 +603,12 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
         }
     }
   __syncthreads();
-  for (int rr = warp; rr < C::kM; rr += kRowWarps) {
-    int qi, h;
-    const bool on = decode(rr, qi, h);
-    if (r0 + rr >= nrows) break;
-    if (!on) {  // no such query: an empty part
-      const int r = r0 + rr, t = r / P.G;
-      qi = (pre ? 0 : b * P.N) + t;
-      h = g * P.G + (r - t * P.G);
-    }
-    const long long orow = static_cast<long long>(qi) * P.Hq + h;
+#pragma unroll
+  for (int i = 0; i < C::kM / kRowWarps; ++i) {
+    const int rr = i * kRowWarps + warp;
+    const int orow = __shfl_sync(FULL_MASK, my_row, rr);
+    const bool on = __shfl_sync(FULL_MASK, my_use, rr);
+    if (orow < 0) continue;
     float M = -INFINITY, Z = -INFINITY, S = 0.f, w[kRowWarps];
 #pragma unroll
     for (int k = 0; k < kRowWarps; ++k) {
@@ -652,21 +666,34 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     for (int s = lane; s < nslots; s += 32) S += ex2(P.ml[static_cast<long long>(s) * P.rows + r].y - zref);
   S = warp_sum(S);
   const float z = S == 0.f ? -INFINITY : zref + log2f(S);
-  float acc[SPEC_MAX_HEAD_DIM / 32] = {0.f, 0.f, 0.f, 0.f};
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};  // columns 4 lane .. 4 lane + 3
   if (S != 0.f)
     for (int s0 = 0; s0 < nslots; s0 += 32) {
       float2 ml = make_float2(-INFINITY, -INFINITY);
       if (s0 + lane < nslots) ml = P.ml[static_cast<long long>(s0 + lane) * P.rows + r];
       const float wl = ex2(ml.x - z);
-      const int top = min(32, nslots - s0);
-      for (int k = 0; k < top; ++k) {
-        const float w = __shfl_sync(FULL_MASK, wl, k);
-        if (__shfl_sync(FULL_MASK, ml.y, k) == -INFINITY) continue;  // an empty part left no sum
-        const float *from = P.part + (static_cast<long long>(s0 + k) * P.rows + r) * P.D;
+      // the parts that left a sum, four at a time: their loads overlap
+      unsigned todo = __ballot_sync(FULL_MASK, ml.y != -INFINITY);
+      while (todo) {
+        float4 x[4];
+        float w[4];
 #pragma unroll
-        for (int i = 0; i < SPEC_MAX_HEAD_DIM / 32; ++i) {
-          const int d = i * 32 + lane;
-          if (d < P.D) acc[i] = fmaf(w, from[d], acc[i]);
+        for (int j = 0; j < 4; ++j) {
+          const int k = todo ? __ffs(todo) - 1 : -1;
+          todo &= todo - 1;
+          w[j] = __shfl_sync(FULL_MASK, wl, k & 31);
+          x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < 0)
+            w[j] = 0.f;
+          else if (lane * 4 < P.D)
+            x[j] = *reinterpret_cast<const float4 *>(P.part + (static_cast<long long>(s0 + k) * P.rows + r) * P.D + lane * 4);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[0] = fmaf(w[j], x[j].x, acc[0]);
+          acc[1] = fmaf(w[j], x[j].y, acc[1]);
+          acc[2] = fmaf(w[j], x[j].z, acc[2]);
+          acc[3] = fmaf(w[j], x[j].w, acc[3]);
         }
       }
     }
@@ -683,9 +710,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         if (!see) continue;
         const unsigned char *const e = P.v + b * P.row_stride + static_cast<long long>(len0 + j) * P.tok_stride;
 #pragma unroll
-        for (int i = 0; i < SPEC_MAX_HEAD_DIM / 32; ++i) {
-          const int d = i * 32 + lane;
-          if (d >= P.D) continue;
+        for (int i = 0; i < 4; ++i) {
+          const int d = lane * 4 + i;
+          if (d >= P.D) break;
           float val;
           if constexpr (E4)
             val = e[P.H * P.D + g] == 255 || (e[g * P.D + d] & 127) == 127 ? __uint_as_float(0x7fc00000u) : 0.f;
@@ -698,16 +725,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < SPEC_MAX_HEAD_DIM / 32; ++i) {
-    const int d = i * 32 + lane;
-    if (d < P.D) {
-      if constexpr (BF)
-        static_cast<__nv_bfloat16 *>(P.out)[r * P.D + d] = __float2bfloat16_rn(acc[i]);
-      else
-        static_cast<__half *>(P.out)[r * P.D + d] = __float2half_rn(acc[i]);
-    }
-  }
+  if (lane * 4 < P.D)
+    *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(P.out) + r * P.D + lane * 4) =
+        make_uint2(pack16<BF>(acc[0], acc[1]), pack16<BF>(acc[2], acc[3]));
   if (lane == 0 && P.lse) P.lse[r] = 0.693147180559945309f * z;
 }
 

@@ -37,8 +37,6 @@ constexpr int kTok = 128;          // tokens per block
 constexpr int kTileThreads = 512;  // softmax A, softmax B, producers, tensor-core issue
 constexpr int kProducers = 128;
 constexpr float kLazy = 8.f;       // log2 of the growth a row's maximum may make before its sums follow
-// registers per thread of the roles: 2 x 184 + 104 + 40 = 4 x 128, what the block is launched with
-constexpr int kRegsSoftmax = 184, kRegsProduce = 104, kRegsIssue = 40;
 
 template <int DP>
 struct TileCfg {
@@ -47,7 +45,7 @@ struct TileCfg {
   static constexpr int kK = 2 * kOp;         // two buffers
   static constexpr int kV = 4 * kOp;         // two buffers
   static constexpr int kCtrl = 6 * kOp;
-  static constexpr int kSmem = kCtrl + 4096 + 1024;  // + control block + alignment
+  static constexpr int kSmem = kCtrl + 6144 + 1024;  // + control block + alignment
 };
 
 struct Ctrl {
@@ -61,8 +59,11 @@ struct Ctrl {
   float vex[2], vtop[2];    // the values' exponent, and the largest so far
   uint32_t red[2][4];       // producers' reductions
   float qfac[256];
+  int orow[256];            // output row of a query row; -1: past the last, or | kUnused
+  long long qoff[256];      // its query's offset in elements
 };
-static_assert(sizeof(Ctrl) <= 4096, "control block");
+static_assert(sizeof(Ctrl) <= 6144, "control block");
+constexpr int kUnused = 1 << 30;  // the row has no such query (its answer is empty)
 
 // ------------------------------------------------------------ tcgen05 wrappers
 __device__ __forceinline__ void tc_alloc(uint32_t *dst) {
@@ -207,27 +208,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   const long long ts = PRE ? P.ptok_stride : P.tok_stride;
   const int n = (t1 - t0 + kTok - 1) / kTok;        // blocks of tokens
   const int tiles = nrows - r0 > 128 ? 2 : 1;       // row tiles in use
-  // query row rr of the block -> its token (flat index) and head; false if it has no use
-  auto decode = [&](int rr, int &qi, int &h) -> bool {
-    const int r = r0 + rr;
-    if (r >= nrows) return false;
-    const int t = r / P.G;
-    h = g * P.G + (r - t * P.G);
-    if constexpr (PRE) {
-      qi = t;
-      const int rb = t / P.N;
-      return t - rb * P.N < row_queries(P, rb);
-    } else {
-      qi = b * P.N + t;
-      return t < cnt;
+  if (tid < 256) {
+    const int r = r0 + tid;
+    int at = -1;
+    if (r < nrows) {
+      const int t = r / P.G, h = g * P.G + (r - t * P.G);
+      const int qb = PRE ? t / P.N : b, qt = PRE ? t - qb * P.N : t;
+      at = (qb * P.N + qt) * P.Hq + h;
+      c->qoff[tid] = qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2];
+      if (n == 0) P.ml[static_cast<long long>(slot) * P.rows + at] = make_float2(-INFINITY, -INFINITY);
+      if (qt >= (PRE ? row_queries(P, qb) : cnt)) at |= kUnused;
     }
-  };
+    c->orow[tid] = at;
+  }
   if (n == 0) {  // nothing here (an empty part, or a row that cannot be used)
-    if (tid < 256 && r0 + tid < nrows) {
-      int qi, h;
-      decode(tid, qi, h);
-      P.ml[static_cast<long long>(slot) * P.rows + static_cast<long long>(qi) * P.Hq + h] = make_float2(-INFINITY, -INFINITY);
-    }
     if (!PRE && tid == 0) P.oflag[blockIdx.x] = 0;
     return;
   }
@@ -249,51 +243,56 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     fence_mbar_init();
   }
   if (warp == 12) tc_alloc(&c->tmem);
+  __syncthreads();
   {
     // DP/8 lanes per row, 16 bytes of the operand each; fp16 for an e4m3
     // cache: a row far outside fp16's range is brought into it by a power of
     // two.  A negative scale turns the queries' sign.
-    constexpr int L = DP / 8;
+    constexpr int L = DP / 8, kIt = 256 * L / kTileThreads, kStep = kTileThreads / L;
     const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
-    for (int i = tid; i < 256 * L; i += kTileThreads) {
-      const int rr = i / L, pc = i % L;
-      int qi = 0, h = 0;
-      const bool on = decode(rr, qi, h) && pc * 8 < P.D;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (on) {
-        const int qb = qi / P.N, qt = qi - qb * P.N;
-        const unsigned short *q = static_cast<const unsigned short *>(P.q) + qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2] + pc * 8;
+    const int pc = tid % L, rr0 = tid / L;
+    uint4 u[kIt];
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      const int rr = rr0 + i * kStep, at = c->orow[rr];
+      u[i] = make_uint4(0, 0, 0, 0);
+      if (at >= 0 && at < kUnused && pc * 8 < P.D) {
+        const unsigned short *q = static_cast<const unsigned short *>(P.q) + c->qoff[rr] + pc * 8;
         if (vec) {
-          u = __ldg(reinterpret_cast<const uint4 *>(q));
+          u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
         } else {
-          u.x = q[0] | static_cast<uint32_t>(q[1]) << 16;
-          u.y = q[2] | static_cast<uint32_t>(q[3]) << 16;
-          u.z = q[4] | static_cast<uint32_t>(q[5]) << 16;
-          u.w = q[6] | static_cast<uint32_t>(q[7]) << 16;
+          u[i].x = q[0] | static_cast<uint32_t>(q[1]) << 16;
+          u[i].y = q[2] | static_cast<uint32_t>(q[3]) << 16;
+          u[i].z = q[4] | static_cast<uint32_t>(q[5]) << 16;
+          u[i].w = q[6] | static_cast<uint32_t>(q[7]) << 16;
         }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      const int rr = rr0 + i * kStep;
+      float fac = 1.f;
       if (E4 && P.qbf16) {
-        float x[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y), bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
+        const float x[8] = {bf16_lo(u[i].x), bf16_hi(u[i].x), bf16_lo(u[i].y), bf16_hi(u[i].y),
+                            bf16_lo(u[i].z), bf16_hi(u[i].z), bf16_lo(u[i].w), bf16_hi(u[i].w)};
         uint32_t a = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
-        float fac = 1.f, by = 1.f;
+        float by = 1.f;
         const int e = static_cast<int>(a >> 23) - 127;
         if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
           const int up = max(-126, min(126, -e));
           by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
           fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
         }
-        u = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
-                       pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
-        if (pc == 0) c->qfac[rr] = fac;
-      } else if (pc == 0) {
-        c->qfac[rr] = 1.f;
+        u[i] = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
+                          pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
       }
-      if (P.scale < 0.f) u.x ^= 0x80008000u, u.y ^= 0x80008000u, u.z ^= 0x80008000u, u.w ^= 0x80008000u;
-      *reinterpret_cast<uint4 *>(smem + C::kQ + (rr / 128) * C::kOp + (pc / 8) * 16384 + (rr % 128) * 128 + (((pc % 8) ^ (rr & 7)) << 4)) = u;
+      if (pc == 0) c->qfac[rr] = fac;
+      if (P.scale < 0.f) u[i].x ^= 0x80008000u, u[i].y ^= 0x80008000u, u[i].z ^= 0x80008000u, u[i].w ^= 0x80008000u;
+      *reinterpret_cast<uint4 *>(smem + C::kQ + (rr / 128) * C::kOp + (pc / 8) * 16384 + (rr % 128) * 128 + (((pc % 8) ^ (rr & 7)) << 4)) = u[i];
     }
   }
   fence_async_smem();
@@ -305,7 +304,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
 
   if (role == 2) {
     // ------------------------------------------------------------ producers
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProduce));
     const int pt = tid - 256;
     bool live = true;
     if constexpr (!E4) {
@@ -314,7 +312,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       const int pc = pt % L, row0 = pt / L;
       const bool col = pc * 8 < P.D;
       const uint32_t dst0 = smem_u32(smem) + (pc / 8) * 16384 + row0 * 128 + (((pc % 8) ^ (row0 & 7)) << 4);
-      const long long src0 = static_cast<long long>(g) * P.D * 2 + pc * 16;
+      const long long src0 = static_cast<long long>(g) * P.D * 2 + (col ? pc * 16 : 0);
+      const unsigned char *kp = kb + src0 + (static_cast<long long>(t0) + row0) * ts;  // this thread's next block
+      const unsigned char *vp = vb + src0 + (static_cast<long long>(t0) + row0) * ts;
+      const long long step = ts * kStep;
       // item 2k: keys of block k, item 2k + 1: its values
       auto issue = [&](int it) {
         if (it < 2 * n && live) {
@@ -322,15 +323,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           uint64_t *const fr = it & 1 ? &c->vfree[s] : &c->kfree[s];
           if (k >= 2) live = wait_for(c, fr, ((k >> 1) - 1) & 1, limit);
           if (live) {
-            const unsigned char *const src = (it & 1 ? vb : kb) + src0;
+            const unsigned char *src = it & 1 ? vp : kp;
             const uint32_t dst = dst0 + (it & 1 ? C::kV : C::kK) + s * C::kOp;
-            const int tb = t0 + k * kTok;
+            const int left = t1 - (t0 + k * kTok) - row0;  // tokens from this thread's first row on
+            if (col && left > (kPer - 1) * kStep) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-              const int t = tb + row0 + i * kStep;
-              const bool on = col && t < t1;
-              cp_async16_zfill(dst + i * kStep * 128, src + static_cast<long long>(on ? t : t0) * ts - (on ? 0 : pc * 16), on);
+              for (int i = 0; i < kPer; ++i) {
+                cp_async16_zfill(dst + i * kStep * 128, src, true);
+                src += step;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kPer; ++i) {
+                const bool on = col && i * kStep < left;
+                cp_async16_zfill(dst + i * kStep * 128, on ? src : kb, on);
+                src += step;
+              }
             }
+            if (it & 1)
+              vp = src;
+            else
+              kp = src;
           }
         }
         cp_async_commit();
@@ -477,7 +490,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     }
   } else if (role == 3) {
     // ------------------------------------------------- tensor-core issue
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 12 && lane == 0) {
       const uint32_t qk = inst_desc(BF, kTok, false), wv = inst_desc(BF, DP, true);
       const uint32_t base = smem_u32(smem);
@@ -530,12 +542,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     }
   } else {
     // --------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int tile = role;
     if (tile < tiles) {
       const int rr = tid;  // row of the block (tile * 128 + lane of tensor memory)
-      int qi = 0, h = 0;
-      const bool on = decode(rr, qi, h);
       const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp & 3) << 21);
       const uint32_t s_addr = lane_addr + tile * 128, o_addr = lane_addr + 256 + tile * 128;
       const float base_sc = fabsf(P.scale) * (E4 ? c->qfac[rr] : 1.f);
@@ -558,46 +567,64 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         live = __all_sync(FULL_MASK, live);
         if (!live) break;
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tc_ld32(s[q], s_addr + q * 32);
-        tc_wait_ld();
         const int tb = t0 + k * kTok;
-        if (tb + kTok > t1 || (!PRE && tb + kTok > len0)) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int tq = tb + q * 32;
-            uint32_t bits;  // tokens tq .. tq + 31 this row sees
-            if (PRE || !anc) {
-              const int see = (PRE ? t1 : min(t1, len0 + my + 1)) - tq;
-              bits = see >= 32 ? 0xffffffffu : see <= 0 ? 0u : (1u << see) - 1u;
+        const bool masked = tb + kTok > t1 || (!PRE && tb + kTok > len0);
+        // which of the 32 tokens from column q * 32 this row sees
+        auto seen = [&](int q) -> uint32_t {
+          const int tq = tb + q * 32;
+          uint32_t bits;
+          if (PRE || !anc) {
+            const int see = (PRE ? t1 : min(t1, len0 + my + 1)) - tq;
+            bits = see >= 32 ? 0xffffffffu : see <= 0 ? 0u : (1u << see) - 1u;
+          } else {
+            const int j = tq - len0;  // first token's index among the pass's own
+            if (j <= -32) {
+              bits = 0xffffffffu;
+            } else if (j < 0) {
+              bits = ((1u << -j) - 1u) | __ldg(anc) << -j;
             } else {
-              const int j = tq - len0;  // first token's index among the pass's own
-              if (j <= -32) {
-                bits = 0xffffffffu;
-              } else if (j < 0) {
-                bits = ((1u << -j) - 1u) | __ldg(anc) << -j;
-              } else {
-                const int wd = j >> 5;
-                const uint32_t lo = wd < P.W ? __ldg(anc + wd) : 0u, hi = wd + 1 < P.W ? __ldg(anc + wd + 1) : 0u;
-                bits = __funnelshift_r(lo, hi, j & 31);
-              }
-              const int in = t1 - tq;
-              if (in < 32) bits &= in <= 0 ? 0u : (1u << in) - 1u;
+              const int wd = j >> 5;
+              const uint32_t lo = wd < P.W ? __ldg(anc + wd) : 0u, hi = wd + 1 < P.W ? __ldg(anc + wd + 1) : 0u;
+              bits = __funnelshift_r(lo, hi, j & 31);
             }
+            const int in = t1 - tq;
+            if (in < 32) bits &= in <= 0 ? 0u : (1u << in) - 1u;
+          }
+          return bits;
+        };
+        // The scores are read twice, 32 columns at a time (tensor memory is
+        // fast, registers are not: the block keeps 128 a thread): once for the
+        // maximum, once for the weights.
+        uint32_t sa[32], sb[32];
+        float mq[4];
+        auto maximum = [&](uint32_t (&s)[32], int q) {
+          if (masked) {
+            const uint32_t bits = seen(q);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!(bits >> j & 1)) s[q][j] = 0xff800000u;
+              if (!(bits >> j & 1)) s[j] = 0xff800000u;
           }
-        }
-        float mq[4];
+          float x = __uint_as_float(s[0]), y = __uint_as_float(s[1]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mq[q] = __uint_as_float(s[q][0]);
-#pragma unroll
-          for (int j = 1; j < 31; j += 2) mq[q] = max3(mq[q], __uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1]));
-          mq[q] = fmaxf(mq[q], __uint_as_float(s[q][31]));
-        }
+          for (int j = 2; j < 32; j += 4) {
+            x = max3(x, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+            if (j + 2 < 32) y = max3(y, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+          }
+          mq[q] = fmaxf(x, y);
+        };
+        tc_ld32(sa, s_addr);
+        tc_wait_ld();
+        tc_ld32(sb, s_addr + 32);
+        maximum(sa, 0);
+        tc_wait_ld();
+        tc_ld32(sa, s_addr + 64);
+        maximum(sb, 1);
+        tc_wait_ld();
+        tc_ld32(sb, s_addr + 96);
+        maximum(sa, 2);
+        tc_wait_ld();
+        tc_ld32(sa, s_addr);  // for the second pass
+        maximum(sb, 3);
         const float top = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
         const float mt = top == -INFINITY ? -INFINITY : fmaf(top, sc, ex);
         float al = 1.f;
@@ -609,29 +636,44 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         if (k > 0 && __any_sync(FULL_MASK, al != 1.f)) {
 #pragma unroll
           for (int q = 0; q < DP / 32; ++q) {
-            uint32_t o[32];
-            tc_ld32(o, o_addr + q * 32);
+            tc_ld32(sb, o_addr + q * 32);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
-            tc_st32(o_addr + q * 32, o);
+            for (int j = 0; j < 32; ++j) sb[j] = __float_as_uint(__uint_as_float(sb[j]) * al);
+            tc_st32(o_addr + q * 32, sb);
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
         const float2 sc2 = make_float2(sc, sc), off2 = make_float2(ex - ref, ex - ref);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto weights = [&](uint32_t (&s)[32], int q) {
+          if (masked) {
+            const uint32_t bits = seen(q);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+            for (int j = 0; j < 32; ++j)
+              if (!(bits >> j & 1)) s[j] = 0xff800000u;
+          }
           uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float2 x = ffma2(make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), sc2, off2);
+            const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), sc2, off2);
             const float2 p = make_float2(ex2(x.x), ex2(x.y));
             sum[j & 1] = fadd2(sum[j & 1], p);
             pk[j] = pack16<BF>(p.x, p.y);
           }
-          tc_st16(s_addr + q * 16, pk);
-        }
+          tc_st16(s_addr + q * 16, pk);  // over scores that have been read: columns 16 q .. 16 q + 15
+        };
+        tc_wait_ld();
+        tc_ld32(sb, s_addr + 32);
+        weights(sa, 0);
+        tc_wait_ld();
+        tc_ld32(sa, s_addr + 64);
+        weights(sb, 1);
+        tc_wait_ld();
+        tc_ld32(sb, s_addr + 96);
+        weights(sa, 2);
+        tc_wait_ld();
+        weights(sb, 3);
         const float add = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if constexpr (E4) {
           // l counts in units of 2^(m - E)
@@ -645,15 +687,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         mbar_arrive(&c->pfull[tile]);
       }
       if (live) live = __all_sync(FULL_MASK, wait_for(c, &c->done[tile], 0, limit));
-      const long long orow = static_cast<long long>(qi) * P.Hq + h;
-      const bool have = r0 + rr < nrows;
+      const int at = c->orow[rr], orow = at & (kUnused - 1);
       if (!live) {
-        if (have) P.ml[static_cast<long long>(slot) * P.rows + orow] = make_float2(-INFINITY, __uint_as_float(kTimeoutBits));
+        if (at >= 0) P.ml[static_cast<long long>(slot) * P.rows + orow] = make_float2(-INFINITY, __uint_as_float(kTimeoutBits));
       } else {
         tc_fence_after();
-        const float z = l == 0.f ? -INFINITY : m + log2f(l) - E;
-        const bool some = on && l != 0.f;
-        if (have) P.ml[static_cast<long long>(slot) * P.rows + orow] = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
+        const bool some = at >= 0 && at < kUnused && l != 0.f;
+        if (at >= 0)
+          P.ml[static_cast<long long>(slot) * P.rows + orow] = some ? make_float2(m, m + log2f(l) - E) : make_float2(-INFINITY, -INFINITY);
         float *const to = P.part + (static_cast<long long>(slot) * P.rows + orow) * P.D;
 #pragma unroll
         for (int q = 0; q < DP / 32; ++q) {
