@@ -29,9 +29,10 @@ namespace sv {
 namespace {
 
 constexpr int kSms = 152;           // parts are sized for this many SMs
-constexpr int kRowWarps = 8;        // warps of attn_rows_kernel, each with its own ring
+constexpr int kRowWarps = 4;        // warps of attn_rows_kernel, each with its own ring
 constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kBlk = 16;            // tokens per block
+constexpr float kRowLazy = 8.f;
 constexpr int kMaskThreads = 256;
 constexpr int kJoinThreads = 256;
 
@@ -74,7 +75,7 @@ template <int CT, int DP, int MT>
 struct RowCfg {
   static constexpr bool E4 = CT == SPEC_E4M3;
   static constexpr int kEsz = E4 ? 1 : 2;
-  static constexpr int kStages = E4 ? 4 : 3;                // 24 KB and 26 KB a warp at most
+  static constexpr int kStages = 3;
   static constexpr int kPitch = DP * kEsz + 16;             // bytes of one token in a ring slot
   static constexpr int kPlane = kBlk * kPitch;              // K or V of a block
   static constexpr int kScales = E4 ? 2 * kBlk * 4 : 0;     // scale words, K then V
@@ -82,7 +83,8 @@ struct RowCfg {
   static constexpr int kQPitch = DP * 2 + 16;
   static constexpr int kM = 16 * MT;
   static constexpr int kRing = kRowWarps * kStages * kStage;
-  static constexpr int kMerge = kRowWarps * kM * (DP + 2) * 4;  // the warps' sums, after the loop
+  static constexpr int kOPitch = DP + (E4 ? 16 : 8);        // floats of a row of the warps' sums: no bank met twice
+  static constexpr int kMerge = kRowWarps * kM * (kOPitch + 2) * 4;  // the warps' sums, after the loop
   static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
   static constexpr int kSmem = kBody + kM * kQPitch + kM * 4;
 };
@@ -436,21 +438,42 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
             if (!see) s4[mt][n][c] = -INFINITY;
           }
     }
-    // --- softmax
+    // --- softmax.  A row's reference follows its maximum only when that has
+    // grown by more than 2^kRowLazy (weights up to that are as exact).
     uint32_t pf[MT][4];
-    bool moved = false;
-    float al[MT][2];
+    float tm[MT][2], al[MT][2];
+    bool grown = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float t = fmaxf(fmaxf(s4[mt][0][2 * hf], s4[mt][0][2 * hf + 1]), fmaxf(s4[mt][1][2 * hf], s4[mt][1][2 * hf + 1]));
-        t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 1));
-        t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 2));
-        const float mn = fmaxf(mx[mt][hf], t);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        al[mt][hf] = ex2(mx[mt][hf] - ref);
-        moved = moved || mn != mx[mt][hf];
+        tm[mt][hf] = fmaxf(fmaxf(s4[mt][0][2 * hf], s4[mt][0][2 * hf + 1]), fmaxf(s4[mt][1][2 * hf], s4[mt][1][2 * hf + 1]));
+        grown = grown || tm[mt][hf] > mx[mt][hf] + kRowLazy || mx[mt][hf] == -INFINITY;
+        al[mt][hf] = 1.f;
+      }
+    const bool moved = __any_sync(FULL_MASK, grown);
+    float old[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) old[mt][0] = mx[mt][0], old[mt][1] = mx[mt][1];
+    if (moved) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float t = tm[mt][hf];
+          t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 1));
+          t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 2));
+          if (t > mx[mt][hf]) {
+            al[mt][hf] = ex2(mx[mt][hf] - t);
+            mx[mt][hf] = t;
+          }
+        }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float ref = mx[mt][hf] == -INFINITY ? 0.f : mx[mt][hf];
         float add = 0.f;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -465,8 +488,8 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
               add += x;
             }
           }
-        const float ll = E4 && dE != 0.f ? ex2(mx[mt][hf] - ref + dE) : al[mt][hf];
-        mx[mt][hf] = mn;
+        // old = -inf: nothing was summed yet
+        const float ll = E4 && dE != 0.f ? (old[mt][hf] == -INFINITY ? 0.f : ex2(old[mt][hf] - ref + dE)) : al[mt][hf];
         l[mt][hf] = fmaf(l[mt][hf], ll, add);
       }
     if constexpr (E4) {
@@ -489,7 +512,7 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
       pf[mt][2] = pack16<BF>(s4[mt][1][0], s4[mt][1][1]);
       pf[mt][3] = pack16<BF>(s4[mt][1][2], s4[mt][1][3]);
     }
-    if (__any_sync(FULL_MASK, moved)) {
+    if (moved) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -579,9 +602,15 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
   cp_async_wait_all();
   odd = __syncthreads_or(odd);
   if (!pre && tid == 0) P.oflag[blockIdx.x - pitems] = odd;
-  float *const om = reinterpret_cast<float *>(smem);                  // [warp][row][DP]
-  float *const mm = om + kRowWarps * C::kM * DP;                      // [warp][row]
+  float *const om = reinterpret_cast<float *>(smem);                  // [warp][row][kOPitch]
+  float *const mm = om + kRowWarps * C::kM * C::kOPitch;                      // [warp][row]
   float *const lm = mm + kRowWarps * C::kM;
+  // where a row keeps column d: for codes, groups of four rotated by the lane that held them
+  auto own_col = [](int d) {
+    if constexpr (!E4) return d;
+    const int run = d / kNt, i = d % kNt / 4;
+    return run * kNt + 4 * ((i + run / 2) & (kNt / 4 - 1)) + d % 4;
+  };
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -594,13 +623,19 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
         mm[warp * C::kM + rr] = mx[mt][hf];
         lm[warp * C::kM + rr] = t == 0.f ? -INFINITY : mx[mt][hf] + log2f(t) - (E4 ? E : 0.f);
       }
+      float *const to = om + (warp * C::kM + rr) * C::kOPitch;
+      if constexpr (E4) {
 #pragma unroll
-      for (int n = 0; n < kNt; ++n)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int d = E4 ? (2 * j4 + c) * kNt + n : n * 8 + 2 * j4 + c;
-          om[(warp * C::kM + rr) * DP + d] = o[mt][n][2 * hf + c];
-        }
+          for (int i = 0; i < kNt / 4; ++i)  // see own_col: the four j4 lie a whole round of banks apart
+            *reinterpret_cast<float4 *>(to + (2 * j4 + c) * kNt + 4 * ((i + j4) & (kNt / 4 - 1))) =
+                make_float4(o[mt][4 * i][2 * hf + c], o[mt][4 * i + 1][2 * hf + c], o[mt][4 * i + 2][2 * hf + c], o[mt][4 * i + 3][2 * hf + c]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+          *reinterpret_cast<float2 *>(to + n * 8 + 2 * j4) = make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
+      }
     }
   __syncthreads();
 #pragma unroll
@@ -629,7 +664,7 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
     for (int d = lane; d < P.D; d += 32) {
       float x = 0.f;
 #pragma unroll
-      for (int k = 0; k < kRowWarps; ++k) x = fmaf(w[k], om[(k * C::kM + rr) * DP + d], x);
+      for (int k = 0; k < kRowWarps; ++k) x = fmaf(w[k], om[(k * C::kM + rr) * C::kOPitch + own_col(d)], x);
       to[d] = x;
     }
   }

@@ -27,6 +27,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "attention.cuh"
 #include "internal.h"
 
@@ -36,6 +38,14 @@ namespace {
 constexpr int kTok = 128;          // tokens per block
 constexpr int kTileThreads = 512;  // softmax A, softmax B, producers, tensor-core issue
 constexpr int kProducers = 128;
+// Registers per thread of the roles.  Their sum over the four groups of 128
+// threads is what the block is launched with, 4 x 128.
+template <bool E4>
+struct Regs {
+  static constexpr int kSoftmax = E4 ? 160 : 176, kProduce = E4 ? 120 : 88, kIssue = 72;
+  static_assert(kSoftmax > 128 && kProduce < 128 && kIssue < 128, "softmax takes more, the others give back");
+  static_assert(2 * kSoftmax + kProduce + kIssue == 512, "the block's registers");
+};
 constexpr float kLazy = 8.f;       // log2 of the growth a row's maximum may make before its sums follow
 
 template <int DP>
@@ -45,7 +55,7 @@ struct TileCfg {
   static constexpr int kK = 2 * kOp;         // two buffers
   static constexpr int kV = 4 * kOp;         // two buffers
   static constexpr int kCtrl = 6 * kOp;
-  static constexpr int kSmem = kCtrl + 6144 + 1024;  // + control block + alignment
+  static constexpr int kSmem = kCtrl + 7168 + 1024;  // + control block + alignment
 };
 
 struct Ctrl {
@@ -58,11 +68,12 @@ struct Ctrl {
   float ksc[2];             // per buffer: the block's scale of the keys
   float vex[2], vtop[2];    // the values' exponent, and the largest so far
   uint32_t red[2][4];       // producers' reductions
+  uint32_t mult[2][128];    // fp16 factors of the block's tokens, keys and values
   float qfac[256];
   int orow[256];            // output row of a query row; -1: past the last, or | kUnused
   long long qoff[256];      // its query's offset in elements
 };
-static_assert(sizeof(Ctrl) <= 6144, "control block");
+static_assert(sizeof(Ctrl) <= 7168, "control block");
 constexpr int kUnused = 1 << 30;  // the row has no such query (its answer is empty)
 
 // ------------------------------------------------------------ tcgen05 wrappers
@@ -304,6 +315,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
 
   if (role == 2) {
     // ------------------------------------------------------------ producers
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4>::kProduce));
     const int pt = tid - 256;
     bool live = true;
     if constexpr (!E4) {
@@ -391,59 +403,58 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       constexpr int kStep = kProducers / L;
       const int pc = pt % L, row0 = pt / L;
       const bool col = pc * 16 < P.D;
-      const long long src0 = static_cast<long long>(g) * P.D + (col ? pc * 16 : 0);
-      const long long sc0 = static_cast<long long>(P.H) * P.D + g;
-      uint4 w[kPer], wn[kPer];
-      uint32_t sc[kPer], scn[kPer];
-      auto fetch = [&](int it, uint4 (&x)[kPer], uint32_t (&y)[kPer]) {
-        const int tb = t0 + (it >> 1) * kTok;
-        const unsigned char *const base = it & 1 ? vb : kb;
+      const long long piece = static_cast<long long>(g) * P.D + (col ? pc * 16 : 0) + (static_cast<long long>(t0) + row0) * ts;
+      const long long byte = static_cast<long long>(P.H) * P.D + g + (static_cast<long long>(t0) + pt) * ts;
+      const unsigned char *src[2] = {kb + piece, vb + piece}, *scl[2] = {kb + byte, vb + byte};
+      const long long step = ts * kStep, jump = ts * kTok;
+      uint4 w[2][kPer];   // keys and values of the next block
+      uint32_t sc[2];     // scale byte of its token pt
+      auto fetch = [&](auto val, int k) {
+        constexpr int V = decltype(val)::value;
+        const int left = t1 - (t0 + k * kTok);
+        const unsigned char *p = src[V];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int t = tb + row0 + i * kStep;
-          x[i] = make_uint4(0, 0, 0, 0);
-          y[i] = 0;
-          if (t < t1) {
-            const unsigned char *const e = base + static_cast<long long>(t) * ts;
-            if (col) x[i] = __ldg(reinterpret_cast<const uint4 *>(e + src0));
-            y[i] = __ldg(e + sc0);
-          }
+          w[V][i] = make_uint4(0, 0, 0, 0);
+          if (col && row0 + i * kStep < left) w[V][i] = __ldg(reinterpret_cast<const uint4 *>(p));
+          p += step;
         }
+        sc[V] = pt < left ? __ldg(scl[V]) : 0u;
+        src[V] += jump;
+        scl[V] += jump;
       };
       float E = kMinExponent, kscale = 1.f;
-      fetch(0, w, sc);
-      for (int it = 0; it < 2 * n; ++it) {
-        if (it + 1 < 2 * n) fetch(it + 1, wn, scn);
-        const int k = it >> 1, s = k & 1;
-        const bool val = it & 1;
+      auto put = [&](auto val, int k) {
+        constexpr int V = decltype(val)::value;
+        const int s = k & 1;
         // the block's largest scale
-        uint32_t top = 1;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (sc[i] != 255u) top = max(top, sc[i]);
-        top = __reduce_max_sync(FULL_MASK, top);
-        if (lane == 0) c->red[it & 1][warp & 3] = top;
+        const uint32_t mine = sc[V];
+        const uint32_t wtop = __reduce_max_sync(FULL_MASK, mine == 255u ? 1u : max(mine, 1u));
+        if (lane == 0) c->red[V][warp & 3] = wtop;
         producer_sync();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, c->red[it & 1][i]);
+        const uint32_t top = max(max(c->red[V][0], c->red[V][1]), max(c->red[V][2], c->red[V][3]));
         float ex = static_cast<float>(static_cast<int>(top) - 127);
-        if (val) {
+        if (V) {
           E = fmaxf(E, ex);
           ex = fmaxf(ex, E - kExponentSpan);
         }
-        const int ref = static_cast<int>(ex) + 127;
-        if (k >= 2 && live) live = wait_for(c, val ? &c->vfree[s] : &c->kfree[s], ((k >> 1) - 1) & 1, limit);
+        {
+          // 2^(scale - block's scale) as fp16: exact down to 2^-24, zero below
+          const int d = static_cast<int>(mine) - (static_cast<int>(ex) + 127);
+          const uint32_t f = mine == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+          c->mult[V][pt] = f | f << 16;
+        }
+        if (k >= 2 && live) live = wait_for(c, V ? &c->vfree[s] : &c->kfree[s], ((k >> 1) - 1) & 1, limit);
+        producer_sync();
         if (live) {
-          unsigned char *const dst = smem + (val ? C::kV : C::kK) + s * C::kOp + (pc / 4) * 16384;
-          const int tb = t0 + k * kTok;
+          unsigned char *const dst = smem + (V ? C::kV : C::kK) + s * C::kOp + (pc / 4) * 16384 + row0 * 128;
+          const int own0 = V && !PRE ? len0 - (t0 + k * kTok) : kTok;  // from this row on: the pass's own tokens
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
             const int row = row0 + i * kStep;
-            // 2^(scale - block's scale) as fp16: exact down to 2^-24, zero below
-            const int d = static_cast<int>(sc[i]) - ref;
-            const uint32_t f = sc[i] == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
-            const __half2 f2 = __halves2half2(__ushort_as_half(static_cast<unsigned short>(f)), __ushort_as_half(static_cast<unsigned short>(f)));
-            const uint32_t cw[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            const uint32_t fw = c->mult[V][row];
+            const __half2 f2 = *reinterpret_cast<const __half2 *>(&fw);
+            const uint32_t cw[4] = {w[V][i].x, w[V][i].y, w[V][i].z, w[V][i].w};
             uint32_t o[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -453,7 +464,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
               o[2 * e] = *reinterpret_cast<const uint32_t *>(&l2);
               o[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&h2);
             }
-            if (!PRE && val && tb + row >= len0) {  // as for 16-bit entries
+            if (V && !PRE && row >= own0) {  // as for 16-bit entries
               bool odd = false;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
@@ -465,48 +476,55 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             // the two 16-byte halves, the upper panel's lanes in the other
             // order: eight lanes then cover all banks
             const int ch = (pc % 4) * 2, first = pc / 4;
-            unsigned char *const at = dst + row * 128;
+            unsigned char *const at = dst + i * kStep * 128;
             const uint4 h0 = make_uint4(o[0], o[1], o[2], o[3]), h1 = make_uint4(o[4], o[5], o[6], o[7]);
             *reinterpret_cast<uint4 *>(at + (((ch + first) ^ (row & 7)) << 4)) = first ? h1 : h0;
             *reinterpret_cast<uint4 *>(at + (((ch + 1 - first) ^ (row & 7)) << 4)) = first ? h0 : h1;
           }
           // the keys' scale goes with the values' exponents: the softmax waits
           // for the values' buffer, which it holds until it is done
-          if (!val) kscale = e4m3_scale(top);
-          if (val && pt == 0) {
+          if (!V) kscale = e4m3_scale(top);
+          if (V && pt == 0) {
             c->ksc[s] = kscale;
             c->vex[s] = ex;
             c->vtop[s] = E;
           }
         }
         fence_async_smem();
-        if (!(P.force_timeout && it == 0)) mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          w[i] = wn[i];
-          sc[i] = scn[i];
-        }
+        if (!(P.force_timeout && k == 0 && !V)) mbar_arrive(V ? &c->vfull[s] : &c->kfull[s]);
+      };
+      using K = std::integral_constant<int, 0>;
+      using V = std::integral_constant<int, 1>;
+      fetch(K{}, 0);
+      fetch(V{}, 0);
+      for (int k = 0; k < n; ++k) {
+        put(K{}, k);
+        if (k + 1 < n) fetch(K{}, k + 1);
+        put(V{}, k);
+        if (k + 1 < n) fetch(V{}, k + 1);
       }
     }
   } else if (role == 3) {
     // ------------------------------------------------- tensor-core issue
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4>::kIssue));
     if (warp == 12 && lane == 0) {
       const uint32_t qk = inst_desc(BF, kTok, false), wv = inst_desc(BF, DP, true);
       const uint32_t base = smem_u32(smem);
+      const uint64_t qd = op_desc(base + C::kQ, 16), kd = op_desc(base + C::kK, 16), vd = op_desc(base + C::kV, 16384);
       auto scores = [&](int tile, int k) {
-        const uint32_t q = base + C::kQ + tile * C::kOp, kk = base + C::kK + (k & 1) * C::kOp;
+        const uint64_t a = qd + static_cast<uint32_t>(tile * C::kOp >> 4), bb = kd + static_cast<uint32_t>((k & 1) * C::kOp >> 4);
 #pragma unroll
         for (int d = 0; d < DP / 16; ++d) {
-          const uint32_t off = (d / 4) * 16384 + (d % 4) * 32;
-          tc_mma_ss(tmem + tile * 128, op_desc(q + off, 16), op_desc(kk + off, 16), qk, d > 0);
+          const int off = ((d / 4) * 16384 + (d % 4) * 32) >> 4;
+          tc_mma_ss(tmem + tile * 128, a + off, bb + off, qk, d > 0);
         }
         tc_commit(&c->sfull[tile]);
       };
       auto values = [&](int tile, int k) {
-        const uint32_t vv = base + C::kV + (k & 1) * C::kOp;
+        const uint64_t bb = vd + static_cast<uint32_t>((k & 1) * C::kOp >> 4);
 #pragma unroll
         for (int j = 0; j < kTok / 16; ++j)
-          tc_mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + j * 8, op_desc(vv + j * 2048, 16384), wv, k > 0 || j > 0);
+          tc_mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + j * 8, bb + (j * 2048 >> 4), wv, k > 0 || j > 0);
       };
       bool live = wait_for(c, &c->kfull[0], 0, limit);
       if (live) {
@@ -542,6 +560,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     }
   } else {
     // --------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<E4>::kSoftmax));
     const int tile = role;
     if (tile < tiles) {
       const int rr = tid;  // row of the block (tile * 128 + lane of tensor memory)
@@ -592,39 +611,43 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
           return bits;
         };
-        // The scores are read twice, 32 columns at a time (tensor memory is
-        // fast, registers are not: the block keeps 128 a thread): once for the
-        // maximum, once for the weights.
-        uint32_t sa[32], sb[32];
-        float mq[4];
-        auto maximum = [&](uint32_t (&s)[32], int q) {
+        // 64 of the row's 128 scores are held at a time (all of them do not fit
+        // in registers beside the rest): the upper half is read for the maximum,
+        // then the lower half, whose weights are taken first, then the upper
+        // half again.
+        uint32_t s[2][32];
+        auto hide = [&](uint32_t (&x)[32], int q) {
           if (masked) {
             const uint32_t bits = seen(q);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!(bits >> j & 1)) s[j] = 0xff800000u;
+              if (!(bits >> j & 1)) x[j] = 0xff800000u;
           }
-          float x = __uint_as_float(s[0]), y = __uint_as_float(s[1]);
-#pragma unroll
-          for (int j = 2; j < 32; j += 4) {
-            x = max3(x, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-            if (j + 2 < 32) y = max3(y, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
-          }
-          mq[q] = fmaxf(x, y);
         };
-        tc_ld32(sa, s_addr);
+        auto largest = [](const uint32_t (&x)[32]) {
+          float y = __uint_as_float(x[0]), z = __uint_as_float(x[1]);
+#pragma unroll
+          for (int j = 2; j < 30; j += 4) {
+            y = max3(y, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+            z = max3(z, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+          }
+          return fmaxf(max3(y, __uint_as_float(x[30]), __uint_as_float(x[31])), z);
+        };
+        float mq[4];
+        tc_ld32(s[0], s_addr + 64);
+        tc_ld32(s[1], s_addr + 96);
         tc_wait_ld();
-        tc_ld32(sb, s_addr + 32);
-        maximum(sa, 0);
+        hide(s[0], 2);
+        hide(s[1], 3);
+        mq[2] = largest(s[0]);
+        mq[3] = largest(s[1]);
+        tc_ld32(s[0], s_addr);
+        tc_ld32(s[1], s_addr + 32);
         tc_wait_ld();
-        tc_ld32(sa, s_addr + 64);
-        maximum(sb, 1);
-        tc_wait_ld();
-        tc_ld32(sb, s_addr + 96);
-        maximum(sa, 2);
-        tc_wait_ld();
-        tc_ld32(sa, s_addr);  // for the second pass
-        maximum(sb, 3);
+        hide(s[0], 0);
+        hide(s[1], 1);
+        mq[0] = largest(s[0]);
+        mq[1] = largest(s[1]);
         const float top = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
         const float mt = top == -INFINITY ? -INFINITY : fmaf(top, sc, ex);
         float al = 1.f;
@@ -636,44 +659,38 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         if (k > 0 && __any_sync(FULL_MASK, al != 1.f)) {
 #pragma unroll
           for (int q = 0; q < DP / 32; ++q) {
-            tc_ld32(sb, o_addr + q * 32);
+            uint32_t o[32];
+            tc_ld32(o, o_addr + q * 32);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) sb[j] = __float_as_uint(__uint_as_float(sb[j]) * al);
-            tc_st32(o_addr + q * 32, sb);
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+            tc_st32(o_addr + q * 32, o);
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
         const float2 sc2 = make_float2(sc, sc), off2 = make_float2(ex - ref, ex - ref);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        auto weights = [&](uint32_t (&s)[32], int q) {
-          if (masked) {
-            const uint32_t bits = seen(q);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(bits >> j & 1)) s[j] = 0xff800000u;
-          }
+        auto weights = [&](const uint32_t (&x)[32], int q) {
           uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), sc2, off2);
-            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+            const float2 y = ffma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sc2, off2);
+            const float2 p = make_float2(ex2(y.x), ex2(y.y));
             sum[j & 1] = fadd2(sum[j & 1], p);
             pk[j] = pack16<BF>(p.x, p.y);
           }
-          tc_st16(s_addr + q * 16, pk);  // over scores that have been read: columns 16 q .. 16 q + 15
+          tc_st16(s_addr + q * 16, pk);  // over scores of the lower half, which have been read
         };
+        weights(s[0], 0);
+        tc_ld32(s[0], s_addr + 64);
+        weights(s[1], 1);
         tc_wait_ld();
-        tc_ld32(sb, s_addr + 32);
-        weights(sa, 0);
+        tc_ld32(s[1], s_addr + 96);
+        hide(s[0], 2);
+        weights(s[0], 2);
         tc_wait_ld();
-        tc_ld32(sa, s_addr + 64);
-        weights(sb, 1);
-        tc_wait_ld();
-        tc_ld32(sb, s_addr + 96);
-        weights(sa, 2);
-        tc_wait_ld();
-        weights(sb, 3);
+        hide(s[1], 3);
+        weights(s[1], 3);
         const float add = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if constexpr (E4) {
           // l counts in units of 2^(m - E)
