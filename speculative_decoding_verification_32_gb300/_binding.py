@@ -6,7 +6,9 @@ include/specverify.h, and returns the output tensors.  Every step of the
 computation runs in the library's kernels; there is no other code path.
 """
 import ctypes
+import functools
 import os
+import struct
 import threading
 
 import torch
@@ -415,42 +417,80 @@ def spec_adaptive_tree_policy(accepted_len, depth, draft_top1, ema, zero_run, al
     return shape
 
 
-class _On:
-    """The stream of one call of the cache, attention and log-probability
-    operators.  With an explicit stream, tensors made inside `with` come from
-    that stream's pool, and use() tells the allocator that the stream reads
-    or writes tensors of another's, so none is handed out again too early.
-    scratch() is a workspace of these calls' own: the verify calls keep a
-    header and stamped records in theirs."""
-
-    def __init__(self, device, stream):
-        self.device = device
-        self.given = stream
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        self.ptr = _P(self.stream.cuda_stream)
-        self._ctx = None
-
-    def __enter__(self):
-        if self.given is not None:
-            self._ctx = torch.cuda.stream(self.given)
-            self._ctx.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-
-    def use(self, *tensors):
-        if self.given is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-
-    def scratch(self, nbytes):
-        return workspace(self.device, nbytes, ("scratch", self.stream.cuda_stream))
-
+# The cache, attention and log-probability operators are called once per layer
+# or step, often on a handful of tokens, so their marshalling is kept short:
+# argument structures are packed in one go (same layout as the Structures
+# above), sizes that depend on numbers alone are remembered, pointers go
+# through as integers.
+_CACHE = "4i3q2Q"
+_PACK_APPEND = struct.Struct("<" + _CACHE + "2i2Q6q2Q")
+_PACK_READ = struct.Struct("<" + _CACHE + "2i4Q")
+_PACK_ATTENTION = struct.Struct("<" + _CACHE + _CACHE + "q3ifQ3q3Q")
+_PACK_LOGPROBS = struct.Struct("<6iq3Q")
+_PACK_LOGPROBS_OUT = struct.Struct("<5Q")
+for _s, _t in ((_PACK_APPEND, SpecKvAppendArgs), (_PACK_READ, SpecKvReadArgs),
+               (_PACK_ATTENTION, SpecAttentionArgs), (_PACK_LOGPROBS, SpecLogprobsArgs),
+               (_PACK_LOGPROBS_OUT, SpecLogprobsOut)):
+    assert _s.size == _c.sizeof(_t), _t
 
 _KV_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_fast = {}
+
+
+def _fn(name, nargs):
+    """The C entry point `name`, taking packed structures (bytes) and addresses (int)."""
+    f = _fast.get(name)
+    if f is None:
+        f = lib()[name]
+        f.argtypes = [_P] * nargs
+        f.restype = _c.c_int
+        _fast[name] = f
+    return f
+
+
+class _On:
+    """A call on a stream that the caller names: tensors made inside `with`
+    come from that stream's pool, and use() tells the allocator that the
+    stream reads or writes tensors of another's, so none is handed out again
+    too early.  Without a stream it does nothing (the current stream)."""
+
+    def __init__(self, stream, *tensors):
+        self.stream = stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        self.ctx.__exit__(*exc)
+
+
+class _Here:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_here = _Here()
+
+
+def _scratch(dev, stream, nbytes):
+    """A workspace of these calls' own: the verify calls keep a header and
+    stamped records in theirs."""
+    buf = _ws.get((dev, "scratch", stream))
+    if buf is not None and buf.numel() >= nbytes:
+        return buf
+    with _ws_lock:
+        buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        _ws[(dev, "scratch", stream)] = buf
+    return buf
 
 
 def _kv_dtype(dtype, name):
@@ -459,6 +499,7 @@ def _kv_dtype(dtype, name):
     return _KV_DTYPES[dtype]
 
 
+@functools.lru_cache(maxsize=None)
 def spec_kv_entry_bytes(heads, head_dim, dtype=torch.uint8):
     """Bytes of one token's entry in one plane of a cache (see spec_kv_cache in
     include/specverify.h): dtype torch.uint8 (e4m3 codes and scale bytes),
@@ -470,34 +511,44 @@ def spec_kv_entry_bytes(heads, head_dim, dtype=torch.uint8):
     return n
 
 
+@functools.lru_cache(maxsize=4096)
+def _logprobs_bytes(B, npos, V):
+    return lib().spec_token_logprobs_workspace_size(B, npos, V)
+
+
 def _kv_cache(cache, heads, head_dim, dev, name):
-    """The C descriptor of a cache tensor: [2, rows, slots, heads, head_dim]
-    bfloat16 / float16, or [2, rows, slots, entry bytes] uint8 (e4m3)."""
+    """The fields of a cache tensor's C descriptor: [2, rows, slots, heads,
+    head_dim] bfloat16 / float16, or [2, rows, slots, entry bytes] uint8 (e4m3)."""
     if not isinstance(cache, torch.Tensor) or cache.device != dev:
         raise ValueError(f"{name} must be a tensor on {dev}")
-    e4m3 = cache.dtype == torch.uint8
-    if not e4m3 and cache.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"{name} must be bfloat16, float16 or uint8 (e4m3 entries), got {cache.dtype}")
-    entry = spec_kv_entry_bytes(heads, head_dim, cache.dtype)
-    want = (entry,) if e4m3 else (heads, head_dim)
-    if cache.dim() != 3 + len(want) or cache.shape[0] != 2 or tuple(cache.shape[3:]) != want:
+    dtype = cache.dtype
+    if dtype == torch.uint8:
+        code, e, entry = SPEC_E4M3, 1, spec_kv_entry_bytes(heads, head_dim)
+        want, dense = (entry,), (1,)
+    elif dtype == torch.bfloat16 or dtype == torch.float16:
+        code, e = _KV_DTYPES[dtype], 2
+        spec_kv_entry_bytes(heads, head_dim, dtype)
+        want, dense = (heads, head_dim), (head_dim, 1)
+    else:
+        raise TypeError(f"{name} must be bfloat16, float16 or uint8 (e4m3 entries), got {dtype}")
+    shape, stride = cache.shape, cache.stride()
+    if len(shape) != 3 + len(want) or shape[0] != 2 or shape[3:] != want:
         raise ValueError(f"{name} must be [2, rows, slots, {', '.join(map(str, want))}], "
-                         f"got {tuple(cache.shape)}")
-    if any(cache.stride(3 + i) != s and cache.shape[3 + i] != 1
-           for i, s in enumerate((1,) if e4m3 else (head_dim, 1))):
+                         f"got {tuple(shape)}")
+    if stride[3:] != dense and any(a != b and n != 1 for a, b, n in zip(stride[3:], dense, want)):
         raise ValueError(f"{name}: one token's entry must be contiguous")
-    e = cache.element_size()
-    return SpecKvCache(cache.shape[1], heads, head_dim,
-                       SPEC_E4M3 if e4m3 else _kv_dtype(cache.dtype, name), cache.shape[2],
-                       cache.stride(1) * e, cache.stride(2) * e, _P(cache.data_ptr()),
-                       _P(cache.data_ptr() + cache.stride(0) * e))
+    k = cache.data_ptr()
+    return (shape[1], heads, head_dim, code, shape[2], stride[1] * e, stride[2] * e, k, k + stride[0] * e)
 
 
-def _rows_i32(t, name, dev, n):
+def _i32(t, name, dev, shape):
+    """The address of an int32 tensor of this shape, or 0 for None."""
+    if t is None:
+        return 0
     _req(t, name, dev, torch.int32)
-    if t is not None and tuple(t.shape) != (n,):
-        raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
-    return t
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
 
 
 def spec_kv_append(cache, k, v, kv_len, count=None, stream=None):
@@ -513,27 +564,25 @@ def spec_kv_append(cache, k, v, kv_len, count=None, stream=None):
     """
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a [B, N, heads, head_dim] tensor")
-    dev = k.device
-    if not isinstance(v, torch.Tensor) or v.device != dev or v.shape != k.shape:
+    dev, shape, dtype = k.device, k.shape, k.dtype
+    if not isinstance(v, torch.Tensor) or v.device != dev or v.shape != shape:
         raise ValueError(f"v must be a tensor like k, on {dev}")
-    if v.dtype != k.dtype:
-        raise TypeError(f"v must be {k.dtype}, got {v.dtype}")
-    B, N, heads, D = k.shape
-    for t, n in ((k, "k"), (v, "v")):
-        if t.stride(3) != 1 and D > 1:
-            raise ValueError(f"{n}: the last dimension must be dense")
+    if v.dtype != dtype:
+        raise TypeError(f"v must be {dtype}, got {v.dtype}")
+    B, N, heads, D = shape
+    ks, vs = k.stride(), v.stride()
+    if (ks[3] != 1 or vs[3] != 1) and D > 1:
+        raise ValueError("k and v: the last dimension must be dense")
     c = _kv_cache(cache, heads, D, dev, "cache")
-    if c.rows != B:
-        raise ValueError(f"cache has {c.rows} rows, k has {B}")
-    _rows_i32(kv_len, "kv_len", dev, B)
-    _rows_i32(count, "count", dev, B)
-    i64x3 = _c.c_int64 * 3
-    a = SpecKvAppendArgs(c, N, _kv_dtype(k.dtype, "k"), _ptr(k), _ptr(v), i64x3(*k.stride()[:3]),
-                         i64x3(*v.stride()[:3]), _ptr(kv_len), _ptr(count))
-    with _On(dev, stream) as on:
-        on.use(cache, k, v, kv_len, count)
+    if c[0] != B:
+        raise ValueError(f"cache has {c[0]} rows, k has {B}")
+    if kv_len is None:
+        raise ValueError("kv_len is needed")
+    a = _PACK_APPEND.pack(*c, N, _kv_dtype(dtype, "k"), k.data_ptr(), v.data_ptr(), *ks[:3], *vs[:3],
+                          _i32(kv_len, "kv_len", dev, (B,)), _i32(count, "count", dev, (B,)))
+    with _here if stream is None else _On(stream, cache, k, v, kv_len, count):
         status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
-        _check(lib().spec_kv_append(_c.byref(a), _ptr(status), on.ptr))
+        _check(_fn("spec_kv_append", 3)(a, status.data_ptr(), _raw_stream(dev.index)))
     return status
 
 
@@ -546,23 +595,25 @@ def spec_kv_read(cache, length, T, heads=None, head_dim=None, start=None, dtype=
     if not isinstance(cache, torch.Tensor) or cache.dim() < 4:
         raise ValueError("cache must be a [2, rows, slots, ...] tensor")
     dev = cache.device
-    if cache.dtype != torch.uint8:
-        heads, head_dim = cache.shape[3:5] if cache.dim() == 5 else (heads, head_dim)
+    if cache.dtype != torch.uint8 and cache.dim() == 5:
+        heads, head_dim = cache.shape[3:5]
     if heads is None or head_dim is None:
         raise ValueError("heads and head_dim are needed for a uint8 cache")
-    c = _kv_cache(cache, int(heads), int(head_dim), dev, "cache")
-    B = c.rows
-    _rows_i32(length, "length", dev, B)
-    _rows_i32(start, "start", dev, B)
-    code = _kv_dtype(dtype, "dtype")
-    with _On(dev, stream) as on:
-        on.use(cache, length, start)
+    c = _kv_cache(cache, heads, head_dim, dev, "cache")
+    B = c[0]
+    if length is None:
+        raise ValueError("length is needed")
+    code, n, s = _kv_dtype(dtype, "dtype"), _i32(length, "length", dev, (B,)), _i32(start, "start", dev, (B,))
+    with _here if stream is None else _On(stream, cache, length, start):
         k = torch.empty(B, T, heads, head_dim, dtype=dtype, device=dev)
         v = torch.empty_like(k)
         status = (torch.empty if T else torch.zeros)(B, dtype=torch.int32, device=dev)
-        a = SpecKvReadArgs(c, int(T), code, _ptr(k), _ptr(v), _ptr(start), _ptr(length))
-        _check(lib().spec_kv_read(_c.byref(a), _ptr(status), on.ptr))
+        a = _PACK_READ.pack(*c, T, code, k.data_ptr(), v.data_ptr(), s, n)
+        _check(_fn("spec_kv_read", 3)(a, status.data_ptr(), _raw_stream(dev.index)))
     return k, v, status
+
+
+_NO_CACHE = (0,) * 9
 
 
 def spec_prefix_attention(q, cache, kv_len, prefix=None, prefix_len=None, parent=None, count=None,
@@ -581,43 +632,45 @@ def spec_prefix_attention(q, cache, kv_len, prefix=None, prefix_len=None, parent
     """
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B, N, q_heads, head_dim] tensor")
-    dev = q.device
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    B, N, heads, D = q.shape
-    if q.stride(3) != 1 and D > 1:
+    dev, shape, dtype = q.device, q.shape, q.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float16:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    B, N, heads, D = shape
+    qs = q.stride()
+    if qs[3] != 1 and D > 1:
         raise ValueError("q: the last dimension must be dense")
     if kv_heads is None:
         if not isinstance(cache, torch.Tensor) or cache.dim() != 5:
             raise ValueError("kv_heads is needed for a uint8 cache")
         kv_heads = cache.shape[3]
     c = _kv_cache(cache, kv_heads, D, dev, "cache")
-    if c.rows != B:
-        raise ValueError(f"cache has {c.rows} rows, q has {B}")
+    if c[0] != B:
+        raise ValueError(f"cache has {c[0]} rows, q has {B}")
     if prefix is not None:
         pc = _kv_cache(prefix, kv_heads, D, dev, "prefix")
-        P = pc.slots if prefix_len is None else int(prefix_len)
+        P = pc[4] if prefix_len is None else int(prefix_len)
     else:
         if prefix_len:
             raise ValueError("prefix_len without a prefix")
-        pc, P = SpecKvCache(), 0
-    _rows_i32(kv_len, "kv_len", dev, B)
-    _rows_i32(count, "count", dev, B)
-    _req(parent, "parent", dev, torch.int32)
-    if parent is not None and tuple(parent.shape) != (B, N):
-        raise ValueError(f"parent must be [{B}, {N}], got {tuple(parent.shape)}")
-    a = SpecAttentionArgs(c, pc, P, N, heads, _KV_DTYPES[q.dtype],
-                          D ** -0.5 if scale is None else float(scale), _ptr(q),
-                          (_c.c_int64 * 3)(*q.stride()[:3]), _ptr(kv_len), _ptr(count), _ptr(parent))
-    L = lib()
-    with _On(dev, stream) as on:
-        on.use(q, cache, kv_len, prefix, parent, count)
-        out = torch.empty(B, N, heads, D, dtype=q.dtype, device=dev)
+        pc, P = _NO_CACHE, 0
+    if kv_len is None:
+        raise ValueError("kv_len is needed")
+    a = _PACK_ATTENTION.pack(*c, *pc, P, N, heads, _KV_DTYPES[dtype], D ** -0.5 if scale is None else scale,
+                             q.data_ptr(), *qs[:3], _i32(kv_len, "kv_len", dev, (B,)),
+                             _i32(count, "count", dev, (B,)), _i32(parent, "parent", dev, (B, N)))
+    f = _fast.get("spec_prefix_attention_workspace_size")
+    if f is None:
+        f = lib()["spec_prefix_attention_workspace_size"]
+        f.argtypes, f.restype = [_P], _c.c_size_t
+        _fast["spec_prefix_attention_workspace_size"] = f
+    with _here if stream is None else _On(stream, q, cache, kv_len, prefix, parent, count):
+        out = torch.empty(shape, dtype=dtype, device=dev)
         lse = torch.empty(B, N, heads, dtype=torch.float32, device=dev)
         status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
-        ws = on.scratch(L.spec_prefix_attention_workspace_size(_c.byref(a)))
-        _check(L.spec_prefix_attention(_c.byref(a), _ptr(out), _ptr(lse), _ptr(status), _ptr(ws),
-                                       ws.numel(), on.ptr))
+        s = _raw_stream(dev.index)
+        ws = _scratch(dev, s, f(a))
+        _check(_fn("spec_prefix_attention", 7)(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(),
+                                               ws.data_ptr(), ws.numel(), s))
     return out, lse, status
 
 
@@ -633,33 +686,33 @@ def spec_token_logprobs(logits, tokens=None, temperature=None, m=0, stream=None)
     """
     if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
         raise ValueError("logits must be a [B, npos, V] tensor")
-    dev = logits.device
+    dev, st = logits.device, logits.stride()
     B, npos, V = logits.shape
     dt = _dtype_code(logits)
-    pitch = logits.stride(1) if npos > 1 else logits.stride(0) if B > 1 else V
-    if (V > 1 and logits.stride(2) != 1) or (B > 1 and logits.stride(0) != npos * pitch):
+    pitch = st[1] if npos > 1 else st[0] if B > 1 else V
+    if (V > 1 and st[2] != 1) or (B > 1 and st[0] != npos * pitch):
         raise ValueError("logits: positions must be evenly spaced with a dense last dimension")
-    _req(tokens, "tokens", dev, torch.int32)
-    if tokens is not None and tuple(tokens.shape) != (B, npos):
-        raise ValueError(f"tokens must be [{B}, {npos}], got {tuple(tokens.shape)}")
-    _req(temperature, "temperature", dev, torch.float32)
-    if temperature is not None and tuple(temperature.shape) != (B,):
-        raise ValueError(f"temperature must be [{B}], got {tuple(temperature.shape)}")
-    L = lib()
-    with _On(dev, stream) as on:
-        on.use(logits, tokens, temperature)
-        out = dict(entropy=torch.empty(B, npos, dtype=torch.float32, device=dev),
+    tk = _i32(tokens, "tokens", dev, (B, npos))
+    if temperature is not None:
+        _req(temperature, "temperature", dev, torch.float32)
+        if temperature.shape != (B,):
+            raise ValueError(f"temperature must be [{B}], got {list(temperature.shape)}")
+    a = _PACK_LOGPROBS.pack(B, npos, V, dt, m, 0, pitch, logits.data_ptr(), tk,
+                            0 if temperature is None else temperature.data_ptr())
+    f32 = torch.float32
+    with _here if stream is None else _On(stream, logits, tokens, temperature):
+        out = dict(entropy=torch.empty(B, npos, dtype=f32, device=dev),
                    status=torch.empty(B, npos, dtype=torch.int32, device=dev),
                    top_ids=torch.empty(B, npos, m, dtype=torch.int32, device=dev),
-                   top_logprobs=torch.empty(B, npos, m, dtype=torch.float32, device=dev))
+                   top_logprobs=torch.empty(B, npos, m, dtype=f32, device=dev))
         if tokens is not None:
-            out["logprob"] = torch.empty(B, npos, dtype=torch.float32, device=dev)
-        a = SpecLogprobsArgs(B, npos, V, dt, int(m), 0, pitch, _ptr(logits), _ptr(tokens),
-                             _ptr(temperature))
-        o = SpecLogprobsOut(_ptr(out.get("logprob")), _ptr(out["entropy"]), _ptr(out["top_ids"]),
-                            _ptr(out["top_logprobs"]), _ptr(out["status"]))
-        ws = on.scratch(L.spec_token_logprobs_workspace_size(B, npos, V))
-        _check(L.spec_token_logprobs(_c.byref(a), _c.byref(o), _ptr(ws), ws.numel(), on.ptr))
+            out["logprob"] = torch.empty(B, npos, dtype=f32, device=dev)
+        o = _PACK_LOGPROBS_OUT.pack(out["logprob"].data_ptr() if tokens is not None else 0,
+                                    out["entropy"].data_ptr(), out["top_ids"].data_ptr(),
+                                    out["top_logprobs"].data_ptr(), out["status"].data_ptr())
+        s = _raw_stream(dev.index)
+        ws = _scratch(dev, s, _logprobs_bytes(B, npos, V))
+        _check(_fn("spec_token_logprobs", 5)(a, o, ws.data_ptr(), ws.numel(), s))
     return out
 
 

@@ -14,6 +14,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kv_layout.cuh"
 #include "specverify.h"
@@ -44,7 +46,7 @@ struct AttnParams {
   int rows;         // B * N * Hq
   int psplits, pchunk;  // prefix parts (slots 0 .. psplits - 1) and tokens in each
   int osplits;          // own parts (slots psplits ..)
-  int chunk;            // own parts are multiples of this many tokens
+  int chunk, min_chunk; // own parts: multiples of `chunk` tokens, `min_chunk` at least
   int oblk;             // query rows per own item
   int32_t *oflag;       // per own item: a value that is not finite was left out of its sums
   // outputs
@@ -69,10 +71,10 @@ __device__ __forceinline__ int row_queries(const AttnParams &P, int b) {
 }
 
 // The own part `split` covers of a row's len entries: equal parts, rounded up
-// to P.chunk tokens.
+// to P.chunk tokens, none shorter than P.min_chunk but the last.
 __device__ __forceinline__ void own_range(const AttnParams &P, int len, int split, int &t0, int &t1) {
   int chunk = (len + P.osplits - 1) / P.osplits;
-  chunk = (chunk + P.chunk - 1) / P.chunk * P.chunk;
+  chunk = max(P.min_chunk, (chunk + P.chunk - 1) / P.chunk * P.chunk);
   const long long a = static_cast<long long>(split) * chunk;
   t0 = static_cast<int>(min(a, static_cast<long long>(len)));
   t1 = static_cast<int>(min(a + chunk, static_cast<long long>(len)));
@@ -149,6 +151,20 @@ __device__ __forceinline__ float scale_exponent(uint32_t c) {
 // span and takes the rest of the factor on its weight.
 constexpr float kMinExponent = -60.f;
 constexpr float kExponentSpan = 60.f;
+
+// Raises a kernel's dynamic shared memory limit, once per device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Host launchers.
 // attn_rows_kernel over the own entries (own) and the prefix (prefix) ...

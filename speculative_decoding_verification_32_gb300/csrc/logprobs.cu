@@ -184,7 +184,9 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   __shared__ LpPart sh[kLpThreads / 32];
   __shared__ int red[kLpThreads / 32];
+  __shared__ int counts[2][kLpThreads / 32][3];
   __shared__ int n_chunks, n_cands;
+  extern __shared__ __align__(16) unsigned char lp_smem[];  // the position's chunk keys
   __shared__ int chunk[kLpChunks];
   __shared__ unsigned long long cand[kLpCands];
   const int tok = P.tokens ? __ldg(P.tokens + r) : -1;
@@ -247,20 +249,39 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_
     }
     return;
   }
-  // The chunk keys' m-th largest: bit by bit, the largest t that at least m
-  // keys reach.  If the position has fewer than m chunks, t = 0: every
+  // The chunk keys' m-th largest: two bits at a time, the largest t that at
+  // least m keys reach.  If the position has fewer than m chunks, t = 0: every
   // chunk is looked at.
   const int nkeys = P.nslices * kLpThreads;
   const unsigned short *ck = P.cmax + static_cast<size_t>(r) * nkeys;
+  unsigned short *const keys = reinterpret_cast<unsigned short *>(lp_smem);
+  for (int i = tid; i < nkeys / 8; i += kLpThreads)
+    reinterpret_cast<uint4 *>(keys)[i] = reinterpret_cast<const uint4 *>(ck)[i];
+  __syncthreads();
+  const uint32_t *const pairs = reinterpret_cast<const uint32_t *>(keys);
   unsigned t16 = 0;
-  for (int bit = 15; bit >= 0; --bit) {
-    const unsigned t = t16 | (1u << bit);
-    int c = 0;
-    for (int i = tid; i < nkeys; i += kLpThreads) c += ck[i] >= t;
-    if (block_sum(c, red) >= P.m) t16 = t;
+  for (int bit = 14; bit >= 0; bit -= 2) {
+    const unsigned q = 1u << bit;
+    int c1 = 0, c2 = 0, c3 = 0;
+    for (int i = tid; i < nkeys / 2; i += kLpThreads) {
+      const uint32_t w = pairs[i], lo = w & 0xffffu, hi = w >> 16;
+      c1 += (lo >= t16 + q) + (hi >= t16 + q);
+      c2 += (lo >= t16 + 2 * q) + (hi >= t16 + 2 * q);
+      c3 += (lo >= t16 + 3 * q) + (hi >= t16 + 3 * q);
+    }
+    c1 = __reduce_add_sync(FULL_MASK, c1);
+    c2 = __reduce_add_sync(FULL_MASK, c2);
+    c3 = __reduce_add_sync(FULL_MASK, c3);
+    int(*const row)[3] = counts[(bit >> 1) & 1];  // two sets: one barrier a step is enough
+    if (lane == 0) row[warp][0] = c1, row[warp][1] = c2, row[warp][2] = c3;
+    __syncthreads();
+    c1 = c2 = c3 = 0;
+#pragma unroll
+    for (int w = 0; w < kLpThreads / 32; ++w) c1 += row[w][0], c2 += row[w][1], c3 += row[w][2];
+    t16 += c3 >= P.m ? 3 * q : c2 >= P.m ? 2 * q : c1 >= P.m ? q : 0u;
   }
   for (int i = tid; i < nkeys; i += kLpThreads)
-    if (ck[i] >= t16) {
+    if (keys[i] >= t16) {
       const int at = atomicAdd(&n_chunks, 1);
       if (at < kLpChunks) chunk[at] = i;
     }
@@ -350,6 +371,7 @@ cudaError_t launch_logprobs(const LpParams &p, bool vec, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.rows);
   cfg.blockDim = dim3(kLpThreads);
+  cfg.dynamicSmemBytes = p.m > 0 ? static_cast<size_t>(p.nslices) * kLpThreads * 2 : 0;  // 32 KB at most
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

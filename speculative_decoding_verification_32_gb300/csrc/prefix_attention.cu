@@ -674,20 +674,25 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
 // One warp per output row: the weights of the parts, then their sum.
 template <bool BF, bool E4>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams P) {
-  grid_dependency_wait();
   const int lane = threadIdx.x % 32;
   const long long r = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
-  if (r >= P.rows) return;
   const int nslots = P.psplits + P.osplits;
   const int b = static_cast<int>(r / (static_cast<long long>(P.N) * P.Hq));
-  const int n = row_queries(P, b);
+  int n = 0;
+  if (r < P.rows && !P.rowinfo) n = row_queries(P, b);  // inputs: no need to wait for the kernels before
+  grid_dependency_wait();
+  if (r >= P.rows) return;
+  if (P.rowinfo) n = row_queries(P, b);
   const int qt = static_cast<int>(r / P.Hq) - b * P.N, h = static_cast<int>(r % P.Hq);
   const bool on = qt < n;
   float Z = -INFINITY;
   bool gone = false;  // a part's kernel gave up: the row is flagged and its answer left empty
+  float2 ml0 = make_float2(-INFINITY, -INFINITY);  // this lane's first part
   if (on)
     for (int s = lane; s < nslots; s += 32) {
-      const float z = P.ml[static_cast<long long>(s) * P.rows + r].y;
+      const float2 x = P.ml[static_cast<long long>(s) * P.rows + r];
+      if (s < 32) ml0 = x;
+      const float z = x.y;
       gone = gone || __float_as_uint(z) == kTimeoutBits;
       Z = fmaxf(Z, z);
     }
@@ -697,15 +702,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   const float zref = Z == -INFINITY ? 0.f : Z;
   float S = 0.f;
   if (gone && lane == 0 && P.row_status) P.row_status[b] = SPEC_ROW_TIMEOUT;
-  if (on && !gone)
-    for (int s = lane; s < nslots; s += 32) S += ex2(P.ml[static_cast<long long>(s) * P.rows + r].y - zref);
+  if (on && !gone) {
+    S = ex2(ml0.y - zref);
+    for (int s = lane + 32; s < nslots; s += 32) S += ex2(P.ml[static_cast<long long>(s) * P.rows + r].y - zref);
+  }
   S = warp_sum(S);
   const float z = S == 0.f ? -INFINITY : zref + log2f(S);
   float acc[4] = {0.f, 0.f, 0.f, 0.f};  // columns 4 lane .. 4 lane + 3
   if (S != 0.f)
     for (int s0 = 0; s0 < nslots; s0 += 32) {
-      float2 ml = make_float2(-INFINITY, -INFINITY);
-      if (s0 + lane < nslots) ml = P.ml[static_cast<long long>(s0 + lane) * P.rows + r];
+      float2 ml = ml0;
+      if (s0 > 0) ml = s0 + lane < nslots ? P.ml[static_cast<long long>(s0 + lane) * P.rows + r] : make_float2(-INFINITY, -INFINITY);
       const float wl = ex2(ml.x - z);
       // the parts that left a sum, four at a time: their loads overlap
       unsigned todo = __ballot_sync(FULL_MASK, ml.y != -INFINITY);
@@ -775,7 +782,7 @@ cudaError_t launch_rows(const AttnParams &p, bool own, bool prefix, cudaStream_t
   const long long pitems = prefix ? static_cast<long long>(p.H) * pblocks * p.psplits : 0;
   const long long items = pitems + (own ? static_cast<long long>(p.B) * p.H * oblocks * p.osplits : 0);
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<CT, DP, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const cudaError_t e = allow_smem<attn_rows_kernel<CT, DP, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
   attn_rows_kernel<CT, DP, MT><<<static_cast<unsigned>(items), kRowThreads, C::kSmem, s>>>(p, static_cast<int>(pitems), pblocks, oblocks);
   return cudaGetLastError();
@@ -793,7 +800,7 @@ cudaError_t launch_rows_d(const AttnParams &p, bool own, bool prefix, cudaStream
 }
 
 struct AttnPlan {
-  int psplits, pchunk, osplits, W;
+  int psplits, pchunk, osplits, min_chunk, W;
   bool ptile, otile;  // attn_tile_kernel for the prefix, for the own entries
   int oblk;           // query rows per own item
   size_t rows, anc_at, info_at, flag_at, ml_at, part_at, bytes;
@@ -863,7 +870,17 @@ AttnPlan plan_attention(const spec_attention_args *a) {
   }
   p.oblk = p.otile ? 256 : two_row_tiles(c.rows, a->N, static_cast<int>(G), a->prefix_len > 0 && !p.ptile) ? 32 : 16;
   const long long oblocks = (a->N * G + p.oblk - 1) / p.oblk;
-  p.osplits = p.otile ? tile_parts(c.rows * c.heads * oblocks, c.slots) : row_parts(c.rows * c.heads * oblocks, c.slots);
+  const long long oitems = c.rows * c.heads * oblocks;
+  p.osplits = p.otile ? tile_parts(oitems, c.slots) : row_parts(oitems, c.slots);
+  p.min_chunk = p.otile ? 128 : 64;
+  if (!p.otile && p.osplits == 1) {
+    // enough items as they are, but rows differ in length: parts of 256
+    // tokens keep a long row from holding up the rest, up to 16 items per SM
+    // (most of them empty if the rows are short).  64 rows of 100 to 2000
+    // tokens: 54 us as whole rows, 37 us in parts.
+    p.osplits = static_cast<int>(std::max<long long>(1, std::min<long long>((c.slots + 255) / 256, 16 * kSms / oitems)));
+    p.min_chunk = 256;
+  }
   p.W = (a->N + 31) / 32;
   size_t at = 0;
   p.anc_at = at;
@@ -951,6 +968,7 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   p.pchunk = plan.pchunk;
   p.osplits = plan.osplits;
   p.chunk = plan.otile ? 128 : 64;
+  p.min_chunk = plan.min_chunk;
   p.oblk = plan.oblk;
   p.oflag = reinterpret_cast<int32_t *>(w + plan.flag_at);
   p.out = out;

@@ -743,7 +743,7 @@ cudaError_t launch(const AttnParams &p, cudaStream_t s) {
   const int blocks = static_cast<int>(((PRE ? static_cast<long long>(p.B) : 1LL) * p.N * p.G + 255) / 256);
   const long long items = PRE ? static_cast<long long>(p.H) * blocks * p.psplits : static_cast<long long>(p.B) * p.H * blocks * p.osplits;
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<CT, DP, PRE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const cudaError_t e = allow_smem<attn_tile_kernel<CT, DP, PRE>>(C::kSmem);
   if (e != cudaSuccess) return e;
   attn_tile_kernel<CT, DP, PRE><<<static_cast<unsigned>(items), kTileThreads, C::kSmem, s>>>(p, blocks);
   return cudaGetLastError();
