@@ -152,6 +152,13 @@ __device__ __forceinline__ float scale_exponent(uint32_t c) {
 constexpr float kMinExponent = -60.f;
 constexpr float kExponentSpan = 60.f;
 
+// 32 bytes, a whole sector, aligned to 32
+__device__ __forceinline__ void st_global_v8(float *p, const uint32_t *r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Raises a kernel's dynamic shared memory limit, once per device.
 template <auto Kernel>
 cudaError_t allow_smem(int bytes) {

@@ -7,12 +7,12 @@
 //  attn_tile_kernel (prefix_attention_tile.cu) -- many query rows.
 //  attn_rows_kernel -- 16 or 32 query rows (the query heads of one KV head and
 //    the tokens of one row; for the prefix, of all rows) against a range of
-//    tokens.  Bound by the cache's bytes, so what matters is bytes in flight:
-//    each warp streams its own blocks of 16 tokens through its own ring of
-//    asynchronous copies and never waits for another warp; the warps' sums
-//    join once at the end.  e4m3 codes are turned into fp16 in registers on
-//    the way to the tensor cores (exact), scales go into the scores and the
-//    weights.
+//    tokens, one warp.  Bound by the cache's bytes, so what matters is bytes in
+//    flight: every warp streams its range through a ring of asynchronous
+//    copies of its own.  e4m3 codes are turned into fp16 in registers on the
+//    way to the tensor cores (exact), scales go into the scores and the
+//    weights.  With this few rows the synchronous matrix instructions keep up
+//    with memory; tensor memory's tiles of 128 rows would be mostly padding.
 //  attn_join_kernel -- one warp per query row adds up the parts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,9 +29,6 @@ namespace sv {
 namespace {
 
 constexpr int kSms = 152;           // parts are sized for this many SMs
-constexpr int kRowWarps = 4;        // warps of attn_rows_kernel, each with its own ring
-constexpr int kRowThreads = 32 * kRowWarps;
-constexpr int kBlk = 16;            // tokens per block
 constexpr float kRowLazy = 8.f;
 constexpr int kMaskThreads = 256;
 constexpr int kJoinThreads = 256;
@@ -75,34 +72,37 @@ template <int CT, int DP, int MT>
 struct RowCfg {
   static constexpr bool E4 = CT == SPEC_E4M3;
   static constexpr int kEsz = E4 ? 1 : 2;
+  static constexpr int kM = 16 * MT;                        // query rows
+  static constexpr int kBlk = E4 && MT == 1 ? 32 : 16;      // tokens per block
   static constexpr int kStages = 3;
   static constexpr int kPitch = DP * kEsz + 16;             // bytes of one token in a ring slot
   static constexpr int kPlane = kBlk * kPitch;              // K or V of a block
   static constexpr int kScales = E4 ? 2 * kBlk * 4 : 0;     // scale words, K then V
   static constexpr int kStage = 2 * kPlane + kScales;
   static constexpr int kQPitch = DP * 2 + 16;
-  static constexpr int kM = 16 * MT;
-  static constexpr int kRing = kRowWarps * kStages * kStage;
-  static constexpr int kOPitch = DP + (E4 ? 16 : 8);        // floats of a row of the warps' sums: no bank met twice
-  static constexpr int kMerge = kRowWarps * kM * (kOPitch + 2) * 4;  // the warps' sums, after the loop
-  static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kSmem = kBody + kM * kQPitch + kM * 4;
+  static constexpr int kQ = kM * kQPitch + kM * 4;          // queries and factors, in the last slot before it is used
+  static constexpr int kSmem = (kStages - 1) * kStage + (kStage > kQ ? kStage : kQ);
 };
 
-// Item: prefix items first (KV head, block of kM rows of all rows' queries,
-// part), then own items (row, KV head, block, part).
+// One warp per item and nothing shared between warps: 8 to 12 items run on an
+// SM side by side, and while one starts or ends the others keep the memory
+// busy.  (Four warps on one item and a join in shared memory: 52 us where this
+// takes 35, 64 chains of 6 tokens over 33 K entries of 8 heads in bf16.)
+// Items: prefix (KV head, block of kM rows of all rows' queries, part), then
+// own (row, KV head, block, part).
 template <int CT, int DP, int MT>
-__global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_constant__ AttnParams P, int pitems,
-                                                                int pblocks, int oblocks) {
+__global__ void __launch_bounds__(32) attn_rows_kernel(const __grid_constant__ AttnParams P, int pitems, int pblocks,
+                                                       int oblocks) {
   using C = RowCfg<CT, DP, MT>;
   constexpr bool E4 = C::E4;
   constexpr bool BF = CT == SPEC_BF16;
-  constexpr int kSteps = DP / 16, kNt = DP / 8;
+  constexpr int kBlk = C::kBlk;
+  constexpr int kSteps = DP / 16, kNt = DP / 8;  // k-steps of the scores, column tiles of the sums
+  constexpr int kTt = kBlk / 8, kTs = kBlk / 16; // token tiles of the scores, k-steps of the sums
   extern __shared__ __align__(16) unsigned char smem[];
-  unsigned char *const qsm = smem + C::kBody;
+  unsigned char *const qsm = smem + (C::kStages - 1) * C::kStage;
   float *const qfac = reinterpret_cast<float *>(qsm + C::kM * C::kQPitch);
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int quad = lane / 4, j4 = lane % 4;
+  const int lane = threadIdx.x, quad = lane / 4, j4 = lane % 4;
 
   // --- the item
   int item = blockIdx.x;
@@ -125,26 +125,27 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
   const int r0 = blk * C::kM;              // first query row of the block
   const int nrows = (pre ? P.B : 1) * P.N * P.G;
   const int slot = pre ? split : P.psplits + split;
-  int t0, t1, len0 = 0;                    // tokens; own slots below len0 are seen by every query
+  int t0, t1, len0 = 0, cnt = 0;           // tokens; own slots below len0 are seen by every query
   const unsigned char *kb, *vb;
   long long ts;
-  int bad_or_count = 0;
   if (pre) {
     t0 = split * P.pchunk;
     t1 = min(P.P, t0 + P.pchunk);
     kb = P.pk, vb = P.pv, ts = P.ptok_stride;
   } else {
-    bad_or_count = row_queries(P, b);
+    cnt = row_queries(P, b);
     len0 = __ldg(P.kv_len + b);
-    if (bad_or_count <= 0)
+    if (cnt <= 0)
       t0 = t1 = 0;
     else
-      own_range(P, len0 + bad_or_count, split, t0, t1);
+      own_range(P, len0 + cnt, split, t0, t1);
     kb = P.k + b * P.row_stride, vb = P.v + b * P.row_stride, ts = P.tok_stride;
+    if (split == 0 && blk == 0 && g == 0 && lane == 0 && P.row_status)
+      P.row_status[b] = cnt >= 0 ? 0 : cnt == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
   }
-  // Lane i of every warp knows query row i of the block (kM <= 32): its output
-  // row (-1 past the last), whether there is such a query, where it is.
-  int my_row = -1, my_tok = 0;
+  // Lane i knows query row i of the block (kM <= 32): its output row (-1 past
+  // the last), its token, where its query is, whether it has a use.
+  int my_row = -1;
   bool my_use = false;
   long long my_q = 0;
   {
@@ -153,36 +154,38 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
       const int t = r / P.G, h = g * P.G + (r - t * P.G);
       const int qb = pre ? t / P.N : b, qt = pre ? t - qb * P.N : t;
       my_row = (qb * P.N + qt) * P.Hq + h;
-      my_tok = qt;
-      my_use = qt < (pre ? row_queries(P, qb) : bad_or_count);
+      my_use = qt < (pre ? row_queries(P, qb) : cnt);
       my_q = qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2];
     }
   }
-  if (!pre && split == 0 && blk == 0 && g == 0 && tid == 0 && P.row_status)
-    P.row_status[b] = bad_or_count >= 0 ? 0 : bad_or_count == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
   if (t0 >= t1) {  // nothing here (an empty part, or a row that cannot be used)
-    if (!pre && tid == 0) P.oflag[blockIdx.x - pitems] = 0;
-    if (warp == 0 && my_row >= 0) P.ml[static_cast<long long>(slot) * P.rows + my_row] = make_float2(-INFINITY, -INFINITY);
+    if (!pre && lane == 0) P.oflag[blockIdx.x - pitems] = 0;
+    if (my_row >= 0) P.ml[static_cast<long long>(slot) * P.rows + my_row] = make_float2(-INFINITY, -INFINITY);
     return;
   }
 
-  // --- this warp's ring of token blocks
-  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage;
+  // --- the ring of token blocks: lanes over a token's 16-byte pieces, then
+  // over tokens; pointers advance
+  const uint32_t ring = smem_u32(smem);
   const int nblk = (t1 - t0 + kBlk - 1) / kBlk;
-  // lanes over a token's 16-byte pieces, then over tokens; pointers advance
   constexpr int L = DP * C::kEsz / 16, kPer = kBlk * L / 32, kStep = 32 / L;
   const int pc = lane % L, row0 = lane / L;
   const bool col = pc * 16 < P.D * C::kEsz;
-  const long long first = static_cast<long long>(t0 + warp * kBlk + row0) * ts +
-                          static_cast<long long>(g) * P.D * C::kEsz + (col ? pc * 16 : 0);
+  const long long first = static_cast<long long>(t0 + row0) * ts + static_cast<long long>(g) * P.D * C::kEsz + (col ? pc * 16 : 0);
   const unsigned char *kp = kb + first, *vp = vb + first;
-  const long long step = ts * kStep, jump = ts * (kRowWarps * kBlk);
-  const unsigned char *sp = nullptr;  // scale words: lanes 0-15 the keys', 16-31 the values'
-  if constexpr (E4)
-    sp = (lane < kBlk ? kb : vb) + static_cast<long long>(t0 + warp * kBlk + lane % kBlk) * ts + static_cast<long long>(P.H) * P.D + (g & ~3);
+  const long long step = ts * kStep;
+  // scale words: item i of 0 .. 2 kBlk - 1 is the keys' of token i, then the values'
+  constexpr int kWords = E4 ? 2 * kBlk / 32 : 1;
+  const unsigned char *sp[kWords] = {};
+  if constexpr (E4) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int w = i * 32 + lane;
+      sp[i] = (w < kBlk ? kb : vb) + static_cast<long long>(t0 + w % kBlk) * ts + static_cast<long long>(P.H) * P.D + (g & ~3);
+    }
+  }
   if (P.D < DP) {  // the columns past the head vector stay zero: no copy writes them
-    for (int i = lane; i < C::kStages * C::kStage / 16; i += 32)
-      *reinterpret_cast<uint4 *>(smem + warp * C::kStages * C::kStage + i * 16) = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < C::kStages * C::kStage / 16; i += 32) *reinterpret_cast<uint4 *>(smem + i * 16) = make_uint4(0, 0, 0, 0);
     __syncwarp();
   }
   auto issue = [&](int blkno, int st) {
@@ -190,84 +193,86 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
       const uint32_t base = ring + st * C::kStage + row0 * C::kPitch + pc * 16;
       const int left = t1 - (t0 + blkno * kBlk);
       if (col) {
-        const unsigned char *k = kp, *v = vp;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const bool on = row0 + i * kStep < left;
-          cp_async16_zfill(base + i * kStep * C::kPitch, on ? k : kb, on);
-          cp_async16_zfill(base + C::kPlane + i * kStep * C::kPitch, on ? v : vb, on);
-          k += step;
-          v += step;
+          cp_async16_zfill(base + i * kStep * C::kPitch, on ? kp : kb, on);
+          cp_async16_zfill(base + C::kPlane + i * kStep * C::kPitch, on ? vp : vb, on);
+          kp += step;
+          vp += step;
         }
       }
-      kp += jump;
-      vp += jump;
       if constexpr (E4) {
-        const bool on = lane % kBlk < left;
-        cp_async4_zfill(ring + st * C::kStage + 2 * C::kPlane + lane * 4, on ? sp : kb, on);
-        sp += jump;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          const int w = i * 32 + lane;
+          const bool on = w % kBlk < left;
+          cp_async4_zfill(ring + st * C::kStage + 2 * C::kPlane + w * 4, on ? sp[i] : kb, on);
+          sp[i] += ts * kBlk;
+        }
       }
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) issue(warp + s * kRowWarps, s);
+  for (int s = 0; s < C::kStages - 1; ++s) issue(s, s);
 
-  // --- queries into shared memory; fp16 for an e4m3 cache: a row far outside
-  // fp16's range is brought into it by a power of two
+  // --- queries into the last ring slot; fp16 for an e4m3 cache: a row far
+  // outside fp16's range is brought into it by a power of two
   {
-    constexpr int QL = DP / 8, kRows = 32 / QL;  // lanes per row, rows per pass
-    constexpr int kPass = C::kM / (kRowWarps * kRows) > 0 ? C::kM / (kRowWarps * kRows) : 1;
+    constexpr int QL = DP / 8, kRows = 32 / QL, kPass = C::kM / kRows;  // lanes per row, rows per pass
     const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
     const int qc = lane % QL;
-    uint4 u[kPass];
+    constexpr int kBatch = kPass < 8 ? kPass : 8;
 #pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-      const int rr = (i * kRowWarps + warp) * kRows + lane / QL;
-      const bool use = __shfl_sync(FULL_MASK, my_use, rr & 31);
-      const long long off = __shfl_sync(FULL_MASK, my_q, rr & 31);
-      u[i] = make_uint4(0, 0, 0, 0);
-      if (rr < C::kM && use && qc * 8 < P.D) {
-        const unsigned short *q = static_cast<const unsigned short *>(P.q) + off + qc * 8;
-        if (vec) {
-          u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
-        } else {
-          u[i].x = q[0] | static_cast<uint32_t>(q[1]) << 16;
-          u[i].y = q[2] | static_cast<uint32_t>(q[3]) << 16;
-          u[i].z = q[4] | static_cast<uint32_t>(q[5]) << 16;
-          u[i].w = q[6] | static_cast<uint32_t>(q[7]) << 16;
+    for (int i0 = 0; i0 < kPass; i0 += kBatch) {
+      uint4 u[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int rr = (i0 + i) * kRows + lane / QL;
+        const bool use = __shfl_sync(FULL_MASK, my_use, rr);
+        const long long off = __shfl_sync(FULL_MASK, my_q, rr);
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (use && qc * 8 < P.D) {
+          const unsigned short *q = static_cast<const unsigned short *>(P.q) + off + qc * 8;
+          if (vec) {
+            u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
+          } else {
+            u[i].x = q[0] | static_cast<uint32_t>(q[1]) << 16;
+            u[i].y = q[2] | static_cast<uint32_t>(q[3]) << 16;
+            u[i].z = q[4] | static_cast<uint32_t>(q[5]) << 16;
+            u[i].w = q[6] | static_cast<uint32_t>(q[7]) << 16;
+          }
         }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-      const int rr = (i * kRowWarps + warp) * kRows + lane / QL;
-      float fac = 1.f;
-      if (E4 && P.qbf16) {
-        const float x[8] = {bf16_lo(u[i].x), bf16_hi(u[i].x), bf16_lo(u[i].y), bf16_hi(u[i].y),
-                            bf16_lo(u[i].z), bf16_hi(u[i].z), bf16_lo(u[i].w), bf16_hi(u[i].w)};
-        uint32_t a = 0;
+      for (int i = 0; i < kBatch; ++i) {
+        const int rr = (i0 + i) * kRows + lane / QL;
+        float fac = 1.f;
+        if (E4 && P.qbf16) {
+          const float x[8] = {bf16_lo(u[i].x), bf16_hi(u[i].x), bf16_lo(u[i].y), bf16_hi(u[i].y),
+                              bf16_lo(u[i].z), bf16_hi(u[i].z), bf16_lo(u[i].w), bf16_hi(u[i].w)};
+          uint32_t a = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
+          for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
 #pragma unroll
-        for (int o = QL / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
-        float by = 1.f;
-        const int e = static_cast<int>(a >> 23) - 127;
-        if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
-          const int up = max(-126, min(126, -e));
-          by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-          fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+          for (int o = QL / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
+          float by = 1.f;
+          const int e = static_cast<int>(a >> 23) - 127;
+          if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
+            const int up = max(-126, min(126, -e));
+            by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+            fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+          }
+          u[i] = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
+                            pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
         }
-        u[i] = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
-                          pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
-      }
-      if (rr < C::kM) {
         if (qc == 0) qfac[rr] = fac;
         *reinterpret_cast<uint4 *>(qsm + rr * C::kQPitch + qc * 16) = u[i];
       }
     }
   }
-  __syncthreads();
+  __syncwarp();
 
   // Fragments.  The contraction over d may run in any order as long as Q and
   // K agree: for codes a thread takes DP/4 consecutive d (a few 16-byte
@@ -292,15 +297,17 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
     }
   }
   scaled = __any_sync(FULL_MASK, scaled);
+  if (P.D < DP) {  // the slot's padding columns were queries
+    __syncwarp();
+    for (int i = lane; i < C::kStage / 16; i += 32) *reinterpret_cast<uint4 *>(qsm + i * 16) = make_uint4(0, 0, 0, 0);
+  }
+  __syncwarp();
   // each thread's rows, for the mask of the pass's own tokens
   int qtok[MT][2];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = r0 + mt * 16 + hf * 8 + quad;
-      qtok[mt][hf] = min(r / P.G, P.N - 1);
-    }
+    for (int hf = 0; hf < 2; ++hf) qtok[mt][hf] = min((r0 + mt * 16 + hf * 8 + quad) / P.G, P.N - 1);
 
   float o[MT][kNt][4];
   float mx[MT][2], l[MT][2];
@@ -317,23 +324,23 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
 
   bool odd = false;
   int st = 0;
-  for (int blkno = warp; blkno < nblk; blkno += kRowWarps) {
-    issue(blkno + (C::kStages - 1) * kRowWarps, (st + C::kStages - 1) % C::kStages);
+  for (int blkno = 0; blkno < nblk; ++blkno) {
+    issue(blkno + C::kStages - 1, st == 0 ? C::kStages - 1 : st - 1);
     cp_async_wait<C::kStages - 1>();
     __syncwarp();
-    const uint32_t kst = ring + st * C::kStage, vst = kst + C::kPlane;
+    const uint32_t kst = ring + st * C::kStage, vst = kst + C::kPlane, sst = kst + 2 * C::kPlane;
     const int tb = t0 + blkno * kBlk;
-    // --- scores: token nt * 8 + 2 j4 + {0, 1} of rows quad and quad + 8
-    float s4[MT][2][4];
+    // --- scores: token n * 8 + 2 j4 + {0, 1} of rows quad and quad + 8
+    float x[MT][kTt][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < kTt; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s4[mt][n][c] = 0.f;
+        for (int c = 0; c < 4; ++c) x[mt][n][c] = 0.f;
     if constexpr (E4) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < kTt; ++n) {
         const uint32_t at = kst + (n * 8 + quad) * C::kPitch + j4 * (DP / 4);
 #pragma unroll
         for (int s0 = 0; s0 < kSteps; s0 += 4) {
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
           for (int s = 0; s < 4; ++s) {
             const uint32_t b0 = e4m3x2_to_f16x2(w[s]), b1 = e4m3x2_to_f16x2_hi(w[s]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816<false>(s4[mt][n], qf[mt][s0 + s], b0, b1);
+            for (int mt = 0; mt < MT; ++mt) mma16816<false>(x[mt][n], qf[mt][s0 + s], b0, b1);
           }
         }
       }
@@ -354,70 +361,73 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
       // matrices: (tokens 0-7, d 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
       const uint32_t at = kst + ((lane / 16) * 8 + lane % 8) * C::kPitch + ((lane / 8) % 2) * 16;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        uint32_t kf[4];
-        ldmatrix_x4(kf, at + s * 32);
+      for (int n = 0; n < kTt; n += 2)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816<BF>(s4[mt][0], qf[mt][s], kf[0], kf[1]);
-          mma16816<BF>(s4[mt][1], qf[mt][s], kf[2], kf[3]);
+        for (int s = 0; s < kSteps; ++s) {
+          uint32_t kf[4];
+          ldmatrix_x4(kf, at + n * 8 * C::kPitch + s * 32);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816<BF>(x[mt][n], qf[mt][s], kf[0], kf[1]);
+            mma16816<BF>(x[mt][n + 1], qf[mt][s], kf[2], kf[3]);
+          }
         }
-      }
     }
     // --- to base-2 exponents of the weights
-    float a4[2][2], e4[2][2], inv[2][2], f4[2][2];
+    float ve[kTt][2], inv[kTt][2], rest[kTt][2];
     bool small = false;
     float dE = 0.f;
     if constexpr (E4) {
+      float ks[kTt][2];
       int top = -127;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < kTt; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int tk = n * 8 + 2 * j4 + c;
           uint32_t kw, vw;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(kst + 2 * C::kPlane + tk * 4) : "memory");
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(kst + 2 * C::kPlane + (kBlk + tk) * 4) : "memory");
-          a4[n][c] = P.scale * e4m3_scale(kw >> (8 * (g & 3)) & 255u);
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(sst + tk * 4) : "memory");
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(sst + (kBlk + tk) * 4) : "memory");
+          ks[n][c] = P.scale * e4m3_scale(kw >> (8 * (g & 3)) & 255u);
           const uint32_t vc = vw >> (8 * (g & 3)) & 255u;
-          e4[n][c] = scale_exponent(vc);
+          ve[n][c] = scale_exponent(vc);
           if (vc != 255u) top = max(top, static_cast<int>(vc) - 127);
         }
       const float En = fmaxf(E, static_cast<float>(__reduce_max_sync(FULL_MASK, top)));
       dE = En - E;
       E = En;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < kTt; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float e = e4[n][c];
-          e4[n][c] = e < E - kExponentSpan ? E - kExponentSpan : e;
-          f4[n][c] = e < E - kExponentSpan ? ex2(e - e4[n][c]) : 1.f;
+          const float e = ve[n][c];
+          ve[n][c] = e < E - kExponentSpan ? E - kExponentSpan : e;
+          rest[n][c] = e < E - kExponentSpan ? ex2(e - ve[n][c]) : 1.f;
           small = small || e < E - kExponentSpan;
-          inv[n][c] = ex2(E - e4[n][c]);
+          inv[n][c] = ex2(E - ve[n][c]);
         }
       small = __any_sync(FULL_MASK, small);
       if (scaled) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < kTt; ++n)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s4[mt][n][c] *= rf[mt][c >> 1];
+            for (int c = 0; c < 4; ++c) x[mt][n][c] *= rf[mt][c >> 1];
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < kTt; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s4[mt][n][c] = fmaf(s4[mt][n][c], a4[n][c & 1], e4[n][c & 1]);
+          for (int c = 0; c < 4; ++c) x[mt][n][c] = fmaf(x[mt][n][c], ks[n][c & 1], ve[n][c & 1]);
     } else {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < kTt; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s4[mt][n][c] *= P.scale;
+          for (int c = 0; c < 4; ++c) x[mt][n][c] *= P.scale;
     }
     // --- masks: the range's end, and the pass's own tokens
     const bool masked = tb + kBlk > t1 || (!pre && tb + kBlk > len0);
@@ -425,7 +435,7 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < kTt; ++n)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int t = tb + n * 8 + 2 * j4 + (c & 1);
@@ -435,26 +445,26 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
               const int qi = qtok[mt][c >> 1];
               see = P.anc ? (__ldg(P.anc + (static_cast<size_t>(b) * P.N + qi) * P.W + (jn >> 5)) >> (jn & 31)) & 1 : jn <= qi;
             }
-            if (!see) s4[mt][n][c] = -INFINITY;
+            if (!see) x[mt][n][c] = -INFINITY;
           }
     }
     // --- softmax.  A row's reference follows its maximum only when that has
     // grown by more than 2^kRowLazy (weights up to that are as exact).
-    uint32_t pf[MT][4];
-    float tm[MT][2], al[MT][2];
+    float tm[MT][2], al[MT][2], old[MT][2];
     bool grown = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        tm[mt][hf] = fmaxf(fmaxf(s4[mt][0][2 * hf], s4[mt][0][2 * hf + 1]), fmaxf(s4[mt][1][2 * hf], s4[mt][1][2 * hf + 1]));
-        grown = grown || tm[mt][hf] > mx[mt][hf] + kRowLazy || mx[mt][hf] == -INFINITY;
+        float t = fmaxf(x[mt][0][2 * hf], x[mt][0][2 * hf + 1]);
+#pragma unroll
+        for (int n = 1; n < kTt; ++n) t = fmaxf(t, fmaxf(x[mt][n][2 * hf], x[mt][n][2 * hf + 1]));
+        tm[mt][hf] = t;
+        old[mt][hf] = mx[mt][hf];
         al[mt][hf] = 1.f;
+        grown = grown || t > mx[mt][hf] + kRowLazy || mx[mt][hf] == -INFINITY;
       }
     const bool moved = __any_sync(FULL_MASK, grown);
-    float old[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) old[mt][0] = mx[mt][0], old[mt][1] = mx[mt][1];
     if (moved) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -468,51 +478,6 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
             mx[mt][hf] = t;
           }
         }
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float ref = mx[mt][hf] == -INFINITY ? 0.f : mx[mt][hf];
-        float add = 0.f;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float &x = s4[mt][n][2 * hf + c];
-            x = ex2(x - ref);
-            if constexpr (E4) {
-              // 0 * NaN: a token that is not seen adds nothing, whatever its scale
-              add += x == 0.f ? 0.f : x * inv[n][c];
-            } else {
-              add += x;
-            }
-          }
-        // old = -inf: nothing was summed yet
-        const float ll = E4 && dE != 0.f ? (old[mt][hf] == -INFINITY ? 0.f : ex2(old[mt][hf] - ref + dE)) : al[mt][hf];
-        l[mt][hf] = fmaf(l[mt][hf], ll, add);
-      }
-    if constexpr (E4) {
-      if (small) {  // the rest of the factor of scales that far below the largest
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              s4[mt][n][c] *= f4[n][c];
-              s4[mt][n][2 + c] *= f4[n][c];
-            }
-      }
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      pf[mt][0] = pack16<BF>(s4[mt][0][0], s4[mt][0][1]);
-      pf[mt][1] = pack16<BF>(s4[mt][0][2], s4[mt][0][3]);
-      pf[mt][2] = pack16<BF>(s4[mt][1][0], s4[mt][1][1]);
-      pf[mt][3] = pack16<BF>(s4[mt][1][2], s4[mt][1][3]);
-    }
-    if (moved) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -523,6 +488,48 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
           o[mt][n][3] *= al[mt][1];
         }
     }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float ref = mx[mt][hf] == -INFINITY ? 0.f : mx[mt][hf];
+        float add = 0.f;
+#pragma unroll
+        for (int n = 0; n < kTt; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float &y = x[mt][n][2 * hf + c];
+            y = ex2(y - ref);
+            // 0 * NaN: a token that is not seen adds nothing, whatever its scale
+            if constexpr (E4)
+              add += y == 0.f ? 0.f : y * inv[n][c];
+            else
+              add += y;
+          }
+        // old = -inf: nothing was summed yet
+        const float ll = E4 && dE != 0.f ? (old[mt][hf] == -INFINITY ? 0.f : ex2(old[mt][hf] - ref + dE)) : al[mt][hf];
+        l[mt][hf] = fmaf(l[mt][hf], ll, add);
+      }
+    if constexpr (E4) {
+      if (small) {  // the rest of the factor of scales that far below the largest
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < kTt; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[mt][n][c] *= rest[n][c & 1];
+      }
+    }
+    uint32_t pf[MT][kTs][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int s = 0; s < kTs; ++s) {
+        pf[mt][s][0] = pack16<BF>(x[mt][2 * s][0], x[mt][2 * s][1]);
+        pf[mt][s][1] = pack16<BF>(x[mt][2 * s][2], x[mt][2 * s][3]);
+        pf[mt][s][2] = pack16<BF>(x[mt][2 * s + 1][0], x[mt][2 * s + 1][1]);
+        pf[mt][s][3] = pack16<BF>(x[mt][2 * s + 1][2], x[mt][2 * s + 1][3]);
+      }
     // --- values of the pass's own tokens that are not finite: a query that
     // does not see them would get 0 * NaN.  They are taken out here and put
     // into the answers of the queries that see them when the parts are joined.
@@ -557,117 +564,87 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const __grid_con
     if constexpr (E4) {
       // tokens 2 j4, 2 j4 + 1, 8 + 2 j4, 9 + 2 j4 of columns quad * kNt + n
 #pragma unroll
-      for (int n0 = 0; n0 < kNt; n0 += 8) {
-        uint32_t w[4][2];
+      for (int s = 0; s < kTs; ++s)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                       : "=r"(w[t][0]), "=r"(w[t][1])
-                       : "r"(vst + ((t / 2) * 8 + 2 * j4 + t % 2) * C::kPitch + quad * kNt + n0)
-                       : "memory");
+        for (int n0 = 0; n0 < kNt; n0 += 8) {
+          uint32_t w[4][2];
 #pragma unroll
-        for (int n = 0; n < 8; n += 2) {
-          // bytes n, n + 1 of two tokens: (t0 n, t1 n, t0 n+1, t1 n+1)
-          const uint32_t sel = n % 4 == 0 ? 0x5140u : 0x7362u;
-          const uint32_t lo = __byte_perm(w[0][n / 4], w[1][n / 4], sel);
-          const uint32_t hi = __byte_perm(w[2][n / 4], w[3][n / 4], sel);
-          const uint32_t b0 = e4m3x2_to_f16x2(lo), b1 = e4m3x2_to_f16x2(hi);
-          const uint32_t c0 = e4m3x2_to_f16x2_hi(lo), c1 = e4m3x2_to_f16x2_hi(hi);
+          for (int t = 0; t < 4; ++t)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(w[t][0]), "=r"(w[t][1])
+                         : "r"(vst + (s * 16 + (t / 2) * 8 + 2 * j4 + t % 2) * C::kPitch + quad * kNt + n0)
+                         : "memory");
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816<false>(o[mt][n0 + n], pf[mt], b0, b1);
-            mma16816<false>(o[mt][n0 + n + 1], pf[mt], c0, c1);
+          for (int n = 0; n < 8; n += 2) {
+            // bytes n, n + 1 of two tokens: (t0 n, t1 n, t0 n+1, t1 n+1)
+            const uint32_t sel = n % 4 == 0 ? 0x5140u : 0x7362u;
+            const uint32_t lo = __byte_perm(w[0][n / 4], w[1][n / 4], sel);
+            const uint32_t hi = __byte_perm(w[2][n / 4], w[3][n / 4], sel);
+            const uint32_t b0 = e4m3x2_to_f16x2(lo), b1 = e4m3x2_to_f16x2(hi);
+            const uint32_t c0 = e4m3x2_to_f16x2_hi(lo), c1 = e4m3x2_to_f16x2_hi(hi);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16816<false>(o[mt][n0 + n], pf[mt][s], b0, b1);
+              mma16816<false>(o[mt][n0 + n + 1], pf[mt][s], c0, c1);
+            }
           }
         }
-      }
     } else {
       // matrices: (tokens 0-7, d 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
       const uint32_t at = vst + (lane % 16) * C::kPitch + (lane / 16) * 16;
 #pragma unroll
-      for (int n = 0; n < kNt; n += 2) {
-        uint32_t vf[4];
-        ldmatrix_x4_trans(vf, at + n * 16);
+      for (int s = 0; s < kTs; ++s)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816<BF>(o[mt][n], pf[mt], vf[0], vf[1]);
-          mma16816<BF>(o[mt][n + 1], pf[mt], vf[2], vf[3]);
+        for (int n = 0; n < kNt; n += 2) {
+          uint32_t vf[4];
+          ldmatrix_x4_trans(vf, at + s * 16 * C::kPitch + n * 16);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816<BF>(o[mt][n], pf[mt][s], vf[0], vf[1]);
+            mma16816<BF>(o[mt][n + 1], pf[mt][s], vf[2], vf[3]);
+          }
         }
-      }
     }
     __syncwarp();
-    st = (st + 1) % C::kStages;
+    st = st == C::kStages - 1 ? 0 : st + 1;
   }
-
-  // --- join the warps: everyone leaves its sums in the ring's memory
   cp_async_wait_all();
-  odd = __syncthreads_or(odd);
-  if (!pre && tid == 0) P.oflag[blockIdx.x - pitems] = odd;
-  float *const om = reinterpret_cast<float *>(smem);                  // [warp][row][kOPitch]
-  float *const mm = om + kRowWarps * C::kM * C::kOPitch;                      // [warp][row]
-  float *const lm = mm + kRowWarps * C::kM;
-  // where a row keeps column d: for codes, groups of four rotated by the lane that held them
-  auto own_col = [](int d) {
-    if constexpr (!E4) return d;
-    const int run = d / kNt, i = d % kNt / 4;
-    return run * kNt + 4 * ((i + run / 2) & (kNt / 4 - 1)) + d % 4;
-  };
+
+  if (!pre && lane == 0) P.oflag[blockIdx.x - pitems] = odd;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const int rr = mt * 16 + hf * 8 + quad;
+      const int orow = __shfl_sync(FULL_MASK, my_row, rr);
+      const bool use = __shfl_sync(FULL_MASK, my_use, rr);
       float t = l[mt][hf];
       t += __shfl_xor_sync(FULL_MASK, t, 1);
       t += __shfl_xor_sync(FULL_MASK, t, 2);
-      if (j4 == 0) {
-        mm[warp * C::kM + rr] = mx[mt][hf];
-        lm[warp * C::kM + rr] = t == 0.f ? -INFINITY : mx[mt][hf] + log2f(t) - (E4 ? E : 0.f);
-      }
-      float *const to = om + (warp * C::kM + rr) * C::kOPitch;
+      if (orow < 0) continue;
+      const bool some = use && t != 0.f;
+      const long long at = static_cast<long long>(slot) * P.rows + orow;
+      if (j4 == 0)
+        P.ml[at] = some ? make_float2(mx[mt][hf], mx[mt][hf] + log2f(t) - (E4 ? E : 0.f)) : make_float2(-INFINITY, -INFINITY);
+      if (!some) continue;
+      float *const to = P.part + at * P.D;
       if constexpr (E4) {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i < kNt / 4; ++i)  // see own_col: the four j4 lie a whole round of banks apart
-            *reinterpret_cast<float4 *>(to + (2 * j4 + c) * kNt + 4 * ((i + j4) & (kNt / 4 - 1))) =
-                make_float4(o[mt][4 * i][2 * hf + c], o[mt][4 * i + 1][2 * hf + c], o[mt][4 * i + 2][2 * hf + c], o[mt][4 * i + 3][2 * hf + c]);
+          for (int n = 0; n < kNt; n += 8) {
+            if ((2 * j4 + c) * kNt + n >= P.D) continue;
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(o[mt][n + e][2 * hf + c]);
+            st_global_v8(to + (2 * j4 + c) * kNt + n, y);
+          }
       } else {
 #pragma unroll
         for (int n = 0; n < kNt; ++n)
-          *reinterpret_cast<float2 *>(to + n * 8 + 2 * j4) = make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
+          if (n * 8 < P.D) *reinterpret_cast<float2 *>(to + n * 8 + 2 * j4) = make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
       }
     }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < C::kM / kRowWarps; ++i) {
-    const int rr = i * kRowWarps + warp;
-    const int orow = __shfl_sync(FULL_MASK, my_row, rr);
-    const bool on = __shfl_sync(FULL_MASK, my_use, rr);
-    if (orow < 0) continue;
-    float M = -INFINITY, Z = -INFINITY, S = 0.f, w[kRowWarps];
-#pragma unroll
-    for (int k = 0; k < kRowWarps; ++k) {
-      M = fmaxf(M, mm[k * C::kM + rr]);
-      Z = fmaxf(Z, lm[k * C::kM + rr]);
-    }
-    const float ref = M == -INFINITY ? 0.f : M, zref = Z == -INFINITY ? 0.f : Z;
-#pragma unroll
-    for (int k = 0; k < kRowWarps; ++k) {
-      w[k] = ex2(mm[k * C::kM + rr] - ref);
-      S += ex2(lm[k * C::kM + rr] - zref);
-    }
-    const bool some = on && S != 0.f;
-    if (lane == 0)
-      P.ml[static_cast<long long>(slot) * P.rows + orow] = some ? make_float2(M, zref + log2f(S)) : make_float2(-INFINITY, -INFINITY);
-    if (!some) continue;
-    float *to = P.part + (static_cast<long long>(slot) * P.rows + orow) * P.D;
-    for (int d = lane; d < P.D; d += 32) {
-      float x = 0.f;
-#pragma unroll
-      for (int k = 0; k < kRowWarps; ++k) x = fmaf(w[k], om[(k * C::kM + rr) * C::kOPitch + own_col(d)], x);
-      to[d] = x;
-    }
-  }
 }
 
 // ------------------------------------------------------------------- join
@@ -784,7 +761,7 @@ cudaError_t launch_rows(const AttnParams &p, bool own, bool prefix, cudaStream_t
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<attn_rows_kernel<CT, DP, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  attn_rows_kernel<CT, DP, MT><<<static_cast<unsigned>(items), kRowThreads, C::kSmem, s>>>(p, static_cast<int>(pitems), pblocks, oblocks);
+  attn_rows_kernel<CT, DP, MT><<<static_cast<unsigned>(items), 32, C::kSmem, s>>>(p, static_cast<int>(pitems), pblocks, oblocks);
   return cudaGetLastError();
 }
 
@@ -844,9 +821,9 @@ AttnPlan plan_attention(const spec_attention_args *a) {
   // more than 32 query rows per KV head would read the keys again for each 32
   p.ptile = q * G > 32;
   p.otile = a->N * G > 32;
-  // rows kernel: enough items for two per SM, no part under 64 tokens
+  // rows kernel: 12 items per SM, no part under 64 tokens
   auto row_parts = [](long long blocks, long long tokens) {
-    const long long want = (2 * kSms + blocks - 1) / blocks;
+    const long long want = (12 * kSms + blocks - 1) / blocks;
     return static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 64})));
   };
   // tile kernel (one item per SM at a time): the fewest rounds of items times
@@ -873,12 +850,10 @@ AttnPlan plan_attention(const spec_attention_args *a) {
   const long long oitems = c.rows * c.heads * oblocks;
   p.osplits = p.otile ? tile_parts(oitems, c.slots) : row_parts(oitems, c.slots);
   p.min_chunk = p.otile ? 128 : 64;
-  if (!p.otile && p.osplits == 1) {
-    // enough items as they are, but rows differ in length: parts of 256
-    // tokens keep a long row from holding up the rest, up to 16 items per SM
-    // (most of them empty if the rows are short).  64 rows of 100 to 2000
-    // tokens: 54 us as whole rows, 37 us in parts.
-    p.osplits = static_cast<int>(std::max<long long>(1, std::min<long long>((c.slots + 255) / 256, 16 * kSms / oitems)));
+  if (!p.otile && oitems >= 2 * kSms) {
+    // rows differ in length: parts of 256 tokens keep a long row from holding
+    // up the rest, up to 24 items per SM (most of them empty if rows are short)
+    p.osplits = static_cast<int>(std::max<long long>(1, std::min<long long>((c.slots + 255) / 256, 24 * kSms / oitems)));
     p.min_chunk = 256;
   }
   p.W = (a->N + 31) / 32;

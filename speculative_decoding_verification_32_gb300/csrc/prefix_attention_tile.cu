@@ -171,12 +171,6 @@ __device__ __forceinline__ bool wait_for(Ctrl *c, uint64_t *bar, uint32_t parity
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
-__device__ __forceinline__ void st_global_v8(float *p, const uint32_t *r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // Item: prefix (PRE): KV head, block of 256 rows of all rows' queries, part;
 // own: row, KV head, block of 256 of the row's queries, part.
 template <int CT, int DP, bool PRE>
