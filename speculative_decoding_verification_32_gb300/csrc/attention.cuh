@@ -54,6 +54,8 @@ struct AttnParams {
   float *lse;
   int32_t *row_status;
   int qbf16;
+  int fuse;    // own items of the tile kernel take the prefix too
+  int direct;  // ... and write the answers themselves: there is nothing to join
   uint64_t wait_limit_ns;
   int force_timeout;
 };
@@ -151,6 +153,19 @@ __device__ __forceinline__ float scale_exponent(uint32_t c) {
 // span and takes the rest of the factor on its weight.
 constexpr float kMinExponent = -60.f;
 constexpr float kExponentSpan = 60.f;
+constexpr float kLn2 = 0.693147180559945309f;
+
+// A value of row b's own entry in slot t if it is not finite, else 0.
+template <int CT>
+__device__ __forceinline__ float odd_value(const AttnParams &P, int b, int t, int g, int d) {
+  const unsigned char *const e = P.v + b * P.row_stride + t * P.tok_stride;
+  float val;
+  if constexpr (CT == SPEC_E4M3)
+    val = e[P.H * P.D + g] == 255 || (e[g * P.D + d] & 127) == 127 ? __uint_as_float(0x7fc00000u) : 0.f;
+  else
+    val = static_cast<float>(reinterpret_cast<const typename CacheType<CT>::type *>(e)[g * P.D + d]);
+  return isfinite(val) ? 0.f : val;
+}
 
 // 32 bytes, a whole sector, aligned to 32
 __device__ __forceinline__ void st_global_v8(float *p, const uint32_t *r) {

@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(32) attn_rows_kernel(const __grid_constant__ A
 
 // ------------------------------------------------------------------- join
 // One warp per output row: the weights of the parts, then their sum.
-template <bool BF, bool E4>
+template <int CT, bool BF>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams P) {
   const int lane = threadIdx.x % 32;
   const long long r = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
@@ -727,27 +727,16 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
       for (int j = 0; j < n; ++j) {
         const bool see = P.anc ? P.anc[(static_cast<size_t>(b) * P.N + qt) * P.W + (j >> 5)] >> (j & 31) & 1u : j <= qt;
         if (!see) continue;
-        const unsigned char *const e = P.v + b * P.row_stride + static_cast<long long>(len0 + j) * P.tok_stride;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int d = lane * 4 + i;
-          if (d >= P.D) break;
-          float val;
-          if constexpr (E4)
-            val = e[P.H * P.D + g] == 255 || (e[g * P.D + d] & 127) == 127 ? __uint_as_float(0x7fc00000u) : 0.f;
-          else if (BF)
-            val = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(e)[g * P.D + d]);
-          else
-            val = __half2float(reinterpret_cast<const __half *>(e)[g * P.D + d]);
-          if (!isfinite(val)) acc[i] += val;
-        }
+        for (int i = 0; i < 4; ++i)
+          if (lane * 4 + i < P.D) acc[i] += odd_value<CT>(P, b, len0 + j, g, lane * 4 + i);
       }
     }
   }
   if (lane * 4 < P.D)
     *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(P.out) + r * P.D + lane * 4) =
         make_uint2(pack16<BF>(acc[0], acc[1]), pack16<BF>(acc[2], acc[3]));
-  if (lane == 0 && P.lse) P.lse[r] = 0.693147180559945309f * z;
+  if (lane == 0 && P.lse) P.lse[r] = kLn2 * z;
 }
 
 // -------------------------------------------------------------------- host
@@ -779,6 +768,7 @@ cudaError_t launch_rows_d(const AttnParams &p, bool own, bool prefix, cudaStream
 struct AttnPlan {
   int psplits, pchunk, osplits, min_chunk, W;
   bool ptile, otile;  // attn_tile_kernel for the prefix, for the own entries
+  bool fuse, direct;  // own items take the prefix too; and nothing is left to join
   int oblk;           // query rows per own item
   size_t rows, anc_at, info_at, flag_at, ml_at, part_at, bytes;
 };
@@ -838,7 +828,12 @@ AttnPlan plan_attention(const spec_attention_args *a) {
     }
     return parts;
   };
-  if (a->prefix_len > 0) {
+  // A tree's queries that nearly fill the row tiles take the prefix in the same
+  // item as the row's own entries: queries are read once and, uncut, nothing
+  // has to be joined.  Rows packed across the batch would save the padding only.
+  const long long rows1 = a->N * G, padded = (rows1 + 127) / 128 * 128;
+  p.fuse = p.otile && a->prefix_len > 0 && 4 * rows1 >= 3 * padded;
+  if (a->prefix_len > 0 && !p.fuse) {
     p.psplits = p.ptile ? tile_parts(c.heads * ((q * G + 255) / 256), a->prefix_len)
                         : row_parts(c.heads * ((q * G + 31) / 32), a->prefix_len);
     const int unit = p.ptile ? 128 : 64;
@@ -848,7 +843,7 @@ AttnPlan plan_attention(const spec_attention_args *a) {
   p.oblk = p.otile ? 256 : two_row_tiles(c.rows, a->N, static_cast<int>(G), a->prefix_len > 0 && !p.ptile) ? 32 : 16;
   const long long oblocks = (a->N * G + p.oblk - 1) / p.oblk;
   const long long oitems = c.rows * c.heads * oblocks;
-  p.osplits = p.otile ? tile_parts(oitems, c.slots) : row_parts(oitems, c.slots);
+  p.osplits = p.otile ? tile_parts(oitems, c.slots + (p.fuse ? a->prefix_len : 0)) : row_parts(oitems, c.slots);
   p.min_chunk = p.otile ? 128 : 64;
   if (!p.otile && oitems >= 2 * kSms) {
     // rows differ in length: parts of 256 tokens keep a long row from holding
@@ -856,6 +851,7 @@ AttnPlan plan_attention(const spec_attention_args *a) {
     p.osplits = static_cast<int>(std::max<long long>(1, std::min<long long>((c.slots + 255) / 256, 24 * kSms / oitems)));
     p.min_chunk = 256;
   }
+  p.direct = p.otile && p.osplits == 1 && p.psplits == 0;
   p.W = (a->N + 31) / 32;
   size_t at = 0;
   p.anc_at = at;
@@ -945,6 +941,7 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   p.chunk = plan.otile ? 128 : 64;
   p.min_chunk = plan.min_chunk;
   p.oblk = plan.oblk;
+  p.fuse = plan.fuse;
   p.oflag = reinterpret_cast<int32_t *>(w + plan.flag_at);
   p.out = out;
   p.lse = lse;
@@ -962,8 +959,13 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
     p.rowinfo = info;
   }
   const bool prefix = p.P > 0;
-  if (prefix && plan.ptile && launch_attn_tile(p, c.dtype, true, s) != cudaSuccess) return SPEC_ERR_CUDA;
-  if (plan.otile && launch_attn_tile(p, c.dtype, false, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (prefix && plan.ptile && !plan.fuse && launch_attn_tile(p, c.dtype, true, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (plan.otile) {
+    p.direct = plan.direct;
+    if (launch_attn_tile(p, c.dtype, false, s) != cudaSuccess) return SPEC_ERR_CUDA;
+    if (plan.direct) return SPEC_OK;
+    p.direct = 0;
+  }
   if ((!plan.otile || (prefix && !plan.ptile)) &&
       launch_attn_rows(p, c.dtype, !plan.otile, prefix && !plan.ptile, s) != cudaSuccess)
     return SPEC_ERR_CUDA;
@@ -976,11 +978,15 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const bool e4 = c.dtype == SPEC_E4M3;
-  const cudaError_t e = p.qbf16 ? (e4 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true, true>, p)
-                                      : cudaLaunchKernelEx(&cfg, attn_join_kernel<true, false>, p))
-                                : (e4 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<false, true>, p)
-                                      : cudaLaunchKernelEx(&cfg, attn_join_kernel<false, false>, p));
+  cudaError_t e;
+  if (c.dtype == SPEC_BF16)
+    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<SPEC_BF16, true>, p);
+  else if (c.dtype == SPEC_F16)
+    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<SPEC_F16, false>, p);
+  else if (p.qbf16)
+    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<SPEC_E4M3, true>, p);
+  else
+    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<SPEC_E4M3, false>, p);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

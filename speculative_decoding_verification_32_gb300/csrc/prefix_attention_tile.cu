@@ -60,7 +60,7 @@ struct TileCfg {
 
 struct Ctrl {
   uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
-  uint64_t sfull[2], pfull[2], done[2], drain;
+  uint64_t sfull[2], pfull[2], done[2], qfull, drain;
   uint32_t tmem;
   int abort;
   int odd;
@@ -171,8 +171,10 @@ __device__ __forceinline__ bool wait_for(Ctrl *c, uint64_t *bar, uint32_t parity
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
-// Item: prefix (PRE): KV head, block of 256 rows of all rows' queries, part;
-// own: row, KV head, block of 256 of the row's queries, part.
+// Items.  PRE: the prefix alone, for (KV head, block of 256 rows of all rows'
+// queries, part).  Else (row, KV head, block of 256 of the row's queries,
+// part) against the row's own entries, after the prefix's if P.fuse; with one
+// part and nothing else to join (P.direct) it writes the answer itself.
 template <int CT, int DP, bool PRE>
 __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid_constant__ AttnParams P, int blocks) {
   using C = TileCfg<DP>;
@@ -194,44 +196,40 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   const int r0 = blk * 256;
   const int nrows = (PRE ? P.B : 1) * P.N * P.G;
   const int slot = PRE ? split : P.psplits + split;
-  int t0, t1, len0 = 0x7fffffff, cnt = 0;
+  // blocks of tokens: the prefix's npre first, then the row's own; this part
+  // takes n of them from block q0 on
+  int npre = PRE || P.fuse ? (P.P + kTok - 1) / kTok : 0;
+  int q0, n, len0 = 0, len = 0, cnt = 0;
   if constexpr (PRE) {
-    t0 = split * P.pchunk;
-    t1 = min(P.P, t0 + P.pchunk);
+    q0 = split * (P.pchunk / kTok);
+    n = min(P.pchunk / kTok, npre - q0);
   } else {
     cnt = row_queries(P, b);
     len0 = __ldg(P.kv_len + b);
+    len = len0 + cnt;
     if (split == 0 && blk == 0 && g == 0 && tid == 0 && P.row_status)
       P.row_status[b] = cnt >= 0 ? 0 : cnt == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
-    if (cnt <= 0)
-      t0 = t1 = 0;
-    else
-      own_range(P, len0 + cnt, split, t0, t1);
+    const int all = cnt > 0 ? npre + (len + kTok - 1) / kTok : 0, per = (all + nsplit - 1) / nsplit;
+    q0 = split * per;
+    n = max(0, min(per, all - q0));
   }
-  const unsigned char *const kb = PRE ? P.pk : P.k + b * P.row_stride;
-  const unsigned char *const vb = PRE ? P.pv : P.v + b * P.row_stride;
-  const long long ts = PRE ? P.ptok_stride : P.tok_stride;
-  const int n = (t1 - t0 + kTok - 1) / kTok;        // blocks of tokens
   const int tiles = nrows - r0 > 128 ? 2 : 1;       // row tiles in use
-  if (tid < 256) {
-    const int r = r0 + tid;
-    int at = -1;
-    if (r < nrows) {
-      const int t = r / P.G, h = g * P.G + (r - t * P.G);
-      const int qb = PRE ? t / P.N : b, qt = PRE ? t - qb * P.N : t;
-      at = (qb * P.N + qt) * P.Hq + h;
-      c->qoff[tid] = qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2];
-      if (n == 0) P.ml[static_cast<long long>(slot) * P.rows + at] = make_float2(-INFINITY, -INFINITY);
-      if (qt >= (PRE ? row_queries(P, qb) : cnt)) at |= kUnused;
-    }
-    c->orow[tid] = at;
-  }
   if (n == 0) {  // nothing here (an empty part, or a row that cannot be used)
+    if (tid < 256 && r0 + tid < nrows) {
+      const int t = (r0 + tid) / P.G;
+      const long long at = static_cast<long long>((PRE ? 0 : b) * P.N + t) * P.Hq + g * P.G + (r0 + tid - t * P.G);
+      if (P.direct) {
+        for (int d = 0; d < P.D; d += 8) *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(P.out) + at * P.D + d) = make_uint4(0, 0, 0, 0);
+        if (P.lse) P.lse[at] = -INFINITY;
+      } else {
+        P.ml[static_cast<long long>(slot) * P.rows + at] = make_float2(-INFINITY, -INFINITY);
+      }
+    }
     if (!PRE && tid == 0) P.oflag[blockIdx.x] = 0;
     return;
   }
 
-  // --- set up: barriers, tensor memory, queries
+  // --- set up: barriers and tensor memory
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->kfull[i], kProducers);
@@ -242,65 +240,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       mbar_init(&c->pfull[i], 128);
       mbar_init(&c->done[i], 1);
     }
+    mbar_init(&c->qfull, 256);
     mbar_init(&c->drain, 1);
     c->abort = 0;
     c->odd = 0;
     fence_mbar_init();
   }
   if (warp == 12) tc_alloc(&c->tmem);
-  __syncthreads();
-  {
-    // DP/8 lanes per row, 16 bytes of the operand each; fp16 for an e4m3
-    // cache: a row far outside fp16's range is brought into it by a power of
-    // two.  A negative scale turns the queries' sign.
-    constexpr int L = DP / 8, kIt = 256 * L / kTileThreads, kStep = kTileThreads / L;
-    const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
-    const int pc = tid % L, rr0 = tid / L;
-    uint4 u[kIt];
-#pragma unroll
-    for (int i = 0; i < kIt; ++i) {
-      const int rr = rr0 + i * kStep, at = c->orow[rr];
-      u[i] = make_uint4(0, 0, 0, 0);
-      if (at >= 0 && at < kUnused && pc * 8 < P.D) {
-        const unsigned short *q = static_cast<const unsigned short *>(P.q) + c->qoff[rr] + pc * 8;
-        if (vec) {
-          u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
-        } else {
-          u[i].x = q[0] | static_cast<uint32_t>(q[1]) << 16;
-          u[i].y = q[2] | static_cast<uint32_t>(q[3]) << 16;
-          u[i].z = q[4] | static_cast<uint32_t>(q[5]) << 16;
-          u[i].w = q[6] | static_cast<uint32_t>(q[7]) << 16;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kIt; ++i) {
-      const int rr = rr0 + i * kStep;
-      float fac = 1.f;
-      if (E4 && P.qbf16) {
-        const float x[8] = {bf16_lo(u[i].x), bf16_hi(u[i].x), bf16_lo(u[i].y), bf16_hi(u[i].y),
-                            bf16_lo(u[i].z), bf16_hi(u[i].z), bf16_lo(u[i].w), bf16_hi(u[i].w)};
-        uint32_t a = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
-        float by = 1.f;
-        const int e = static_cast<int>(a >> 23) - 127;
-        if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
-          const int up = max(-126, min(126, -e));
-          by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-          fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-        }
-        u[i] = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
-                          pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
-      }
-      if (pc == 0) c->qfac[rr] = fac;
-      if (P.scale < 0.f) u[i].x ^= 0x80008000u, u[i].y ^= 0x80008000u, u[i].z ^= 0x80008000u, u[i].w ^= 0x80008000u;
-      *reinterpret_cast<uint4 *>(smem + C::kQ + (rr / 128) * C::kOp + (pc / 8) * 16384 + (rr % 128) * 128 + (((pc % 8) ^ (rr & 7)) << 4)) = u[i];
-    }
-  }
-  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -312,192 +258,162 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4>::kProduce));
     const int pt = tid - 256;
     bool live = true;
-    if constexpr (!E4) {
-      constexpr int L = DP / 8, kPer = L;  // 16-byte pieces per row; pieces per thread and operand tile
-      constexpr int kStep = kProducers / L;
-      const int pc = pt % L, row0 = pt / L;
-      const bool col = pc * 8 < P.D;
-      const uint32_t dst0 = smem_u32(smem) + (pc / 8) * 16384 + row0 * 128 + (((pc % 8) ^ (row0 & 7)) << 4);
-      const long long src0 = static_cast<long long>(g) * P.D * 2 + (col ? pc * 16 : 0);
-      const unsigned char *kp = kb + src0 + (static_cast<long long>(t0) + row0) * ts;  // this thread's next block
-      const unsigned char *vp = vb + src0 + (static_cast<long long>(t0) + row0) * ts;
-      const long long step = ts * kStep;
-      // item 2k: keys of block k, item 2k + 1: its values
-      auto issue = [&](int it) {
-        if (it < 2 * n && live) {
-          const int k = it >> 1, s = k & 1;
-          uint64_t *const fr = it & 1 ? &c->vfree[s] : &c->kfree[s];
-          if (k >= 2) live = wait_for(c, fr, ((k >> 1) - 1) & 1, limit);
-          if (live) {
-            const unsigned char *src = it & 1 ? vp : kp;
-            const uint32_t dst = dst0 + (it & 1 ? C::kV : C::kK) + s * C::kOp;
-            const int left = t1 - (t0 + k * kTok) - row0;  // tokens from this thread's first row on
-            if (col && left > (kPer - 1) * kStep) {
-#pragma unroll
-              for (int i = 0; i < kPer; ++i) {
-                cp_async16_zfill(dst + i * kStep * 128, src, true);
-                src += step;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < kPer; ++i) {
-                const bool on = col && i * kStep < left;
-                cp_async16_zfill(dst + i * kStep * 128, on ? src : kb, on);
-                src += step;
-              }
-            }
-            if (it & 1)
-              vp = src;
-            else
-              kp = src;
-          }
-        }
-        cp_async_commit();
-      };
-      issue(0);
-      issue(1);
-      for (int it = 0; it < 2 * n; ++it) {
-        issue(it + 2);
-        cp_async_wait<2>();
-        const int k = it >> 1, s = k & 1;
-        if (!PRE && (it & 1) && live) {
-          // values of the pass's own tokens that are not finite: a query that
-          // does not see them would get 0 * NaN.  They are taken out here and
-          // put into the answers of the queries that see them when the parts
-          // are joined.
-          const int tb = t0 + k * kTok;
-          if (tb + kTok > len0) {
+    // A thread brings 16-byte pieces of every kStep-th token.  Item 2k: keys
+    // of block k, item 2k + 1: its values.  16-bit entries go where the tensor
+    // cores want them; codes land in the same buffer as they are and are turned
+    // into fp16 there once they have arrived.
+    constexpr int L = E4 ? DP / 16 : DP / 8, kPer = L, kStep = kProducers / L;
+    const int pc = pt % L, row0 = pt / L;
+    const bool col = pc * 16 < P.D * (E4 ? 1 : 2);
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t put0 = E4 ? pt * 16 : (pc / 8) * 16384 + row0 * 128 + (((pc % 8) ^ (row0 & 7)) << 4);
+    constexpr int kPut = E4 ? kProducers * 16 : kStep * 128;
+    const long long src0 = static_cast<long long>(g) * P.D * (E4 ? 1 : 2) + (col ? pc * 16 : 0);
+    const unsigned char *const ok = P.k + b * P.row_stride, *const ov = P.v + b * P.row_stride;
+    // copies of item it; for codes, the scale byte of the block's token pt
+    auto issue = [&](int it) -> uint32_t {
+      uint32_t byte = 0;
+      if (it < 2 * n) {
+        const int k = it >> 1, s = k & 1, q = q0 + k;
+        const bool pre = PRE || q < npre, val = it & 1;
+        const int tb = (pre ? q : q - npre) * kTok, left = (pre ? P.P : len) - tb;
+        const long long ts = pre ? P.ptok_stride : P.tok_stride;
+        const unsigned char *const base = (pre ? (val ? P.pv : P.pk) : (val ? ov : ok)) + tb * ts;
+        if constexpr (E4)
+          if (pt < left) byte = __ldg(base + pt * ts + static_cast<long long>(P.H) * P.D + g);
+        if (k >= 2 && live) live = wait_for(c, val ? &c->vfree[s] : &c->kfree[s], ((k >> 1) - 1) & 1, limit);
+        if (live) {
+          const unsigned char *src = base + src0 + row0 * ts;
+          const uint32_t dst = sbase + put0 + (val ? C::kV : C::kK) + s * C::kOp;
+          const long long step = ts * kStep;
+          if (col && row0 + (kPer - 1) * kStep < left) {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-              const int t = tb + row0 + i * kStep;
-              if (t < len0 || t >= t1) continue;
-              const uint32_t at = dst0 + C::kV + s * C::kOp + i * kStep * 128;
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
-              bool odd = false;
+              cp_async16_zfill(dst + i * kPut, src, true);
+              src += step;
+            }
+          } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
-                if ((w[e] & top) == top) w[e] &= 0xffff0000u, odd = true;
-                if ((w[e] >> 16 & top) == top) w[e] &= 0x0000ffffu, odd = true;
-              }
-              if (odd) {
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-                c->odd = 1;
-              }
+            for (int i = 0; i < kPer; ++i) {
+              const bool on = col && row0 + i * kStep < left;
+              cp_async16_zfill(dst + i * kPut, on ? src : base, on);
+              src += step;
             }
           }
         }
-        fence_async_smem();
-        if (!(P.force_timeout && it == 0)) mbar_arrive(it & 1 ? &c->vfull[s] : &c->kfull[s]);
       }
-      cp_async_wait_all();
-    } else {
-      constexpr int L = DP / 16, kPer = L;  // 16-code pieces per row; pieces per thread and operand tile
-      constexpr int kStep = kProducers / L;
-      const int pc = pt % L, row0 = pt / L;
-      const bool col = pc * 16 < P.D;
-      const long long piece = static_cast<long long>(g) * P.D + (col ? pc * 16 : 0) + (static_cast<long long>(t0) + row0) * ts;
-      const long long byte = static_cast<long long>(P.H) * P.D + g + (static_cast<long long>(t0) + pt) * ts;
-      const unsigned char *src[2] = {kb + piece, vb + piece}, *scl[2] = {kb + byte, vb + byte};
-      const long long step = ts * kStep, jump = ts * kTok;
-      uint4 w[2][kPer];   // keys and values of the next block
-      uint32_t sc[2];     // scale byte of its token pt
-      auto fetch = [&](auto val, int k) {
-        constexpr int V = decltype(val)::value;
-        const int left = t1 - (t0 + k * kTok);
-        const unsigned char *p = src[V];
+      cp_async_commit();
+      return byte;
+    };
+    float E = kMinExponent, kscale = 1.f;
+    uint32_t sc0 = issue(0), sc1 = issue(1);
+    for (int it = 0; it < 2 * n; ++it) {
+      const uint32_t sc2 = issue(it + 2);
+      cp_async_wait<2>();
+      const int k = it >> 1, s = k & 1, q = q0 + k;
+      const bool val = it & 1;
+      // From this row of the block on, values are the pass's own tokens'.
+      // Those that are not finite are taken out (a query that does not see
+      // them would get 0 * NaN) and put into the answers of the queries that
+      // see them at the end.
+      const int own0 = !PRE && val && q >= npre ? len0 - (q - npre) * kTok : kTok;
+      if constexpr (!E4) {
+        if (own0 < kTok && live) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          w[V][i] = make_uint4(0, 0, 0, 0);
-          if (col && row0 + i * kStep < left) w[V][i] = __ldg(reinterpret_cast<const uint4 *>(p));
-          p += step;
+          for (int i = 0; i < kPer; ++i) {
+            if (row0 + i * kStep < own0) continue;
+            const uint32_t at = sbase + put0 + C::kV + s * C::kOp + i * kPut;
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
+              if ((w[e] & top) == top) w[e] &= 0xffff0000u, odd = true;
+              if ((w[e] >> 16 & top) == top) w[e] &= 0x0000ffffu, odd = true;
+            }
+            if (odd) {
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+              c->odd = 1;
+            }
+          }
         }
-        sc[V] = pt < left ? __ldg(scl[V]) : 0u;
-        src[V] += jump;
-        scl[V] += jump;
-      };
-      float E = kMinExponent, kscale = 1.f;
-      auto put = [&](auto val, int k) {
-        constexpr int V = decltype(val)::value;
-        const int s = k & 1;
+      } else {
+        const uint32_t buf = sbase + (val ? C::kV : C::kK) + s * C::kOp;
+        uint32_t w[kPer][4];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                       : "r"(buf + put0 + i * kPut)
+                       : "memory");
         // the block's largest scale
-        const uint32_t mine = sc[V];
-        const uint32_t wtop = __reduce_max_sync(FULL_MASK, mine == 255u ? 1u : max(mine, 1u));
-        if (lane == 0) c->red[V][warp & 3] = wtop;
-        producer_sync();
-        const uint32_t top = max(max(c->red[V][0], c->red[V][1]), max(c->red[V][2], c->red[V][3]));
+        const uint32_t wtop = __reduce_max_sync(FULL_MASK, sc0 == 255u ? 1u : max(sc0, 1u));
+        if (lane == 0) c->red[it & 1][warp & 3] = wtop;
+        producer_sync();  // also: every code of the block has been read
+        const uint32_t top = max(max(c->red[it & 1][0], c->red[it & 1][1]), max(c->red[it & 1][2], c->red[it & 1][3]));
         float ex = static_cast<float>(static_cast<int>(top) - 127);
-        if (V) {
+        if (val) {
           E = fmaxf(E, ex);
           ex = fmaxf(ex, E - kExponentSpan);
         }
         {
           // 2^(scale - block's scale) as fp16: exact down to 2^-24, zero below
-          const int d = static_cast<int>(mine) - (static_cast<int>(ex) + 127);
-          const uint32_t f = mine == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
-          c->mult[V][pt] = f | f << 16;
+          const int d = static_cast<int>(sc0) - (static_cast<int>(ex) + 127);
+          const uint32_t f = sc0 == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+          c->mult[it & 1][pt] = f | f << 16;
         }
-        if (k >= 2 && live) live = wait_for(c, V ? &c->vfree[s] : &c->kfree[s], ((k >> 1) - 1) & 1, limit);
         producer_sync();
-        if (live) {
-          unsigned char *const dst = smem + (V ? C::kV : C::kK) + s * C::kOp + (pc / 4) * 16384 + row0 * 128;
-          const int own0 = V && !PRE ? len0 - (t0 + k * kTok) : kTok;  // from this row on: the pass's own tokens
+        const uint32_t dst = buf + (pc / 4) * 16384 + row0 * 128;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int row = row0 + i * kStep;
-            const uint32_t fw = c->mult[V][row];
-            const __half2 f2 = *reinterpret_cast<const __half2 *>(&fw);
-            const uint32_t cw[4] = {w[V][i].x, w[V][i].y, w[V][i].z, w[V][i].w};
-            uint32_t o[8];
+        for (int i = 0; i < kPer; ++i) {
+          const int row = row0 + i * kStep;
+          const uint32_t fw = c->mult[it & 1][row];
+          const __half2 f2 = *reinterpret_cast<const __half2 *>(&fw);
+          uint32_t o[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t lo = e4m3x2_to_f16x2(cw[e]), hi = e4m3x2_to_f16x2_hi(cw[e]);
-              const __half2 l2 = __hmul2(*reinterpret_cast<const __half2 *>(&lo), f2);
-              const __half2 h2 = __hmul2(*reinterpret_cast<const __half2 *>(&hi), f2);
-              o[2 * e] = *reinterpret_cast<const uint32_t *>(&l2);
-              o[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&h2);
-            }
-            if (V && !PRE && row >= own0) {  // as for 16-bit entries
-              bool odd = false;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if ((o[e] & 0x7c00u) == 0x7c00u) o[e] &= 0xffff0000u, odd = true;
-                if ((o[e] >> 16 & 0x7c00u) == 0x7c00u) o[e] &= 0x0000ffffu, odd = true;
-              }
-              if (odd) c->odd = 1;
-            }
-            // the two 16-byte halves, the upper panel's lanes in the other
-            // order: eight lanes then cover all banks
-            const int ch = (pc % 4) * 2, first = pc / 4;
-            unsigned char *const at = dst + i * kStep * 128;
-            const uint4 h0 = make_uint4(o[0], o[1], o[2], o[3]), h1 = make_uint4(o[4], o[5], o[6], o[7]);
-            *reinterpret_cast<uint4 *>(at + (((ch + first) ^ (row & 7)) << 4)) = first ? h1 : h0;
-            *reinterpret_cast<uint4 *>(at + (((ch + 1 - first) ^ (row & 7)) << 4)) = first ? h0 : h1;
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = e4m3x2_to_f16x2(w[i][e]), hi = e4m3x2_to_f16x2_hi(w[i][e]);
+            const __half2 l2 = __hmul2(*reinterpret_cast<const __half2 *>(&lo), f2);
+            const __half2 h2 = __hmul2(*reinterpret_cast<const __half2 *>(&hi), f2);
+            o[2 * e] = *reinterpret_cast<const uint32_t *>(&l2);
+            o[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&h2);
           }
-          // the keys' scale goes with the values' exponents: the softmax waits
-          // for the values' buffer, which it holds until it is done
-          if (!V) kscale = e4m3_scale(top);
-          if (V && pt == 0) {
-            c->ksc[s] = kscale;
-            c->vex[s] = ex;
-            c->vtop[s] = E;
+          if (row >= own0) {
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if ((o[e] & 0x7c00u) == 0x7c00u) o[e] &= 0xffff0000u, odd = true;
+              if ((o[e] >> 16 & 0x7c00u) == 0x7c00u) o[e] &= 0x0000ffffu, odd = true;
+            }
+            if (odd) c->odd = 1;
           }
+          // the two 16-byte halves, the upper panel's lanes in the other
+          // order: eight lanes then cover all banks
+          const int ch = (pc % 4) * 2, up = pc / 4;
+          const uint32_t at = dst + i * kStep * 128;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((ch + up) ^ (row & 7)) << 4)),
+                       "r"(up ? o[4] : o[0]), "r"(up ? o[5] : o[1]), "r"(up ? o[6] : o[2]), "r"(up ? o[7] : o[3])
+                       : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((ch + 1 - up) ^ (row & 7)) << 4)),
+                       "r"(up ? o[0] : o[4]), "r"(up ? o[1] : o[5]), "r"(up ? o[2] : o[6]), "r"(up ? o[3] : o[7])
+                       : "memory");
         }
-        fence_async_smem();
-        if (!(P.force_timeout && k == 0 && !V)) mbar_arrive(V ? &c->vfull[s] : &c->kfull[s]);
-      };
-      using K = std::integral_constant<int, 0>;
-      using V = std::integral_constant<int, 1>;
-      fetch(K{}, 0);
-      fetch(V{}, 0);
-      for (int k = 0; k < n; ++k) {
-        put(K{}, k);
-        if (k + 1 < n) fetch(K{}, k + 1);
-        put(V{}, k);
-        if (k + 1 < n) fetch(V{}, k + 1);
+        // the keys' scale goes with the values' exponents: the softmax waits
+        // for the values' buffer, which it holds until it is done
+        if (!val) kscale = e4m3_scale(top);
+        if (val && pt == 0) {
+          c->ksc[s] = kscale;
+          c->vex[s] = ex;
+          c->vtop[s] = E;
+        }
       }
+      fence_async_smem();
+      if (!(P.force_timeout && it == 0)) mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
+      sc0 = sc1;
+      sc1 = sc2;
     }
+    cp_async_wait_all();
   } else if (role == 3) {
     // ------------------------------------------------- tensor-core issue
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4>::kIssue));
@@ -520,7 +436,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         for (int j = 0; j < kTok / 16; ++j)
           tc_mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + j * 8, bb + (j * 2048 >> 4), wv, k > 0 || j > 0);
       };
-      bool live = wait_for(c, &c->kfull[0], 0, limit);
+      bool live = wait_for(c, &c->qfull, 0, limit) && wait_for(c, &c->kfull[0], 0, limit);
       if (live) {
         tc_fence_after();
         for (int t = 0; t < tiles; ++t) scores(t, 0);
@@ -555,6 +471,79 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   } else {
     // --------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<E4>::kSoftmax));
+    // --- queries of rows tid (table) and of all 256 rows (operand): DP/8 lanes
+    // per row, 16 bytes each; fp16 for an e4m3 cache: a row far outside fp16's
+    // range is brought into it by a power of two.  A negative scale turns the
+    // queries' sign.
+    int at = -1;  // the thread's output row; -1: past the last, kUnused: no such query
+    {
+      const int r = r0 + tid;
+      long long off = 0;
+      if (r < nrows) {
+        const int t = r / P.G, h = g * P.G + (r - t * P.G);
+        const int qb = PRE ? t / P.N : b, qt = PRE ? t - qb * P.N : t;
+        at = (qb * P.N + qt) * P.Hq + h;
+        off = qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2];
+        if (qt >= (PRE ? row_queries(P, qb) : cnt)) at |= kUnused;
+      }
+      c->orow[tid] = at;
+      c->qoff[tid] = off;
+    }
+    asm volatile("bar.sync 2, 256;" ::: "memory");
+    {
+      constexpr int L = DP / 8, kIt = L, kBatch = 8, kStep = 256 / L;
+      const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
+      const int pc = tid % L, rr0 = tid / L;
+#pragma unroll
+      for (int i0 = 0; i0 < kIt; i0 += kBatch) {
+        uint4 u[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int rr = rr0 + (i0 + i) * kStep, row = c->orow[rr];
+          u[i] = make_uint4(0, 0, 0, 0);
+          if (row >= 0 && row < kUnused && pc * 8 < P.D) {
+            const unsigned short *q = static_cast<const unsigned short *>(P.q) + c->qoff[rr] + pc * 8;
+            if (vec) {
+              u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
+            } else {
+              u[i].x = q[0] | static_cast<uint32_t>(q[1]) << 16;
+              u[i].y = q[2] | static_cast<uint32_t>(q[3]) << 16;
+              u[i].z = q[4] | static_cast<uint32_t>(q[5]) << 16;
+              u[i].w = q[6] | static_cast<uint32_t>(q[7]) << 16;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int rr = rr0 + (i0 + i) * kStep;
+          float fac = 1.f;
+          if (E4 && P.qbf16) {
+            const float x[8] = {bf16_lo(u[i].x), bf16_hi(u[i].x), bf16_lo(u[i].y), bf16_hi(u[i].y),
+                                bf16_lo(u[i].z), bf16_hi(u[i].z), bf16_lo(u[i].w), bf16_hi(u[i].w)};
+            uint32_t a = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
+            float by = 1.f;
+            const int e = static_cast<int>(a >> 23) - 127;
+            if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
+              const int up = max(-126, min(126, -e));
+              by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+              fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            }
+            u[i] = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
+                              pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
+          }
+          if (pc == 0) c->qfac[rr] = fac;
+          if (P.scale < 0.f) u[i].x ^= 0x80008000u, u[i].y ^= 0x80008000u, u[i].z ^= 0x80008000u, u[i].w ^= 0x80008000u;
+          *reinterpret_cast<uint4 *>(smem + C::kQ + (rr / 128) * C::kOp + (pc / 8) * 16384 + (rr % 128) * 128 + (((pc % 8) ^ (rr & 7)) << 4)) = u[i];
+        }
+      }
+    }
+    fence_async_smem();
+    mbar_arrive(&c->qfull);
+    asm volatile("bar.sync 2, 256;" ::: "memory");  // the factors, for every row's thread
     const int tile = role;
     if (tile < tiles) {
       const int rr = tid;  // row of the block (tile * 128 + lane of tensor memory)
@@ -580,14 +569,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         live = __all_sync(FULL_MASK, live);
         if (!live) break;
         tc_fence_after();
-        const int tb = t0 + k * kTok;
-        const bool masked = tb + kTok > t1 || (!PRE && tb + kTok > len0);
-        // which of the 32 tokens from column q * 32 this row sees
-        auto seen = [&](int q) -> uint32_t {
-          const int tq = tb + q * 32;
+        const int q = q0 + k;
+        const bool pre = PRE || q < npre;
+        const int tb = (pre ? q : q - npre) * kTok;
+        const bool masked = tb + kTok > (pre ? P.P : len0);
+        // which of the 32 tokens from column 32 c32 this row sees
+        auto seen = [&](int c32) -> uint32_t {
+          const int tq = tb + c32 * 32;
           uint32_t bits;
-          if (PRE || !anc) {
-            const int see = (PRE ? t1 : min(t1, len0 + my + 1)) - tq;
+          if (pre || !anc) {
+            const int see = (pre ? P.P : min(len, len0 + my + 1)) - tq;
             bits = see >= 32 ? 0xffffffffu : see <= 0 ? 0u : (1u << see) - 1u;
           } else {
             const int j = tq - len0;  // first token's index among the pass's own
@@ -600,7 +591,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
               const uint32_t lo = wd < P.W ? __ldg(anc + wd) : 0u, hi = wd + 1 < P.W ? __ldg(anc + wd + 1) : 0u;
               bits = __funnelshift_r(lo, hi, j & 31);
             }
-            const int in = t1 - tq;
+            const int in = len - tq;
             if (in < 32) bits &= in <= 0 ? 0u : (1u << in) - 1u;
           }
           return bits;
@@ -698,24 +689,64 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         mbar_arrive(&c->pfull[tile]);
       }
       if (live) live = __all_sync(FULL_MASK, wait_for(c, &c->done[tile], 0, limit));
-      const int at = c->orow[rr], orow = at & (kUnused - 1);
+      const long long orow = at & (kUnused - 1);
+      float2 *const ml = P.ml + static_cast<long long>(slot) * P.rows + orow;
       if (!live) {
-        if (at >= 0) P.ml[static_cast<long long>(slot) * P.rows + orow] = make_float2(-INFINITY, __uint_as_float(kTimeoutBits));
+        if (at >= 0 && !P.direct) *ml = make_float2(-INFINITY, __uint_as_float(kTimeoutBits));
+        if (at >= 0 && P.direct) {
+          for (int d = 0; d < P.D; d += 8) *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(P.out) + orow * P.D + d) = make_uint4(0, 0, 0, 0);
+          if (P.lse) P.lse[orow] = -INFINITY;
+          if (P.row_status) P.row_status[b] = SPEC_ROW_TIMEOUT;
+        }
       } else {
         tc_fence_after();
         const bool some = at >= 0 && at < kUnused && l != 0.f;
-        if (at >= 0)
-          P.ml[static_cast<long long>(slot) * P.rows + orow] = some ? make_float2(m, m + log2f(l) - E) : make_float2(-INFINITY, -INFINITY);
-        float *const to = P.part + (static_cast<long long>(slot) * P.rows + orow) * P.D;
+        const float z = some ? m + log2f(l) - E : -INFINITY;
+        if (P.direct) {  // every thread loads: tensor memory is read by whole warps
+          const float w = some ? ex2(m - z) : 0.f;
+          const bool odd = some && c->odd;
+          if (at >= 0 && P.lse) P.lse[orow] = kLn2 * z;
 #pragma unroll
-        for (int q = 0; q < DP / 32; ++q) {
-          uint32_t o[32];
-          tc_ld32(o, o_addr + q * 32);
-          tc_wait_ld();
-          if (some) {
+          for (int q = 0; q < DP / 32; ++q) {
+            uint32_t o[32];
+            __syncwarp();
+            tc_ld32(o, o_addr + q * 32);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = some ? __float_as_uint(__uint_as_float(o[j]) * w) : 0u;
+            if (odd)  // values that are not finite, of the pass's tokens that this query sees
+              for (int t = 0; t < cnt; ++t)
+                if (anc ? anc[t >> 5] >> (t & 31) & 1u : t <= my)
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    if (q * 32 + j < P.D) o[j] = __float_as_uint(__uint_as_float(o[j]) + odd_value<CT>(P, b, len0 + t, g, q * 32 + j));
+            unsigned short *const to = static_cast<unsigned short *>(P.out) + orow * P.D + q * 32;
 #pragma unroll
             for (int j = 0; j < 32; j += 8)
-              if (q * 32 + j < P.D) st_global_v8(to + q * 32 + j, o + j);
+              if (at >= 0 && q * 32 + j < P.D) {
+                uint32_t y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float lo = __uint_as_float(o[j + 2 * e]), hi = __uint_as_float(o[j + 2 * e + 1]);
+                  y[e] = P.qbf16 ? pack16<true>(lo, hi) : pack16<false>(lo, hi);
+                }
+                *reinterpret_cast<uint4 *>(to + j) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+          }
+        } else {
+          if (at >= 0) *ml = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
+          float *const to = P.part + (static_cast<long long>(slot) * P.rows + orow) * P.D;
+#pragma unroll
+          for (int q = 0; q < DP / 32; ++q) {
+            uint32_t o[32];
+            __syncwarp();
+            tc_ld32(o, o_addr + q * 32);
+            tc_wait_ld();
+            if (some) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8)
+                if (q * 32 + j < P.D) st_global_v8(to + q * 32 + j, o + j);
+            }
           }
         }
         tc_fence_before();

@@ -393,3 +393,53 @@ def test_a_wait_that_runs_out_is_reported(sv):
         assert float(out.abs().max()) == 0.0 and bool((lse == float("-inf")).all())
         out, lse, st = p.call()
         assert st.tolist() == [0] * 24 and torch.equal(out, out0) and torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("kind,qt", KINDS)
+@pytest.mark.parametrize("P,D", [(130, 64), (0, 128), (256, 128)])
+def test_trees_that_need_no_join(sv, kind, qt, P, D):
+    """Enough rows that no part is cut: the kernel writes the answers itself, bad rows, fewer queries
+    and values that are not finite among them."""
+    import torch
+    B, N = 80, 32
+    rng = np.random.default_rng(P + D)
+    lens = rng.integers(0, 200, B)
+    count = rng.integers(0, N + 1, B)
+    count[:4] = [N, 0, N, 1]
+    p = Problem(sv, B, N, 8, 2, D, P, lens, kind, qt, True, count=count, seed=P)
+    out0, lse0 = p.check(rows=[0, 1, 2, 3, 41, 79])
+    p.parent[2, 5], p.lens[3] = 5, -3
+    bad = int(np.flatnonzero(count[10:] > 8)[0]) + 10
+    j = int(count[bad]) - 3
+    at = int(p.lens[bad]) + j
+    if kind == "uint8":
+        p.cache[1, bad, at, 3] = 0x7f                  # a code that stands for NaN: head 0, column 3
+    else:
+        p.cache[1, bad, at, 0, 3] = float("-inf")
+    out, lse, st = p.call()
+    want = torch.zeros(B, dtype=torch.int32)
+    want[2], want[3] = 4, 8
+    assert torch.equal(st.cpu(), want)
+    for b in (2, 3):
+        assert float(out[b].abs().max()) == 0.0 and bool((lse[b] == float("-inf")).all())
+    keep = torch.ones(B, dtype=torch.bool)
+    keep[[2, 3, bad]] = False
+    assert torch.equal(out[keep], out0[keep]) and torch.equal(lse, lse0.index_put((torch.tensor([2, 3]).cuda(),), torch.tensor(float("-inf")).cuda()))
+    sees = torch.from_numpy(seen(N, p.parent[bad])[:, j] & (np.arange(N) < count[bad])).cuda()
+    assert torch.equal(out[bad][~sees], out0[bad][~sees])
+    hit = out[bad][sees][:, :4, 3]                     # the queries of KV head 0
+    assert bool((torch.isnan(hit) if kind == "uint8" else hit == float("-inf")).all())
+    rest = out[bad].clone()
+    rest[:, :4, 3] = out0[bad][:, :4, 3]
+    assert torch.equal(rest, out0[bad])
+    limit = sv.get_wait_timeout_ns()
+    try:
+        sv.set_wait_timeout_ns(2_000_000)
+        sv.debug_force_wait_timeout(True)
+        out, lse, st = p.call()
+        torch.cuda.synchronize()
+    finally:
+        sv.debug_force_wait_timeout(False)
+        sv.set_wait_timeout_ns(limit)
+    want[torch.from_numpy(count > 0) & (want == 0)] = 6
+    assert torch.equal(st.cpu(), want) and float(out.abs().max()) == 0.0
