@@ -308,8 +308,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     float E = kMinExponent, kscale = 1.f;
     uint32_t sc0 = issue(0), sc1 = issue(1);
     for (int it = 0; it < 2 * n; ++it) {
-      const uint32_t sc2 = issue(it + 2);
-      cp_async_wait<2>();
+      cp_async_wait<1>();
       const int k = it >> 1, s = k & 1, q = q0 + k;
       const bool val = it & 1;
       // From this row of the block on, values are the pass's own tokens'.
@@ -411,7 +410,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       fence_async_smem();
       if (!(P.force_timeout && it == 0)) mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
       sc0 = sc1;
-      sc1 = sc2;
+      sc1 = issue(it + 2);  // after this item is handed over: its buffer may be a while in coming free
     }
     cp_async_wait_all();
   } else if (role == 3) {
