@@ -174,15 +174,23 @@ __device__ __forceinline__ void st_global_v8(float *p, const uint32_t *r) {
                : "memory");
 }
 
-// Raises a kernel's dynamic shared memory limit, once per device.
+// Raises a kernel's dynamic shared memory limit, once per device.  A kernel
+// whose roles trade registers must have been given `regs` of them at launch
+// (else the roles that take more would wait for ever): checked here.
 template <auto Kernel>
-cudaError_t allow_smem(int bytes) {
+cudaError_t allow_smem(int bytes, int regs = 0) {
   static std::atomic<uint64_t> done{0};
   int dev;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (regs) {
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, Kernel);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs != regs) return cudaErrorInvalidConfiguration;
+  }
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;

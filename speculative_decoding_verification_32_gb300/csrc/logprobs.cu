@@ -47,10 +47,11 @@ struct LpParams {
   const float *temperature;
   float *logprob, *entropy, *top_logprobs;
   int32_t *top_ids, *status;
-  LpPart *part;          // [rows * nslices]
+  LpPart *part;          // [rows * nparts]
   unsigned short *cmax;  // [rows * nslices * kLpThreads]
   long long row_stride;
   int rows, npos, V, m, slice, nslices;
+  int run, nparts;       // slices per stream item, records per position
 };
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -87,67 +88,101 @@ __device__ __forceinline__ float row_scale(const LpParams &P, int r, uint32_t &f
   return kLog2e / T;
 }
 
+// One slice's logits of a thread, as they are in memory.
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kLpThreads) logprobs_stream_kernel(const __grid_constant__ LpParams P) {
-  constexpr int E = BF16 ? 8 : 4;
-  const int r = blockIdx.y * 32768 + blockIdx.z, sl = blockIdx.x, tid = threadIdx.x;
-  if (r >= P.rows) return;
-  if (P.tokens && __ldg(P.tokens + r) == -1) return;
-  uint32_t flags = 0;
-  const float sc = row_scale(P, r, flags);
-  const size_t esz = BF16 ? 2 : 4;
-  const char *row = static_cast<const char *>(P.logits) + static_cast<size_t>(r) * P.row_stride * esz;
-  const int v0 = sl * P.slice;
-  float x[kLpVecs * E];
-  if constexpr (VEC) {
-    const uint64_t pol = l2_policy_evict_first();
-    uint4 w[kLpVecs];
+struct LpSlice {
+  static constexpr int E = BF16 ? 8 : 4;
+  uint4 w[kLpVecs];
+
+  __device__ __forceinline__ void load(const char *row, int v0, int V, int tid, uint64_t pol) {
 #pragma unroll
     for (int i = 0; i < kLpVecs; ++i) {
       const int v = v0 + (i * kLpThreads + tid) * E;
-      // V is a multiple of E here: a vector is inside or outside as a whole
+      // -inf past the end
       w[i] = BF16 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
                   : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-      if (v < P.V) w[i] = ld_stream_u4(row + static_cast<size_t>(v) * esz, pol);
+      if constexpr (VEC) {
+        // V is a multiple of E here: a vector is inside or outside as a whole
+        if (v < V) w[i] = ld_stream_u4(row + static_cast<size_t>(v) * (BF16 ? 2 : 4), pol);
+      } else {
+        uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (v + j < V) {
+            if constexpr (BF16) {
+              const uint32_t h = __ldg(reinterpret_cast<const unsigned short *>(row) + v + j);
+              u[j / 2] = j & 1 ? (u[j / 2] & 0xffffu) | h << 16 : (u[j / 2] & 0xffff0000u) | h;
+            } else {
+              u[j] = __ldg(reinterpret_cast<const uint32_t *>(row) + v + j);
+            }
+          }
+        w[i] = make_uint4(u[0], u[1], u[2], u[3]);
+      }
     }
+  }
+  __device__ __forceinline__ float2 pair(int i, int j) const {  // elements 2 j, 2 j + 1 of vector i
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    if constexpr (BF16) return make_float2(bf16_lo(u[j]), bf16_hi(u[j]));
+    return make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+  }
+};
+
+// Item: position r, slices sl0 .. sl0 + P.run - 1 of it.  The next slice's
+// loads are on their way while a slice is worked on.
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_stream_kernel(const __grid_constant__ LpParams P) {
+  constexpr int E = BF16 ? 8 : 4;
+  const int r = blockIdx.y * 32768 + blockIdx.z, sl0 = blockIdx.x * P.run, tid = threadIdx.x;
+  if (r >= P.rows) return;
+  const char *row = static_cast<const char *>(P.logits) + static_cast<size_t>(r) * P.row_stride * (BF16 ? 2 : 4);
+  const uint64_t pol = l2_policy_evict_first();
+  const int sl1 = min(sl0 + P.run, P.nslices);
+  if (P.tokens && __ldg(P.tokens + r) == -1) return;
+  LpSlice<BF16, VEC> cur, nxt;
+  cur.load(row, sl0 * P.slice, P.V, tid, pol);
+  uint32_t flags = 0;
+  const float sc = row_scale(P, r, flags);
+  float m = -INFINITY, s = 0.f, u = 0.f;
+  for (int sl = sl0; sl < sl1; ++sl) {
+    if (sl + 1 < sl1) nxt.load(row, (sl + 1) * P.slice, P.V, tid, pol);
+    float c = -INFINITY;  // this thread's largest
 #pragma unroll
     for (int i = 0; i < kLpVecs; ++i) {
-      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      if constexpr (BF16) {
+        // packed: one instruction for two pairs
+        const uint32_t t = bf16x2_max_nan(bf16x2_max_nan(cur.w[i].x, cur.w[i].y), bf16x2_max_nan(cur.w[i].z, cur.w[i].w));
+        c = fmax_nan(c, fmax_nan(bf16_lo(t), bf16_hi(t)));
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (BF16) {
-          x[i * E + 2 * j] = bf16_lo(u[j]);
-          x[i * E + 2 * j + 1] = bf16_hi(u[j]);
-        } else {
-          x[i * E + j] = __uint_as_float(u[j]);
+        for (int j = 0; j < 2; ++j) c = fmax_nan(c, fmax_nan(cur.pair(i, j).x, cur.pair(i, j).y));
+      }
+    }
+    if (!(c < INFINITY)) flags |= F_NONFINITE;  // NaN or +inf
+    if (P.m > 0) P.cmax[(static_cast<size_t>(r) * P.nslices + sl) * kLpThreads + tid] = static_cast<unsigned short>(order_key(c) >> 16);
+    if (c > m) {  // the sums follow the largest so far
+      const float d = fmaxf((m - c) * sc, kFloorY), f = ex2(d);
+      u = f * (u + d * s);
+      s *= f;
+      m = c;
+    }
+    if (m > -INFINITY) {
+      const float2 sc2 = make_float2(sc, sc), off2 = make_float2(-m, -m);
+      float2 s2 = make_float2(0.f, 0.f), u2 = s2;
+#pragma unroll
+      for (int i = 0; i < kLpVecs; ++i)
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) {
+          float2 y = fmul2(fadd2(cur.pair(i, j), off2), sc2);
+          y = make_float2(fmaxf(y.x, kFloorY), fmaxf(y.y, kFloorY));
+          const float2 e = make_float2(ex2(y.x), ex2(y.y));
+          s2 = fadd2(s2, e);
+          u2 = ffma2(y, e, u2);
         }
-      }
+      s += s2.x + s2.y;
+      u += u2.x + u2.y;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kLpVecs; ++i)
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int v = v0 + (i * kLpThreads + tid) * E + j;
-        x[i * E + j] = v < P.V ? logit_at<BF16>(row, v) : -INFINITY;
-      }
+    cur = nxt;
   }
-  float m = x[0];
-#pragma unroll
-  for (int i = 1; i < kLpVecs * E; ++i) m = fmax_nan(m, x[i]);
-  if (!(m < INFINITY)) flags |= F_NONFINITE;  // NaN or +inf
-  float s = 0.f, u = 0.f;
-  if (m > -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < kLpVecs * E; ++i) {
-      const float y = fmaxf((x[i] - m) * sc, kFloorY);
-      const float e = ex2(y);
-      s += e;
-      u = fmaf(y, e, u);
-    }
-  }
-  const size_t item = static_cast<size_t>(r) * P.nslices + sl;
-  if (P.m > 0) P.cmax[item * kLpThreads + tid] = static_cast<unsigned short>(order_key(m) >> 16);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     join(m, s, u, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, s, o),
@@ -156,12 +191,15 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_stream_kernel(const __gri
   __shared__ LpPart sh[kLpThreads / 32];
   if (tid % 32 == 0) sh[tid / 32] = LpPart{m, s, u, flags};
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kLpThreads / 32; ++w) {
-      join(m, s, u, sh[w].m, sh[w].s, sh[w].u, sc);
-      flags |= sh[w].flags;
-    }
-    P.part[item] = LpPart{m, s, u, flags};
+  if (tid < 32) {
+    const LpPart p = tid < kLpThreads / 32 ? sh[tid] : LpPart{-INFINITY, 0.f, 0.f, 0u};
+    m = p.m, s = p.s, u = p.u, flags = p.flags;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+      join(m, s, u, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, s, o),
+           __shfl_xor_sync(FULL_MASK, u, o), sc);
+    flags = __reduce_or_sync(FULL_MASK, flags);
+    if (tid == 0) P.part[static_cast<size_t>(r) * P.nparts + blockIdx.x] = LpPart{m, s, u, flags};
   }
 }
 
@@ -182,7 +220,6 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_
   constexpr int E = BF16 ? 8 : 4;
   constexpr int kChunk = kLpVecs * E;
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  __shared__ LpPart sh[kLpThreads / 32];
   __shared__ int red[kLpThreads / 32];
   __shared__ int counts[2][kLpThreads / 32][3];
   __shared__ int n_chunks, n_cands;
@@ -212,10 +249,15 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_
     }
     return;
   }
-  // the slices' records
+  // the chunk keys, then the records (every warp joins them all: no barrier)
+  const int nkeys = P.nslices * kLpThreads;
+  unsigned short *const keys = reinterpret_cast<unsigned short *>(lp_smem);
+  if (P.m > 0)
+    for (int i = tid; i < nkeys / 8; i += kLpThreads)
+      cp_async16(keys + 8 * i, P.cmax + static_cast<size_t>(r) * nkeys + 8 * i);
   float m = -INFINITY, s = 0.f, u = 0.f;
-  for (int i = tid; i < P.nslices; i += kLpThreads) {
-    const LpPart p = P.part[static_cast<size_t>(r) * P.nslices + i];
+  for (int i = lane; i < P.nparts; i += 32) {
+    const LpPart p = P.part[static_cast<size_t>(r) * P.nparts + i];
     join(m, s, u, p.m, p.s, p.u, sc);
     flags |= p.flags;
   }
@@ -223,14 +265,13 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_
   for (int o = 16; o > 0; o >>= 1)
     join(m, s, u, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, s, o),
          __shfl_xor_sync(FULL_MASK, u, o), sc);
+  // one lane's rounding for all: which thread writes which output is a matter of timing
+  m = __shfl_sync(FULL_MASK, m, 0);
+  s = __shfl_sync(FULL_MASK, s, 0);
+  u = __shfl_sync(FULL_MASK, u, 0);
   flags = __reduce_or_sync(FULL_MASK, flags);
-  if (lane == 0) sh[warp] = LpPart{m, s, u, flags};
+  cp_async_wait_all();
   __syncthreads();
-  m = sh[0].m, s = sh[0].s, u = sh[0].u, flags = sh[0].flags;
-  for (int w = 1; w < kLpThreads / 32; ++w) {
-    join(m, s, u, sh[w].m, sh[w].s, sh[w].u, sc);
-    flags |= sh[w].flags;
-  }
   if (m == -INFINITY && !(flags & F_NONFINITE)) flags |= F_EMPTY;
   const float lgs = log2f(s);
   const bool bad = flags != 0;
@@ -252,12 +293,6 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_
   // The chunk keys' m-th largest: two bits at a time, the largest t that at
   // least m keys reach.  If the position has fewer than m chunks, t = 0: every
   // chunk is looked at.
-  const int nkeys = P.nslices * kLpThreads;
-  const unsigned short *ck = P.cmax + static_cast<size_t>(r) * nkeys;
-  unsigned short *const keys = reinterpret_cast<unsigned short *>(lp_smem);
-  for (int i = tid; i < nkeys / 8; i += kLpThreads)
-    reinterpret_cast<uint4 *>(keys)[i] = reinterpret_cast<const uint4 *>(ck)[i];
-  __syncthreads();
   const uint32_t *const pairs = reinterpret_cast<const uint32_t *>(keys);
   unsigned t16 = 0;
   for (int bit = 14; bit >= 0; bit -= 2) {
@@ -351,6 +386,12 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_
 }
 
 int lp_slice(bool bf16) { return kLpThreads * kLpVecs * (bf16 ? 8 : 4); }
+// Slices per stream item: as many as leave eight items per SM.
+int lp_run(long long rows, int nslices) {
+  int run = 1;
+  while (run < 8 && rows * ((nslices + 2 * run - 1) / (2 * run)) >= 8 * 152) run *= 2;
+  return run;
+}
 size_t lp_round(size_t x) { return (x + 255) / 256 * 256; }
 bool lp_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -361,7 +402,7 @@ bool lp_sizes(int32_t B, int32_t npos, int32_t V) {
 template <bool BF16>
 cudaError_t launch_logprobs(const LpParams &p, bool vec, cudaStream_t s) {
   // rows over y and z (65535 at most in each)
-  const dim3 grid(p.nslices, (p.rows + 32767) / 32768, p.rows < 32768 ? p.rows : 32768);
+  const dim3 grid(p.nparts, (p.rows + 32767) / 32768, p.rows < 32768 ? p.rows : 32768);
   if (vec)
     logprobs_stream_kernel<BF16, true><<<grid, kLpThreads, 0, s>>>(p);
   else
@@ -428,9 +469,14 @@ spec_status spec_token_logprobs(const spec_logprobs_args *a, const spec_logprobs
   p.m = a->m;
   p.slice = lp_slice(bf16);
   p.nslices = (a->V + p.slice - 1) / p.slice;
+  // few positions: a CTA per slice, so that more SMs share a position; many:
+  // up to 8 slices each, so that starts and ends weigh less (224 positions of
+  // 128256 bf16 logits: 23 us at one slice each, 13 at four)
+  p.run = lp_run(p.rows, p.nslices);
+  p.nparts = (p.nslices + p.run - 1) / p.run;
   p.part = static_cast<LpPart *>(ws);
   p.cmax = reinterpret_cast<unsigned short *>(static_cast<char *>(ws) +
-                                              lp_round(static_cast<size_t>(p.rows) * p.nslices * sizeof(LpPart)));
+                                              lp_round(static_cast<size_t>(p.rows) * p.nparts * sizeof(LpPart)));
   const bool vec = lp_aligned(a->logits, 16) && (a->row_stride * esz) % 16 == 0 && (static_cast<long long>(a->V) * esz) % 16 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = bf16 ? launch_logprobs<true>(p, vec, s) : launch_logprobs<false>(p, vec, s);

@@ -35,16 +35,19 @@
 namespace sv {
 namespace {
 
-constexpr int kTok = 128;          // tokens per block
-constexpr int kTileThreads = 512;  // softmax A, softmax B, producers, tensor-core issue
-constexpr int kProducers = 128;
-// Registers per thread of the roles.  Their sum over the four groups of 128
-// threads is what the block is launched with, 4 x 128.
+constexpr int kTok = 128;          // tokens per block, a producer thread each
+// Groups of 128 threads: softmax of tiles A and B, producers, tensor-core
+// issue.  Their registers per thread add up to what the block is launched
+// with.  (Two groups of producers for codes, at 96 registers a thread: 288 us
+// where one group takes 267, 32 trees of 60 nodes behind 4097 tokens.)
 template <bool E4>
-struct Regs {
+struct Roles {
+  static constexpr int kGroups = 4, kThreads = 128 * kGroups, kProducers = 128;
+  static constexpr int kIssueWarp = 4 * (kGroups - 1);
+  static constexpr int kLaunch = 128;  // registers per thread at launch: 65536 / kThreads
   static constexpr int kSoftmax = E4 ? 160 : 176, kProduce = E4 ? 120 : 88, kIssue = 72;
-  static_assert(kSoftmax > 128 && kProduce < 128 && kIssue < 128, "softmax takes more, the others give back");
-  static_assert(2 * kSoftmax + kProduce + kIssue == 512, "the block's registers");
+  static_assert(kSoftmax > kLaunch && kProduce < kLaunch && kIssue < kLaunch, "softmax takes more, the others give back");
+  static_assert(2 * kSoftmax + kProduce + kIssue == kGroups * kLaunch, "the block's registers");
 };
 constexpr float kLazy = 8.f;       // log2 of the growth a row's maximum may make before its sums follow
 
@@ -153,7 +156,10 @@ __device__ __forceinline__ uint32_t inst_desc(bool bf16, int n, bool b_cols) {
 }
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void producer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void producer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
 
 // Bounded wait that also ends when another role has given up.
 __device__ __forceinline__ bool wait_for(Ctrl *c, uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
@@ -176,8 +182,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(
 // part) against the row's own entries, after the prefix's if P.fuse; with one
 // part and nothing else to join (P.direct) it writes the answer itself.
 template <int CT, int DP, bool PRE>
-__global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid_constant__ AttnParams P, int blocks) {
+__global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile_kernel(const __grid_constant__ AttnParams P, int blocks) {
   using C = TileCfg<DP>;
+  using R = Roles<CT == SPEC_E4M3>;
+  constexpr int kProducers = R::kProducers;
   constexpr bool E4 = CT == SPEC_E4M3, BF = CT == SPEC_BF16;
   extern __shared__ unsigned char raw[];
   unsigned char *const smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -246,23 +254,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     c->odd = 0;
     fence_mbar_init();
   }
-  if (warp == 12) tc_alloc(&c->tmem);
+  if (warp == R::kIssueWarp) tc_alloc(&c->tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c->tmem;
   const uint64_t limit = P.wait_limit_ns;
 
-  if (role == 2) {
+  if (role >= 2 && role < R::kGroups - 1) {
     // ------------------------------------------------------------ producers
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4>::kProduce));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kProduce));
     const int pt = tid - 256;
     bool live = true;
     // A thread brings 16-byte pieces of every kStep-th token.  Item 2k: keys
     // of block k, item 2k + 1: its values.  16-bit entries go where the tensor
     // cores want them; codes land in the same buffer as they are and are turned
     // into fp16 there once they have arrived.
-    constexpr int L = E4 ? DP / 16 : DP / 8, kPer = L, kStep = kProducers / L;
+    constexpr int L = E4 ? DP / 16 : DP / 8, kStep = kProducers / L, kPer = kTok / kStep;
     const int pc = pt % L, row0 = pt / L;
     const bool col = pc * 16 < P.D * (E4 ? 1 : 2);
     const uint32_t sbase = smem_u32(smem);
@@ -348,8 +356,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                        : "memory");
         // the block's largest scale
         const uint32_t wtop = __reduce_max_sync(FULL_MASK, sc0 == 255u ? 1u : max(sc0, 1u));
-        if (lane == 0) c->red[it & 1][warp & 3] = wtop;
-        producer_sync();  // also: every code of the block has been read
+        if (lane == 0) c->red[it & 1][pt / 32] = wtop;
+        producer_sync<kProducers>();  // also: every code of the block has been read
         const uint32_t top = max(max(c->red[it & 1][0], c->red[it & 1][1]), max(c->red[it & 1][2], c->red[it & 1][3]));
         float ex = static_cast<float>(static_cast<int>(top) - 127);
         if (val) {
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           const uint32_t f = sc0 == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
           c->mult[it & 1][pt] = f | f << 16;
         }
-        producer_sync();
+        producer_sync<kProducers>();
         const uint32_t dst = buf + (pc / 4) * 16384 + row0 * 128;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -413,10 +421,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       sc1 = issue(it + 2);  // after this item is handed over: its buffer may be a while in coming free
     }
     cp_async_wait_all();
-  } else if (role == 3) {
+  } else if (role == R::kGroups - 1) {
     // ------------------------------------------------- tensor-core issue
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4>::kIssue));
-    if (warp == 12 && lane == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssue));
+    if (warp == R::kIssueWarp && lane == 0) {
       const uint32_t qk = inst_desc(BF, kTok, false), wv = inst_desc(BF, DP, true);
       const uint32_t base = smem_u32(smem);
       const uint64_t qd = op_desc(base + C::kQ, 16), kd = op_desc(base + C::kK, 16), vd = op_desc(base + C::kV, 16384);
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     }
   } else {
     // --------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<E4>::kSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmax));
     // --- queries of rows tid (table) and of all 256 rows (operand): DP/8 lanes
     // per row, 16 bytes each; fp16 for an e4m3 cache: a row far outside fp16's
     // range is brought into it by a power of two.  A negative scale turns the
@@ -754,7 +762,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   }
   __syncthreads();
   if (!PRE && tid == 0) P.oflag[blockIdx.x] = c->odd;
-  if (warp == 12) {
+  if (warp == R::kIssueWarp) {
     __syncwarp();
     tc_fence_after();
     tc_dealloc(tmem);
@@ -767,9 +775,9 @@ cudaError_t launch(const AttnParams &p, cudaStream_t s) {
   const int blocks = static_cast<int>(((PRE ? static_cast<long long>(p.B) : 1LL) * p.N * p.G + 255) / 256);
   const long long items = PRE ? static_cast<long long>(p.H) * blocks * p.psplits : static_cast<long long>(p.B) * p.H * blocks * p.osplits;
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<attn_tile_kernel<CT, DP, PRE>>(C::kSmem);
+  const cudaError_t e = allow_smem<attn_tile_kernel<CT, DP, PRE>>(C::kSmem, Roles<CT == SPEC_E4M3>::kLaunch);
   if (e != cudaSuccess) return e;
-  attn_tile_kernel<CT, DP, PRE><<<static_cast<unsigned>(items), kTileThreads, C::kSmem, s>>>(p, blocks);
+  attn_tile_kernel<CT, DP, PRE><<<static_cast<unsigned>(items), Roles<CT == SPEC_E4M3>::kThreads, C::kSmem, s>>>(p, blocks);
   return cudaGetLastError();
 }
 
