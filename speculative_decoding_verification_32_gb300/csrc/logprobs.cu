@@ -52,6 +52,7 @@ struct LpParams {
   long long row_stride;
   int rows, npos, V, m, slice, nslices;
   int run, nparts;       // slices per stream item, records per position
+  int vec;               // rows are 16-byte aligned
 };
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -218,10 +219,8 @@ __device__ __forceinline__ int block_sum(int v, int *sh) {
 template <bool BF16>
 __global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_constant__ LpParams P) {
   constexpr int E = BF16 ? 8 : 4;
-  constexpr int kChunk = kLpVecs * E;
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   __shared__ int red[kLpThreads / 32];
-  __shared__ int counts[2][kLpThreads / 32][3];
   __shared__ int n_chunks, n_cands;
   extern __shared__ __align__(16) unsigned char lp_smem[];  // the position's chunk keys
   __shared__ int chunk[kLpChunks];
@@ -290,47 +289,46 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_
     }
     return;
   }
-  // The chunk keys' m-th largest: two bits at a time, the largest t that at
-  // least m keys reach.  If the position has fewer than m chunks, t = 0: every
-  // chunk is looked at.
-  const uint32_t *const pairs = reinterpret_cast<const uint32_t *>(keys);
+  // A lower bound of the m-th largest chunk key: the m-th largest of the 256
+  // threads' own maxima, bit by bit (a barrier counts).  At least m chunks reach
+  // it, and few more.  With fewer than m maxima it is 0: all are looked at.
+  unsigned mine = 0;
+#pragma unroll 8
+  for (int i = tid; i < nkeys; i += kLpThreads) mine = max(mine, static_cast<unsigned>(keys[i]));
   unsigned t16 = 0;
-  for (int bit = 14; bit >= 0; bit -= 2) {
-    const unsigned q = 1u << bit;
-    int c1 = 0, c2 = 0, c3 = 0;
-    for (int i = tid; i < nkeys / 2; i += kLpThreads) {
-      const uint32_t w = pairs[i], lo = w & 0xffffu, hi = w >> 16;
-      c1 += (lo >= t16 + q) + (hi >= t16 + q);
-      c2 += (lo >= t16 + 2 * q) + (hi >= t16 + 2 * q);
-      c3 += (lo >= t16 + 3 * q) + (hi >= t16 + 3 * q);
-    }
-    c1 = __reduce_add_sync(FULL_MASK, c1);
-    c2 = __reduce_add_sync(FULL_MASK, c2);
-    c3 = __reduce_add_sync(FULL_MASK, c3);
-    int(*const row)[3] = counts[(bit >> 1) & 1];  // two sets: one barrier a step is enough
-    if (lane == 0) row[warp][0] = c1, row[warp][1] = c2, row[warp][2] = c3;
-    __syncthreads();
-    c1 = c2 = c3 = 0;
 #pragma unroll
-    for (int w = 0; w < kLpThreads / 32; ++w) c1 += row[w][0], c2 += row[w][1], c3 += row[w][2];
-    t16 += c3 >= P.m ? 3 * q : c2 >= P.m ? 2 * q : c1 >= P.m ? q : 0u;
+  for (int bit = 15; bit >= 0; --bit) {
+    const unsigned t = t16 | (1u << bit);
+    if (__syncthreads_count(mine >= t) >= P.m) t16 = t;
   }
-  for (int i = tid; i < nkeys; i += kLpThreads)
-    if (keys[i] >= t16) {
-      const int at = atomicAdd(&n_chunks, 1);
-      if (at < kLpChunks) chunk[at] = i;
-    }
+  if (mine >= t16)
+    for (int i = tid; i < nkeys; i += kLpThreads)
+      if (keys[i] >= t16) {
+        const int at = atomicAdd(&n_chunks, 1);
+        if (at < kLpChunks) chunk[at] = i;
+      }
   __syncthreads();
   const int nc = n_chunks;
   if (nc <= kLpChunks) {
-    for (int i = tid; i < nc * kChunk; i += kLpThreads) {
-      const int c = chunk[i / kChunk], e = i % kChunk;
-      const int v = (c / kLpThreads) * P.slice + ((e / E) * kLpThreads + c % kLpThreads) * E + e % E;
-      if (v >= P.V) continue;
-      const uint32_t k = order_key(logit_at<BF16>(row, v));
-      if ((k >> 16) < t16) continue;
-      const int at = atomicAdd(&n_cands, 1);
-      if (at < kLpCands) cand[at] = static_cast<unsigned long long>(k) << 32 | (0xffffffffu - v);
+    // a 16-byte vector per thread
+    for (int i = tid; i < nc * kLpVecs; i += kLpThreads) {
+      const int c = chunk[i / kLpVecs];
+      const int v0 = (c / kLpThreads) * P.slice + ((i % kLpVecs) * kLpThreads + c % kLpThreads) * E;
+      if (v0 >= P.V) continue;
+      uint32_t w[4];
+      if (P.vec) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row + v0 * esz));
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (v0 + e >= P.V) break;
+        const float x = !P.vec ? logit_at<BF16>(row, v0 + e) : BF16 ? (e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2])) : __uint_as_float(w[BF16 ? 0 : e]);
+        const uint32_t k = order_key(x);
+        if ((k >> 16) < t16) continue;
+        const int at = atomicAdd(&n_cands, 1);
+        if (at < kLpCands) cand[at] = static_cast<unsigned long long>(k) << 32 | (0xffffffffu - (v0 + e));
+      }
     }
   }
   __syncthreads();
@@ -478,6 +476,7 @@ spec_status spec_token_logprobs(const spec_logprobs_args *a, const spec_logprobs
   p.cmax = reinterpret_cast<unsigned short *>(static_cast<char *>(ws) +
                                               lp_round(static_cast<size_t>(p.rows) * p.nparts * sizeof(LpPart)));
   const bool vec = lp_aligned(a->logits, 16) && (a->row_stride * esz) % 16 == 0 && (static_cast<long long>(a->V) * esz) % 16 == 0;
+  p.vec = vec;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = bf16 ? launch_logprobs<true>(p, vec, s) : launch_logprobs<false>(p, vec, s);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
