@@ -559,7 +559,7 @@ spec_status spec_kv_read(const spec_kv_read_args *args, int32_t *row_status, voi
  * prefix_len slots (prefix_len 0: `prefix` is ignored).  out [rows, N,
  * q_heads, head_dim] of q_dtype and lse [rows, N, q_heads] fp32 (optional) are
  * dense, 16-byte aligned.  N <= SPEC_MAX_TREE_NODES,
- * rows * N * q_heads < 2^31 / 256.
+ * rows * N * q_heads < 2^31 / 256, tok_stride of both caches < 2^27.
  *
  * row_status [rows] (optional): SPEC_ROW_BAD_SLOT (kv_len[b] < 0, count[b]
  * outside [0, N], kv_len[b] + count[b] > slots) or SPEC_ROW_BAD_PARENT; such a

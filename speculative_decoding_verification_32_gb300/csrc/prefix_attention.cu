@@ -73,15 +73,17 @@ struct RowCfg {
   static constexpr bool E4 = CT == SPEC_E4M3;
   static constexpr int kEsz = E4 ? 1 : 2;
   static constexpr int kM = 16 * MT;                        // query rows
-  static constexpr int kBlk = E4 && MT == 1 ? 32 : 16;      // tokens per block
+  static constexpr int kBlk = 16;                           // tokens per block
   static constexpr int kStages = 3;
   static constexpr int kPitch = DP * kEsz + 16;             // bytes of one token in a ring slot
   static constexpr int kPlane = kBlk * kPitch;              // K or V of a block
   static constexpr int kScales = E4 ? 2 * kBlk * 4 : 0;     // scale words, K then V
+  static constexpr int kTable = E4 ? kBlk * 16 : 0;         // what they come to, per token
   static constexpr int kStage = 2 * kPlane + kScales;
   static constexpr int kQPitch = DP * 2 + 16;
   static constexpr int kQ = kM * kQPitch + kM * 4;          // queries and factors, in the last slot before it is used
-  static constexpr int kSmem = (kStages - 1) * kStage + (kStage > kQ ? kStage : kQ);
+  static constexpr int kSmem = (kStages - 1) * kStage + (kStage > kQ ? kStage : kQ) + kTable;
+  static constexpr int kWarps = MT == 2 || !E4 ? 8 : 12;    // items per SM: registers, and shared memory for 16-bit rings
 };
 
 // One warp per item and nothing shared between warps: 8 to 12 items run on an
@@ -91,7 +93,7 @@ struct RowCfg {
 // Items: prefix (KV head, block of kM rows of all rows' queries, part), then
 // own (row, KV head, block, part).
 template <int CT, int DP, int MT>
-__global__ void __launch_bounds__(32) attn_rows_kernel(const __grid_constant__ AttnParams P, int pitems, int pblocks,
+__global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kernel(const __grid_constant__ AttnParams P, int pitems, int pblocks,
                                                        int oblocks) {
   using C = RowCfg<CT, DP, MT>;
   constexpr bool E4 = C::E4;
@@ -173,17 +175,12 @@ __global__ void __launch_bounds__(32) attn_rows_kernel(const __grid_constant__ A
   const bool col = pc * 16 < P.D * C::kEsz;
   const long long first = static_cast<long long>(t0 + row0) * ts + static_cast<long long>(g) * P.D * C::kEsz + (col ? pc * 16 : 0);
   const unsigned char *kp = kb + first, *vp = vb + first;
-  const long long step = ts * kStep;
-  // scale words: item i of 0 .. 2 kBlk - 1 is the keys' of token i, then the values'
-  constexpr int kWords = E4 ? 2 * kBlk / 32 : 1;
-  const unsigned char *sp[kWords] = {};
-  if constexpr (E4) {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const int w = i * 32 + lane;
-      sp[i] = (w < kBlk ? kb : vb) + static_cast<long long>(t0 + w % kBlk) * ts + static_cast<long long>(P.H) * P.D + (g & ~3);
-    }
-  }
+  const uint32_t step = static_cast<uint32_t>(ts) * kStep;  // fits: strides are below 2^27
+  const long long jump = ts * kBlk;
+  // scale words: lanes 0-15 the keys', 16-31 the values' of token lane % 16
+  const unsigned char *sp = nullptr;
+  if constexpr (E4)
+    sp = (lane < kBlk ? kb : vb) + static_cast<long long>(t0 + lane % kBlk) * ts + static_cast<long long>(P.H) * P.D + (g & ~3);
   if (P.D < DP) {  // the columns past the head vector stay zero: no copy writes them
     for (int i = lane; i < C::kStages * C::kStage / 16; i += 32) *reinterpret_cast<uint4 *>(smem + i * 16) = make_uint4(0, 0, 0, 0);
     __syncwarp();
@@ -192,24 +189,28 @@ __global__ void __launch_bounds__(32) attn_rows_kernel(const __grid_constant__ A
     if (blkno < nblk) {
       const uint32_t base = ring + st * C::kStage + row0 * C::kPitch + pc * 16;
       const int left = t1 - (t0 + blkno * kBlk);
-      if (col) {
+      if (left >= kBlk) {
+        if (col) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            cp_async16_zfill(base + i * kStep * C::kPitch, kp + static_cast<uint64_t>(step) * i, true);
+            cp_async16_zfill(base + C::kPlane + i * kStep * C::kPitch, vp + static_cast<uint64_t>(step) * i, true);
+          }
+        }
+      } else if (col) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const bool on = row0 + i * kStep < left;
-          cp_async16_zfill(base + i * kStep * C::kPitch, on ? kp : kb, on);
-          cp_async16_zfill(base + C::kPlane + i * kStep * C::kPitch, on ? vp : vb, on);
-          kp += step;
-          vp += step;
+          cp_async16_zfill(base + i * kStep * C::kPitch, on ? kp + static_cast<uint64_t>(step) * i : kb, on);
+          cp_async16_zfill(base + C::kPlane + i * kStep * C::kPitch, on ? vp + static_cast<uint64_t>(step) * i : vb, on);
         }
       }
+      kp += jump;
+      vp += jump;
       if constexpr (E4) {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          const int w = i * 32 + lane;
-          const bool on = w % kBlk < left;
-          cp_async4_zfill(ring + st * C::kStage + 2 * C::kPlane + w * 4, on ? sp[i] : kb, on);
-          sp[i] += ts * kBlk;
-        }
+        const bool on = lane % kBlk < left;
+        cp_async4_zfill(ring + st * C::kStage + 2 * C::kPlane + lane * 4, on ? sp : kb, on);
+        sp += jump;
       }
     }
     cp_async_commit();
@@ -378,35 +379,35 @@ __global__ void __launch_bounds__(32) attn_rows_kernel(const __grid_constant__ A
     bool small = false;
     float dE = 0.f;
     if constexpr (E4) {
-      float ks[kTt][2];
-      int top = -127;
-#pragma unroll
-      for (int n = 0; n < kTt; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int tk = n * 8 + 2 * j4 + c;
-          uint32_t kw, vw;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(sst + tk * 4) : "memory");
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(sst + (kBlk + tk) * 4) : "memory");
-          ks[n][c] = P.scale * e4m3_scale(kw >> (8 * (g & 3)) & 255u);
-          const uint32_t vc = vw >> (8 * (g & 3)) & 255u;
-          ve[n][c] = scale_exponent(vc);
-          if (vc != 255u) top = max(top, static_cast<int>(vc) - 127);
-        }
-      const float En = fmaxf(E, static_cast<float>(__reduce_max_sync(FULL_MASK, top)));
+      // lane i < 16: token i's key scale; lane 16 + i: its value scale
+      uint32_t w;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(sst + lane * 4) : "memory");
+      const uint32_t byte = w >> (8 * (g & 3)) & 255u;
+      const float e = scale_exponent(byte);
+      const float En = fmaxf(E, static_cast<float>(__reduce_max_sync(FULL_MASK, lane < kBlk || byte == 255u ? -127 : static_cast<int>(byte) - 127)));
       dE = En - E;
       E = En;
+      const bool low = lane >= kBlk && e < E - kExponentSpan;
+      small = __any_sync(FULL_MASK, low);
+      const float ec = low ? E - kExponentSpan : e;
+      const uint32_t tab = smem_u32(smem) + C::kSmem - C::kTable;
+      if (lane < kBlk)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(tab + lane * 16), "f"(P.scale * e4m3_scale(byte)) : "memory");
+      else
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(tab + (lane - kBlk) * 16 + 8), "f"(ec), "f"(low ? ex2(e - ec) : 1.f) : "memory");
+      __syncwarp();
+      float ks[kTt][2];
 #pragma unroll
       for (int n = 0; n < kTt; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float e = ve[n][c];
-          ve[n][c] = e < E - kExponentSpan ? E - kExponentSpan : e;
-          rest[n][c] = e < E - kExponentSpan ? ex2(e - ve[n][c]) : 1.f;
-          small = small || e < E - kExponentSpan;
+          float unused;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(ks[n][c]), "=f"(unused), "=f"(ve[n][c]), "=f"(rest[n][c])
+                       : "r"(tab + (n * 8 + 2 * j4 + c) * 16)
+                       : "memory");
           inv[n][c] = ex2(E - ve[n][c]);
         }
-      small = __any_sync(FULL_MASK, small);
       if (scaled) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -795,6 +796,8 @@ spec_status check_attention(const spec_attention_args *a) {
   if (a->N < 0 || a->N > SPEC_MAX_TREE_NODES || a->q_heads < 1 || a->q_heads % c.heads) return SPEC_ERR_SHAPE;
   if (static_cast<long long>(c.rows) * a->N >= 0x7fffffffLL / 256 / a->q_heads) return SPEC_ERR_SHAPE;
   if (c.slots > 0x7fffffffLL - 4096) return SPEC_ERR_SHAPE;
+  // the kernels step over a few tokens at a time in 32 bits
+  if (c.tok_stride >= 1LL << 27 || (a->prefix_len > 0 && a->prefix.tok_stride >= 1LL << 27)) return SPEC_ERR_SHAPE;
   for (int i = 0; i < 3; ++i)
     if (a->q_stride[i] < 0) return SPEC_ERR_SHAPE;
   if (!std::isfinite(a->scale)) return SPEC_ERR_ARG;
@@ -813,7 +816,7 @@ AttnPlan plan_attention(const spec_attention_args *a) {
   p.otile = a->N * G > 32;
   // rows kernel: 12 items per SM, no part under 64 tokens
   auto row_parts = [](long long blocks, long long tokens) {
-    const long long want = (12 * kSms + blocks - 1) / blocks;
+    const long long want = (8 * kSms + blocks - 1) / blocks;
     return static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 64})));
   };
   // tile kernel (one item per SM at a time): the fewest rounds of items times

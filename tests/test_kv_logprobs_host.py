@@ -155,6 +155,7 @@ def attention(L, c=None, pc=None, P_len=64, N=3, q_heads=16, q_dtype=BF16, scale
     (dict(pc=dict(dtype=BF16, tok=2048)), DTYPE), (dict(c=dict(rows=-1)), SHAPE), (dict(pc=dict(rows=0)), SHAPE),
     (dict(P_len=-1), SHAPE), (dict(P_len=65), SHAPE), (dict(pc=dict(heads=4)), SHAPE), (dict(N=-1), SHAPE),
     (dict(N=1025), SHAPE), (dict(q_heads=12), SHAPE), (dict(q_heads=0), SHAPE), (dict(q_heads=8 << 20), SHAPE),
+    (dict(c=dict(tok=1 << 27)), SHAPE), (dict(pc=dict(tok=1 << 27)), SHAPE),
     (dict(qs=(0, -1, 0)), SHAPE), (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG),
     (dict(c=dict(k=P + 8)), ALIGN), (dict(pc=dict(v=P + 8)), ALIGN), (dict(out=P + 8), ALIGN),
     (dict(q=P + 1), ALIGN), (dict(kv_len=P + 2), ALIGN), (dict(parent=P + 2), ALIGN), (dict(count=P + 1), ALIGN),
