@@ -47,6 +47,7 @@ struct AttnParams {
   int psplits, pchunk;  // prefix parts (slots 0 .. psplits - 1) and tokens in each
   int osplits;          // own parts (slots psplits ..)
   int chunk, min_chunk; // own parts: multiples of `chunk` tokens, `min_chunk` at least
+  int budget;           // > 0: cut the rows so that they make about this many parts (see part_length)
   int oblk;             // query rows per own item
   int32_t *oflag;       // per own item: a value that is not finite was left out of its sums
   // outputs
@@ -54,6 +55,7 @@ struct AttnParams {
   float *lse;
   int32_t *row_status;
   int qbf16;
+  int beside;  // the rows kernel runs beside the prefix's tile kernel
   int fuse;    // own items of the tile kernel take the prefix too
   int direct;  // ... and write the answers themselves: there is nothing to join
   uint64_t wait_limit_ns;
@@ -72,11 +74,28 @@ __device__ __forceinline__ int row_queries(const AttnParams &P, int b) {
   return c;
 }
 
+// The smallest length of a part (all lanes of a warp take part).  With a
+// budget of parts, rows of any lengths together make at most
+// sum ceil(len / c) <= sum len / c + B of them, so c = sum len / (budget - B)
+// keeps them within it: one round of items, none much longer than another.
+__device__ __forceinline__ int part_length(const AttnParams &P) {
+  if (P.budget <= 0) return P.min_chunk;
+  const int lane = threadIdx.x % 32;
+  uint32_t sum = 0;
+  for (int i = lane; i < P.B; i += 32) {
+    const long long n = static_cast<long long>(__ldg(P.kv_len + i)) + P.N;
+    sum += static_cast<uint32_t>(n < 0 ? 0 : n < P.slots ? n : P.slots) >> 4;  // in units of 16 tokens: B slots fit
+  }
+  sum = __reduce_add_sync(FULL_MASK, sum);
+  const uint32_t c = (sum + P.budget - P.B - 1) / (P.budget - P.B) * 16;
+  return max(P.min_chunk, static_cast<int>(min(c, 1u << 30) + P.chunk - 1) / P.chunk * P.chunk);
+}
+
 // The own part `split` covers of a row's len entries: equal parts, rounded up
-// to P.chunk tokens, none shorter than P.min_chunk but the last.
-__device__ __forceinline__ void own_range(const AttnParams &P, int len, int split, int &t0, int &t1) {
+// to P.chunk tokens, none shorter than `least` but the last.
+__device__ __forceinline__ void own_range(const AttnParams &P, int len, int split, int least, int &t0, int &t1) {
   int chunk = (len + P.osplits - 1) / P.osplits;
-  chunk = max(P.min_chunk, (chunk + P.chunk - 1) / P.chunk * P.chunk);
+  chunk = max(least, (chunk + P.chunk - 1) / P.chunk * P.chunk);
   const long long a = static_cast<long long>(split) * chunk;
   t0 = static_cast<int>(min(a, static_cast<long long>(len)));
   t1 = static_cast<int>(min(a + chunk, static_cast<long long>(len)));

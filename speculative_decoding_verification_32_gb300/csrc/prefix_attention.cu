@@ -90,11 +90,15 @@ struct RowCfg {
 // SM side by side, and while one starts or ends the others keep the memory
 // busy.  (Four warps on one item and a join in shared memory: 52 us where this
 // takes 35, 64 chains of 6 tokens over 33 K entries of 8 heads in bf16.)
-// Items: prefix (KV head, block of kM rows of all rows' queries, part), then
-// own (row, KV head, block, part).
+// Items: prefix (part, block of kM rows of all rows' queries, KV head), then
+// own (row, part, block, KV head).
 template <int CT, int DP, int MT>
 __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kernel(const __grid_constant__ AttnParams P, int pitems, int pblocks,
                                                        int oblocks) {
+  // Launched to run beside the prefix's tile kernel, which it has nothing to
+  // do with; its last item ends after that kernel, so that whoever waits for
+  // this grid has waited for both.
+  const bool last = P.beside && blockIdx.x == gridDim.x - 1;
   using C = RowCfg<CT, DP, MT>;
   constexpr bool E4 = C::E4;
   constexpr bool BF = CT == SPEC_BF16;
@@ -111,22 +115,23 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
   const bool pre = item < pitems;
   if (!pre) item -= pitems;
   int b = 0, g, blk, split;
+  // KV heads first: the heads of a token lie side by side in memory, so the
+  // items that run together read whole entries
+  g = item % P.H;
+  item /= P.H;
   if (pre) {
-    split = item % P.psplits;
-    item /= P.psplits;
     blk = item % pblocks;
-    g = item / pblocks;
+    split = item / pblocks;
   } else {
-    split = item % P.osplits;
-    item /= P.osplits;
     blk = item % oblocks;
     item /= oblocks;
-    g = item % P.H;
-    b = item / P.H;
+    split = item % P.osplits;
+    b = item / P.osplits;
   }
   const int r0 = blk * C::kM;              // first query row of the block
   const int nrows = (pre ? P.B : 1) * P.N * P.G;
   const int slot = pre ? split : P.psplits + split;
+  const long long flag = ((static_cast<long long>(b) * P.H + g) * oblocks + blk) * P.osplits + split;
   int t0, t1, len0 = 0, cnt = 0;           // tokens; own slots below len0 are seen by every query
   const unsigned char *kb, *vb;
   long long ts;
@@ -140,7 +145,7 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
     if (cnt <= 0)
       t0 = t1 = 0;
     else
-      own_range(P, len0 + cnt, split, t0, t1);
+      own_range(P, len0 + cnt, split, part_length(P), t0, t1);
     kb = P.k + b * P.row_stride, vb = P.v + b * P.row_stride, ts = P.tok_stride;
     if (split == 0 && blk == 0 && g == 0 && lane == 0 && P.row_status)
       P.row_status[b] = cnt >= 0 ? 0 : cnt == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
@@ -161,8 +166,9 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
     }
   }
   if (t0 >= t1) {  // nothing here (an empty part, or a row that cannot be used)
-    if (!pre && lane == 0) P.oflag[blockIdx.x - pitems] = 0;
+    if (!pre && lane == 0) P.oflag[flag] = 0;
     if (my_row >= 0) P.ml[static_cast<long long>(slot) * P.rows + my_row] = make_float2(-INFINITY, -INFINITY);
+    if (last) grid_dependency_wait();
     return;
   }
 
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
   }
   cp_async_wait_all();
 
-  if (!pre && lane == 0) P.oflag[blockIdx.x - pitems] = odd;
+  if (!pre && lane == 0) P.oflag[flag] = odd;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -646,6 +652,7 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
           if (n * 8 < P.D) *reinterpret_cast<float2 *>(to + n * 8 + 2 * j4) = make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
       }
     }
+  if (last) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------- join
@@ -751,8 +758,23 @@ cudaError_t launch_rows(const AttnParams &p, bool own, bool prefix, cudaStream_t
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<attn_rows_kernel<CT, DP, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  attn_rows_kernel<CT, DP, MT><<<static_cast<unsigned>(items), 32, C::kSmem, s>>>(p, static_cast<int>(pitems), pblocks, oblocks);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items));
+  cfg.blockDim = dim3(32);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_rows_kernel<CT, DP, MT>, p, static_cast<int>(pitems), pblocks, oblocks);
+}
+
+// Items of the rows kernel that run on an SM at a time.
+int rows_per_sm(int dtype, int oblk) {
+  if (dtype == SPEC_E4M3) return oblk == 16 ? RowCfg<SPEC_E4M3, 128, 1>::kWarps : RowCfg<SPEC_E4M3, 128, 2>::kWarps;
+  return oblk == 16 ? RowCfg<SPEC_BF16, 128, 1>::kWarps : RowCfg<SPEC_BF16, 128, 2>::kWarps;
 }
 
 // 16 query rows an item where no item would use more (half the sums and
@@ -767,7 +789,7 @@ cudaError_t launch_rows_d(const AttnParams &p, bool own, bool prefix, cudaStream
 }
 
 struct AttnPlan {
-  int psplits, pchunk, osplits, min_chunk, W;
+  int psplits, pchunk, osplits, min_chunk, budget, W;
   bool ptile, otile;  // attn_tile_kernel for the prefix, for the own entries
   bool fuse, direct;  // own items take the prefix too; and nothing is left to join
   int oblk;           // query rows per own item
@@ -849,10 +871,16 @@ AttnPlan plan_attention(const spec_attention_args *a) {
   p.osplits = p.otile ? tile_parts(oitems, c.slots + (p.fuse ? a->prefix_len : 0)) : row_parts(oitems, c.slots);
   p.min_chunk = p.otile ? 128 : 64;
   if (!p.otile && oitems >= 2 * kSms) {
-    // rows differ in length: parts of 256 tokens keep a long row from holding
-    // up the rest, up to 24 items per SM (most of them empty if rows are short)
-    p.osplits = static_cast<int>(std::max<long long>(1, std::min<long long>((c.slots + 255) / 256, 24 * kSms / oitems)));
-    p.min_chunk = 256;
+    // rows differ in length: cut so that all parts run side by side and none
+    // is much longer than the rest (part_length); a grid of up to 24 items per
+    // SM leaves most empty
+    p.osplits = static_cast<int>(std::max<long long>(1, std::min<long long>((c.slots + 63) / 64, 24 * kSms / oitems)));
+    p.min_chunk = 64;
+    const long long budget = rows_per_sm(c.dtype, p.oblk) * kSms / (c.heads * oblocks);
+    if (budget > c.rows)
+      p.budget = static_cast<int>(budget);
+    else
+      p.osplits = 1;
   }
   p.direct = p.otile && p.osplits == 1 && p.psplits == 0;
   p.W = (a->N + 31) / 32;
@@ -943,6 +971,7 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   p.osplits = plan.osplits;
   p.chunk = plan.otile ? 128 : 64;
   p.min_chunk = plan.min_chunk;
+  p.budget = plan.budget;
   p.oblk = plan.oblk;
   p.fuse = plan.fuse;
   p.oflag = reinterpret_cast<int32_t *>(w + plan.flag_at);
@@ -969,6 +998,7 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
     if (plan.direct) return SPEC_OK;
     p.direct = 0;
   }
+  p.beside = prefix && plan.ptile && !plan.otile;
   if ((!plan.otile || (prefix && !plan.ptile)) &&
       launch_attn_rows(p, c.dtype, !plan.otile, prefix && !plan.ptile, s) != cudaSuccess)
     return SPEC_ERR_CUDA;
