@@ -47,7 +47,8 @@ struct AttnParams {
   int psplits, pchunk;  // prefix parts (slots 0 .. psplits - 1) and tokens in each
   int osplits;          // own parts (slots psplits ..)
   int chunk, min_chunk; // own parts: multiples of `chunk` tokens, `min_chunk` at least
-  int budget;           // > 0: cut the rows so that they make about this many parts (see part_length)
+  int budget;           // > 0: the rows are cut into at most this many parts (cut_rows) ...
+  int32_t *nparts;      // ... each into this many (else osplits)
   int oblk;             // query rows per own item
   int32_t *oflag;       // per own item: a value that is not finite was left out of its sums
   // outputs
@@ -74,28 +75,82 @@ __device__ __forceinline__ int row_queries(const AttnParams &P, int b) {
   return c;
 }
 
-// The smallest length of a part (all lanes of a warp take part).  With a
-// budget of parts, rows of any lengths together make at most
-// sum ceil(len / c) <= sum len / c + B of them, so c = sum len / (budget - B)
-// keeps them within it: one round of items, none much longer than another.
-__device__ __forceinline__ int part_length(const AttnParams &P) {
-  if (P.budget <= 0) return P.min_chunk;
+// How a few rows of any lengths are cut into at most `budget` parts that can all
+// run side by side, none much longer than another (the lanes of a warp together):
+// item `idx` is part `split` of row `b`, tokens t0 .. t1 - 1.  A lane keeps rows
+// 4 lane .. 4 lane + 3.  Lengths count in blocks of 16 tokens (w); a row makes
+// max(1, ceil(w / c)) parts of c blocks, and c is the shortest length, searched
+// upwards from sum w / budget, at which the budget holds: it does for
+// c = sum w / (budget - B) + 1, since sum ceil(w / c) <= sum w / c + B.
+constexpr int kKeep = 4;
+constexpr int kMaxCutRows = 32 * kKeep;
+__device__ __forceinline__ void cut_rows(const AttnParams &P, int idx, int &b, int &split, int &parts, int &t0, int &t1) {
   const int lane = threadIdx.x % 32;
-  uint32_t sum = 0;
-  for (int i = lane; i < P.B; i += 32) {
-    const long long n = static_cast<long long>(__ldg(P.kv_len + i)) + P.N;
-    sum += static_cast<uint32_t>(n < 0 ? 0 : n < P.slots ? n : P.slots) >> 4;  // in units of 16 tokens: B slots fit
+  uint32_t w[kKeep], sum = 0, top = 0;
+#pragma unroll
+  for (int q = 0; q < kKeep; ++q) {
+    const int r = lane * kKeep + q;
+    w[q] = 0;
+    if (r < P.B) {
+      const int c = row_queries(P, r);
+      if (c > 0) w[q] = static_cast<uint32_t>(__ldg(P.kv_len + r) + c + 15) / 16;
+    }
+    sum += w[q];
+    top = max(top, w[q]);
   }
   sum = __reduce_add_sync(FULL_MASK, sum);
-  const uint32_t c = (sum + P.budget - P.B - 1) / (P.budget - P.B) * 16;
-  return max(P.min_chunk, static_cast<int>(min(c, 1u << 30) + P.chunk - 1) / P.chunk * P.chunk);
+  top = __reduce_max_sync(FULL_MASK, top);
+  const uint32_t least = max((top + P.osplits - 1) / P.osplits, static_cast<uint32_t>(P.min_chunk / 16));
+  const uint32_t most = sum / (P.budget - P.B) + 1;
+  uint32_t c = sum / P.budget + 1, n[kKeep], mine;
+  while (true) {
+    c = max(min(c, most), least);
+    mine = 0;
+#pragma unroll
+    for (int q = 0; q < kKeep; ++q) {
+      n[q] = lane * kKeep + q < P.B ? max(1u, (w[q] + c - 1) / c) : 0u;
+      mine += n[q];
+    }
+    if (c >= most || __reduce_add_sync(FULL_MASK, mine) <= static_cast<uint32_t>(P.budget)) break;
+    c += c / 16 + 1;
+  }
+  // the row of item idx: inclusive sums over the lanes
+  uint32_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(FULL_MASK, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const uint32_t from = upto - mine;
+  const unsigned owner = __ballot_sync(FULL_MASK, static_cast<uint32_t>(idx) >= from && static_cast<uint32_t>(idx) < upto);
+  b = -1;
+  if (!owner) return;  // past the last part
+  uint32_t k = idx - from;
+  int row = lane * kKeep, cnt = 0, blocks = 0;
+#pragma unroll
+  for (int q = 0; q < kKeep; ++q) {
+    if (q < kKeep - 1 && row == lane * kKeep + q && k >= n[q]) {
+      k -= n[q];
+      ++row;
+    } else if (row == lane * kKeep + q) {
+      cnt = static_cast<int>(n[q]);
+      blocks = static_cast<int>(w[q]);
+    }
+  }
+  const int src = __ffs(owner) - 1;
+  b = __shfl_sync(FULL_MASK, row, src);
+  split = __shfl_sync(FULL_MASK, static_cast<int>(k), src);
+  parts = __shfl_sync(FULL_MASK, cnt, src);
+  blocks = __shfl_sync(FULL_MASK, blocks, src);
+  t0 = min(split * static_cast<int>(c), blocks) * 16;
+  t1 = min(t0 + static_cast<int>(c) * 16, blocks * 16);  // the last part's end is the row's, which the caller knows
 }
 
 // The own part `split` covers of a row's len entries: equal parts, rounded up
-// to P.chunk tokens, none shorter than `least` but the last.
-__device__ __forceinline__ void own_range(const AttnParams &P, int len, int split, int least, int &t0, int &t1) {
+// to P.chunk tokens (a power of two), none shorter than P.min_chunk but the last.
+__device__ __forceinline__ void own_range(const AttnParams &P, int len, int split, int &t0, int &t1) {
   int chunk = (len + P.osplits - 1) / P.osplits;
-  chunk = max(least, (chunk + P.chunk - 1) / P.chunk * P.chunk);
+  chunk = max(P.min_chunk, (chunk + P.chunk - 1) & -P.chunk);
   const long long a = static_cast<long long>(split) * chunk;
   t0 = static_cast<int>(min(a, static_cast<long long>(len)));
   t1 = static_cast<int>(min(a + chunk, static_cast<long long>(len)));

@@ -90,15 +90,16 @@ struct RowCfg {
 // SM side by side, and while one starts or ends the others keep the memory
 // busy.  (Four warps on one item and a join in shared memory: 52 us where this
 // takes 35, 64 chains of 6 tokens over 33 K entries of 8 heads in bf16.)
-// Items: prefix (part, block of kM rows of all rows' queries, KV head), then
-// own (row, part, block, KV head).
+// Items: x: KV head and block of kM query rows, y: part, z: row (or, cut by a
+// budget, y: a part of any row, z: 0), or one past the last for the prefix (whose
+// query rows are those of all rows).
 template <int CT, int DP, int MT>
-__global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kernel(const __grid_constant__ AttnParams P, int pitems, int pblocks,
-                                                       int oblocks) {
+__global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kernel(const __grid_constant__ AttnParams P, int own,
+                                                                                   int pblocks, int oblocks) {
   // Launched to run beside the prefix's tile kernel, which it has nothing to
   // do with; its last item ends after that kernel, so that whoever waits for
   // this grid has waited for both.
-  const bool last = P.beside && blockIdx.x == gridDim.x - 1;
+  const bool last = P.beside && blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z;
   using C = RowCfg<CT, DP, MT>;
   constexpr bool E4 = C::E4;
   constexpr bool BF = CT == SPEC_BF16;
@@ -110,29 +111,25 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
   float *const qfac = reinterpret_cast<float *>(qsm + C::kM * C::kQPitch);
   const int lane = threadIdx.x, quad = lane / 4, j4 = lane % 4;
 
-  // --- the item
-  int item = blockIdx.x;
-  const bool pre = item < pitems;
-  if (!pre) item -= pitems;
-  int b = 0, g, blk, split;
-  // KV heads first: the heads of a token lie side by side in memory, so the
-  // items that run together read whole entries
-  g = item % P.H;
-  item /= P.H;
-  if (pre) {
-    blk = item % pblocks;
-    split = item / pblocks;
-  } else {
-    blk = item % oblocks;
-    item /= oblocks;
-    split = item % P.osplits;
-    b = item / P.osplits;
+  // --- the item: KV heads first (the heads of a token lie side by side in
+  // memory, so the items that run together read whole entries), then parts
+  int b = blockIdx.z, split = blockIdx.y;
+  const int blk = blockIdx.x / static_cast<unsigned>(P.H), g = blockIdx.x - blk * P.H;
+  const bool pre = b >= own;  // the prefix's items come after those of the `own` rows
+  int t0 = 0, t1 = 0, len0 = 0, cnt = 0;   // tokens; own slots below len0 are seen by every query
+  if (!pre && P.budget > 0) {
+    int parts;
+    cut_rows(P, split, b, split, parts, t0, t1);
+    if (b >= 0 && split == 0 && blk == 0 && g == 0 && lane == 0) P.nparts[b] = parts;
+  }
+  if (b < 0 || blk >= (pre ? pblocks : oblocks) || split >= (pre ? P.psplits : P.osplits)) {  // the grid is a box
+    if (last) grid_dependency_wait();
+    return;
   }
   const int r0 = blk * C::kM;              // first query row of the block
   const int nrows = (pre ? P.B : 1) * P.N * P.G;
   const int slot = pre ? split : P.psplits + split;
   const long long flag = ((static_cast<long long>(b) * P.H + g) * oblocks + blk) * P.osplits + split;
-  int t0, t1, len0 = 0, cnt = 0;           // tokens; own slots below len0 are seen by every query
   const unsigned char *kb, *vb;
   long long ts;
   if (pre) {
@@ -144,8 +141,10 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
     len0 = __ldg(P.kv_len + b);
     if (cnt <= 0)
       t0 = t1 = 0;
+    else if (P.budget > 0)
+      t1 = min(t1, len0 + cnt);
     else
-      own_range(P, len0 + cnt, split, part_length(P), t0, t1);
+      own_range(P, len0 + cnt, split, t0, t1);
     kb = P.k + b * P.row_stride, vb = P.v + b * P.row_stride, ts = P.tok_stride;
     if (split == 0 && blk == 0 && g == 0 && lane == 0 && P.row_status)
       P.row_status[b] = cnt >= 0 ? 0 : cnt == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
@@ -541,29 +540,29 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
     // does not see them would get 0 * NaN.  They are taken out here and put
     // into the answers of the queries that see them when the parts are joined.
     if (masked && !pre) {
-      const int per = P.D * C::kEsz / 4;  // words of a head vector
       bool bad = false;
-      for (int i = lane; i < kBlk * per; i += 32) {
-        const int tk = i / per;
-        if (tb + tk < len0) continue;
-        const uint32_t at = vst + tk * C::kPitch + (i - tk * per) * 4;
-        uint32_t w;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
-        uint32_t r = w;
-        if constexpr (E4) {
+      for (int tk = max(0, len0 - tb); tk < min(kBlk, t1 - tb); ++tk)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if ((w >> (8 * c) & 127u) == 127u) r &= ~(255u << (8 * c));
-        } else {
-          constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
-          if ((w & top) == top) r &= 0xffff0000u;
-          if ((w >> 16 & top) == top) r &= 0x0000ffffu;
+        for (int i = 0; i < (DP * C::kEsz + 127) / 128; ++i) {  // words of a head vector
+          if ((i * 32 + lane) * 4 >= P.D * C::kEsz) continue;
+          const uint32_t at = vst + tk * C::kPitch + (i * 32 + lane) * 4;
+          uint32_t w;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+          uint32_t r = w;
+          if constexpr (E4) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if ((w >> (8 * c) & 127u) == 127u) r &= ~(255u << (8 * c));
+          } else {
+            constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
+            if ((w & top) == top) r &= 0xffff0000u;
+            if ((w >> 16 & top) == top) r &= 0x0000ffffu;
+          }
+          if (r != w) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(r) : "memory");
+            bad = true;
+          }
         }
-        if (r != w) {
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(r) : "memory");
-          bad = true;
-        }
-      }
       odd = __any_sync(FULL_MASK, bad) || odd;
       __syncwarp();
     }
@@ -661,13 +660,14 @@ template <int CT, bool BF>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams P) {
   const int lane = threadIdx.x % 32;
   const long long r = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
-  const int nslots = P.psplits + P.osplits;
+  int nslots = P.psplits + P.osplits;
   const int b = static_cast<int>(r / (static_cast<long long>(P.N) * P.Hq));
   int n = 0;
   if (r < P.rows && !P.rowinfo) n = row_queries(P, b);  // inputs: no need to wait for the kernels before
   grid_dependency_wait();
   if (r >= P.rows) return;
   if (P.rowinfo) n = row_queries(P, b);
+  if (P.budget > 0) nslots = P.psplits + P.nparts[b];
   const int qt = static_cast<int>(r / P.Hq) - b * P.N, h = static_cast<int>(r % P.Hq);
   const bool on = qt < n;
   float Z = -INFINITY;
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int g = h / P.G, blocks = (P.N * P.G + P.oblk - 1) / P.oblk;
     const int32_t *flag = P.oflag + ((static_cast<long long>(b) * P.H + g) * blocks + (qt * P.G + h % P.G) / P.oblk) * P.osplits;
     bool odd = false;
-    for (int s = lane; s < P.osplits; s += 32) odd = odd || flag[s];
+    for (int s = lane; s < nslots - P.psplits; s += 32) odd = odd || flag[s];
     if (__any_sync(FULL_MASK, odd)) {
       const int len0 = P.kv_len[b];
       for (int j = 0; j < n; ++j) {
@@ -753,13 +753,13 @@ cudaError_t launch_rows(const AttnParams &p, bool own, bool prefix, cudaStream_t
   using C = RowCfg<CT, DP, MT>;
   const int pblocks = static_cast<int>((static_cast<long long>(p.B) * p.N * p.G + C::kM - 1) / C::kM);
   const int oblocks = (p.N * p.G + C::kM - 1) / C::kM;
-  const long long pitems = prefix ? static_cast<long long>(p.H) * pblocks * p.psplits : 0;
-  const long long items = pitems + (own ? static_cast<long long>(p.B) * p.H * oblocks * p.osplits : 0);
-  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int blocks = std::max(own ? oblocks : 0, prefix ? pblocks : 0);
+  const int zown = !own ? 0 : p.budget > 0 ? 1 : p.B;
+  const dim3 grid(p.H * blocks, std::max(!own ? 1 : p.budget > 0 ? p.budget : p.osplits, prefix ? p.psplits : 1), zown + (prefix ? 1 : 0));
   const cudaError_t e = allow_smem<attn_rows_kernel<CT, DP, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(32);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -768,7 +768,7 @@ cudaError_t launch_rows(const AttnParams &p, bool own, bool prefix, cudaStream_t
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = p.beside ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_rows_kernel<CT, DP, MT>, p, static_cast<int>(pitems), pblocks, oblocks);
+  return cudaLaunchKernelEx(&cfg, attn_rows_kernel<CT, DP, MT>, p, zown, pblocks, oblocks);
 }
 
 // Items of the rows kernel that run on an SM at a time.
@@ -793,7 +793,7 @@ struct AttnPlan {
   bool ptile, otile;  // attn_tile_kernel for the prefix, for the own entries
   bool fuse, direct;  // own items take the prefix too; and nothing is left to join
   int oblk;           // query rows per own item
-  size_t rows, anc_at, info_at, flag_at, ml_at, part_at, bytes;
+  size_t rows, anc_at, info_at, flag_at, count_at, ml_at, part_at, bytes;
 };
 
 size_t at_round(size_t x) { return (x + 255) / 256 * 256; }
@@ -871,16 +871,14 @@ AttnPlan plan_attention(const spec_attention_args *a) {
   p.osplits = p.otile ? tile_parts(oitems, c.slots + (p.fuse ? a->prefix_len : 0)) : row_parts(oitems, c.slots);
   p.min_chunk = p.otile ? 128 : 64;
   if (!p.otile && oitems >= 2 * kSms) {
-    // rows differ in length: cut so that all parts run side by side and none
-    // is much longer than the rest (part_length); a grid of up to 24 items per
-    // SM leaves most empty
-    p.osplits = static_cast<int>(std::max<long long>(1, std::min<long long>((c.slots + 63) / 64, 24 * kSms / oitems)));
-    p.min_chunk = 64;
+    // Rows differ in length.  A few rows are cut by a budget of parts so that
+    // all items run side by side; for many, whole rows balance well enough.
     const long long budget = rows_per_sm(c.dtype, p.oblk) * kSms / (c.heads * oblocks);
-    if (budget > c.rows)
+    p.osplits = 1;
+    if (c.rows <= kMaxCutRows && budget > c.rows) {
       p.budget = static_cast<int>(budget);
-    else
-      p.osplits = 1;
+      p.osplits = static_cast<int>(std::min<long long>({(c.slots + 63) / 64, budget / c.rows * 4, 64}));
+    }
   }
   p.direct = p.otile && p.osplits == 1 && p.psplits == 0;
   p.W = (a->N + 31) / 32;
@@ -891,6 +889,8 @@ AttnPlan plan_attention(const spec_attention_args *a) {
   at += at_round(static_cast<size_t>(c.rows) * 4);
   p.flag_at = at;
   at += at_round(static_cast<size_t>(c.rows) * c.heads * oblocks * p.osplits * 4);
+  p.count_at = at;
+  at += at_round(static_cast<size_t>(c.rows) * 4);
   p.ml_at = at;
   const size_t slots = static_cast<size_t>(p.psplits) + p.osplits;
   at += at_round(slots * p.rows * sizeof(float2));
@@ -972,6 +972,7 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   p.chunk = plan.otile ? 128 : 64;
   p.min_chunk = plan.min_chunk;
   p.budget = plan.budget;
+  p.nparts = reinterpret_cast<int32_t *>(w + plan.count_at);
   p.oblk = plan.oblk;
   p.fuse = plan.fuse;
   p.oflag = reinterpret_cast<int32_t *>(w + plan.flag_at);

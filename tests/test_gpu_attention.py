@@ -152,9 +152,9 @@ class Problem:
         return self.sv.spec_prefix_attention(self.q, self.cache, i32(self.lens), prefix=self.prefix, prefix_len=self.P or None,
                                              parent=i32(self.parent), count=i32(self.count), kv_heads=self.H, **kw)
 
-    def check(self, rows=None):
+    def check(self, rows=None, status=None):
         out, lse, st = self.call()
-        assert st.tolist() == [0] * self.B
+        assert st.tolist() == (status or [0] * self.B)
         got, lg = out.cpu().double().numpy(), lse.cpu().double().numpy()
         again, lse2, _ = self.call()
         assert np.array_equal(got, again.cpu().double().numpy(), equal_nan=True)
@@ -443,3 +443,23 @@ def test_trees_that_need_no_join(sv, kind, qt, P, D):
         sv.set_wait_timeout_ns(limit)
     want[torch.from_numpy(count > 0) & (want == 0)] = 6
     assert torch.equal(st.cpu(), want) and float(out.abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("kind,qt", KINDS)
+@pytest.mark.parametrize("B,N,Hq,H,D,P,top", [(64, 1, 32, 8, 64, 500, 700), (100, 2, 8, 4, 128, 0, 300), (128, 3, 12, 4, 64, 70, 40),
+                                             (32, 1, 16, 16, 64, 200, 2000)])
+def test_rows_cut_by_a_budget(sv, kind, qt, B, N, Hq, H, D, P, top):
+    """Enough rows that they are cut into parts by their lengths: very uneven ones, empty ones, unused ones."""
+    rng = np.random.default_rng(B)
+    lens = (top * rng.random(B)**3).astype(np.int32)
+    lens[3], lens[7], lens[B - 1] = top, 0, 1
+    count = rng.integers(0, N + 1, B)
+    count[:2], count[3], count[B - 1] = 0, N, N
+    p = Problem(sv, B, N, Hq, H, D, P, lens, kind, qt, count=count, seed=B)
+    p.check(rows=[0, 2, 3, 7, 8, B // 2, B - 2, B - 1])
+    # rows that cannot be used change the cut of the others, so their last bits, and nothing more
+    p.lens[5], p.count[6] = -7, N + 1
+    bad = [5, 6]
+    out, lse = p.check(rows=[2, 3, 7, 8, B - 1], status=[8 if b in bad else 0 for b in range(B)])
+    assert bool((lse[bad] == float("-inf")).all())
+    assert float(out[bad].abs().max()) == 0.0
