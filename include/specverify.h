@@ -610,10 +610,9 @@ spec_status spec_prefix_attention(const spec_attention_args *args, void *out, fl
  * may be NULL).  status [B, npos]: SPEC_ROW_* per position (NONFINITE: a NaN
  * or +inf logit; EMPTY: no finite logit; BAD_TOKEN: outside [-1, V);
  * BAD_TEMPERATURE); a flagged position's floats are NaN and its ids -1.
- * B * npos < 2^31 / 64.  Workspace: spec_token_logprobs_workspace_size bytes;
- * nothing in it is kept between calls.  Two kernels: one pass over the logits
- * that also keeps the largest of every 32 (bf16) or 16 (fp32) of them, then
- * one CTA per position.
+ * B * npos < 2^31 / 64.  One launch, no workspace: each position's CTAs pass over
+ * its logits once, keep the largest of every 32 (bf16) or 16 (fp32) of them, and
+ * look again only at those that can hold one of the top m.
  */
 typedef struct {
   int32_t B, npos, V;
@@ -634,11 +633,8 @@ typedef struct {
   int32_t *status;           /* [B, npos] */
 } spec_logprobs_out;
 
-/* Bytes of workspace (any dtype, any m).  0 on invalid sizes. */
-size_t spec_token_logprobs_workspace_size(int32_t B, int32_t npos, int32_t V);
-
 spec_status spec_token_logprobs(const spec_logprobs_args *args, const spec_logprobs_out *out,
-                                void *ws, size_t ws_bytes, void *stream);
+                                void *stream);
 
 /* Zero-fill a workspace on `stream` (a cudaMemsetAsync).  Optional: the
  * verify calls do not need a zeroed workspace. */

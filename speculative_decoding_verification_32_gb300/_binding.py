@@ -163,10 +163,7 @@ def _bind(L):
     L.spec_prefix_attention_workspace_size.restype = sz
     L.spec_prefix_attention.argtypes = [_c.POINTER(SpecAttentionArgs), _P, _P, _P, _P, sz, _P]
     L.spec_prefix_attention.restype = _c.c_int
-    L.spec_token_logprobs_workspace_size.argtypes = [i32, i32, i32]
-    L.spec_token_logprobs_workspace_size.restype = sz
-    L.spec_token_logprobs.argtypes = [_c.POINTER(SpecLogprobsArgs), _c.POINTER(SpecLogprobsOut),
-                                      _P, sz, _P]
+    L.spec_token_logprobs.argtypes = [_c.POINTER(SpecLogprobsArgs), _c.POINTER(SpecLogprobsOut), _P]
     L.spec_token_logprobs.restype = _c.c_int
     L.spec_workspace_init.argtypes = [_P, sz, _P]
     L.spec_workspace_init.restype = _c.c_int
@@ -511,11 +508,6 @@ def spec_kv_entry_bytes(heads, head_dim, dtype=torch.uint8):
     return n
 
 
-@functools.lru_cache(maxsize=4096)
-def _logprobs_bytes(B, npos, V):
-    return lib().spec_token_logprobs_workspace_size(B, npos, V)
-
-
 def _kv_cache(cache, heads, head_dim, dev, name):
     """The fields of a cache tensor's C descriptor: [2, rows, slots, heads,
     head_dim] bfloat16 / float16, or [2, rows, slots, entry bytes] uint8 (e4m3)."""
@@ -710,9 +702,7 @@ def spec_token_logprobs(logits, tokens=None, temperature=None, m=0, stream=None)
         o = _PACK_LOGPROBS_OUT.pack(out["logprob"].data_ptr() if tokens is not None else 0,
                                     out["entropy"].data_ptr(), out["top_ids"].data_ptr(),
                                     out["top_logprobs"].data_ptr(), out["status"].data_ptr())
-        s = _raw_stream(dev.index)
-        ws = _scratch(dev, s, _logprobs_bytes(B, npos, V))
-        _check(_fn("spec_token_logprobs", 5)(a, o, ws.data_ptr(), ws.numel(), s))
+        _check(_fn("spec_token_logprobs", 3)(a, o, _raw_stream(dev.index)))
     return out
 
 

@@ -56,7 +56,6 @@ struct AttnParams {
   float *lse;
   int32_t *row_status;
   int qbf16;
-  int beside;  // the rows kernel runs beside the prefix's tile kernel
   int fuse;    // own items of the tile kernel take the prefix too
   int direct;  // ... and write the answers themselves: there is nothing to join
   uint64_t wait_limit_ns;
@@ -84,6 +83,12 @@ __device__ __forceinline__ int row_queries(const AttnParams &P, int b) {
 // c = sum w / (budget - B) + 1, since sum ceil(w / c) <= sum w / c + B.
 constexpr int kKeep = 4;
 constexpr int kMaxCutRows = 32 * kKeep;
+// ceil(w / c) for w < 2^24: the quotient by a reciprocal, put right by one
+__device__ __forceinline__ uint32_t ceil_quotient(uint32_t w, uint32_t c, float inv) {
+  uint32_t q = static_cast<uint32_t>(static_cast<float>(w) * inv);
+  if (q * c >= w + c) --q;  // one too many
+  return q + (q * c < w);
+}
 __device__ __forceinline__ void cut_rows(const AttnParams &P, int idx, int &b, int &split, int &parts, int &t0, int &t1) {
   const int lane = threadIdx.x % 32;
   uint32_t w[kKeep], sum = 0, top = 0;
@@ -93,7 +98,7 @@ __device__ __forceinline__ void cut_rows(const AttnParams &P, int idx, int &b, i
     w[q] = 0;
     if (r < P.B) {
       const int c = row_queries(P, r);
-      if (c > 0) w[q] = static_cast<uint32_t>(__ldg(P.kv_len + r) + c + 15) / 16;
+      if (c > 0) w[q] = static_cast<uint32_t>(__ldg(P.kv_len + r) + c + 15) / 16;  // < 2^24 blocks (checked by the caller)
     }
     sum += w[q];
     top = max(top, w[q]);
@@ -106,9 +111,10 @@ __device__ __forceinline__ void cut_rows(const AttnParams &P, int idx, int &b, i
   while (true) {
     c = max(min(c, most), least);
     mine = 0;
+    const float inv = 1.f / static_cast<float>(c);
 #pragma unroll
     for (int q = 0; q < kKeep; ++q) {
-      n[q] = lane * kKeep + q < P.B ? max(1u, (w[q] + c - 1) / c) : 0u;
+      n[q] = lane * kKeep + q < P.B ? max(1u, ceil_quotient(w[q], c, inv)) : 0u;
       mine += n[q];
     }
     if (c >= most || __reduce_add_sync(FULL_MASK, mine) <= static_cast<uint32_t>(P.budget)) break;

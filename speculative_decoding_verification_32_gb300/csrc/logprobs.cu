@@ -7,16 +7,18 @@
 // (max, S, U) of two parts join by shifting to the larger max, so one pass
 // over the logits is enough; its HBM read is what bounds the call.
 //
-//  logprobs_stream_kernel -- one CTA per slice of 256 x 4 16-byte vectors of a
-//    position: every thread loads its four vectors at once (64 KB in flight
-//    on an SM at 4 CTAs), takes the largest of its 32 bf16 or 16 fp32 logits,
-//    its own S and U against that, and the CTA joins the threads'.  The
-//    thread maxima are kept as 16-bit order keys (1/32 of the bf16 traffic):
-//  logprobs_pick_kernel -- one CTA per position joins the slices' records and
-//    finds the top m without reading the logits again: the m-th largest of
-//    the chunk keys is a lower bound of the m-th largest logit's key, so only
-//    the few chunks that reach it are looked at.  Positions where that leaves
-//    too many (masses of equal logits) are searched whole.
+// One kernel: a cluster of 1 to 8 CTAs per position (few positions are spread
+// over the SMs, many take a CTA each).  A CTA runs through its slices of
+// 256 x 4 16-byte vectors with the next slice's loads on their way; a thread
+// takes the largest of its 32 bf16 or 16 fp32 logits (a chunk), its S and U
+// against the largest so far, and leaves the chunk's maximum as a 16-bit order
+// key in shared memory.  The CTAs' records join through distributed shared
+// memory.  The top m are found without reading the position again: the m-th
+// largest of the 256 threads' maxima is a lower bound of the m-th largest
+// logit's key, and only the few chunks that reach it are looked at.  Positions
+// where that leaves too many (masses of equal logits) are searched whole.
+// While one position's CTAs are at that, others keep the memory busy: with a
+// second kernel for it, 224 positions of 128256 bf16 logits took 23 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -33,8 +35,9 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.442695040888963407f;
 // 2^-200 is zero in fp32: stands in for the y of a masked logit, so that y 2^y is 0 and not NaN
 constexpr float kFloorY = -200.f;
-constexpr int kLpChunks = 1024;  // candidate chunks the pick kernel lists
+constexpr int kLpChunks = 1024;  // candidate chunks a CTA lists
 constexpr int kLpCands = 1024;   // candidate logits it ranks
+constexpr int kLpMaxCluster = 8;
 
 struct LpPart {
   float m, s, u;
@@ -47,12 +50,9 @@ struct LpParams {
   const float *temperature;
   float *logprob, *entropy, *top_logprobs;
   int32_t *top_ids, *status;
-  LpPart *part;          // [rows * nparts]
-  unsigned short *cmax;  // [rows * nslices * kLpThreads]
   long long row_stride;
   int rows, npos, V, m, slice, nslices;
-  int run, nparts;       // slices per stream item, records per position
-  int vec;               // rows are 16-byte aligned
+  int run;               // slices per CTA
 };
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -128,29 +128,85 @@ struct LpSlice {
   }
 };
 
-// Item: position r, slices sl0 .. sl0 + P.run - 1 of it.  The next slice's
-// loads are on their way while a slice is worked on.
-template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kLpThreads, 4) logprobs_stream_kernel(const __grid_constant__ LpParams P) {
+// Sum over the CTA of one int per thread (all threads get it).
+__device__ __forceinline__ int block_sum(int v, int *sh) {
+  v = __reduce_add_sync(FULL_MASK, v);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
+  __syncthreads();
+  int t = 0;
+#pragma unroll
+  for (int w = 0; w < kLpThreads / 32; ++w) t += sh[w];
+  return t;
+}
+
+__device__ __forceinline__ LpPart ld_remote_part(const LpPart *p, uint32_t rank) {
+  const float4 v = ld_dsmem_f4(dsmem_addr(p, rank));
+  return LpPart{v.x, v.y, v.z, __float_as_uint(v.w)};
+}
+__device__ __forceinline__ uint32_t ld_remote_u32(const void *p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(dsmem_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned long long ld_remote_u64(const void *p, uint32_t rank) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(dsmem_addr(p, rank)) : "memory");
+  return v;
+}
+
+// Grid: position * cluster size + rank (SPREAD: clusters of more than one).
+template <bool BF16, bool VEC, bool SPREAD>
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_constant__ LpParams P) {
   constexpr int E = BF16 ? 8 : 4;
-  const int r = blockIdx.y * 32768 + blockIdx.z, sl0 = blockIdx.x * P.run, tid = threadIdx.x;
-  if (r >= P.rows) return;
-  const char *row = static_cast<const char *>(P.logits) + static_cast<size_t>(r) * P.row_stride * (BF16 ? 2 : 4);
-  const uint64_t pol = l2_policy_evict_first();
-  const int sl1 = min(sl0 + P.run, P.nslices);
-  if (P.tokens && __ldg(P.tokens + r) == -1) return;
+  __shared__ __align__(16) LpPart sh[kLpThreads / 32];
+  __shared__ __align__(16) LpPart whole;        // this CTA's record
+  __shared__ uint32_t tmax[kLpThreads];
+  __shared__ int red[kLpThreads / 32];
+  __shared__ int n_chunks, n_cands;
+  __shared__ int chunk[kLpChunks];
+  __shared__ unsigned long long cand[kLpCands];
+  extern __shared__ __align__(16) unsigned char lp_smem[];  // this CTA's chunk keys
+  unsigned short *const keys = reinterpret_cast<unsigned short *>(lp_smem);
+  const uint32_t ranks = SPREAD ? cluster_nctarank() : 1u, rank = SPREAD ? cluster_ctarank() : 0u;
+  const int r = blockIdx.x / ranks, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const size_t esz = BF16 ? 2 : 4;
+  const char *row = static_cast<const char *>(P.logits) + static_cast<size_t>(r) * P.row_stride * esz;
+  const int sl0 = rank * P.run, sl1 = min(sl0 + P.run, P.nslices);
+  const int tok = P.tokens ? __ldg(P.tokens + r) : -1;
+  int32_t *ids = P.top_ids + static_cast<size_t>(r) * P.m;
+  float *lps = P.top_logprobs + static_cast<size_t>(r) * P.m;
+  if (P.tokens && tok == -1) {  // the whole cluster leaves
+    if (rank == 0) {
+      for (int i = tid; i < P.m; i += kLpThreads) {
+        ids[i] = -1;
+        lps[i] = NAN;
+      }
+      if (tid == 0) {
+        P.logprob[r] = NAN;
+        P.entropy[r] = NAN;
+        P.status[r] = 0;
+      }
+    }
+    return;
+  }
+  const uint64_t pol = l2_policy_evict_normal();  // a few lines are looked at again
   LpSlice<BF16, VEC> cur, nxt;
-  cur.load(row, sl0 * P.slice, P.V, tid, pol);
+  if (sl0 < sl1) cur.load(row, sl0 * P.slice, P.V, tid, pol);
   uint32_t flags = 0;
   const float sc = row_scale(P, r, flags);
+  if (P.tokens && (tok < -1 || tok >= P.V)) flags |= F_BAD_TOKEN;
+  float xt = 0.f;  // the given token's logit
+  if (tok >= 0 && tok < P.V) xt = logit_at<BF16>(row, tok);
+  if (tid == 0) n_chunks = n_cands = 0;
   float m = -INFINITY, s = 0.f, u = 0.f;
+  uint32_t mine = 0;  // the largest of this thread's chunk keys
   for (int sl = sl0; sl < sl1; ++sl) {
     if (sl + 1 < sl1) nxt.load(row, (sl + 1) * P.slice, P.V, tid, pol);
-    float c = -INFINITY;  // this thread's largest
+    float c = -INFINITY;  // the chunk's largest
 #pragma unroll
     for (int i = 0; i < kLpVecs; ++i) {
       if constexpr (BF16) {
-        // packed: one instruction for two pairs
         const uint32_t t = bf16x2_max_nan(bf16x2_max_nan(cur.w[i].x, cur.w[i].y), bf16x2_max_nan(cur.w[i].z, cur.w[i].w));
         c = fmax_nan(c, fmax_nan(bf16_lo(t), bf16_hi(t)));
       } else {
@@ -159,7 +215,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_stream_kernel(const __
       }
     }
     if (!(c < INFINITY)) flags |= F_NONFINITE;  // NaN or +inf
-    if (P.m > 0) P.cmax[(static_cast<size_t>(r) * P.nslices + sl) * kLpThreads + tid] = static_cast<unsigned short>(order_key(c) >> 16);
+    if (P.m > 0) {
+      const uint32_t k = order_key(c) >> 16;
+      keys[(sl - sl0) * kLpThreads + tid] = static_cast<unsigned short>(k);
+      mine = max(mine, k);
+    }
     if (c > m) {  // the sums follow the largest so far
       const float d = fmaxf((m - c) * sc, kFloorY), f = ex2(d);
       u = f * (u + d * s);
@@ -184,156 +244,116 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_stream_kernel(const __
     }
     cur = nxt;
   }
+  // --- the position's record: threads, warps, CTAs
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     join(m, s, u, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, s, o),
          __shfl_xor_sync(FULL_MASK, u, o), sc);
   flags = __reduce_or_sync(FULL_MASK, flags);
-  __shared__ LpPart sh[kLpThreads / 32];
-  if (tid % 32 == 0) sh[tid / 32] = LpPart{m, s, u, flags};
+  if (lane == 0) sh[warp] = LpPart{m, s, u, flags};
+  if (SPREAD) tmax[tid] = mine;
   __syncthreads();
-  if (tid < 32) {
-    const LpPart p = tid < kLpThreads / 32 ? sh[tid] : LpPart{-INFINITY, 0.f, 0.f, 0u};
+  {
+    // every warp joins the warps' records; lanes of a butterfly may round
+    // differently, so one lane's result counts
+    const LpPart p = lane < kLpThreads / 32 ? sh[lane] : LpPart{-INFINITY, 0.f, 0.f, 0u};
     m = p.m, s = p.s, u = p.u, flags = p.flags;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1)
       join(m, s, u, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, s, o),
            __shfl_xor_sync(FULL_MASK, u, o), sc);
     flags = __reduce_or_sync(FULL_MASK, flags);
-    if (tid == 0) P.part[static_cast<size_t>(r) * P.nparts + blockIdx.x] = LpPart{m, s, u, flags};
   }
-}
-
-// Sum over the CTA of one int per thread (all threads get it).
-__device__ __forceinline__ int block_sum(int v, int *sh) {
-  v = __reduce_add_sync(FULL_MASK, v);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
-  __syncthreads();
-  int t = 0;
+  if constexpr (SPREAD) {
+    if (tid == 0) whole = LpPart{m, s, u, flags};
+    cluster_sync();
+    const LpPart p = lane < static_cast<int>(ranks) ? ld_remote_part(&whole, lane) : LpPart{-INFINITY, 0.f, 0.f, 0u};
+    m = p.m, s = p.s, u = p.u, flags = p.flags;
 #pragma unroll
-  for (int w = 0; w < kLpThreads / 32; ++w) t += sh[w];
-  return t;
-}
-
-template <bool BF16>
-__global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_constant__ LpParams P) {
-  constexpr int E = BF16 ? 8 : 4;
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  __shared__ int red[kLpThreads / 32];
-  __shared__ int n_chunks, n_cands;
-  extern __shared__ __align__(16) unsigned char lp_smem[];  // the position's chunk keys
-  __shared__ int chunk[kLpChunks];
-  __shared__ unsigned long long cand[kLpCands];
-  const int tok = P.tokens ? __ldg(P.tokens + r) : -1;
-  const bool skip = P.tokens && tok == -1;
-  uint32_t flags = 0;
-  const float sc = row_scale(P, r, flags);
-  if (P.tokens && (tok < -1 || tok >= P.V)) flags |= F_BAD_TOKEN;
-  const size_t esz = BF16 ? 2 : 4;
-  const char *row = static_cast<const char *>(P.logits) + static_cast<size_t>(r) * P.row_stride * esz;
-  float xt = 0.f;  // the given token's logit
-  if (tok >= 0 && tok < P.V) xt = logit_at<BF16>(row, tok);
-  if (tid == 0) n_chunks = n_cands = 0;
-  grid_dependency_wait();
-  if (skip) {
-    for (int i = tid; i < P.m; i += kLpThreads) {
-      P.top_ids[static_cast<size_t>(r) * P.m + i] = -1;
-      P.top_logprobs[static_cast<size_t>(r) * P.m + i] = NAN;
-    }
-    if (tid == 0) {
-      P.logprob[r] = NAN;
-      P.entropy[r] = NAN;
-      P.status[r] = 0;
-    }
-    return;
+    for (int o = kLpMaxCluster / 2; o > 0; o >>= 1)
+      join(m, s, u, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, s, o),
+           __shfl_xor_sync(FULL_MASK, u, o), sc);
+    flags = __reduce_or_sync(FULL_MASK, flags);
+    for (uint32_t k = 0; k < ranks; ++k) mine = max(mine, ld_remote_u32(&tmax[tid], k));
   }
-  // the chunk keys, then the records (every warp joins them all: no barrier)
-  const int nkeys = P.nslices * kLpThreads;
-  unsigned short *const keys = reinterpret_cast<unsigned short *>(lp_smem);
-  if (P.m > 0)
-    for (int i = tid; i < nkeys / 8; i += kLpThreads)
-      cp_async16(keys + 8 * i, P.cmax + static_cast<size_t>(r) * nkeys + 8 * i);
-  float m = -INFINITY, s = 0.f, u = 0.f;
-  for (int i = lane; i < P.nparts; i += 32) {
-    const LpPart p = P.part[static_cast<size_t>(r) * P.nparts + i];
-    join(m, s, u, p.m, p.s, p.u, sc);
-    flags |= p.flags;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    join(m, s, u, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, s, o),
-         __shfl_xor_sync(FULL_MASK, u, o), sc);
-  // one lane's rounding for all: which thread writes which output is a matter of timing
   m = __shfl_sync(FULL_MASK, m, 0);
   s = __shfl_sync(FULL_MASK, s, 0);
   u = __shfl_sync(FULL_MASK, u, 0);
-  flags = __reduce_or_sync(FULL_MASK, flags);
-  cp_async_wait_all();
-  __syncthreads();
   if (m == -INFINITY && !(flags & F_NONFINITE)) flags |= F_EMPTY;
   const float lgs = log2f(s);
   const bool bad = flags != 0;
-  if (tid == 0) {
+  if (rank == 0 && tid == 0) {
     if (P.tokens) P.logprob[r] = bad ? NAN : kLn2 * ((xt - m) * sc - lgs);
     P.entropy[r] = bad ? NAN : fmaxf(0.f, kLn2 * (lgs - u / s));
     P.status[r] = lowest_code(flags);
   }
-  if (P.m == 0) return;
-  int32_t *ids = P.top_ids + static_cast<size_t>(r) * P.m;
-  float *lps = P.top_logprobs + static_cast<size_t>(r) * P.m;
-  if (bad) {
-    for (int i = tid; i < P.m; i += kLpThreads) {
-      ids[i] = -1;
-      lps[i] = NAN;
-    }
+  if (P.m == 0 || bad) {
+    if (rank == 0)
+      for (int i = tid; i < P.m; i += kLpThreads) {
+        ids[i] = -1;
+        lps[i] = NAN;
+      }
+    if (SPREAD) cluster_sync();  // the others may still be reading this CTA's memory
     return;
   }
-  // A lower bound of the m-th largest chunk key: the m-th largest of the 256
-  // threads' own maxima, bit by bit (a barrier counts).  At least m chunks reach
-  // it, and few more.  With fewer than m maxima it is 0: all are looked at.
-  unsigned mine = 0;
-#pragma unroll 8
-  for (int i = tid; i < nkeys; i += kLpThreads) mine = max(mine, static_cast<unsigned>(keys[i]));
+  // --- a lower bound of the m-th largest chunk key: the m-th largest of the 256
+  // threads' maxima, bit by bit (a barrier counts).  At least m chunks reach it,
+  // and few more.  With fewer than m maxima it is 0: all are looked at.
   unsigned t16 = 0;
 #pragma unroll
   for (int bit = 15; bit >= 0; --bit) {
     const unsigned t = t16 | (1u << bit);
     if (__syncthreads_count(mine >= t) >= P.m) t16 = t;
   }
-  if (mine >= t16)
-    for (int i = tid; i < nkeys; i += kLpThreads)
-      if (keys[i] >= t16) {
-        const int at = atomicAdd(&n_chunks, 1);
-        if (at < kLpChunks) chunk[at] = i;
-      }
+  // --- this CTA's chunks that reach it, and their logits that do, a 16-byte
+  // vector per thread
+  for (int i = tid; i < (sl1 - sl0) * kLpThreads; i += kLpThreads)
+    if (keys[i] >= t16) {
+      const int at = atomicAdd(&n_chunks, 1);
+      if (at < kLpChunks) chunk[at] = i;
+    }
   __syncthreads();
   const int nc = n_chunks;
-  if (nc <= kLpChunks) {
-    // a 16-byte vector per thread
-    for (int i = tid; i < nc * kLpVecs; i += kLpThreads) {
-      const int c = chunk[i / kLpVecs];
-      const int v0 = (c / kLpThreads) * P.slice + ((i % kLpVecs) * kLpThreads + c % kLpThreads) * E;
-      if (v0 >= P.V) continue;
-      uint32_t w[4];
-      if (P.vec) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row + v0 * esz));
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-      }
+  for (int i = tid; i < min(nc, kLpChunks) * kLpVecs; i += kLpThreads) {
+    const int c = chunk[i / kLpVecs];
+    const int v0 = (sl0 + c / kLpThreads) * P.slice + ((i % kLpVecs) * kLpThreads + c % kLpThreads) * E;
+    if (v0 >= P.V) continue;
+    uint32_t w[4];
+    if constexpr (VEC) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4 *>(row + v0 * esz));
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    }
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        if (v0 + e >= P.V) break;
-        const float x = !P.vec ? logit_at<BF16>(row, v0 + e) : BF16 ? (e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2])) : __uint_as_float(w[BF16 ? 0 : e]);
-        const uint32_t k = order_key(x);
-        if ((k >> 16) < t16) continue;
-        const int at = atomicAdd(&n_cands, 1);
-        if (at < kLpCands) cand[at] = static_cast<unsigned long long>(k) << 32 | (0xffffffffu - (v0 + e));
-      }
+    for (int e = 0; e < E; ++e) {
+      if (v0 + e >= P.V) break;
+      const float x = !VEC ? logit_at<BF16>(row, v0 + e) : BF16 ? (e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2])) : __uint_as_float(w[BF16 ? 0 : e]);
+      const uint32_t k = order_key(x);
+      if ((k >> 16) < t16) continue;
+      const int at = atomicAdd(&n_cands, 1);
+      if (at < kLpCands) cand[at] = static_cast<unsigned long long>(k) << 32 | (0xffffffffu - (v0 + e));
     }
   }
   __syncthreads();
+  bool over = nc > kLpChunks || n_cands > kLpCands;  // too many to list
   int n = n_cands;
-  if (nc > kLpChunks || n > kLpCands) {
+  if constexpr (SPREAD) {
+    if (tid == 0 && over) n_cands = kLpCands + 1;
+    cluster_sync();
+    if (rank != 0) {
+      cluster_sync();  // until rank 0 has read this CTA's list
+      return;
+    }
+    // rank 0 appends the others' lists to its own
+    for (uint32_t k = 1; k < ranks; ++k) {
+      const int more = static_cast<int>(ld_remote_u32(&n_cands, k));
+      over = over || more > kLpCands || n + more > kLpCands;
+      if (!over)
+        for (int i = tid; i < more; i += kLpThreads) cand[n + i] = ld_remote_u64(&cand[i], k);
+      n += more;
+    }
+    cluster_sync();
+  }
+  if (over) {
     // Whole-position search: the m-th largest key exactly, bit by bit, then
     // everything above it (fewer than m) and the first of the equal ones.
     uint32_t t = 0;
@@ -384,40 +404,34 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_pick_kernel(const __grid_
 }
 
 int lp_slice(bool bf16) { return kLpThreads * kLpVecs * (bf16 ? 8 : 4); }
-// Slices per stream item: as many as leave eight items per SM.
-int lp_run(long long rows, int nslices) {
-  int run = 1;
-  while (run < 8 && rows * ((nslices + 2 * run - 1) / (2 * run)) >= 8 * 152) run *= 2;
-  return run;
+// CTAs per position: doubled while that leaves each a slice and the grid within
+// two rounds of the 4 CTAs that an SM holds (384 positions of 128256 bf16 logits,
+// 224 of them asked for: 28 us with one CTA each, 24 with two, 30 with four).
+int lp_ranks(long long rows, int nslices) {
+  int ranks = 1;
+  while (ranks < kLpMaxCluster && 2 * ranks <= nslices && rows * 2 * ranks <= 8 * 152) ranks *= 2;
+  return ranks;
 }
-size_t lp_round(size_t x) { return (x + 255) / 256 * 256; }
 bool lp_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 bool lp_sizes(int32_t B, int32_t npos, int32_t V) {
   return B >= 0 && npos >= 1 && V >= 1 && V <= SPEC_MAX_V && static_cast<long long>(B) * npos < 0x7fffffffLL / 64;
 }
 
-template <bool BF16>
-cudaError_t launch_logprobs(const LpParams &p, bool vec, cudaStream_t s) {
-  // rows over y and z (65535 at most in each)
-  const dim3 grid(p.nparts, (p.rows + 32767) / 32768, p.rows < 32768 ? p.rows : 32768);
-  if (vec)
-    logprobs_stream_kernel<BF16, true><<<grid, kLpThreads, 0, s>>>(p);
-  else
-    logprobs_stream_kernel<BF16, false><<<grid, kLpThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+template <bool BF16, bool VEC>
+cudaError_t launch_logprobs(const LpParams &p, int ranks, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.rows);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * ranks);
   cfg.blockDim = dim3(kLpThreads);
-  cfg.dynamicSmemBytes = p.m > 0 ? static_cast<size_t>(p.nslices) * kLpThreads * 2 : 0;  // 32 KB at most
+  cfg.dynamicSmemBytes = p.m > 0 ? static_cast<size_t>(p.run) * kLpThreads * 2 : 0;  // 32 KB at most
   cfg.stream = s;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {static_cast<unsigned>(ranks), 1, 1};
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_pick_kernel<BF16>, p);
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
+  return ranks > 1 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<BF16, VEC, true>, p)
+                   : cudaLaunchKernelEx(&cfg, logprobs_kernel<BF16, VEC, false>, p);
 }
 
 }  // namespace
@@ -427,14 +441,7 @@ using namespace sv;
 
 extern "C" {
 
-size_t spec_token_logprobs_workspace_size(int32_t B, int32_t npos, int32_t V) {
-  if (!lp_sizes(B, npos, V)) return 0;
-  const size_t items = static_cast<size_t>(B) * npos * ((V + lp_slice(false) - 1) / lp_slice(false));
-  return lp_round(items * sizeof(LpPart)) + lp_round(items * kLpThreads * 2) + 256;
-}
-
-spec_status spec_token_logprobs(const spec_logprobs_args *a, const spec_logprobs_out *o, void *ws,
-                                size_t ws_bytes, void *stream) {
+spec_status spec_token_logprobs(const spec_logprobs_args *a, const spec_logprobs_out *o, void *stream) {
   if (!a || !o) return SPEC_ERR_NULL;
   if (!lp_sizes(a->B, a->npos, a->V)) return SPEC_ERR_SHAPE;
   if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
@@ -449,8 +456,6 @@ spec_status spec_token_logprobs(const spec_logprobs_args *a, const spec_logprobs
   const void *w4[] = {a->tokens, a->temperature, o->logprob, o->entropy, o->top_ids, o->top_logprobs, o->status};
   for (const void *q : w4)
     if (!lp_aligned(q, 4)) return SPEC_ERR_ALIGN;
-  if (!ws || !lp_aligned(ws, 256) || ws_bytes < spec_token_logprobs_workspace_size(a->B, a->npos, a->V))
-    return SPEC_ERR_WORKSPACE;
   LpParams p = {};
   p.logits = a->logits;
   p.tokens = a->tokens;
@@ -467,18 +472,12 @@ spec_status spec_token_logprobs(const spec_logprobs_args *a, const spec_logprobs
   p.m = a->m;
   p.slice = lp_slice(bf16);
   p.nslices = (a->V + p.slice - 1) / p.slice;
-  // few positions: a CTA per slice, so that more SMs share a position; many:
-  // up to 8 slices each, so that starts and ends weigh less (224 positions of
-  // 128256 bf16 logits: 23 us at one slice each, 13 at four)
-  p.run = lp_run(p.rows, p.nslices);
-  p.nparts = (p.nslices + p.run - 1) / p.run;
-  p.part = static_cast<LpPart *>(ws);
-  p.cmax = reinterpret_cast<unsigned short *>(static_cast<char *>(ws) +
-                                              lp_round(static_cast<size_t>(p.rows) * p.nparts * sizeof(LpPart)));
+  const int ranks = lp_ranks(p.rows, p.nslices);
+  p.run = (p.nslices + ranks - 1) / ranks;
   const bool vec = lp_aligned(a->logits, 16) && (a->row_stride * esz) % 16 == 0 && (static_cast<long long>(a->V) * esz) % 16 == 0;
-  p.vec = vec;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = bf16 ? launch_logprobs<true>(p, vec, s) : launch_logprobs<false>(p, vec, s);
+  const cudaError_t e = bf16 ? (vec ? launch_logprobs<true, true>(p, ranks, s) : launch_logprobs<true, false>(p, ranks, s))
+                             : (vec ? launch_logprobs<false, true>(p, ranks, s) : launch_logprobs<false, false>(p, ranks, s));
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

@@ -96,10 +96,6 @@ struct RowCfg {
 template <int CT, int DP, int MT>
 __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kernel(const __grid_constant__ AttnParams P, int own,
                                                                                    int pblocks, int oblocks) {
-  // Launched to run beside the prefix's tile kernel, which it has nothing to
-  // do with; its last item ends after that kernel, so that whoever waits for
-  // this grid has waited for both.
-  const bool last = P.beside && blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z;
   using C = RowCfg<CT, DP, MT>;
   constexpr bool E4 = C::E4;
   constexpr bool BF = CT == SPEC_BF16;
@@ -122,10 +118,7 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
     cut_rows(P, split, b, split, parts, t0, t1);
     if (b >= 0 && split == 0 && blk == 0 && g == 0 && lane == 0) P.nparts[b] = parts;
   }
-  if (b < 0 || blk >= (pre ? pblocks : oblocks) || split >= (pre ? P.psplits : P.osplits)) {  // the grid is a box
-    if (last) grid_dependency_wait();
-    return;
-  }
+  if (b < 0 || blk >= (pre ? pblocks : oblocks) || split >= (pre ? P.psplits : P.osplits)) return;  // the grid is a box
   const int r0 = blk * C::kM;              // first query row of the block
   const int nrows = (pre ? P.B : 1) * P.N * P.G;
   const int slot = pre ? split : P.psplits + split;
@@ -167,7 +160,6 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
   if (t0 >= t1) {  // nothing here (an empty part, or a row that cannot be used)
     if (!pre && lane == 0) P.oflag[flag] = 0;
     if (my_row >= 0) P.ml[static_cast<long long>(slot) * P.rows + my_row] = make_float2(-INFINITY, -INFINITY);
-    if (last) grid_dependency_wait();
     return;
   }
 
@@ -651,7 +643,6 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
           if (n * 8 < P.D) *reinterpret_cast<float2 *>(to + n * 8 + 2 * j4) = make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
       }
     }
-  if (last) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------- join
@@ -758,17 +749,8 @@ cudaError_t launch_rows(const AttnParams &p, bool own, bool prefix, cudaStream_t
   const dim3 grid(p.H * blocks, std::max(!own ? 1 : p.budget > 0 ? p.budget : p.osplits, prefix ? p.psplits : 1), zown + (prefix ? 1 : 0));
   const cudaError_t e = allow_smem<attn_rows_kernel<CT, DP, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(32);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = p.beside ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_rows_kernel<CT, DP, MT>, p, zown, pblocks, oblocks);
+  attn_rows_kernel<CT, DP, MT><<<grid, 32, C::kSmem, s>>>(p, zown, pblocks, oblocks);
+  return cudaGetLastError();
 }
 
 // Items of the rows kernel that run on an SM at a time.
@@ -875,7 +857,7 @@ AttnPlan plan_attention(const spec_attention_args *a) {
     // all items run side by side; for many, whole rows balance well enough.
     const long long budget = rows_per_sm(c.dtype, p.oblk) * kSms / (c.heads * oblocks);
     p.osplits = 1;
-    if (c.rows <= kMaxCutRows && budget > c.rows) {
+    if (c.rows <= kMaxCutRows && budget > c.rows && c.slots < 1LL << 28) {
       p.budget = static_cast<int>(budget);
       p.osplits = static_cast<int>(std::min<long long>({(c.slots + 63) / 64, budget / c.rows * 4, 64}));
     }
@@ -999,7 +981,6 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
     if (plan.direct) return SPEC_OK;
     p.direct = 0;
   }
-  p.beside = prefix && plan.ptile && !plan.otile;
   if ((!plan.otile || (prefix && !plan.ptile)) &&
       launch_attn_rows(p, c.dtype, !plan.otile, prefix && !plan.ptile, s) != cudaSuccess)
     return SPEC_ERR_CUDA;

@@ -191,7 +191,6 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
   unsigned char *const smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Ctrl *const c = reinterpret_cast<Ctrl *>(smem + C::kCtrl);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, role = tid / 128;
-  allow_dependents();  // the own entries' kernel fills what SMs are left
 
   // --- the item
   int item = blockIdx.x;

@@ -77,12 +77,12 @@ def test_read_refusals(L, kw, want):
 
 
 def logprobs(L, B=2, npos=3, V=1000, dtype=BF16, m=5, pitch=None, logits=P, tokens=P, temperature=None,
-             logprob=P, entropy=P, ids=P, tops=P, status=P, ws=P, ws_bytes=1 << 30):
+             logprob=P, entropy=P, ids=P, tops=P, status=P):
     from speculative_decoding_verification_32_gb300._binding import SpecLogprobsArgs, SpecLogprobsOut
     a = SpecLogprobsArgs(B, npos, V, dtype, m, 0, V if pitch is None else pitch, ptr(logits), ptr(tokens),
                          ptr(temperature))
     o = SpecLogprobsOut(ptr(logprob), ptr(entropy), ptr(ids), ptr(tops), ptr(status))
-    return L.spec_token_logprobs(ctypes.byref(a), ctypes.byref(o), ptr(ws), ws_bytes, None)
+    return L.spec_token_logprobs(ctypes.byref(a), ctypes.byref(o), None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -91,23 +91,9 @@ def logprobs(L, B=2, npos=3, V=1000, dtype=BF16, m=5, pitch=None, logits=P, toke
     (dict(V=4), ARG), (dict(pitch=999), ARG), (dict(logits=0), NULL), (dict(entropy=0), NULL),
     (dict(status=0), NULL), (dict(logprob=0), NULL), (dict(ids=0), NULL), (dict(tops=0), NULL),
     (dict(logits=P + 1), ALIGN), (dict(tokens=P + 2), ALIGN), (dict(temperature=P + 1), ALIGN),
-    (dict(tops=P + 1), ALIGN), (dict(ws=0), WORKSPACE), (dict(ws=P + 16), WORKSPACE),
-    (dict(ws_bytes=1000), WORKSPACE), (dict(B=0), OK)])
+    (dict(tops=P + 1), ALIGN), (dict(B=0), OK)])
 def test_logprobs_refusals(L, kw, want):
     assert logprobs(L, **kw) == want
-
-
-def test_logprobs_workspace_holds_records_and_keys(L):
-    """A 16-byte record and 256 2-byte keys per slice, for both tilings, in
-    256-byte aligned areas."""
-    def al(x):
-        return -(-x // 256) * 256
-    for B, npos, V in [(1, 1, 1), (64, 6, 128256), (3, 5, 4097), (2, 1, 262144)]:
-        need = L.spec_token_logprobs_workspace_size(B, npos, V)
-        for tile in (8192, 4096):
-            items = B * npos * -(-V // tile)
-            assert need >= al(items * 16) + al(items * 512)
-    assert L.spec_token_logprobs_workspace_size(1, 0, 10) == 0
 
 
 def test_binding_refusals(L):
