@@ -26,6 +26,11 @@ struct AttnParams {
   // caches
   const unsigned char *k, *v;    // own entries
   const unsigned char *pk, *pv;  // prefix entries
+  // the prefix of an e4m3 cache as fp16 (attn_widen_kernel), or NULL: keys then
+  // values, [P][H][D]; and per head and 128 tokens the keys' scale, then the
+  // values' scale exponent
+  unsigned char *wide;
+  float *wide_scale;
   long long row_stride, tok_stride, ptok_stride, slots;
   int P;  // prefix length
   // queries
@@ -277,9 +282,11 @@ cudaError_t allow_smem(int bytes, int regs = 0) {
 }
 
 // Host launchers.
-// attn_rows_kernel over the own entries (own) and the prefix (prefix) ...
+// attn_rows_kernel over the own entries (own) and the prefix (prefix).
 cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool own, bool prefix, cudaStream_t s);
-// ... and attn_tile_kernel over one of the two.
+// The prefix of an e4m3 cache into P.wide.
+cudaError_t launch_attn_widen(const AttnParams &p, cudaStream_t s);
+// attn_tile_kernel over the prefix, or over the own entries.
 cudaError_t launch_attn_tile(const AttnParams &p, int ctype, bool prefix, cudaStream_t s);
 
 }  // namespace sv

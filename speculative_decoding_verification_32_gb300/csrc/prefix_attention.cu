@@ -774,8 +774,9 @@ struct AttnPlan {
   int psplits, pchunk, osplits, min_chunk, budget, W;
   bool ptile, otile;  // attn_tile_kernel for the prefix, for the own entries
   bool fuse, direct;  // own items take the prefix too; and nothing is left to join
+  bool widen;         // an e4m3 prefix is turned into fp16 first
   int oblk;           // query rows per own item
-  size_t rows, anc_at, info_at, flag_at, count_at, ml_at, part_at, bytes;
+  size_t rows, anc_at, info_at, flag_at, count_at, ml_at, part_at, wide_at, scale_at, bytes;
 };
 
 size_t at_round(size_t x) { return (x + 255) / 256 * 256; }
@@ -878,6 +879,16 @@ AttnPlan plan_attention(const spec_attention_args *a) {
   at += at_round(slots * p.rows * sizeof(float2));
   p.part_at = at;
   at += at_round(slots * p.rows * c.head_dim * 4);
+  // An e4m3 prefix that several blocks of 256 query rows read is converted once
+  // (two blocks: 4 us for the conversion of 8192 tokens of 8 heads where it saves 8)
+  const long long readers = p.fuse ? c.rows * oblocks : p.ptile ? (q * G + 255) / 256 : 0;
+  p.widen = c.dtype == SPEC_E4M3 && a->prefix_len > 0 && readers >= 2;
+  if (p.widen) {
+    p.wide_at = at;
+    at += at_round(static_cast<size_t>(a->prefix_len) * c.heads * c.head_dim * 4);
+    p.scale_at = at;
+    at += at_round(static_cast<size_t>((a->prefix_len + 127) / 128) * c.heads * 2 * 4);
+  }
   p.bytes = at + 256;
   return p;
 }
@@ -972,6 +983,11 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
     if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
     p.anc = anc;
     p.rowinfo = info;
+  }
+  if (plan.widen) {
+    p.wide = reinterpret_cast<unsigned char *>(w + plan.wide_at);
+    p.wide_scale = reinterpret_cast<float *>(w + plan.scale_at);
+    if (launch_attn_widen(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
   }
   const bool prefix = p.P > 0;
   if (prefix && plan.ptile && !plan.fuse && launch_attn_tile(p, c.dtype, true, s) != cudaSuccess) return SPEC_ERR_CUDA;

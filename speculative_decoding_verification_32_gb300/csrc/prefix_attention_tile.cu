@@ -278,13 +278,36 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
     constexpr int kPut = E4 ? kProducers * 16 : kStep * 128;
     const long long src0 = static_cast<long long>(g) * P.D * (E4 ? 1 : 2) + (col ? pc * 16 : 0);
     const unsigned char *const ok = P.k + b * P.row_stride, *const ov = P.v + b * P.row_stride;
-    // copies of item it; for codes, the scale byte of the block's token pt
+    // copies of item it; for codes, the scale byte of the block's token pt (of a
+    // prefix that is fp16 already, the bits of the block's scale)
     auto issue = [&](int it) -> uint32_t {
       uint32_t byte = 0;
       if (it < 2 * n) {
         const int k = it >> 1, s = k & 1, q = q0 + k;
         const bool pre = PRE || q < npre, val = it & 1;
         const int tb = (pre ? q : q - npre) * kTok, left = (pre ? P.P : len) - tb;
+        if constexpr (E4) {
+          if (pre && P.wide) {
+            constexpr int WL = DP / 8, kWStep = kProducers / WL;
+            const int wc = pt % WL, wrow = pt / WL;
+            const long long ts = static_cast<long long>(P.H) * P.D * 2;
+            const unsigned char *src = P.wide + (static_cast<long long>(val ? P.P : 0) + tb + wrow) * ts + static_cast<long long>(g) * P.D * 2 + wc * 16;
+            byte = __float_as_uint(__ldg(P.wide_scale + (static_cast<long long>(val ? P.H : 0) + g) * npre + q));
+            if (k >= 2 && live) live = wait_for(c, val ? &c->vfree[s] : &c->kfree[s], ((k >> 1) - 1) & 1, limit);
+            if (live) {
+              const uint32_t dst = sbase + (val ? C::kV : C::kK) + s * C::kOp + (wc / 8) * 16384 + wrow * 128 + (((wc % 8) ^ (wrow & 7)) << 4);
+              const bool in = wc * 16 < P.D * 2;
+#pragma unroll
+              for (int i = 0; i < kTok / kWStep; ++i) {
+                const bool on = in && wrow + i * kWStep < left;
+                cp_async16_zfill(dst + i * kWStep * 128, on ? src : P.wide, on);
+                src += ts * kWStep;
+              }
+            }
+            cp_async_commit();
+            return byte;
+          }
+        }
         const long long ts = pre ? P.ptok_stride : P.tok_stride;
         const unsigned char *const base = (pre ? (val ? P.pv : P.pk) : (val ? ov : ok)) + tb * ts;
         if constexpr (E4)
@@ -343,6 +366,17 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
               asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
               c->odd = 1;
             }
+          }
+        }
+      } else if ((PRE || q < npre) && P.wide) {
+        if (!val) kscale = __uint_as_float(sc0);
+        if (val) {
+          const float ex = __uint_as_float(sc0);
+          E = fmaxf(E, ex);
+          if (pt == 0) {
+            c->ksc[s] = kscale;
+            c->vex[s] = ex;
+            c->vtop[s] = E;
           }
         }
       } else {
@@ -687,7 +721,7 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         if constexpr (E4) {
           // l counts in units of 2^(m - E)
           const float ll = grow != 0.f ? (old == -INFINITY ? 0.f : ex2(old - m + grow)) : al;
-          l = fmaf(l, ll, add * ex2(E - ex));
+          l = fmaf(l, ll, add * ex2(fminf(E - ex, 126.f)));
         } else {
           l = fmaf(l, al, add);
         }
@@ -769,6 +803,66 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
   }
 }
 
+// ------------------------------------------------------ a prefix read often
+// An e4m3 prefix that many blocks of query rows will read is turned into fp16
+// once: 128 tokens of a head and plane per CTA, relative to their largest scale
+// as the tile kernel does it.  Costs one read of the codes and one write of
+// twice as many bytes, and saves every item the conversion, which takes longer
+// than the tensor cores do (a block of tokens: 3.2 us with it, 1.8 without).
+constexpr int kWidenThreads = 256;
+__global__ void __launch_bounds__(kWidenThreads) attn_widen_kernel(const __grid_constant__ AttnParams P) {
+  __shared__ uint32_t warp_top[4];
+  __shared__ uint32_t mult[kTok];
+  const int blk = blockIdx.x, g = blockIdx.y, val = blockIdx.z, tid = threadIdx.x;
+  const int tb = blk * kTok, left = P.P - tb;
+  const unsigned char *const base = (val ? P.pv : P.pk) + tb * P.ptok_stride;
+  uint32_t byte = 0;
+  if (tid < kTok) {
+    if (tid < left) byte = __ldg(base + tid * P.ptok_stride + static_cast<long long>(P.H) * P.D + g);
+    const uint32_t top = __reduce_max_sync(FULL_MASK, byte == 255u ? 1u : max(byte, 1u));
+    if (tid % 32 == 0) warp_top[tid / 32] = top;
+  }
+  // two 16-code pieces of tokens a thread, while the scales settle
+  const int parts = P.D / 16, pieces = kTok * parts;
+  constexpr int kMost = kTok * (SPEC_MAX_HEAD_DIM / 16) / kWidenThreads;
+  uint4 w[kMost];
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int x = i * kWidenThreads + tid, t = x / parts, pc = x - t * parts;
+    if (x < pieces && t < left) w[i] = __ldg(reinterpret_cast<const uint4 *>(base + t * P.ptok_stride + static_cast<long long>(g) * P.D + pc * 16));
+  }
+  __syncthreads();
+  // scales below 2^-120 count as that: nothing they hold is seen beside the least exponent of the sums
+  const int ref = max(7, static_cast<int>(max(max(warp_top[0], warp_top[1]), max(warp_top[2], warp_top[3]))));
+  if (tid < kTok) {
+    const int d = static_cast<int>(byte) - ref;
+    const uint32_t f = byte == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+    mult[tid] = f | f << 16;
+  }
+  if (tid == 0)
+    P.wide_scale[(static_cast<long long>(val ? P.H : 0) + g) * gridDim.x + blk] = val ? static_cast<float>(ref - 127) : e4m3_scale(ref);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int x = i * kWidenThreads + tid, t = x / parts, pc = x - t * parts;
+    if (x >= pieces || t >= left) continue;
+    const __half2 f2 = *reinterpret_cast<const __half2 *>(&mult[t]);
+    const uint32_t cw[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t lo = e4m3x2_to_f16x2(cw[e]), hi = e4m3x2_to_f16x2_hi(cw[e]);
+      const __half2 l2 = __hmul2(*reinterpret_cast<const __half2 *>(&lo), f2);
+      const __half2 h2 = __hmul2(*reinterpret_cast<const __half2 *>(&hi), f2);
+      o[2 * e] = *reinterpret_cast<const uint32_t *>(&l2);
+      o[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&h2);
+    }
+    uint4 *const to = reinterpret_cast<uint4 *>(P.wide + ((static_cast<long long>(val ? P.P : 0) + tb + t) * P.H + g) * P.D * 2 + pc * 32);
+    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
 template <int CT, int DP, bool PRE>
 cudaError_t launch(const AttnParams &p, cudaStream_t s) {
   using C = TileCfg<DP>;
@@ -788,6 +882,12 @@ cudaError_t launch_d(const AttnParams &p, bool prefix, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_attn_widen(const AttnParams &p, cudaStream_t s) {
+  const dim3 grid((p.P + kTok - 1) / kTok, p.H, 2);
+  attn_widen_kernel<<<grid, kWidenThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_attn_tile(const AttnParams &p, int ctype, bool prefix, cudaStream_t s) {
   if (ctype == SPEC_E4M3) return launch_d<SPEC_E4M3>(p, prefix, s);
