@@ -73,8 +73,7 @@ struct Ctrl {
   uint32_t red[2][4];       // producers' reductions
   uint32_t mult[2][128];    // fp16 factors of the block's tokens, keys and values
   float qfac[256];
-  int orow[256];            // output row of a query row; -1: past the last, or | kUnused
-  long long qoff[256];      // its query's offset in elements
+  long long qoff[256];      // where a query row's elements are; -1: past the last
 };
 static_assert(sizeof(Ctrl) <= 7168, "control block");
 constexpr int kUnused = 1 << 30;  // the row has no such query (its answer is empty)
@@ -519,20 +518,18 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
     int at = -1;  // the thread's output row; -1: past the last, kUnused: no such query
     {
       const int r = r0 + tid;
-      long long off = 0;
+      long long off = -1;
       if (r < nrows) {
         const int t = r / P.G, h = g * P.G + (r - t * P.G);
         const int qb = PRE ? t / P.N : b, qt = PRE ? t - qb * P.N : t;
         at = (qb * P.N + qt) * P.Hq + h;
         off = qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2];
-        if (qt >= (PRE ? row_queries(P, qb) : cnt)) at |= kUnused;
       }
-      c->orow[tid] = at;
       c->qoff[tid] = off;
     }
     asm volatile("bar.sync 2, 256;" ::: "memory");
     {
-      constexpr int L = DP / 8, kIt = L, kBatch = 8, kStep = 256 / L;
+      constexpr int L = DP / 8, kIt = L, kBatch = kIt, kStep = 256 / L;
       const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
       const int pc = tid % L, rr0 = tid / L;
 #pragma unroll
@@ -540,10 +537,10 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         uint4 u[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          const int rr = rr0 + (i0 + i) * kStep, row = c->orow[rr];
+          const long long off = c->qoff[rr0 + (i0 + i) * kStep];
           u[i] = make_uint4(0, 0, 0, 0);
-          if (row >= 0 && row < kUnused && pc * 8 < P.D) {
-            const unsigned short *q = static_cast<const unsigned short *>(P.q) + c->qoff[rr] + pc * 8;
+          if (off >= 0 && pc * 8 < P.D) {
+            const unsigned short *q = static_cast<const unsigned short *>(P.q) + off + pc * 8;
             if (vec) {
               u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
             } else {
@@ -584,6 +581,11 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
     }
     fence_async_smem();
     mbar_arrive(&c->qfull);
+    // queries that a row does not have were read all the same: nothing of them is kept
+    if (at >= 0) {
+      const int t = (r0 + tid) / P.G, qb = PRE ? t / P.N : b;
+      if ((PRE ? t - qb * P.N : t) >= (PRE ? row_queries(P, qb) : cnt)) at |= kUnused;
+    }
     asm volatile("bar.sync 2, 256;" ::: "memory");  // the factors, for every row's thread
     const int tile = role;
     if (tile < tiles) {
