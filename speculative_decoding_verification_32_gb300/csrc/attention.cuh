@@ -61,6 +61,7 @@ struct AttnParams {
   float *lse;
   int32_t *row_status;
   int qbf16;
+  int next;    // the rows kernel follows the prefix's tile kernel: started while that one ends
   int fuse;    // own items of the tile kernel take the prefix too
   int direct;  // ... and write the answers themselves: there is nothing to join
   uint64_t wait_limit_ns;

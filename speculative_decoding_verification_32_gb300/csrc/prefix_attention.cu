@@ -118,7 +118,10 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
     cut_rows(P, split, b, split, parts, t0, t1);
     if (b >= 0 && split == 0 && blk == 0 && g == 0 && lane == 0) P.nparts[b] = parts;
   }
-  if (b < 0 || blk >= (pre ? pblocks : oblocks) || split >= (pre ? P.psplits : P.osplits)) return;  // the grid is a box
+  if (b < 0 || blk >= (pre ? pblocks : oblocks) || split >= (pre ? P.psplits : P.osplits)) {  // the grid is a box
+    grid_dependency_wait();
+    return;
+  }
   const int r0 = blk * C::kM;              // first query row of the block
   const int nrows = (pre ? P.B : 1) * P.N * P.G;
   const int slot = pre ? split : P.psplits + split;
@@ -160,6 +163,7 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
   if (t0 >= t1) {  // nothing here (an empty part, or a row that cannot be used)
     if (!pre && lane == 0) P.oflag[flag] = 0;
     if (my_row >= 0) P.ml[static_cast<long long>(slot) * P.rows + my_row] = make_float2(-INFINITY, -INFINITY);
+    grid_dependency_wait();
     return;
   }
 
@@ -643,6 +647,9 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
           if (n * 8 < P.D) *reinterpret_cast<float2 *>(to + n * 8 + 2 * j4) = make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
       }
     }
+  // Started while the prefix's kernel ends, with which this one shares nothing:
+  // it must not be over before that one, since the join waits for this one.
+  grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------- join
@@ -749,8 +756,17 @@ cudaError_t launch_rows(const AttnParams &p, bool own, bool prefix, cudaStream_t
   const dim3 grid(p.H * blocks, std::max(!own ? 1 : p.budget > 0 ? p.budget : p.osplits, prefix ? p.psplits : 1), zown + (prefix ? 1 : 0));
   const cudaError_t e = allow_smem<attn_rows_kernel<CT, DP, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  attn_rows_kernel<CT, DP, MT><<<grid, 32, C::kSmem, s>>>(p, zown, pblocks, oblocks);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.next ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_rows_kernel<CT, DP, MT>, p, zown, pblocks, oblocks);
 }
 
 // Items of the rows kernel that run on an SM at a time.
@@ -990,6 +1006,11 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
     if (launch_attn_widen(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
   }
   const bool prefix = p.P > 0;
+  // The rows kernel may start while the tile kernel ends where both divide an
+  // SM's memory alike, as with 16-bit rings (64 chains, bf16: 107 -> 103 us);
+  // for codes each SM would have to be emptied in between (64 decoding rows: 79
+  // -> 88 us), so there the kernels run one after the other.
+  p.next = prefix && plan.ptile && !plan.otile && c.dtype != SPEC_E4M3;
   if (prefix && plan.ptile && !plan.fuse && launch_attn_tile(p, c.dtype, true, s) != cudaSuccess) return SPEC_ERR_CUDA;
   if (plan.otile) {
     p.direct = plan.direct;

@@ -732,6 +732,7 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         mbar_arrive(&c->pfull[tile]);
       }
       if (live) live = __all_sync(FULL_MASK, wait_for(c, &c->done[tile], 0, limit));
+      if (PRE && P.next) allow_dependents();  // the rows kernel's items may take the SMs as they come free
       const long long orow = at & (kUnused - 1);
       float2 *const ml = P.ml + static_cast<long long>(slot) * P.rows + orow;
       if (!live) {
