@@ -167,6 +167,32 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
     return;
   }
 
+  // --- the queries' loads, before the many of the ring
+  constexpr int QL = DP / 8, kRows = 32 / QL, kPass = C::kM / kRows;  // lanes per row, rows per pass
+  const int qc = lane % QL;
+  uint4 u[kPass];
+  {
+    const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
+#pragma unroll
+    for (int i = 0; i < kPass; ++i) {
+      const int rr = i * kRows + lane / QL;
+      const bool use = __shfl_sync(FULL_MASK, my_use, rr);
+      const long long off = __shfl_sync(FULL_MASK, my_q, rr);
+      u[i] = make_uint4(0, 0, 0, 0);
+      if (use && qc * 8 < P.D) {
+        const unsigned short *q = static_cast<const unsigned short *>(P.q) + off + qc * 8;
+        if (vec) {
+          u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
+        } else {
+          u[i].x = q[0] | static_cast<uint32_t>(q[1]) << 16;
+          u[i].y = q[2] | static_cast<uint32_t>(q[3]) << 16;
+          u[i].z = q[4] | static_cast<uint32_t>(q[5]) << 16;
+          u[i].w = q[6] | static_cast<uint32_t>(q[7]) << 16;
+        }
+      }
+    }
+  }
+
   // --- the ring of token blocks: lanes over a token's 16-byte pieces, then
   // over tokens; pointers advance
   const uint32_t ring = smem_u32(smem);
@@ -221,58 +247,30 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
 
   // --- queries into the last ring slot; fp16 for an e4m3 cache: a row far
   // outside fp16's range is brought into it by a power of two
-  {
-    constexpr int QL = DP / 8, kRows = 32 / QL, kPass = C::kM / kRows;  // lanes per row, rows per pass
-    const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
-    const int qc = lane % QL;
-    constexpr int kBatch = kPass < 8 ? kPass : 8;
 #pragma unroll
-    for (int i0 = 0; i0 < kPass; i0 += kBatch) {
-      uint4 u[kBatch];
+  for (int i = 0; i < kPass; ++i) {
+    const int rr = i * kRows + lane / QL;
+    float fac = 1.f;
+    if (E4 && P.qbf16) {
+      const float x[8] = {bf16_lo(u[i].x), bf16_hi(u[i].x), bf16_lo(u[i].y), bf16_hi(u[i].y),
+                          bf16_lo(u[i].z), bf16_hi(u[i].z), bf16_lo(u[i].w), bf16_hi(u[i].w)};
+      uint32_t a = 0;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int rr = (i0 + i) * kRows + lane / QL;
-        const bool use = __shfl_sync(FULL_MASK, my_use, rr);
-        const long long off = __shfl_sync(FULL_MASK, my_q, rr);
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (use && qc * 8 < P.D) {
-          const unsigned short *q = static_cast<const unsigned short *>(P.q) + off + qc * 8;
-          if (vec) {
-            u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
-          } else {
-            u[i].x = q[0] | static_cast<uint32_t>(q[1]) << 16;
-            u[i].y = q[2] | static_cast<uint32_t>(q[3]) << 16;
-            u[i].z = q[4] | static_cast<uint32_t>(q[5]) << 16;
-            u[i].w = q[6] | static_cast<uint32_t>(q[7]) << 16;
-          }
-        }
+      for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = QL / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
+      float by = 1.f;
+      const int e = static_cast<int>(a >> 23) - 127;
+      if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
+        const int up = max(-126, min(126, -e));
+        by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+        fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
       }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int rr = (i0 + i) * kRows + lane / QL;
-        float fac = 1.f;
-        if (E4 && P.qbf16) {
-          const float x[8] = {bf16_lo(u[i].x), bf16_hi(u[i].x), bf16_lo(u[i].y), bf16_hi(u[i].y),
-                              bf16_lo(u[i].z), bf16_hi(u[i].z), bf16_lo(u[i].w), bf16_hi(u[i].w)};
-          uint32_t a = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
-#pragma unroll
-          for (int o = QL / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
-          float by = 1.f;
-          const int e = static_cast<int>(a >> 23) - 127;
-          if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
-            const int up = max(-126, min(126, -e));
-            by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-            fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-          }
-          u[i] = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
-                            pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
-        }
-        if (qc == 0) qfac[rr] = fac;
-        *reinterpret_cast<uint4 *>(qsm + rr * C::kQPitch + qc * 16) = u[i];
-      }
+      u[i] = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
+                        pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
     }
+    if (qc == 0) qfac[rr] = fac;
+    *reinterpret_cast<uint4 *>(qsm + rr * C::kQPitch + qc * 16) = u[i];
   }
   __syncwarp();
 
