@@ -61,6 +61,7 @@ struct AttnParams {
   float *lse;
   int32_t *row_status;
   int qbf16;
+  int first;   // the tile kernel is the first of its kind in the call
   int next;    // the rows kernel follows the prefix's tile kernel: started while that one ends
   int fuse;    // own items of the tile kernel take the prefix too
   int direct;  // ... and write the answers themselves: there is nothing to join
@@ -282,10 +283,27 @@ cudaError_t allow_smem(int bytes, int regs = 0) {
   return e;
 }
 
+// A launch that may start before the kernel ahead of it in the stream is over
+// (`early`; it then waits for that one itself, grid_dependency_wait).
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s, bool early, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Host launchers.
 // attn_rows_kernel over the own entries (own) and the prefix (prefix).
 cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool own, bool prefix, cudaStream_t s);
-// The prefix of an e4m3 cache into P.wide.
+// The prefix of an e4m3 cache into P.wide; runs beside the mask kernel, if there is one.
 cudaError_t launch_attn_widen(const AttnParams &p, cudaStream_t s);
 // attn_tile_kernel over the prefix, or over the own entries.
 cudaError_t launch_attn_tile(const AttnParams &p, int ctype, bool prefix, cudaStream_t s);

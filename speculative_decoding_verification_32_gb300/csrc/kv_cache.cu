@@ -20,7 +20,8 @@
 namespace sv {
 namespace {
 
-constexpr int kKvcThreads = 256;
+// small blocks: 32768 tokens of 8 heads appended in 37.8 us at 256 threads, 35.4 at 128
+constexpr int kKvcThreads = 128;
 
 struct AppendParams {
   unsigned char *kc, *vc;

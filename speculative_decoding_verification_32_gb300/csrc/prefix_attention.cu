@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kMaskThreads) attn_mask_kernel(const int32_t *
                                                                  uint32_t *anc, int32_t *rowinfo) {
   __shared__ int par[SPEC_MAX_TREE_NODES];
   const int b = blockIdx.x, tid = threadIdx.x;
+  allow_dependents();
   const int n = kv_len[b], c = count ? count[b] : N;
   const bool slot_ok = n >= 0 && c >= 0 && c <= N && static_cast<long long>(n) + c <= slots;
   const int used = max(0, min(c, N));
@@ -754,17 +755,7 @@ cudaError_t launch_rows(const AttnParams &p, bool own, bool prefix, cudaStream_t
   const dim3 grid(p.H * blocks, std::max(!own ? 1 : p.budget > 0 ? p.budget : p.osplits, prefix ? p.psplits : 1), zown + (prefix ? 1 : 0));
   const cudaError_t e = allow_smem<attn_rows_kernel<CT, DP, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(32);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = p.next ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_rows_kernel<CT, DP, MT>, p, zown, pblocks, oblocks);
+  return launch_after(attn_rows_kernel<CT, DP, MT>, grid, 32, C::kSmem, s, p.next, p, zown, pblocks, oblocks);
 }
 
 // Items of the rows kernel that run on an SM at a time.
@@ -1009,7 +1000,11 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   // for codes each SM would have to be emptied in between (64 decoding rows: 79
   // -> 88 us), so there the kernels run one after the other.
   p.next = prefix && plan.ptile && !plan.otile && c.dtype != SPEC_E4M3;
-  if (prefix && plan.ptile && !plan.fuse && launch_attn_tile(p, c.dtype, true, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  p.first = 1;
+  if (prefix && plan.ptile && !plan.fuse) {
+    if (launch_attn_tile(p, c.dtype, true, s) != cudaSuccess) return SPEC_ERR_CUDA;
+    p.first = 0;
+  }
   if (plan.otile) {
     p.direct = plan.direct;
     if (launch_attn_tile(p, c.dtype, false, s) != cudaSuccess) return SPEC_ERR_CUDA;
@@ -1019,24 +1014,12 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   if ((!plan.otile || (prefix && !plan.ptile)) &&
       launch_attn_rows(p, c.dtype, !plan.otile, prefix && !plan.ptile, s) != cudaSuccess)
     return SPEC_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaError_t e;
-  if (c.dtype == SPEC_BF16)
-    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<SPEC_BF16, true>, p);
-  else if (c.dtype == SPEC_F16)
-    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<SPEC_F16, false>, p);
-  else if (p.qbf16)
-    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<SPEC_E4M3, true>, p);
-  else
-    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<SPEC_E4M3, false>, p);
+  const dim3 grid((p.rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+  auto join = [&](auto kernel) { return launch_after(kernel, grid, kJoinThreads, 0, s, true, p); };
+  const cudaError_t e = c.dtype == SPEC_BF16  ? join(attn_join_kernel<SPEC_BF16, true>)
+                        : c.dtype == SPEC_F16 ? join(attn_join_kernel<SPEC_F16, false>)
+                        : p.qbf16             ? join(attn_join_kernel<SPEC_E4M3, true>)
+                                              : join(attn_join_kernel<SPEC_E4M3, false>);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

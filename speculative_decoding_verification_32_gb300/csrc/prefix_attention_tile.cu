@@ -191,6 +191,8 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
   Ctrl *const c = reinterpret_cast<Ctrl *>(smem + C::kCtrl);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, role = tid / 128;
 
+  grid_dependency_wait();
+
   // --- the item
   int item = blockIdx.x;
   const int nsplit = PRE ? P.psplits : P.osplits;
@@ -817,6 +819,7 @@ __global__ void __launch_bounds__(kWidenThreads) attn_widen_kernel(const __grid_
   __shared__ uint32_t warp_top[4];
   __shared__ uint32_t mult[kTok];
   const int blk = blockIdx.x, g = blockIdx.y, val = blockIdx.z, tid = threadIdx.x;
+  allow_dependents();
   const int tb = blk * kTok, left = P.P - tb;
   const unsigned char *const base = (val ? P.pv : P.pk) + tb * P.ptok_stride;
   uint32_t byte = 0;
@@ -864,6 +867,7 @@ __global__ void __launch_bounds__(kWidenThreads) attn_widen_kernel(const __grid_
     to[0] = make_uint4(o[0], o[1], o[2], o[3]);
     to[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
+  grid_dependency_wait();  // over only after the mask kernel: the next kernel waits for this one alone
 }
 
 template <int CT, int DP, bool PRE>
@@ -874,8 +878,9 @@ cudaError_t launch(const AttnParams &p, cudaStream_t s) {
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<attn_tile_kernel<CT, DP, PRE>>(C::kSmem, Roles<CT == SPEC_E4M3>::kLaunch);
   if (e != cudaSuccess) return e;
-  attn_tile_kernel<CT, DP, PRE><<<static_cast<unsigned>(items), Roles<CT == SPEC_E4M3>::kThreads, C::kSmem, s>>>(p, blocks);
-  return cudaGetLastError();
+  // the mask and conversion kernels ahead of it let it start early
+  return launch_after(attn_tile_kernel<CT, DP, PRE>, dim3(static_cast<unsigned>(items)), Roles<CT == SPEC_E4M3>::kThreads,
+                      C::kSmem, s, p.first && (p.anc || p.wide), p, blocks);
 }
 
 template <int CT>
@@ -888,8 +893,7 @@ cudaError_t launch_d(const AttnParams &p, bool prefix, cudaStream_t s) {
 
 cudaError_t launch_attn_widen(const AttnParams &p, cudaStream_t s) {
   const dim3 grid((p.P + kTok - 1) / kTok, p.H, 2);
-  attn_widen_kernel<<<grid, kWidenThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(attn_widen_kernel, grid, kWidenThreads, 0, s, p.anc != nullptr, p);
 }
 
 cudaError_t launch_attn_tile(const AttnParams &p, int ctype, bool prefix, cudaStream_t s) {
