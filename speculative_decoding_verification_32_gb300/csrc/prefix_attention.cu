@@ -610,6 +610,7 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
     st = st == C::kStages - 1 ? 0 : st + 1;
   }
   cp_async_wait_all();
+  allow_dependents();  // the join's blocks may take the places that come free
 
   if (!pre && lane == 0) P.oflag[flag] = odd;
 #pragma unroll
