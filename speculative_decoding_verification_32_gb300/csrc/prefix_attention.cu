@@ -31,7 +31,7 @@ namespace {
 constexpr int kSms = 152;           // parts are sized for this many SMs
 constexpr float kRowLazy = 8.f;
 constexpr int kMaskThreads = 256;
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
 
 // ---------------------------------------------------------------- tree mask
 __global__ void __launch_bounds__(kMaskThreads) attn_mask_kernel(const int32_t *parent, const int32_t *kv_len,
@@ -697,13 +697,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
       float2 ml = ml0;
       if (s0 > 0) ml = s0 + lane < nslots ? P.ml[static_cast<long long>(s0 + lane) * P.rows + r] : make_float2(-INFINITY, -INFINITY);
       const float wl = ex2(ml.x - z);
-      // the parts that left a sum, four at a time: their loads overlap
+      // the parts that left a sum, eight at a time: their loads overlap
       unsigned todo = __ballot_sync(FULL_MASK, ml.y != -INFINITY);
       while (todo) {
-        float4 x[4];
-        float w[4];
+        float4 x[8];
+        float w[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
           const int k = todo ? __ffs(todo) - 1 : -1;
           todo &= todo - 1;
           w[j] = __shfl_sync(FULL_MASK, wl, k & 31);
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
             x[j] = *reinterpret_cast<const float4 *>(P.part + (static_cast<long long>(s0 + k) * P.rows + r) * P.D + lane * 4);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
           acc[0] = fmaf(w[j], x[j].x, acc[0]);
           acc[1] = fmaf(w[j], x[j].y, acc[1]);
           acc[2] = fmaf(w[j], x[j].z, acc[2]);

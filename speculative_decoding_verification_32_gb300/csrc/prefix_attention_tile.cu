@@ -598,15 +598,33 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
       const int my = PRE ? 0 : min((r0 + rr) / P.G, P.N - 1);  // the row's token
       const uint32_t *const anc = PRE || !P.anc ? nullptr : P.anc + (static_cast<size_t>(b) * P.N + my) * P.W;
       float m = -INFINITY, l = 0.f, E = E4 ? kMinExponent : 0.f;
+      const float *const wscale = E4 && P.wide ? P.wide_scale + static_cast<long long>(g) * npre : nullptr;
+      float kscale = 1.f, vexp = 0.f;
+      if (E4 && P.wide && q0 < npre) {
+        kscale = __ldg(wscale + q0);
+        vexp = __ldg(wscale + static_cast<long long>(P.H) * npre + q0);
+      }
       bool live = true;
       for (int k = 0; k < n; ++k) {
         live = wait_for(c, &c->sfull[tile], k & 1, limit);
         float ex = 0.f, sc = base_sc, grow = 0.f;
         if constexpr (E4) {
-          if (live) live = wait_for(c, &c->vfull[k & 1], (k >> 1) & 1, limit);
-          sc *= c->ksc[k & 1];
-          ex = c->vex[k & 1];
-          const float En = c->vtop[k & 1];
+          float En;
+          if ((PRE || q0 + k < npre) && P.wide) {
+            // a converted prefix's scales, read a block ahead: the softmax need not wait for the values
+            sc *= kscale;
+            ex = vexp;
+            En = fmaxf(E, ex);
+            if (k + 1 < n && q0 + k + 1 < npre) {
+              kscale = __ldg(wscale + q0 + k + 1);
+              vexp = __ldg(wscale + static_cast<long long>(P.H) * npre + q0 + k + 1);
+            }
+          } else {
+            if (live) live = wait_for(c, &c->vfull[k & 1], (k >> 1) & 1, limit);
+            sc *= c->ksc[k & 1];
+            ex = c->vex[k & 1];
+            En = c->vtop[k & 1];
+          }
           grow = En - E;
           E = En;
         }
