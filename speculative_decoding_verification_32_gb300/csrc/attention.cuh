@@ -31,6 +31,7 @@ struct AttnParams {
   // values' scale exponent
   unsigned char *wide;
   float *wide_scale;
+  int32_t *wide_far;  // ... whether the block's scales lie too far apart for fp16
   long long row_stride, tok_stride, ptok_stride, slots;
   int P;  // prefix length
   // queries
@@ -254,6 +255,11 @@ __device__ __forceinline__ float odd_value(const AttnParams &P, int b, int t, in
   return isfinite(val) ? 0.f : val;
 }
 
+// A query's element.
+__device__ __forceinline__ float query_value(unsigned short u, int bf16) {
+  return bf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u));
+}
+
 // 32 bytes, a whole sector, aligned to 32
 __device__ __forceinline__ void st_global_v8(float *p, const uint32_t *r) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
@@ -302,7 +308,7 @@ cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t sm
 
 // Host launchers.
 // attn_rows_kernel over the own entries (own) and the prefix (prefix).
-cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool own, bool prefix, cudaStream_t s);
+cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool prefix, cudaStream_t s);
 // The prefix of an e4m3 cache into P.wide; runs beside the mask kernel, if there is one.
 cudaError_t launch_attn_widen(const AttnParams &p, cudaStream_t s);
 // attn_tile_kernel over the prefix, or over the own entries.

@@ -747,13 +747,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 
 // -------------------------------------------------------------------- host
 template <int CT, int DP, int MT>
-cudaError_t launch_rows(const AttnParams &p, bool own, bool prefix, cudaStream_t s) {
+cudaError_t launch_rows(const AttnParams &p, bool prefix, cudaStream_t s) {
   using C = RowCfg<CT, DP, MT>;
   const int pblocks = static_cast<int>((static_cast<long long>(p.B) * p.N * p.G + C::kM - 1) / C::kM);
   const int oblocks = (p.N * p.G + C::kM - 1) / C::kM;
-  const int blocks = std::max(own ? oblocks : 0, prefix ? pblocks : 0);
-  const int zown = !own ? 0 : p.budget > 0 ? 1 : p.B;
-  const dim3 grid(p.H * blocks, std::max(!own ? 1 : p.budget > 0 ? p.budget : p.osplits, prefix ? p.psplits : 1), zown + (prefix ? 1 : 0));
+  const int blocks = std::max(oblocks, prefix ? pblocks : 0);
+  const int zown = p.budget > 0 ? 1 : p.B;
+  const dim3 grid(p.H * blocks, std::max(p.budget > 0 ? p.budget : p.osplits, prefix ? p.psplits : 1), zown + (prefix ? 1 : 0));
   const cudaError_t e = allow_smem<attn_rows_kernel<CT, DP, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
   return launch_after(attn_rows_kernel<CT, DP, MT>, grid, 32, C::kSmem, s, p.next, p, zown, pblocks, oblocks);
@@ -770,10 +770,10 @@ int rows_per_sm(int dtype, int oblk) {
 bool two_row_tiles(int B, int N, int G, bool prefix) { return N * G > 16 || (prefix && static_cast<long long>(B) * N * G > 16); }
 
 template <int CT>
-cudaError_t launch_rows_d(const AttnParams &p, bool own, bool prefix, cudaStream_t s) {
+cudaError_t launch_rows_d(const AttnParams &p, bool prefix, cudaStream_t s) {
   const bool two = two_row_tiles(p.B, p.N, p.G, prefix);
-  if (p.D <= 64) return two ? launch_rows<CT, 64, 2>(p, own, prefix, s) : launch_rows<CT, 64, 1>(p, own, prefix, s);
-  return two ? launch_rows<CT, 128, 2>(p, own, prefix, s) : launch_rows<CT, 128, 1>(p, own, prefix, s);
+  if (p.D <= 64) return two ? launch_rows<CT, 64, 2>(p, prefix, s) : launch_rows<CT, 64, 1>(p, prefix, s);
+  return two ? launch_rows<CT, 128, 2>(p, prefix, s) : launch_rows<CT, 128, 1>(p, prefix, s);
 }
 
 struct AttnPlan {
@@ -782,7 +782,7 @@ struct AttnPlan {
   bool fuse, direct;  // own items take the prefix too; and nothing is left to join
   bool widen;         // an e4m3 prefix is turned into fp16 first
   int oblk;           // query rows per own item
-  size_t rows, anc_at, info_at, flag_at, count_at, ml_at, part_at, wide_at, scale_at, bytes;
+  size_t rows, anc_at, info_at, flag_at, count_at, ml_at, part_at, wide_at, scale_at, far_at, bytes;
 };
 
 size_t at_round(size_t x) { return (x + 255) / 256 * 256; }
@@ -825,7 +825,7 @@ AttnPlan plan_attention(const spec_attention_args *a) {
   // more than 32 query rows per KV head would read the keys again for each 32
   p.ptile = q * G > 32;
   p.otile = a->N * G > 32;
-  // rows kernel: 12 items per SM, no part under 64 tokens
+  // rows kernel: 8 items per SM, no part under 64 tokens
   auto row_parts = [](long long blocks, long long tokens) {
     const long long want = (8 * kSms + blocks - 1) / blocks;
     return static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 64})));
@@ -894,6 +894,8 @@ AttnPlan plan_attention(const spec_attention_args *a) {
     at += at_round(static_cast<size_t>(a->prefix_len) * c.heads * c.head_dim * 4);
     p.scale_at = at;
     at += at_round(static_cast<size_t>((a->prefix_len + 127) / 128) * c.heads * 2 * 4);
+    p.far_at = at;
+    at += at_round(static_cast<size_t>((a->prefix_len + 127) / 128) * c.heads * 2 * 4);
   }
   p.bytes = at + 256;
   return p;
@@ -901,10 +903,10 @@ AttnPlan plan_attention(const spec_attention_args *a) {
 
 }  // namespace
 
-cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool own, bool prefix, cudaStream_t s) {
-  if (ctype == SPEC_E4M3) return launch_rows_d<SPEC_E4M3>(p, own, prefix, s);
-  if (ctype == SPEC_BF16) return launch_rows_d<SPEC_BF16>(p, own, prefix, s);
-  return launch_rows_d<SPEC_F16>(p, own, prefix, s);
+cudaError_t launch_attn_rows(const AttnParams &p, int ctype, bool prefix, cudaStream_t s) {
+  if (ctype == SPEC_E4M3) return launch_rows_d<SPEC_E4M3>(p, prefix, s);
+  if (ctype == SPEC_BF16) return launch_rows_d<SPEC_BF16>(p, prefix, s);
+  return launch_rows_d<SPEC_F16>(p, prefix, s);
 }
 
 }  // namespace sv
@@ -993,6 +995,7 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   if (plan.widen) {
     p.wide = reinterpret_cast<unsigned char *>(w + plan.wide_at);
     p.wide_scale = reinterpret_cast<float *>(w + plan.scale_at);
+    p.wide_far = reinterpret_cast<int32_t *>(w + plan.far_at);
     if (launch_attn_widen(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
   }
   const bool prefix = p.P > 0;
@@ -1012,8 +1015,8 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
     if (plan.direct) return SPEC_OK;
     p.direct = 0;
   }
-  if ((!plan.otile || (prefix && !plan.ptile)) &&
-      launch_attn_rows(p, c.dtype, !plan.otile, prefix && !plan.ptile, s) != cudaSuccess)
+  if (!plan.otile &&
+      launch_attn_rows(p, c.dtype, prefix && !plan.ptile, s) != cudaSuccess)
     return SPEC_ERR_CUDA;
   const dim3 grid((p.rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
   auto join = [&](auto kernel) { return launch_after(kernel, grid, kJoinThreads, 0, s, true, p); };

@@ -20,8 +20,9 @@
 //   - four warps bring keys and values into shared memory, two buffers each:
 //     16-bit entries by asynchronous copies, e4m3 codes through registers as
 //     fp16 numbers relative to the block's largest scale (exact for scales
-//     down to 2^-15 of it, off by at most 2^-25 of it below), so that the
-//     block's scale is one factor on the scores and one on the sums.
+//     down to 2^-15 of it), so that the block's scale is one factor on the
+//     scores and one on the sums.  A part with a block whose scales lie further
+//     apart is taken once more in fp32 (exact_part).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -67,7 +68,7 @@ struct Ctrl {
   uint32_t tmem;
   int abort;
   int odd;
-  int pad;
+  int far_apart;            // scales that the conversion or the sums do not span: exact_part
   float ksc[2];             // per buffer: the block's scale of the keys
   float vex[2], vtop[2];    // the values' exponent, and the largest so far
   uint32_t red[2][4];       // producers' reductions
@@ -76,6 +77,11 @@ struct Ctrl {
   long long qoff[256];      // where a query row's elements are; -1: past the last
 };
 static_assert(sizeof(Ctrl) <= 7168, "control block");
+// scale bytes up to this (2^-120) hold nothing that counts beside others
+constexpr uint32_t kLeastScale = 7;
+// l counts in units of 2^(m - E): with exponents no further apart than this it
+// stays in fp32's range for any number of tokens
+constexpr float kSumSpan = 80.f;
 constexpr int kUnused = 1 << 30;  // the row has no such query (its answer is empty)
 
 // ------------------------------------------------------------ tcgen05 wrappers
@@ -176,6 +182,109 @@ __device__ __forceinline__ bool wait_for(Ctrl *c, uint64_t *bar, uint32_t parity
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
+// A query's sums over blocks q0 .. q0 + n - 1 of an e4m3 cache from the codes, in
+// fp32, by one thread: for parts in which scales lie further apart than fp16
+// numbers relative to the largest can hold (a token that nothing sees, or whose
+// weight is nothing, must not cost the others their bits).  Slower than the
+// tensor cores by two orders, and not met by scales within 2^15 of one another.
+template <int DP>
+__device__ __forceinline__ void exact_part(const AttnParams &P, int b, int g, int q0, int n, int npre, int len0, int len, int my,
+                                           const uint32_t *anc, bool use, long long qoff, long long orow, int slot, bool odd) {
+  const unsigned short *const q = static_cast<const unsigned short *>(P.q) + qoff;
+  float m = -INFINITY, top = -INFINITY, l = 0.f, z = -INFINITY;
+  // the first round: maxima and the sum of the softmax; then 32 columns a round
+#pragma unroll 1
+  for (int d0 = -32; d0 < P.D; d0 += 32) {
+    float o[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) o[j] = 0.f;
+#pragma unroll 1
+    for (int k = 0; use && k < n; ++k) {
+      const bool pre = q0 + k < npre;
+      const int tb = (pre ? q0 + k : q0 + k - npre) * kTok, end = min(tb + kTok, pre ? P.P : len);
+      const long long ts = pre ? P.ptok_stride : P.tok_stride;
+      const unsigned char *const kb = pre ? P.pk : P.k + b * P.row_stride, *const vb = pre ? P.pv : P.v + b * P.row_stride;
+#pragma unroll 1
+      for (int t = tb; t < end; ++t) {
+        const int own = pre ? -1 : t - len0;  // index among the pass's own tokens
+        if (own >= 0 && !(anc ? __ldg(anc + (own >> 5)) >> (own & 31) & 1u : own <= my)) continue;
+        const unsigned char *const ke = kb + t * ts, *const ve = vb + t * ts;
+        float x = 0.f;
+#pragma unroll 1
+        for (int d = 0; d < P.D; d += 16) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4 *>(ke + static_cast<long long>(g) * P.D + d));
+          const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t h = e & 1 ? e4m3x2_to_f16x2_hi(cw[e / 2]) : e4m3x2_to_f16x2(cw[e / 2]);
+            const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            x = fmaf(query_value(q[d + 2 * e], P.qbf16), y.x, x);
+            x = fmaf(query_value(q[d + 2 * e + 1], P.qbf16), y.y, x);
+          }
+        }
+        x = x * e4m3_scale(__ldg(ke + static_cast<long long>(P.H) * P.D + g)) * P.scale;
+        const uint32_t vc = __ldg(ve + static_cast<long long>(P.H) * P.D + g);
+        const float xe = x + (vc == 255u ? 0.f : scale_exponent(vc));
+        if (d0 < 0) {
+          m = fmaxf(m, xe);
+          if (x > top) {
+            l *= ex2(top - x);
+            top = x;
+          }
+          l += x == -INFINITY ? 0.f : ex2(x - top);
+          continue;
+        }
+        const float w = ex2(xe - m);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (d0 + c * 16 >= P.D) continue;
+          const uint4 u = __ldg(reinterpret_cast<const uint4 *>(ve + static_cast<long long>(g) * P.D + d0 + c * 16));
+          const uint32_t cw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t h = e & 1 ? e4m3x2_to_f16x2_hi(cw[e / 2]) : e4m3x2_to_f16x2(cw[e / 2]);
+            float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            if (vc == 255u) y.x = y.y = __uint_as_float(0x7fc00000u);
+            if (own >= 0) {  // put into the answers at the end, as in every part
+              if (!isfinite(y.x)) y.x = 0.f;
+              if (!isfinite(y.y)) y.y = 0.f;
+            }
+            o[c * 16 + 2 * e] = fmaf(w, y.x, o[c * 16 + 2 * e]);
+            o[c * 16 + 2 * e + 1] = fmaf(w, y.y, o[c * 16 + 2 * e + 1]);
+          }
+        }
+      }
+    }
+    const bool some = use && l != 0.f;
+    if (d0 < 0) {
+      z = some ? top + log2f(l) : -INFINITY;
+      if (!P.direct)
+        P.ml[static_cast<long long>(slot) * P.rows + orow] = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
+      else if (P.lse)
+        P.lse[orow] = kLn2 * z;
+      continue;
+    }
+    if (P.direct) {
+      const float w = some ? ex2(m - z) : 0.f;
+      unsigned short *const to = static_cast<unsigned short *>(P.out) + orow * P.D + d0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        if (d0 + j >= P.D) continue;
+        float y = some ? o[j] * w : 0.f;
+        if (some && odd)
+          for (int t = 0; t < len - len0; ++t)
+            if (anc ? __ldg(anc + (t >> 5)) >> (t & 31) & 1u : t <= my) y += odd_value<SPEC_E4M3>(P, b, len0 + t, g, d0 + j);
+        to[j] = static_cast<unsigned short>(P.qbf16 ? pack16<true>(y, 0.f) : pack16<false>(y, 0.f));
+      }
+    } else if (some) {
+      float *const to = P.part + (static_cast<long long>(slot) * P.rows + orow) * P.D + d0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (d0 + j < P.D) to[j] = o[j];
+    }
+  }
+}
+
 // Items.  PRE: the prefix alone, for (KV head, block of 256 rows of all rows'
 // queries, part).  Else (row, KV head, block of 256 of the row's queries,
 // part) against the row's own entries, after the prefix's if P.fuse; with one
@@ -253,6 +362,7 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
     mbar_init(&c->drain, 1);
     c->abort = 0;
     c->odd = 0;
+    c->far_apart = 0;
     fence_mbar_init();
   }
   if (warp == R::kIssueWarp) tc_alloc(&c->tmem);
@@ -337,8 +447,13 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
       cp_async_commit();
       return byte;
     };
-    float E = kMinExponent, kscale = 1.f;
+    float E = kMinExponent, low = 0.f, kscale = 1.f;  // the largest and smallest exponent of a block of values
     uint32_t sc0 = issue(0), sc1 = issue(1);
+    if (E4 && P.wide) {
+      const int32_t *const far = P.wide_far + static_cast<long long>(g) * npre;
+      for (int q = q0 + pt; q < min(npre, q0 + n); q += kProducers)
+        if (__ldg(far + q) | __ldg(far + static_cast<long long>(P.H) * npre + q)) c->far_apart = 1;
+    }
     for (int it = 0; it < 2 * n; ++it) {
       cp_async_wait<1>();
       const int k = it >> 1, s = k & 1, q = q0 + k;
@@ -374,7 +489,9 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         if (val) {
           const float ex = __uint_as_float(sc0);
           E = fmaxf(E, ex);
+          low = fminf(low, ex);
           if (pt == 0) {
+            if (E - low > kSumSpan) c->far_apart = 1;
             c->ksc[s] = kscale;
             c->vex[s] = ex;
             c->vtop[s] = E;
@@ -398,12 +515,15 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         if (val) {
           E = fmaxf(E, ex);
           ex = fmaxf(ex, E - kExponentSpan);
+          low = fminf(low, ex);
+          if (pt == 0 && E - low > kSumSpan) c->far_apart = 1;
         }
         {
           // 2^(scale - block's scale) as fp16: exact down to 2^-24, zero below
           const int d = static_cast<int>(sc0) - (static_cast<int>(ex) + 127);
           const uint32_t f = sc0 == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
           c->mult[it & 1][pt] = f | f << 16;
+          if (d < -15 && sc0 > kLeastScale && sc0 != 255u) c->far_apart = 1;
         }
         producer_sync<kProducers>();
         const uint32_t dst = buf + (pc / 4) * 16384 + row0 * 128;
@@ -766,7 +886,10 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         tc_fence_after();
         const bool some = at >= 0 && at < kUnused && l != 0.f;
         const float z = some ? m + log2f(l) - E : -INFINITY;
-        if (P.direct) {  // every thread loads: tensor memory is read by whole warps
+        if (E4 && c->far_apart) {
+          if (at >= 0)
+            exact_part<DP>(P, b, g, q0, n, npre, len0, len, my, anc, at < kUnused, c->qoff[rr], orow, slot, c->odd);
+        } else if (P.direct) {  // every thread loads: tensor memory is read by whole warps
           const float w = some ? ex2(m - z) : 0.f;
           const bool odd = some && c->odd;
           if (at >= 0 && P.lse) P.lse[orow] = kLn2 * z;
@@ -841,6 +964,7 @@ __global__ void __launch_bounds__(kWidenThreads) attn_widen_kernel(const __grid_
   const int tb = blk * kTok, left = P.P - tb;
   const unsigned char *const base = (val ? P.pv : P.pk) + tb * P.ptok_stride;
   uint32_t byte = 0;
+  int far = 0;
   if (tid < kTok) {
     if (tid < left) byte = __ldg(base + tid * P.ptok_stride + static_cast<long long>(P.H) * P.D + g);
     const uint32_t top = __reduce_max_sync(FULL_MASK, byte == 255u ? 1u : max(byte, 1u));
@@ -857,15 +981,17 @@ __global__ void __launch_bounds__(kWidenThreads) attn_widen_kernel(const __grid_
   }
   __syncthreads();
   // scales below 2^-120 count as that: nothing they hold is seen beside the least exponent of the sums
-  const int ref = max(7, static_cast<int>(max(max(warp_top[0], warp_top[1]), max(warp_top[2], warp_top[3]))));
+  const int ref = max(static_cast<int>(kLeastScale), static_cast<int>(max(max(warp_top[0], warp_top[1]), max(warp_top[2], warp_top[3]))));
   if (tid < kTok) {
     const int d = static_cast<int>(byte) - ref;
     const uint32_t f = byte == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
     mult[tid] = f | f << 16;
+    far = d < -15 && byte > kLeastScale && byte != 255u;
   }
+  far = __syncthreads_or(far);
+  if (tid == 0) P.wide_far[(static_cast<long long>(val ? P.H : 0) + g) * gridDim.x + blk] = far;
   if (tid == 0)
     P.wide_scale[(static_cast<long long>(val ? P.H : 0) + g) * gridDim.x + blk] = val ? static_cast<float>(ref - 127) : e4m3_scale(ref);
-  __syncthreads();
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
     const int x = i * kWidenThreads + tid, t = x / parts, pc = x - t * parts;

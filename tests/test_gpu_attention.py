@@ -463,3 +463,39 @@ def test_rows_cut_by_a_budget(sv, kind, qt, B, N, Hq, H, D, P, top):
     out, lse = p.check(rows=[2, 3, 7, 8, B - 1], status=[8 if b in bad else 0 for b in range(B)])
     assert bool((lse[bad] == float("-inf")).all())
     assert float(out[bad].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("qt", ["bfloat16", "float16"])
+@pytest.mark.parametrize("B,N,D,P,top,tree", [
+    (1, 50, 64, 200, 20, True),     # prefix and own entries in one item, cut into parts
+    (2, 60, 128, 300, 150, True),   # a prefix that is converted once
+    (80, 32, 128, 256, 100, True),  # no join
+    (40, 6, 64, 500, 60, False),    # the prefix alone
+])
+def test_e4m3_scales_far_apart_in_tiles(sv, qt, B, N, D, P, top, tree):
+    """Values and keys 2^40 to 2^100 apart within 128 tokens: a token of the pass that most queries do
+    not see, one of the prefix whose weight is nothing, tiny ones and zeros beside them."""
+    import torch
+    lens = np.random.default_rng(B).integers(0, top, B)
+    p = Problem(sv, B, N, 8, 2, D, P, lens, "uint8", qt, tree, seed=D)
+    p.q = p.q.abs() + 1
+    p.qx = p.q.cpu().double().numpy()
+    zeros = torch.zeros(B, dtype=torch.int32, device="cuda")
+    total = torch.from_numpy(np.asarray(lens + N, np.int32)).cuda()
+    k, v = (torch.from_numpy(x).float().cuda() for x in (p.kx, p.vx))
+    for b in range(0, B, 3):
+        at = int(lens[b]) + N // 2
+        k[b, at] *= 2.0**40
+        v[b, at] *= 2.0**40
+    sv.spec_kv_append(p.cache, k, v, zeros, count=total)
+    kx, vx, _ = sv.spec_kv_read(p.cache, total, p.S, heads=2, head_dim=D, dtype=torch.float32)
+    p.kx, p.vx = kx.cpu().double().numpy(), vx.cpu().double().numpy()
+    pk, pv = (torch.from_numpy(x).float().cuda()[None] for x in (p.pk, p.pv))
+    pk[0, 7], pv[0, 7] = -8.0, pv[0, 7] * 2.0**60      # scores so low that the weight is 0 in 64 bits' reach
+    pv[0, 20:30] *= 2.0**-40
+    pk[0, 40] *= 2.0**-60
+    pk[0, 41], pv[0, 41] = 0.0, 0.0
+    sv.spec_kv_append(p.prefix, pk, pv, zeros[:1])
+    kx, vx, _ = sv.spec_kv_read(p.prefix, total[:1] * 0 + P, P, heads=2, head_dim=D, dtype=torch.float32)
+    p.pk, p.pv = kx[0].cpu().double().numpy(), vx[0].cpu().double().numpy()
+    p.check(rows=range(min(B, 4)))
