@@ -480,7 +480,11 @@ _here = _Here()
 
 def _scratch(dev, stream, nbytes):
     """A workspace of these calls' own: the verify calls keep a header and
-    stamped records in theirs."""
+    stamped records in theirs.  A call captured into a graph gets one from the
+    graph's pool: a replay may run beside later calls, and after the stream's
+    workspace has grown into another buffer."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     buf = _ws.get((dev, "scratch", stream))
     if buf is not None and buf.numel() >= nbytes:
         return buf

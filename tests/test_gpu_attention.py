@@ -499,3 +499,29 @@ def test_e4m3_scales_far_apart_in_tiles(sv, qt, B, N, D, P, top, tree):
     kx, vx, _ = sv.spec_kv_read(p.prefix, total[:1] * 0 + P, P, heads=2, head_dim=D, dtype=torch.float32)
     p.pk, p.pv = kx[0].cpu().double().numpy(), vx[0].cpu().double().numpy()
     p.check(rows=range(min(B, 4)))
+
+
+def test_graphs_have_workspaces_of_their_own(sv):
+    """Two graphs captured on one stream and replayed side by side, after eager calls of other sizes."""
+    import torch
+    from speculative_decoding_verification_32_gb300 import _binding
+    ps = [Problem(sv, 4, 6, 8, 2, 128, 600, [30, 900, 5, 77], kind, "bfloat16", seed=40) for kind in ("uint8", "bfloat16")]
+    want = [p.check() for p in ps]
+    lens = torch.from_numpy(ps[0].lens).cuda()
+    before = dict(_binding._ws)
+    graphs, got = [], []
+    for p in ps:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(sv.spec_prefix_attention(p.q, p.cache, lens, prefix=p.prefix, kv_heads=2))
+    assert _binding._ws.keys() == before.keys() and all(_binding._ws[x] is before[x] for x in before)
+    Problem(sv, 9, 30, 8, 2, 128, 3000, [500] * 9, "uint8", seed=41).call()
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (out, lse), (o, ls, _) in zip(want, got):
+        assert torch.equal(out, o) and torch.equal(lse, ls)
