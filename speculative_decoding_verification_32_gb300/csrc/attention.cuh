@@ -236,11 +236,14 @@ __device__ __forceinline__ float scale_exponent(uint32_t c) {
   return c == 255u ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(c) - 127);
 }
 // sum_t 2^(x_t - m) is kept as l 2^-E, E the largest scale exponent met so far
-// (at least kMinExponent), so that it stays in range for all scales; a token
+// (at least kMinExponent), so that it stays in range for scales this near; a token
 // whose scale is more than 2^kExponentSpan below the largest counts with that
-// span and takes the rest of the factor on its weight.
+// span and takes the rest of the factor on its weight.  That is right for the
+// least scales (bytes up to kLeastScale, 2^-120: zero vectors), whose weight is
+// nothing; where others lie that far apart, the kernels go other ways.
 constexpr float kMinExponent = -60.f;
 constexpr float kExponentSpan = 60.f;
+constexpr uint32_t kLeastScale = 7;
 constexpr float kLn2 = 0.693147180559945309f;
 
 // A value of row b's own entry in slot t if it is not finite, else 0.
@@ -258,6 +261,111 @@ __device__ __forceinline__ float odd_value(const AttnParams &P, int b, int t, in
 // A query's element.
 __device__ __forceinline__ float query_value(unsigned short u, int bf16) {
   return bf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u));
+}
+
+// A query's sums over tokens p0 .. p1 - 1 of the prefix and t0 .. t1 - 1 of its row's
+// own e4m3 entries from the codes, in fp32, by one thread: for parts in which
+// scales lie further apart than the kernels' ways span (a token that nothing
+// sees, or whose weight is nothing, must not cost the others their bits).
+// Slower by two orders, and not met by scales within 2^15 of one another.
+// len0: own entries that every query sees; my, anc: the query's index and
+// ancestor bits; qoff: where it is; odd: values of the pass's own tokens that
+// are not finite are to be put into an answer that is written here (P.direct).
+__device__ __forceinline__ void exact_part(const AttnParams &P, int b, int g, int p0, int p1, int t0, int t1, int len0, int cnt, int my,
+                                           const uint32_t *anc, bool use, long long qoff, long long orow, int slot, bool odd) {
+  const unsigned short *const q = static_cast<const unsigned short *>(P.q) + qoff;
+  float m = -INFINITY, top = -INFINITY, l = 0.f, z = -INFINITY;
+  // the first round: maxima and the sum of the softmax; then 32 columns a round
+#pragma unroll 1
+  for (int d0 = -32; d0 < P.D; d0 += 32) {
+    float o[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) o[j] = 0.f;
+#pragma unroll 1
+    for (int part = 0; use && part < 2; ++part) {
+      const bool pre = part == 0;
+      const int end = pre ? p1 : t1;
+      const long long ts = pre ? P.ptok_stride : P.tok_stride;
+      const unsigned char *const kb = pre ? P.pk : P.k + b * P.row_stride, *const vb = pre ? P.pv : P.v + b * P.row_stride;
+#pragma unroll 1
+      for (int t = pre ? p0 : t0; t < end; ++t) {
+        const int own = pre ? -1 : t - len0;  // index among the pass's own tokens
+        if (own >= 0 && !(anc ? __ldg(anc + (own >> 5)) >> (own & 31) & 1u : own <= my)) continue;
+        const unsigned char *const ke = kb + t * ts, *const ve = vb + t * ts;
+        float x = 0.f;
+#pragma unroll 1
+        for (int d = 0; d < P.D; d += 16) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4 *>(ke + static_cast<long long>(g) * P.D + d));
+          const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t h = e & 1 ? e4m3x2_to_f16x2_hi(cw[e / 2]) : e4m3x2_to_f16x2(cw[e / 2]);
+            const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            x = fmaf(query_value(q[d + 2 * e], P.qbf16), y.x, x);
+            x = fmaf(query_value(q[d + 2 * e + 1], P.qbf16), y.y, x);
+          }
+        }
+        x = x * e4m3_scale(__ldg(ke + static_cast<long long>(P.H) * P.D + g)) * P.scale;
+        const uint32_t vc = __ldg(ve + static_cast<long long>(P.H) * P.D + g);
+        const float xe = x + (vc == 255u ? 0.f : scale_exponent(vc));
+        if (d0 < 0) {
+          m = fmaxf(m, xe);
+          if (x > top) {
+            l *= ex2(top - x);
+            top = x;
+          }
+          l += x == -INFINITY ? 0.f : ex2(x - top);
+          continue;
+        }
+        const float w = ex2(xe - m);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (d0 + c * 16 >= P.D) continue;
+          const uint4 u = __ldg(reinterpret_cast<const uint4 *>(ve + static_cast<long long>(g) * P.D + d0 + c * 16));
+          const uint32_t cw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t h = e & 1 ? e4m3x2_to_f16x2_hi(cw[e / 2]) : e4m3x2_to_f16x2(cw[e / 2]);
+            float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            if (vc == 255u) y.x = y.y = __uint_as_float(0x7fc00000u);
+            if (own >= 0) {  // put into the answers at the end, as in every part
+              if (!isfinite(y.x)) y.x = 0.f;
+              if (!isfinite(y.y)) y.y = 0.f;
+            }
+            o[c * 16 + 2 * e] = fmaf(w, y.x, o[c * 16 + 2 * e]);
+            o[c * 16 + 2 * e + 1] = fmaf(w, y.y, o[c * 16 + 2 * e + 1]);
+          }
+        }
+      }
+    }
+    const bool some = use && l != 0.f;
+    if (d0 < 0) {
+      z = some ? top + log2f(l) : -INFINITY;
+      if (!P.direct)
+        P.ml[static_cast<long long>(slot) * P.rows + orow] = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
+      else if (P.lse)
+        P.lse[orow] = kLn2 * z;
+      continue;
+    }
+    if (P.direct) {
+      const float w = some ? ex2(m - z) : 0.f;
+      unsigned short *const to = static_cast<unsigned short *>(P.out) + orow * P.D + d0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        if (d0 + j >= P.D) continue;
+        float y = some ? o[j] * w : 0.f;
+        if (some && odd)
+          for (int t = 0; t < cnt; ++t)
+            if (anc ? __ldg(anc + (t >> 5)) >> (t & 31) & 1u : t <= my) y += odd_value<SPEC_E4M3>(P, b, len0 + t, g, d0 + j);
+        to[j] = static_cast<unsigned short>(P.qbf16 ? pack16<true>(y, 0.f) : pack16<false>(y, 0.f));
+      }
+    } else if (some) {
+      float *const to = P.part + (static_cast<long long>(slot) * P.rows + orow) * P.D + d0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (d0 + j < P.D) to[j] = o[j];
+    }
+  }
 }
 
 // 32 bytes, a whole sector, aligned to 32

@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kSms = 152;           // parts are sized for this many SMs
 constexpr float kRowLazy = 8.f;
+constexpr float kExponentGrowth = 20.f, kFarApart = -INFINITY;
 constexpr int kMaskThreads = 256;
 constexpr int kJoinThreads = 128;
 
@@ -313,6 +314,9 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
   float o[MT][kNt][4];
   float mx[MT][2], l[MT][2];
   float E = kMinExponent;  // l counts in units of 2^(mx - E), E the largest scale exponent so far
+  // what E may grow to after the first block that holds more than the least
+  // scales; kFarApart: scales lie too far apart for such units
+  float limit = INFINITY;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     mx[mt][0] = mx[mt][1] = -INFINITY;
@@ -384,11 +388,15 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(sst + lane * 4) : "memory");
       const uint32_t byte = w >> (8 * (g & 3)) & 255u;
       const float e = scale_exponent(byte);
-      const float En = fmaxf(E, static_cast<float>(__reduce_max_sync(FULL_MASK, lane < kBlk || byte == 255u ? -127 : static_cast<int>(byte) - 127)));
+      const int most = __reduce_max_sync(FULL_MASK, lane < kBlk || byte == 255u ? -127 : static_cast<int>(byte) - 127);
+      const float En = fmaxf(E, static_cast<float>(most));
+      if (En > limit) limit = kFarApart;
+      if (limit == INFINITY && most + 127 > static_cast<int>(kLeastScale)) limit = En + kExponentGrowth;
       dE = En - E;
       E = En;
       const bool low = lane >= kBlk && e < E - kExponentSpan;
       small = __any_sync(FULL_MASK, low);
+      if (small && __any_sync(FULL_MASK, low && byte > kLeastScale)) limit = kFarApart;
       const float ec = low ? E - kExponentSpan : e;
       const uint32_t tab = smem_u32(smem) + C::kSmem - C::kTable;
       if (lane < kBlk)
@@ -613,6 +621,16 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
   allow_dependents();  // the join's blocks may take the places that come free
 
   if (!pre && lane == 0) P.oflag[flag] = odd;
+  if (E4 && limit == kFarApart) {
+    if (my_row >= 0) {
+      const int h = my_row % P.Hq, t = my_row / P.Hq, qb = t / P.N, qt = t - qb * P.N;
+      const uint32_t *const anc = pre || !P.anc ? nullptr : P.anc + static_cast<size_t>(t) * P.W;
+      exact_part(P, b, g, pre ? t0 : 0, pre ? t1 : 0, pre ? 0 : t0, pre ? 0 : t1, len0, cnt, qt, anc, my_use,
+                 qb * P.qs[0] + qt * P.qs[1] + h * P.qs[2], my_row, slot, false);
+    }
+    grid_dependency_wait();
+    return;
+  }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll

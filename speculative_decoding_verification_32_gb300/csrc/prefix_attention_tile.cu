@@ -39,14 +39,16 @@ namespace {
 constexpr int kTok = 128;          // tokens per block, a producer thread each
 // Groups of 128 threads: softmax of tiles A and B, producers, tensor-core
 // issue.  Their registers per thread add up to what the block is launched
-// with.  (Two groups of producers for codes, at 96 registers a thread: 288 us
-// where one group takes 267, 32 trees of 60 nodes behind 4097 tokens.)
+// with, and are split so that no role's loop spills: with 160 for the softmax
+// and 120 for producers of codes, 32 trees of 60 nodes behind 4097 tokens take
+// 212 us where this split takes 200.  (Two groups of producers, 96 registers a
+// thread, were 8 % slower than one.)
 template <bool E4>
 struct Roles {
   static constexpr int kGroups = 4, kThreads = 128 * kGroups, kProducers = 128;
   static constexpr int kIssueWarp = 4 * (kGroups - 1);
   static constexpr int kLaunch = 128;  // registers per thread at launch: 65536 / kThreads
-  static constexpr int kSoftmax = E4 ? 160 : 176, kProduce = E4 ? 120 : 88, kIssue = 72;
+  static constexpr int kSoftmax = E4 ? 176 : 184, kProduce = E4 ? 88 : 72, kIssue = 72;
   static_assert(kSoftmax > kLaunch && kProduce < kLaunch && kIssue < kLaunch, "softmax takes more, the others give back");
   static_assert(2 * kSoftmax + kProduce + kIssue == kGroups * kLaunch, "the block's registers");
 };
@@ -77,8 +79,6 @@ struct Ctrl {
   long long qoff[256];      // where a query row's elements are; -1: past the last
 };
 static_assert(sizeof(Ctrl) <= 7168, "control block");
-// scale bytes up to this (2^-120) hold nothing that counts beside others
-constexpr uint32_t kLeastScale = 7;
 // l counts in units of 2^(m - E): with exponents no further apart than this it
 // stays in fp32's range for any number of tokens
 constexpr float kSumSpan = 80.f;
@@ -181,109 +181,6 @@ __device__ __forceinline__ bool wait_for(Ctrl *c, uint64_t *bar, uint32_t parity
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-
-// A query's sums over blocks q0 .. q0 + n - 1 of an e4m3 cache from the codes, in
-// fp32, by one thread: for parts in which scales lie further apart than fp16
-// numbers relative to the largest can hold (a token that nothing sees, or whose
-// weight is nothing, must not cost the others their bits).  Slower than the
-// tensor cores by two orders, and not met by scales within 2^15 of one another.
-template <int DP>
-__device__ __forceinline__ void exact_part(const AttnParams &P, int b, int g, int q0, int n, int npre, int len0, int len, int my,
-                                           const uint32_t *anc, bool use, long long qoff, long long orow, int slot, bool odd) {
-  const unsigned short *const q = static_cast<const unsigned short *>(P.q) + qoff;
-  float m = -INFINITY, top = -INFINITY, l = 0.f, z = -INFINITY;
-  // the first round: maxima and the sum of the softmax; then 32 columns a round
-#pragma unroll 1
-  for (int d0 = -32; d0 < P.D; d0 += 32) {
-    float o[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) o[j] = 0.f;
-#pragma unroll 1
-    for (int k = 0; use && k < n; ++k) {
-      const bool pre = q0 + k < npre;
-      const int tb = (pre ? q0 + k : q0 + k - npre) * kTok, end = min(tb + kTok, pre ? P.P : len);
-      const long long ts = pre ? P.ptok_stride : P.tok_stride;
-      const unsigned char *const kb = pre ? P.pk : P.k + b * P.row_stride, *const vb = pre ? P.pv : P.v + b * P.row_stride;
-#pragma unroll 1
-      for (int t = tb; t < end; ++t) {
-        const int own = pre ? -1 : t - len0;  // index among the pass's own tokens
-        if (own >= 0 && !(anc ? __ldg(anc + (own >> 5)) >> (own & 31) & 1u : own <= my)) continue;
-        const unsigned char *const ke = kb + t * ts, *const ve = vb + t * ts;
-        float x = 0.f;
-#pragma unroll 1
-        for (int d = 0; d < P.D; d += 16) {
-          const uint4 w = __ldg(reinterpret_cast<const uint4 *>(ke + static_cast<long long>(g) * P.D + d));
-          const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t h = e & 1 ? e4m3x2_to_f16x2_hi(cw[e / 2]) : e4m3x2_to_f16x2(cw[e / 2]);
-            const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            x = fmaf(query_value(q[d + 2 * e], P.qbf16), y.x, x);
-            x = fmaf(query_value(q[d + 2 * e + 1], P.qbf16), y.y, x);
-          }
-        }
-        x = x * e4m3_scale(__ldg(ke + static_cast<long long>(P.H) * P.D + g)) * P.scale;
-        const uint32_t vc = __ldg(ve + static_cast<long long>(P.H) * P.D + g);
-        const float xe = x + (vc == 255u ? 0.f : scale_exponent(vc));
-        if (d0 < 0) {
-          m = fmaxf(m, xe);
-          if (x > top) {
-            l *= ex2(top - x);
-            top = x;
-          }
-          l += x == -INFINITY ? 0.f : ex2(x - top);
-          continue;
-        }
-        const float w = ex2(xe - m);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (d0 + c * 16 >= P.D) continue;
-          const uint4 u = __ldg(reinterpret_cast<const uint4 *>(ve + static_cast<long long>(g) * P.D + d0 + c * 16));
-          const uint32_t cw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t h = e & 1 ? e4m3x2_to_f16x2_hi(cw[e / 2]) : e4m3x2_to_f16x2(cw[e / 2]);
-            float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            if (vc == 255u) y.x = y.y = __uint_as_float(0x7fc00000u);
-            if (own >= 0) {  // put into the answers at the end, as in every part
-              if (!isfinite(y.x)) y.x = 0.f;
-              if (!isfinite(y.y)) y.y = 0.f;
-            }
-            o[c * 16 + 2 * e] = fmaf(w, y.x, o[c * 16 + 2 * e]);
-            o[c * 16 + 2 * e + 1] = fmaf(w, y.y, o[c * 16 + 2 * e + 1]);
-          }
-        }
-      }
-    }
-    const bool some = use && l != 0.f;
-    if (d0 < 0) {
-      z = some ? top + log2f(l) : -INFINITY;
-      if (!P.direct)
-        P.ml[static_cast<long long>(slot) * P.rows + orow] = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
-      else if (P.lse)
-        P.lse[orow] = kLn2 * z;
-      continue;
-    }
-    if (P.direct) {
-      const float w = some ? ex2(m - z) : 0.f;
-      unsigned short *const to = static_cast<unsigned short *>(P.out) + orow * P.D + d0;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (d0 + j >= P.D) continue;
-        float y = some ? o[j] * w : 0.f;
-        if (some && odd)
-          for (int t = 0; t < len - len0; ++t)
-            if (anc ? __ldg(anc + (t >> 5)) >> (t & 31) & 1u : t <= my) y += odd_value<SPEC_E4M3>(P, b, len0 + t, g, d0 + j);
-        to[j] = static_cast<unsigned short>(P.qbf16 ? pack16<true>(y, 0.f) : pack16<false>(y, 0.f));
-      }
-    } else if (some) {
-      float *const to = P.part + (static_cast<long long>(slot) * P.rows + orow) * P.D + d0;
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (d0 + j < P.D) to[j] = o[j];
-    }
-  }
-}
 
 // Items.  PRE: the prefix alone, for (KV head, block of 256 rows of all rows'
 // queries, part).  Else (row, KV head, block of 256 of the row's queries,
@@ -888,7 +785,8 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         const float z = some ? m + log2f(l) - E : -INFINITY;
         if (E4 && c->far_apart) {
           if (at >= 0)
-            exact_part<DP>(P, b, g, q0, n, npre, len0, len, my, anc, at < kUnused, c->qoff[rr], orow, slot, c->odd);
+            exact_part(P, b, g, q0 * kTok, min(min(q0 + n, npre) * kTok, P.P), max(0, q0 - npre) * kTok, min((q0 + n - npre) * kTok, len), len0, cnt,
+                       my, anc, at < kUnused, c->qoff[rr], orow, slot, c->odd);
         } else if (P.direct) {  // every thread loads: tensor memory is read by whole warps
           const float w = some ? ex2(m - z) : 0.f;
           const bool odd = some && c->odd;

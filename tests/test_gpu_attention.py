@@ -501,6 +501,32 @@ def test_e4m3_scales_far_apart_in_tiles(sv, qt, B, N, D, P, top, tree):
     p.check(rows=range(min(B, 4)))
 
 
+@pytest.mark.parametrize("B,N,D,P,lens", [(1, 4, 64, 0, [100]), (3, 6, 128, 70, [5, 400, 33]), (70, 2, 64, 0, [90] * 70)])
+@pytest.mark.parametrize("up", [40, 100])
+def test_e4m3_scales_far_apart_in_rows(sv, B, N, D, P, lens, up):
+    """Values 2^40 and 2^100 above the rest: the pass's last token, which the queries before it do not
+    see, and a token whose weight is nothing; growth after the first blocks, zeros, tiny values."""
+    import torch
+    p = Problem(sv, B, N, 4, 2, D, P, lens, "uint8", "bfloat16", seed=up + D)
+    p.q = p.q.abs() + 1
+    p.qx = p.q.cpu().double().numpy()
+    total = torch.from_numpy(np.asarray(p.lens + N, np.int32)).cuda()
+    k, v = (torch.from_numpy(x).float().cuda() for x in (p.kx, p.vx))
+    v[:, :4] = 0.0
+    for b in range(0, B, 2):
+        at = int(p.lens[b])
+        v[b, at + N - 1] *= 2.0**up
+        if at > 60:
+            k[b, 50], v[b, 50] = -8.0, v[b, 50] * 2.0**up
+            v[b, 20:24] *= 2.0**-up
+            v[b, 51:55] *= 2.0**30
+    zeros = torch.zeros(B, dtype=torch.int32, device="cuda")
+    sv.spec_kv_append(p.cache, k, v, zeros, count=total)
+    kx, vx, _ = sv.spec_kv_read(p.cache, total, p.S, heads=2, head_dim=D, dtype=torch.float32)
+    p.kx, p.vx = kx.cpu().double().numpy(), vx.cpu().double().numpy()
+    p.check(rows=range(min(B, 4)))
+
+
 def test_graphs_have_workspaces_of_their_own(sv):
     """Two graphs captured on one stream and replayed side by side, after eager calls of other sizes."""
     import torch
