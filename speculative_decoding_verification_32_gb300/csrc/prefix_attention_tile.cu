@@ -41,7 +41,7 @@ constexpr int kTok = 128;          // tokens per block, a producer thread each
 // issue.  Their registers per thread add up to what the block is launched
 // with, and are split so that no role's loop spills: with 160 for the softmax
 // and 120 for producers of codes, 32 trees of 60 nodes behind 4097 tokens take
-// 212 us where this split takes 200.  (Two groups of producers, 96 registers a
+// 212 us where this split takes 201.  (Two groups of producers, 96 registers a
 // thread, were 8 % slower than one.)
 template <bool E4>
 struct Roles {
@@ -346,11 +346,6 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
     };
     float E = kMinExponent, low = 0.f, kscale = 1.f;  // the largest and smallest exponent of a block of values
     uint32_t sc0 = issue(0), sc1 = issue(1);
-    if (E4 && P.wide) {
-      const int32_t *const far = P.wide_far + static_cast<long long>(g) * npre;
-      for (int q = q0 + pt; q < min(npre, q0 + n); q += kProducers)
-        if (__ldg(far + q) | __ldg(far + static_cast<long long>(P.H) * npre + q)) c->far_apart = 1;
-    }
     for (int it = 0; it < 2 * n; ++it) {
       cp_async_wait<1>();
       const int k = it >> 1, s = k & 1, q = q0 + k;
@@ -383,6 +378,7 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         }
       } else if ((PRE || q < npre) && P.wide) {
         if (!val) kscale = __uint_as_float(sc0);
+        if (pt == 0 && __ldg(P.wide_far + (static_cast<long long>(val ? P.H : 0) + g) * npre + q)) c->far_apart = 1;
         if (val) {
           const float ex = __uint_as_float(sc0);
           E = fmaxf(E, ex);
