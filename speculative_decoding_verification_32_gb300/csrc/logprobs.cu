@@ -156,10 +156,12 @@ __device__ __forceinline__ unsigned long long ld_remote_u64(const void *p, uint3
 }
 
 // Grid: position * cluster size + rank (SPREAD: clusters of more than one).
-// CTAs per SM as measured: bf16 224 positions 20 us at 3 and 23 at 4, fp32 2047
-// positions of 32000 logits 61 us at 3 and 56 at 4.
+// CTAs per SM as measured: 224 positions of 128256 bf16 logits 20 us at 3 and 23
+// at 4 (8.4 would be the bytes at the copy rate: the rest is the end of a
+// position); 2047 positions of 32000 fp32 logits 61 us at 3, 56 at 4, 54 at 5
+// (4.8 TB/s, 0.72 of the copy rate) and 70 at 6, where registers spill.
 template <bool BF16, bool VEC, bool SPREAD>
-__global__ void __launch_bounds__(kLpThreads, BF16 ? 3 : 4) logprobs_kernel(const __grid_constant__ LpParams P) {
+__global__ void __launch_bounds__(kLpThreads, BF16 ? 3 : 5) logprobs_kernel(const __grid_constant__ LpParams P) {
   constexpr int E = BF16 ? 8 : 4;
   __shared__ __align__(16) LpPart sh[kLpThreads / 32];
   __shared__ __align__(16) LpPart whole;        // this CTA's record
@@ -408,8 +410,8 @@ __global__ void __launch_bounds__(kLpThreads, BF16 ? 3 : 4) logprobs_kernel(cons
 
 int lp_slice(bool bf16) { return kLpThreads * kLpVecs * (bf16 ? 8 : 4); }
 // CTAs per position: doubled while that leaves each a slice and the grid within
-// eight per SM (384 positions of 128256 bf16 logits, 224 of them asked for: 28 us
-// with one CTA each, 24 with two, 30 with four).
+// eight per SM (384 positions of 128256 bf16 logits, 224 of them asked for: 26 us
+// with one CTA each, 20 with two, 34 with four; 2047 positions of 32000 fp32 logits: 56 us with one, 80 with two).
 int lp_ranks(long long rows, int nslices) {
   int ranks = 1;
   while (ranks < kLpMaxCluster && 2 * ranks <= nslices && rows * 2 * ranks <= 8 * 152) ranks *= 2;
