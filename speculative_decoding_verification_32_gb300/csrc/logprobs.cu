@@ -411,7 +411,8 @@ __global__ void __launch_bounds__(kLpThreads, BF16 ? 3 : 5) logprobs_kernel(cons
 int lp_slice(bool bf16) { return kLpThreads * kLpVecs * (bf16 ? 8 : 4); }
 // CTAs per position: doubled while that leaves each a slice and the grid within
 // eight per SM (384 positions of 128256 bf16 logits, 224 of them asked for: 26 us
-// with one CTA each, 20 with two, 34 with four; 2047 positions of 32000 fp32 logits: 56 us with one, 80 with two).
+// with one CTA each, 20 with two, 34 with four; 2047 positions of 32000 fp32
+// logits: 56 us with one, 80 with two).
 int lp_ranks(long long rows, int nslices) {
   int ranks = 1;
   while (ranks < kLpMaxCluster && 2 * ranks <= nslices && rows * 2 * ranks <= 8 * 152) ranks *= 2;
