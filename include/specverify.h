@@ -563,11 +563,15 @@ spec_status spec_kv_read(const spec_kv_read_args *args, int32_t *row_status, voi
  *
  * row_status [rows] (optional): SPEC_ROW_BAD_SLOT (kv_len[b] < 0, count[b]
  * outside [0, N], kv_len[b] + count[b] > slots) or SPEC_ROW_BAD_PARENT; such a
- * row, and a query i >= count[b], gets zeros and lse = -inf.
+ * row, and a query i >= count[b], gets zeros and lse = -inf.  A row
+ * whose kernel gave up waiting (see spec_set_wait_timeout_ns) gets the same with
+ * SPEC_ROW_TIMEOUT.
  *
  * Sums, maxima and softmax statistics are fp32; the softmax weights are
  * rounded once to the cache's 16-bit type (fp16 for SPEC_E4M3) for the product
  * with v.  Results do not depend on timing: every sum has a fixed order.
+ * Scales of an SPEC_E4M3 cache may lie any distance apart; where those of
+ * neighbouring tokens are more than 2^15 apart the call takes longer.
  * Workspace: spec_prefix_attention_workspace_size(args) bytes, no contents
  * kept between calls.
  */

@@ -23,6 +23,11 @@
 //     down to 2^-15 of it), so that the block's scale is one factor on the
 //     scores and one on the sums.  A part with a block whose scales lie further
 //     apart is taken once more in fp32 (exact_part).
+// Measured with 32 query heads and 8 KV heads of 128: a block of 128 tokens takes
+// both tiles 1.84 us in bf16 (the products alone 1.6; 1.35 at the library's dense
+// rate), an item's start and end about 11; 64 chains of 6 tokens behind 8192: 50
+// us.  32 trees of 60 nodes in e4m3: 201 us, two rounds of items where 1.7 would
+// do.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
