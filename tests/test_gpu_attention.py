@@ -471,6 +471,7 @@ def test_rows_cut_by_a_budget(sv, kind, qt, B, N, Hq, H, D, P, top):
     (2, 60, 128, 300, 150, True),   # a prefix that is converted once
     (80, 32, 128, 256, 100, True),  # no join
     (40, 6, 64, 500, 60, False),    # the prefix alone
+    (16, 2, 128, 700, 40, False),   # the prefix alone, unconverted
 ])
 def test_e4m3_scales_far_apart_in_tiles(sv, qt, B, N, D, P, top, tree):
     """Values and keys 2^40 to 2^100 apart within 128 tokens: a token of the pass that most queries do
