@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
 SPEC_F32, SPEC_BF16, SPEC_F16, SPEC_E4M3 = 0, 1, 2, 3
 SPEC_STOCHASTIC, SPEC_GREEDY = 0, 1
+SPEC_ERR_WORKSPACE = 7
 ROW_STATUS = {0: "OK", 1: "NONFINITE", 2: "BAD_TOKEN", 3: "BAD_UNIFORM", 4: "BAD_PARENT",
               5: "EMPTY", 6: "TIMEOUT", 7: "BAD_TEMPERATURE", 8: "BAD_SLOT"}
 
@@ -479,18 +480,14 @@ _here = _Here()
 
 
 def _scratch(dev, stream, nbytes):
-    """A workspace of these calls' own: the verify calls keep a header and
-    stamped records in theirs.  A call captured into a graph gets one from the
-    graph's pool: a replay may run beside later calls, and after the stream's
-    workspace has grown into another buffer."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    buf = _ws.get((dev, "scratch", stream))
-    if buf is not None and buf.numel() >= nbytes:
-        return buf
-    with _ws_lock:
-        buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        _ws[(dev, "scratch", stream)] = buf
+    """A workspace of these calls' own (the verify calls keep a header and
+    stamped records in theirs): the stream's, or a larger one in its place.  A
+    call captured into a graph gets one from the graph's pool: a replay may run
+    beside later calls, and after the stream's has been replaced."""
+    buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    if not torch.cuda.is_current_stream_capturing():
+        with _ws_lock:
+            _ws[(dev, "scratch", stream)] = buf
     return buf
 
 
@@ -612,6 +609,15 @@ def spec_kv_read(cache, length, T, heads=None, head_dim=None, start=None, dtype=
 _NO_CACHE = (0,) * 9
 
 
+def _attention_bytes(a):
+    f = _fast.get("spec_prefix_attention_workspace_size")
+    if f is None:
+        f = lib()["spec_prefix_attention_workspace_size"]
+        f.argtypes, f.restype = [_P], _c.c_size_t
+        _fast["spec_prefix_attention_workspace_size"] = f
+    return f(a)
+
+
 def spec_prefix_attention(q, cache, kv_len, prefix=None, prefix_len=None, parent=None, count=None,
                           scale=None, kv_heads=None, stream=None):
     """The verify pass's attention over a shared prefix and each row's own cache
@@ -654,19 +660,19 @@ def spec_prefix_attention(q, cache, kv_len, prefix=None, prefix_len=None, parent
     a = _PACK_ATTENTION.pack(*c, *pc, P, N, heads, _KV_DTYPES[dtype], D ** -0.5 if scale is None else scale,
                              q.data_ptr(), *qs[:3], _i32(kv_len, "kv_len", dev, (B,)),
                              _i32(count, "count", dev, (B,)), _i32(parent, "parent", dev, (B, N)))
-    f = _fast.get("spec_prefix_attention_workspace_size")
-    if f is None:
-        f = lib()["spec_prefix_attention_workspace_size"]
-        f.argtypes, f.restype = [_P], _c.c_size_t
-        _fast["spec_prefix_attention_workspace_size"] = f
     with _here if stream is None else _On(stream, q, cache, kv_len, prefix, parent, count):
         out = torch.empty(shape, dtype=dtype, device=dev)
         lse = torch.empty(B, N, heads, dtype=torch.float32, device=dev)
         status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
         s = _raw_stream(dev.index)
-        ws = _scratch(dev, s, f(a))
-        _check(_fn("spec_prefix_attention", 7)(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(),
-                                               ws.data_ptr(), ws.numel(), s))
+        f, code = _fn("spec_prefix_attention", 7), SPEC_ERR_WORKSPACE
+        ws = None if torch.cuda.is_current_stream_capturing() else _ws.get((dev, "scratch", s))
+        if ws is not None:  # the call itself says if that is too small, before it launches anything
+            code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
+        if code == SPEC_ERR_WORKSPACE:
+            ws = _scratch(dev, s, _attention_bytes(a))
+            code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
+        _check(code)
     return out, lse, status
 
 
