@@ -434,6 +434,7 @@ for _s, _t in ((_PACK_APPEND, SpecKvAppendArgs), (_PACK_READ, SpecKvReadArgs),
 _KV_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 _fast = {}
 
 
@@ -485,7 +486,7 @@ def _scratch(dev, stream, nbytes):
     call captured into a graph gets one from the graph's pool: a replay may run
     beside later calls, and after the stream's has been replaced."""
     buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    if not torch.cuda.is_current_stream_capturing():
+    if not _capturing():
         with _ws_lock:
             _ws[(dev, "scratch", stream)] = buf
     return buf
@@ -666,7 +667,7 @@ def spec_prefix_attention(q, cache, kv_len, prefix=None, prefix_len=None, parent
         status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
         s = _raw_stream(dev.index)
         f, code = _fn("spec_prefix_attention", 7), SPEC_ERR_WORKSPACE
-        ws = None if torch.cuda.is_current_stream_capturing() else _ws.get((dev, "scratch", s))
+        ws = None if _capturing() else _ws.get((dev, "scratch", s))
         if ws is not None:  # the call itself says if that is too small, before it launches anything
             code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
         if code == SPEC_ERR_WORKSPACE:
