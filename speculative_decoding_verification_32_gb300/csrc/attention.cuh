@@ -231,10 +231,8 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2_hi(uint32_t w) {
   return r;
 }
 
-// Exponent of a scale byte as a float.
-__device__ __forceinline__ float scale_exponent(uint32_t c) {
-  return c == 255u ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(c) - 127);
-}
+// Exponent of a scale byte as a float; 255 (NaN) has none, and its callers give it one.
+__device__ __forceinline__ float scale_exponent(uint32_t c) { return static_cast<float>(static_cast<int>(c) - 127); }
 // sum_t 2^(x_t - m) is kept as l 2^-E, E the largest scale exponent met so far
 // (at least kMinExponent), so that it stays in range for scales this near; a token
 // whose scale is more than 2^kExponentSpan below the largest counts with that

@@ -397,10 +397,22 @@ __global__ void __launch_bounds__(32, RowCfg<CT, DP, MT>::kWarps) attn_rows_kern
       if (limit == INFINITY && most + 127 > static_cast<int>(kLeastScale)) limit = En + kExponentGrowth;
       dE = En - E;
       E = En;
-      const bool low = lane >= kBlk && e < E - kExponentSpan;
-      small = __any_sync(FULL_MASK, low);
-      if (small && __any_sync(FULL_MASK, low && byte > kLeastScale)) limit = kFarApart;
-      const float ec = low ? E - kExponentSpan : e;
+      const bool none = byte == 255u, low = lane >= kBlk && e < E - kExponentSpan;
+      if (__any_sync(FULL_MASK, low || none)) {
+        small = __any_sync(FULL_MASK, low);
+        if (__any_sync(FULL_MASK, low && byte > kLeastScale)) limit = kFarApart;
+        // value vectors of NaN: the keys alone decide the softmax, and the NaN comes in with the values
+        const unsigned nans = __ballot_sync(FULL_MASK, none) >> kBlk;
+        for (int tk = 0; tk < kBlk; ++tk) {
+          if (!(nans >> tk & 1u)) continue;
+          if (!pre && tb + tk >= len0)  // one of the pass's own: put into the answers that see it
+            odd = true;
+          else if (lane * 4 < P.D)  // every query sees it
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(vst + tk * C::kPitch + lane * 4), "r"(0x7f7f7f7fu) : "memory");
+        }
+        __syncwarp();
+      }
+      const float ec = low ? E - kExponentSpan : none ? E : e;
       const uint32_t tab = smem_u32(smem) + C::kSmem - C::kTable;
       if (lane < kBlk)
         asm volatile("st.shared.f32 [%0], %1;" ::"r"(tab + lane * 16), "f"(P.scale * e4m3_scale(byte)) : "memory");
