@@ -571,7 +571,9 @@ spec_status spec_kv_read(const spec_kv_read_args *args, int32_t *row_status, voi
  * rounded once to the cache's 16-bit type (fp16 for SPEC_E4M3) for the product
  * with v.  Results do not depend on timing: every sum has a fixed order.
  * Scales of an SPEC_E4M3 cache may lie any distance apart; where those of
- * neighbouring tokens are more than 2^15 apart the call takes longer.
+ * neighbouring tokens are more than 2^15 apart the call takes longer.  (Beside
+ * a token whose values are all zero and whose weight is more than 2^15 times
+ * every other's, the others' weights may be rounded to multiples of 2^-39.)
  * Workspace: spec_prefix_attention_workspace_size(args) bytes, no contents
  * kept between calls.
  */

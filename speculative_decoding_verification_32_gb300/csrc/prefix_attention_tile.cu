@@ -16,7 +16,8 @@
 //     the scores and are the product's left operand from there;
 //   - a thread owns a row, so its softmax needs no exchange.  The sums are
 //     rescaled only when a row's maximum has grown by more than 2^8 since
-//     the last time: weights up to 2^8 are as exact as weights up to 1;
+//     the last time (codes: before a weight would leave fp16's range): weights
+//     up to 2^8 are as exact as weights up to 1;
 //   - four warps bring keys and values into shared memory, two buffers each:
 //     16-bit entries by asynchronous copies, e4m3 codes through registers as
 //     fp16 numbers relative to the block's largest scale (exact for scales
@@ -57,7 +58,7 @@ struct Roles {
   static_assert(kSoftmax > kLaunch && kProduce < kLaunch && kIssue < kLaunch, "softmax takes more, the others give back");
   static_assert(2 * kSoftmax + kProduce + kIssue == kGroups * kLaunch, "the block's registers");
 };
-constexpr float kLazy = 8.f;       // log2 of the growth a row's maximum may make before its sums follow
+constexpr float kLazy = 8.f;       // 16-bit caches: log2 of the growth a row's maximum may make before its sums follow
 
 template <int DP>
 struct TileCfg {
@@ -78,6 +79,7 @@ struct Ctrl {
   int far_apart;            // scales that the conversion or the sums do not span: exact_part
   float ksc[2];             // per buffer: the block's scale of the keys
   float vex[2], vtop[2];    // the values' exponent, and the largest so far
+  int uneven[2];            // the values' scales differ by more than kEvenSpan
   uint32_t red[2][4];       // producers' reductions
   uint32_t mult[2][128];    // fp16 factors of the block's tokens, keys and values
   float qfac[256];
@@ -87,6 +89,17 @@ static_assert(sizeof(Ctrl) <= 7168, "control block");
 // l counts in units of 2^(m - E): with exponents no further apart than this it
 // stays in fp32's range for any number of tokens
 constexpr float kSumSpan = 80.f;
+// Codes: a row's reference m must not pass max_t (x_t + e_t) over the tokens it
+// sees, or weights that count are lost in fp16's steps.  What is at hand of a block
+// is its largest score and its largest exponent, ex, which may be different
+// tokens' (one that nothing sees, one whose weight is nothing).  So m is put
+// below their sum: by kEvenBelow where all exponents lie within kEvenSpan of ex,
+// else by kUnevenBelow, as far as exponents can lie below ex (further down, only
+// zeros: a vector of zeros with more than 2^15 times all other weight is the one
+// thing that still costs the others bits, on a grid of 2^-39 of the whole).  m
+// follows only before a weight would leave fp16's range, 2^kWeightTop.
+constexpr float kEvenSpan = 4.f, kEvenBelow = 4.5f, kUnevenBelow = 15.f, kWeightTop = 15.5f;
+constexpr float kUnevenMark = 1024.f;  // added to a converted block's value exponent
 constexpr int kUnused = 1 << 30;  // the row has no such query (its answer is empty)
 
 // ------------------------------------------------------------ tcgen05 wrappers
@@ -385,7 +398,8 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         if (!val) kscale = __uint_as_float(sc0);
         if (pt == 0 && __ldg(P.wide_far + (static_cast<long long>(val ? P.H : 0) + g) * npre + q)) c->far_apart = 1;
         if (val) {
-          const float ex = __uint_as_float(sc0);
+          float ex = __uint_as_float(sc0);
+          if (ex > kUnevenMark / 2) ex -= kUnevenMark;
           E = fmaxf(E, ex);
           low = fminf(low, ex);
           if (pt == 0) {
@@ -407,6 +421,7 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         // the block's largest scale
         const uint32_t wtop = __reduce_max_sync(FULL_MASK, sc0 == 255u ? 1u : max(sc0, 1u));
         if (lane == 0) c->red[it & 1][pt / 32] = wtop;
+        if (val && pt == 0) c->uneven[s] = 0;
         producer_sync<kProducers>();  // also: every code of the block has been read
         const uint32_t top = max(max(c->red[it & 1][0], c->red[it & 1][1]), max(c->red[it & 1][2], c->red[it & 1][3]));
         float ex = static_cast<float>(static_cast<int>(top) - 127);
@@ -422,6 +437,7 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
           const uint32_t f = sc0 == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
           c->mult[it & 1][pt] = f | f << 16;
           if (d < -15 && sc0 > kLeastScale && sc0 != 255u) c->far_apart = 1;
+          if (val && static_cast<float>(d) < -kEvenSpan && pt < (PRE || q < npre ? P.P - q * kTok : len - (q - npre) * kTok)) c->uneven[s] = 1;
         }
         producer_sync<kProducers>();
         const uint32_t dst = buf + (pc / 4) * 16384 + row0 * 128;
@@ -625,13 +641,15 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
       bool live = true;
       for (int k = 0; k < n; ++k) {
         live = wait_for(c, &c->sfull[tile], k & 1, limit);
-        float ex = 0.f, sc = base_sc, grow = 0.f;
+        float ex = 0.f, sc = base_sc, grow = 0.f, below = 0.f;
         if constexpr (E4) {
           float En;
           if ((PRE || q0 + k < npre) && P.wide) {
             // a converted prefix's scales, read a block ahead: the softmax need not wait for the values
             sc *= kscale;
             ex = vexp;
+            below = kEvenBelow;
+            if (ex > kUnevenMark / 2) ex -= kUnevenMark, below = kUnevenBelow;
             En = fmaxf(E, ex);
             if (k + 1 < n && q0 + k + 1 < npre) {
               kscale = __ldg(wscale + q0 + k + 1);
@@ -641,6 +659,7 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
             if (live) live = wait_for(c, &c->vfull[k & 1], (k >> 1) & 1, limit);
             sc *= c->ksc[k & 1];
             ex = c->vex[k & 1];
+            below = c->uneven[k & 1] ? kUnevenBelow : kEvenBelow;
             En = c->vtop[k & 1];
           }
           grow = En - E;
@@ -718,9 +737,10 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         const float mt = top == -INFINITY ? -INFINITY : fmaf(top, sc, ex);
         float al = 1.f;
         const float old = m;
-        if (mt > m + kLazy || m == -INFINITY) {
-          al = mt == -INFINITY ? 1.f : ex2(m - mt);
-          m = mt;
+        if (mt > m + (E4 ? kWeightTop : kLazy) || m == -INFINITY) {
+          const float to = E4 ? mt - below : mt;
+          al = to == -INFINITY ? 1.f : ex2(m - to);
+          m = to;
         }
         if (k > 0 && __any_sync(FULL_MASK, al != 1.f)) {
 #pragma unroll
@@ -863,7 +883,7 @@ __global__ void __launch_bounds__(kWidenThreads) attn_widen_kernel(const __grid_
   const int tb = blk * kTok, left = P.P - tb;
   const unsigned char *const base = (val ? P.pv : P.pk) + tb * P.ptok_stride;
   uint32_t byte = 0;
-  int far = 0;
+  int far = 0, uneven = 0;
   if (tid < kTok) {
     if (tid < left) byte = __ldg(base + tid * P.ptok_stride + static_cast<long long>(P.H) * P.D + g);
     const uint32_t top = __reduce_max_sync(FULL_MASK, byte == 255u ? 1u : max(byte, 1u));
@@ -886,11 +906,14 @@ __global__ void __launch_bounds__(kWidenThreads) attn_widen_kernel(const __grid_
     const uint32_t f = byte == 255u ? 0x7e00u : d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
     mult[tid] = f | f << 16;
     far = d < -15 && byte > kLeastScale && byte != 255u;
+    uneven = val && tid < left && static_cast<float>(d) < -kEvenSpan;
   }
   far = __syncthreads_or(far);
+  uneven = __syncthreads_or(uneven);
   if (tid == 0) P.wide_far[(static_cast<long long>(val ? P.H : 0) + g) * gridDim.x + blk] = far;
   if (tid == 0)
-    P.wide_scale[(static_cast<long long>(val ? P.H : 0) + g) * gridDim.x + blk] = val ? static_cast<float>(ref - 127) : e4m3_scale(ref);
+    P.wide_scale[(static_cast<long long>(val ? P.H : 0) + g) * gridDim.x + blk] =
+        val ? static_cast<float>(ref - 127) + (uneven ? kUnevenMark : 0.f) : e4m3_scale(ref);
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
     const int x = i * kWidenThreads + tid, t = x / parts, pc = x - t * parts;

@@ -1,5 +1,6 @@
-"""Attention over caches whose entries are extreme: value vectors that are NaN (needs a GB300).  The plain restatement and its
-tolerances are those of test_gpu_attention.py."""
+"""Attention over caches whose entries are extreme: value vectors that are NaN, scales of
+tokens that carry no weight (needs a GB300).  The plain restatement and its tolerances are those of
+test_gpu_attention.py."""
 import numpy as np
 import pytest
 
@@ -56,3 +57,55 @@ def test_a_nan_value_vector_is_no_matter_for_lse(sv, qt, zeros, B, N, G, D, P, t
             assert torch.equal(out[b, ~hit, G:], out0[b, ~hit, G:])
             assert bool(torch.isnan(out[b, hit, G:]).all())
             assert bool(((lse[b] - lse0[b]).abs().double() <= lse_bound(p, b, lse0[b].double())).all()), where
+
+
+@pytest.mark.parametrize("qt", ["bfloat16", "float16"])
+@pytest.mark.parametrize("sink", [False, True])
+@pytest.mark.parametrize("up", [3, 5, 9, 12, 15])
+@pytest.mark.parametrize("B,N,G,D,P,tree", [
+    (16, 2, 4, 128, 5000, False),   # the prefix alone, unconverted
+    (40, 3, 4, 64, 5000, False),    # the prefix alone, converted
+    (2, 60, 4, 128, 5000, True),    # prefix and own entries in one item
+    (1, 50, 4, 64, 0, True),        # own entries
+    (1, 5, 4, 64, 3000, False),     # few query rows
+])
+def test_scales_of_tokens_without_weight(sv, qt, up, sink, B, N, G, D, P, tree):
+    """Tokens of no weight whose values lie 2^up above the others' or (sink) a token of zeros that has 2^13.7
+    times any other's weight: thousands of tokens 2^-11 below the largest weight behind them count all the same."""
+    import torch
+    H = 16  # enough that a part is many blocks long
+    own = 4000 if P == 0 else 40
+    p = Problem(sv, B, N, G * H, H, D, P, [own] * B, "uint8", qt, tree, seed=up)
+    p.q = torch.ones_like(p.q)
+    p.qx = p.q.cpu().double().numpy()
+    rng = np.random.default_rng(up)
+    unit = 1.0 / (D * p.scale)
+
+    def keys(shape):
+        """[..., H, D] of constant vectors: scores 0, or -4 to -8.5 in nats."""
+        s = rng.choice([-4.0, -6.5, -7.75, -8.5], shape)
+        s[..., 3::600] = 0.0
+        return np.broadcast_to((s * unit)[..., None, None], shape + (H, D)).copy()
+
+    k, v = keys((B, own + N)), np.abs(p.vx[:, :own + N])
+    pk, pv = (keys((1, P)), np.abs(p.pv[None])) if P else (None, None)
+    for kk, vv in ((pk, pv), (k, v)):
+        if kk is None or (kk is k and P):
+            continue
+        kk[:, 7::600] = -30.0 * unit
+        vv[:, 7::600] *= 2.0**up
+        if sink:
+            kk[:, 9], vv[:, 9] = 9.5 * unit, 0.0
+    if tree:  # a token of the pass that few see
+        v[:, own + N // 2] *= 2.0**up
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    total = torch.full((B,), own + N, dtype=torch.int32, device="cuda")
+    f32 = lambda a: torch.from_numpy(a).float().cuda()  # noqa: E731
+    sv.spec_kv_append(p.cache, f32(k), f32(v), zero)
+    kx, vx, _ = sv.spec_kv_read(p.cache, total, p.S, heads=H, head_dim=D, dtype=torch.float32)
+    p.kx, p.vx = kx.cpu().double().numpy(), vx.cpu().double().numpy()
+    if P:
+        sv.spec_kv_append(p.prefix, f32(pk), f32(pv), zero[:1])
+        kx, vx, _ = sv.spec_kv_read(p.prefix, zero[:1] + P, P, heads=H, head_dim=D, dtype=torch.float32)
+        p.pk, p.pv = kx[0].cpu().double().numpy(), vx[0].cpu().double().numpy()
+    p.check(rows=[B - 1])
