@@ -901,7 +901,7 @@ AttnPlan plan_attention(const spec_attention_args *a) {
     p.osplits = 1;
     if (c.rows <= kMaxCutRows && budget > c.rows && c.slots < 1LL << 28) {
       p.budget = static_cast<int>(budget);
-      p.osplits = static_cast<int>(std::min<long long>({(c.slots + 63) / 64, budget / c.rows * 4, 64}));
+      p.osplits = static_cast<int>(std::min<long long>({std::max<long long>(1, (c.slots + 63) / 64), budget / c.rows * 4, 64}));
     }
   }
   p.direct = p.otile && p.osplits == 1 && p.psplits == 0;

@@ -1,6 +1,8 @@
 """Attention over caches whose entries are extreme: value vectors that are NaN, scales of
-tokens that carry no weight (needs a GB300).  The plain restatement and its tolerances are those of
+tokens that carry no weight, no slots at all (needs a GB300).  The plain restatement and its tolerances are those of
 test_gpu_attention.py."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -109,3 +111,27 @@ def test_scales_of_tokens_without_weight(sv, qt, up, sink, B, N, G, D, P, tree):
         kx, vx, _ = sv.spec_kv_read(p.prefix, zero[:1] + P, P, heads=H, head_dim=D, dtype=torch.float32)
         p.pk, p.pv = kx[0].cpu().double().numpy(), vx[0].cpu().double().numpy()
     p.check(rows=[B - 1])
+
+
+def test_a_cache_without_slots(sv):
+    """No slots at all: rows that ask for none are right and empty, others are refused."""
+    import torch
+    from speculative_decoding_verification_32_gb300 import _binding as b
+    L = b.lib()
+    for B, H, N in ((64, 8, 1), (64, 8, 20), (3, 2, 2)):
+        D, Hq = 64, 2 * H
+        q = torch.randn(B, N, Hq, D, device="cuda").bfloat16()
+        some = torch.zeros(64, dtype=torch.bfloat16, device="cuda")
+        count = torch.arange(B, dtype=torch.int32, device="cuda") % 2
+        lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        c = b.SpecKvCache(B, H, D, b.SPEC_BF16, 0, 0, 0, some.data_ptr(), some.data_ptr())
+        a = b.SpecAttentionArgs(c, b.SpecKvCache(), 0, N, Hq, b.SPEC_BF16, 0.1, q.data_ptr(),
+                                (ctypes.c_int64 * 3)(N * Hq * D, Hq * D, D), lens.data_ptr(), count.data_ptr(), None)
+        need = L.spec_prefix_attention_workspace_size(ctypes.byref(a))
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        out, lse = torch.full_like(q, 7), torch.full((B, N, Hq), 7.0, device="cuda")
+        status = torch.full((B,), 77, dtype=torch.int32, device="cuda")
+        assert L.spec_prefix_attention(ctypes.byref(a), out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), need,
+                                       ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+        assert status.tolist() == [8 * (i % 2) for i in range(B)]
+        assert float(out.abs().max()) == 0 and bool((lse == float("-inf")).all())
