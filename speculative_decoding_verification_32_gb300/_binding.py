@@ -225,6 +225,27 @@ def workspace(device, nbytes, stream):
     return buf
 
 
+class _Here:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_here = _Here()
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _device(device, stream=None):
+    """The context of a call's launches: its tensors' device is the current one."""
+    if device.type != "cuda":
+        raise ValueError(f"the library's calls need CUDA tensors, got tensors on {device}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return _here if _current_device() == device.index else torch.cuda.device(device)
+
+
 def _stream(device, stream):
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return s, _P(s.cuda_stream)
@@ -276,18 +297,20 @@ def spec_verify_chain(target_logits, draft_logits, draft_tokens, temperature=Non
     truncated = top_k is not None or top_p is not None
     nbytes = (L.spec_verify_chain_truncated_workspace_size if truncated
               else L.spec_verify_chain_workspace_size)(B, K, V)
+    on = _device(dev, stream)
     s, sp = _stream(dev, stream)
     ws = workspace(dev, nbytes, s.cuda_stream)
-    if not truncated:
-        _check(L.spec_verify_chain(_c.byref(args), _c.byref(o), _ptr(ws), ws.numel(), sp))
-    else:
-        if greedy:
-            raise ValueError("top_k / top_p apply to mode='stochastic' only")
-        _req(top_k, "top_k", dev, torch.int32)
-        _req(top_p, "top_p", dev, torch.float32)
-        t = SpecTruncation(_ptr(top_k), _ptr(top_p))
-        _check(L.spec_verify_chain_truncated(_c.byref(args), _c.byref(t), _c.byref(o), _ptr(ws),
-                                             ws.numel(), sp))
+    with on:
+        if not truncated:
+            _check(L.spec_verify_chain(_c.byref(args), _c.byref(o), _ptr(ws), ws.numel(), sp))
+        else:
+            if greedy:
+                raise ValueError("top_k / top_p apply to mode='stochastic' only")
+            _req(top_k, "top_k", dev, torch.int32)
+            _req(top_p, "top_p", dev, torch.float32)
+            t = SpecTruncation(_ptr(top_k), _ptr(top_p))
+            _check(L.spec_verify_chain_truncated(_c.byref(args), _c.byref(t), _c.byref(o), _ptr(ws),
+                                                 ws.numel(), sp))
     return out
 
 
@@ -318,9 +341,11 @@ def spec_verify_tree(target_logits, parent, node_tokens, temperature=None, margi
                     _ptr(out["num_emitted"]), _ptr(out["row_status"]))
     L = lib()
     nbytes = L.spec_verify_tree_workspace_size(B, N, V)
+    on = _device(dev, stream)
     s, sp = _stream(dev, stream)
     ws = workspace(dev, nbytes, s.cuda_stream)
-    _check(L.spec_verify_tree(_c.byref(args), _c.byref(o), _ptr(ws), ws.numel(), sp))
+    with on:
+        _check(L.spec_verify_tree(_c.byref(args), _c.byref(o), _ptr(ws), ws.numel(), sp))
     return out
 
 
@@ -337,10 +362,12 @@ def spec_rollback_lengths(kv_len_in, accepted_len, num_emitted, out_tokens, eos_
     B, max_emit = out_tokens.shape
     committed = torch.empty(B, dtype=torch.int32, device=dev)
     n_out = torch.empty(B, dtype=torch.int32, device=dev)
+    on = _device(dev, stream)
     _, sp = _stream(dev, stream)
-    _check(lib().spec_rollback_lengths(B, max_emit, _ptr(kv_len_in), _ptr(accepted_len),
-                                       _ptr(num_emitted), _ptr(out_tokens), int(eos_id),
-                                       _ptr(max_len), _ptr(committed), _ptr(n_out), sp))
+    with on:
+        _check(lib().spec_rollback_lengths(B, max_emit, _ptr(kv_len_in), _ptr(accepted_len),
+                                           _ptr(num_emitted), _ptr(out_tokens), int(eos_id),
+                                           _ptr(max_len), _ptr(committed), _ptr(n_out), sp))
     return committed, n_out
 
 
@@ -362,10 +389,12 @@ def spec_drift_residuals(target_logits, draft_logits, temperature=None, m=32, st
                          None, None)
     L = lib()
     nbytes = L.spec_verify_chain_truncated_workspace_size(B, K, V)
+    on = _device(dev, stream)
     s, sp = _stream(dev, stream)
     ws = workspace(dev, nbytes, s.cuda_stream)
-    _check(L.spec_drift_residuals(_c.byref(args), int(m), _ptr(sup), _ptr(res), _ptr(st),
-                                  _ptr(ws), ws.numel(), sp))
+    with on:
+        _check(L.spec_drift_residuals(_c.byref(args), int(m), _ptr(sup), _ptr(res), _ptr(st),
+                                      _ptr(ws), ws.numel(), sp))
     return sup, res, st
 
 
@@ -388,8 +417,10 @@ def spec_kv_compact_tree(kv, kv_len_in, accepted_len, path_nodes, stream=None):
     status = torch.empty(B, dtype=torch.int32, device=dev)
     a = SpecKvCompactArgs(B, path_nodes.shape[1], planes, 0, S_max, E, B * S_max * E, S_max * E, E,
                           _ptr(kv), _ptr(kv_len_in), _ptr(accepted_len), _ptr(path_nodes))
+    on = _device(dev, stream)
     _, sp = _stream(dev, stream)
-    _check(lib().spec_kv_compact_tree(_c.byref(a), _ptr(status), sp))
+    with on:
+        _check(lib().spec_kv_compact_tree(_c.byref(a), _ptr(status), sp))
     return status
 
 
@@ -408,10 +439,12 @@ def spec_adaptive_tree_policy(accepted_len, depth, draft_top1, ema, zero_run, al
     shape = torch.empty(B, 3, dtype=torch.int32, device=dev)
     q = SpecAdaptiveParams(float(alpha), float(divisor), float(ema0), (_c.c_int32 * 3)(*shallow),
                            (_c.c_int32 * 3)(*deep), (_c.c_int32 * 3)(*start), int(breaker))
+    on = _device(dev, stream)
     _, sp = _stream(dev, stream)
-    _check(lib().spec_adaptive_tree_policy(_c.byref(q), B, _ptr(accepted_len), _ptr(depth),
-                                           _ptr(draft_top1), _ptr(ema), _ptr(zero_run),
-                                           _ptr(shape), sp))
+    with on:
+        _check(lib().spec_adaptive_tree_policy(_c.byref(q), B, _ptr(accepted_len), _ptr(depth),
+                                               _ptr(draft_top1), _ptr(ema), _ptr(zero_run),
+                                               _ptr(shape), sp))
     return shape
 
 
@@ -453,7 +486,7 @@ class _On:
     """A call on a stream that the caller names: tensors made inside `with`
     come from that stream's pool, and use() tells the allocator that the
     stream reads or writes tensors of another's, so none is handed out again
-    too early.  Without a stream it does nothing (the current stream)."""
+    too early."""
 
     def __init__(self, stream, *tensors):
         self.stream = stream
@@ -469,15 +502,13 @@ class _On:
         self.ctx.__exit__(*exc)
 
 
-class _Here:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_here = _Here()
+def _on(device, stream, *tensors):
+    """The context in which a call makes its outputs and launches: on `stream`,
+    or (None) on the current stream of `device`."""
+    if stream is None:
+        return _here if device.index == _current_device() and device.type == "cuda" else _device(device)
+    _device(device, stream)
+    return _On(stream, *tensors)
 
 
 def _scratch(dev, stream, nbytes):
@@ -574,7 +605,7 @@ def spec_kv_append(cache, k, v, kv_len, count=None, stream=None):
         raise ValueError("kv_len is needed")
     a = _PACK_APPEND.pack(*c, N, _kv_dtype(dtype, "k"), k.data_ptr(), v.data_ptr(), *ks[:3], *vs[:3],
                           _i32(kv_len, "kv_len", dev, (B,)), _i32(count, "count", dev, (B,)))
-    with _here if stream is None else _On(stream, cache, k, v, kv_len, count):
+    with _on(dev, stream, cache, k, v, kv_len, count):
         status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
         _check(_fn("spec_kv_append", 3)(a, status.data_ptr(), _raw_stream(dev.index)))
     return status
@@ -598,7 +629,7 @@ def spec_kv_read(cache, length, T, heads=None, head_dim=None, start=None, dtype=
     if length is None:
         raise ValueError("length is needed")
     code, n, s = _kv_dtype(dtype, "dtype"), _i32(length, "length", dev, (B,)), _i32(start, "start", dev, (B,))
-    with _here if stream is None else _On(stream, cache, length, start):
+    with _on(dev, stream, cache, length, start):
         k = torch.empty(B, T, heads, head_dim, dtype=dtype, device=dev)
         v = torch.empty_like(k)
         status = (torch.empty if T else torch.zeros)(B, dtype=torch.int32, device=dev)
@@ -661,7 +692,7 @@ def spec_prefix_attention(q, cache, kv_len, prefix=None, prefix_len=None, parent
     a = _PACK_ATTENTION.pack(*c, *pc, P, N, heads, _KV_DTYPES[dtype], D ** -0.5 if scale is None else scale,
                              q.data_ptr(), *qs[:3], _i32(kv_len, "kv_len", dev, (B,)),
                              _i32(count, "count", dev, (B,)), _i32(parent, "parent", dev, (B, N)))
-    with _here if stream is None else _On(stream, q, cache, kv_len, prefix, parent, count):
+    with _on(dev, stream, q, cache, kv_len, prefix, parent, count):
         out = torch.empty(shape, dtype=dtype, device=dev)
         lse = torch.empty(B, N, heads, dtype=torch.float32, device=dev)
         status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
@@ -703,7 +734,7 @@ def spec_token_logprobs(logits, tokens=None, temperature=None, m=0, stream=None)
     a = _PACK_LOGPROBS.pack(B, npos, V, dt, m, 0, pitch, logits.data_ptr(), tk,
                             0 if temperature is None else temperature.data_ptr())
     f32 = torch.float32
-    with _here if stream is None else _On(stream, logits, tokens, temperature):
+    with _on(dev, stream, logits, tokens, temperature):
         out = dict(entropy=torch.empty(B, npos, dtype=f32, device=dev),
                    status=torch.empty(B, npos, dtype=torch.int32, device=dev),
                    top_ids=torch.empty(B, npos, m, dtype=torch.int32, device=dev),
