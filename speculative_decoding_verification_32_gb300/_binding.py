@@ -506,7 +506,7 @@ def _on(device, stream, *tensors):
     """The context in which a call makes its outputs and launches: on `stream`,
     or (None) on the current stream of `device`."""
     if stream is None:
-        return _here if device.index == _current_device() and device.type == "cuda" else _device(device)
+        return _here if device.type == "cuda" and device.index == _current_device() else _device(device)
     _device(device, stream)
     return _On(stream, *tensors)
 
