@@ -45,8 +45,10 @@
  *    stamped on every record the call writes, so nothing an earlier call
  *    left behind is ever read, whatever its shapes.  Keep
  *    passing the same `ws_bytes` for the same buffer.  Calls on one stream
- *    may share a workspace; calls that may overlap in time (different
- *    streams) need separate workspaces.
+ *    may share a workspace if they are enqueued one after the other: a call
+ *    enqueues several kernels, so host threads that share a stream and a
+ *    workspace need a lock around their calls.  Calls that may overlap in
+ *    time (different streams) need separate workspaces.
  *  - Each verify call enqueues a streaming kernel (a truncated verify adds
  *    a selection kernel after it) and a small per-row kernel that starts
  *    early and waits for it on the device (programmatic dependent launch);

@@ -225,6 +225,18 @@ def workspace(device, nbytes, stream):
     return buf
 
 
+# A call enqueues several kernels that hand data to one another through the
+# stream's workspace, and other host threads run meanwhile: a call's kernels are
+# enqueued as a whole before another call's on the same stream.  (Reentrant: an
+# allocation may run a finaliser that makes a call of its own.)
+_enqueue_locks = {}
+
+
+def _enqueuing(device, stream):
+    key = (device, stream)
+    return _enqueue_locks.get(key) or _enqueue_locks.setdefault(key, threading.RLock())
+
+
 class _Here:
     def __enter__(self):
         pass
@@ -299,8 +311,8 @@ def spec_verify_chain(target_logits, draft_logits, draft_tokens, temperature=Non
               else L.spec_verify_chain_workspace_size)(B, K, V)
     on = _device(dev, stream)
     s, sp = _stream(dev, stream)
-    ws = workspace(dev, nbytes, s.cuda_stream)
-    with on:
+    with on, _enqueuing(dev, s.cuda_stream):
+        ws = workspace(dev, nbytes, s.cuda_stream)
         if not truncated:
             _check(L.spec_verify_chain(_c.byref(args), _c.byref(o), _ptr(ws), ws.numel(), sp))
         else:
@@ -343,8 +355,8 @@ def spec_verify_tree(target_logits, parent, node_tokens, temperature=None, margi
     nbytes = L.spec_verify_tree_workspace_size(B, N, V)
     on = _device(dev, stream)
     s, sp = _stream(dev, stream)
-    ws = workspace(dev, nbytes, s.cuda_stream)
-    with on:
+    with on, _enqueuing(dev, s.cuda_stream):
+        ws = workspace(dev, nbytes, s.cuda_stream)
         _check(L.spec_verify_tree(_c.byref(args), _c.byref(o), _ptr(ws), ws.numel(), sp))
     return out
 
@@ -391,8 +403,8 @@ def spec_drift_residuals(target_logits, draft_logits, temperature=None, m=32, st
     nbytes = L.spec_verify_chain_truncated_workspace_size(B, K, V)
     on = _device(dev, stream)
     s, sp = _stream(dev, stream)
-    ws = workspace(dev, nbytes, s.cuda_stream)
-    with on:
+    with on, _enqueuing(dev, s.cuda_stream):
+        ws = workspace(dev, nbytes, s.cuda_stream)
         _check(L.spec_drift_residuals(_c.byref(args), int(m), _ptr(sup), _ptr(res), _ptr(st),
                                       _ptr(ws), ws.numel(), sp))
     return sup, res, st
@@ -698,12 +710,13 @@ def spec_prefix_attention(q, cache, kv_len, prefix=None, prefix_len=None, parent
         status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
         s = _raw_stream(dev.index)
         f, code = _fn("spec_prefix_attention", 7), SPEC_ERR_WORKSPACE
-        ws = None if _capturing() else _ws.get((dev, "scratch", s))
-        if ws is not None:  # the call itself says if that is too small, before it launches anything
-            code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
-        if code == SPEC_ERR_WORKSPACE:
-            ws = _scratch(dev, s, _attention_bytes(a))
-            code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
+        with _enqueuing(dev, s):
+            ws = None if _capturing() else _ws.get((dev, "scratch", s))
+            if ws is not None:  # the call itself says if that is too small, before it launches anything
+                code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
+            if code == SPEC_ERR_WORKSPACE:
+                ws = _scratch(dev, s, _attention_bytes(a))
+                code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
         _check(code)
     return out, lse, status
 
