@@ -215,12 +215,16 @@ _ws = {}
 _ws_lock = threading.Lock()
 
 
-def workspace(device, nbytes, stream):
-    key = (device, stream)
+def workspace(device, nbytes, handle, stream=None):
+    """The workspace of the stream with this handle.  `stream`: that stream, if it
+    may not be the current one: a new buffer is filled, and a replaced one is
+    given back, in its order."""
+    key = (device, handle)
     with _ws_lock:
         buf = _ws.get(key)
         if buf is None or buf.numel() < nbytes:
-            buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+            with _here if stream is None else torch.cuda.stream(stream):
+                buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
             _ws[key] = buf
     return buf
 
@@ -312,7 +316,7 @@ def spec_verify_chain(target_logits, draft_logits, draft_tokens, temperature=Non
     on = _device(dev, stream)
     s, sp = _stream(dev, stream)
     with on, _enqueuing(dev, s.cuda_stream):
-        ws = workspace(dev, nbytes, s.cuda_stream)
+        ws = workspace(dev, nbytes, s.cuda_stream, stream)
         if not truncated:
             _check(L.spec_verify_chain(_c.byref(args), _c.byref(o), _ptr(ws), ws.numel(), sp))
         else:
@@ -356,7 +360,7 @@ def spec_verify_tree(target_logits, parent, node_tokens, temperature=None, margi
     on = _device(dev, stream)
     s, sp = _stream(dev, stream)
     with on, _enqueuing(dev, s.cuda_stream):
-        ws = workspace(dev, nbytes, s.cuda_stream)
+        ws = workspace(dev, nbytes, s.cuda_stream, stream)
         _check(L.spec_verify_tree(_c.byref(args), _c.byref(o), _ptr(ws), ws.numel(), sp))
     return out
 
@@ -404,7 +408,7 @@ def spec_drift_residuals(target_logits, draft_logits, temperature=None, m=32, st
     on = _device(dev, stream)
     s, sp = _stream(dev, stream)
     with on, _enqueuing(dev, s.cuda_stream):
-        ws = workspace(dev, nbytes, s.cuda_stream)
+        ws = workspace(dev, nbytes, s.cuda_stream, stream)
         _check(L.spec_drift_residuals(_c.byref(args), int(m), _ptr(sup), _ptr(res), _ptr(st),
                                       _ptr(ws), ws.numel(), sp))
     return sup, res, st
