@@ -565,9 +565,10 @@ spec_status spec_kv_read(const spec_kv_read_args *args, int32_t *row_status, voi
  *
  * row_status [rows] (optional): SPEC_ROW_BAD_SLOT (kv_len[b] < 0, count[b]
  * outside [0, N], kv_len[b] + count[b] > slots) or SPEC_ROW_BAD_PARENT; such a
- * row, and a query i >= count[b], gets zeros and lse = -inf.  A row
- * whose kernel gave up waiting (see spec_set_wait_timeout_ns) gets the same with
- * SPEC_ROW_TIMEOUT.
+ * row, and a query i >= count[b], gets zeros and lse = -inf.  A row any part
+ * of whose work gave up waiting (see spec_set_wait_timeout_ns) is flagged
+ * SPEC_ROW_TIMEOUT: the queries and heads that the part belonged to get zeros
+ * and lse = -inf, the row's others keep their answers.
  *
  * Sums, maxima and softmax statistics are fp32; the softmax weights are
  * rounded once to the cache's 16-bit type (fp16 for SPEC_E4M3) for the product
@@ -660,8 +661,9 @@ const char *spec_status_string(spec_status s);
  * spec_debug_force_wait_timeout(1) tests the give-up path on a healthy GPU:
  * the bulk-copy stream waits on a barrier that nothing completes, and the
  * truncation and DRIFT kernels withhold their records, so every reader gives
- * up (or finds a record missing) and its rows report SPEC_ROW_TIMEOUT; 0
- * turns it off.
+ * up (or finds a record missing) and its rows report SPEC_ROW_TIMEOUT.  The
+ * attention's kernel for many query rows withholds its first keys.  2 + g: that
+ * of KV head g alone does, and the verify calls are as ever; 0 turns it off.
  */
 void spec_set_wait_timeout_ns(uint64_t ns);
 uint64_t spec_get_wait_timeout_ns(void);

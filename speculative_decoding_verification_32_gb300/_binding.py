@@ -774,4 +774,4 @@ def get_wait_timeout_ns():
 
 
 def debug_force_wait_timeout(on):
-    lib().spec_debug_force_wait_timeout(1 if on else 0)
+    lib().spec_debug_force_wait_timeout(int(on))

@@ -202,7 +202,7 @@ spec_status setup_stochastic(const spec_chain_args *a, void *ws, size_t ws_bytes
   p.use_tma = aligned(a->target_logits, 16) && (K == 0 || aligned(a->draft_logits, 16)) &&
               (static_cast<long long>(a->V) * esz) % 16 == 0;
   p.wait_limit_ns = g_wait_ns.load();
-  p.force_timeout = g_force_timeout.load();
+  p.force_timeout = g_force_timeout.load() == 1;
   // workspace tail: a 16-byte header {claim counter, generation, -}
   {
     char *end = static_cast<char *>(ws) + (ws_bytes & ~static_cast<size_t>(15));
@@ -279,7 +279,7 @@ spec_status setup_stochastic(const spec_chain_args *a, void *ws, size_t ws_bytes
 
 }  // namespace
 
-bool sv::force_wait_timeout() { return g_force_timeout.load() != 0; }
+int sv::force_wait_timeout() { return g_force_timeout.load(); }
 
 extern "C" {
 
@@ -593,7 +593,7 @@ const char *spec_status_string(spec_status s) {
 
 void spec_set_wait_timeout_ns(uint64_t ns) { g_wait_ns.store(ns); }
 uint64_t spec_get_wait_timeout_ns(void) { return g_wait_ns.load(); }
-void spec_debug_force_wait_timeout(int on) { g_force_timeout.store(on ? 1 : 0); }
+void spec_debug_force_wait_timeout(int on) { g_force_timeout.store(on < 0 ? 0 : on); }
 
 #ifdef SV_BOUNDS
 // Bounds-check builds only (-DSV_BOUNDS): the number of bad indexes the

@@ -67,7 +67,7 @@ struct AttnParams {
   int fuse;    // own items of the tile kernel take the prefix too
   int direct;  // ... and write the answers themselves: there is nothing to join
   uint64_t wait_limit_ns;
-  int force_timeout;
+  int force_timeout;  // 1: every item; 2 + g: those of KV head g
 };
 
 constexpr int kRowBadSlot = -1, kRowBadParent = -2;

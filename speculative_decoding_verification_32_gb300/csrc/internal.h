@@ -184,8 +184,8 @@ cudaError_t launch_drift(const ChainStochParams &p, bool bf16, int grid, size_t 
 cudaError_t launch_greedy(const GreedyParams &p, bool bf16, int grid, cudaStream_t s);
 cudaError_t greedy_max_blocks_per_sm(bool bf16, bool vec, int *blocks);
 cudaError_t launch_rollback(const RollbackParams &p, cudaStream_t s);
-// Whether spec_debug_force_wait_timeout is on.
-bool force_wait_timeout();
+// What spec_debug_force_wait_timeout was given last.
+int force_wait_timeout();
 // Shape, dtype and alignment checks of a cache descriptor.
 spec_status check_kv_cache(const spec_kv_cache &c);
 #ifdef SV_BOUNDS

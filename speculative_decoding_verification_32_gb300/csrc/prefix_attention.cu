@@ -36,16 +36,18 @@ constexpr int kJoinThreads = 128;
 
 // ---------------------------------------------------------------- tree mask
 // Latency alone: three dependent loads and a walk up the deepest path, under the
-// conversion and tile kernels' own starts.
+// conversion and tile kernels' own starts.  Where the tile kernel writes the
+// answers itself, row_status is written here, so that no CTA's "fine" can come
+// after another's timeout (chains: parent is NULL, and that is all there is to do).
 __global__ void __launch_bounds__(kMaskThreads) attn_mask_kernel(const int32_t *parent, const int32_t *kv_len,
                                                                  const int32_t *count, long long slots, int N, int W,
-                                                                 uint32_t *anc, int32_t *rowinfo) {
+                                                                 uint32_t *anc, int32_t *rowinfo, int32_t *row_status) {
   __shared__ int par[SPEC_MAX_TREE_NODES];
   const int b = blockIdx.x, tid = threadIdx.x;
   allow_dependents();
   const int n = kv_len[b], c = count ? count[b] : N;
   const bool slot_ok = n >= 0 && c >= 0 && c <= N && static_cast<long long>(n) + c <= slots;
-  const int used = max(0, min(c, N));
+  const int used = parent ? max(0, min(c, N)) : 0;
   bool ok = true;
   for (int i = tid; i < used; i += kMaskThreads) {
     const int p = parent[static_cast<size_t>(b) * N + i];
@@ -54,6 +56,7 @@ __global__ void __launch_bounds__(kMaskThreads) attn_mask_kernel(const int32_t *
   }
   ok = __syncthreads_and(ok);
   if (tid == 0) rowinfo[b] = !ok ? kRowBadParent : !slot_ok ? kRowBadSlot : c;
+  if (tid == 0 && row_status) row_status[b] = !ok ? SPEC_ROW_BAD_PARENT : !slot_ok ? SPEC_ROW_BAD_SLOT : 0;
   if (!ok || !slot_ok) return;
   for (int i = tid; i < used; i += kMaskThreads) {
     uint32_t *row = anc + (static_cast<size_t>(b) * N + i) * W;
@@ -1019,12 +1022,14 @@ spec_status spec_prefix_attention(const spec_attention_args *a, void *out, float
   p.wait_limit_ns = spec_get_wait_timeout_ns();
   p.force_timeout = force_wait_timeout();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a->parent) {
+  int32_t *const status_here = plan.direct ? row_status : nullptr;
+  if (a->parent || status_here) {
     uint32_t *anc = reinterpret_cast<uint32_t *>(w + plan.anc_at);
     int32_t *info = reinterpret_cast<int32_t *>(w + plan.info_at);
-    attn_mask_kernel<<<p.B, kMaskThreads, 0, s>>>(a->parent, a->kv_len, a->count, c.slots, p.N, p.W, anc, info);
+    attn_mask_kernel<<<p.B, a->parent ? kMaskThreads : 32, 0, s>>>(a->parent, a->kv_len, a->count, c.slots, p.N, p.W, anc, info,
+                                                                   status_here);
     if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
-    p.anc = anc;
+    if (a->parent) p.anc = anc;
     p.rowinfo = info;
   }
   if (plan.widen) {

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
     cnt = row_queries(P, b);
     len0 = __ldg(P.kv_len + b);
     len = len0 + cnt;
-    if (split == 0 && blk == 0 && g == 0 && tid == 0 && P.row_status)
+    if (split == 0 && blk == 0 && g == 0 && tid == 0 && P.row_status && !P.direct)  // P.direct: the mask kernel has
       P.row_status[b] = cnt >= 0 ? 0 : cnt == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
     const int all = cnt > 0 ? npre + (len + kTok - 1) / kTok : 0, per = (all + nsplit - 1) / nsplit;
     q0 = split * per;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
         }
       }
       fence_async_smem();
-      if (!(P.force_timeout && it == 0)) mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
+      if (!(it == 0 && (P.force_timeout == 1 || P.force_timeout == g + 2))) mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
       sc0 = sc1;
       sc1 = issue(it + 2);  // after this item is handed over: its buffer may be a while in coming free
     }
@@ -946,7 +946,7 @@ cudaError_t launch(const AttnParams &p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // the mask and conversion kernels ahead of it let it start early
   return launch_after(attn_tile_kernel<CT, DP, PRE>, dim3(static_cast<unsigned>(items)), Roles<CT == SPEC_E4M3>::kThreads,
-                      C::kSmem, s, p.first && (p.anc || p.wide), p, blocks);
+                      C::kSmem, s, p.first && (p.rowinfo || p.wide), p, blocks);
 }
 
 template <int CT>
@@ -959,7 +959,7 @@ cudaError_t launch_d(const AttnParams &p, bool prefix, cudaStream_t s) {
 
 cudaError_t launch_attn_widen(const AttnParams &p, cudaStream_t s) {
   const dim3 grid((p.P + kTok - 1) / kTok, p.H, 2);
-  return launch_after(attn_widen_kernel, grid, kWidenThreads, 0, s, p.anc != nullptr, p);
+  return launch_after(attn_widen_kernel, grid, kWidenThreads, 0, s, p.rowinfo != nullptr, p);
 }
 
 cudaError_t launch_attn_tile(const AttnParams &p, int ctype, bool prefix, cudaStream_t s) {
