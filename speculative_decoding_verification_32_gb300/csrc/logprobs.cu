@@ -80,13 +80,25 @@ __device__ __forceinline__ void join(float &m, float &s, float &u, float m2, flo
   m = M;
 }
 
+// log2(e) / T, at most kMostScale: past fp32's range (T below 2^-127) any factor puts
+// every logit but the largest out of the sums, and must not make NaN of the largest.
+constexpr float kMostScale = 0x1p127f;
+__device__ __forceinline__ float row_temperature(const LpParams &P, int r) {
+  return P.temperature ? __ldg(P.temperature + r / P.npos) : 1.f;
+}
 __device__ __forceinline__ float row_scale(const LpParams &P, int r, uint32_t &flags) {
-  const float T = P.temperature ? __ldg(P.temperature + r / P.npos) : 1.f;
+  const float T = row_temperature(P, r);
   if (!(T > 0.f) || isinf(T)) {
     flags |= F_BAD_TEMPERATURE;
     return 1.f;
   }
-  return kLog2e / T;
+  return fminf(kLog2e / T, kMostScale);
+}
+// log p of a logit d above the largest; in nats from the start (in base 2 the
+// product may pass fp32's range where the result does not)
+__device__ __forceinline__ float log_p(const LpParams &P, int r, float d, float sc, float lgs) {
+  const float y = sc == kMostScale ? d / row_temperature(P, r) : d * (sc * kLn2);
+  return y - kLn2 * lgs;
 }
 
 // One slice's logits of a thread, as they are in memory.
@@ -288,7 +300,7 @@ __global__ void __launch_bounds__(kLpThreads, BF16 ? 3 : 5) logprobs_kernel(cons
   const float lgs = log2f(s);
   const bool bad = flags != 0;
   if (rank == 0 && tid == 0) {
-    if (P.tokens) P.logprob[r] = bad ? NAN : kLn2 * ((xt - m) * sc - lgs);
+    if (P.tokens) P.logprob[r] = bad ? NAN : log_p(P, r, xt - m, sc, lgs);
     P.entropy[r] = bad ? NAN : fmaxf(0.f, kLn2 * (lgs - u / s));
     P.status[r] = lowest_code(flags);
   }
@@ -403,7 +415,7 @@ __global__ void __launch_bounds__(kLpThreads, BF16 ? 3 : 5) logprobs_kernel(cons
     for (int j = 0; j < n; ++j) rank += cand[j] > k;
     if (rank < P.m) {
       ids[rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k));
-      lps[rank] = kLn2 * ((from_key(static_cast<uint32_t>(k >> 32)) - m) * sc - lgs);
+      lps[rank] = log_p(P, r, from_key(static_cast<uint32_t>(k >> 32)) - m, sc, lgs);
     }
   }
 }
