@@ -236,9 +236,9 @@ def workspace(device, nbytes, handle, stream=None):
 _enqueue_locks = {}
 
 
-def _enqueuing(device, stream):
-    key = (device, stream)
-    return _enqueue_locks.get(key) or _enqueue_locks.setdefault(key, threading.RLock())
+def _enqueuing(key):
+    """The lock of the workspace with this key."""
+    return _enqueue_locks.setdefault(key, threading.RLock())
 
 
 class _Here:
@@ -315,7 +315,7 @@ def spec_verify_chain(target_logits, draft_logits, draft_tokens, temperature=Non
               else L.spec_verify_chain_workspace_size)(B, K, V)
     on = _device(dev, stream)
     s, sp = _stream(dev, stream)
-    with on, _enqueuing(dev, s.cuda_stream):
+    with on, _enqueuing((dev, s.cuda_stream)):
         ws = workspace(dev, nbytes, s.cuda_stream, stream)
         if not truncated:
             _check(L.spec_verify_chain(_c.byref(args), _c.byref(o), _ptr(ws), ws.numel(), sp))
@@ -359,7 +359,7 @@ def spec_verify_tree(target_logits, parent, node_tokens, temperature=None, margi
     nbytes = L.spec_verify_tree_workspace_size(B, N, V)
     on = _device(dev, stream)
     s, sp = _stream(dev, stream)
-    with on, _enqueuing(dev, s.cuda_stream):
+    with on, _enqueuing((dev, s.cuda_stream)):
         ws = workspace(dev, nbytes, s.cuda_stream, stream)
         _check(L.spec_verify_tree(_c.byref(args), _c.byref(o), _ptr(ws), ws.numel(), sp))
     return out
@@ -407,7 +407,7 @@ def spec_drift_residuals(target_logits, draft_logits, temperature=None, m=32, st
     nbytes = L.spec_verify_chain_truncated_workspace_size(B, K, V)
     on = _device(dev, stream)
     s, sp = _stream(dev, stream)
-    with on, _enqueuing(dev, s.cuda_stream):
+    with on, _enqueuing((dev, s.cuda_stream)):
         ws = workspace(dev, nbytes, s.cuda_stream, stream)
         _check(L.spec_drift_residuals(_c.byref(args), int(m), _ptr(sup), _ptr(res), _ptr(st),
                                       _ptr(ws), ws.numel(), sp))
@@ -521,13 +521,23 @@ class _On:
 def _on(device, stream, *tensors):
     """The context in which a call makes its outputs and launches: on `stream`,
     or (None) on the current stream of `device`."""
-    if stream is None:
-        return _here if device.type == "cuda" and device.index == _current_device() else _device(device)
-    _device(device, stream)
-    return _On(stream, *tensors)
+    on = _device(device, stream)
+    return on if stream is None else _On(stream, *tensors)
 
 
-def _scratch(dev, stream, nbytes):
+def _enter(device, stream, *tensors):
+    """That context, entered (the calls skip it where it would do nothing)."""
+    on = _on(device, stream, *tensors)
+    on.__enter__()
+    return on
+
+
+def _leave(on):
+    if on is not None:
+        on.__exit__(None, None, None)
+
+
+def _scratch(dev, key, nbytes):
     """A workspace of these calls' own (the verify calls keep a header and
     stamped records in theirs): the stream's, or a larger one in its place.  A
     call captured into a graph gets one from the graph's pool: a replay may run
@@ -535,7 +545,7 @@ def _scratch(dev, stream, nbytes):
     buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     if not _capturing():
         with _ws_lock:
-            _ws[(dev, "scratch", stream)] = buf
+            _ws[key] = buf
     return buf
 
 
@@ -621,9 +631,13 @@ def spec_kv_append(cache, k, v, kv_len, count=None, stream=None):
         raise ValueError("kv_len is needed")
     a = _PACK_APPEND.pack(*c, N, _kv_dtype(dtype, "k"), k.data_ptr(), v.data_ptr(), *ks[:3], *vs[:3],
                           _i32(kv_len, "kv_len", dev, (B,)), _i32(count, "count", dev, (B,)))
-    with _on(dev, stream, cache, k, v, kv_len, count):
+    index = dev.index
+    on = None if stream is None and k.is_cuda and index == _current_device() else _enter(dev, stream, cache, k, v, kv_len, count)
+    try:
         status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
-        _check(_fn("spec_kv_append", 3)(a, status.data_ptr(), _raw_stream(dev.index)))
+        _check(_fn("spec_kv_append", 3)(a, status.data_ptr(), _raw_stream(index)))
+    finally:
+        _leave(on)
     return status
 
 
@@ -645,12 +659,16 @@ def spec_kv_read(cache, length, T, heads=None, head_dim=None, start=None, dtype=
     if length is None:
         raise ValueError("length is needed")
     code, n, s = _kv_dtype(dtype, "dtype"), _i32(length, "length", dev, (B,)), _i32(start, "start", dev, (B,))
-    with _on(dev, stream, cache, length, start):
+    index = dev.index
+    on = None if stream is None and cache.is_cuda and index == _current_device() else _enter(dev, stream, cache, length, start)
+    try:
         k = torch.empty(B, T, heads, head_dim, dtype=dtype, device=dev)
         v = torch.empty_like(k)
         status = (torch.empty if T else torch.zeros)(B, dtype=torch.int32, device=dev)
         a = _PACK_READ.pack(*c, T, code, k.data_ptr(), v.data_ptr(), s, n)
-        _check(_fn("spec_kv_read", 3)(a, status.data_ptr(), _raw_stream(dev.index)))
+        _check(_fn("spec_kv_read", 3)(a, status.data_ptr(), _raw_stream(index)))
+    finally:
+        _leave(on)
     return k, v, status
 
 
@@ -708,20 +726,25 @@ def spec_prefix_attention(q, cache, kv_len, prefix=None, prefix_len=None, parent
     a = _PACK_ATTENTION.pack(*c, *pc, P, N, heads, _KV_DTYPES[dtype], D ** -0.5 if scale is None else scale,
                              q.data_ptr(), *qs[:3], _i32(kv_len, "kv_len", dev, (B,)),
                              _i32(count, "count", dev, (B,)), _i32(parent, "parent", dev, (B, N)))
-    with _on(dev, stream, q, cache, kv_len, prefix, parent, count):
+    index = dev.index
+    on = None if stream is None and q.is_cuda and index == _current_device() else \
+        _enter(dev, stream, q, cache, kv_len, prefix, parent, count)
+    try:
         out = torch.empty(shape, dtype=dtype, device=dev)
         lse = torch.empty(B, N, heads, dtype=torch.float32, device=dev)
         status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
-        s = _raw_stream(dev.index)
-        f, code = _fn("spec_prefix_attention", 7), SPEC_ERR_WORKSPACE
-        with _enqueuing(dev, s):
-            ws = None if _capturing() else _ws.get((dev, "scratch", s))
+        s = _raw_stream(index)
+        f, code, key = _fn("spec_prefix_attention", 7), SPEC_ERR_WORKSPACE, (index, "scratch", s)
+        with _enqueue_locks.get(key) or _enqueuing(key):
+            ws = None if _capturing() else _ws.get(key)
             if ws is not None:  # the call itself says if that is too small, before it launches anything
                 code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
             if code == SPEC_ERR_WORKSPACE:
-                ws = _scratch(dev, s, _attention_bytes(a))
+                ws = _scratch(dev, key, _attention_bytes(a))
                 code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
         _check(code)
+    finally:
+        _leave(on)
     return out, lse, status
 
 
@@ -751,7 +774,9 @@ def spec_token_logprobs(logits, tokens=None, temperature=None, m=0, stream=None)
     a = _PACK_LOGPROBS.pack(B, npos, V, dt, m, 0, pitch, logits.data_ptr(), tk,
                             0 if temperature is None else temperature.data_ptr())
     f32 = torch.float32
-    with _on(dev, stream, logits, tokens, temperature):
+    index = dev.index
+    on = None if stream is None and logits.is_cuda and index == _current_device() else _enter(dev, stream, logits, tokens, temperature)
+    try:
         out = dict(entropy=torch.empty(B, npos, dtype=f32, device=dev),
                    status=torch.empty(B, npos, dtype=torch.int32, device=dev),
                    top_ids=torch.empty(B, npos, m, dtype=torch.int32, device=dev),
@@ -761,7 +786,9 @@ def spec_token_logprobs(logits, tokens=None, temperature=None, m=0, stream=None)
         o = _PACK_LOGPROBS_OUT.pack(out["logprob"].data_ptr() if tokens is not None else 0,
                                     out["entropy"].data_ptr(), out["top_ids"].data_ptr(),
                                     out["top_logprobs"].data_ptr(), out["status"].data_ptr())
-        _check(_fn("spec_token_logprobs", 3)(a, o, _raw_stream(dev.index)))
+        _check(_fn("spec_token_logprobs", 3)(a, o, _raw_stream(index)))
+    finally:
+        _leave(on)
     return out
 
 
