@@ -498,7 +498,8 @@ size_t spec_kv_entry_bytes(int32_t heads, int32_t head_dim, int32_t dtype);
  * element by element.  count [rows] (NULL: N for every row) is how many of the
  * N tokens row b has.  row_status [rows] (optional): SPEC_ROW_BAD_SLOT where
  * kv_len[b] < 0, count[b] is outside [0, N] or kv_len[b] + count[b] > slots;
- * such a row is left untouched.  One launch, no workspace.
+ * such a row is left untouched.  One launch, no workspace.  N = 0 is a no-op, and
+ * row_status is not written.
  */
 typedef struct {
   spec_kv_cache cache;
@@ -520,7 +521,8 @@ spec_status spec_kv_append(const spec_kv_append_args *args, int32_t *row_status,
  * t < length[b], and zero from there to T.  Values are exact in fp32, then
  * rounded once to out_dtype.  row_status [rows] (optional): SPEC_ROW_BAD_SLOT
  * where start[b] < 0, length[b] is outside [0, T] or start[b] + length[b] >
- * slots; such a row reads as zeros.  One launch, no workspace.
+ * slots; such a row reads as zeros.  One launch, no workspace.  T = 0 is a no-op,
+ * and row_status is not written.
  */
 typedef struct {
   spec_kv_cache cache;
@@ -574,11 +576,13 @@ spec_status spec_kv_read(const spec_kv_read_args *args, int32_t *row_status, voi
  * rounded once to the cache's 16-bit type (fp16 for SPEC_E4M3) for the product
  * with v.  Results do not depend on timing: every sum has a fixed order.
  * Scales of an SPEC_E4M3 cache may lie any distance apart; where those of
- * neighbouring tokens are more than 2^15 apart the call takes longer.  (Beside
+ * neighbouring tokens (of 128, in the kernel for many query rows) are more than
+ * 2^15 apart the part of the call that holds them is taken again in fp32, which
+ * takes milliseconds, up to 0.7 s for 1920 queries over 4097 entries.  (Beside
  * a token whose values are all zero and whose weight is more than 2^15 times
  * every other's, the others' weights may be rounded to multiples of 2^-39.)
  * Workspace: spec_prefix_attention_workspace_size(args) bytes, no contents
- * kept between calls.
+ * kept between calls.  N = 0 is a no-op, and row_status is not written.
  */
 typedef struct {
   spec_kv_cache cache;     /* the rows' own entries */
@@ -621,7 +625,9 @@ spec_status spec_prefix_attention(const spec_attention_args *args, void *out, fl
  * BAD_TEMPERATURE); a flagged position's floats are NaN and its ids -1.
  * B * npos < 2^31 / 64.  One launch, no workspace: each position's CTAs pass over
  * its logits once, keep the largest of every 32 (bf16) or 16 (fp32) of them, and
- * look again only at those that can hold one of the top m.
+ * look again only at those that can hold one of the top m.  Where more than 1024
+ * can (masses of equal logits, or fewer than m that are finite) one CTA searches
+ * the position bit by bit: slower by a factor of 14 to 42 as measured.
  */
 typedef struct {
   int32_t B, npos, V;

@@ -265,7 +265,11 @@ __device__ __forceinline__ float query_value(unsigned short u, int bf16) {
 // own e4m3 entries from the codes, in fp32, by one thread: for parts in which
 // scales lie further apart than the kernels' ways span (a token that nothing
 // sees, or whose weight is nothing, must not cost the others their bits).
-// Slower by two orders, and not met by scales within 2^15 of one another.
+// Not met by scales within 2^15 of one another, and slower by up to three and a half
+// orders: with one prefix token's values 2^40 up, 32 trees of 60 nodes behind 4097
+// tokens (the answers' items hold prefix and own entries) take 0.70 s where they take
+// 0.20 ms without; 64 decoding rows behind 8192, parts of four blocks, 42 ms where
+// they take 0.077, and 4.7 ms with such a token in every row's own entries instead.
 // len0: own entries that every query sees; my, anc: the query's index and
 // ancestor bits; qoff: where it is; odd: values of the pass's own tokens that
 // are not finite are to be put into an answer that is written here (P.direct).

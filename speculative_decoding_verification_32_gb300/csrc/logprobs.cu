@@ -16,8 +16,10 @@
 // memory.  The top m are found without reading the position again: the m-th
 // largest of the 256 threads' maxima is a lower bound of the m-th largest
 // logit's key, and only the few chunks that reach it are looked at.  Positions
-// where that leaves too many (masses of equal logits) are searched whole.
-// While one position's CTAs are at that, others keep the memory busy: with a
+// where that leaves too many (masses of equal logits; fewer finite ones than m,
+// so that -inf is among the alternatives) are searched whole by one CTA: 224
+// positions of 128256 bf16 logits take 0.73 ms then, where they take 20 us.
+// While one position's CTAs are at its end, others keep the memory busy: with a
 // second kernel for it, 224 positions of 128256 bf16 logits took 23 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -170,8 +172,9 @@ __device__ __forceinline__ unsigned long long ld_remote_u64(const void *p, uint3
 // Grid: position * cluster size + rank (SPREAD: clusters of more than one).
 // CTAs per SM as measured: 224 positions of 128256 bf16 logits 20 us at 3 and 23
 // at 4 (8.4 would be the bytes at the copy rate: the rest is the end of a
-// position); 2047 positions of 32000 fp32 logits 61 us at 3, 56 at 4, 54 at 5
-// (4.8 TB/s, 0.72 of the copy rate) and 70 at 6, where registers spill.
+// position); 2047 positions of 32000 fp32 logits 61 us at 3, 56 at 4, 54 to 56 at 5
+// (4.7 TB/s, 0.69 of the copy rate; 48 registers, 32 to 96 bytes a thread spill)
+// and 70 at 6, where more does.
 template <bool BF16, bool VEC, bool SPREAD>
 __global__ void __launch_bounds__(kLpThreads, BF16 ? 3 : 5) logprobs_kernel(const __grid_constant__ LpParams P) {
   constexpr int E = BF16 ? 8 : 4;

@@ -27,7 +27,7 @@
 // Measured with 32 query heads and 8 KV heads of 128: a block of 128 tokens takes
 // both tiles 1.84 us in bf16 (the products alone 1.6; 1.35 at the library's dense
 // rate), an item's start and end about 11; 64 chains of 6 tokens behind 8192: 50
-// us.  32 trees of 60 nodes in e4m3: 201 us, two rounds of items where 1.7 would
+// us.  32 trees of 60 nodes in e4m3: 202 us, two rounds of items where 1.7 would
 // do.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,7 +45,8 @@ namespace {
 constexpr int kTok = 128;          // tokens per block, a producer thread each
 // Groups of 128 threads: softmax of tiles A and B, producers, tensor-core
 // issue.  Their registers per thread add up to what the block is launched
-// with, and are split so that no role's loop spills: with 160 for the softmax
+// with, and are split so that the loops hold what they need (12 to 20 bytes spill
+// in three of the variants for codes): with 160 for the softmax
 // and 120 for producers of codes, 32 trees of 60 nodes behind 4097 tokens take
 // 212 us where this split takes 201.  (Two groups of producers, 96 registers a
 // thread, were 8 % slower than one.)
