@@ -6,7 +6,8 @@
 // c_t = v_t in a 16-bit cache; in an e4m3 cache c_t are the codes and 2^e_t the
 // scale).  A part of the keys is summed up as
 //   m = max_t (x_t + e_t),  O = sum_t 2^(x_t + e_t - m) c_t,  z = log2 sum_t 2^x_t,
-// so the weights of the codes never exceed 1, whatever the scales, and the
+// (m may lie below that: weights of the codes then reach 2^8, in the tile kernel
+// 2^15.5) so the weights of the codes stay in range, whatever the scales, and the
 // query's answer over several parts is
 //   Z = log2 sum 2^z,  out = sum 2^(m - Z) O,  lse = ln 2 Z.
 #pragma once
