@@ -101,7 +101,9 @@ enum {
   SPEC_ROW_EMPTY = 5,           /* a logit row that is -inf everywhere */
   SPEC_ROW_TIMEOUT = 6,         /* a bounded on-device wait gave up (see below) */
   SPEC_ROW_BAD_TEMPERATURE = 7, /* temperature used and not finite and > 0 */
-  SPEC_ROW_BAD_SLOT = 8         /* KV cache: a length, start or count outside the row's slots */
+  SPEC_ROW_BAD_SLOT = 8,        /* KV cache: a length, start or count outside the row's slots, or
+                                   a page number outside the cache */
+  SPEC_ROW_NO_PAGES = 9         /* spec_page_plan: not enough free pages for the row */
 };
 
 /* Logits are SPEC_F32 or SPEC_BF16; the cache and attention calls also use
@@ -116,6 +118,7 @@ typedef enum { SPEC_STOCHASTIC = 0, SPEC_GREEDY = 1 } spec_mode;
 #define SPEC_MAX_HEAD_DIM 128    /* KV cache and attention: head size, a multiple of 16 */
 #define SPEC_MAX_HEADS 1024      /* KV cache and attention: heads per token */
 #define SPEC_MAX_TOP 64          /* spec_token_logprobs: alternatives per position */
+#define SPEC_MAX_PAGE 1024       /* paged cache: tokens per page, a multiple of 16 */
 
 /* ------------------------------------------------------------------ chain */
 
@@ -650,6 +653,215 @@ typedef struct {
 
 spec_status spec_token_logprobs(const spec_logprobs_args *args, const spec_logprobs_out *out,
                                 void *stream);
+
+/* ------------------------------------------------------------ a paged cache */
+
+/*
+ * A cache whose rows are cut into pages: pages of page_size token slots out of
+ * one pool that all rows share.  block_table [B, columns] names each row's
+ * pages: token t of row b is slot t % page_size of page
+ * block_table[b][t / page_size]; a negative entry is no page.  The token's place
+ * in the pool, page * page_size + t % page_size, is its slot number: with the
+ * pool described as a spec_kv_cache of one row of pages * page_size slots,
+ * rows = B * N, row_stride = 0 and kv_len = the slot map, spec_kv_append with
+ * N = 1 writes each token of the pass to its slot (and leaves those whose slot is
+ * -1 alone, as SPEC_ROW_BAD_SLOT).
+ *
+ * spec_page_plan -- block tables and slot maps from the rows' lengths, on the
+ * device, once per pass ("Speculative Decoding: Draft, Verify, and Correct",
+ * 'Speculation needs cache rollback': lengths go up by the pass's tokens and
+ * back by the rejected ones).  Row b holds kv_len[b] tokens and this pass brings
+ * count[b] more (NULL: N).  Its live pages are those that hold one of these
+ * kv_len[b] + count[b] tokens, without the pages that no query from position
+ * kv_len[b] on can see: with a window > 0, pages all of whose tokens t have
+ * t >= sinks and t <= kv_len[b] - window (see spec_paged_attention).  The call
+ *   - gives a live place without a page the next free one, and
+ *   - gives pages at places that are not live back, and sets these to -1.
+ * A finished row gives all its pages back with kv_len = count = 0.
+ *
+ * Free pages are a ring: free_pages [num_pages] holds free_state[1] page
+ * numbers from index free_state[0] on (wrapping around).  Pages are taken from
+ * its head and given back behind its tail, both in the order of rows, then
+ * places, so the result does not depend on timing; pages given back by a call
+ * are not taken by the same call.  A new ring is {0, 1, ..., num_pages - 1}
+ * with free_state {0, num_pages}.
+ *
+ * slot_map [B, N]: the slot number of token kv_len[b] + i for i < count[b], else
+ * -1.  row_status [B] (optional):
+ *   SPEC_ROW_BAD_SLOT: kv_len[b] < 0, count[b] outside [0, N], kv_len[b] +
+ *     count[b] > columns * page_size, or a page number >= num_pages in the row;
+ *     it is left untouched, its slots are -1.  Likewise every row if free_state
+ *     is not a ring's.  (A ring that holds a number outside [0, num_pages), or
+ *     has no room for what comes back, was broken before: the rows that meet
+ *     this get the code too, a bad number is not put into the table, its tokens'
+ *     slots are -1, and a page without room is dropped.)
+ *   SPEC_ROW_NO_PAGES: rows are served in order; one for which not enough free
+ *     pages are left, counting those that the rows before it wanted, takes none
+ *     (it gives its dead pages back all the same), and its slots are -1.
+ * block_table, free_pages and free_state are read and written; other arrays must
+ * not overlap them.  0 <= N, 1 <= columns, columns * page_size < 2^31,
+ * num_pages * page_size < 2^31, B * N < 2^31, B * columns < 2^31, B <= 2^20,
+ * 0 <= window, 0 <= sinks (sinks without a window have no effect).  Two launches.
+ * Workspace: spec_page_plan_workspace_size(B) bytes.
+ */
+typedef struct {
+  int32_t B;             /* rows */
+  int32_t N;             /* tokens per row in this pass, at most */
+  int32_t columns;       /* places per row in block_table */
+  int32_t page_size;     /* 16 .. SPEC_MAX_PAGE, a multiple of 16 */
+  int32_t num_pages;     /* pages in the pool */
+  int32_t window;        /* 0: every token stays visible */
+  int32_t sinks;         /* first tokens that stay visible all the same */
+  int32_t pad;
+  int32_t *block_table;  /* [B, columns] */
+  int32_t *free_pages;   /* [num_pages] */
+  int32_t *free_state;   /* [2] {head, free pages} */
+  const int32_t *kv_len; /* [B] */
+  const int32_t *count;  /* [B] or NULL */
+} spec_page_plan_args;
+
+size_t spec_page_plan_workspace_size(int32_t B);
+
+spec_status spec_page_plan(const spec_page_plan_args *args, int32_t *slot_map, int32_t *row_status,
+                           void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * spec_kv_compact_pages -- spec_kv_compact_tree for a paged cache: the entry of
+ * path node path_nodes[b][k] (token kv_len_in[b] + path_nodes[b][k] of the row)
+ * moves to token kv_len_in[b] + 1 + k, k < accepted_len[b], in every plane.
+ * The entry of (plane p, page g, slot s) starts at kv + p*plane_stride +
+ * g*page_stride + s*tok_stride and is entry_bytes long; kv is 16-byte aligned,
+ * entry_bytes and the strides are multiples of 16 (else SPEC_ERR_ALIGN).
+ * row_status[b] (optional): SPEC_ROW_BAD_PARENT for a path that is not strictly
+ * increasing within [1, N), SPEC_ROW_BAD_SLOT where kv_len_in[b] < 0, the path's
+ * last node lies past the table or one of the places it moves from or to has no
+ * page in [0, num_pages); such a row is left untouched.  accepted_len <= 0 is a
+ * no-op.  B, planes <= 65535.  No workspace.
+ */
+typedef struct {
+  int32_t B, N, planes, columns;
+  int32_t page_size, num_pages;
+  int64_t entry_bytes, plane_stride, page_stride, tok_stride;
+  void *kv;                     /* device, read and written in place */
+  const int32_t *block_table;   /* [B, columns] */
+  const int32_t *kv_len_in;     /* [B] cache length before the verify pass */
+  const int32_t *accepted_len;  /* [B] from spec_verify_tree */
+  const int32_t *path_nodes;    /* [B, N] from spec_verify_tree */
+} spec_page_compact_args;
+
+spec_status spec_kv_compact_pages(const spec_page_compact_args *args, int32_t *row_status,
+                                  void *stream);
+
+/*
+ * spec_paged_attention -- attention over a paged cache: a prompt's tokens, single
+ * tokens, chains or trees of drafted tokens ("Speculative Decoding: Draft, Verify,
+ * and Correct", 'Verify several proposed tokens in one target pass'; "Speculative
+ * Decoding: How a Small Model Speeds Up a Big One", 'Beyond Two Models: The EAGLE
+ * Line'), with a sliding window and first tokens that stay visible.
+ *
+ * Query i of row b (i < count[b], count NULL: N) is the token that was written
+ * to token slot kv_len[b] + i of the row's pages.  It stands at position
+ * p = kv_len[b] + i, or kv_len[b] + depth in a tree (parent [B, N] as in
+ * spec_verify_tree), and its head h reads KV head h / (q_heads / heads).  Of the
+ * row's tokens 0 .. kv_len[b] - 1, each at its own position, and of the pass's own
+ * tokens up to itself (in a tree: its ancestors and itself) it sees those at a
+ * position t with t < sinks or p - t < window (window 0: all of them).  Over these
+ *   x_t = scale * q . k_t,  out = sum_t softmax(x)_t v_t,  lse = ln sum_t exp(x_t).
+ * Nothing else is read into the result: other tokens, slots past the row's last
+ * token and pages that hold none of the above may hold anything, NaN included,
+ * and table entries of pages that no query of the row sees may be anything.
+ *
+ * The entry of slot s of page g starts at k (or v) + g * page_stride + s *
+ * tok_stride bytes and is spec_kv_entry_bytes(heads, head_dim, cache_dtype) long
+ * (the layouts of spec_kv_cache).  q [B, N, q_heads, head_dim] of q_dtype
+ * (SPEC_BF16 or SPEC_F16) with strides in elements for row, token and head and a
+ * dense last dimension; q_heads is a multiple of heads; the cache has q_dtype or
+ * SPEC_E4M3.  out [B, N, q_heads, head_dim] of q_dtype and lse [B, N, q_heads]
+ * fp32 (optional) are dense, 16-byte aligned.  B <= 65535, N <=
+ * SPEC_MAX_TREE_NODES in a tree, B * N * q_heads < 2^31 / 256,
+ * columns * page_size <= 2^31 - 4097, num_pages * page_size < 2^31, tok_stride < 2^27.
+ *
+ * row_status [B] (optional): SPEC_ROW_BAD_SLOT (kv_len[b] < 0, count[b] outside
+ * [0, N], kv_len[b] + count[b] > columns * page_size, or a page that the row's
+ * queries see outside [0, num_pages)) or SPEC_ROW_BAD_PARENT; such a row, and a
+ * query i >= count[b], gets zeros and lse = -inf.
+ *
+ * Sums, maxima and softmax statistics are fp32; the softmax weights are rounded
+ * once to the product's 16-bit type (the cache's; fp16 for SPEC_E4M3, where the
+ * weight of a value's code, weight times scale, is rounded).  Results do not
+ * depend on timing: every sum has a fixed order.
+ * Workspace: spec_paged_attention_workspace_size(args) bytes, no contents kept
+ * between calls.  N = 0 is a no-op, and row_status is not written.
+ */
+typedef struct {
+  int32_t B, N, q_heads, heads, head_dim;
+  int32_t q_dtype, cache_dtype;
+  int32_t columns;             /* places per row in block_table */
+  int32_t page_size, num_pages;
+  int32_t window, sinks;
+  float scale;                 /* finite */
+  int32_t pad;
+  int64_t page_stride, tok_stride;  /* bytes */
+  int64_t q_stride[3];         /* elements: row, token, head */
+  const void *k, *v, *q;       /* device */
+  const int32_t *block_table;  /* [B, columns] */
+  const int32_t *kv_len;       /* [B] tokens before this pass */
+  const int32_t *count;        /* [B] or NULL */
+  const int32_t *parent;       /* [B, N] or NULL (a chain) */
+} spec_paged_attention_args;
+
+size_t spec_paged_attention_workspace_size(const spec_paged_attention_args *args);
+
+spec_status spec_paged_attention(const spec_paged_attention_args *args, void *out, float *lse,
+                                 int32_t *row_status, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ drafting */
+
+/*
+ * spec_sample -- one token per row, as a drafter draws its tokens
+ * ("Speculative Decoding: Draft, Verify, and Correct", 'Preserve the distribution
+ * you actually intend': q must be the law that actually produced the draft).
+ * Under p = softmax(logits / T_b), in this order:
+ *   top-k (1 <= top_k[b] < V, else off) keeps the tokens whose logit is >= the
+ *     k-th largest (ties at the boundary kept);
+ *   top-p (0 < top_p[b] < 1, else off) keeps, of those, whole groups of equal
+ *     logits in descending order until their renormalised mass reaches top_p[b];
+ *   min-p (0 < min_p[b] <= 1, else off) keeps, of those, the tokens with
+ *     p >= min_p[b] times the largest p, decided as l - l_max >= T_b ln(min_p[b])
+ *     in fp64.
+ * The token is the smallest v whose running sum, over the kept tokens in
+ * vocabulary order, exceeds u[b] times the whole; prob (optional) its probability
+ * under the kept, renormalised law.  With the same temperature, top_k and top_p,
+ * and without min_p, this is the law q of spec_verify_chain_truncated.
+ *
+ * logits [B, V], rows row_stride elements apart (>= V), SPEC_BF16 or SPEC_F32.
+ * row_status [B]: NONFINITE (a NaN or +inf logit), BAD_UNIFORM, EMPTY (no finite
+ * logit), BAD_TEMPERATURE; a flagged row's token is -1 and its prob NaN.
+ * Weights are fp32 with relative errors of about 2^-22, which average out in
+ * the sums; sums are exact integers of 2^-44, the same in any order.  A draw
+ * within about 1e-8 of a boundary of the law, or a top_p within that of a
+ * group's mass, may fall to either side.  One launch, no workspace; B < 2^25.
+ */
+typedef struct {
+  int32_t B, V;
+  int32_t dtype;             /* SPEC_BF16 or SPEC_F32 */
+  int32_t pad;
+  int64_t row_stride;        /* elements */
+  const void *logits;
+  const float *u;            /* [B] uniforms in [0, 1) */
+  const float *temperature;  /* [B] or NULL = 1 */
+  const int32_t *top_k;      /* [B] or NULL */
+  const float *top_p;        /* [B] or NULL */
+  const float *min_p;        /* [B] or NULL */
+} spec_sample_args;
+
+typedef struct {
+  int32_t *token;            /* [B] */
+  float *prob;               /* [B] or NULL */
+  int32_t *row_status;       /* [B] */
+} spec_sample_out;
+
+spec_status spec_sample(const spec_sample_args *args, const spec_sample_out *out, void *stream);
 
 /* Zero-fill a workspace on `stream` (a cudaMemsetAsync).  Optional: the
  * verify calls do not need a zeroed workspace. */

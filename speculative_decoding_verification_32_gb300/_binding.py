@@ -20,7 +20,8 @@ SPEC_F32, SPEC_BF16, SPEC_F16, SPEC_E4M3 = 0, 1, 2, 3
 SPEC_STOCHASTIC, SPEC_GREEDY = 0, 1
 SPEC_ERR_WORKSPACE = 7
 ROW_STATUS = {0: "OK", 1: "NONFINITE", 2: "BAD_TOKEN", 3: "BAD_UNIFORM", 4: "BAD_PARENT",
-              5: "EMPTY", 6: "TIMEOUT", 7: "BAD_TEMPERATURE", 8: "BAD_SLOT"}
+              5: "EMPTY", 6: "TIMEOUT", 7: "BAD_TEMPERATURE", 8: "BAD_SLOT",
+              9: "NO_PAGES"}
 
 _c = ctypes
 _P = _c.c_void_p
@@ -101,6 +102,36 @@ class SpecLogprobsOut(_c.Structure):
                 ("status", _P)]
 
 
+class SpecPagePlanArgs(_c.Structure):
+    _fields_ = [(n, _c.c_int32) for n in ("B", "N", "columns", "page_size", "num_pages", "window",
+                                          "sinks", "pad")] + \
+        [(n, _P) for n in ("block_table", "free_pages", "free_state", "kv_len", "count")]
+
+
+class SpecPageCompactArgs(_c.Structure):
+    _fields_ = [(n, _c.c_int32) for n in ("B", "N", "planes", "columns", "page_size", "num_pages")] + \
+        [(n, _c.c_int64) for n in ("entry_bytes", "plane_stride", "page_stride", "tok_stride")] + \
+        [(n, _P) for n in ("kv", "block_table", "kv_len_in", "accepted_len", "path_nodes")]
+
+
+class SpecPagedAttentionArgs(_c.Structure):
+    _fields_ = [(n, _c.c_int32) for n in ("B", "N", "q_heads", "heads", "head_dim", "q_dtype", "cache_dtype",
+                                          "columns", "page_size", "num_pages", "window", "sinks")] + \
+        [("scale", _c.c_float), ("pad", _c.c_int32), ("page_stride", _c.c_int64), ("tok_stride", _c.c_int64),
+         ("q_stride", _c.c_int64 * 3)] + \
+        [(n, _P) for n in ("k", "v", "q", "block_table", "kv_len", "count", "parent")]
+
+
+class SpecSampleArgs(_c.Structure):
+    _fields_ = [("B", _c.c_int32), ("V", _c.c_int32), ("dtype", _c.c_int32), ("pad", _c.c_int32),
+                ("row_stride", _c.c_int64)] + \
+        [(n, _P) for n in ("logits", "u", "temperature", "top_k", "top_p", "min_p")]
+
+
+class SpecSampleOut(_c.Structure):
+    _fields_ = [("token", _P), ("prob", _P), ("row_status", _P)]
+
+
 class SpecError(RuntimeError):
     """A spec_* entry point returned a non-zero spec_status."""
 
@@ -166,6 +197,18 @@ def _bind(L):
     L.spec_prefix_attention.restype = _c.c_int
     L.spec_token_logprobs.argtypes = [_c.POINTER(SpecLogprobsArgs), _c.POINTER(SpecLogprobsOut), _P]
     L.spec_token_logprobs.restype = _c.c_int
+    L.spec_page_plan_workspace_size.argtypes = [i32]
+    L.spec_page_plan_workspace_size.restype = sz
+    L.spec_page_plan.argtypes = [_c.POINTER(SpecPagePlanArgs), _P, _P, _P, sz, _P]
+    L.spec_page_plan.restype = _c.c_int
+    L.spec_kv_compact_pages.argtypes = [_c.POINTER(SpecPageCompactArgs), _P, _P]
+    L.spec_kv_compact_pages.restype = _c.c_int
+    L.spec_paged_attention_workspace_size.argtypes = [_c.POINTER(SpecPagedAttentionArgs)]
+    L.spec_paged_attention_workspace_size.restype = sz
+    L.spec_paged_attention.argtypes = [_c.POINTER(SpecPagedAttentionArgs), _P, _P, _P, _P, sz, _P]
+    L.spec_paged_attention.restype = _c.c_int
+    L.spec_sample.argtypes = [_c.POINTER(SpecSampleArgs), _c.POINTER(SpecSampleOut), _P]
+    L.spec_sample.restype = _c.c_int
     L.spec_workspace_init.argtypes = [_P, sz, _P]
     L.spec_workspace_init.restype = _c.c_int
     L.spec_status_string.argtypes = [_c.c_int]
@@ -475,9 +518,16 @@ _PACK_READ = struct.Struct("<" + _CACHE + "2i4Q")
 _PACK_ATTENTION = struct.Struct("<" + _CACHE + _CACHE + "q3ifQ3q3Q")
 _PACK_LOGPROBS = struct.Struct("<6iq3Q")
 _PACK_LOGPROBS_OUT = struct.Struct("<5Q")
+_PACK_PLAN = struct.Struct("<8i5Q")
+_PACK_COMPACT = struct.Struct("<6i4q5Q")
+_PACK_PAGED = struct.Struct("<12ifi5q7Q")
+_PACK_SAMPLE = struct.Struct("<4iq6Q")
+_PACK_SAMPLE_OUT = struct.Struct("<3Q")
 for _s, _t in ((_PACK_APPEND, SpecKvAppendArgs), (_PACK_READ, SpecKvReadArgs),
                (_PACK_ATTENTION, SpecAttentionArgs), (_PACK_LOGPROBS, SpecLogprobsArgs),
-               (_PACK_LOGPROBS_OUT, SpecLogprobsOut)):
+               (_PACK_LOGPROBS_OUT, SpecLogprobsOut), (_PACK_PLAN, SpecPagePlanArgs),
+               (_PACK_COMPACT, SpecPageCompactArgs), (_PACK_PAGED, SpecPagedAttentionArgs), (_PACK_SAMPLE, SpecSampleArgs),
+               (_PACK_SAMPLE_OUT, SpecSampleOut)):
     assert _s.size == _c.sizeof(_t), _t
 
 _KV_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
@@ -675,12 +725,12 @@ def spec_kv_read(cache, length, T, heads=None, head_dim=None, start=None, dtype=
 _NO_CACHE = (0,) * 9
 
 
-def _attention_bytes(a):
-    f = _fast.get("spec_prefix_attention_workspace_size")
+def _attention_bytes(a, name="spec_prefix_attention_workspace_size"):
+    f = _fast.get(name)
     if f is None:
-        f = lib()["spec_prefix_attention_workspace_size"]
+        f = lib()[name]
         f.argtypes, f.restype = [_P], _c.c_size_t
-        _fast["spec_prefix_attention_workspace_size"] = f
+        _fast[name] = f
     return f(a)
 
 
@@ -787,6 +837,195 @@ def spec_token_logprobs(logits, tokens=None, temperature=None, m=0, stream=None)
                                     out["entropy"].data_ptr(), out["top_ids"].data_ptr(),
                                     out["top_logprobs"].data_ptr(), out["status"].data_ptr())
         _check(_fn("spec_token_logprobs", 3)(a, o, _raw_stream(index)))
+    finally:
+        _leave(on)
+    return out
+
+
+def _same_device(stream, t):
+    """Whether a call on t's device needs no context of its own."""
+    return stream is None and t.is_cuda and t.device.index == _current_device()
+
+
+def spec_page_plan(block_table, free_pages, free_state, kv_len, N, page_size, count=None, window=0, sinks=0,
+                   stream=None):
+    """Block tables and slot maps of a paged cache from the rows' lengths (see
+    spec_page_plan in include/specverify.h).
+
+    block_table [B, columns], free_pages [num_pages] (a ring) and free_state [2]
+    int32 are updated in place: every page that row b needs for its kv_len[b]
+    tokens and the count[b] (None: N) of this pass is there afterwards, and the
+    pages it no longer needs are free.  window, sinks: as in
+    spec_paged_attention; pages that lie behind the window are given back.
+    Returns (slot_map [B, N] int32, row_status [B] int32).
+    """
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a [B, columns] tensor")
+    dev = block_table.device
+    B, columns = block_table.shape
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a [num_pages] tensor")
+    if kv_len is None or free_state is None:
+        raise ValueError("kv_len and free_state are needed")
+    head = (B, N, columns, page_size, free_pages.shape[0], window, sinks, 0,
+            _i32(block_table, "block_table", dev, (B, columns)), _i32(free_pages, "free_pages", dev, free_pages.shape),
+            _i32(free_state, "free_state", dev, (2,)), _i32(kv_len, "kv_len", dev, (B,)),
+            _i32(count, "count", dev, (B,)))
+    a = _PACK_PLAN.pack(*head)
+    on = None if _same_device(stream, block_table) else _enter(dev, stream, block_table, free_pages, free_state, kv_len, count)
+    try:
+        slots = torch.empty(B, max(N, 0), dtype=torch.int32, device=dev)
+        status = torch.empty(B, dtype=torch.int32, device=dev)
+        s = _raw_stream(dev.index)
+        f, code, key = _fn("spec_page_plan", 6), SPEC_ERR_WORKSPACE, (dev.index, "scratch", s)
+        with _enqueue_locks.get(key) or _enqueuing(key):
+            ws = None if _capturing() else _ws.get(key)
+            if ws is not None:
+                code = f(a, slots.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
+            if code == SPEC_ERR_WORKSPACE:
+                ws = _scratch(dev, key, lib().spec_page_plan_workspace_size(B))
+                code = f(a, slots.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
+        _check(code)
+    finally:
+        _leave(on)
+    return slots, status
+
+
+def spec_kv_compact_pages(kv, block_table, kv_len_in, accepted_len, path_nodes, stream=None):
+    """Compact each row's accepted tree path in place in a paged cache (see
+    spec_kv_compact_pages in include/specverify.h).
+
+    kv: a CUDA tensor [planes, pages, page_size, ...] whose trailing dimensions
+    form one token's entry (contiguous, any dtype); block_table [B, columns] and
+    path_nodes [B, N] int32.  Returns row_status [B] int32.
+    """
+    if not isinstance(kv, torch.Tensor) or kv.dim() < 4 or not kv.is_contiguous():
+        raise ValueError("kv must be a contiguous [planes, pages, page_size, ...] tensor")
+    dev = kv.device
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a [B, columns] tensor")
+    if not isinstance(path_nodes, torch.Tensor) or path_nodes.dim() != 2:
+        raise ValueError("path_nodes must be a [B, N] tensor")
+    if kv_len_in is None or accepted_len is None:
+        raise ValueError("kv_len_in and accepted_len are needed")
+    B, columns = block_table.shape
+    planes, pages, page = kv.shape[:3]
+    E = kv.element_size()
+    for n in kv.shape[3:]:
+        E *= n
+    a = _PACK_COMPACT.pack(B, path_nodes.shape[1], planes, columns, page, pages, E, pages * page * E, page * E, E,
+                           kv.data_ptr(), _i32(block_table, "block_table", dev, (B, columns)),
+                           _i32(kv_len_in, "kv_len_in", dev, (B,)), _i32(accepted_len, "accepted_len", dev, (B,)),
+                           _i32(path_nodes, "path_nodes", dev, (B, path_nodes.shape[1])))
+    on = None if _same_device(stream, kv) else _enter(dev, stream, kv, block_table, kv_len_in, accepted_len, path_nodes)
+    try:
+        status = torch.empty(B, dtype=torch.int32, device=dev)
+        _check(_fn("spec_kv_compact_pages", 3)(a, status.data_ptr(), _raw_stream(dev.index)))
+    finally:
+        _leave(on)
+    return status
+
+
+def spec_paged_attention(q, cache, block_table, kv_len, parent=None, count=None, window=0, sinks=0, scale=None,
+                         kv_heads=None, stream=None):
+    """Attention over a paged cache with a sliding window and first tokens that
+    stay visible (see spec_paged_attention in include/specverify.h).
+
+    q [B, N, q_heads, D] (bfloat16 or float16, any strides with a dense last
+    dimension): the pass's tokens, already written to token slots kv_len[b] + i of
+    their row; cache [2, pages, page_size, kv_heads, D] (q's dtype) or [2, pages,
+    page_size, entry bytes] uint8 (kv_heads needed); block_table [B, columns]
+    int32; parent [B, N] int32 for draft trees (None: chains); count [B] int32
+    queries per row (None: N); window: how many positions back a query sees,
+    itself included (0: all), sinks: first tokens that it sees all the same;
+    scale: 1/sqrt(D) if None.  Returns (out like q, dense; lse [B, N, q_heads]
+    float32; row_status [B] int32).
+    """
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, N, q_heads, head_dim] tensor")
+    dev, shape, dtype = q.device, q.shape, q.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float16:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    B, N, heads, D = shape
+    qs = q.stride()
+    if qs[3] != 1 and D > 1:
+        raise ValueError("q: the last dimension must be dense")
+    if kv_heads is None:
+        if not isinstance(cache, torch.Tensor) or cache.dim() != 5:
+            raise ValueError("kv_heads is needed for a uint8 cache")
+        kv_heads = cache.shape[3]
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a [B, columns] tensor")
+    columns = block_table.shape[1]
+    if kv_len is None:
+        raise ValueError("kv_len is needed")
+    pages, _, _, code, page, page_stride, tok_stride, k, v = _kv_cache(cache, kv_heads, D, dev, "cache")
+    a = _PACK_PAGED.pack(B, N, heads, kv_heads, D, _KV_DTYPES[dtype], code, columns, page, pages, window, sinks,
+                         D ** -0.5 if scale is None else scale, 0, page_stride, tok_stride, *qs[:3], k, v, q.data_ptr(),
+                         _i32(block_table, "block_table", dev, (B, columns)), _i32(kv_len, "kv_len", dev, (B,)),
+                         _i32(count, "count", dev, (B,)), _i32(parent, "parent", dev, (B, N)))
+    index = dev.index
+    on = None if _same_device(stream, q) else _enter(dev, stream, q, cache, block_table, kv_len, parent, count)
+    try:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+        lse = torch.empty(B, N, heads, dtype=torch.float32, device=dev)
+        status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
+        s = _raw_stream(index)
+        f, code, key = _fn("spec_paged_attention", 7), SPEC_ERR_WORKSPACE, (index, "scratch", s)
+        with _enqueue_locks.get(key) or _enqueuing(key):
+            ws = None if _capturing() else _ws.get(key)
+            if ws is not None:
+                code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
+            if code == SPEC_ERR_WORKSPACE:
+                ws = _scratch(dev, key, _attention_bytes(a, "spec_paged_attention_workspace_size"))
+                code = f(a, out.data_ptr(), lse.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), s)
+        _check(code)
+    finally:
+        _leave(on)
+    return out, lse, status
+
+
+def _per_row(t, name, dev, dtype, B):
+    """The address of a tensor of one number per row, or 0 for None."""
+    if t is None:
+        return 0
+    _req(t, name, dev, dtype)
+    if t.shape != (B,):
+        raise ValueError(f"{name} must be [{B}], got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def spec_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """One token per row under temperature, top-k, top-p and min-p, from given
+    uniforms (see spec_sample in include/specverify.h).
+
+    logits [B, V] (bfloat16 or float32; rows may be spaced wider than V), u [B]
+    float32 in [0, 1), temperature, top_p, min_p [B] float32 and top_k [B] int32
+    or None.  Returns a dict: token [B] int32, prob [B] float32 (the token's
+    probability under the truncated law), row_status [B] int32.
+    """
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a [B, V] tensor")
+    dev, st = logits.device, logits.stride()
+    B, V = logits.shape
+    dt = _dtype_code(logits)
+    pitch = st[0] if B > 1 else V
+    if V > 1 and st[1] != 1:
+        raise ValueError("logits: the last dimension must be dense")
+    if u is None:
+        raise ValueError("u is needed")
+    f32 = torch.float32
+    a = _PACK_SAMPLE.pack(B, V, dt, 0, pitch, logits.data_ptr(), _per_row(u, "u", dev, f32, B),
+                          _per_row(temperature, "temperature", dev, f32, B),
+                          _per_row(top_k, "top_k", dev, torch.int32, B), _per_row(top_p, "top_p", dev, f32, B),
+                          _per_row(min_p, "min_p", dev, f32, B))
+    on = None if _same_device(stream, logits) else _enter(dev, stream, logits, u, temperature, top_k, top_p, min_p)
+    try:
+        out = dict(token=torch.empty(B, dtype=torch.int32, device=dev),
+                   prob=torch.empty(B, dtype=f32, device=dev),
+                   row_status=torch.empty(B, dtype=torch.int32, device=dev))
+        o = _PACK_SAMPLE_OUT.pack(out["token"].data_ptr(), out["prob"].data_ptr(), out["row_status"].data_ptr())
+        _check(_fn("spec_sample", 3)(a, o, _raw_stream(dev.index)))
     finally:
         _leave(on)
     return out

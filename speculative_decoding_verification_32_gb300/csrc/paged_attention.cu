@@ -1,0 +1,872 @@
+// paged_attention.cu -- attention over a paged cache with a sliding window and
+// first tokens that stay visible (spec_paged_attention): the entry point, the
+// check of the rows, the kernel for few query rows and the join of the parts.
+//
+//  paged_check_kernel -- one CTA per row: lengths, the pages that the row needs,
+//    and for draft trees the parents, each node's depth and which of the pass's
+//    tokens it sees.  The attention kernel runs beside it and looks at the
+//    result before it writes anything.
+//  paged_rows_kernel -- 16 or 32 query rows (the query heads of one KV head and
+//    tokens of one row) against a part of their keys, one warp.
+//  paged_join_kernel -- one warp per query row adds up the parts.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "paged_attention.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kPaSms = 152;  // parts are sized for this many SMs
+constexpr float kPaLazy = 8.f;
+constexpr int kCheckThreads = 256;
+constexpr int kPaJoinThreads = 128;
+
+// -------------------------------------------------------------- row check
+__global__ void __launch_bounds__(kCheckThreads) paged_check_kernel(const __grid_constant__ PagedParams P, const int32_t *parent,
+                                                                    int32_t *rowinfo, uint32_t *anc, int32_t *depth) {
+  __shared__ int par[SPEC_MAX_TREE_NODES];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  allow_dependents();
+  int n;
+  const int c = paged_queries(P, b, n);
+  bool tree = true, paged = true;
+  const int used = parent ? max(0, min(P.count ? P.count[b] : P.N, P.N)) : 0;
+  for (int i = tid; i < used; i += kCheckThreads) {
+    const int p = parent[static_cast<size_t>(b) * P.N + i];
+    par[i] = p;
+    tree = tree && (i == 0 ? p == -1 : p >= 0 && p < i);
+  }
+  if (c > 0) {  // the pages of what the row's first query and later ones see
+    const Keys keys(P, n, n + c);
+    const int per = P.page / kGroup, row = keys.n;
+    for (int k = tid; k < row; k += kCheckThreads) {
+      const int g = keys.token(k) / kGroup;
+      if (k > 0 && k != keys.sink && g % per) continue;  // the page of the group before
+      const int pg = __ldg(P.table + static_cast<size_t>(b) * P.columns + g / per);
+      paged = paged && pg >= 0 && pg < P.pages;
+    }
+  }
+  tree = __syncthreads_and(tree);
+  paged = __syncthreads_and(paged);
+  const int code = !tree ? kRowBadParent : !paged || c < 0 ? kRowBadSlot : c;
+  if (tid == 0) {
+    rowinfo[b] = code;
+    if (P.row_status) P.row_status[b] = code >= 0 ? 0 : code == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
+  }
+  if (code < 0) return;
+  for (int i = tid; i < used; i += kCheckThreads) {
+    int d = 0;
+    for (int j = par[i]; j >= 0; j = par[j]) ++d;
+    depth[static_cast<size_t>(b) * P.N + i] = d;
+    // ancestors within the window, or sinks themselves, from the node up
+    uint32_t *const row = anc + (static_cast<size_t>(b) * P.N + i) * P.W;
+    int w = P.W - 1, back = 0;
+    uint32_t bits = 0;
+    for (int j = i; j >= 0; j = par[j], ++back) {  // indexes fall strictly on the way up
+      while (w > (j >> 5)) {
+        row[w--] = bits;
+        bits = 0;
+      }
+      if (back < P.window || n + d - back < P.sinks) bits |= 1u << (j & 31);
+    }
+    while (w >= 0) {
+      row[w--] = bits;
+      bits = 0;
+    }
+  }
+}
+
+// ------------------------------------------------------------- row kernel
+template <int CT, int DP, int MT>
+struct PagedRowCfg {
+  static constexpr bool E4 = CT == SPEC_E4M3;
+  static constexpr int kEsz = E4 ? 1 : 2;
+  static constexpr int kM = 16 * MT;                        // query rows
+  static constexpr int kStages = 3;
+  static constexpr int kPitch = DP * kEsz + 16;             // bytes of one token in a ring slot
+  static constexpr int kPlane = kGroup * kPitch;            // K or V of a group
+  static constexpr int kScales = E4 ? 2 * kGroup * 4 : 0;   // scale words, K then V
+  static constexpr int kTable = E4 ? kGroup * 8 : 0;        // what they come to, per token
+  static constexpr int kStage = 2 * kPlane + kScales;
+  static constexpr int kQPitch = DP * 2 + 16;
+  static constexpr int kQ = kM * kQPitch + kM * 4;          // queries and factors, in the last slot before it is used
+  static constexpr int kSmem = (kStages - 1) * kStage + (kStage > kQ ? kStage : kQ) + kTable;
+  static constexpr int kWarps = MT == 2 || !E4 ? 8 : 12;    // items per SM
+};
+
+// Items: x: KV head and block of kM query rows, y: part, z: row.
+template <int CT, int DP, int MT>
+__global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, MT>::kWarps) paged_rows_kernel(const __grid_constant__ PagedParams P) {
+  using C = PagedRowCfg<CT, DP, MT>;
+  constexpr bool E4 = C::E4;
+  constexpr bool BF = CT == SPEC_BF16;
+  constexpr int kSteps = DP / 16, kNt = DP / 8;  // k-steps of the scores, column tiles of the sums
+  extern __shared__ __align__(16) unsigned char smem[];
+  unsigned char *const qsm = smem + (C::kStages - 1) * C::kStage;
+  float *const qfac = reinterpret_cast<float *>(qsm + C::kM * C::kQPitch);
+  const int lane = threadIdx.x, quad = lane / 4, j4 = lane % 4;
+
+  // --- the item: KV heads first (the heads of a token lie side by side in
+  // memory, so the items that run together read whole entries), then parts
+  const int b = blockIdx.z, split = blockIdx.y;
+  const int blk = blockIdx.x / static_cast<unsigned>(P.H), g = blockIdx.x - blk * P.H;
+  const int blocks = gridDim.x / P.H;
+  const int r0 = blk * C::kM, nrows = P.N * P.G;
+  const long long flag = ((static_cast<long long>(b) * P.H + g) * blocks + blk) * P.splits + split;
+  int n;
+  const int cnt = paged_queries(P, b, n);
+  const bool tree = P.anc != nullptr;
+  if (tree) grid_dependency_wait();
+  const int q_first = r0 / P.G, q_last = min((r0 + C::kM - 1) / P.G, P.N - 1);
+  // Lane i knows query row i of the block (kM <= 32): its output row (-1 past
+  // the last), whether it has a use, where its query is, and its position.
+  int my_row = -1, my_pos = 0;
+  bool my_use = false;
+  long long my_q = 0;
+  {
+    const int r = r0 + lane;
+    if (lane < C::kM && r < nrows) {
+      const int t = r / P.G, h = g * P.G + (r - t * P.G);
+      my_row = (b * P.N + t) * P.Hq + h;
+      my_use = t < cnt;
+      my_q = b * P.qs[0] + t * P.qs[1] + h * P.qs[2];
+      my_pos = n + (tree && my_use && P.rowinfo[b] > 0 ? P.depth[static_cast<size_t>(b) * P.N + t] : tree ? 0 : t);
+    }
+  }
+  const int end = cnt <= q_first ? 0 : tree ? n + cnt : n + min(cnt, q_last + 1);  // tokens below it
+  const int p0 = tree ? n : n + q_first, p1 = tree ? n + cnt : n + q_last;          // positions lie in p0 .. p1
+  const Keys keys(P, p0, end);
+  int g0 = 0, g1 = keys.n;
+  if (P.splits > 1) {
+    const int per = max(P.min_groups, (keys.n + P.splits - 1) / P.splits);
+    g0 = min(keys.n, split * per);
+    g1 = min(keys.n, g0 + per);
+  }
+  if (g0 >= g1 && P.splits > 1) {  // nothing here
+    if (lane == 0) P.oflag[flag] = 0;
+    if (my_row >= 0) P.ml[static_cast<long long>(split) * P.rows + my_row] = make_float2(-INFINITY, -INFINITY);
+    grid_dependency_wait();
+    return;
+  }
+
+  // --- the queries' loads, before the many of the ring
+  constexpr int QL = DP / 8, kRows = 32 / QL, kPass = C::kM / kRows;  // lanes per row, rows per pass
+  const int qc = lane % QL;
+  uint4 u[kPass];
+  {
+    const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
+#pragma unroll
+    for (int i = 0; i < kPass; ++i) {
+      const int rr = i * kRows + lane / QL;
+      const bool use = __shfl_sync(FULL_MASK, my_use, rr);
+      const long long off = __shfl_sync(FULL_MASK, my_q, rr);
+      u[i] = make_uint4(0, 0, 0, 0);
+      if (use && qc * 8 < P.D) {
+        const unsigned short *q = static_cast<const unsigned short *>(P.q) + off + qc * 8;
+        if (vec) {
+          u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
+        } else {
+          u[i].x = q[0] | static_cast<uint32_t>(q[1]) << 16;
+          u[i].y = q[2] | static_cast<uint32_t>(q[3]) << 16;
+          u[i].z = q[4] | static_cast<uint32_t>(q[5]) << 16;
+          u[i].w = q[6] | static_cast<uint32_t>(q[7]) << 16;
+        }
+      }
+    }
+  }
+
+  // --- the ring of groups: lanes over a token's 16-byte pieces, then over tokens
+  const uint32_t ring = smem_u32(smem);
+  constexpr int L = DP * C::kEsz / 16, kPer = kGroup * L / 32, kStep = 32 / L;
+  const int pc = lane % L, row0 = lane / L;
+  const bool col = pc * 16 < P.D * C::kEsz;
+  const int32_t *const trow = P.table + static_cast<size_t>(b) * P.columns;
+  const long long piece = static_cast<long long>(g) * P.D * C::kEsz + (col ? pc * 16 : 0);
+  // lane i: where group base + i of the part starts in its plane (-1: on no page)
+  long long where = -1;
+  auto look_up = [&](int base) {
+    where = -1;
+    if (base + lane < g1) {
+      const int t = keys.token(base + lane), j = t / P.page, pg = __ldg(trow + j);
+      if (pg >= 0 && pg < P.pages) where = pg * P.page_stride + (t - j * P.page) * P.tok_stride;
+    }
+  };
+  if (P.D < DP) {  // the columns past the head vector stay zero: no copy writes them
+    for (int i = lane; i < C::kStages * C::kStage / 16; i += 32) *reinterpret_cast<uint4 *>(smem + i * 16) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+  auto issue = [&](int gi, int st) {
+    if (gi < g1) {
+      if ((gi - g0) % 32 == 0) look_up(gi);
+      const long long at = __shfl_sync(FULL_MASK, where, (gi - g0) % 32);
+      const uint32_t base = ring + st * C::kStage + row0 * C::kPitch + pc * 16;
+      const int left = at < 0 ? 0 : end - keys.token(gi);
+      const long long off = at < 0 ? 0 : at + piece + row0 * P.tok_stride;
+      if (col) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const bool on = row0 + i * kStep < left;
+          const long long o = on ? off + i * kStep * P.tok_stride : 0;
+          cp_async16_zfill(base + i * kStep * C::kPitch, P.k + o, on);
+          cp_async16_zfill(base + C::kPlane + i * kStep * C::kPitch, P.v + o, on);
+        }
+      }
+      if constexpr (E4) {  // scale words: lanes 0-15 the keys', 16-31 the values' of token lane % 16
+        const bool on = lane % kGroup < left;
+        const long long o = on ? at + lane % kGroup * P.tok_stride + static_cast<long long>(P.H) * P.D + (g & ~3) : 0;
+        cp_async4_zfill(ring + st * C::kStage + 2 * C::kPlane + lane * 4, (lane < kGroup ? P.k : P.v) + o, on);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < C::kStages - 1; ++s) issue(g0 + s, s);
+
+  // --- queries into the last ring slot; fp16 for an e4m3 cache: a row far
+  // outside fp16's range is brought into it by a power of two
+#pragma unroll
+  for (int i = 0; i < kPass; ++i) {
+    const int rr = i * kRows + lane / QL;
+    float fac = 1.f;
+    if (E4 && P.qbf16) {
+      const float x[8] = {bf16_lo(u[i].x), bf16_hi(u[i].x), bf16_lo(u[i].y), bf16_hi(u[i].y),
+                          bf16_lo(u[i].z), bf16_hi(u[i].z), bf16_lo(u[i].w), bf16_hi(u[i].w)};
+      uint32_t a = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = QL / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
+      float by = 1.f;
+      const int e = static_cast<int>(a >> 23) - 127;
+      if (a != 0 && a < 0x7f800000u && (e < -4 || e > 14)) {
+        const int up = max(-126, min(126, -e));
+        by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+        fac = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+      }
+      u[i] = make_uint4(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by),
+                        pack16<false>(x[4] * by, x[5] * by), pack16<false>(x[6] * by, x[7] * by));
+    }
+    if (qc == 0) qfac[rr] = fac;
+    *reinterpret_cast<uint4 *>(qsm + rr * C::kQPitch + qc * 16) = u[i];
+  }
+  __syncwarp();
+
+  // Fragments.  The contraction over d may run in any order as long as Q and
+  // K agree: for codes a thread takes DP/4 consecutive d (a few 16-byte
+  // reads), for 16-bit entries the order ldmatrix gives.
+  uint32_t qf[MT][kSteps][4];
+  float rf[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int rr = mt * 16 + hf * 8 + quad;
+      rf[mt][hf] = qfac[rr];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int d0 = E4 ? j4 * (DP / 4) + s * 4 : s * 16 + j4 * 2;
+        const int d1 = E4 ? d0 + 2 : d0 + 8;
+        qf[mt][s][hf] = *reinterpret_cast<const uint32_t *>(qsm + rr * C::kQPitch + d0 * 2);
+        qf[mt][s][2 + hf] = *reinterpret_cast<const uint32_t *>(qsm + rr * C::kQPitch + d1 * 2);
+      }
+    }
+  }
+  if (P.D < DP) {  // the slot's padding columns were queries
+    __syncwarp();
+    for (int i = lane; i < C::kStage / 16; i += 32) *reinterpret_cast<uint4 *>(qsm + i * 16) = make_uint4(0, 0, 0, 0);
+  }
+  __syncwarp();
+  // each thread's rows, for the masks
+  int qtok[MT][2], qpos[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      qtok[mt][hf] = min((r0 + mt * 16 + hf * 8 + quad) / P.G, P.N - 1);
+      qpos[mt][hf] = __shfl_sync(FULL_MASK, my_pos, mt * 16 + hf * 8 + quad);
+    }
+
+  float o[MT][kNt][4];
+  // l counts in units of 2^mx, o in units of 2^mv (one and the same for 16-bit entries)
+  float mx[MT][2], mv[MT][2], l[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    mx[mt][0] = mx[mt][1] = mv[mt][0] = mv[mt][1] = -INFINITY;
+    l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+    for (int t = 0; t < kNt; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[mt][t][c] = 0.f;
+  }
+
+  bool odd = false;
+  int st = 0;
+  for (int gi = g0; gi < g1; ++gi) {
+    issue(gi + C::kStages - 1, st == 0 ? C::kStages - 1 : st - 1);
+    cp_async_wait<C::kStages - 1>();
+    __syncwarp();
+    const uint32_t kst = ring + st * C::kStage, vst = kst + C::kPlane, sst = kst + 2 * C::kPlane;
+    const int tb = keys.token(gi);
+    // some query of the block does not see some token of the group
+    const bool masked = tb + kGroup - 1 > (tree ? n - 1 : p0) || (tb + kGroup > P.sinks && tb < window_from(P, p1));
+    // --- scores: token n * 8 + 2 j4 + {0, 1} of rows quad and quad + 8
+    float x[MT][2][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[mt][t][c] = 0.f;
+    if constexpr (E4) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t at = kst + (t * 8 + quad) * C::kPitch + j4 * (DP / 4);
+#pragma unroll
+        for (int s0 = 0; s0 < kSteps; s0 += 4) {
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(at + s0 * 4)
+                       : "memory");
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t b0 = e4m3x2_to_f16x2(w[s]), b1 = e4m3x2_to_f16x2_hi(w[s]);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mma16816<false>(x[mt][t], qf[mt][s0 + s], b0, b1);
+          }
+        }
+      }
+    } else {
+      // matrices: (tokens 0-7, d 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
+      const uint32_t at = kst + ((lane / 16) * 8 + lane % 8) * C::kPitch + ((lane / 8) % 2) * 16;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint32_t kf[4];
+        ldmatrix_x4(kf, at + s * 32);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816<BF>(x[mt][0], qf[mt][s], kf[0], kf[1]);
+          mma16816<BF>(x[mt][1], qf[mt][s], kf[2], kf[3]);
+        }
+      }
+    }
+    // --- to base-2 exponents
+    float ve[2][2];  // the values' scale exponents
+    if constexpr (E4) {
+      uint32_t w;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(sst + lane * 4) : "memory");
+      const uint32_t byte = w >> (8 * (g & 3)) & 255u;
+      // value vectors of NaN: the keys alone decide the softmax, and the NaN comes in with the values
+      const unsigned nans = __ballot_sync(FULL_MASK, byte == 255u) >> kGroup;
+      if (nans) {
+        for (int tk = 0; tk < kGroup; ++tk) {
+          if (!(nans >> tk & 1u)) continue;
+          if (masked)  // not every query sees it: put into the answers of those that do
+            odd = true;
+          else if (lane * 4 < P.D)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(vst + tk * C::kPitch + lane * 4), "r"(0x7f7f7f7fu) : "memory");
+        }
+        __syncwarp();
+      }
+      const uint32_t tab = smem_u32(smem) + C::kSmem - C::kTable;
+      if (lane < kGroup)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(tab + lane * 8), "f"(P.scale * e4m3_scale(byte)) : "memory");
+      else
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(tab + (lane - kGroup) * 8 + 4), "f"(byte == 255u ? 0.f : scale_exponent(byte)) : "memory");
+      __syncwarp();
+      float ks[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(ks[t][0]), "=f"(ve[t][0]), "=f"(ks[t][1]), "=f"(ve[t][1])
+                     : "r"(tab + (t * 8 + 2 * j4) * 8)
+                     : "memory");
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[mt][t][c] *= rf[mt][c >> 1] * ks[t][c & 1];
+    } else {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[mt][t][c] *= P.scale;
+    }
+    if (masked) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int tk = tb + t * 8 + 2 * j4 + (c & 1);
+            if (tk >= end || !paged_sees(P, b, qtok[mt][c >> 1], n, qpos[mt][c >> 1], tk)) x[mt][t][c] = -INFINITY;
+          }
+    }
+    // --- softmax.  A row's references follow its maxima only when these have
+    // grown by more than 2^kPaLazy (weights up to that are as exact), whatever
+    // other rows' do: nothing of a row depends on its neighbours in the block.
+    float tm[MT][2], tv[MT][2];
+    bool grown = false;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        tm[mt][hf] = fmaxf(fmaxf(x[mt][0][2 * hf], x[mt][0][2 * hf + 1]), fmaxf(x[mt][1][2 * hf], x[mt][1][2 * hf + 1]));
+        grown = grown || tm[mt][hf] > mx[mt][hf] + kPaLazy || mx[mt][hf] == -INFINITY;
+        if constexpr (E4) {
+          tv[mt][hf] = fmaxf(fmaxf(x[mt][0][2 * hf] + ve[0][0], x[mt][0][2 * hf + 1] + ve[0][1]),
+                             fmaxf(x[mt][1][2 * hf] + ve[1][0], x[mt][1][2 * hf + 1] + ve[1][1]));
+          grown = grown || tv[mt][hf] > mv[mt][hf] + kPaLazy;
+        }
+      }
+    if (__any_sync(FULL_MASK, grown)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float al[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float t = tm[mt][hf];
+          t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 1));
+          t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 2));
+          al[hf] = 1.f;
+          if (t > mx[mt][hf] + kPaLazy || (mx[mt][hf] == -INFINITY && t > -INFINITY)) {
+            al[hf] = ex2(mx[mt][hf] - t);
+            l[mt][hf] *= al[hf];
+            mx[mt][hf] = t;
+          }
+          if constexpr (E4) {
+            t = tv[mt][hf];
+            t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 1));
+            t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 2));
+            al[hf] = 1.f;
+            if (t > mv[mt][hf] + kPaLazy || (mv[mt][hf] == -INFINITY && t > -INFINITY)) {
+              al[hf] = ex2(mv[mt][hf] - t);
+              mv[mt][hf] = t;
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < kNt; ++t) {
+          o[mt][t][0] *= al[0];
+          o[mt][t][1] *= al[0];
+          o[mt][t][2] *= al[1];
+          o[mt][t][3] *= al[1];
+        }
+      }
+    }
+    uint32_t pf[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float ref = mx[mt][hf] == -INFINITY ? 0.f : mx[mt][hf], rev = mv[mt][hf] == -INFINITY ? 0.f : mv[mt][hf];
+        float add = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float &y = x[mt][t][2 * hf + c];
+            const float w = ex2(y - ref);
+            add += w;
+            y = E4 ? ex2(y + (ve[t][c] - rev)) : w;
+          }
+        l[mt][hf] += add;
+      }
+      pf[mt][0] = pack16<BF>(x[mt][0][0], x[mt][0][1]);
+      pf[mt][1] = pack16<BF>(x[mt][0][2], x[mt][0][3]);
+      pf[mt][2] = pack16<BF>(x[mt][1][0], x[mt][1][1]);
+      pf[mt][3] = pack16<BF>(x[mt][1][2], x[mt][1][3]);
+    }
+    // --- in masked groups, values that are not finite are taken out
+    if (masked) {
+      bool bad = false;
+      for (int tk = 0; tk < kGroup; ++tk)
+#pragma unroll
+        for (int i = 0; i < (DP * C::kEsz + 127) / 128; ++i) {  // words of a head vector
+          if ((i * 32 + lane) * 4 >= P.D * C::kEsz) continue;
+          const uint32_t at = vst + tk * C::kPitch + (i * 32 + lane) * 4;
+          uint32_t w;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+          uint32_t r = w;
+          if constexpr (E4) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if ((w >> (8 * c) & 127u) == 127u) r &= ~(255u << (8 * c));
+          } else {
+            constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
+            if ((w & top) == top) r &= 0xffff0000u;
+            if ((w >> 16 & top) == top) r &= 0x0000ffffu;
+          }
+          if (r != w) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(r) : "memory");
+            bad = true;
+          }
+        }
+      odd = __any_sync(FULL_MASK, bad) || odd;
+      __syncwarp();
+    }
+    // --- weights times values
+    if constexpr (E4) {
+      // tokens 2 j4, 2 j4 + 1, 8 + 2 j4, 9 + 2 j4 of columns quad * kNt + n
+#pragma unroll
+      for (int n0 = 0; n0 < kNt; n0 += 8) {
+        uint32_t w[4][2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                       : "=r"(w[t][0]), "=r"(w[t][1])
+                       : "r"(vst + ((t / 2) * 8 + 2 * j4 + t % 2) * C::kPitch + quad * kNt + n0)
+                       : "memory");
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          // bytes i, i + 1 of two tokens: (t0 i, t1 i, t0 i+1, t1 i+1)
+          const uint32_t sel = i % 4 == 0 ? 0x5140u : 0x7362u;
+          const uint32_t lo = __byte_perm(w[0][i / 4], w[1][i / 4], sel);
+          const uint32_t hi = __byte_perm(w[2][i / 4], w[3][i / 4], sel);
+          const uint32_t b0 = e4m3x2_to_f16x2(lo), b1 = e4m3x2_to_f16x2(hi);
+          const uint32_t c0 = e4m3x2_to_f16x2_hi(lo), c1 = e4m3x2_to_f16x2_hi(hi);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816<false>(o[mt][n0 + i], pf[mt], b0, b1);
+            mma16816<false>(o[mt][n0 + i + 1], pf[mt], c0, c1);
+          }
+        }
+      }
+    } else {
+      // matrices: (tokens 0-7, d 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+      const uint32_t at = vst + (lane % 16) * C::kPitch + (lane / 16) * 16;
+#pragma unroll
+      for (int t = 0; t < kNt; t += 2) {
+        uint32_t vf[4];
+        ldmatrix_x4_trans(vf, at + t * 16);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816<BF>(o[mt][t], pf[mt], vf[0], vf[1]);
+          mma16816<BF>(o[mt][t + 1], pf[mt], vf[2], vf[3]);
+        }
+      }
+    }
+    __syncwarp();
+    st = st == C::kStages - 1 ? 0 : st + 1;
+  }
+  cp_async_wait_all();
+  allow_dependents();  // the join's blocks may take the places that come free
+  grid_dependency_wait();  // the row's check
+  const bool usable = P.rowinfo[b] >= 0;
+  odd = __any_sync(FULL_MASK, odd);
+  if (P.splits > 1 && lane == 0) P.oflag[flag] = odd;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int rr = mt * 16 + hf * 8 + quad;
+      const int orow = __shfl_sync(FULL_MASK, my_row, rr);
+      const bool use = __shfl_sync(FULL_MASK, my_use, rr);
+      float t = l[mt][hf];
+      t += __shfl_xor_sync(FULL_MASK, t, 1);
+      t += __shfl_xor_sync(FULL_MASK, t, 2);
+      if (orow < 0) continue;
+      const bool some = usable && use && t != 0.f;
+      const float m = E4 ? mv[mt][hf] : mx[mt][hf];
+      const float z = some ? mx[mt][hf] + log2f(t) : -INFINITY;
+      if (P.splits > 1) {
+        const long long at = static_cast<long long>(split) * P.rows + orow;
+        if (j4 == 0) P.ml[at] = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
+        if (!some) continue;
+        float *const to = P.part + at * P.D;
+        if constexpr (E4) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < kNt; i += 8) {
+              if ((2 * j4 + c) * kNt + i >= P.D) continue;
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(o[mt][i + e][2 * hf + c]);
+              st_global_v8(to + (2 * j4 + c) * kNt + i, y);
+            }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kNt; ++i)
+            if (i * 8 < P.D) *reinterpret_cast<float2 *>(to + i * 8 + 2 * j4) = make_float2(o[mt][i][2 * hf], o[mt][i][2 * hf + 1]);
+        }
+        continue;
+      }
+      const float w = some ? ex2(m - z) : 0.f;
+      if (j4 == 0 && P.lse) P.lse[orow] = kLn2 * z;
+      unsigned short *const to = static_cast<unsigned short *>(P.out) + static_cast<long long>(orow) * P.D;
+      // column d of the answer from its sum
+      auto value = [&](float y, int d) {
+        y = some ? y * w : 0.f;
+        if (some && odd) y += paged_odd_sum<CT>(P, b, qtok[mt][hf], cnt, n, qpos[mt][hf], g, d);
+        return y;
+      };
+      if constexpr (E4) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < kNt; i += 8) {
+            const int d = (2 * j4 + c) * kNt + i;
+            if (d >= P.D) continue;
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float lo = value(o[mt][i + 2 * e][2 * hf + c], d + 2 * e), hi = value(o[mt][i + 2 * e + 1][2 * hf + c], d + 2 * e + 1);
+              y[e] = P.qbf16 ? pack16<true>(lo, hi) : pack16<false>(lo, hi);
+            }
+            *reinterpret_cast<uint4 *>(to + d) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kNt; ++i)
+          if (i * 8 < P.D) {
+            const int d = i * 8 + 2 * j4;
+            const float lo = value(o[mt][i][2 * hf], d), hi = value(o[mt][i][2 * hf + 1], d + 1);
+            *reinterpret_cast<uint32_t *>(to + d) = BF ? pack16<true>(lo, hi) : pack16<false>(lo, hi);
+          }
+      }
+    }
+}
+
+// ------------------------------------------------------------------- join
+// One warp per output row: the weights of the parts, then their sum, eight parts'
+// loads at a time.
+template <int CT, bool BF>
+__global__ void __launch_bounds__(kPaJoinThreads) paged_join_kernel(const __grid_constant__ PagedParams P) {
+  const int lane = threadIdx.x % 32;
+  const long long r = static_cast<long long>(blockIdx.x) * (kPaJoinThreads / 32) + threadIdx.x / 32;
+  grid_dependency_wait();
+  if (r >= P.rows) return;
+  const int b = static_cast<int>(r / (static_cast<long long>(P.N) * P.Hq));
+  const int qt = static_cast<int>(r / P.Hq) - b * P.N, h = static_cast<int>(r % P.Hq);
+  const int c = P.rowinfo[b];
+  const bool on = qt < c;
+  float Z = -INFINITY;
+  bool gone = false;  // a part's kernel gave up waiting: the row is flagged and its answer left empty
+  float2 ml = make_float2(-INFINITY, -INFINITY);  // this lane's part (there are 32 at most)
+  if (on && lane < P.splits) ml = P.ml[static_cast<long long>(lane) * P.rows + r];
+  gone = __any_sync(FULL_MASK, __float_as_uint(ml.y) == kTimeoutBits);
+  if (gone && lane == 0 && P.row_status) P.row_status[b] = SPEC_ROW_TIMEOUT;
+  Z = ml.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) Z = fmax_nan(Z, __shfl_xor_sync(FULL_MASK, Z, o));
+  const float zref = Z == -INFINITY ? 0.f : Z;
+  const float S = gone ? 0.f : warp_sum(ex2(ml.y - zref));
+  const float z = S == 0.f ? -INFINITY : zref + log2f(S);
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};  // columns 4 lane .. 4 lane + 3
+  if (S != 0.f) {
+    const float wl = ex2(ml.x - z);
+    unsigned todo = __ballot_sync(FULL_MASK, ml.y != -INFINITY);
+    while (todo) {
+      float4 x[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = todo ? __ffs(todo) - 1 : -1;
+        todo &= todo - 1;
+        w[j] = __shfl_sync(FULL_MASK, wl, k & 31);
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < 0)
+          w[j] = 0.f;
+        else if (lane * 4 < P.D)
+          x[j] = *reinterpret_cast<const float4 *>(P.part + (static_cast<long long>(k) * P.rows + r) * P.D + lane * 4);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        acc[0] = fmaf(w[j], x[j].x, acc[0]);
+        acc[1] = fmaf(w[j], x[j].y, acc[1]);
+        acc[2] = fmaf(w[j], x[j].z, acc[2]);
+        acc[3] = fmaf(w[j], x[j].w, acc[3]);
+      }
+    }
+    const int g = h / P.G, blocks = (P.N * P.G + P.oblk - 1) / P.oblk;
+    const int32_t *flag = P.oflag + ((static_cast<long long>(b) * P.H + g) * blocks + (qt * P.G + h % P.G) / P.oblk) * P.splits;
+    if (__any_sync(FULL_MASK, lane < P.splits && flag[lane])) {
+      const int n = P.kv_len[b], p = n + (P.anc ? P.depth[static_cast<size_t>(b) * P.N + qt] : qt);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lane * 4 + i < P.D) acc[i] += paged_odd_sum<CT>(P, b, qt, c, n, p, g, lane * 4 + i);
+    }
+  }
+  if (lane * 4 < P.D)
+    *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(P.out) + r * P.D + lane * 4) =
+        make_uint2(pack16<BF>(acc[0], acc[1]), pack16<BF>(acc[2], acc[3]));
+  if (lane == 0 && P.lse) P.lse[r] = kLn2 * z;
+}
+
+// -------------------------------------------------------------------- host
+template <int CT, int DP, int MT>
+cudaError_t launch_rows(const PagedParams &p, cudaStream_t s) {
+  using C = PagedRowCfg<CT, DP, MT>;
+  const int blocks = (p.N * p.G + C::kM - 1) / C::kM;
+  const dim3 grid(p.H * blocks, p.splits, p.B);
+  const cudaError_t e = allow_smem<paged_rows_kernel<CT, DP, MT>>(C::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_after(paged_rows_kernel<CT, DP, MT>, grid, 32, C::kSmem, s, true, p);
+}
+
+template <int CT>
+cudaError_t launch_rows_d(const PagedParams &p, cudaStream_t s) {
+  const bool two = p.oblk == 32;
+  if (p.D <= 64) return two ? launch_rows<CT, 64, 2>(p, s) : launch_rows<CT, 64, 1>(p, s);
+  return two ? launch_rows<CT, 128, 2>(p, s) : launch_rows<CT, 128, 1>(p, s);
+}
+
+struct PagedPlan {
+  int splits, oblk, W;
+  size_t rows, info_at, anc_at, depth_at, flag_at, ml_at, part_at, bytes;
+};
+
+size_t pa_round(size_t x) { return (x + 255) / 256 * 256; }
+bool pa_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Sizes and types (no pointers).
+spec_status check_paged(const spec_paged_attention_args *a) {
+  const long long most = 0x7fffffffLL;
+  if (a->q_dtype != SPEC_BF16 && a->q_dtype != SPEC_F16) return SPEC_ERR_DTYPE;
+  if (a->cache_dtype != SPEC_E4M3 && a->cache_dtype != a->q_dtype) return SPEC_ERR_DTYPE;
+  const size_t entry = spec_kv_entry_bytes(a->heads, a->head_dim, a->cache_dtype);
+  if (entry == 0 || a->B < 0 || a->B > 65535 || a->N < 0 || a->q_heads < 1 || a->q_heads % a->heads) return SPEC_ERR_SHAPE;
+  if (a->columns < 1 || a->page_size < 16 || a->page_size > SPEC_MAX_PAGE || a->page_size % 16 || a->num_pages < 0) return SPEC_ERR_SHAPE;
+  // positions leave room for a window's end and a group past the last token
+  if (static_cast<long long>(a->columns) * a->page_size > most - 4096 || static_cast<long long>(a->num_pages) * a->page_size > most)
+    return SPEC_ERR_SHAPE;
+  if (a->parent && a->N > SPEC_MAX_TREE_NODES) return SPEC_ERR_SHAPE;
+  if (a->N > 0 && static_cast<long long>(a->B) * a->N >= most / 256 / a->q_heads) return SPEC_ERR_SHAPE;
+  if (static_cast<long long>(a->N) * (a->q_heads / a->heads) > most / 2) return SPEC_ERR_SHAPE;
+  if (a->page_stride < 0 || a->tok_stride < static_cast<int64_t>(entry) || a->tok_stride >= 1LL << 27) return SPEC_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i)
+    if (a->q_stride[i] < 0) return SPEC_ERR_SHAPE;
+  if (!std::isfinite(a->scale) || a->window < 0 || a->sinks < 0) return SPEC_ERR_ARG;
+  return SPEC_OK;
+}
+
+PagedPlan plan_paged(const spec_paged_attention_args *a) {
+  PagedPlan p = {};
+  const long long G = a->q_heads / a->heads, rows1 = a->N * G;
+  p.rows = static_cast<size_t>(a->B) * a->N * a->q_heads;
+  p.oblk = rows1 > 16 ? 32 : 16;
+  const long long blocks = (rows1 + p.oblk - 1) / p.oblk, items = a->B * a->heads * blocks;
+  // tokens that an item may see
+  long long tokens = static_cast<long long>(a->columns) * a->page_size;
+  if (a->window > 0) tokens = std::min(tokens, static_cast<long long>(a->window) + a->sinks + p.oblk / G + 1 + 2 * kGroup);
+  const long long want = (8LL * kPaSms * 2 + items - 1) / items;
+  p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 32})));
+  p.W = a->parent ? (a->N + 31) / 32 : 0;
+  const size_t q = static_cast<size_t>(a->B) * a->N;
+  size_t at = 0;
+  p.info_at = at;
+  at += pa_round(static_cast<size_t>(a->B) * 4);
+  p.anc_at = at;
+  at += pa_round(q * p.W * 4);
+  p.depth_at = at;
+  at += pa_round(a->parent ? q * 4 : 0);
+  p.flag_at = at;
+  if (p.splits > 1) at += pa_round(static_cast<size_t>(items) * p.splits * 4);
+  p.ml_at = at;
+  if (p.splits > 1) at += pa_round(p.splits * p.rows * sizeof(float2));
+  p.part_at = at;
+  if (p.splits > 1) at += pa_round(p.splits * p.rows * a->head_dim * 4);
+  p.bytes = at + 256;
+  return p;
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+size_t spec_paged_attention_workspace_size(const spec_paged_attention_args *a) {
+  if (!a || check_paged(a) != SPEC_OK) return 0;
+  if (a->B == 0 || a->N == 0) return 256;
+  return plan_paged(a).bytes;
+}
+
+spec_status spec_paged_attention(const spec_paged_attention_args *a, void *out, float *lse, int32_t *row_status,
+                                 void *ws, size_t ws_bytes, void *stream) {
+  if (!a) return SPEC_ERR_NULL;
+  const spec_status st = check_paged(a);
+  if (st != SPEC_OK) return st;
+  if (!pa_aligned(a->k, 16) || !pa_aligned(a->v, 16) || a->page_stride % 16 || a->tok_stride % 16 || !pa_aligned(a->q, 2) ||
+      !pa_aligned(out, 16) || !pa_aligned(lse, 16) || !pa_aligned(row_status, 4) || !pa_aligned(a->block_table, 4) ||
+      !pa_aligned(a->kv_len, 4) || !pa_aligned(a->count, 4) || !pa_aligned(a->parent, 4))
+    return SPEC_ERR_ALIGN;
+  if (a->B == 0 || a->N == 0) return SPEC_OK;
+  if (!a->q || !out || !a->kv_len || !a->block_table || ((!a->k || !a->v) && a->num_pages > 0)) return SPEC_ERR_NULL;
+  const PagedPlan plan = plan_paged(a);
+  if (!ws || !pa_aligned(ws, 256) || ws_bytes < plan.bytes) return SPEC_ERR_WORKSPACE;
+  char *w = static_cast<char *>(ws);
+  PagedParams p = {};
+  p.k = static_cast<const unsigned char *>(a->k);
+  p.v = static_cast<const unsigned char *>(a->v);
+  if (a->num_pages == 0) p.k = p.v = reinterpret_cast<const unsigned char *>(w);  // nothing of it is read
+  p.page_stride = a->page_stride;
+  p.tok_stride = a->tok_stride;
+  p.page = a->page_size;
+  p.pages = a->num_pages;
+  p.columns = a->columns;
+  p.table = a->block_table;
+  p.q = a->q;
+  for (int i = 0; i < 3; ++i) p.qs[i] = a->q_stride[i];
+  p.scale = a->scale * 1.442695040888963407f;
+  p.B = a->B;
+  p.N = a->N;
+  p.Hq = a->q_heads;
+  p.H = a->heads;
+  p.G = a->q_heads / a->heads;
+  p.D = a->head_dim;
+  p.kv_len = a->kv_len;
+  p.count = a->count;
+  p.window = a->window > 0 ? a->window : 0x7fffffff;
+  p.sinks = a->window > 0 ? a->sinks : 0;
+  p.W = plan.W;
+  p.rows = static_cast<int>(plan.rows);
+  p.splits = plan.splits;
+  p.min_groups = 4;
+  p.oblk = plan.oblk;
+  p.ml = reinterpret_cast<float2 *>(w + plan.ml_at);
+  p.part = reinterpret_cast<float *>(w + plan.part_at);
+  p.oflag = reinterpret_cast<int32_t *>(w + plan.flag_at);
+  p.out = out;
+  p.lse = lse;
+  p.row_status = row_status;
+  p.qbf16 = a->q_dtype == SPEC_BF16;
+  p.wait_limit_ns = spec_get_wait_timeout_ns();
+  p.force_timeout = force_wait_timeout();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t *info = reinterpret_cast<int32_t *>(w + plan.info_at);
+  uint32_t *anc = reinterpret_cast<uint32_t *>(w + plan.anc_at);
+  int32_t *depth = reinterpret_cast<int32_t *>(w + plan.depth_at);
+  paged_check_kernel<<<p.B, kCheckThreads, 0, s>>>(p, a->parent, info, anc, depth);
+  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  p.rowinfo = info;
+  if (a->parent) p.anc = anc, p.depth = depth;
+  const int ct = a->cache_dtype;
+  cudaError_t e = ct == SPEC_E4M3   ? launch_rows_d<SPEC_E4M3>(p, s)
+                  : ct == SPEC_BF16 ? launch_rows_d<SPEC_BF16>(p, s)
+                                    : launch_rows_d<SPEC_F16>(p, s);
+  if (e != cudaSuccess) return SPEC_ERR_CUDA;
+  if (p.splits == 1) return SPEC_OK;
+  const dim3 grid((p.rows + kPaJoinThreads / 32 - 1) / (kPaJoinThreads / 32));
+  auto join = [&](auto kernel) { return launch_after(kernel, grid, kPaJoinThreads, 0, s, true, p); };
+  e = ct == SPEC_BF16  ? join(paged_join_kernel<SPEC_BF16, true>)
+      : ct == SPEC_F16 ? join(paged_join_kernel<SPEC_F16, false>)
+      : p.qbf16        ? join(paged_join_kernel<SPEC_E4M3, true>)
+                       : join(paged_join_kernel<SPEC_E4M3, false>);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // extern "C"

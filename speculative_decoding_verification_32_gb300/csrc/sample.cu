@@ -1,0 +1,742 @@
+// sample.cu -- one token per row from a truncated law at a given uniform
+// (spec_sample).
+//
+// Every truncation is a floor on the logit: with the row's logits l, its largest
+// M, w_v = exp((l_v - M) / T) and mass(t) = sum of w_v over l_v >= t,
+//   top-k:  the largest t that k logits reach,
+//   top-p:  the largest t with mass(t) >= top_p mass(top-k's floor),
+//   min-p:  M + T ln(min_p);
+// the law is w over the logits that reach all three, and the token the smallest
+// v whose running sum in vocabulary order passes u times the whole.
+//
+// One cluster of CTAs per row.  Each keeps its slice of the row in shared memory,
+// so memory is read once and everything after the maximum runs on chip.  Sums
+// are integers (w 2^44, at most 2^18 of them): they do not depend on the order in
+// which they are made.  The floors are found among few candidates: a bound
+// below the floor that is cheap (the k-th largest of the threads' own maxima;
+// for top-p a histogram of the weights by their leading bits) leaves about as
+// many logits as the law keeps.  These meet in the first CTA, in vocabulary
+// order, where the floors are searched bit by bit.  Where more are left than it
+// can list, all CTAs search together.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "internal.h"
+#include "specverify.h"
+
+namespace sv {
+namespace {
+
+constexpr int kSmThreads = 256;
+constexpr int kSmWarps = kSmThreads / 32;
+constexpr int kSmMaxCluster = 8;
+constexpr int kSmBatch = 8;       // 16-byte loads of a thread in flight
+constexpr int kSmCands = 2048;    // candidates the first CTA lists, an equal share of them from each CTA
+constexpr int kSmPer = kSmCands / kSmThreads;
+constexpr int kSmBins = 512;      // weights 1 down to 2^-64, eight bins an octave
+constexpr float kSmFix = 0x1p44f; // a weight of 1 as an integer
+constexpr float kSmMostScale = 0x1p127f;  // log2(e) / T at most: past fp32's range only the largest logit counts
+constexpr uint32_t kSmMinusInf = 0x007fffffu;  // the key of -inf, the least a logit can have
+
+struct SampleParams {
+  const void *logits;
+  const float *u, *temperature, *top_p, *min_p;
+  const int32_t *top_k;
+  int32_t *token, *row_status;
+  float *prob;
+  long long row_stride;
+  int B, V;
+  int slice;  // elements per CTA, a multiple of a vector's
+};
+
+typedef long long i64;
+typedef unsigned long long u64;
+
+__device__ __forceinline__ uint32_t smp_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);  // -0 counts as +0
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float smp_from_key(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ void st_cluster_u64(const void *p, uint32_t rank, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dsmem_addr(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(const void *p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void add_cluster_u64(const void *p, uint32_t rank, u64 v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(dsmem_addr(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void max_cluster_u32(const void *p, uint32_t rank, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(dsmem_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+struct SampleShared {
+  u64 part[2][kSmMaxCluster];       // what the CTAs tell one another, two rounds in turn
+  u64 part2[2][kSmMaxCluster];
+  u64 warp[2][kSmWarps];            // this CTA's warps, two rounds in turn
+  u64 warp2[2][kSmWarps];
+  uint32_t tmax[kSmThreads];        // threads' largest keys, of the whole cluster
+  u64 hist[kSmBins];                // first CTA: the cluster's
+  uint32_t mine[kSmBins];           // this CTA's
+  uint32_t cnt[kSmMaxCluster];      // candidates of each CTA
+  float floor;                      // what top-p's histogram says
+  u64 cand[kSmCands];               // first CTA: key << 32 | token
+};
+
+// Warp sum of 64-bit integers.
+__device__ __forceinline__ i64 warp_sum64(i64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+  return v;
+}
+
+// The weights of a row: w(l) = 2^((l - M) log2(e) / T).  The exponent is kept to
+// more than fp32's 24 bits (its rounding, times 20 or so, would show in the sums):
+// what the difference, the factor and the product lose goes in to first order.
+struct Weight {
+  float M, sc, sc_lo;
+  __device__ __forceinline__ float operator()(float l) const {
+    const float x = fmaxf(l, -3e38f);
+    const float t = x - M;
+    const float lost = x - (t + M);  // what the difference lost, where that counts
+    const float y = fmaxf(t * sc, -200.f);
+    float r = fmaf(t, sc, -y);
+    r = fmaf(t, sc_lo, fmaf(lost, sc, r));
+    const float w = ex2(y);
+    const float c = fmaf(w, r * 0.693147180559945309f, w);
+    return w > 0.f && l > -INFINITY ? c : 0.f;
+  }
+};
+
+template <bool BF16>
+__device__ __forceinline__ float element(const uint4 &q, int e) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if constexpr (BF16) return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+  return __uint_as_float(w[e]);
+}
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constant__ SampleParams P) {
+  constexpr int E = BF16 ? 8 : 4;
+  __shared__ SampleShared S;
+  extern __shared__ __align__(16) unsigned char smp_raw[];
+  uint4 *const data = reinterpret_cast<uint4 *>(smp_raw);
+  const uint32_t ranks = cluster_nctarank(), rank = cluster_ctarank();
+  const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const char *row = static_cast<const char *>(P.logits) + static_cast<size_t>(b) * P.row_stride * (BF16 ? 2 : 4);
+  const int first = rank * P.slice, last = min(P.V, first + P.slice);  // may be empty
+  const int vecs = last > first ? (last - first + E - 1) / E : 0;
+  // a warp's vectors lie side by side, so that warps and lanes are in vocabulary order
+  const int per = (vecs + 32 * kSmWarps - 1) / (32 * kSmWarps) * 32;
+  const int v0 = min(vecs, warp * per), v1 = min(vecs, v0 + per);
+
+  cluster_arrive();  // the others must be running before anything is stored into their memory
+  // --- the slice, and its largest logit
+  uint32_t flags = 0;
+  float top = -INFINITY;
+  for (int i0 = v0 + lane; i0 < v1; i0 += 32 * kSmBatch) {
+    uint4 q[kSmBatch];
+#pragma unroll
+    for (int i = 0; i < kSmBatch; ++i) {
+      const int v = i0 + i * 32;
+      if (v < v1) {
+        if constexpr (VEC) {
+          q[i] = ld_stream_u4(row + (static_cast<size_t>(first) + static_cast<size_t>(v) * E) * (BF16 ? 2 : 4), l2_policy_evict_first());
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int at = first + v * E + e * (E / 4);
+            if constexpr (BF16) {
+              const unsigned short *p = reinterpret_cast<const unsigned short *>(row) + at;
+              w[e] = (at < last ? __ldg(p) : 0xff80u) | (at + 1 < last ? static_cast<uint32_t>(__ldg(p + 1)) : 0xff80u) << 16;
+            } else {
+              w[e] = at < last ? __ldg(reinterpret_cast<const uint32_t *>(row) + at) : 0xff800000u;
+            }
+          }
+          q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSmBatch; ++i) {
+      const int v = i0 + i * 32;
+      if (v < v1) {
+        data[v] = q[i];
+        float c = element<BF16>(q[i], 0);
+#pragma unroll
+        for (int e = 1; e < E; ++e) c = fmax_nan(c, element<BF16>(q[i], e));
+        if (!(c < INFINITY)) flags |= F_NONFINITE;  // NaN or +inf
+        top = fmaxf(top, c);
+      }
+    }
+  }
+  const uint32_t my_top = smp_key(top);
+  {
+    const uint32_t k = __reduce_max_sync(FULL_MASK, my_top);
+    flags = __reduce_or_sync(FULL_MASK, flags);
+    if (lane == 0) S.warp[0][warp] = static_cast<u64>(k) << 32 | flags;
+  }
+  for (int i = tid; i < kSmBins; i += kSmThreads) S.hist[i] = S.mine[i] = 0;
+  S.tmax[tid] = 0;
+  __syncthreads();
+  cluster_wait();
+  {
+    u64 k = 0;
+    uint32_t f = 0;
+#pragma unroll
+    for (int w = 0; w < kSmWarps; ++w) {
+      k = max(k, S.warp[0][w] >> 32);
+      f |= static_cast<uint32_t>(S.warp[0][w]);
+    }
+    if (tid < static_cast<int>(ranks)) st_cluster_u64(&S.part[0][rank], tid, k << 32 | f);
+  }
+  cluster_sync();
+  uint32_t top_key = 0;
+  flags = 0;
+  for (uint32_t k = 0; k < ranks; ++k) {
+    top_key = max(top_key, static_cast<uint32_t>(S.part[0][k] >> 32));
+    flags |= static_cast<uint32_t>(S.part[0][k]);
+  }
+  const float M = smp_from_key(top_key);
+  // --- the row's numbers
+  const float T = P.temperature ? __ldg(P.temperature + b) : 1.f, u = __ldg(P.u + b);
+  if (!(T > 0.f) || isinf(T)) flags |= F_BAD_TEMPERATURE;
+  if (!(u >= 0.f && u < 1.f)) flags |= F_BAD_UNIFORM;
+  if (M == -INFINITY && !(flags & F_NONFINITE)) flags |= F_EMPTY;
+  if (flags) {  // the whole cluster leaves
+    if (rank == 0 && tid == 0) {
+      P.token[b] = -1;
+      if (P.prob) P.prob[b] = NAN;
+      P.row_status[b] = lowest_code(flags);
+    }
+    return;
+  }
+  Weight weight;
+  weight.M = M;
+  {
+    const double s = 1.4426950408889634074 / static_cast<double>(T);
+    weight.sc = fminf(static_cast<float>(s), kSmMostScale);
+    weight.sc_lo = weight.sc == kSmMostScale ? 0.f : static_cast<float>(s - static_cast<double>(weight.sc));
+  }
+  const int k_raw = P.top_k ? __ldg(P.top_k + b) : 0;
+  const int top_k = k_raw >= 1 && k_raw < P.V ? k_raw : 0;  // 0: off
+  const float p_raw = P.top_p ? __ldg(P.top_p + b) : 1.f;
+  const bool use_p = p_raw > 0.f && p_raw < 1.f;
+  const double top_p = p_raw;
+  const float m_raw = P.min_p ? __ldg(P.min_p + b) : 0.f;
+  // min-p's floor: the least logit with l - M >= T ln(min_p)
+  uint32_t floor_key = kSmMinusInf;
+  if (m_raw > 0.f && m_raw <= 1.f) {
+    const double c = static_cast<double>(T) * log(static_cast<double>(m_raw));
+    const double at = static_cast<double>(M) + c;
+    uint32_t k = smp_key(at < -3.4028234e38 ? -3.4028234e38f : static_cast<float>(at));
+    while (static_cast<double>(smp_from_key(k)) - static_cast<double>(M) < c) ++k;
+    while (k > 0x00800000u && static_cast<double>(smp_from_key(k - 1)) - static_cast<double>(M) >= c) --k;
+    floor_key = k;
+  }
+
+  // this thread's sum over its vectors of the weights that reach `floor`, as integers
+  auto vector_mass = [&](const uint4 &q, float floor) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float l = element<BF16>(q, e);
+      if (l >= floor) s += weight(l);
+    }
+    return __float2ll_rn(s * kSmFix);
+  };
+  int round = 1;  // of the exchange: buffers in turn
+  // sums over the cluster (two at a time), the same in every thread; `upto`: this CTA's warps' sums
+  auto exchange = [&](i64 a, i64 c, i64 &A, i64 &C) {
+    const int r = round & 1;
+    ++round;
+    a = warp_sum64(a);
+    c = warp_sum64(c);
+    if (lane == 0) S.warp[r][warp] = static_cast<u64>(a), S.warp2[r][warp] = static_cast<u64>(c);
+    __syncthreads();
+    u64 x = 0, y = 0;
+#pragma unroll
+    for (int w = 0; w < kSmWarps; ++w) x += S.warp[r][w], y += S.warp2[r][w];
+    if (tid < static_cast<int>(ranks)) {
+      st_cluster_u64(&S.part[r][rank], tid, x);
+      st_cluster_u64(&S.part2[r][rank], tid, y);
+    }
+    cluster_sync();
+    A = C = 0;
+    for (uint32_t k = 0; k < ranks; ++k) A += static_cast<i64>(S.part[r][k]), C += static_cast<i64>(S.part2[r][k]);
+    return r;
+  };
+  // mass and count of what reaches the key
+  auto reach = [&](uint32_t key, i64 &mass, i64 &count) {
+    const float floor = smp_from_key(key);
+    i64 a = 0;
+    int n = 0;
+    for (int v = v0 + lane; v < v1; v += 32) {
+      const uint4 q = data[v];
+      a += vector_mass(q, floor);
+#pragma unroll
+      for (int e = 0; e < E; ++e) n += element<BF16>(q, e) >= floor;
+    }
+    return exchange(a, n, mass, count);
+  };
+  // the token at u: all CTAs together, from the sums that exchange number r left
+  auto choose = [&](float floor, int r, i64 Z) {
+    const double target = static_cast<double>(u) * static_cast<double>(Z);
+    // the CTA: the first whose running sum passes the target, else the last with any mass
+    int owner = -1, backup = 0;
+    i64 before = 0, at = 0;
+    for (uint32_t k = 0; k < ranks; ++k) {
+      const i64 x = static_cast<i64>(S.part[r][k]);
+      if (x > 0) backup = k;
+      if (owner < 0 && static_cast<double>(before + x) > target) owner = k, at = before;
+      before += x;
+    }
+    const bool rest = owner < 0;  // u Z was rounded up to Z
+    if (rest) owner = backup;
+    if (owner != static_cast<int>(rank)) return;
+    int w = -1, wb = 0;
+    i64 sum = at;
+    for (int k = 0; k < kSmWarps; ++k) {
+      const i64 x = static_cast<i64>(S.warp[r][k]);
+      if (x > 0) wb = k;
+      if (w < 0 && !rest && static_cast<double>(sum + x) > target) w = k, at = sum;
+      sum += x;
+    }
+    if (w < 0) w = wb;
+    if (w != warp) return;
+    i64 run = at;
+    int found = -1, tail = -1;  // the last kept token as a fallback
+    for (int v = v0; v < v1 && found < 0; v += 32) {
+      const int mine = v + lane;
+      uint4 q = make_uint4(0, 0, 0, 0);
+      i64 x = 0;
+      if (mine < v1) {
+        q = data[mine];
+        x = vector_mass(q, floor);
+      }
+      i64 inc = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const i64 y = __shfl_up_sync(FULL_MASK, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const unsigned some = __ballot_sync(FULL_MASK, x > 0);
+      const unsigned hit = rest ? 0u : __ballot_sync(FULL_MASK, x > 0 && static_cast<double>(run + inc) > target);
+      const int who = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : -1;
+      int tok = -1;
+      if (who == lane) {
+        float s = 0.f;
+        for (int e = 0; e < E; ++e) {
+          const float l = element<BF16>(q, e), y = l >= floor ? weight(l) : 0.f;
+          s += y;
+          if (y > 0.f) tok = first + mine * E + e;
+          if (hit && y > 0.f && static_cast<double>(run + inc - x + __float2ll_rn(s * kSmFix)) > target) break;
+        }
+      }
+      if (who >= 0) tok = __shfl_sync(FULL_MASK, tok, who);
+      if (hit) found = tok;
+      if (tok >= 0) tail = tok;
+      run += __shfl_sync(FULL_MASK, inc, 31);
+    }
+    if (found < 0) found = tail;
+    if (lane == 0) {
+      const int at_slice = found - first;
+      const uint4 q = data[at_slice / E];
+      float x = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e == at_slice % E) x = element<BF16>(q, e);
+      P.token[b] = found;
+      if (P.prob) P.prob[b] = static_cast<float>(static_cast<double>(weight(x)) * static_cast<double>(kSmFix) / static_cast<double>(Z));
+      P.row_status[b] = 0;
+    }
+  };
+
+  // --- the whole row's mass; the threads' maxima for top-k's bound
+  if (top_k)
+    for (uint32_t k = 0; k < ranks; ++k) max_cluster_u32(&S.tmax[tid], k, my_top);
+  i64 Z, unused;
+  {
+    i64 a = 0;
+    for (int v = v0 + lane; v < v1; v += 32) a += vector_mass(data[v], -INFINITY);
+    const int r = exchange(a, 0, Z, unused);
+    if (!top_k && !use_p && floor_key == kSmMinusInf) {
+      choose(-INFINITY, r, Z);
+      return;
+    }
+  }
+  // --- a bound that the law's floor does not lie below (where top-p goes by the
+  // mass that top-k leaves, what reaches top-k's floor has to be listed whole)
+  uint32_t bound = top_k && use_p ? kSmMinusInf : floor_key;
+  if (top_k && top_k <= kSmThreads) {
+    // the k-th largest of the 256 columns' maxima, to 16 bits (a barrier counts)
+    const uint32_t mine = S.tmax[tid] >> 16;
+    uint32_t t = 0;
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t x = t | 1u << bit;
+      if (__syncthreads_count(mine >= x) >= top_k) t = x;
+    }
+    bound = max(bound, t << 16);
+  }
+  if (use_p && !top_k) {
+    // What is dropped weighs less than (1 - top_p) Z, so a token of less than a
+    // V-th of that cannot be the last one kept: such tokens are not looked at.
+    const float least = static_cast<float>((1.0 - top_p) * static_cast<double>(Z) / static_cast<double>(kSmFix) / P.V);
+    const float far = M + (log2f(fmaxf(least, 1e-37f)) - 0.01f) / weight.sc;
+    const float from = fmaxf(far, smp_from_key(bound));
+    // Bins by exponent and three more bits of the weight; each adds up the
+    // leading 16 bits of its weights, cut off: never too much.
+    for (int v = v0 + lane; v < v1; v += 32) {
+      const uint4 q = data[v];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float l = element<BF16>(q, e);
+        if (l >= from) {
+          const uint32_t x = __float_as_uint(fminf(weight(l), 1.f));
+          const int bin = (127 << 3) - static_cast<int>(x >> 20);
+          if (bin < kSmBins) atomicAdd(&S.mine[bin], ((x & 0x7fffffu) | 0x800000u) >> 8);
+        }
+      }
+    }
+    __syncthreads();  // (a slice has at most 2^15 logits: its sums stay below 2^32)
+    for (int i = tid; i < kSmBins; i += kSmThreads)
+      if (S.mine[i]) add_cluster_u64(&S.hist[i], 0, S.mine[i]);
+    cluster_sync();
+    if (rank == 0 && warp == 0) {
+      // running sums from the largest weights down, in units of 1
+      double run = 0.0;
+      const double want = top_p * (static_cast<double>(Z) / static_cast<double>(kSmFix));
+      int at = kSmBins;
+      for (int i0 = 0; i0 < kSmBins && at == kSmBins; i0 += 32) {
+        const int i = i0 + lane;
+        // bin i holds weights of exponent 127 - ceil(i / 8)
+        double x = static_cast<double>(S.hist[i]) * exp2(-15.0 - static_cast<double>((i + 7) / 8));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double y = __shfl_up_sync(FULL_MASK, x, o);
+          if (lane >= o) x += y;
+        }
+        const unsigned hit = __ballot_sync(FULL_MASK, run + x >= want);
+        if (hit) at = i0 + __ffs(hit) - 1;
+        run += __shfl_sync(FULL_MASK, x, 31);
+      }
+      // the bin's least weight, as a logit
+      const float edge = at < kSmBins ? M + (log2f(__uint_as_float(static_cast<uint32_t>((127 << 3) - at) << 20)) - 0.001f) / weight.sc : -INFINITY;
+      if (lane < static_cast<int>(ranks)) st_cluster_u32(&S.floor, lane, __float_as_uint(fmaxf(edge, from)));
+    }
+    cluster_sync();
+    bound = max(bound, smp_key(S.floor));
+  }
+  // --- the candidates, in vocabulary order
+  const int share = kSmCands / static_cast<int>(ranks);
+  int total = 0;
+  bool listed = true;
+  {
+    const float from = smp_from_key(bound);
+    int n = 0;
+    for (int v = v0 + lane; v < v1; v += 32) {
+      const uint4 q = data[v];
+#pragma unroll
+      for (int e = 0; e < E; ++e) n += element<BF16>(q, e) >= from;
+    }
+    n = __reduce_add_sync(FULL_MASK, n);
+    const int r = round & 1;
+    ++round;
+    if (lane == 0) S.warp[r][warp] = n;
+    __syncthreads();
+    int at = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSmWarps; ++w) {
+      const int x = static_cast<int>(S.warp[r][w]);
+      if (w < warp) at += x;
+      all += x;
+    }
+    if (tid < static_cast<int>(ranks)) st_cluster_u32(&S.cnt[rank], tid, all);
+    if (all <= share && n > 0) {
+      for (int v = v0; v < v1; v += 32) {
+        const int mine = v + lane;
+        uint4 q = make_uint4(0, 0, 0, 0);
+        int c = 0;
+        if (mine < v1) {
+          q = data[mine];
+#pragma unroll
+          for (int e = 0; e < E; ++e) c += element<BF16>(q, e) >= from;
+        }
+        if (!__any_sync(FULL_MASK, c > 0)) continue;
+        int inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(FULL_MASK, inc, o);
+          if (lane >= o) inc += y;
+        }
+        int to = at + inc - c;
+        if (c > 0) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float l = element<BF16>(q, e);
+            if (l >= from) st_cluster_u64(&S.cand[rank * share + to++], 0, static_cast<u64>(smp_key(l)) << 32 | static_cast<uint32_t>(first + mine * E + e));
+          }
+        }
+        at += __shfl_sync(FULL_MASK, inc, 31);
+      }
+    }
+    cluster_sync();
+    for (uint32_t k = 0; k < ranks; ++k) {
+      total += static_cast<int>(S.cnt[k]);
+      listed = listed && static_cast<int>(S.cnt[k]) <= share;
+    }
+  }
+  constexpr int kLow = BF16 ? 16 : 0;  // a bf16 logit's key is its upper 16 bits
+  if (!listed) {
+    // --- too many: the floors by bisection, all CTAs together.  (In units of
+    // 2^kLow; a key's lower bits are ones for negative numbers, so the unit's
+    // first key reaches what the unit's logit does.)
+    i64 mass = 0, count = 0;
+    uint32_t floor = floor_key;
+    int r = 0;
+    if (top_k) {
+      uint32_t lo = bound >> kLow, hi = top_key >> kLow;
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        reach(mid << kLow, mass, count);
+        if (count >= top_k) lo = mid;
+        else hi = mid - 1;
+      }
+      floor = max(floor_key, lo << kLow);
+      if (use_p) {
+        reach(lo << kLow, mass, count);
+        Z = mass;
+        bound = max(bound, lo << kLow);
+      }
+    }
+    if (use_p) {
+      const double want = top_p * static_cast<double>(Z);
+      uint32_t lo = bound >> kLow, hi = top_key >> kLow;
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        reach(mid << kLow, mass, count);
+        if (static_cast<double>(mass) >= want) lo = mid;
+        else hi = mid - 1;
+      }
+      floor = max(floor, lo << kLow);
+    }
+    r = reach(floor, mass, count);
+    choose(smp_from_key(floor), r, mass);
+    return;
+  }
+  if (rank != 0) return;
+  // --- the first CTA: a thread takes neighbouring candidates
+  uint32_t key[kSmPer];
+  int id[kSmPer];
+  i64 w[kSmPer];
+  const int each = (total + kSmThreads - 1) / kSmThreads;  // at most kSmPer
+  uint32_t least = 0xffffffffu;
+  {
+    int seg = 0, skip = tid * each;
+    while (seg < static_cast<int>(ranks) && skip >= static_cast<int>(S.cnt[seg])) skip -= static_cast<int>(S.cnt[seg++]);
+#pragma unroll
+    for (int i = 0; i < kSmPer; ++i) {
+      key[i] = 0;
+      id[i] = -1;
+      w[i] = 0;
+      if (i < each && seg < static_cast<int>(ranks)) {
+        const u64 c = S.cand[seg * share + skip];
+        key[i] = static_cast<uint32_t>(c >> 32);
+        id[i] = static_cast<int>(static_cast<uint32_t>(c));
+        w[i] = __float2ll_rn(weight(smp_from_key(key[i])) * kSmFix);
+        least = min(least, key[i]);
+        ++skip;
+        while (seg < static_cast<int>(ranks) && skip >= static_cast<int>(S.cnt[seg])) skip = 0, ++seg;
+      }
+    }
+  }
+  auto block_sum64 = [&](i64 a) {
+    const int r = round & 1;
+    ++round;
+    a = warp_sum64(a);
+    if (lane == 0) S.warp[r][warp] = static_cast<u64>(a);
+    __syncthreads();
+    u64 x = 0;
+#pragma unroll
+    for (int k = 0; k < kSmWarps; ++k) x += S.warp[r][k];
+    return static_cast<i64>(x);
+  };
+  auto block_count = [&](int a) {
+    const int r = round & 1;
+    ++round;
+    a = __reduce_add_sync(FULL_MASK, a);
+    if (lane == 0) S.warp[r][warp] = static_cast<u64>(a);
+    __syncthreads();
+    int x = 0;
+#pragma unroll
+    for (int k = 0; k < kSmWarps; ++k) x += static_cast<int>(S.warp[r][k]);
+    return x;
+  };
+  uint32_t floor = floor_key;
+  {
+    const int r = round & 1;
+    ++round;
+    least = __reduce_min_sync(FULL_MASK, least);
+    if (lane == 0) S.warp[r][warp] = least;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSmWarps; ++k) least = min(least, static_cast<uint32_t>(S.warp[r][k]));
+  }
+  if (top_k) {
+    uint32_t lo = least >> kLow, hi = top_key >> kLow;
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kSmPer; ++i) n += id[i] >= 0 && key[i] >= mid << kLow;
+      if (block_count(n) >= top_k) lo = mid;
+      else hi = mid - 1;
+    }
+    floor = max(floor, lo << kLow);
+    if (use_p) {
+      i64 a = 0;
+#pragma unroll
+      for (int i = 0; i < kSmPer; ++i)
+        if (key[i] >= lo << kLow) a += w[i];
+      Z = block_sum64(a);
+      least = max(least, lo << kLow);
+    }
+  }
+  if (use_p) {
+    const double want = top_p * static_cast<double>(Z);
+    uint32_t lo = least >> kLow, hi = top_key >> kLow;
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      i64 a = 0;
+#pragma unroll
+      for (int i = 0; i < kSmPer; ++i)
+        if (key[i] >= mid << kLow) a += w[i];
+      if (static_cast<double>(block_sum64(a)) >= want) lo = mid;
+      else hi = mid - 1;
+    }
+    floor = max(floor, lo << kLow);
+  }
+  // --- running sums in vocabulary order
+  i64 mine = 0;
+#pragma unroll
+  for (int i = 0; i < kSmPer; ++i) {
+    if (id[i] < 0 || key[i] < floor) w[i] = 0;
+    mine += w[i];
+  }
+  i64 inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const i64 y = __shfl_up_sync(FULL_MASK, inc, o);
+    if (lane >= o) inc += y;
+  }
+  const int r = round & 1;
+  if (lane == 31) S.warp[r][warp] = static_cast<u64>(inc);
+  __syncthreads();
+  i64 run = inc - mine, all = 0;
+#pragma unroll
+  for (int k = 0; k < kSmWarps; ++k) {
+    const i64 x = static_cast<i64>(S.warp[r][k]);
+    if (k < warp) run += x;
+    all += x;
+  }
+  const double target = static_cast<double>(u) * static_cast<double>(all);
+#pragma unroll
+  for (int i = 0; i < kSmPer; ++i) {
+    const i64 to = run + w[i];
+    // the first that passes the target; where rounding took u Z to Z, the last with any mass
+    const bool hit = w[i] > 0 && static_cast<double>(run) <= target && static_cast<double>(to) > target;
+    const bool end = w[i] > 0 && to == all && static_cast<double>(all) <= target;
+    if (hit || end) {
+      P.token[b] = id[i];
+      if (P.prob) P.prob[b] = static_cast<float>(static_cast<double>(w[i]) / static_cast<double>(all));
+      P.row_status[b] = 0;
+    }
+    run = to;
+  }
+}
+
+bool smp_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Dynamic shared memory above 48 KB has to be asked for, once per device.
+template <bool BF16, bool VEC>
+cudaError_t launch_sample(const SampleParams &p, int ranks, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(sample_kernel<BF16, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * ranks);
+  cfg.blockDim = dim3(kSmThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.slice) * (BF16 ? 2 : 4);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {static_cast<unsigned>(ranks), 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<BF16, VEC>, p);
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+spec_status spec_sample(const spec_sample_args *a, const spec_sample_out *o, void *stream) {
+  if (!a || !o) return SPEC_ERR_NULL;
+  if (a->B < 0 || a->B > 0x7fffffff / 64 || a->V < 1 || a->V > SPEC_MAX_V) return SPEC_ERR_SHAPE;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
+  if (a->row_stride < a->V) return SPEC_ERR_ARG;
+  if (a->B == 0) return SPEC_OK;
+  if (!a->logits || !a->u || !o->token || !o->row_status) return SPEC_ERR_NULL;
+  const bool bf16 = a->dtype == SPEC_BF16;
+  const int esz = bf16 ? 2 : 4;
+  if (!smp_aligned(a->logits, esz)) return SPEC_ERR_ALIGN;
+  const void *w4[] = {a->u, a->temperature, a->top_k, a->top_p, a->min_p, o->token, o->prob, o->row_status};
+  for (const void *q : w4)
+    if (!smp_aligned(q, 4)) return SPEC_ERR_ALIGN;
+  SampleParams p = {};
+  p.logits = a->logits;
+  p.u = a->u;
+  p.temperature = a->temperature;
+  p.top_k = a->top_k;
+  p.top_p = a->top_p;
+  p.min_p = a->min_p;
+  p.token = o->token;
+  p.prob = o->prob;
+  p.row_status = o->row_status;
+  p.row_stride = a->row_stride;
+  p.B = a->B;
+  p.V = a->V;
+  // CTAs per row: slices of at most 32 KB, as far as eight go
+  const long long bytes = static_cast<long long>(a->V) * esz;
+  int ranks = 1;
+  while (ranks < kSmMaxCluster && bytes > ranks * (32LL << 10)) ranks *= 2;
+  const int unit = 16 / esz;
+  p.slice = ((a->V + ranks - 1) / ranks + unit - 1) / unit * unit;
+  const bool vec = smp_aligned(a->logits, 16) && (a->row_stride * esz) % 16 == 0 && bytes % 16 == 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = bf16 ? (vec ? launch_sample<true, true>(p, ranks, s) : launch_sample<true, false>(p, ranks, s))
+                             : (vec ? launch_sample<false, true>(p, ranks, s) : launch_sample<false, false>(p, ranks, s));
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // extern "C"
