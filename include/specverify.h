@@ -787,9 +787,14 @@ spec_status spec_kv_compact_pages(const spec_page_compact_args *args, int32_t *r
  * query i >= count[b], gets zeros and lse = -inf.
  *
  * Sums, maxima and softmax statistics are fp32; the softmax weights are rounded
- * once to the product's 16-bit type (the cache's; fp16 for SPEC_E4M3, where the
- * weight of a value's code, weight times scale, is rounded).  Results do not
- * depend on timing: every sum has a fixed order.
+ * once to the product's 16-bit type, which is the cache's.  Over SPEC_E4M3 it is
+ * bf16 (scaled codes are bf16 numbers exactly) for SPEC_BF16 queries of more than
+ * 32 rows per KV head, N * q_heads / heads; else fp16, and what is rounded is the
+ * weight of a value's code, weight times scale.  Results do not depend on timing:
+ * every sum has a fixed order.  A row any part of whose work gave up waiting (see
+ * spec_set_wait_timeout_ns) is flagged SPEC_ROW_TIMEOUT: the queries and heads
+ * that the part belonged to get zeros and lse = -inf, the row's others keep their
+ * answers.
  * Workspace: spec_paged_attention_workspace_size(args) bytes, no contents kept
  * between calls.  N = 0 is a no-op, and row_status is not written.
  */
@@ -880,7 +885,7 @@ const char *spec_status_string(spec_status s);
  * the bulk-copy stream waits on a barrier that nothing completes, and the
  * truncation and DRIFT kernels withhold their records, so every reader gives
  * up (or finds a record missing) and its rows report SPEC_ROW_TIMEOUT.  The
- * attention's kernel for many query rows withholds its first keys.  2 + g: that
+ * attention's kernels for many query rows withhold their first keys.  2 + g: that
  * of KV head g alone does, and the verify calls are as ever; 0 turns it off.
  */
 void spec_set_wait_timeout_ns(uint64_t ns);

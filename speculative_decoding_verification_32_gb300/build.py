@@ -24,7 +24,8 @@ VARIANTS = {None: (BUILD, LIB, []),
                        os.path.join(HERE, "libspecverify_bounds.so"), ["-DSV_BOUNDS"])}
 SOURCES = ["api.cu", "chain_stochastic.cu", "greedy.cu", "rollback.cu", "kv_policy.cu",
            "kv_cache.cu", "logprobs.cu", "prefix_attention.cu",
-           "prefix_attention_tile.cu", "pages.cu", "paged_attention.cu", "sample.cu"]
+           "prefix_attention_tile.cu", "pages.cu", "paged_attention.cu",
+           "paged_attention_tile.cu", "sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -6,6 +6,7 @@
 //    and for draft trees the parents, each node's depth and which of the pass's
 //    tokens it sees.  The attention kernel runs beside it and looks at the
 //    result before it writes anything.
+//  paged_tile_kernel (paged_attention_tile.cu) -- many query rows.
 //  paged_rows_kernel -- 16 or 32 query rows (the query heads of one KV head and
 //    tokens of one row) against a part of their keys, one warp.
 //  paged_join_kernel -- one warp per query row adds up the parts.
@@ -23,7 +24,6 @@
 namespace sv {
 namespace {
 
-constexpr int kPaSms = 152;  // parts are sized for this many SMs
 constexpr float kPaLazy = 8.f;
 constexpr int kCheckThreads = 256;
 constexpr int kPaJoinThreads = 128;
@@ -724,6 +724,7 @@ cudaError_t launch_rows_d(const PagedParams &p, cudaStream_t s) {
 }
 
 struct PagedPlan {
+  bool tile;           // paged_tile_kernel
   int splits, oblk, W;
   size_t rows, info_at, anc_at, depth_at, flag_at, ml_at, part_at, bytes;
 };
@@ -756,13 +757,29 @@ PagedPlan plan_paged(const spec_paged_attention_args *a) {
   PagedPlan p = {};
   const long long G = a->q_heads / a->heads, rows1 = a->N * G;
   p.rows = static_cast<size_t>(a->B) * a->N * a->q_heads;
-  p.oblk = rows1 > 16 ? 32 : 16;
+  // More than 32 query rows per KV head would read the keys again for each 32.  (fp16
+  // queries over codes go that way all the same: as bf16, which the tile kernel
+  // turns codes into, they would lose three bits.)
+  p.tile = rows1 > 32 && !(a->cache_dtype == SPEC_E4M3 && a->q_dtype == SPEC_F16);
+  p.oblk = p.tile ? 256 : rows1 > 16 ? 32 : 16;
   const long long blocks = (rows1 + p.oblk - 1) / p.oblk, items = a->B * a->heads * blocks;
   // tokens that an item may see
   long long tokens = static_cast<long long>(a->columns) * a->page_size;
   if (a->window > 0) tokens = std::min(tokens, static_cast<long long>(a->window) + a->sinks + p.oblk / G + 1 + 2 * kGroup);
-  const long long want = (8LL * kPaSms * 2 + items - 1) / items;
-  p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 32})));
+  if (p.tile) {
+    // one CTA per SM runs through items: the fewest rounds of items times their
+    // blocks of 128 keys, an item's ends counting as two
+    const long long n = (tokens + 127) / 128;
+    long long best = -1;
+    p.splits = 1;
+    for (long long s = 1; s <= std::min<long long>(n, 32); ++s) {
+      const long long cost = (items * s + kPagedSms - 1) / kPagedSms * ((n + s - 1) / s + 2) + (s > 1 ? 3 : 0);
+      if (best < 0 || cost < best) best = cost, p.splits = static_cast<int>(s);
+    }
+  } else {
+    const long long want = (8LL * kPagedSms * 2 + items - 1) / items;
+    p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 32})));
+  }
   p.W = a->parent ? (a->N + 31) / 32 : 0;
   const size_t q = static_cast<size_t>(a->B) * a->N;
   size_t at = 0;
@@ -855,7 +872,8 @@ spec_status spec_paged_attention(const spec_paged_attention_args *a, void *out, 
   p.rowinfo = info;
   if (a->parent) p.anc = anc, p.depth = depth;
   const int ct = a->cache_dtype;
-  cudaError_t e = ct == SPEC_E4M3   ? launch_rows_d<SPEC_E4M3>(p, s)
+  cudaError_t e = plan.tile         ? launch_paged_tile(p, ct, s)
+                  : ct == SPEC_E4M3 ? launch_rows_d<SPEC_E4M3>(p, s)
                   : ct == SPEC_BF16 ? launch_rows_d<SPEC_BF16>(p, s)
                                     : launch_rows_d<SPEC_F16>(p, s);
   if (e != cudaSuccess) return SPEC_ERR_CUDA;

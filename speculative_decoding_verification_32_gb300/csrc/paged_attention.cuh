@@ -25,7 +25,8 @@
 
 namespace sv {
 
-constexpr int kGroup = 16;  // tokens
+constexpr int kGroup = 16;       // tokens
+constexpr int kPagedSms = 152;   // items and parts are sized for this many SMs
 
 struct PagedParams {
   const unsigned char *k, *v;  // entries
@@ -125,5 +126,8 @@ __device__ __noinline__ float paged_odd_sum(const PagedParams &P, int b, int i, 
   }
   return y;
 }
+
+// paged_tile_kernel over all rows.
+cudaError_t launch_paged_tile(const PagedParams &p, int ctype, cudaStream_t s);
 
 }  // namespace sv
