@@ -14,9 +14,10 @@
 //     memory.  That is exact (4 bits of significand, and bf16 has fp32's
 //     exponents), so scales may lie any distance apart;
 //   - a CTA runs through many items (a prompt has hundreds of them), and the
-//     roles do not meet between them: a warpgroup loads its next queries as soon
-//     as its last scores are in, the tensor cores start on them while it writes
-//     the answers, and the producers run on through the pages.
+//     roles do not meet between them.  One warp works the items out and hands
+//     them on; the producers bring the next queries as soon as a tile's last
+//     scores are made and run on through the pages, and the tensor cores start
+//     on them while the softmax writes the answers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -32,7 +33,7 @@ namespace {
 constexpr int kBlk = 128;               // keys per block
 constexpr int kBlkGroups = kBlk / kGroup;
 constexpr int kTileThreads = 512;       // softmax of tiles A and B, producers, tensor-core issue
-constexpr int kIssueWarp = 12;
+constexpr int kIssueWarp = 12, kItemWarp = 13;
 constexpr int kLaunchRegs = 128;        // 65536 / kTileThreads
 template <bool E4>
 struct Regs {
@@ -49,21 +50,37 @@ struct Layout {
   static constexpr int kK = 2 * kOp;         // two buffers
   static constexpr int kV = 4 * kOp;         // two buffers
   static constexpr int kCtrl = 6 * kOp;
-  static constexpr int kSmem = kCtrl + 4096 + 1024;  // + control block + alignment
+  static constexpr int kStage = kCtrl + 1024;        // codes: two buffers of a block's keys or values as they are
+  static constexpr int smem(bool codes) { return kStage + (codes ? kOp : 0) + 1024; }  // + alignment
 };
 
+// One (row, block of 256 query rows, KV head, part of the keys), and what all
+// roles have to know of it.
+struct TileItem {
+  int item;            // negative: there are no more
+  int b, g, blk, split;
+  int n, cnt;          // tokens before the pass; queries (negative: the row cannot be used)
+  int r0;              // first query row
+  int tiles;           // row tiles in use
+  int end;             // keys lie below this token
+  int p0, p1;          // the queries' positions lie in p0 .. p1
+  int g0, g1;          // groups of keys
+  int nblk;            // blocks of keys
+};
+
+constexpr int kItemSlots = 4;
 struct TileCtrl {
   uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
-  uint64_t sfull[2], pfull[2], done[2], qfull[2], ofree[2], drain;
+  uint64_t sfull[2], pfull[2], done[2], qfull[2], qfree[2], ofree[2], drain;
+  uint64_t ifull[kItemSlots], ifree[kItemSlots];
   uint32_t tmem;
   int abort;
-  // 1 + the item in which a value that is not finite was taken out, four items
-  // in turn (the producers are at most two blocks ahead of the tensor cores)
-  int odd[4];
-  uint32_t factor[2][kBlk];   // codes: the tokens' scales, keys and values
-  int qoff[256][2];           // where a query row's elements are (two halves of 64 bits); -1: past the last
+  // 1 + the item in which a value that is not finite was taken out, items with
+  // keys in turn (the producers are at most two blocks ahead of the answers)
+  int odd[kItemSlots];
+  TileItem items[kItemSlots];
 };
-static_assert(sizeof(TileCtrl) <= 4096, "control block");
+static_assert(sizeof(TileCtrl) <= 1024, "control block");
 
 __device__ __forceinline__ bool wait_on(TileCtrl *c, uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
   if (mbar_try_wait(bar, parity, 10000)) return true;
@@ -78,44 +95,44 @@ __device__ __forceinline__ bool wait_on(TileCtrl *c, uint64_t *bar, uint32_t par
   }
 }
 
-// One (row, block of 256 query rows, KV head, part of the keys), and what all
-// roles have to know of it.
-struct TileItem {
-  int b, g, blk, split;
-  int n, cnt;          // tokens before the pass; queries (negative: the row cannot be used)
-  int r0;              // first query row
-  int tiles;           // row tiles in use
-  int end;             // keys lie below this token
-  int p0, p1;          // the queries' positions lie in p0 .. p1
-  int g0, g1;          // groups of keys
-  int nblk;            // blocks of keys
-  __device__ __forceinline__ TileItem(const PagedParams &P, int item, int blocks) {
-    g = item % P.H;
-    item /= P.H;
-    split = item % P.splits;
-    item /= P.splits;
-    blk = blocks - 1 - item % blocks;  // the last block of a prompt sees most, so it comes first
-    b = item / blocks;
-    cnt = paged_queries(P, b, n);
-    r0 = blk * 256;
-    const int left = P.N * P.G - r0;
-    tiles = left > 128 ? 2 : 1;
-    const int q_first = r0 / P.G, q_last = min((r0 + 255) / P.G, P.N - 1);
-    const bool tree = P.W > 0;
-    end = cnt <= q_first ? 0 : tree ? n + cnt : n + min(cnt, q_last + 1);
-    p0 = tree ? n : n + q_first;
-    p1 = tree ? n + cnt : n + q_last;
-    const Keys keys(P, p0, end);
-    g0 = 0;
-    g1 = keys.n;
-    if (P.splits > 1) {  // parts of whole blocks
-      const int per = ((keys.n + P.splits - 1) / P.splits + kBlkGroups - 1) / kBlkGroups * kBlkGroups;
-      g0 = min(keys.n, split * per);
-      g1 = min(keys.n, g0 + per);
-    }
-    nblk = (g1 - g0 + kBlkGroups - 1) / kBlkGroups;
+__device__ __forceinline__ TileItem make_item(const PagedParams &P, int item, int blocks) {
+  TileItem I;
+  I.item = item;
+  I.g = item % P.H;
+  item /= P.H;
+  I.split = item % P.splits;
+  item /= P.splits;
+  I.blk = blocks - 1 - item % blocks;  // the last block of a prompt sees most, so it comes first
+  I.b = item / blocks;
+  I.cnt = paged_queries(P, I.b, I.n);
+  I.r0 = I.blk * 256;
+  I.tiles = P.N * P.G - I.r0 > 128 ? 2 : 1;
+  const int q_first = I.r0 / P.G, q_last = min((I.r0 + 255) / P.G, P.N - 1);
+  const bool tree = P.W > 0;
+  I.end = I.cnt <= q_first ? 0 : tree ? I.n + I.cnt : I.n + min(I.cnt, q_last + 1);
+  I.p0 = tree ? I.n : I.n + q_first;
+  I.p1 = tree ? I.n + I.cnt : I.n + q_last;
+  const Keys keys(P, I.p0, I.end);
+  I.g0 = 0;
+  I.g1 = keys.n;
+  if (P.splits > 1) {  // parts of whole blocks
+    const int per = ((keys.n + P.splits - 1) / P.splits + kBlkGroups - 1) / kBlkGroups * kBlkGroups;
+    I.g0 = min(keys.n, I.split * per);
+    I.g1 = min(keys.n, I.g0 + per);
   }
-};
+  I.nblk = (I.g1 - I.g0 + kBlkGroups - 1) / kBlkGroups;
+  return I;
+}
+
+// The it-th item, by all lanes of a warp; false: a wait ran out.
+__device__ __forceinline__ bool take_item(TileCtrl *c, int it, TileItem &I, uint64_t limit) {
+  const int s = it % kItemSlots;
+  if (!__all_sync(FULL_MASK, wait_on(c, &c->ifull[s], (it / kItemSlots) & 1, limit))) return false;
+  I = c->items[s];
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_arrive(&c->ifree[s]);
+  return true;
+}
 
 // Whether some query at a position in p0 .. p1 does not see some token of the group.
 __device__ __forceinline__ bool group_masked(const PagedParams &P, int t0, int n, int p0, int p1) {
@@ -147,27 +164,64 @@ __device__ __forceinline__ uint32_t group_seen(const PagedParams &P, int t0, int
 
 // Four e4m3 codes as bf16 numbers times a power of two (all of it exact): a code's
 // exponent and fraction are moved to where bf16 has them, which makes it 2^-120 of
-// its value (its subnormal numbers are bf16's there), and multiplied up.
-__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); }
-__device__ __forceinline__ uint32_t from_bf2(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+// its value (its subnormal numbers are bf16's there), and multiplied up: at once
+// by 2^120 and the scale where that is a bf16 number (scales up to 2^7), else in
+// two steps.  A code of NaN comes out as 480 times the scale, which code_nan() tells.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t factor) {
   const uint32_t lo = __byte_perm(w, 0, 0x1404), hi = __byte_perm(w, 0, 0x3424);
-  const __nv_bfloat162 up = as_bf2(0x7b807b80u);  // 2^120
-  const __nv_bfloat162 a = __hmul2(as_bf2((lo & 0x80008000u) | ((lo >> 4) & 0x07f007f0u)), up);
-  const __nv_bfloat162 b = __hmul2(as_bf2((hi & 0x80008000u) | ((hi >> 4) & 0x07f007f0u)), up);
-  uint2 r = make_uint2(from_bf2(__hmul2(a, as_bf2(factor))), from_bf2(__hmul2(b, as_bf2(factor))));
-  if (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {  // codes of NaN
-    if ((w & 0x7fu) == 0x7fu) r.x |= 0x7fc0u;
-    if ((w & 0x7f00u) == 0x7f00u) r.x |= 0x7fc00000u;
-    if ((w & 0x7f0000u) == 0x7f0000u) r.y |= 0x7fc0u;
-    if ((w & 0x7f000000u) == 0x7f000000u) r.y |= 0x7fc00000u;
-  }
+  return make_uint2(mul_bf16x2((lo & 0x80008000u) | ((lo >> 4) & 0x07f007f0u), factor),
+                    mul_bf16x2((hi & 0x80008000u) | ((hi >> 4) & 0x07f007f0u), factor));
+}
+// Nonzero in the upper bit of every byte that is a code of NaN.
+__device__ __forceinline__ uint32_t code_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint2 with_nans(uint2 r, uint32_t nan) {
+  if (nan & 0x80u) r.x |= 0x7fc0u;
+  if (nan & 0x8000u) r.x |= 0x7fc00000u;
+  if (nan & 0x800000u) r.y |= 0x7fc0u;
+  if (nan & 0x80000000u) r.y |= 0x7fc00000u;
   return r;
 }
-// 2^(c - 127) as a pair of bf16; NaN for 255
-__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t c) {
-  const uint32_t h = c == 255u ? 0x7fc0u : c ? c << 7 : 0x0040u;
+constexpr uint32_t kTopScale = 134;  // the largest scale byte that goes with 2^120 in one bf16 number
+// 2^120 times the scale of byte c (of kTopScale, if c is larger), as a pair of bf16; NaN for 255
+__device__ __forceinline__ uint32_t first_factor(uint32_t c) {
+  const uint32_t h = c == 255u ? 0x7fc0u : (min(c, kTopScale) + 120u) << 7;
   return h | h << 16;
+}
+// the rest of the scale
+__device__ __forceinline__ uint32_t second_factor(uint32_t c) {
+  const uint32_t h = c == 255u || c <= kTopScale ? 0x3f80u : (c - kTopScale + 127u) << 7;
+  return h | h << 16;
+}
+
+// Whether one of eight 16-bit numbers is an infinity or NaN; these set to zero.
+template <bool BF>
+__device__ __forceinline__ bool not_finite(const uint4 &u) {
+  constexpr uint32_t top = BF ? 0x7f807f80u : 0x7c007c00u, one = BF ? 0x00800080u : 0x04000400u;
+  return (((u.x & top) + one) | ((u.y & top) + one) | ((u.z & top) + one) | ((u.w & top) + one)) & 0x80008000u;
+}
+template <bool BF>
+__device__ __forceinline__ void drop_not_finite(uint4 &u) {
+  constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if ((w[e] & top) == top) w[e] &= 0xffff0000u;
+    if ((w[e] >> 16 & top) == top) w[e] &= 0x0000ffffu;
+  }
+  u = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight elements from any address; zeros if not `on`.
+__device__ __noinline__ void copy_eight(unsigned char *to, const unsigned short *q, bool on) {
+  uint32_t u[4] = {0, 0, 0, 0};
+  if (on)
+    for (int i = 0; i < 4; ++i) u[i] = q[2 * i] | static_cast<uint32_t>(q[2 * i + 1]) << 16;
+  *reinterpret_cast<uint4 *>(to) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 __device__ __forceinline__ float max3f(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
@@ -192,8 +246,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
       mbar_init(&c->pfull[i], 128);
       mbar_init(&c->done[i], 1);
       mbar_init(&c->qfull[i], 128);
+      mbar_init(&c->qfree[i], 1);
       mbar_init(&c->ofree[i], 128);
-      c->odd[i] = c->odd[i + 2] = 0;
+    }
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(&c->ifull[i], 1);
+      mbar_init(&c->ifree[i], 4 + 1 + 8);  // warps: producers, issue, softmax
+      c->odd[i] = 0;
     }
     mbar_init(&c->drain, 1);
     c->abort = 0;
@@ -212,17 +271,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kProduce));
     const int pt = tid - 256;
     bool live = true;
-    // A thread brings 16-byte pieces of every kStep-th token of a block.
+    // A thread brings 16-byte pieces of every kStep-th token of a block: 16-bit
+    // entries where the tensor cores want them, codes into a buffer of their own
+    // (each thread turns what it brought itself into bf16).
     constexpr int L = E4 ? DP / 16 : DP / 8, kStep = 128 / L, kPer = kBlk / kStep;
+    static_assert(!E4 || kPer == L, "a lane's piece is the number of the token whose scale it reads");
     const int pc = pt % L, row0 = pt / L;
     const bool col = pc * 16 < P.D * (E4 ? 1 : 2);
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t put0 = E4 ? pt * 16 : (pc / 8) * 16384 + row0 * 128 + (((pc % 8) ^ (row0 & 7)) << 4);
+    const uint32_t put0 = E4 ? C::kStage + pt * 16 : (pc / 8) * 16384 + row0 * 128 + (((pc % 8) ^ (row0 & 7)) << 4);
     constexpr int kPut = E4 ? 2048 : kStep * 128;
-    int kb = 0;     // blocks handed over so far
-    int odd_at = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-      const TileItem I(P, item, blocks);
+    int kb = 0, worked = 0, ni[2] = {0, 0};  // blocks and items so far, items of each tile
+    const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
+    TileItem I;
+    for (int turn = 0; live && take_item(c, turn, I, limit) && I.item >= 0; ++turn) {
       if (I.nblk == 0) continue;
       const Keys keys(P, I.p0, I.end);
       const int32_t *const trow = P.table + static_cast<size_t>(I.b) * P.columns;
@@ -240,7 +302,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
           if (pg >= 0 && pg < P.pages) where = pg * P.page_stride + (first - j * P.page) * P.tok_stride;
         }
       };
-      // copies of block k's keys or values; codes: the scale byte of the block's token pt
+      auto buffer_free = [&](int at, bool val) {
+        const int s = at & 1;
+        if (at >= 2 && live) live = wait_on(c, val ? &c->vfree[s] : &c->kfree[s], ((at >> 1) - 1) & 1, limit);
+        live = __all_sync(FULL_MASK, live);
+      };
+      // copies of block k's keys (it = 2 k) or values (2 k + 1); codes: the scale
+      // byte of the block's token row0 + pc kStep
       auto issue = [&](int it) -> uint32_t {
         uint32_t byte = 0;
         if (it < 2 * I.nblk) {
@@ -250,14 +318,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
           const int base = (k % 4) * kBlkGroups;
           const unsigned char *const plane = val ? P.v : P.k;
           if constexpr (E4) {
-            const long long w = __shfl_sync(FULL_MASK, where, base + pt / 16);
-            const int t = __shfl_sync(FULL_MASK, first, base + pt / 16) + pt % 16;
-            if (w >= 0 && t < I.end) byte = __ldg(plane + w + pt % 16 * P.tok_stride + static_cast<long long>(P.H) * P.D + I.g);
+            const int row = row0 + pc * kStep;
+            const long long w = __shfl_sync(FULL_MASK, where, base + row / 16);
+            const int t0 = __shfl_sync(FULL_MASK, first, base + row / 16);
+            if (w >= 0 && t0 + row % 16 < I.end) byte = __ldg(plane + w + row % 16 * P.tok_stride + static_cast<long long>(P.H) * P.D + I.g);
+          } else {
+            buffer_free(at, val);
           }
-          if (at >= 2 && live) live = wait_on(c, val ? &c->vfree[s] : &c->kfree[s], ((at >> 1) - 1) & 1, limit);
-          live = __all_sync(FULL_MASK, live);
           if (live) {
-            const uint32_t dst = sbase + put0 + (val ? C::kV : C::kK) + s * C::kOp;
+            const uint32_t dst = sbase + put0 + (E4 ? (it & 1) * (C::kOp / 2) : (val ? C::kV : C::kK) + s * C::kOp);
             constexpr int kSame = kStep < 16 ? 16 / kStep : 1;  // neighbouring copies in one group
 #pragma unroll
             for (int i0 = 0; i0 < kPer; i0 += kSame) {
@@ -277,94 +346,146 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
         cp_async_commit();
         return byte;
       };
-      uint32_t sc0 = issue(0), sc1 = issue(1);
-      for (int it = 0; it < 2 * I.nblk; ++it) {
-        cp_async_wait<1>();
-        const int k = it >> 1, at = kb + k, s = at & 1;
-        const bool val = it & 1;
-        // In groups that some query does not see whole, values that are not
-        // finite are taken out (it would get 0 * NaN) and put into the answers of
-        // the queries that see them at the end.
-        unsigned part = 0;  // such groups of the block
-        if (val) {
+      // queries: DP / 8 lanes per row, 16 bytes each, once the scores that the
+      // item before made of the tile's are done
+      {
+        constexpr int QL = DP / 8, kRows = 128 / QL;
+        const int qc = pt % QL;
 #pragma unroll
-          for (int i = 0; i < kBlkGroups; ++i) {
-            const int gi = I.g0 + k * kBlkGroups + i;
-            if (gi < I.g1 && group_masked(P, keys.token(gi), I.n, I.p0, I.p1)) part |= 1u << i;
+        for (int tile = 0; tile < 2; ++tile) {
+          if (tile >= I.tiles) break;
+          if (ni[tile] > 0 && live) live = wait_on(c, &c->qfree[tile], (ni[tile] - 1) & 1, limit);
+          live = __all_sync(FULL_MASK, live);
+          if (!live) break;
+          ++ni[tile];
+          const int r = I.r0 + tile * 128 + pt / QL;
+          int t = r / P.G, h = r - t * P.G;  // the row's token and head of the group
+          const unsigned short *q = static_cast<const unsigned short *>(P.q) + I.b * P.qs[0] + t * P.qs[1] +
+                                    (static_cast<long long>(I.g) * P.G + h) * P.qs[2] + qc * 8;
+          unsigned char *to = smem + C::kQ + tile * C::kOp + (qc / 8) * 16384 + (pt / QL) * 128 + (((qc % 8) ^ (pt / QL & 7)) << 4);
+          const int dt = kRows / P.G, dh = kRows - dt * P.G;
+          const long long step = dt * P.qs[1] + dh * P.qs[2], wrap = P.qs[1] - P.G * P.qs[2];
+          const bool in = qc * 8 < P.D;
+#pragma unroll 2
+          for (int i = 0; i < 128 / kRows; ++i) {
+            const bool on = in && t < P.N;
+            if (vec)
+              cp_async16_zfill(smem_u32(to), on ? q : static_cast<const unsigned short *>(P.q), on);
+            else
+              copy_eight(to, q, on);
+            to += kRows * 128;
+            t += dt;
+            h += dh;
+            q += step;
+            if (h >= P.G) h -= P.G, ++t, q += wrap;
           }
         }
-        const uint32_t buf = sbase + (val ? C::kV : C::kK) + s * C::kOp;
-        if constexpr (!E4) {
-          if (part && live) {
+        cp_async_commit();
+      }
+      uint32_t sc0 = 0, sc1 = 0;
+      // two turns ahead: what is issued in one is handed over in the next but one
+      for (int it = -2; it < 2 * I.nblk; ++it) {
+        if (it >= 0) {
+          cp_async_wait<1>();
+          const int k = it >> 1, at = kb + k, s = at & 1;
+          const bool val = it & 1;
+          // In groups that some query does not see whole, values that are not
+          // finite are taken out (it would get 0 * NaN) and put into the answers of
+          // the queries that see them at the end.
+          unsigned part = 0;  // such groups of the block
+          if (val) {
+            const int gi = I.g0 + k * kBlkGroups + (lane & 7);
+            part = __ballot_sync(FULL_MASK, gi < I.g1 && group_masked(P, keys.token(gi), I.n, I.p0, I.p1)) & 0xffu;
+          }
+          unsigned char *const buf = smem + (val ? C::kV : C::kK) + s * C::kOp;
+          bool odd = false;
+          if constexpr (!E4) {
+            if (part) {
+              constexpr int kRun = kPer < 8 ? kPer : 8;
+              bool some = false;
+#pragma unroll
+              for (int i0 = 0; i0 < kPer; i0 += kRun) {
+                uint4 w[kRun];
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) w[i] = *reinterpret_cast<const uint4 *>(buf + put0 + (i0 + i) * kPut);
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) some = some || not_finite<BF>(w[i]);
+              }
+              if (some) {
+#pragma unroll 1
+                for (int i = 0; i < kPer; ++i) {
+                  uint4 w = *reinterpret_cast<const uint4 *>(buf + put0 + i * kPut);
+                  if (!(part >> ((row0 + i * kStep) / 16) & 1u) || !not_finite<BF>(w)) continue;
+                  drop_not_finite<BF>(w);
+                  *reinterpret_cast<uint4 *>(buf + put0 + i * kPut) = w;
+                  odd = true;
+                }
+              }
+            }
+          } else {
+            buffer_free(at, val);
+            const unsigned char *const codes = smem + put0 + (it & 1) * (C::kOp / 2);
+            uint32_t nans = 0;
+            // (255 among them: a scale of NaN)
+            const bool large = __any_sync(FULL_MASK, sc0 > kTopScale);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
               const int row = row0 + i * kStep;
-              if (!(part >> (row / 16) & 1u)) continue;
-              const uint32_t to = buf + put0 + i * kPut;
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(to) : "memory");
-              bool odd = false;
+              const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * kPut);
+              const uint32_t f = first_factor(__shfl_sync(FULL_MASK, sc0, (lane & ~(L - 1)) + i));
+              nans |= code_nan(w.x) | code_nan(w.y) | code_nan(w.z) | code_nan(w.w);
+              const uint2 y0 = codes_to_bf16(w.x, f), y1 = codes_to_bf16(w.y, f), y2 = codes_to_bf16(w.z, f), y3 = codes_to_bf16(w.w, f);
+              // the two 16-byte halves, the upper panel's lanes in the other
+              // order: eight lanes then cover all banks
+              const int ch = (pc % 4) * 2, up = pc / 4;
+              unsigned char *const to = buf + up * 16384 + row * 128;
+              const uint4 lo = make_uint4(y0.x, y0.y, y1.x, y1.y), hi = make_uint4(y2.x, y2.y, y3.x, y3.y);
+              *reinterpret_cast<uint4 *>(to + (((ch + up) ^ (row & 7)) << 4)) = up ? hi : lo;
+              *reinterpret_cast<uint4 *>(to + (((ch + 1 - up) ^ (row & 7)) << 4)) = up ? lo : hi;
+            }
+            // what is rare: large scales, codes and scales of NaN
+            if (large || __any_sync(FULL_MASK, nans != 0)) {
+#pragma unroll 1
+              for (int i = 0; i < kPer; ++i) {
+                const int row = row0 + i * kStep;
+                const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * kPut);
+                const uint32_t c0 = __shfl_sync(FULL_MASK, sc0, (lane & ~(L - 1)) + i);
+                const uint32_t f = first_factor(c0), f2 = second_factor(c0);
+                uint32_t cw[4] = {w.x, w.y, w.z, w.w}, y[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
-                if ((w[e] & top) == top) w[e] &= 0xffff0000u, odd = true;
-                if ((w[e] >> 16 & top) == top) w[e] &= 0x0000ffffu, odd = true;
-              }
-              if (odd) {
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-                c->odd[odd_at & 3] = item + 1;
+                for (int e = 0; e < 4; ++e) {
+                  uint2 z = codes_to_bf16(cw[e], f);
+                  z = with_nans(make_uint2(mul_bf16x2(z.x, f2), mul_bf16x2(z.y, f2)), code_nan(cw[e]));
+                  y[2 * e] = z.x, y[2 * e + 1] = z.y;
+                }
+                uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+                if ((part >> (row / 16) & 1u) && (not_finite<true>(lo) || not_finite<true>(hi))) {
+                  drop_not_finite<true>(lo);
+                  drop_not_finite<true>(hi);
+                  odd = true;
+                }
+                const int ch = (pc % 4) * 2, up = pc / 4;
+                unsigned char *const to = buf + up * 16384 + row * 128;
+                *reinterpret_cast<uint4 *>(to + ((ch ^ (row & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4 *>(to + (((ch + 1) ^ (row & 7)) << 4)) = hi;
               }
             }
           }
-        } else {
-          uint32_t w[kPer][4];
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
-                         : "r"(buf + put0 + i * kPut)
-                         : "memory");
-          c->factor[it & 1][pt] = scale_bf16x2(sc0);
-          asm volatile("bar.sync 1, 128;" ::: "memory");  // every code has been read, every scale is there
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int row = row0 + i * kStep;
-            const uint32_t f = c->factor[it & 1][row];
-            uint32_t o[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint2 y = codes_to_bf16(w[i][e], f);
-              o[2 * e] = y.x;
-              o[2 * e + 1] = y.y;
-            }
-            if (part >> (row / 16) & 1u) {
-              bool odd = false;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if ((o[e] & 0x7f80u) == 0x7f80u) o[e] &= 0xffff0000u, odd = true;
-                if ((o[e] >> 16 & 0x7f80u) == 0x7f80u) o[e] &= 0x0000ffffu, odd = true;
-              }
-              if (odd) c->odd[odd_at & 3] = item + 1;
-            }
-            // the two 16-byte halves, the upper panel's lanes in the other
-            // order: eight lanes then cover all banks
-            const int ch = (pc % 4) * 2, up = pc / 4;
-            const uint32_t to = buf + up * 16384 + row * 128;
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((ch + up) ^ (row & 7)) << 4)),
-                         "r"(up ? o[4] : o[0]), "r"(up ? o[5] : o[1]), "r"(up ? o[6] : o[2]), "r"(up ? o[7] : o[3])
-                         : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((ch + 1 - up) ^ (row & 7)) << 4)),
-                         "r"(up ? o[0] : o[4]), "r"(up ? o[1] : o[5]), "r"(up ? o[2] : o[6]), "r"(up ? o[3] : o[7])
-                         : "memory");
-          }
+          if (odd) c->odd[worked % kItemSlots] = I.item + 1;
+          fence_async_smem();
+          if (!(it == 0 && (P.force_timeout == 1 || P.force_timeout == I.g + 2))) mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
         }
-        fence_async_smem();
-        if (!(it == 0 && (P.force_timeout == 1 || P.force_timeout == I.g + 2))) mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
         sc0 = sc1;
-        sc1 = issue(it + 2);  // after this one is handed over: its buffer may be a while in coming free
+        sc1 = issue(it + 2);  // after this turn's is handed over: its buffer may be a while in coming free
+        if (it == -1) {
+          cp_async_wait<2>();  // the queries
+          fence_async_smem();
+          mbar_arrive(&c->qfull[0]);
+          if (I.tiles > 1) mbar_arrive(&c->qfull[1]);
+        }
       }
       kb += I.nblk;
-      ++odd_at;
+      ++worked;
     }
     cp_async_wait_all();
   } else if (role == 3) {
@@ -391,8 +512,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
       };
       bool live = true;
       int kb = 0, nb[2] = {0, 0}, ni[2] = {0, 0};  // blocks in all; of each tile; items of each tile
-      for (int item = blockIdx.x; item < items && live; item += gridDim.x) {
-        const TileItem I(P, item, blocks);
+      for (int turn = 0; live; ++turn) {
+        const int slot = turn % kItemSlots;
+        live = wait_on(c, &c->ifull[slot], (turn / kItemSlots) & 1, limit);
+        if (!live) break;
+        const TileItem I = c->items[slot];
+        mbar_arrive(&c->ifree[slot]);
+        if (I.item < 0) break;
         if (I.nblk == 0) continue;
         for (int t = 0; t < I.tiles && live; ++t) {
           live = wait_on(c, &c->qfull[t], ni[t] & 1, limit);
@@ -400,6 +526,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
           if (!live) break;
           tc_fence_after();
           scores(t, kb);
+          if (I.nblk == 1) tc_commit(&c->qfree[t]);
         }
         if (live) tc_commit(&c->kfree[kb & 1]);
         for (int k = 0; k < I.nblk && live; ++k) {
@@ -417,6 +544,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
               if (!live) break;
               tc_fence_after();
               scores(t, at + 1);
+              if (k + 2 == I.nblk) tc_commit(&c->qfree[t]);  // the tile's last scores
             } else {
               tc_commit(&c->done[t]);
             }
@@ -433,6 +561,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
         tc_commit(&c->drain);
         mbar_wait_bounded(&c->drain, 0, limit);
       }
+    } else if (warp == kItemWarp) {
+      // ------------------------------------------------------------- items
+      if (lane == 0) {
+        bool live = true;
+        for (int turn = 0, item = blockIdx.x; live; ++turn, item += gridDim.x) {
+          const int slot = turn % kItemSlots;
+          TileItem I;
+          if (item < items)
+            I = make_item(P, item, blocks);
+          else
+            I.item = -1;
+          if (turn >= kItemSlots) live = wait_on(c, &c->ifree[slot], (turn / kItemSlots - 1) & 1, limit);
+          if (!live) break;
+          c->items[slot] = I;
+          mbar_arrive(&c->ifull[slot]);
+          if (item >= items) break;
+        }
+      }
     }
   } else {
     // --------------------------------------------------------------- softmax
@@ -442,73 +588,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp & 3) << 21);
     const uint32_t s_addr = lane_addr + tile * 128, o_addr = lane_addr + 256 + tile * 128;
     const float sc = fmaxf(fabsf(P.scale), 1e-37f);  // not zero: a key that is not seen has the score -inf
-    bool live = true;
-    int nb = 0, ni = 0, odd_at = 0;
+    const bool minus = P.scale < 0.f, sectors = reinterpret_cast<uintptr_t>(P.out) % 32 == 0;
+    bool live = true, checked = false;
+    int nb = 0, ni = 0, worked = 0;  // the tile's blocks and items; items with keys
     if (tree) grid_dependency_wait();
-
-    // Queries of the tile's rows into shared memory: DP / 8 lanes per row, 16 bytes
-    // each.  A negative scale turns their sign.
-    auto load_queries = [&](const TileItem &I) {
-      const int r = I.r0 + rr;
-      long long off = -1;
-      if (r < P.N * P.G) {
-        const int t = r / P.G, h = I.g * P.G + (r - t * P.G);
-        off = I.b * P.qs[0] + t * P.qs[1] + h * P.qs[2];
+    for (int turn = 0;; ++turn) {
+      TileItem I;
+      if (live) live = take_item(c, turn, I, limit);
+      if (!live) {  // what is left is empty, too
+        const int item = blockIdx.x + turn * gridDim.x;
+        if (item >= items) break;
+        I = make_item(P, item, blocks);
       }
-      c->qoff[rr][0] = static_cast<int>(off);
-      c->qoff[rr][1] = static_cast<int>(off >> 32);
-      if (tile == 0)
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-      else
-        asm volatile("bar.sync 3, 128;" ::: "memory");
-      constexpr int L = DP / 8, kBatch = L, kStep = 128 / L;
-      const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
-      const int pc = wt % L, rr0 = wt / L;
-      uint4 u[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int row = tile * 128 + rr0 + i * kStep;
-        const long long o = static_cast<long long>(static_cast<uint32_t>(c->qoff[row][0])) | static_cast<long long>(c->qoff[row][1]) << 32;
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (o >= 0 && pc * 8 < P.D) {
-          const unsigned short *q = static_cast<const unsigned short *>(P.q) + o + pc * 8;
-          if (vec) {
-            u[i] = __ldg(reinterpret_cast<const uint4 *>(q));
-          } else {
-            u[i].x = q[0] | static_cast<uint32_t>(q[1]) << 16;
-            u[i].y = q[2] | static_cast<uint32_t>(q[3]) << 16;
-            u[i].z = q[4] | static_cast<uint32_t>(q[5]) << 16;
-            u[i].w = q[6] | static_cast<uint32_t>(q[7]) << 16;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int row = rr0 + i * kStep;
-        if (P.scale < 0.f) u[i].x ^= 0x80008000u, u[i].y ^= 0x80008000u, u[i].z ^= 0x80008000u, u[i].w ^= 0x80008000u;
-        *reinterpret_cast<uint4 *>(smem + C::kQ + tile * C::kOp + (pc / 8) * 16384 + row * 128 + (((pc % 8) ^ (row & 7)) << 4)) = u[i];
-      }
-      fence_async_smem();
-      mbar_arrive(&c->qfull[tile]);
-    };
-    // the tile's next item with work, from `item` on
-    auto next_item = [&](int item) {
-      for (; item < items; item += gridDim.x) {
-        const TileItem I(P, item, blocks);
-        if (I.nblk > 0 && tile < I.tiles) break;
-      }
-      return item;
-    };
-    {
-      const int item = next_item(blockIdx.x);
-      if (item < items) load_queries(TileItem(P, item, blocks));
-    }
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-      const TileItem I(P, item, blocks);
-      if (tile >= I.tiles) {
-        if (I.nblk > 0) ++odd_at;
-        continue;
-      }
+      if (I.item < 0) break;
+      const int slot = worked % kItemSlots;
+      worked += I.nblk > 0;
+      if (tile >= I.tiles) continue;
       const int r = I.r0 + rr;
       int at = -1, my = 0;  // the thread's output row (-1: past the last) and token
       if (r < P.N * P.G) {
@@ -529,9 +624,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
         if (P.lse) P.lse[at] = -INFINITY;
         if (timeout && P.row_status) P.row_status[I.b] = SPEC_ROW_TIMEOUT;
       };
-      if (I.nblk == 0) {
+      if (I.nblk == 0 || !live) {
         if (wt == 0 && tile == 0 && P.splits > 1) P.oflag[flag] = 0;
-        empty(false);
+        if (!checked) grid_dependency_wait();  // the status may not come before the check's
+        checked = true;
+        empty(I.nblk > 0);
         continue;
       }
       const bool mine = use && (!tree || P.rowinfo[I.b] >= 0);
@@ -539,31 +636,45 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
       const int from = window_from(P, p);
       const uint32_t *const anc = tree ? P.anc + (static_cast<size_t>(I.b) * P.N + my) * P.W : nullptr;
       const Keys keys(P, I.p0, I.end);
-      // the tile's own positions
-      const int q_first = (I.r0 + tile * 128) / P.G, q_last = min((I.r0 + tile * 128 + 127) / P.G, P.N - 1);
+      // the warp's own positions
+      const int r_first = I.r0 + (rr & ~31), q_first = min(r_first / P.G, P.N - 1), q_last = min((r_first + 31) / P.G, P.N - 1);
       const int p0 = tree ? I.p0 : I.n + q_first, p1 = tree ? I.p1 : I.n + q_last;
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < I.nblk; ++k) {
-        if (live) live = wait_on(c, &c->sfull[tile], (nb + k) & 1, limit);
-        live = __all_sync(FULL_MASK, live);
+        live = __all_sync(FULL_MASK, wait_on(c, &c->sfull[tile], (nb + k) & 1, limit));
         if (!live) break;
         tc_fence_after();
-        unsigned part = 0;  // groups of the block that some query of the tile does not see whole
+        // Groups of the block that some query of the warp does not see whole: what is
+        // not seen gets the score -inf, in tensor memory and ahead of the rest, so
+        // that this code, which most blocks pass by, stays out of the loop's way (the
+        // roles' loops together just fit the instruction cache).
+        unsigned part;
         {
           const int gi = I.g0 + k * kBlkGroups + (lane & 7);
           part = __ballot_sync(FULL_MASK, gi >= I.g1 || group_masked(P, keys.token(gi), I.n, p0, p1)) & 0xffu;
         }
-        auto hide = [&](uint32_t (&x)[32], int q) {  // columns 32 q on: groups 2 q and 2 q + 1
-          if (part >> (2 * q) & 3u) {
-            const int gi = I.g0 + k * kBlkGroups + 2 * q;
-            const uint32_t lo = gi < I.g1 ? group_seen(P, keys.token(gi), p, from, I.n, I.end, anc) : 0u;
-            const uint32_t hi = gi + 1 < I.g1 ? group_seen(P, keys.token(gi + 1), p, from, I.n, I.end, anc) : 0u;
-            const uint32_t bits = lo | hi << 16;
+        if (part || minus) {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q, part >>= 2) {
+            uint32_t bits = 0xffffffffu;
+            if (part & 3u) {
+              bits = 0;
+#pragma unroll 1
+              for (int j = 0; j < 2; ++j) {
+                const int gi = I.g0 + k * kBlkGroups + 2 * q + j;
+                if (gi < I.g1) bits |= group_seen(P, keys.token(gi), p, from, I.n, I.end, anc) << (16 * j);
+              }
+            }
+            if (__all_sync(FULL_MASK, bits == 0xffffffffu) && !minus) continue;
+            uint32_t x[32];
+            tc_ld32(x, s_addr + q * 32);
+            tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(bits >> j & 1)) x[j] = 0xff800000u;
+            for (int j = 0; j < 32; ++j) x[j] = bits >> j & 1 ? minus ? x[j] ^ 0x80000000u : x[j] : 0xff800000u;
+            tc_st32(s_addr + q * 32, x);
           }
-        };
+          tc_wait_st();
+        }
         auto largest = [](const uint32_t (&x)[32]) {
           float y = __uint_as_float(x[0]), z = __uint_as_float(x[1]);
 #pragma unroll
@@ -582,15 +693,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
         tc_ld32(s[0], s_addr + 64);
         tc_ld32(s[1], s_addr + 96);
         tc_wait_ld();
-        hide(s[0], 2);
-        hide(s[1], 3);
         mq[2] = largest(s[0]);
         mq[3] = largest(s[1]);
         tc_ld32(s[0], s_addr);
         tc_ld32(s[1], s_addr + 32);
         tc_wait_ld();
-        hide(s[0], 0);
-        hide(s[1], 1);
         mq[0] = largest(s[0]);
         mq[1] = largest(s[1]);
         const float mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sc;
@@ -600,7 +707,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
           m = mt;
         }
         if (k > 0 && __any_sync(FULL_MASK, al != 1.f)) {
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < DP / 32; ++q) {
             uint32_t o[32];
             tc_ld32(o, o_addr + q * 32);
@@ -629,10 +736,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
         weights(s[1], 1);
         tc_wait_ld();
         tc_ld32(s[1], s_addr + 96);
-        hide(s[0], 2);
         weights(s[0], 2);
         tc_wait_ld();
-        hide(s[1], 3);
         weights(s[1], 3);
         l = fmaf(l, al, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
         tc_wait_st();
@@ -640,72 +745,68 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
         mbar_arrive(&c->pfull[tile]);
       }
       nb += I.nblk;
-      // the next queries may come: this item's scores are all taken
-      if (live) {
-        const int next = next_item(item + gridDim.x);
-        if (next < items) load_queries(TileItem(P, next, blocks));
-      }
-      if (live) live = wait_on(c, &c->done[tile], ni & 1, limit);
-      live = __all_sync(FULL_MASK, live);
+      if (!checked) grid_dependency_wait();  // the row's check
+      checked = true;
+      const bool some = use && P.rowinfo[I.b] >= 0 && l != 0.f;
+      const float z = some ? m + log2f(l) : -INFINITY;
+      if (live) live = __all_sync(FULL_MASK, wait_on(c, &c->done[tile], ni & 1, limit));
       ++ni;
-      grid_dependency_wait();  // the row's check
       if (!live) {
         empty(true);
         if (wt == 0 && tile == 0 && P.splits > 1) P.oflag[flag] = 0;
-        ++odd_at;
         continue;
       }
       tc_fence_after();
-      const bool odd = *reinterpret_cast<volatile int *>(&c->odd[odd_at & 3]) == item + 1;
-      const bool some = use && P.rowinfo[I.b] >= 0 && l != 0.f;
-      const float z = some ? m + log2f(l) : -INFINITY;
-      if (P.splits > 1) {
+      const bool odd = *reinterpret_cast<volatile int *>(&c->odd[slot]) == I.item + 1;
+      const bool split = P.splits > 1;
+      const float w = split ? 1.f : some ? ex2(m - z) : 0.f;
+      float *const to = P.part + ml_at * P.D;
+      if (split) {
         if (wt == 0 && tile == 0) P.oflag[flag] = odd;
         if (at >= 0) P.ml[ml_at] = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
-        float *const to = P.part + ml_at * P.D;
+      } else if (at >= 0 && P.lse) {
+        P.lse[at] = kLn2 * z;
+      }
+#pragma unroll 1
+      for (int q = 0; q < DP / 32; ++q) {
+        uint32_t o[32];
+        __syncwarp();
+        tc_ld32(o, o_addr + q * 32);
+        tc_wait_ld();
+        if (q == DP / 32 - 1) {  // the sums are all read
+          tc_fence_before();
+          mbar_arrive(&c->ofree[tile]);
+        }
 #pragma unroll
-        for (int q = 0; q < DP / 32; ++q) {
-          uint32_t o[32];
-          __syncwarp();
-          tc_ld32(o, o_addr + q * 32);
-          tc_wait_ld();
-          if (some) {
+        for (int j = 0; j < 32; j += 16) {  // head sizes are multiples of 16: whole sectors
+          if (q * 32 + j >= P.D) continue;
+          if (split) {
+            if (some) {
+              st_global_v8(to + q * 32 + j, o + j);
+              st_global_v8(to + q * 32 + j + 8, o + j + 8);
+            }
+          } else if (at >= 0) {
+            uint32_t y[8];
 #pragma unroll
-            for (int j = 0; j < 32; j += 8)
-              if (q * 32 + j < P.D) st_global_v8(to + q * 32 + j, o + j);
+            for (int e = 0; e < 8; ++e)
+              y[e] = some ? pack16<BF>(__uint_as_float(o[j + 2 * e]) * w, __uint_as_float(o[j + 2 * e + 1]) * w) : 0u;
+            if (sectors) {
+              st_global_v8(reinterpret_cast<float *>(answer + q * 32 + j), y);
+            } else {
+              *reinterpret_cast<uint4 *>(answer + q * 32 + j) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4 *>(answer + q * 32 + j + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
           }
         }
-      } else {
-        const float w = some ? ex2(m - z) : 0.f;
-        if (at >= 0 && P.lse) P.lse[at] = kLn2 * z;
-#pragma unroll
-        for (int q = 0; q < DP / 32; ++q) {
-          uint32_t o[32];
-          __syncwarp();
-          tc_ld32(o, o_addr + q * 32);
-          tc_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = some ? __float_as_uint(__uint_as_float(o[j]) * w) : 0u;
-          if (some && odd)
-            for (int j = 0; j < 32 && q * 32 + j < P.D; ++j) {
-              const float y = paged_odd_sum<CT>(P, I.b, my, I.cnt, I.n, p, I.g, q * 32 + j);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (e == j) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
-            }
-#pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            if (at >= 0 && q * 32 + j < P.D) {
-              uint32_t y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = pack16<BF>(__uint_as_float(o[j + 2 * e]), __uint_as_float(o[j + 2 * e + 1]));
-              *reinterpret_cast<uint4 *>(answer + q * 32 + j) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
+      }
+      if (odd && some && !split) {
+        using T = typename CacheType<BF ? SPEC_BF16 : SPEC_F16>::type;
+#pragma unroll 1
+        for (int d = 0; d < P.D; ++d) {
+          T *const y = reinterpret_cast<T *>(answer) + d;
+          *y = T(static_cast<float>(*y) + paged_odd_sum<CT>(P, I.b, my, I.cnt, I.n, p, I.g, d));
         }
       }
-      tc_fence_before();
-      mbar_arrive(&c->ofree[tile]);
-      ++odd_at;
     }
   }
   __syncthreads();
@@ -723,10 +824,12 @@ cudaError_t launch(const PagedParams &p, cudaStream_t s) {
   const int blocks = (p.N * p.G + 255) / 256;
   const long long items = static_cast<long long>(p.B) * p.H * blocks * p.splits;
   if (items > 0x7fffffffLL - 4096) return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<paged_tile_kernel<CT, DP>>(C::kSmem, kLaunchRegs);
+  constexpr int smem = C::smem(CT == SPEC_E4M3);
+  static_assert(smem <= 227 * 1024, "shared memory of a block");
+  const cudaError_t e = allow_smem<paged_tile_kernel<CT, DP>>(smem, kLaunchRegs);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(items < kPagedSms ? items : kPagedSms);
-  return launch_after(paged_tile_kernel<CT, DP>, dim3(grid), kTileThreads, C::kSmem, s, true, p, blocks, static_cast<int>(items));
+  return launch_after(paged_tile_kernel<CT, DP>, dim3(grid), kTileThreads, smem, s, true, p, blocks, static_cast<int>(items));
 }
 
 template <int CT>
