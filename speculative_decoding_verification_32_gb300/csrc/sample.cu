@@ -14,10 +14,12 @@
 // are integers (w 2^44, at most 2^18 of them): they do not depend on the order in
 // which they are made.  The floors are found among few candidates: a bound
 // below the floor that is cheap (the k-th largest of the threads' own maxima;
-// for top-p a histogram of the weights by their leading bits) leaves about as
-// many logits as the law keeps.  These meet in the first CTA, in vocabulary
-// order, where the floors are searched bit by bit.  Where more are left than it
-// can list, all CTAs search together.
+// for top-p six octaves below the largest weight, where these hold enough mass,
+// else a histogram of the weights by their leading bits) leaves not many more
+// logits than the law keeps.  These meet in the first CTA, in vocabulary order,
+// where a short list's members are held against each other and a longer one's
+// floors searched bit by bit.  Where more are left than it can list, all CTAs
+// search together.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -35,7 +37,9 @@ constexpr int kSmThreads = 256;
 constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmMaxCluster = 8;
 constexpr int kSmBatch = 8;       // 16-byte loads of a thread in flight
-constexpr int kSmCands = 2048;    // candidates the first CTA lists, an equal share of them from each CTA
+constexpr int kSmCands = 1024;    // candidates the first CTA lists, an equal share of them from each CTA
+constexpr int kSmPairs = 128;     // ... up to so many are held against each other
+constexpr float kSmNear = 6.f;    // octaves
 constexpr int kSmPer = kSmCands / kSmThreads;
 constexpr int kSmBins = 512;      // weights 1 down to 2^-64, eight bins an octave
 constexpr float kSmFix = 0x1p44f; // a weight of 1 as an integer
@@ -85,11 +89,17 @@ struct SampleShared {
   u64 warp[2][kSmWarps];            // this CTA's warps, two rounds in turn
   u64 warp2[2][kSmWarps];
   uint32_t tmax[kSmThreads];        // threads' largest keys, of the whole cluster
-  u64 hist[kSmBins];                // first CTA: the cluster's
-  uint32_t mine[kSmBins];           // this CTA's
   uint32_t cnt[kSmMaxCluster];      // candidates of each CTA
+  uint32_t min_p_key;
   float floor;                      // what top-p's histogram says
-  u64 cand[kSmCands];               // first CTA: key << 32 | token
+  union {
+    struct {
+      u64 hist[kSmBins];            // first CTA: the cluster's
+      uint32_t mine[kSmBins];       // this CTA's
+    };
+    u64 cand[kSmCands];             // first CTA: key << 32 | token
+  };
+  u64 mass[kSmPairs];               // first CTA: a short list's weights
 };
 
 // Warp sum of 64-bit integers.
@@ -98,22 +108,52 @@ __device__ __forceinline__ i64 warp_sum64(i64 v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
   return v;
 }
+__device__ __forceinline__ i64 warp_scan64(i64 v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const i64 y = __shfl_up_sync(FULL_MASK, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// floor(f n) and ceil(f n) for 0 <= f < 1 and n >= 0, exactly (fp64 runs at a
+// sixty-fourth of fp32's rate here, and the whole CTA would compute it).
+__device__ __forceinline__ i64 fraction_of(float f, i64 n, bool up) {
+  const uint32_t b = __float_as_uint(f);
+  const uint32_t e = b >> 23;
+  const u64 m = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const int s = 150 - static_cast<int>(e ? e : 1u);  // f = m 2^-s, s >= 24
+  const u64 lo = m * static_cast<u64>(n), hi = __umul64hi(m, static_cast<u64>(n));
+  u64 r, rest;
+  if (s >= 128) {
+    r = 0, rest = lo | hi;
+  } else if (s >= 64) {
+    r = s == 64 ? hi : hi >> (s - 64);
+    rest = lo | (s == 64 ? 0 : hi << (128 - s));
+  } else {
+    r = hi << (64 - s) | lo >> s;
+    rest = lo << (64 - s);
+  }
+  return static_cast<i64>(r + (up && rest ? 1 : 0));
+}
 
 // The weights of a row: w(l) = 2^((l - M) log2(e) / T).  The exponent is kept to
 // more than fp32's 24 bits (its rounding, times 20 or so, would show in the sums):
-// what the difference, the factor and the product lose goes in to first order.
+// what the factor and the product lose goes in to first order, and for fp32
+// logits what the difference loses (bf16 logits of like size have an exact one).
+template <bool BF16>
 struct Weight {
-  float M, sc, sc_lo;
+  float M, sc, sc_lo, least;  // least: differences below it have weight zero
+  bool far;                   // a temperature at which only -inf has (least is -inf)
   __device__ __forceinline__ float operator()(float l) const {
-    const float x = fmaxf(l, -3e38f);
-    const float t = x - M;
-    const float lost = x - (t + M);  // what the difference lost, where that counts
-    const float y = fmaxf(t * sc, -200.f);
-    float r = fmaf(t, sc, -y);
-    r = fmaf(t, sc_lo, fmaf(lost, sc, r));
+    const float d = l - M, t = fmaxf(d, far ? -3e38f : least);
+    const float y = t * sc;
+    float r = fmaf(t, sc_lo, fmaf(t, sc, -y));
+    if constexpr (!BF16) r = fmaf(d >= least ? l - (d + M) : 0.f, sc, r);
     const float w = ex2(y);
     const float c = fmaf(w, r * 0.693147180559945309f, w);
-    return w > 0.f && l > -INFINITY ? c : 0.f;
+    return far && l == -INFINITY ? 0.f : c;
   }
 };
 
@@ -123,9 +163,18 @@ __device__ __forceinline__ float element(const uint4 &q, int e) {
   if constexpr (BF16) return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
   return __uint_as_float(w[e]);
 }
+// The largest of a vector's logits; NaN if one is.
+template <bool BF16>
+__device__ __forceinline__ float vector_max(const uint4 &q) {
+  if constexpr (BF16) {
+    const uint32_t t = bf16x2_max_nan(bf16x2_max_nan(q.x, q.y), bf16x2_max_nan(q.z, q.w));
+    return fmax_nan(bf16_lo(t), bf16_hi(t));
+  }
+  return fmax_nan(fmax_nan(element<BF16>(q, 0), element<BF16>(q, 1)), fmax_nan(element<BF16>(q, 2), element<BF16>(q, 3)));
+}
 
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constant__ SampleParams P) {
+__global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_constant__ SampleParams P) {
   constexpr int E = BF16 ? 8 : 4;
   __shared__ SampleShared S;
   extern __shared__ __align__(16) unsigned char smp_raw[];
@@ -172,21 +221,25 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       const int v = i0 + i * 32;
       if (v < v1) {
         data[v] = q[i];
-        float c = element<BF16>(q[i], 0);
-#pragma unroll
-        for (int e = 1; e < E; ++e) c = fmax_nan(c, element<BF16>(q[i], e));
+        const float c = vector_max<BF16>(q[i]);
         if (!(c < INFINITY)) flags |= F_NONFINITE;  // NaN or +inf
         top = fmaxf(top, c);
       }
     }
   }
+  const float T = P.temperature ? __ldg(P.temperature + b) : 1.f, u = __ldg(P.u + b);
+  const int k_raw = P.top_k ? __ldg(P.top_k + b) : 0;
+  const int top_k = k_raw >= 1 && k_raw < P.V ? k_raw : 0;  // 0: off
+  const float top_p = P.top_p ? __ldg(P.top_p + b) : 1.f, min_p = P.min_p ? __ldg(P.min_p + b) : 0.f;
+  const bool use_p = top_p > 0.f && top_p < 1.f, use_m = min_p > 0.f && min_p <= 1.f;
+  double below = 0.0;  // T ln(min_p), in one thread
+  if (use_m && tid == kSmThreads - 1) below = static_cast<double>(T) * log(static_cast<double>(min_p));
   const uint32_t my_top = smp_key(top);
   {
     const uint32_t k = __reduce_max_sync(FULL_MASK, my_top);
     flags = __reduce_or_sync(FULL_MASK, flags);
     if (lane == 0) S.warp[0][warp] = static_cast<u64>(k) << 32 | flags;
   }
-  for (int i = tid; i < kSmBins; i += kSmThreads) S.hist[i] = S.mine[i] = 0;
   S.tmax[tid] = 0;
   __syncthreads();
   cluster_wait();
@@ -209,7 +262,6 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   }
   const float M = smp_from_key(top_key);
   // --- the row's numbers
-  const float T = P.temperature ? __ldg(P.temperature + b) : 1.f, u = __ldg(P.u + b);
   if (!(T > 0.f) || isinf(T)) flags |= F_BAD_TEMPERATURE;
   if (!(u >= 0.f && u < 1.f)) flags |= F_BAD_UNIFORM;
   if (M == -INFINITY && !(flags & F_NONFINITE)) flags |= F_EMPTY;
@@ -221,42 +273,41 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     }
     return;
   }
-  Weight weight;
-  weight.M = M;
+  Weight<BF16> weight;
   {
-    const double s = 1.4426950408889634074 / static_cast<double>(T);
-    weight.sc = fminf(static_cast<float>(s), kSmMostScale);
-    weight.sc_lo = weight.sc == kSmMostScale ? 0.f : static_cast<float>(s - static_cast<double>(weight.sc));
+    // log2(e) / T to twice fp32's precision
+    constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;
+    const float s = kHi / T;
+    weight.M = M;
+    weight.sc = fminf(s, kSmMostScale);
+    weight.sc_lo = s > kSmMostScale ? 0.f : (fmaf(-s, T, kHi) + kLo) / T;
+    weight.least = -190.f / weight.sc;
+    weight.far = weight.least == -INFINITY;
   }
-  const int k_raw = P.top_k ? __ldg(P.top_k + b) : 0;
-  const int top_k = k_raw >= 1 && k_raw < P.V ? k_raw : 0;  // 0: off
-  const float p_raw = P.top_p ? __ldg(P.top_p + b) : 1.f;
-  const bool use_p = p_raw > 0.f && p_raw < 1.f;
-  const double top_p = p_raw;
-  const float m_raw = P.min_p ? __ldg(P.min_p + b) : 0.f;
-  // min-p's floor: the least logit with l - M >= T ln(min_p)
-  uint32_t floor_key = kSmMinusInf;
-  if (m_raw > 0.f && m_raw <= 1.f) {
-    const double c = static_cast<double>(T) * log(static_cast<double>(m_raw));
-    const double at = static_cast<double>(M) + c;
-    uint32_t k = smp_key(at < -3.4028234e38 ? -3.4028234e38f : static_cast<float>(at));
-    while (static_cast<double>(smp_from_key(k)) - static_cast<double>(M) < c) ++k;
-    while (k > 0x00800000u && static_cast<double>(smp_from_key(k - 1)) - static_cast<double>(M) >= c) --k;
-    floor_key = k;
+  // min-p's floor: the least logit with l - M >= T ln(min_p), by the thread that has it
+  if (tid == kSmThreads - 1) {
+    uint32_t k = kSmMinusInf;
+    if (use_m) {
+      const double at = static_cast<double>(M) + below;
+      k = smp_key(at < -3.4028234e38 ? -3.4028234e38f : static_cast<float>(at));
+      while (static_cast<double>(smp_from_key(k)) - static_cast<double>(M) < below) ++k;
+      while (k > 0x00800000u && static_cast<double>(smp_from_key(k - 1)) - static_cast<double>(M) >= below) --k;
+    }
+    S.min_p_key = k;
   }
 
-  // this thread's sum over its vectors of the weights that reach `floor`, as integers
+  // a vector's sum of the weights that reach `floor`, as an integer
   auto vector_mass = [&](const uint4 &q, float floor) {
     float s = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float l = element<BF16>(q, e);
-      if (l >= floor) s += weight(l);
+      const float l = element<BF16>(q, e), w = weight(l);
+      s += l >= floor ? w : 0.f;
     }
     return __float2ll_rn(s * kSmFix);
   };
   int round = 1;  // of the exchange: buffers in turn
-  // sums over the cluster (two at a time), the same in every thread; `upto`: this CTA's warps' sums
+  // sums over the cluster (two at a time), the same in every thread
   auto exchange = [&](i64 a, i64 c, i64 &A, i64 &C) {
     const int r = round & 1;
     ++round;
@@ -264,10 +315,10 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     c = warp_sum64(c);
     if (lane == 0) S.warp[r][warp] = static_cast<u64>(a), S.warp2[r][warp] = static_cast<u64>(c);
     __syncthreads();
-    u64 x = 0, y = 0;
-#pragma unroll
-    for (int w = 0; w < kSmWarps; ++w) x += S.warp[r][w], y += S.warp2[r][w];
     if (tid < static_cast<int>(ranks)) {
+      u64 x = 0, y = 0;
+#pragma unroll
+      for (int w = 0; w < kSmWarps; ++w) x += S.warp[r][w], y += S.warp2[r][w];
       st_cluster_u64(&S.part[r][rank], tid, x);
       st_cluster_u64(&S.part2[r][rank], tid, y);
     }
@@ -283,40 +334,34 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     int n = 0;
     for (int v = v0 + lane; v < v1; v += 32) {
       const uint4 q = data[v];
+      if (!(vector_max<BF16>(q) >= floor)) continue;
       a += vector_mass(q, floor);
 #pragma unroll
       for (int e = 0; e < E; ++e) n += element<BF16>(q, e) >= floor;
     }
     return exchange(a, n, mass, count);
   };
-  // the token at u: all CTAs together, from the sums that exchange number r left
+  // the token at u: all CTAs together, from the sums that exchange number r left.
+  // A running sum of integers passes u Z where it passes floor(u Z).
   auto choose = [&](float floor, int r, i64 Z) {
-    const double target = static_cast<double>(u) * static_cast<double>(Z);
-    // the CTA: the first whose running sum passes the target, else the last with any mass
-    int owner = -1, backup = 0;
-    i64 before = 0, at = 0;
+    const i64 target = fraction_of(u, Z, false);  // less than Z, so it is passed
+    int owner = 0;
+    i64 before = 0;
     for (uint32_t k = 0; k < ranks; ++k) {
       const i64 x = static_cast<i64>(S.part[r][k]);
-      if (x > 0) backup = k;
-      if (owner < 0 && static_cast<double>(before + x) > target) owner = k, at = before;
+      if (before + x > target) break;
+      before += x;
+      ++owner;
+    }
+    if (owner != static_cast<int>(rank)) return;
+    int w = 0;
+    for (; w < kSmWarps; ++w) {
+      const i64 x = static_cast<i64>(S.warp[r][w]);
+      if (before + x > target) break;
       before += x;
     }
-    const bool rest = owner < 0;  // u Z was rounded up to Z
-    if (rest) owner = backup;
-    if (owner != static_cast<int>(rank)) return;
-    int w = -1, wb = 0;
-    i64 sum = at;
-    for (int k = 0; k < kSmWarps; ++k) {
-      const i64 x = static_cast<i64>(S.warp[r][k]);
-      if (x > 0) wb = k;
-      if (w < 0 && !rest && static_cast<double>(sum + x) > target) w = k, at = sum;
-      sum += x;
-    }
-    if (w < 0) w = wb;
     if (w != warp) return;
-    i64 run = at;
-    int found = -1, tail = -1;  // the last kept token as a fallback
-    for (int v = v0; v < v1 && found < 0; v += 32) {
+    for (int v = v0; v < v1; v += 32) {
       const int mine = v + lane;
       uint4 q = make_uint4(0, 0, 0, 0);
       i64 x = 0;
@@ -324,57 +369,67 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
         q = data[mine];
         x = vector_mass(q, floor);
       }
-      i64 inc = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const i64 y = __shfl_up_sync(FULL_MASK, inc, o);
-        if (lane >= o) inc += y;
+      const i64 inc = warp_scan64(x, lane);
+      const unsigned hit = __ballot_sync(FULL_MASK, before + inc > target);
+      if (!hit) {
+        before += __shfl_sync(FULL_MASK, inc, 31);
+        continue;
       }
-      const unsigned some = __ballot_sync(FULL_MASK, x > 0);
-      const unsigned hit = rest ? 0u : __ballot_sync(FULL_MASK, x > 0 && static_cast<double>(run + inc) > target);
-      const int who = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : -1;
-      int tok = -1;
-      if (who == lane) {
-        float s = 0.f;
+      if (lane == __ffs(hit) - 1) {  // its sums up to each element, as the vector's was made
+        float s = 0.f, prob = 0.f;
+        int tok = -1;
+        bool found = false;
+#pragma unroll
         for (int e = 0; e < E; ++e) {
           const float l = element<BF16>(q, e), y = l >= floor ? weight(l) : 0.f;
           s += y;
-          if (y > 0.f) tok = first + mine * E + e;
-          if (hit && y > 0.f && static_cast<double>(run + inc - x + __float2ll_rn(s * kSmFix)) > target) break;
+          if (!found && y > 0.f) {
+            tok = first + mine * E + e;
+            prob = y;
+            found = before + inc - x + __float2ll_rn(s * kSmFix) > target;
+          }
         }
+        P.token[b] = tok;
+        if (P.prob) P.prob[b] = prob * kSmFix / static_cast<float>(Z);
+        P.row_status[b] = 0;
       }
-      if (who >= 0) tok = __shfl_sync(FULL_MASK, tok, who);
-      if (hit) found = tok;
-      if (tok >= 0) tail = tok;
-      run += __shfl_sync(FULL_MASK, inc, 31);
-    }
-    if (found < 0) found = tail;
-    if (lane == 0) {
-      const int at_slice = found - first;
-      const uint4 q = data[at_slice / E];
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (e == at_slice % E) x = element<BF16>(q, e);
-      P.token[b] = found;
-      if (P.prob) P.prob[b] = static_cast<float>(static_cast<double>(weight(x)) * static_cast<double>(kSmFix) / static_cast<double>(Z));
-      P.row_status[b] = 0;
+      return;
     }
   };
 
-  // --- the whole row's mass; the threads' maxima for top-k's bound
+  // --- the whole row's mass; the threads' maxima for top-k's bound; for top-p
+  // the mass within kSmNear octaves of the largest weight
+  const bool near = use_p && !top_k;
   if (top_k)
     for (uint32_t k = 0; k < ranks; ++k) max_cluster_u32(&S.tmax[tid], k, my_top);
-  i64 Z, unused;
+  i64 Z, within;
+  const float near_floor = M - kSmNear / weight.sc;
   {
     i64 a = 0;
-    for (int v = v0 + lane; v < v1; v += 32) a += vector_mass(data[v], -INFINITY);
-    const int r = exchange(a, 0, Z, unused);
-    if (!top_k && !use_p && floor_key == kSmMinusInf) {
+    float c = 0.f;
+    if (near) {
+      for (int v = v0 + lane; v < v1; v += 32) {
+        const uint4 q = data[v];
+        a += vector_mass(q, -INFINITY);
+        if (vector_max<BF16>(q) >= near_floor) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float l = element<BF16>(q, e);
+            if (l >= near_floor) c += ex2((l - M) * weight.sc);
+          }
+        }
+      }
+    } else {
+      for (int v = v0 + lane; v < v1; v += 32) a += vector_mass(data[v], -INFINITY);
+    }
+    // (the second sum is a bound: cut by more than its rounding)
+    const int r = exchange(a, __float2ll_rn(c * (kSmFix * (1.f - 0x1p-14f))), Z, within);
+    if (!top_k && !use_p && !use_m) {
       choose(-INFINITY, r, Z);
       return;
     }
   }
+  const uint32_t floor_key = S.min_p_key;
   // --- a bound that the law's floor does not lie below (where top-p goes by the
   // mass that top-k leaves, what reaches top-k's floor has to be listed whole)
   uint32_t bound = top_k && use_p ? kSmMinusInf : floor_key;
@@ -388,64 +443,78 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     }
     bound = max(bound, t << 16);
   }
-  if (use_p && !top_k) {
-    // What is dropped weighs less than (1 - top_p) Z, so a token of less than a
-    // V-th of that cannot be the last one kept: such tokens are not looked at.
-    const float least = static_cast<float>((1.0 - top_p) * static_cast<double>(Z) / static_cast<double>(kSmFix) / P.V);
-    const float far = M + (log2f(fmaxf(least, 1e-37f)) - 0.01f) / weight.sc;
-    const float from = fmaxf(far, smp_from_key(bound));
-    // Bins by exponent and three more bits of the weight; each adds up the
-    // leading 16 bits of its weights, cut off: never too much.
-    for (int v = v0 + lane; v < v1; v += 32) {
-      const uint4 q = data[v];
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float l = element<BF16>(q, e);
-        if (l >= from) {
-          const uint32_t x = __float_as_uint(fminf(weight(l), 1.f));
-          const int bin = (127 << 3) - static_cast<int>(x >> 20);
-          if (bin < kSmBins) atomicAdd(&S.mine[bin], ((x & 0x7fffffu) | 0x800000u) >> 8);
-        }
-      }
-    }
-    __syncthreads();  // (a slice has at most 2^15 logits: its sums stay below 2^32)
-    for (int i = tid; i < kSmBins; i += kSmThreads)
-      if (S.mine[i]) add_cluster_u64(&S.hist[i], 0, S.mine[i]);
-    cluster_sync();
-    if (rank == 0 && warp == 0) {
-      // running sums from the largest weights down, in units of 1
-      double run = 0.0;
-      const double want = top_p * (static_cast<double>(Z) / static_cast<double>(kSmFix));
-      int at = kSmBins;
-      for (int i0 = 0; i0 < kSmBins && at == kSmBins; i0 += 32) {
-        const int i = i0 + lane;
-        // bin i holds weights of exponent 127 - ceil(i / 8)
-        double x = static_cast<double>(S.hist[i]) * exp2(-15.0 - static_cast<double>((i + 7) / 8));
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(FULL_MASK, x, o);
-          if (lane >= o) x += y;
-        }
-        const unsigned hit = __ballot_sync(FULL_MASK, run + x >= want);
-        if (hit) at = i0 + __ffs(hit) - 1;
-        run += __shfl_sync(FULL_MASK, x, 31);
-      }
-      // the bin's least weight, as a logit
-      const float edge = at < kSmBins ? M + (log2f(__uint_as_float(static_cast<uint32_t>((127 << 3) - at) << 20)) - 0.001f) / weight.sc : -INFINITY;
-      if (lane < static_cast<int>(ranks)) st_cluster_u32(&S.floor, lane, __float_as_uint(fmaxf(edge, from)));
-    }
-    cluster_sync();
-    bound = max(bound, smp_key(S.floor));
-  }
-  // --- the candidates, in vocabulary order
+  const i64 want = use_p ? fraction_of(top_p, Z, true) : 0;  // of the whole row's mass
+  bool binned = !near;
+  if (near && within >= want) bound = max(bound, smp_key(near_floor));  // else nothing is known yet
   const int share = kSmCands / static_cast<int>(ranks);
   int total = 0;
-  bool listed = true;
-  {
+  bool listed = false;
+  while (true) {
+    // --- where the law keeps much: what lies within octaves says little
+    if (!binned && (within < want || total > 0)) {
+      binned = true;
+      for (int i = tid; i < kSmBins; i += kSmThreads) S.hist[i] = 0, S.mine[i] = 0;
+      cluster_sync();
+      // What is dropped weighs less than (1 - top_p) Z, so a token of less than a
+      // V-th of that cannot be the last one kept: such tokens are not looked at.
+      const float least = (1.f - top_p) * 0.999f * (static_cast<float>(Z) / kSmFix) / P.V;
+      const float far = M + (log2f(fmaxf(least, 1e-37f)) - 0.01f) / weight.sc;
+      const float from = fmaxf(far, smp_from_key(bound));
+      // Bins by exponent and three more bits of the weight; each adds up the
+      // leading 16 bits of its weights, cut off: never too much.
+      for (int v = v0 + lane; v < v1; v += 32) {
+        const uint4 q = data[v];
+        if (!(vector_max<BF16>(q) >= from)) continue;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float l = element<BF16>(q, e);
+          if (l >= from) {
+            const uint32_t x = __float_as_uint(fminf(weight(l), 1.f));
+            const int bin = (127 << 3) - static_cast<int>(x >> 20);
+            if (bin < kSmBins) atomicAdd(&S.mine[bin], ((x & 0x7fffffu) | 0x800000u) >> 8);
+          }
+        }
+      }
+      __syncthreads();  // (a slice has at most 2^15 logits: its sums stay below 2^32)
+      for (int i = tid; i < kSmBins; i += kSmThreads)
+        if (S.mine[i]) add_cluster_u64(&S.hist[i], 0, S.mine[i]);
+      cluster_sync();
+      if (rank == 0) {
+        // running sums from the largest weights down, in the sums' unit; bin i
+        // holds weights of exponent -ceil(i / 8), 16 bits of each
+        const int i0 = 2 * tid;
+        i64 x[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int s = 44 - 15 - (i0 + j + 7) / 8;
+          x[j] = static_cast<i64>(s >= 0 ? S.hist[i0 + j] << s : -s < 64 ? S.hist[i0 + j] >> -s : 0);
+        }
+        const i64 inc = warp_scan64(x[0] + x[1], lane);
+        const int r = round & 1;
+        if (lane == 31) S.warp[r][warp] = static_cast<u64>(inc);
+        if (tid == 0) S.floor = from;
+        __syncthreads();
+        i64 run = inc - x[0] - x[1];
+        for (int w = 0; w < warp; ++w) run += static_cast<i64>(S.warp[r][w]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (run < want && run + x[j] >= want)  // one bin only: its least weight, as a logit
+            S.floor = fmaxf(from, M + (log2f(__uint_as_float(static_cast<uint32_t>((127 << 3) - i0 - j) << 20)) - 0.001f) / weight.sc);
+          run += x[j];
+        }
+        __syncthreads();
+        if (tid > 0 && tid < static_cast<int>(ranks)) st_cluster_u32(&S.floor, tid, __float_as_uint(S.floor));
+      }
+      ++round;
+      cluster_sync();
+      bound = max(bound, smp_key(S.floor));
+    }
+    // --- the candidates, in vocabulary order
     const float from = smp_from_key(bound);
     int n = 0;
     for (int v = v0 + lane; v < v1; v += 32) {
       const uint4 q = data[v];
+      if (!(vector_max<BF16>(q) >= from)) continue;
 #pragma unroll
       for (int e = 0; e < E; ++e) n += element<BF16>(q, e) >= from;
     }
@@ -469,8 +538,10 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
         int c = 0;
         if (mine < v1) {
           q = data[mine];
+          if (vector_max<BF16>(q) >= from) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) c += element<BF16>(q, e) >= from;
+            for (int e = 0; e < E; ++e) c += element<BF16>(q, e) >= from;
+          }
         }
         if (!__any_sync(FULL_MASK, c > 0)) continue;
         int inc = c;
@@ -491,19 +562,22 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       }
     }
     cluster_sync();
+    listed = true;
+    total = 0;
     for (uint32_t k = 0; k < ranks; ++k) {
       total += static_cast<int>(S.cnt[k]);
       listed = listed && static_cast<int>(S.cnt[k]) <= share;
     }
+    if (listed || binned) break;
+    cluster_sync();  // the histogram takes the candidates' place
   }
   constexpr int kLow = BF16 ? 16 : 0;  // a bf16 logit's key is its upper 16 bits
   if (!listed) {
     // --- too many: the floors by bisection, all CTAs together.  (In units of
     // 2^kLow; a key's lower bits are ones for negative numbers, so the unit's
     // first key reaches what the unit's logit does.)
-    i64 mass = 0, count = 0;
+    i64 mass = 0, count = 0, need = want;
     uint32_t floor = floor_key;
-    int r = 0;
     if (top_k) {
       uint32_t lo = bound >> kLow, hi = top_key >> kLow;
       while (lo < hi) {
@@ -514,52 +588,26 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       }
       floor = max(floor_key, lo << kLow);
       if (use_p) {
-        reach(lo << kLow, mass, count);
-        Z = mass;
+        reach(max(lo << kLow, kSmMinusInf), mass, count);
+        need = fraction_of(top_p, mass, true);
         bound = max(bound, lo << kLow);
       }
     }
     if (use_p) {
-      const double want = top_p * static_cast<double>(Z);
       uint32_t lo = bound >> kLow, hi = top_key >> kLow;
       while (lo < hi) {
         const uint32_t mid = lo + (hi - lo + 1) / 2;
         reach(mid << kLow, mass, count);
-        if (static_cast<double>(mass) >= want) lo = mid;
+        if (mass >= need) lo = mid;
         else hi = mid - 1;
       }
       floor = max(floor, lo << kLow);
     }
-    r = reach(floor, mass, count);
+    const int r = reach(floor, mass, count);
     choose(smp_from_key(floor), r, mass);
     return;
   }
   if (rank != 0) return;
-  // --- the first CTA: a thread takes neighbouring candidates
-  uint32_t key[kSmPer];
-  int id[kSmPer];
-  i64 w[kSmPer];
-  const int each = (total + kSmThreads - 1) / kSmThreads;  // at most kSmPer
-  uint32_t least = 0xffffffffu;
-  {
-    int seg = 0, skip = tid * each;
-    while (seg < static_cast<int>(ranks) && skip >= static_cast<int>(S.cnt[seg])) skip -= static_cast<int>(S.cnt[seg++]);
-#pragma unroll
-    for (int i = 0; i < kSmPer; ++i) {
-      key[i] = 0;
-      id[i] = -1;
-      w[i] = 0;
-      if (i < each && seg < static_cast<int>(ranks)) {
-        const u64 c = S.cand[seg * share + skip];
-        key[i] = static_cast<uint32_t>(c >> 32);
-        id[i] = static_cast<int>(static_cast<uint32_t>(c));
-        w[i] = __float2ll_rn(weight(smp_from_key(key[i])) * kSmFix);
-        least = min(least, key[i]);
-        ++skip;
-        while (seg < static_cast<int>(ranks) && skip >= static_cast<int>(S.cnt[seg])) skip = 0, ++seg;
-      }
-    }
-  }
   auto block_sum64 = [&](i64 a) {
     const int r = round & 1;
     ++round;
@@ -571,74 +619,102 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     for (int k = 0; k < kSmWarps; ++k) x += S.warp[r][k];
     return static_cast<i64>(x);
   };
-  auto block_count = [&](int a) {
-    const int r = round & 1;
-    ++round;
-    a = __reduce_add_sync(FULL_MASK, a);
-    if (lane == 0) S.warp[r][warp] = static_cast<u64>(a);
-    __syncthreads();
-    int x = 0;
+  // where this thread's first of `each` neighbouring candidates is
+  const int each = (total + kSmThreads - 1) / kSmThreads;  // at most kSmPer
+  int seg = 0, skip = tid * each;
+  while (seg < static_cast<int>(ranks) && skip >= static_cast<int>(S.cnt[seg])) skip -= static_cast<int>(S.cnt[seg++]);
+  uint32_t key[kSmPer];
+  int id[kSmPer];
+  i64 w[kSmPer];
 #pragma unroll
-    for (int k = 0; k < kSmWarps; ++k) x += static_cast<int>(S.warp[r][k]);
-    return x;
-  };
+  for (int i = 0; i < kSmPer; ++i) {
+    key[i] = 0;
+    id[i] = -1;
+    w[i] = 0;
+    if (i < each && seg < static_cast<int>(ranks)) {
+      const u64 c = S.cand[seg * share + skip];
+      key[i] = static_cast<uint32_t>(c >> 32);
+      id[i] = static_cast<int>(static_cast<uint32_t>(c));
+      w[i] = __float2ll_rn(weight(smp_from_key(key[i])) * kSmFix);
+      ++skip;
+      while (seg < static_cast<int>(ranks) && skip >= static_cast<int>(S.cnt[seg])) skip = 0, ++seg;
+    }
+  }
   uint32_t floor = floor_key;
-  {
-    const int r = round & 1;
-    ++round;
-    least = __reduce_min_sync(FULL_MASK, least);
-    if (lane == 0) S.warp[r][warp] = least;
+  if (total <= kSmPairs) {
+    // --- few: each thread holds its candidate (each = 1) against all of them
+    if (tid < total) S.mass[tid] = static_cast<u64>(w[0]), S.tmax[tid] = key[0];
     __syncthreads();
+    i64 above = 0;
+    int larger = 0;
+    if (tid < total)
+      for (int j = 0; j < total; ++j) {
+        const bool gt = S.tmax[j] > key[0];
+        larger += gt;
+        above += gt ? static_cast<i64>(S.mass[j]) : 0;
+      }
+    bool keep = tid < total && key[0] >= floor && (!top_k || larger < top_k);
+    i64 need = want;
+    if (top_k && use_p) need = fraction_of(top_p, block_sum64(tid < total && larger < top_k ? w[0] : 0), true);
+    if (use_p) keep = keep && above < need;
+    if (!keep) w[0] = 0;
+  } else {
+    uint32_t least = 0xffffffffu;
 #pragma unroll
-    for (int k = 0; k < kSmWarps; ++k) least = min(least, static_cast<uint32_t>(S.warp[r][k]));
-  }
-  if (top_k) {
-    uint32_t lo = least >> kLow, hi = top_key >> kLow;
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo + 1) / 2;
-      int n = 0;
+    for (int i = 0; i < kSmPer; ++i)
+      if (id[i] >= 0) least = min(least, key[i]);
+    {
+      const int r = round & 1;
+      ++round;
+      least = __reduce_min_sync(FULL_MASK, least);
+      if (lane == 0) S.warp[r][warp] = least;
+      __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kSmPer; ++i) n += id[i] >= 0 && key[i] >= mid << kLow;
-      if (block_count(n) >= top_k) lo = mid;
-      else hi = mid - 1;
+      for (int k = 0; k < kSmWarps; ++k) least = min(least, static_cast<uint32_t>(S.warp[r][k]));
     }
-    floor = max(floor, lo << kLow);
+    i64 need = want;
+    if (top_k) {
+      uint32_t lo = least >> kLow, hi = top_key >> kLow;
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kSmPer; ++i) n += id[i] >= 0 && key[i] >= mid << kLow;
+        if (block_sum64(n) >= top_k) lo = mid;
+        else hi = mid - 1;
+      }
+      floor = max(floor, lo << kLow);
+      if (use_p) {
+        i64 a = 0;
+#pragma unroll
+        for (int i = 0; i < kSmPer; ++i)
+          if (key[i] >= lo << kLow) a += w[i];
+        need = fraction_of(top_p, block_sum64(a), true);
+        least = max(least, lo << kLow);
+      }
+    }
     if (use_p) {
-      i64 a = 0;
+      uint32_t lo = least >> kLow, hi = top_key >> kLow;
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        i64 a = 0;
 #pragma unroll
-      for (int i = 0; i < kSmPer; ++i)
-        if (key[i] >= lo << kLow) a += w[i];
-      Z = block_sum64(a);
-      least = max(least, lo << kLow);
+        for (int i = 0; i < kSmPer; ++i)
+          if (key[i] >= mid << kLow) a += w[i];
+        if (block_sum64(a) >= need) lo = mid;
+        else hi = mid - 1;
+      }
+      floor = max(floor, lo << kLow);
     }
-  }
-  if (use_p) {
-    const double want = top_p * static_cast<double>(Z);
-    uint32_t lo = least >> kLow, hi = top_key >> kLow;
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo + 1) / 2;
-      i64 a = 0;
 #pragma unroll
-      for (int i = 0; i < kSmPer; ++i)
-        if (key[i] >= mid << kLow) a += w[i];
-      if (static_cast<double>(block_sum64(a)) >= want) lo = mid;
-      else hi = mid - 1;
-    }
-    floor = max(floor, lo << kLow);
+    for (int i = 0; i < kSmPer; ++i)
+      if (key[i] < floor) w[i] = 0;
   }
   // --- running sums in vocabulary order
   i64 mine = 0;
 #pragma unroll
-  for (int i = 0; i < kSmPer; ++i) {
-    if (id[i] < 0 || key[i] < floor) w[i] = 0;
-    mine += w[i];
-  }
-  i64 inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const i64 y = __shfl_up_sync(FULL_MASK, inc, o);
-    if (lane >= o) inc += y;
-  }
+  for (int i = 0; i < kSmPer; ++i) mine += w[i];
+  const i64 inc = warp_scan64(mine, lane);
   const int r = round & 1;
   if (lane == 31) S.warp[r][warp] = static_cast<u64>(inc);
   __syncthreads();
@@ -649,19 +725,15 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     if (k < warp) run += x;
     all += x;
   }
-  const double target = static_cast<double>(u) * static_cast<double>(all);
+  const i64 target = fraction_of(u, all, false);
 #pragma unroll
   for (int i = 0; i < kSmPer; ++i) {
-    const i64 to = run + w[i];
-    // the first that passes the target; where rounding took u Z to Z, the last with any mass
-    const bool hit = w[i] > 0 && static_cast<double>(run) <= target && static_cast<double>(to) > target;
-    const bool end = w[i] > 0 && to == all && static_cast<double>(all) <= target;
-    if (hit || end) {
+    if (run <= target && run + w[i] > target) {
       P.token[b] = id[i];
-      if (P.prob) P.prob[b] = static_cast<float>(static_cast<double>(w[i]) / static_cast<double>(all));
+      if (P.prob) P.prob[b] = static_cast<float>(w[i]) / static_cast<float>(all);
       P.row_status[b] = 0;
     }
-    run = to;
+    run += w[i];
   }
 }
 
