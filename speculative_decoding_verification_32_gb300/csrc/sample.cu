@@ -14,12 +14,13 @@
 // are integers (w 2^44, at most 2^18 of them): they do not depend on the order in
 // which they are made.  The floors are found among few candidates: a bound
 // below the floor that is cheap (the k-th largest of the threads' own maxima;
-// for top-p six octaves below the largest weight, where these hold enough mass,
-// else a histogram of the weights by their leading bits) leaves not many more
-// logits than the law keeps.  These meet in the first CTA, in vocabulary order,
-// where a short list's members are held against each other and a longer one's
-// floors searched bit by bit.  Where more are left than it can list, all CTAs
-// search together.
+// for top-p some octaves below the largest weight) leaves not many more logits
+// than the law keeps.  The pass that adds up the row's mass sends these to the
+// first CTA, in vocabulary order, where a short list's members are held against
+// each other and a longer one's floors searched bit by bit.  Where the octaves do
+// not hold enough mass or too many logits, a histogram of the weights by their
+// leading bits gives a nearer bound; and where more are left than the first CTA
+// can list, all CTAs search together.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -37,10 +38,10 @@ constexpr int kSmThreads = 256;
 constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmMaxCluster = 8;
 constexpr int kSmBatch = 8;       // 16-byte loads of a thread in flight
-constexpr int kSmCands = 1024;    // candidates the first CTA lists, an equal share of them from each CTA
-constexpr int kSmPairs = 128;     // ... up to so many are held against each other
-constexpr float kSmNear = 6.f;    // octaves
+constexpr int kSmCands = 2048;    // candidates the first CTA lists, an equal share of them from each CTA
+constexpr int kSmPairs = 256;     // ... up to so many are held against each other
 constexpr int kSmPer = kSmCands / kSmThreads;
+constexpr int kSmSegs = kSmWarps * kSmMaxCluster;
 constexpr int kSmBins = 512;      // weights 1 down to 2^-64, eight bins an octave
 constexpr float kSmFix = 0x1p44f; // a weight of 1 as an integer
 constexpr float kSmMostScale = 0x1p127f;  // log2(e) / T at most: past fp32's range only the largest logit counts
@@ -89,7 +90,8 @@ struct SampleShared {
   u64 warp[2][kSmWarps];            // this CTA's warps, two rounds in turn
   u64 warp2[2][kSmWarps];
   uint32_t tmax[kSmThreads];        // threads' largest keys, of the whole cluster
-  uint32_t cnt[kSmMaxCluster];      // candidates of each CTA
+  uint32_t cnt[kSmSegs];            // candidates of each warp, or of each CTA
+  uint32_t over[kSmMaxCluster];     // CTAs with a warp that has too many to list
   uint32_t min_p_key;
   float floor;                      // what top-p's histogram says
   union {
@@ -100,6 +102,7 @@ struct SampleShared {
     u64 cand[kSmCands];             // first CTA: key << 32 | token
   };
   u64 mass[kSmPairs];               // first CTA: a short list's weights
+  int at[kSmSegs];                  // ... and where its segments start
 };
 
 // Warp sum of 64-bit integers.
@@ -157,6 +160,33 @@ struct Weight {
   }
 };
 
+// Sums of the weights of pairs of logits, two at a time.
+template <bool BF16>
+struct WeightSum {
+  float2 M, sc, neg, lo, s, c;
+  float least, lim;
+  __device__ __forceinline__ explicit WeightSum(const Weight<BF16> &w) {
+    M = make_float2(w.M, w.M), sc = make_float2(w.sc, w.sc), neg = make_float2(-w.sc, -w.sc), lo = make_float2(w.sc_lo, w.sc_lo);
+    least = w.least, lim = 1.f / w.sc;
+    s = c = make_float2(0.f, 0.f);
+  }
+  __device__ __forceinline__ void add(float2 l) {
+    const float2 d = fadd2(l, make_float2(-M.x, -M.y));
+    const float2 t = make_float2(fmaxf(d.x, least), fmaxf(d.y, least));
+    const float2 y = fmul2(t, neg);
+    float2 r = ffma2(t, lo, ffma2(t, sc, y));
+    if constexpr (!BF16) {
+      float2 e = fadd2(d, M);
+      e = make_float2(fminf(fmaxf(l.x - e.x, -lim), lim), fminf(fmaxf(l.y - e.y, -lim), lim));  // NaN beside -inf: weight zero
+      r = ffma2(e, sc, r);
+    }
+    const float2 w = make_float2(ex2(-y.x), ex2(-y.y));
+    s = fadd2(s, w);
+    c = ffma2(w, r, c);
+  }
+  __device__ __forceinline__ float sum() const { return fmaf(c.x + c.y, 0.693147180559945309f, s.x + s.y); }
+};
+
 template <bool BF16>
 __device__ __forceinline__ float element(const uint4 &q, int e) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -188,6 +218,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   const int per = (vecs + 32 * kSmWarps - 1) / (32 * kSmWarps) * 32;
   const int v0 = min(vecs, warp * per), v1 = min(vecs, v0 + per);
 
+  S.tmax[tid] = 0;
   cluster_arrive();  // the others must be running before anything is stored into their memory
   // --- the slice, and its largest logit
   uint32_t flags = 0;
@@ -232,15 +263,12 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   const int top_k = k_raw >= 1 && k_raw < P.V ? k_raw : 0;  // 0: off
   const float top_p = P.top_p ? __ldg(P.top_p + b) : 1.f, min_p = P.min_p ? __ldg(P.min_p + b) : 0.f;
   const bool use_p = top_p > 0.f && top_p < 1.f, use_m = min_p > 0.f && min_p <= 1.f;
-  double below = 0.0;  // T ln(min_p), in one thread
-  if (use_m && tid == kSmThreads - 1) below = static_cast<double>(T) * log(static_cast<double>(min_p));
   const uint32_t my_top = smp_key(top);
   {
     const uint32_t k = __reduce_max_sync(FULL_MASK, my_top);
     flags = __reduce_or_sync(FULL_MASK, flags);
     if (lane == 0) S.warp[0][warp] = static_cast<u64>(k) << 32 | flags;
   }
-  S.tmax[tid] = 0;
   __syncthreads();
   cluster_wait();
   {
@@ -253,6 +281,9 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
     if (tid < static_cast<int>(ranks)) st_cluster_u64(&S.part[0][rank], tid, k << 32 | f);
   }
+  // (every CTA's columns have been cleared: it has arrived)
+  if (top_k && top_k <= kSmThreads)
+    for (uint32_t k = 0; k < ranks; ++k) max_cluster_u32(&S.tmax[tid], k, my_top);
   cluster_sync();
   uint32_t top_key = 0;
   flags = 0;
@@ -284,25 +315,23 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     weight.least = -190.f / weight.sc;
     weight.far = weight.least == -INFINITY;
   }
-  // min-p's floor: the least logit with l - M >= T ln(min_p), by the thread that has it
-  if (tid == kSmThreads - 1) {
-    uint32_t k = kSmMinusInf;
-    if (use_m) {
-      const double at = static_cast<double>(M) + below;
-      k = smp_key(at < -3.4028234e38 ? -3.4028234e38f : static_cast<float>(at));
-      while (static_cast<double>(smp_from_key(k)) - static_cast<double>(M) < below) ++k;
-      while (k > 0x00800000u && static_cast<double>(smp_from_key(k - 1)) - static_cast<double>(M) >= below) --k;
-    }
-    S.min_p_key = k;
-  }
+  // min-p's floor in fp32, put below it by more than what that rounds
+  const float min_p_low = use_m ? M + log2f(min_p) / weight.sc - (1e-5f - 1e-5f * log2f(min_p)) / weight.sc - 0x1p-21f * fabsf(M) : -INFINITY;
 
-  // a vector's sum of the weights that reach `floor`, as an integer
-  auto vector_mass = [&](const uint4 &q, float floor) {
+  // a vector's sum of the weights, or of those that reach `floor`, as an integer
+  auto vector_mass = [&](const uint4 &q, float floor, bool whole) {
     float s = 0.f;
+    if (whole && !weight.far) {
+      WeightSum<BF16> sum(weight);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float l = element<BF16>(q, e), w = weight(l);
-      s += l >= floor ? w : 0.f;
+      for (int e = 0; e < E; e += 2) sum.add(make_float2(element<BF16>(q, e), element<BF16>(q, e + 1)));
+      s = sum.sum();
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float l = element<BF16>(q, e), w = weight(l);
+        s += l >= floor ? w : 0.f;
+      }
     }
     return __float2ll_rn(s * kSmFix);
   };
@@ -335,7 +364,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     for (int v = v0 + lane; v < v1; v += 32) {
       const uint4 q = data[v];
       if (!(vector_max<BF16>(q) >= floor)) continue;
-      a += vector_mass(q, floor);
+      a += vector_mass(q, floor, false);
 #pragma unroll
       for (int e = 0; e < E; ++e) n += element<BF16>(q, e) >= floor;
     }
@@ -343,7 +372,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   };
   // the token at u: all CTAs together, from the sums that exchange number r left.
   // A running sum of integers passes u Z where it passes floor(u Z).
-  auto choose = [&](float floor, int r, i64 Z) {
+  auto choose = [&](float floor, bool whole, int r, i64 Z) {
     const i64 target = fraction_of(u, Z, false);  // less than Z, so it is passed
     int owner = 0;
     i64 before = 0;
@@ -367,7 +396,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       i64 x = 0;
       if (mine < v1) {
         q = data[mine];
-        x = vector_mass(q, floor);
+        x = vector_mass(q, floor, whole);
       }
       const i64 inc = warp_scan64(x, lane);
       const unsigned hit = __ballot_sync(FULL_MASK, before + inc > target);
@@ -397,61 +426,112 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
   };
 
-  // --- the whole row's mass; the threads' maxima for top-k's bound; for top-p
-  // the mass within kSmNear octaves of the largest weight
+  // --- a bound that the law's floor does not lie below: the k-th largest of the
+  // 256 columns' maxima, to 16 bits; min-p's floor; and for top-p some octaves
+  // below the largest weight, which holds if the mass within them, found in the
+  // same pass, is enough.  (Where top-p goes by the mass that top-k leaves, what
+  // reaches top-k's floor has to be listed whole.)
   const bool near = use_p && !top_k;
-  if (top_k)
-    for (uint32_t k = 0; k < ranks; ++k) max_cluster_u32(&S.tmax[tid], k, my_top);
+  const float near_floor = near ? M - (5.f - log2f(1.f - top_p)) / weight.sc : -INFINITY;
+  float from = top_k && use_p ? -INFINITY : fmaxf(min_p_low, near_floor);
+  if (top_k && top_k <= kSmThreads) {
+    uint32_t t = 0, mine[kSmThreads / 32];
+#pragma unroll
+    for (int i = 0; i < kSmThreads / 32; ++i) mine[i] = S.tmax[i * 32 + lane] >> 16;
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t x = t | 1u << bit;
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kSmThreads / 32; ++i) n += mine[i] >= x;
+      if (static_cast<int>(__reduce_add_sync(FULL_MASK, n)) >= top_k) t = x;
+    }
+    from = fmaxf(from, smp_from_key(max(t << 16, kSmMinusInf)));
+  }
+  const bool plain = !top_k && !use_p && !use_m, bounded = from > -INFINITY;
+  // --- the row's mass, and the logits from the bound on into the first CTA's
+  // list, warp by warp and so in vocabulary order
+  int nseg = kSmWarps * ranks, seglen = kSmCands / nseg;
   i64 Z, within;
-  const float near_floor = M - kSmNear / weight.sc;
   {
+    const int seg = rank * kSmWarps + warp;
+    const bool count_near = near && from == near_floor;
     i64 a = 0;
     float c = 0.f;
-    if (near) {
-      for (int v = v0 + lane; v < v1; v += 32) {
-        const uint4 q = data[v];
-        a += vector_mass(q, -INFINITY);
-        if (vector_max<BF16>(q) >= near_floor) {
+    int n = 0;
+    for (int v = v0; v < v1; v += 32) {
+      const int mine = v + lane;
+      uint4 q = make_uint4(0, 0, 0, 0);
+      int hits = 0;
+      if (mine < v1) {
+        q = data[mine];
+        a += vector_mass(q, -INFINITY, true);
+        if (bounded && vector_max<BF16>(q) >= from) {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const float l = element<BF16>(q, e);
-            if (l >= near_floor) c += ex2((l - M) * weight.sc);
+            if (l >= from) {
+              ++hits;
+              if (count_near) c += ex2((l - M) * weight.sc);
+            }
           }
         }
       }
-    } else {
-      for (int v = v0 + lane; v < v1; v += 32) a += vector_mass(data[v], -INFINITY);
+      if (!__any_sync(FULL_MASK, hits > 0)) continue;
+      int inc = hits;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(FULL_MASK, inc, o);
+        if (lane >= o) inc += y;
+      }
+      int to = n + inc - hits;
+      n += __shfl_sync(FULL_MASK, inc, 31);
+      if (n <= seglen && hits > 0) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float l = element<BF16>(q, e);
+          if (l >= from) st_cluster_u64(&S.cand[seg * seglen + to++], 0, static_cast<u64>(smp_key(l)) << 32 | static_cast<uint32_t>(first + mine * E + e));
+        }
+      }
     }
+    if (lane == 0) st_cluster_u32(&S.cnt[seg], 0, n);
+    const bool many = __syncthreads_or(n > seglen);
+    if (tid < static_cast<int>(ranks)) st_cluster_u32(&S.over[rank], tid, many);
     // (the second sum is a bound: cut by more than its rounding)
     const int r = exchange(a, __float2ll_rn(c * (kSmFix * (1.f - 0x1p-14f))), Z, within);
-    if (!top_k && !use_p && !use_m) {
-      choose(-INFINITY, r, Z);
+    if (plain) {
+      choose(-INFINITY, true, r, Z);
       return;
     }
-  }
-  const uint32_t floor_key = S.min_p_key;
-  // --- a bound that the law's floor does not lie below (where top-p goes by the
-  // mass that top-k leaves, what reaches top-k's floor has to be listed whole)
-  uint32_t bound = top_k && use_p ? kSmMinusInf : floor_key;
-  if (top_k && top_k <= kSmThreads) {
-    // the k-th largest of the 256 columns' maxima, to 16 bits (a barrier counts)
-    const uint32_t mine = S.tmax[tid] >> 16;
-    uint32_t t = 0;
-    for (int bit = 15; bit >= 0; --bit) {
-      const uint32_t x = t | 1u << bit;
-      if (__syncthreads_count(mine >= x) >= top_k) t = x;
-    }
-    bound = max(bound, t << 16);
+    if (!count_near) within = Z;  // the bound holds as it is
   }
   const i64 want = use_p ? fraction_of(top_p, Z, true) : 0;  // of the whole row's mass
+  bool listed = bounded && within >= want;
+  for (uint32_t k = 0; k < ranks; ++k) listed = listed && !S.over[k];
+  uint32_t floor_key = kSmMinusInf;  // min-p's, where the list's members are not asked themselves
+  bool ask = use_m;
+  uint32_t bound = smp_key(near && within < want ? min_p_low : from);
+  if (!listed) {
+    ask = false;
+    // min-p's floor: the least logit with l - M >= T ln(min_p)
+    if (tid == 0) {
+      uint32_t k = kSmMinusInf;
+      if (use_m) {
+        const double below = static_cast<double>(T) * log(static_cast<double>(min_p)), at = static_cast<double>(M) + below;
+        k = smp_key(at < -3.4028234e38 ? -3.4028234e38f : static_cast<float>(at));
+        while (static_cast<double>(smp_from_key(k)) - static_cast<double>(M) < below) ++k;
+        while (k > 0x00800000u && static_cast<double>(smp_from_key(k - 1)) - static_cast<double>(M) >= below) --k;
+      }
+      S.min_p_key = k;
+    }
+    cluster_sync();  // (the list is read by no one, and may be written over)
+    floor_key = S.min_p_key;
+    if (!(top_k && use_p)) bound = max(bound, floor_key);
+  }
   bool binned = !near;
-  if (near && within >= want) bound = max(bound, smp_key(near_floor));  // else nothing is known yet
   const int share = kSmCands / static_cast<int>(ranks);
-  int total = 0;
-  bool listed = false;
-  while (true) {
-    // --- where the law keeps much: what lies within octaves says little
-    if (!binned && (within < want || total > 0)) {
+  if (!listed) {
+    // --- where the law keeps much, or top-p's mass reaches far down
+    if (!binned) {
       binned = true;
       for (int i = tid; i < kSmBins; i += kSmThreads) S.hist[i] = 0, S.mine[i] = 0;
       cluster_sync();
@@ -459,7 +539,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       // V-th of that cannot be the last one kept: such tokens are not looked at.
       const float least = (1.f - top_p) * 0.999f * (static_cast<float>(Z) / kSmFix) / P.V;
       const float far = M + (log2f(fmaxf(least, 1e-37f)) - 0.01f) / weight.sc;
-      const float from = fmaxf(far, smp_from_key(bound));
+      from = fmaxf(far, smp_from_key(bound));
       // Bins by exponent and three more bits of the weight; each adds up the
       // leading 16 bits of its weights, cut off: never too much.
       for (int v = v0 + lane; v < v1; v += 32) {
@@ -510,7 +590,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       bound = max(bound, smp_key(S.floor));
     }
     // --- the candidates, in vocabulary order
-    const float from = smp_from_key(bound);
+    from = smp_from_key(bound);
     int n = 0;
     for (int v = v0 + lane; v < v1; v += 32) {
       const uint4 q = data[v];
@@ -563,13 +643,8 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
     cluster_sync();
     listed = true;
-    total = 0;
-    for (uint32_t k = 0; k < ranks; ++k) {
-      total += static_cast<int>(S.cnt[k]);
-      listed = listed && static_cast<int>(S.cnt[k]) <= share;
-    }
-    if (listed || binned) break;
-    cluster_sync();  // the histogram takes the candidates' place
+    for (uint32_t k = 0; k < ranks; ++k) listed = listed && static_cast<int>(S.cnt[k]) <= share;
+    nseg = ranks, seglen = share;
   }
   constexpr int kLow = BF16 ? 16 : 0;  // a bf16 logit's key is its upper 16 bits
   if (!listed) {
@@ -604,7 +679,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       floor = max(floor, lo << kLow);
     }
     const int r = reach(floor, mass, count);
-    choose(smp_from_key(floor), r, mass);
+    choose(smp_from_key(floor), false, r, mass);
     return;
   }
   if (rank != 0) return;
@@ -619,25 +694,50 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     for (int k = 0; k < kSmWarps; ++k) x += S.warp[r][k];
     return static_cast<i64>(x);
   };
-  // where this thread's first of `each` neighbouring candidates is
-  const int each = (total + kSmThreads - 1) / kSmThreads;  // at most kSmPer
-  int seg = 0, skip = tid * each;
-  while (seg < static_cast<int>(ranks) && skip >= static_cast<int>(S.cnt[seg])) skip -= static_cast<int>(S.cnt[seg++]);
+  // the list's segments, one after the other
+  int total = 0;
+  {
+    // two counts a lane, their running sums, in every warp
+    const int c0 = 2 * lane < nseg ? static_cast<int>(S.cnt[2 * lane]) : 0, c1 = 2 * lane + 1 < nseg ? static_cast<int>(S.cnt[2 * lane + 1]) : 0;
+    int inc = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(FULL_MASK, inc, o);
+      if (lane >= o) inc += y;
+    }
+    total = __shfl_sync(FULL_MASK, inc, 31);
+    if (warp == 0) S.at[2 * lane] = inc - c0 - c1, S.at[2 * lane + 1] = inc - c1;
+  }
+  __syncthreads();
+  const int each = (total + kSmThreads - 1) / kSmThreads;  // neighbours in a thread, at most kSmPer
   uint32_t key[kSmPer];
   int id[kSmPer];
   i64 w[kSmPer];
+  bool low[kSmPer];  // out by min-p
 #pragma unroll
   for (int i = 0; i < kSmPer; ++i) {
+    low[i] = false;
     key[i] = 0;
     id[i] = -1;
     w[i] = 0;
-    if (i < each && seg < static_cast<int>(ranks)) {
-      const u64 c = S.cand[seg * share + skip];
+    const int at = tid * each + i;
+    if (i < each && at < total) {
+      int seg = 0;  // the last segment that starts at or before `at`
+#pragma unroll
+      for (int step = kSmSegs / 2; step > 0; step >>= 1)
+        if (seg + step < nseg && S.at[seg + step] <= at) seg += step;
+      const u64 c = S.cand[seg * seglen + at - S.at[seg]];
       key[i] = static_cast<uint32_t>(c >> 32);
       id[i] = static_cast<int>(static_cast<uint32_t>(c));
-      w[i] = __float2ll_rn(weight(smp_from_key(key[i])) * kSmFix);
-      ++skip;
-      while (seg < static_cast<int>(ranks) && skip >= static_cast<int>(S.cnt[seg])) skip = 0, ++seg;
+      const float l = smp_from_key(key[i]), y = weight(l);
+      w[i] = __float2ll_rn(y * kSmFix);
+      // min-p: by the weight, or in fp64 where that is too near to say
+      if (ask) {
+        bool out = y < min_p;
+        if (fabsf(y - min_p) <= 1e-5f * min_p)
+          out = static_cast<double>(l) - static_cast<double>(M) < static_cast<double>(T) * log(static_cast<double>(min_p));
+        low[i] = out;
+      }
     }
   }
   uint32_t floor = floor_key;
@@ -653,7 +753,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
         larger += gt;
         above += gt ? static_cast<i64>(S.mass[j]) : 0;
       }
-    bool keep = tid < total && key[0] >= floor && (!top_k || larger < top_k);
+    bool keep = tid < total && key[0] >= floor && !low[0] && (!top_k || larger < top_k);
     i64 need = want;
     if (top_k && use_p) need = fraction_of(top_p, block_sum64(tid < total && larger < top_k ? w[0] : 0), true);
     if (use_p) keep = keep && above < need;
@@ -708,7 +808,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
 #pragma unroll
     for (int i = 0; i < kSmPer; ++i)
-      if (key[i] < floor) w[i] = 0;
+      if (key[i] < floor || low[i]) w[i] = 0;
   }
   // --- running sums in vocabulary order
   i64 mine = 0;
