@@ -37,7 +37,9 @@ namespace {
 constexpr int kSmThreads = 256;
 constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmMaxCluster = 8;
-constexpr int kSmBatch = 8;       // 16-byte loads of a thread in flight
+constexpr int kSmResident = 4 * 152;  // CTAs that run at a time
+constexpr int kSmBatch = 8;       // 16-byte loads of a thread in flight, first pass
+constexpr int kSmAhead = 4;       // ... and in the second
 constexpr int kSmCands = 2048;    // candidates the first CTA lists, an equal share of them from each CTA
 constexpr int kSmPairs = 256;     // ... up to so many are held against each other
 constexpr int kSmPer = kSmCands / kSmThreads;
@@ -81,8 +83,14 @@ __device__ __forceinline__ void add_cluster_u64(const void *p, uint32_t rank, u6
 __device__ __forceinline__ void max_cluster_u32(const void *p, uint32_t rank, uint32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(dsmem_addr(p, rank)), "r"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The cluster's barrier, thread by thread: some come to it from branches of their
+// own (the aligned form wants whole warps).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void cluster_meet() {
+  cluster_arrive();
+  cluster_wait();
+}
 
 struct SampleShared {
   u64 part[2][kSmMaxCluster];       // what the CTAs tell one another, two rounds in turn
@@ -141,50 +149,18 @@ __device__ __forceinline__ i64 fraction_of(float f, i64 n, bool up) {
   return static_cast<i64>(r + (up && rest ? 1 : 0));
 }
 
-// The weights of a row: w(l) = 2^((l - M) log2(e) / T).  The exponent is kept to
-// more than fp32's 24 bits (its rounding, times 20 or so, would show in the sums):
-// what the factor and the product lose goes in to first order, and for fp32
-// logits what the difference loses (bf16 logits of like size have an exact one).
-template <bool BF16>
+// The weights of a row: w(l) = 2^((l - M) log2(e) / T).  The exponent is rounded
+// to fp32 like its factors, so a weight of 2^-y is off by about y 2^-24, and by the
+// hardware's 2^-22 at most: each on its own, so that in the sums it evens out.
+// (Exponents to twice the bits, as first-order corrections, took twice the
+// instructions of the pass and left the hardware's error.)
 struct Weight {
-  float M, sc, sc_lo, least;  // least: differences below it have weight zero
-  bool far;                   // a temperature at which only -inf has (least is -inf)
-  __device__ __forceinline__ float operator()(float l) const {
-    const float d = l - M, t = fmaxf(d, far ? -3e38f : least);
-    const float y = t * sc;
-    float r = fmaf(t, sc_lo, fmaf(t, sc, -y));
-    if constexpr (!BF16) r = fmaf(d >= least ? l - (d + M) : 0.f, sc, r);
-    const float w = ex2(y);
-    const float c = fmaf(w, r * 0.693147180559945309f, w);
-    return far && l == -INFINITY ? 0.f : c;
+  float M, sc;
+  __device__ __forceinline__ float operator()(float l) const { return ex2((l - M) * sc); }
+  __device__ __forceinline__ float2 operator()(float2 l) const {
+    const float2 y = fmul2(fadd2(l, make_float2(-M, -M)), make_float2(sc, sc));
+    return make_float2(ex2(y.x), ex2(y.y));
   }
-};
-
-// Sums of the weights of pairs of logits, two at a time.
-template <bool BF16>
-struct WeightSum {
-  float2 M, sc, neg, lo, s, c;
-  float least, lim;
-  __device__ __forceinline__ explicit WeightSum(const Weight<BF16> &w) {
-    M = make_float2(w.M, w.M), sc = make_float2(w.sc, w.sc), neg = make_float2(-w.sc, -w.sc), lo = make_float2(w.sc_lo, w.sc_lo);
-    least = w.least, lim = 1.f / w.sc;
-    s = c = make_float2(0.f, 0.f);
-  }
-  __device__ __forceinline__ void add(float2 l) {
-    const float2 d = fadd2(l, make_float2(-M.x, -M.y));
-    const float2 t = make_float2(fmaxf(d.x, least), fmaxf(d.y, least));
-    const float2 y = fmul2(t, neg);
-    float2 r = ffma2(t, lo, ffma2(t, sc, y));
-    if constexpr (!BF16) {
-      float2 e = fadd2(d, M);
-      e = make_float2(fminf(fmaxf(l.x - e.x, -lim), lim), fminf(fmaxf(l.y - e.y, -lim), lim));  // NaN beside -inf: weight zero
-      r = ffma2(e, sc, r);
-    }
-    const float2 w = make_float2(ex2(-y.x), ex2(-y.y));
-    s = fadd2(s, w);
-    c = ffma2(w, r, c);
-  }
-  __device__ __forceinline__ float sum() const { return fmaf(c.x + c.y, 0.693147180559945309f, s.x + s.y); }
 };
 
 template <bool BF16>
@@ -203,7 +179,25 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
   return fmax_nan(fmax_nan(element<BF16>(q, 0), element<BF16>(q, 1)), fmax_nan(element<BF16>(q, 2), element<BF16>(q, 3)));
 }
 
+// A vector of a row from memory; -inf past the end.
 template <bool BF16, bool VEC>
+__device__ __forceinline__ uint4 load_vector(const char *row, int at, int last, uint64_t policy) {
+  if constexpr (VEC) return ld_stream_u4(row + static_cast<size_t>(at) * (BF16 ? 2 : 4), policy);
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (BF16) {
+      const unsigned short *p = reinterpret_cast<const unsigned short *>(row) + at + 2 * e;
+      w[e] = (at + 2 * e < last ? __ldg(p) : 0xff80u) | (at + 2 * e + 1 < last ? static_cast<uint32_t>(__ldg(p + 1)) : 0xff80u) << 16;
+    } else {
+      w[e] = at + e < last ? __ldg(reinterpret_cast<const uint32_t *>(row) + at + e) : 0xff800000u;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// KEEP: slices stay in shared memory; else later passes read them again, from L2.
+template <bool BF16, bool VEC, bool KEEP>
 __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_constant__ SampleParams P) {
   constexpr int E = BF16 ? 8 : 4;
   __shared__ SampleShared S;
@@ -221,6 +215,8 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   S.tmax[tid] = 0;
   cluster_arrive();  // the others must be running before anything is stored into their memory
   // --- the slice, and its largest logit
+  const uint64_t policy = KEEP ? l2_policy_evict_first() : l2_policy_evict_normal();
+  auto vector_at = [&](int v) { return KEEP ? data[v] : load_vector<BF16, VEC>(row, first + v * E, last, policy); };
   uint32_t flags = 0;
   float top = -INFINITY;
   for (int i0 = v0 + lane; i0 < v1; i0 += 32 * kSmBatch) {
@@ -228,30 +224,13 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < kSmBatch; ++i) {
       const int v = i0 + i * 32;
-      if (v < v1) {
-        if constexpr (VEC) {
-          q[i] = ld_stream_u4(row + (static_cast<size_t>(first) + static_cast<size_t>(v) * E) * (BF16 ? 2 : 4), l2_policy_evict_first());
-        } else {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int at = first + v * E + e * (E / 4);
-            if constexpr (BF16) {
-              const unsigned short *p = reinterpret_cast<const unsigned short *>(row) + at;
-              w[e] = (at < last ? __ldg(p) : 0xff80u) | (at + 1 < last ? static_cast<uint32_t>(__ldg(p + 1)) : 0xff80u) << 16;
-            } else {
-              w[e] = at < last ? __ldg(reinterpret_cast<const uint32_t *>(row) + at) : 0xff800000u;
-            }
-          }
-          q[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
+      if (v < v1) q[i] = load_vector<BF16, VEC>(row, first + v * E, last, policy);
     }
 #pragma unroll
     for (int i = 0; i < kSmBatch; ++i) {
       const int v = i0 + i * 32;
       if (v < v1) {
-        data[v] = q[i];
+        if constexpr (KEEP) data[v] = q[i];
         const float c = vector_max<BF16>(q[i]);
         if (!(c < INFINITY)) flags |= F_NONFINITE;  // NaN or +inf
         top = fmaxf(top, c);
@@ -263,6 +242,8 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   const int top_k = k_raw >= 1 && k_raw < P.V ? k_raw : 0;  // 0: off
   const float top_p = P.top_p ? __ldg(P.top_p + b) : 1.f, min_p = P.min_p ? __ldg(P.min_p + b) : 0.f;
   const bool use_p = top_p > 0.f && top_p < 1.f, use_m = min_p > 0.f && min_p <= 1.f;
+  Weight weight;
+  weight.sc = fminf(1.4426950408889634f / T, kSmMostScale);
   const uint32_t my_top = smp_key(top);
   {
     const uint32_t k = __reduce_max_sync(FULL_MASK, my_top);
@@ -284,7 +265,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   // (every CTA's columns have been cleared: it has arrived)
   if (top_k && top_k <= kSmThreads)
     for (uint32_t k = 0; k < ranks; ++k) max_cluster_u32(&S.tmax[tid], k, my_top);
-  cluster_sync();
+  cluster_meet();
   uint32_t top_key = 0;
   flags = 0;
   for (uint32_t k = 0; k < ranks; ++k) {
@@ -304,36 +285,21 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
     return;
   }
-  Weight<BF16> weight;
-  {
-    // log2(e) / T to twice fp32's precision
-    constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;
-    const float s = kHi / T;
-    weight.M = M;
-    weight.sc = fminf(s, kSmMostScale);
-    weight.sc_lo = s > kSmMostScale ? 0.f : (fmaf(-s, T, kHi) + kLo) / T;
-    weight.least = -190.f / weight.sc;
-    weight.far = weight.least == -INFINITY;
-  }
+  weight.M = M;
   // min-p's floor in fp32, put below it by more than what that rounds
   const float min_p_low = use_m ? M + log2f(min_p) / weight.sc - (1e-5f - 1e-5f * log2f(min_p)) / weight.sc - 0x1p-21f * fabsf(M) : -INFINITY;
 
   // a vector's sum of the weights, or of those that reach `floor`, as an integer
   auto vector_mass = [&](const uint4 &q, float floor, bool whole) {
-    float s = 0.f;
-    if (whole && !weight.far) {
-      WeightSum<BF16> sum(weight);
+    float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < E; e += 2) sum.add(make_float2(element<BF16>(q, e), element<BF16>(q, e + 1)));
-      s = sum.sum();
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float l = element<BF16>(q, e), w = weight(l);
-        s += l >= floor ? w : 0.f;
-      }
+    for (int e = 0; e < E; e += 2) {
+      const float2 l = make_float2(element<BF16>(q, e), element<BF16>(q, e + 1));
+      float2 w = weight(l);
+      if (!whole) w = make_float2(l.x >= floor ? w.x : 0.f, l.y >= floor ? w.y : 0.f);
+      s = fadd2(s, w);
     }
-    return __float2ll_rn(s * kSmFix);
+    return __float2ll_rn((s.x + s.y) * kSmFix);
   };
   int round = 1;  // of the exchange: buffers in turn
   // sums over the cluster (two at a time), the same in every thread
@@ -351,7 +317,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       st_cluster_u64(&S.part[r][rank], tid, x);
       st_cluster_u64(&S.part2[r][rank], tid, y);
     }
-    cluster_sync();
+    cluster_meet();
     A = C = 0;
     for (uint32_t k = 0; k < ranks; ++k) A += static_cast<i64>(S.part[r][k]), C += static_cast<i64>(S.part2[r][k]);
     return r;
@@ -362,7 +328,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     i64 a = 0;
     int n = 0;
     for (int v = v0 + lane; v < v1; v += 32) {
-      const uint4 q = data[v];
+      const uint4 q = vector_at(v);
       if (!(vector_max<BF16>(q) >= floor)) continue;
       a += vector_mass(q, floor, false);
 #pragma unroll
@@ -395,7 +361,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       uint4 q = make_uint4(0, 0, 0, 0);
       i64 x = 0;
       if (mine < v1) {
-        q = data[mine];
+        q = vector_at(mine);
         x = vector_mass(q, floor, whole);
       }
       const i64 inc = warp_scan64(x, lane);
@@ -438,12 +404,16 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     uint32_t t = 0, mine[kSmThreads / 32];
 #pragma unroll
     for (int i = 0; i < kSmThreads / 32; ++i) mine[i] = S.tmax[i * 32 + lane] >> 16;
-    for (int bit = 15; bit >= 0; --bit) {
-      const uint32_t x = t | 1u << bit;
-      int n = 0;
+#pragma unroll 1
+    for (int bit = 14; bit >= 0; bit -= 2) {  // two bits a round, three counts in a word
+      uint32_t n = 0;
 #pragma unroll
-      for (int i = 0; i < kSmThreads / 32; ++i) n += mine[i] >= x;
-      if (static_cast<int>(__reduce_add_sync(FULL_MASK, n)) >= top_k) t = x;
+      for (int i = 0; i < kSmThreads / 32; ++i)
+#pragma unroll
+        for (int j = 1; j < 4; ++j) n += mine[i] >= (t | j << bit) ? 1u << (10 * (j - 1)) : 0u;
+      n = __reduce_add_sync(FULL_MASK, n);
+      const uint32_t k = top_k;
+      t |= ((n & 1023u) >= k ? (n >> 10 & 1023u) >= k ? (n >> 20) >= k ? 3u : 2u : 1u : 0u) << bit;
     }
     from = fmaxf(from, smp_from_key(max(t << 16, kSmMinusInf)));
   }
@@ -458,38 +428,53 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     i64 a = 0;
     float c = 0.f;
     int n = 0;
-    for (int v = v0; v < v1; v += 32) {
-      const int mine = v + lane;
-      uint4 q = make_uint4(0, 0, 0, 0);
-      int hits = 0;
-      if (mine < v1) {
-        q = data[mine];
-        a += vector_mass(q, -INFINITY, true);
-        if (bounded && vector_max<BF16>(q) >= from) {
+    for (int i0 = v0; i0 < v1; i0 += 32 * kSmAhead) {
+      uint4 q[kSmAhead];
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float l = element<BF16>(q, e);
-            if (l >= from) {
-              ++hits;
-              if (count_near) c += ex2((l - M) * weight.sc);
-            }
+      for (int i = 0; i < kSmAhead; ++i)
+        if (i0 + i * 32 + lane < v1) q[i] = vector_at(i0 + i * 32 + lane);
+#pragma unroll
+      for (int i = 0; i < kSmAhead; ++i) {
+        const int mine = i0 + i * 32 + lane;
+        if (i0 + i * 32 >= v1) break;
+        uint32_t bits = 0;  // of the vector's logits
+        if (mine < v1) {
+          a += vector_mass(q[i], -INFINITY, true);
+          if (bounded && vector_max<BF16>(q[i]) >= from) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) bits |= element<BF16>(q[i], e) >= from ? 1u << e : 0u;
           }
         }
-      }
-      if (!__any_sync(FULL_MASK, hits > 0)) continue;
-      int inc = hits;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(FULL_MASK, inc, o);
-        if (lane >= o) inc += y;
-      }
-      int to = n + inc - hits;
-      n += __shfl_sync(FULL_MASK, inc, 31);
-      if (n <= seglen && hits > 0) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float l = element<BF16>(q, e);
-          if (l >= from) st_cluster_u64(&S.cand[seg * seglen + to++], 0, static_cast<u64>(smp_key(l)) << 32 | static_cast<uint32_t>(first + mine * E + e));
+        const unsigned some = __ballot_sync(FULL_MASK, bits != 0);
+        if (!some) continue;
+        int to, all;  // the lane's first place, and places for the warp
+        if (__any_sync(FULL_MASK, bits & (bits - 1))) {
+          const int hits = __popc(bits);
+          int inc = hits;
+#pragma unroll 1
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL_MASK, inc, o);
+            if (lane >= o) inc += y;
+          }
+          to = n + inc - hits;
+          all = __shfl_sync(FULL_MASK, inc, 31);
+        } else {
+          to = n + __popc(some & ((1u << lane) - 1u));
+          all = __popc(some);
+        }
+        n += all;
+        while (bits) {
+          const int e = __ffs(bits) - 1;
+          bits &= bits - 1;
+          const int at = mine * E + e;
+          float l;
+          if constexpr (BF16)
+            l = __uint_as_float(static_cast<uint32_t>(KEEP ? reinterpret_cast<const unsigned short *>(data)[at]
+                                                           : __ldg(reinterpret_cast<const unsigned short *>(row) + first + at)) << 16);
+          else
+            l = KEEP ? reinterpret_cast<const float *>(data)[at] : __ldg(reinterpret_cast<const float *>(row) + first + at);
+          if (count_near) c += ex2((l - M) * weight.sc);
+          if (n <= seglen) st_cluster_u64(&S.cand[seg * seglen + to++], 0, static_cast<u64>(smp_key(l)) << 32 | static_cast<uint32_t>(first + at));
         }
       }
     }
@@ -523,7 +508,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       }
       S.min_p_key = k;
     }
-    cluster_sync();  // (the list is read by no one, and may be written over)
+    cluster_meet();  // (the list is read by no one, and may be written over)
     floor_key = S.min_p_key;
     if (!(top_k && use_p)) bound = max(bound, floor_key);
   }
@@ -534,7 +519,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     if (!binned) {
       binned = true;
       for (int i = tid; i < kSmBins; i += kSmThreads) S.hist[i] = 0, S.mine[i] = 0;
-      cluster_sync();
+      cluster_meet();
       // What is dropped weighs less than (1 - top_p) Z, so a token of less than a
       // V-th of that cannot be the last one kept: such tokens are not looked at.
       const float least = (1.f - top_p) * 0.999f * (static_cast<float>(Z) / kSmFix) / P.V;
@@ -543,7 +528,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       // Bins by exponent and three more bits of the weight; each adds up the
       // leading 16 bits of its weights, cut off: never too much.
       for (int v = v0 + lane; v < v1; v += 32) {
-        const uint4 q = data[v];
+        const uint4 q = vector_at(v);
         if (!(vector_max<BF16>(q) >= from)) continue;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -555,10 +540,10 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
           }
         }
       }
-      __syncthreads();  // (a slice has at most 2^15 logits: its sums stay below 2^32)
+      __syncthreads();  // (a slice has at most 2^16 logits: its sums stay below 2^32)
       for (int i = tid; i < kSmBins; i += kSmThreads)
         if (S.mine[i]) add_cluster_u64(&S.hist[i], 0, S.mine[i]);
-      cluster_sync();
+      cluster_meet();
       if (rank == 0) {
         // running sums from the largest weights down, in the sums' unit; bin i
         // holds weights of exponent -ceil(i / 8), 16 bits of each
@@ -586,14 +571,14 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
         if (tid > 0 && tid < static_cast<int>(ranks)) st_cluster_u32(&S.floor, tid, __float_as_uint(S.floor));
       }
       ++round;
-      cluster_sync();
+      cluster_meet();
       bound = max(bound, smp_key(S.floor));
     }
     // --- the candidates, in vocabulary order
     from = smp_from_key(bound);
     int n = 0;
     for (int v = v0 + lane; v < v1; v += 32) {
-      const uint4 q = data[v];
+      const uint4 q = vector_at(v);
       if (!(vector_max<BF16>(q) >= from)) continue;
 #pragma unroll
       for (int e = 0; e < E; ++e) n += element<BF16>(q, e) >= from;
@@ -617,7 +602,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
         uint4 q = make_uint4(0, 0, 0, 0);
         int c = 0;
         if (mine < v1) {
-          q = data[mine];
+          q = vector_at(mine);
           if (vector_max<BF16>(q) >= from) {
 #pragma unroll
             for (int e = 0; e < E; ++e) c += element<BF16>(q, e) >= from;
@@ -641,7 +626,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
         at += __shfl_sync(FULL_MASK, inc, 31);
       }
     }
-    cluster_sync();
+    cluster_meet();
     listed = true;
     for (uint32_t k = 0; k < ranks; ++k) listed = listed && static_cast<int>(S.cnt[k]) <= share;
     nseg = ranks, seglen = share;
@@ -840,29 +825,35 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
 bool smp_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // Dynamic shared memory above 48 KB has to be asked for, once per device.
-template <bool BF16, bool VEC>
+template <bool BF16, bool VEC, bool KEEP>
 cudaError_t launch_sample(const SampleParams &p, int ranks, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
-  int dev;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (!(done.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(sample_kernel<BF16, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
+  if (KEEP) {
+    static std::atomic<uint64_t> done{0};
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_relaxed);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(sample_kernel<BF16, VEC, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
+      if (e != cudaSuccess) return e;
+      done.fetch_or(bit, std::memory_order_relaxed);
+    }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * ranks);
   cfg.blockDim = dim3(kSmThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.slice) * (BF16 ? 2 : 4);
+  cfg.dynamicSmemBytes = KEEP ? static_cast<size_t>(p.slice) * (BF16 ? 2 : 4) : 0;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim = {static_cast<unsigned>(ranks), 1, 1};
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<BF16, VEC>, p);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<BF16, VEC, KEEP>, p);
+}
+template <bool BF16, bool VEC>
+cudaError_t launch_sample(const SampleParams &p, int ranks, bool keep, cudaStream_t s) {
+  return keep ? launch_sample<BF16, VEC, true>(p, ranks, s) : launch_sample<BF16, VEC, false>(p, ranks, s);
 }
 
 }  // namespace
@@ -898,16 +889,24 @@ spec_status spec_sample(const spec_sample_args *a, const spec_sample_out *o, voi
   p.row_stride = a->row_stride;
   p.B = a->B;
   p.V = a->V;
-  // CTAs per row: slices of at most 32 KB, as far as eight go
+  // CTAs per row: slices of at most 32 KB, as far as eight go, which stay in shared
+  // memory.  More rows than run side by side that way are cut into fewer slices
+  // (of 2^16 logits at most), which are read a second time: from L2, since what runs
+  // at a time fits (256 rows of 128256 bf16 logits 35 us, and 43 with slices kept;
+  // 64 rows 16 and 15).
   const long long bytes = static_cast<long long>(a->V) * esz;
   int ranks = 1;
   while (ranks < kSmMaxCluster && bytes > ranks * (32LL << 10)) ranks *= 2;
+  const bool keep = static_cast<long long>(a->B) * ranks <= kSmResident;
+  if (!keep) {
+    while (ranks > 1 && static_cast<long long>(a->B) * ranks > kSmResident && (a->V + ranks / 2 - 1) / (ranks / 2) <= 1 << 16) ranks /= 2;
+  }
   const int unit = 16 / esz;
   p.slice = ((a->V + ranks - 1) / ranks + unit - 1) / unit * unit;
   const bool vec = smp_aligned(a->logits, 16) && (a->row_stride * esz) % 16 == 0 && bytes % 16 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = bf16 ? (vec ? launch_sample<true, true>(p, ranks, s) : launch_sample<true, false>(p, ranks, s))
-                             : (vec ? launch_sample<false, true>(p, ranks, s) : launch_sample<false, false>(p, ranks, s));
+  const cudaError_t e = bf16 ? (vec ? launch_sample<true, true>(p, ranks, keep, s) : launch_sample<true, false>(p, ranks, keep, s))
+                             : (vec ? launch_sample<false, true>(p, ranks, keep, s) : launch_sample<false, false>(p, ranks, keep, s));
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
