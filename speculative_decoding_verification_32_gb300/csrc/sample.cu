@@ -9,15 +9,15 @@
 // the law is w over the logits that reach all three, and the token the smallest
 // v whose running sum in vocabulary order passes u times the whole.
 //
-// One cluster of CTAs per row.  Each keeps its slice of the row in shared memory,
-// so memory is read once and everything after the maximum runs on chip.  Sums
-// are integers (w 2^44, at most 2^18 of them): they do not depend on the order in
-// which they are made.  The floors are found among few candidates: a bound
+// One cluster of CTAs per row.  The pass over memory finds the threads' largest
+// logits and their masses against these; a slice stays in shared memory or is read
+// again from L2.  Sums over threads are integers (w 2^44, at most 2^18 of them):
+// they do not depend on the order in which they are made.  The floors are found among few candidates: a bound
 // below the floor that is cheap (the k-th largest of the threads' own maxima;
 // for top-p some octaves below the largest weight) leaves not many more logits
-// than the law keeps.  The pass that adds up the row's mass sends these to the
-// first CTA, in vocabulary order, where a short list's members are held against
-// each other and a longer one's floors searched bit by bit.  Where the octaves do
+// than the law keeps.  A second pass sends these to the first CTA, in vocabulary
+// order, where a short list's members are held against each other and a longer
+// one's floors searched bit by bit.  Where the octaves do
 // not hold enough mass or too many logits, a histogram of the weights by their
 // leading bits gives a nearer bound; and where more are left than the first CTA
 // can list, all CTAs search together.
@@ -39,7 +39,6 @@ constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmMaxCluster = 8;
 constexpr int kSmResident = 4 * 152;  // CTAs that run at a time
 constexpr int kSmBatch = 8;       // 16-byte loads of a thread in flight, first pass
-constexpr int kSmAhead = 4;       // ... and in the second
 constexpr int kSmCands = 2048;    // candidates the first CTA lists, an equal share of them from each CTA
 constexpr int kSmPairs = 256;     // ... up to so many are held against each other
 constexpr int kSmPer = kSmCands / kSmThreads;
@@ -57,7 +56,8 @@ struct SampleParams {
   float *prob;
   long long row_stride;
   int B, V;
-  int slice;  // elements per CTA, a multiple of a vector's
+  int slice;    // elements per CTA, a multiple of a vector's
+  int batches;  // of kSmBatch vectors, per thread
 };
 
 typedef long long i64;
@@ -182,18 +182,21 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
 // A vector of a row from memory; -inf past the end.
 template <bool BF16, bool VEC>
 __device__ __forceinline__ uint4 load_vector(const char *row, int at, int last, uint64_t policy) {
-  if constexpr (VEC) return ld_stream_u4(row + static_cast<size_t>(at) * (BF16 ? 2 : 4), policy);
-  uint32_t w[4];
+  if constexpr (VEC) {
+    return ld_stream_u4(row + static_cast<size_t>(at) * (BF16 ? 2 : 4), policy);
+  } else {
+    uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if constexpr (BF16) {
-      const unsigned short *p = reinterpret_cast<const unsigned short *>(row) + at + 2 * e;
-      w[e] = (at + 2 * e < last ? __ldg(p) : 0xff80u) | (at + 2 * e + 1 < last ? static_cast<uint32_t>(__ldg(p + 1)) : 0xff80u) << 16;
-    } else {
-      w[e] = at + e < last ? __ldg(reinterpret_cast<const uint32_t *>(row) + at + e) : 0xff800000u;
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (BF16) {
+        const unsigned short *p = reinterpret_cast<const unsigned short *>(row) + at + 2 * e;
+        w[e] = (at + 2 * e < last ? __ldg(p) : 0xff80u) | (at + 2 * e + 1 < last ? static_cast<uint32_t>(__ldg(p + 1)) : 0xff80u) << 16;
+      } else {
+        w[e] = at + e < last ? __ldg(reinterpret_cast<const uint32_t *>(row) + at + e) : 0xff800000u;
+      }
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // KEEP: slices stay in shared memory; else later passes read them again, from L2.
@@ -202,7 +205,9 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   constexpr int E = BF16 ? 8 : 4;
   __shared__ SampleShared S;
   extern __shared__ __align__(16) unsigned char smp_raw[];
-  uint4 *const data = reinterpret_cast<uint4 *>(smp_raw);
+  // the largest logit of every batch of vectors of every thread, then the slice
+  float *const largest = reinterpret_cast<float *>(smp_raw);
+  uint4 *const data = reinterpret_cast<uint4 *>(smp_raw + P.batches * kSmThreads * 4);
   const uint32_t ranks = cluster_nctarank(), rank = cluster_ctarank();
   const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const char *row = static_cast<const char *>(P.logits) + static_cast<size_t>(b) * P.row_stride * (BF16 ? 2 : 4);
@@ -217,26 +222,6 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   // --- the slice, and its largest logit
   const uint64_t policy = KEEP ? l2_policy_evict_first() : l2_policy_evict_normal();
   auto vector_at = [&](int v) { return KEEP ? data[v] : load_vector<BF16, VEC>(row, first + v * E, last, policy); };
-  uint32_t flags = 0;
-  float top = -INFINITY;
-  for (int i0 = v0 + lane; i0 < v1; i0 += 32 * kSmBatch) {
-    uint4 q[kSmBatch];
-#pragma unroll
-    for (int i = 0; i < kSmBatch; ++i) {
-      const int v = i0 + i * 32;
-      if (v < v1) q[i] = load_vector<BF16, VEC>(row, first + v * E, last, policy);
-    }
-#pragma unroll
-    for (int i = 0; i < kSmBatch; ++i) {
-      const int v = i0 + i * 32;
-      if (v < v1) {
-        if constexpr (KEEP) data[v] = q[i];
-        const float c = vector_max<BF16>(q[i]);
-        if (!(c < INFINITY)) flags |= F_NONFINITE;  // NaN or +inf
-        top = fmaxf(top, c);
-      }
-    }
-  }
   const float T = P.temperature ? __ldg(P.temperature + b) : 1.f, u = __ldg(P.u + b);
   const int k_raw = P.top_k ? __ldg(P.top_k + b) : 0;
   const int top_k = k_raw >= 1 && k_raw < P.V ? k_raw : 0;  // 0: off
@@ -244,6 +229,41 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   const bool use_p = top_p > 0.f && top_p < 1.f, use_m = min_p > 0.f && min_p <= 1.f;
   Weight weight;
   weight.sc = fminf(1.4426950408889634f / T, kSmMostScale);
+  uint32_t flags = 0;
+  float top = -INFINITY, mass = 0.f;  // sum of the weights against the thread's largest so far
+  int chunk = 0;
+  for (int i0 = v0 + lane; i0 < v1; i0 += 32 * kSmBatch, ++chunk) {
+    uint4 q[kSmBatch];
+#pragma unroll
+    for (int i = 0; i < kSmBatch; ++i) {
+      const int v = i0 + i * 32;
+      q[i] = BF16 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
+                  : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+      if (v < v1) q[i] = load_vector<BF16, VEC>(row, first + v * E, last, policy);
+    }
+    float c = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kSmBatch; ++i) {
+      const int v = i0 + i * 32;
+      if (KEEP && v < v1) data[v] = q[i];
+      c = fmax_nan(c, vector_max<BF16>(q[i]));
+    }
+    largest[chunk * kSmThreads + tid] = c;
+    if (!(c < INFINITY)) flags |= F_NONFINITE;  // NaN or +inf
+    if (c > top) {
+      mass *= ex2((top - c) * weight.sc);
+      top = c;
+    }
+    if (top > -INFINITY) {
+      weight.M = top;
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kSmBatch; ++i)
+#pragma unroll
+        for (int e = 0; e < E; e += 2) s = fadd2(s, weight(make_float2(element<BF16>(q[i], e), element<BF16>(q[i], e + 1))));
+      mass += s.x + s.y;
+    }
+  }
   const uint32_t my_top = smp_key(top);
   {
     const uint32_t k = __reduce_max_sync(FULL_MASK, my_top);
@@ -289,15 +309,13 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   // min-p's floor in fp32, put below it by more than what that rounds
   const float min_p_low = use_m ? M + log2f(min_p) / weight.sc - (1e-5f - 1e-5f * log2f(min_p)) / weight.sc - 0x1p-21f * fabsf(M) : -INFINITY;
 
-  // a vector's sum of the weights, or of those that reach `floor`, as an integer
-  auto vector_mass = [&](const uint4 &q, float floor, bool whole) {
+  // a vector's sum of the weights that reach `floor`, as an integer
+  auto vector_mass = [&](const uint4 &q, float floor) {
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
-      const float2 l = make_float2(element<BF16>(q, e), element<BF16>(q, e + 1));
-      float2 w = weight(l);
-      if (!whole) w = make_float2(l.x >= floor ? w.x : 0.f, l.y >= floor ? w.y : 0.f);
-      s = fadd2(s, w);
+      const float2 l = make_float2(element<BF16>(q, e), element<BF16>(q, e + 1)), w = weight(l);
+      s = fadd2(s, make_float2(l.x >= floor ? w.x : 0.f, l.y >= floor ? w.y : 0.f));
     }
     return __float2ll_rn((s.x + s.y) * kSmFix);
   };
@@ -330,7 +348,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     for (int v = v0 + lane; v < v1; v += 32) {
       const uint4 q = vector_at(v);
       if (!(vector_max<BF16>(q) >= floor)) continue;
-      a += vector_mass(q, floor, false);
+      a += vector_mass(q, floor);
 #pragma unroll
       for (int e = 0; e < E; ++e) n += element<BF16>(q, e) >= floor;
     }
@@ -338,7 +356,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   };
   // the token at u: all CTAs together, from the sums that exchange number r left.
   // A running sum of integers passes u Z where it passes floor(u Z).
-  auto choose = [&](float floor, bool whole, int r, i64 Z) {
+  auto choose = [&](float floor, int r, i64 Z) {
     const i64 target = fraction_of(u, Z, false);  // less than Z, so it is passed
     int owner = 0;
     i64 before = 0;
@@ -355,40 +373,74 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       if (before + x > target) break;
       before += x;
     }
-    if (w != warp) return;
-    for (int v = v0; v < v1; v += 32) {
+    // that warp's part of the slice, an eighth to each warp
+    const int lo = min(vecs, w * per), hi = min(vecs, lo + per), each = (per / 32 + kSmWarps - 1) / kSmWarps * 32;
+    const int a0 = min(hi, lo + warp * each), a1 = min(hi, a0 + each);
+    i64 sum = 0;
+    for (int i0 = a0 + lane; i0 < a1; i0 += 32 * 4) {
+      uint4 q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i * 32 < a1) q[i] = vector_at(i0 + i * 32);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i * 32 < a1) sum += vector_mass(q[i], floor);
+    }
+    sum = warp_sum64(sum);
+    if (lane == 0) S.warp2[r][warp] = static_cast<u64>(sum);
+    __syncthreads();
+    int part = -1;
+    for (int k = 0; k < kSmWarps; ++k) {
+      const i64 x = static_cast<i64>(S.warp2[r][k]);
+      if (x == 0) continue;
+      if (part >= 0) before += static_cast<i64>(S.warp2[r][part]);
+      part = k;
+      if (before + x > target) break;
+    }
+    if (part != warp) return;
+    // (what is added up again may round to a little less than that warp's sum, which
+    // was made against the threads' own maxima: the last kept token, then)
+    int tok = -1;
+    float prob = 0.f;
+    bool done = false;
+    for (int v = a0; v < a1 && !done; v += 32) {
       const int mine = v + lane;
       uint4 q = make_uint4(0, 0, 0, 0);
       i64 x = 0;
-      if (mine < v1) {
+      if (mine < a1) {
         q = vector_at(mine);
-        x = vector_mass(q, floor, whole);
+        x = vector_mass(q, floor);
       }
       const i64 inc = warp_scan64(x, lane);
-      const unsigned hit = __ballot_sync(FULL_MASK, before + inc > target);
-      if (!hit) {
-        before += __shfl_sync(FULL_MASK, inc, 31);
-        continue;
-      }
-      if (lane == __ffs(hit) - 1) {  // its sums up to each element, as the vector's was made
-        float s = 0.f, prob = 0.f;
-        int tok = -1;
-        bool found = false;
+      const unsigned hit = __ballot_sync(FULL_MASK, before + inc > target), some = __ballot_sync(FULL_MASK, x > 0);
+      const int who = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : -1;
+      if (who >= 0) {
+        int mine_tok = -1;
+        float mine_prob = 0.f;
+        if (lane == who) {  // its sums up to each element
+          float s = 0.f;
+          bool found = false;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float l = element<BF16>(q, e), y = l >= floor ? weight(l) : 0.f;
-          s += y;
-          if (!found && y > 0.f) {
-            tok = first + mine * E + e;
-            prob = y;
-            found = before + inc - x + __float2ll_rn(s * kSmFix) > target;
+          for (int e = 0; e < E; ++e) {
+            const float l = element<BF16>(q, e), y = l >= floor ? weight(l) : 0.f;
+            s += y;
+            if (!found && y > 0.f) {
+              mine_tok = first + mine * E + e;
+              mine_prob = y;
+              found = before + inc - x + __float2ll_rn(s * kSmFix) > target;
+            }
           }
         }
-        P.token[b] = tok;
-        if (P.prob) P.prob[b] = prob * kSmFix / static_cast<float>(Z);
-        P.row_status[b] = 0;
+        tok = __shfl_sync(FULL_MASK, mine_tok, who);
+        prob = __shfl_sync(FULL_MASK, mine_prob, who);
       }
-      return;
+      done = hit != 0;
+      before += __shfl_sync(FULL_MASK, inc, 31);
+    }
+    if (lane == 0) {
+      P.token[b] = tok;
+      if (P.prob) P.prob[b] = prob * kSmFix / static_cast<float>(Z);
+      P.row_status[b] = 0;
     }
   };
 
@@ -401,50 +453,59 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   const float near_floor = near ? M - (5.f - log2f(1.f - top_p)) / weight.sc : -INFINITY;
   float from = top_k && use_p ? -INFINITY : fmaxf(min_p_low, near_floor);
   if (top_k && top_k <= kSmThreads) {
-    uint32_t t = 0, mine[kSmThreads / 32];
+    uint32_t mine[kSmThreads / 32], least = 0xffffu;
 #pragma unroll
-    for (int i = 0; i < kSmThreads / 32; ++i) mine[i] = S.tmax[i * 32 + lane] >> 16;
+    for (int i = 0; i < kSmThreads / 32; ++i) least = min(least, mine[i] = S.tmax[i * 32 + lane] >> 16);
+    least = __reduce_min_sync(FULL_MASK, least);
+    // all of them reach the least; the bits below those that all have in common
+    const uint32_t apart = least ^ (top_key >> 16);
+    int bit = apart ? 31 - __clz(apart) : -1;
+    uint32_t t = bit < 0 ? least : least >> (bit + 1) << (bit + 1);
 #pragma unroll 1
-    for (int bit = 14; bit >= 0; bit -= 2) {  // two bits a round, three counts in a word
-      uint32_t n = 0;
+    for (; bit >= 0; --bit) {
+      const uint32_t x = t | 1u << bit;
+      int n = 0;
 #pragma unroll
-      for (int i = 0; i < kSmThreads / 32; ++i)
-#pragma unroll
-        for (int j = 1; j < 4; ++j) n += mine[i] >= (t | j << bit) ? 1u << (10 * (j - 1)) : 0u;
-      n = __reduce_add_sync(FULL_MASK, n);
-      const uint32_t k = top_k;
-      t |= ((n & 1023u) >= k ? (n >> 10 & 1023u) >= k ? (n >> 20) >= k ? 3u : 2u : 1u : 0u) << bit;
+      for (int i = 0; i < kSmThreads / 32; ++i) n += mine[i] >= x;
+      if (static_cast<int>(__reduce_add_sync(FULL_MASK, n)) >= top_k) t = x;
     }
     from = fmaxf(from, smp_from_key(max(t << 16, kSmMinusInf)));
   }
   const bool plain = !top_k && !use_p && !use_m, bounded = from > -INFINITY;
-  // --- the row's mass, and the logits from the bound on into the first CTA's
-  // list, warp by warp and so in vocabulary order
+  // --- the logits from the bound on into the first CTA's list, warp by warp and so
+  // in vocabulary order; and the row's mass
   int nseg = kSmWarps * ranks, seglen = kSmCands / nseg;
   i64 Z, within;
   {
     const int seg = rank * kSmWarps + warp;
     const bool count_near = near && from == near_floor;
-    i64 a = 0;
+    const i64 a = top > -INFINITY ? __float2ll_rn(mass * ex2((top - M) * weight.sc) * kSmFix) : 0;
     float c = 0.f;
     int n = 0;
-    for (int i0 = v0; i0 < v1; i0 += 32 * kSmAhead) {
-      uint4 q[kSmAhead];
+    // (only batches that hold one are looked at)
+    for (int i0 = v0, turn = 0; i0 < v1 && bounded; i0 += 32 * kSmBatch, ++turn) {
+      const bool here = i0 + lane < v1 && largest[turn * kSmThreads + tid] >= from;
+      if (!__any_sync(FULL_MASK, here)) continue;
+      u64 hits = 0;  // E bits for each of the batch's vectors
 #pragma unroll
-      for (int i = 0; i < kSmAhead; ++i)
-        if (i0 + i * 32 + lane < v1) q[i] = vector_at(i0 + i * 32 + lane);
+      for (int j = 0; j < kSmBatch; j += 4) {
+        uint4 q[4];
 #pragma unroll
-      for (int i = 0; i < kSmAhead; ++i) {
-        const int mine = i0 + i * 32 + lane;
-        if (i0 + i * 32 >= v1) break;
-        uint32_t bits = 0;  // of the vector's logits
-        if (mine < v1) {
-          a += vector_mass(q[i], -INFINITY, true);
-          if (bounded && vector_max<BF16>(q[i]) >= from) {
+        for (int i = 0; i < 4; ++i)
+          if (here && i0 + (j + i) * 32 + lane < v1) q[i] = vector_at(i0 + (j + i) * 32 + lane);
 #pragma unroll
-            for (int e = 0; e < E; ++e) bits |= element<BF16>(q[i], e) >= from ? 1u << e : 0u;
+        for (int i = 0; i < 4; ++i)
+          if (here && i0 + (j + i) * 32 + lane < v1 && vector_max<BF16>(q[i]) >= from) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) m |= element<BF16>(q[i], e) >= from ? 1u << e : 0u;
+            hits |= static_cast<u64>(m) << ((j + i) * E);
           }
-        }
+      }
+#pragma unroll 1
+      for (int i = 0; i < kSmBatch; ++i) {
+        const int mine = i0 + i * 32 + lane;
+        uint32_t bits = static_cast<uint32_t>(hits >> (i * E)) & ((1u << E) - 1u);
         const unsigned some = __ballot_sync(FULL_MASK, bits != 0);
         if (!some) continue;
         int to, all;  // the lane's first place, and places for the warp
@@ -484,7 +545,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     // (the second sum is a bound: cut by more than its rounding)
     const int r = exchange(a, __float2ll_rn(c * (kSmFix * (1.f - 0x1p-14f))), Z, within);
     if (plain) {
-      choose(-INFINITY, true, r, Z);
+      choose(-INFINITY, r, Z);
       return;
     }
     if (!count_near) within = Z;  // the bound holds as it is
@@ -620,7 +681,8 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const float l = element<BF16>(q, e);
-            if (l >= from) st_cluster_u64(&S.cand[rank * share + to++], 0, static_cast<u64>(smp_key(l)) << 32 | static_cast<uint32_t>(first + mine * E + e));
+            // (the bound on `to` holds even if another stream is writing the row meanwhile)
+            if (l >= from && to < share) st_cluster_u64(&S.cand[rank * share + to++], 0, static_cast<u64>(smp_key(l)) << 32 | static_cast<uint32_t>(first + mine * E + e));
           }
         }
         at += __shfl_sync(FULL_MASK, inc, 31);
@@ -664,7 +726,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       floor = max(floor, lo << kLow);
     }
     const int r = reach(floor, mass, count);
-    choose(smp_from_key(floor), false, r, mass);
+    choose(smp_from_key(floor), r, mass);
     return;
   }
   if (rank != 0) return;
@@ -834,7 +896,7 @@ cudaError_t launch_sample(const SampleParams &p, int ranks, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (!(done.load(std::memory_order_relaxed) & bit)) {
-      e = cudaFuncSetAttribute(sample_kernel<BF16, VEC, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
+      e = cudaFuncSetAttribute(sample_kernel<BF16, VEC, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, 144 << 10);
       if (e != cudaSuccess) return e;
       done.fetch_or(bit, std::memory_order_relaxed);
     }
@@ -842,7 +904,7 @@ cudaError_t launch_sample(const SampleParams &p, int ranks, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * ranks);
   cfg.blockDim = dim3(kSmThreads);
-  cfg.dynamicSmemBytes = KEEP ? static_cast<size_t>(p.slice) * (BF16 ? 2 : 4) : 0;
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.batches) * kSmThreads * 4 + (KEEP ? static_cast<size_t>(p.slice) * (BF16 ? 2 : 4) : 0);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -903,6 +965,9 @@ spec_status spec_sample(const spec_sample_args *a, const spec_sample_out *o, voi
   }
   const int unit = 16 / esz;
   p.slice = ((a->V + ranks - 1) / ranks + unit - 1) / unit * unit;
+  // (a warp's vectors are whole rows of 32, as in the kernel)
+  const int turns = (p.slice / unit + 32 * kSmWarps - 1) / (32 * kSmWarps);
+  p.batches = (turns + kSmBatch - 1) / kSmBatch;
   const bool vec = smp_aligned(a->logits, 16) && (a->row_stride * esz) % 16 == 0 && bytes % 16 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = bf16 ? (vec ? launch_sample<true, true>(p, ranks, keep, s) : launch_sample<true, false>(p, ranks, keep, s))
