@@ -101,7 +101,74 @@ struct PagedRowCfg {
   static constexpr int kWarps = MT == 2 || !E4 ? 8 : 12;    // items per SM
 };
 
-// Items: x: KV head and block of kM query rows, y: part, z: row.
+// How a few rows of any lengths are cut into at most `budget` parts that run side
+// by side, none much longer than another (the lanes of a warp together): item
+// `idx` is part `split` of row `b`, of its `parts`.  A lane keeps rows 4 lane ..
+// 4 lane + 3.  A row of w groups makes max(1, ceil(w / c)) parts, and c is the
+// least, searched upwards from sum w / budget, for which the budget holds: it
+// does for c = sum w / (budget - B) + 1, since sum ceil(w / c) <= sum w / c + B.
+__device__ __forceinline__ void cut_groups(const PagedParams &P, int idx, int &b, int &split, int &parts) {
+  const int lane = threadIdx.x % 32;
+  uint32_t w[kKeep], sum = 0, top = 0;
+#pragma unroll
+  for (int q = 0; q < kKeep; ++q) {
+    const int r = lane * kKeep + q;
+    w[q] = 0;
+    if (r < P.B) {
+      int n;
+      const int c = paged_queries(P, r, n);
+      if (c > 0) w[q] = Keys(P, n, n + c).n;  // < 2^24 (checked by the caller)
+    }
+    sum += w[q];
+    top = max(top, w[q]);
+  }
+  sum = __reduce_add_sync(FULL_MASK, sum);
+  top = __reduce_max_sync(FULL_MASK, top);
+  const uint32_t least = max((top + P.splits - 1) / P.splits, static_cast<uint32_t>(P.min_groups));
+  const uint32_t most = sum / (P.budget - P.B) + 1;
+  uint32_t c = sum / P.budget + 1, n[kKeep], mine;
+  while (true) {
+    c = max(min(c, most), least);
+    mine = 0;
+    const float inv = 1.f / static_cast<float>(c);
+#pragma unroll
+    for (int q = 0; q < kKeep; ++q) {
+      n[q] = lane * kKeep + q < P.B ? max(1u, ceil_quotient(w[q], c, inv)) : 0u;
+      mine += n[q];
+    }
+    if (c >= most || __reduce_add_sync(FULL_MASK, mine) <= static_cast<uint32_t>(P.budget)) break;
+    c += c / 16 + 1;
+  }
+  // the row of item idx: running sums over the lanes
+  uint32_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(FULL_MASK, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const uint32_t from = upto - mine;
+  const unsigned owner = __ballot_sync(FULL_MASK, static_cast<uint32_t>(idx) >= from && static_cast<uint32_t>(idx) < upto);
+  b = -1;
+  if (!owner) return;  // past the last part
+  uint32_t k = idx - from;
+  int row = lane * kKeep, cnt = 0;
+#pragma unroll
+  for (int q = 0; q < kKeep; ++q) {
+    if (q < kKeep - 1 && row == lane * kKeep + q && k >= n[q]) {
+      k -= n[q];
+      ++row;
+    } else if (row == lane * kKeep + q) {
+      cnt = static_cast<int>(n[q]);
+    }
+  }
+  const int src = __ffs(owner) - 1;
+  b = __shfl_sync(FULL_MASK, row, src);
+  split = __shfl_sync(FULL_MASK, static_cast<int>(k), src);
+  parts = __shfl_sync(FULL_MASK, cnt, src);
+}
+
+// Items: x: KV head and block of kM query rows, y: part, z: row; or (cut by a
+// budget) y: a part of any row, z: 0.
 template <int CT, int DP, int MT>
 __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, MT>::kWarps) paged_rows_kernel(const __grid_constant__ PagedParams P) {
   using C = PagedRowCfg<CT, DP, MT>;
@@ -115,9 +182,17 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, MT>::kWarps) paged_row
 
   // --- the item: KV heads first (the heads of a token lie side by side in
   // memory, so the items that run together read whole entries), then parts
-  const int b = blockIdx.z, split = blockIdx.y;
+  int b = blockIdx.z, split = blockIdx.y, parts = P.splits;
   const int blk = blockIdx.x / static_cast<unsigned>(P.H), g = blockIdx.x - blk * P.H;
   const int blocks = gridDim.x / P.H;
+  if (P.budget > 0) {
+    cut_groups(P, split, b, split, parts);
+    if (b < 0) {
+      grid_dependency_wait();
+      return;
+    }
+    if (split == 0 && blk == 0 && g == 0 && lane == 0) P.nparts[b] = parts;
+  }
   const int r0 = blk * C::kM, nrows = P.N * P.G;
   const long long flag = ((static_cast<long long>(b) * P.H + g) * blocks + blk) * P.splits + split;
   int n;
@@ -145,7 +220,7 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, MT>::kWarps) paged_row
   const Keys keys(P, p0, end);
   int g0 = 0, g1 = keys.n;
   if (P.splits > 1) {
-    const int per = max(P.min_groups, (keys.n + P.splits - 1) / P.splits);
+    const int per = max(P.min_groups, (keys.n + parts - 1) / parts);
     g0 = min(keys.n, split * per);
     g1 = min(keys.n, g0 + per);
   }
@@ -655,7 +730,8 @@ __global__ void __launch_bounds__(kPaJoinThreads) paged_join_kernel(const __grid
   float Z = -INFINITY;
   bool gone = false;  // a part's kernel gave up waiting: the row is flagged and its answer left empty
   float2 ml = make_float2(-INFINITY, -INFINITY);  // this lane's part (there are 32 at most)
-  if (on && lane < P.splits) ml = P.ml[static_cast<long long>(lane) * P.rows + r];
+  const int parts = P.budget > 0 ? P.nparts[b] : P.splits;
+  if (on && lane < parts) ml = P.ml[static_cast<long long>(lane) * P.rows + r];
   gone = __any_sync(FULL_MASK, __float_as_uint(ml.y) == kTimeoutBits);
   if (gone && lane == 0 && P.row_status) P.row_status[b] = SPEC_ROW_TIMEOUT;
   Z = ml.y;
@@ -692,7 +768,7 @@ __global__ void __launch_bounds__(kPaJoinThreads) paged_join_kernel(const __grid
     }
     const int g = h / P.G, blocks = (P.N * P.G + P.oblk - 1) / P.oblk;
     const int32_t *flag = P.oflag + ((static_cast<long long>(b) * P.H + g) * blocks + (qt * P.G + h % P.G) / P.oblk) * P.splits;
-    if (__any_sync(FULL_MASK, lane < P.splits && flag[lane])) {
+    if (__any_sync(FULL_MASK, lane < parts && flag[lane])) {
       const int n = P.kv_len[b], p = n + (P.anc ? P.depth[static_cast<size_t>(b) * P.N + qt] : qt);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -710,7 +786,7 @@ template <int CT, int DP, int MT>
 cudaError_t launch_rows(const PagedParams &p, cudaStream_t s) {
   using C = PagedRowCfg<CT, DP, MT>;
   const int blocks = (p.N * p.G + C::kM - 1) / C::kM;
-  const dim3 grid(p.H * blocks, p.splits, p.B);
+  const dim3 grid(p.H * blocks, p.budget > 0 ? p.budget : p.splits, p.budget > 0 ? 1 : p.B);
   const cudaError_t e = allow_smem<paged_rows_kernel<CT, DP, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
   return launch_after(paged_rows_kernel<CT, DP, MT>, grid, 32, C::kSmem, s, true, p);
@@ -723,10 +799,16 @@ cudaError_t launch_rows_d(const PagedParams &p, cudaStream_t s) {
   return two ? launch_rows<CT, 128, 2>(p, s) : launch_rows<CT, 128, 1>(p, s);
 }
 
+// Items of the rows kernel that run on an SM at a time.
+int rows_per_sm(int dtype, int oblk) {
+  if (dtype == SPEC_E4M3) return oblk == 16 ? PagedRowCfg<SPEC_E4M3, 128, 1>::kWarps : PagedRowCfg<SPEC_E4M3, 128, 2>::kWarps;
+  return oblk == 16 ? PagedRowCfg<SPEC_BF16, 128, 1>::kWarps : PagedRowCfg<SPEC_BF16, 128, 2>::kWarps;
+}
+
 struct PagedPlan {
   bool tile;           // paged_tile_kernel
-  int splits, oblk, W;
-  size_t rows, info_at, anc_at, depth_at, flag_at, ml_at, part_at, bytes;
+  int splits, budget, oblk, W;
+  size_t rows, info_at, count_at, anc_at, depth_at, flag_at, ml_at, part_at, bytes;
 };
 
 size_t pa_round(size_t x) { return (x + 255) / 256 * 256; }
@@ -779,11 +861,19 @@ PagedPlan plan_paged(const spec_paged_attention_args *a) {
   } else {
     const long long want = (8LL * kPagedSms * 2 + items - 1) / items;
     p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 32})));
+    // A few rows are cut by a budget of parts, all items side by side.
+    const long long budget = static_cast<long long>(rows_per_sm(a->cache_dtype, p.oblk)) * kPagedSms / a->heads;
+    if (blocks == 1 && a->B <= kMaxCutRows && budget > a->B) {
+      p.budget = static_cast<int>(budget);
+      p.splits = static_cast<int>(std::min<long long>({32, (tokens + 63) / 64, budget - a->B + 1}));
+    }
   }
   p.W = a->parent ? (a->N + 31) / 32 : 0;
   const size_t q = static_cast<size_t>(a->B) * a->N;
   size_t at = 0;
   p.info_at = at;
+  at += pa_round(static_cast<size_t>(a->B) * 4);
+  p.count_at = at;
   at += pa_round(static_cast<size_t>(a->B) * 4);
   p.anc_at = at;
   at += pa_round(q * p.W * 4);
@@ -852,6 +942,8 @@ spec_status spec_paged_attention(const spec_paged_attention_args *a, void *out, 
   p.W = plan.W;
   p.rows = static_cast<int>(plan.rows);
   p.splits = plan.splits;
+  p.budget = plan.splits > 1 ? plan.budget : 0;
+  p.nparts = reinterpret_cast<int32_t *>(w + plan.count_at);
   p.min_groups = 4;
   p.oblk = plan.oblk;
   p.ml = reinterpret_cast<float2 *>(w + plan.ml_at);

@@ -51,7 +51,9 @@ struct PagedParams {
   float *part;
   float2 *ml;
   int rows;                    // B * N * Hq
-  int splits;                  // parts of an item's keys; 1: the answers are written at once
+  int splits;                  // parts of an item's keys, at most; 1: the answers are written at once
+  int budget;                  // > 0: the rows are cut into at most this many parts (cut_groups) ...
+  int32_t *nparts;             // ... each into this many
   int min_groups;              // groups in a part, at least
   int oblk;                    // query rows per item
   int32_t *oflag;              // per item and part: a value that is not finite was left out of its sums
