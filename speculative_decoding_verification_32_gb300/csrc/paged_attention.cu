@@ -7,7 +7,7 @@
 //    tokens it sees.  The attention kernel runs beside it and looks at the
 //    result before it writes anything.
 //  paged_tile_kernel (paged_attention_tile.cu) -- many query rows.
-//  paged_rows_kernel -- 16 or 32 query rows (the query heads of one KV head and
+//  paged_rows_kernel -- 8 to 32 query rows (the query heads of one KV head and
 //    tokens of one row) against a part of their keys, one warp.
 //  paged_join_kernel -- one warp per query row adds up the parts.
 #include <cuda_bf16.h>
@@ -84,22 +84,35 @@ __global__ void __launch_bounds__(kCheckThreads) paged_check_kernel(const __grid
 }
 
 // ------------------------------------------------------------- row kernel
-template <int CT, int DP, int MT>
+// The products are made the other way round: scores as K Q^T, sums as V^T P^T, so
+// that keys fill the matrix instruction's 16 rows and query rows go in eights: 4
+// rows of a decoding token are padded to 8, 24 of a chain not at all.  (With the
+// queries as the 16 rows every item did twice to 4/3 of the work, at twice the
+// registers: 64 decoding rows in e4m3 100 us, 64 chains of 24 in bf16 97.)
+template <int CT, int DP, int NT>
 struct PagedRowCfg {
   static constexpr bool E4 = CT == SPEC_E4M3;
   static constexpr int kEsz = E4 ? 1 : 2;
-  static constexpr int kM = 16 * MT;                        // query rows
-  static constexpr int kStages = 3;
+  static constexpr int kM = 8 * NT;                         // query rows
+  static constexpr int kStages = E4 ? 3 : 2;
   static constexpr int kPitch = DP * kEsz + 16;             // bytes of one token in a ring slot
   static constexpr int kPlane = kGroup * kPitch;            // K or V of a group
   static constexpr int kScales = E4 ? 2 * kGroup * 4 : 0;   // scale words, K then V
-  static constexpr int kTable = E4 ? kGroup * 8 : 0;        // what they come to, per token
   static constexpr int kStage = 2 * kPlane + kScales;
   static constexpr int kQPitch = DP * 2 + 16;
   static constexpr int kQ = kM * kQPitch + kM * 4;          // queries and factors, in the last slot before it is used
-  static constexpr int kSmem = (kStages - 1) * kStage + (kStage > kQ ? kStage : kQ) + kTable;
-  static constexpr int kWarps = MT == 2 || !E4 ? 8 : 12;    // items per SM
+  static constexpr int kOPitch = DP + 4;                    // floats: eight rows of sums at the end
+  static constexpr int kLast = (kStages - 1) * kStage + (kStage > kQ ? kStage : kQ);
+  static constexpr int kSmem = kLast > 8 * kOPitch * 4 ? kLast : 8 * kOPitch * 4;
+  static constexpr int kWarps = DP <= 64 ? (NT <= 2 ? 16 : 12) : NT <= 1 ? (E4 ? 14 : 12) : NT == 2 ? 12 : 8;  // items per SM
 };
+
+// The 8 x 8 matrix of 16-bit numbers whose rows the lanes' quads hold, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
 
 // How a few rows of any lengths are cut into at most `budget` parts that run side
 // by side, none much longer than another (the lanes of a warp together): item
@@ -169,12 +182,12 @@ __device__ __forceinline__ void cut_groups(const PagedParams &P, int idx, int &b
 
 // Items: x: KV head and block of kM query rows, y: part, z: row; or (cut by a
 // budget) y: a part of any row, z: 0.
-template <int CT, int DP, int MT>
-__global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, MT>::kWarps) paged_rows_kernel(const __grid_constant__ PagedParams P) {
-  using C = PagedRowCfg<CT, DP, MT>;
+template <int CT, int DP, int NT>
+__global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_rows_kernel(const __grid_constant__ PagedParams P) {
+  using C = PagedRowCfg<CT, DP, NT>;
   constexpr bool E4 = C::E4;
   constexpr bool BF = CT == SPEC_BF16;
-  constexpr int kSteps = DP / 16, kNt = DP / 8;  // k-steps of the scores, column tiles of the sums
+  constexpr int kSteps = DP / 16;  // steps of the scores' contraction, tiles of the sums' rows
   extern __shared__ __align__(16) unsigned char smem[];
   unsigned char *const qsm = smem + (C::kStages - 1) * C::kStage;
   float *const qfac = reinterpret_cast<float *>(qsm + C::kM * C::kQPitch);
@@ -336,49 +349,49 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, MT>::kWarps) paged_row
   // Fragments.  The contraction over d may run in any order as long as Q and
   // K agree: for codes a thread takes DP/4 consecutive d (a few 16-byte
   // reads), for 16-bit entries the order ldmatrix gives.
-  uint32_t qf[MT][kSteps][4];
-  float rf[MT][2];
+  uint32_t qf[NT][kSteps][2];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int rr = mt * 16 + hf * 8 + quad;
-      rf[mt][hf] = qfac[rr];
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int d0 = E4 ? j4 * (DP / 4) + s * 4 : s * 16 + j4 * 2;
-        const int d1 = E4 ? d0 + 2 : d0 + 8;
-        qf[mt][s][hf] = *reinterpret_cast<const uint32_t *>(qsm + rr * C::kQPitch + d0 * 2);
-        qf[mt][s][2 + hf] = *reinterpret_cast<const uint32_t *>(qsm + rr * C::kQPitch + d1 * 2);
-      }
+    for (int s = 0; s < kSteps; ++s) {
+      const int d0 = E4 ? j4 * (DP / 4) + s * 4 : s * 16 + j4 * 2, d1 = E4 ? d0 + 2 : d0 + 8;
+      qf[t][s][0] = *reinterpret_cast<const uint32_t *>(qsm + (t * 8 + quad) * C::kQPitch + d0 * 2);
+      qf[t][s][1] = *reinterpret_cast<const uint32_t *>(qsm + (t * 8 + quad) * C::kQPitch + d1 * 2);
     }
-  }
+  // the thread's query rows 8 t + 2 j4 and the next: factors, for the masks tokens and positions
+  float rf[NT][2];
+  int qtok[NT][2], qpos[NT][2];
+  bool scaled = false;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int rr = t * 8 + 2 * j4 + c;
+      rf[t][c] = qfac[rr];
+      scaled = scaled || rf[t][c] != 1.f;
+      qtok[t][c] = min((r0 + rr) / P.G, P.N - 1);
+      qpos[t][c] = __shfl_sync(FULL_MASK, my_pos, rr);
+    }
+  scaled = E4 && __any_sync(FULL_MASK, scaled);
   if (P.D < DP) {  // the slot's padding columns were queries
     __syncwarp();
     for (int i = lane; i < C::kStage / 16; i += 32) *reinterpret_cast<uint4 *>(qsm + i * 16) = make_uint4(0, 0, 0, 0);
   }
   __syncwarp();
-  // each thread's rows, for the masks
-  int qtok[MT][2], qpos[MT][2];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      qtok[mt][hf] = min((r0 + mt * 16 + hf * 8 + quad) / P.G, P.N - 1);
-      qpos[mt][hf] = __shfl_sync(FULL_MASK, my_pos, mt * 16 + hf * 8 + quad);
-    }
 
-  float o[MT][kNt][4];
+  // sums: tile s of 16 columns d; components d of the quad and the other half's,
+  // each of the thread's two query rows
+  float o[kSteps][NT][4];
   // l counts in units of 2^mx, o in units of 2^mv (one and the same for 16-bit entries)
-  float mx[MT][2], mv[MT][2], l[MT][2];
+  float mx[NT][2], mv[NT][2], l[NT][2];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    mx[mt][0] = mx[mt][1] = mv[mt][0] = mv[mt][1] = -INFINITY;
-    l[mt][0] = l[mt][1] = 0.f;
+  for (int t = 0; t < NT; ++t) {
+    mx[t][0] = mx[t][1] = mv[t][0] = mv[t][1] = -INFINITY;
+    l[t][0] = l[t][1] = 0.f;
 #pragma unroll
-    for (int t = 0; t < kNt; ++t)
+    for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[mt][t][c] = 0.f;
+      for (int c = 0; c < 4; ++c) o[s][t][c] = 0.f;
   }
 
   bool odd = false;
@@ -391,178 +404,6 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, MT>::kWarps) paged_row
     const int tb = keys.token(gi);
     // some query of the block does not see some token of the group
     const bool masked = tb + kGroup - 1 > (tree ? n - 1 : p0) || (tb + kGroup > P.sinks && tb < window_from(P, p1));
-    // --- scores: token n * 8 + 2 j4 + {0, 1} of rows quad and quad + 8
-    float x[MT][2][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[mt][t][c] = 0.f;
-    if constexpr (E4) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint32_t at = kst + (t * 8 + quad) * C::kPitch + j4 * (DP / 4);
-#pragma unroll
-        for (int s0 = 0; s0 < kSteps; s0 += 4) {
-          uint32_t w[4];
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(at + s0 * 4)
-                       : "memory");
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const uint32_t b0 = e4m3x2_to_f16x2(w[s]), b1 = e4m3x2_to_f16x2_hi(w[s]);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816<false>(x[mt][t], qf[mt][s0 + s], b0, b1);
-          }
-        }
-      }
-    } else {
-      // matrices: (tokens 0-7, d 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
-      const uint32_t at = kst + ((lane / 16) * 8 + lane % 8) * C::kPitch + ((lane / 8) % 2) * 16;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        uint32_t kf[4];
-        ldmatrix_x4(kf, at + s * 32);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816<BF>(x[mt][0], qf[mt][s], kf[0], kf[1]);
-          mma16816<BF>(x[mt][1], qf[mt][s], kf[2], kf[3]);
-        }
-      }
-    }
-    // --- to base-2 exponents
-    float ve[2][2];  // the values' scale exponents
-    if constexpr (E4) {
-      uint32_t w;
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(sst + lane * 4) : "memory");
-      const uint32_t byte = w >> (8 * (g & 3)) & 255u;
-      // value vectors of NaN: the keys alone decide the softmax, and the NaN comes in with the values
-      const unsigned nans = __ballot_sync(FULL_MASK, byte == 255u) >> kGroup;
-      if (nans) {
-        for (int tk = 0; tk < kGroup; ++tk) {
-          if (!(nans >> tk & 1u)) continue;
-          if (masked)  // not every query sees it: put into the answers of those that do
-            odd = true;
-          else if (lane * 4 < P.D)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(vst + tk * C::kPitch + lane * 4), "r"(0x7f7f7f7fu) : "memory");
-        }
-        __syncwarp();
-      }
-      const uint32_t tab = smem_u32(smem) + C::kSmem - C::kTable;
-      if (lane < kGroup)
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(tab + lane * 8), "f"(P.scale * e4m3_scale(byte)) : "memory");
-      else
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(tab + (lane - kGroup) * 8 + 4), "f"(byte == 255u ? 0.f : scale_exponent(byte)) : "memory");
-      __syncwarp();
-      float ks[2][2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(ks[t][0]), "=f"(ve[t][0]), "=f"(ks[t][1]), "=f"(ve[t][1])
-                     : "r"(tab + (t * 8 + 2 * j4) * 8)
-                     : "memory");
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[mt][t][c] *= rf[mt][c >> 1] * ks[t][c & 1];
-    } else {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[mt][t][c] *= P.scale;
-    }
-    if (masked) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int tk = tb + t * 8 + 2 * j4 + (c & 1);
-            if (tk >= end || !paged_sees(P, b, qtok[mt][c >> 1], n, qpos[mt][c >> 1], tk)) x[mt][t][c] = -INFINITY;
-          }
-    }
-    // --- softmax.  A row's references follow its maxima only when these have
-    // grown by more than 2^kPaLazy (weights up to that are as exact), whatever
-    // other rows' do: nothing of a row depends on its neighbours in the block.
-    float tm[MT][2], tv[MT][2];
-    bool grown = false;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        tm[mt][hf] = fmaxf(fmaxf(x[mt][0][2 * hf], x[mt][0][2 * hf + 1]), fmaxf(x[mt][1][2 * hf], x[mt][1][2 * hf + 1]));
-        grown = grown || tm[mt][hf] > mx[mt][hf] + kPaLazy || mx[mt][hf] == -INFINITY;
-        if constexpr (E4) {
-          tv[mt][hf] = fmaxf(fmaxf(x[mt][0][2 * hf] + ve[0][0], x[mt][0][2 * hf + 1] + ve[0][1]),
-                             fmaxf(x[mt][1][2 * hf] + ve[1][0], x[mt][1][2 * hf + 1] + ve[1][1]));
-          grown = grown || tv[mt][hf] > mv[mt][hf] + kPaLazy;
-        }
-      }
-    if (__any_sync(FULL_MASK, grown)) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float al[2];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float t = tm[mt][hf];
-          t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 1));
-          t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 2));
-          al[hf] = 1.f;
-          if (t > mx[mt][hf] + kPaLazy || (mx[mt][hf] == -INFINITY && t > -INFINITY)) {
-            al[hf] = ex2(mx[mt][hf] - t);
-            l[mt][hf] *= al[hf];
-            mx[mt][hf] = t;
-          }
-          if constexpr (E4) {
-            t = tv[mt][hf];
-            t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 1));
-            t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 2));
-            al[hf] = 1.f;
-            if (t > mv[mt][hf] + kPaLazy || (mv[mt][hf] == -INFINITY && t > -INFINITY)) {
-              al[hf] = ex2(mv[mt][hf] - t);
-              mv[mt][hf] = t;
-            }
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < kNt; ++t) {
-          o[mt][t][0] *= al[0];
-          o[mt][t][1] *= al[0];
-          o[mt][t][2] *= al[1];
-          o[mt][t][3] *= al[1];
-        }
-      }
-    }
-    uint32_t pf[MT][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float ref = mx[mt][hf] == -INFINITY ? 0.f : mx[mt][hf], rev = mv[mt][hf] == -INFINITY ? 0.f : mv[mt][hf];
-        float add = 0.f;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float &y = x[mt][t][2 * hf + c];
-            const float w = ex2(y - ref);
-            add += w;
-            y = E4 ? ex2(y + (ve[t][c] - rev)) : w;
-          }
-        l[mt][hf] += add;
-      }
-      pf[mt][0] = pack16<BF>(x[mt][0][0], x[mt][0][1]);
-      pf[mt][1] = pack16<BF>(x[mt][0][2], x[mt][0][3]);
-      pf[mt][2] = pack16<BF>(x[mt][1][0], x[mt][1][1]);
-      pf[mt][3] = pack16<BF>(x[mt][1][2], x[mt][1][3]);
-    }
     // --- in masked groups, values that are not finite are taken out
     if (masked) {
       bool bad = false;
@@ -591,45 +432,207 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, MT>::kWarps) paged_row
       odd = __any_sync(FULL_MASK, bad) || odd;
       __syncwarp();
     }
-    // --- weights times values
+    // lane i < 16: token i's key scale; lane 16 + i: its value scale
+    uint32_t byte = 0;
     if constexpr (E4) {
-      // tokens 2 j4, 2 j4 + 1, 8 + 2 j4, 9 + 2 j4 of columns quad * kNt + n
+      uint32_t w;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(sst + lane * 4) : "memory");
+      byte = w >> (8 * (g & 3)) & 255u;
+      // value vectors of NaN: the keys alone decide the softmax, and the NaN comes in with the values
+      const unsigned nans = __ballot_sync(FULL_MASK, byte == 255u) >> kGroup;
+      if (nans) {
+        for (int tk = 0; tk < kGroup; ++tk) {
+          if (!(nans >> tk & 1u)) continue;
+          if (masked)  // not every query sees it: put into the answers of those that do
+            odd = true;
+          else if (lane * 4 < P.D)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(vst + tk * C::kPitch + lane * 4), "r"(0x7f7f7f7fu) : "memory");
+        }
+        __syncwarp();
+      }
+    }
+    // --- scores: tokens quad (c < 2) and quad + 8, query rows 8 t + 2 j4 + c % 2
+    // (two sums each, for shorter chains)
+    float x[NT][4], x2[NT][4];
 #pragma unroll
-      for (int n0 = 0; n0 < kNt; n0 += 8) {
-        uint32_t w[4][2];
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                       : "=r"(w[t][0]), "=r"(w[t][1])
-                       : "r"(vst + ((t / 2) * 8 + 2 * j4 + t % 2) * C::kPitch + quad * kNt + n0)
+      for (int c = 0; c < 4; ++c) x[t][c] = x2[t][c] = 0.f;
+    if constexpr (E4) {
+      const uint32_t at = kst + quad * C::kPitch + j4 * (DP / 4);
+#pragma unroll
+      for (int s0 = 0; s0 < kSteps; s0 += 4) {
+        uint32_t w[2][4];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[hf][0]), "=r"(w[hf][1]), "=r"(w[hf][2]), "=r"(w[hf][3])
+                       : "r"(at + hf * 8 * C::kPitch + s0 * 4)
                        : "memory");
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const uint32_t kf[4] = {e4m3x2_to_f16x2(w[0][s]), e4m3x2_to_f16x2(w[1][s]), e4m3x2_to_f16x2_hi(w[0][s]), e4m3x2_to_f16x2_hi(w[1][s])};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma16816<false>(s & 1 ? x2[t] : x[t], kf, qf[t][s0 + s][0], qf[t][s0 + s][1]);
+        }
+      }
+    } else {
+      // matrices: (tokens 0-7, d 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+      const uint32_t at = kst + (lane % 16) * C::kPitch + (lane / 16) * 16;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint32_t kf[4];
+        ldmatrix_x4(kf, at + s * 32);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma16816<BF>(s & 1 ? x2[t] : x[t], kf, qf[t][s][0], qf[t][s][1]);
+      }
+    }
+    // the values' loads, ahead of what their weights take
+    constexpr int kCols = DP / 8;  // codes: columns of a quad
+    constexpr bool kEarly = E4 ? NT <= 2 : NT <= 3;
+    uint32_t vw[E4 ? kCols / 8 : 1][4][2], vf[E4 ? 1 : kSteps][4];
+    auto load_codes = [&](int n0) {
+      // of tokens 2 j4, 2 j4 + 1, 8 + 2 j4, 9 + 2 j4 the quad's columns
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(vw[n0 / 8][t][0]), "=r"(vw[n0 / 8][t][1])
+                     : "r"(vst + ((t / 2) * 8 + 2 * j4 + t % 2) * C::kPitch + quad * kCols + n0)
+                     : "memory");
+    };
+    // matrices: (tokens 0-7, d 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15), each transposed
+    const uint32_t vat = vst + ((lane / 16) * 8 + lane % 8) * C::kPitch + ((lane / 8) % 2) * 16;
+    if constexpr (kEarly && E4) {
+#pragma unroll
+      for (int n0 = 0; n0 < kCols; n0 += 8) load_codes(n0);
+    } else if constexpr (kEarly) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) ldmatrix_x4_trans(vf[s], vat + s * 32);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[t][c] += x2[t][c];
+    // --- to base-2 exponents
+    float ve[2] = {0.f, 0.f};  // the values' scale exponents of the thread's two tokens
+    if constexpr (E4) {
+      const float mine = lane < kGroup ? P.scale * e4m3_scale(byte) : byte == 255u ? 0.f : scale_exponent(byte);
+      float ks[2];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        ks[hf] = __shfl_sync(FULL_MASK, mine, quad + 8 * hf);
+        ve[hf] = __shfl_sync(FULL_MASK, mine, kGroup + quad + 8 * hf);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[t][c] *= ks[c >> 1];
+      if (scaled) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[t][c] *= rf[t][c & 1];
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[t][c] *= P.scale;
+    }
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int tk = tb + quad + 8 * (c >> 1);
+          if (tk >= end || !paged_sees(P, b, qtok[t][c & 1], n, qpos[t][c & 1], tk)) x[t][c] = -INFINITY;
+        }
+    }
+    // --- softmax.  A row's references follow its maxima only when these have
+    // grown by more than 2^kPaLazy (weights up to that are as exact), whatever
+    // other rows' do: nothing of a row depends on its neighbours in the block.
+    bool grown = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float a = fmaxf(x[t][c], x[t][2 + c]);
+        grown = grown || a > mx[t][c] + kPaLazy || mx[t][c] == -INFINITY;
+        if constexpr (E4) grown = grown || fmaxf(x[t][c] + ve[0], x[t][2 + c] + ve[1]) > mv[t][c] + kPaLazy;
+      }
+    if (__any_sync(FULL_MASK, grown)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float al[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float a = fmaxf(x[t][c], x[t][2 + c]);
+#pragma unroll
+          for (int q = 4; q < 32; q <<= 1) a = fmaxf(a, __shfl_xor_sync(FULL_MASK, a, q));
+          al[c] = 1.f;
+          if (a > mx[t][c] + kPaLazy || (mx[t][c] == -INFINITY && a > -INFINITY)) {
+            al[c] = ex2(mx[t][c] - a);
+            l[t][c] *= al[c];
+            mx[t][c] = a;
+          }
+          if constexpr (E4) {
+            a = fmaxf(x[t][c] + ve[0], x[t][2 + c] + ve[1]);
+#pragma unroll
+            for (int q = 4; q < 32; q <<= 1) a = fmaxf(a, __shfl_xor_sync(FULL_MASK, a, q));
+            al[c] = 1.f;
+            if (a > mv[t][c] + kPaLazy || (mv[t][c] == -INFINITY && a > -INFINITY)) {
+              al[c] = ex2(mv[t][c] - a);
+              mv[t][c] = a;
+            }
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[s][t][c] *= al[c & 1];
+      }
+    }
+    uint32_t pf[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float ref = mx[t][c] == -INFINITY ? 0.f : mx[t][c], rev = mv[t][c] == -INFINITY ? 0.f : mv[t][c];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float &y = x[t][2 * hf + c];
+          const float w = ex2(y - ref);
+          l[t][c] += w;
+          y = E4 ? ex2(y + (ve[hf] - rev)) : w;
+        }
+      }
+      pf[t][0] = transpose8(pack16<BF>(x[t][0], x[t][1]));
+      pf[t][1] = transpose8(pack16<BF>(x[t][2], x[t][3]));
+    }
+    // --- values times weights
+    if constexpr (E4) {
+      // a tile takes two of the quad's columns
+#pragma unroll
+      for (int n0 = 0; n0 < kCols; n0 += 8) {
+        if constexpr (!kEarly) load_codes(n0);
+        const uint32_t(&w)[4][2] = vw[n0 / 8];
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           // bytes i, i + 1 of two tokens: (t0 i, t1 i, t0 i+1, t1 i+1)
           const uint32_t sel = i % 4 == 0 ? 0x5140u : 0x7362u;
           const uint32_t lo = __byte_perm(w[0][i / 4], w[1][i / 4], sel);
           const uint32_t hi = __byte_perm(w[2][i / 4], w[3][i / 4], sel);
-          const uint32_t b0 = e4m3x2_to_f16x2(lo), b1 = e4m3x2_to_f16x2(hi);
-          const uint32_t c0 = e4m3x2_to_f16x2_hi(lo), c1 = e4m3x2_to_f16x2_hi(hi);
+          const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2_hi(lo), e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2_hi(hi)};
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816<false>(o[mt][n0 + i], pf[mt], b0, b1);
-            mma16816<false>(o[mt][n0 + i + 1], pf[mt], c0, c1);
-          }
+          for (int t = 0; t < NT; ++t) mma16816<false>(o[(n0 + i) / 2][t], a, pf[t][0], pf[t][1]);
         }
       }
     } else {
-      // matrices: (tokens 0-7, d 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
-      const uint32_t at = vst + (lane % 16) * C::kPitch + (lane / 16) * 16;
 #pragma unroll
-      for (int t = 0; t < kNt; t += 2) {
-        uint32_t vf[4];
-        ldmatrix_x4_trans(vf, at + t * 16);
+      for (int s = 0; s < kSteps; ++s) {
+        if constexpr (!kEarly) ldmatrix_x4_trans(vf[s], vat + s * 32);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816<BF>(o[mt][t], pf[mt], vf[0], vf[1]);
-          mma16816<BF>(o[mt][t + 1], pf[mt], vf[2], vf[3]);
-        }
+        for (int t = 0; t < NT; ++t) mma16816<BF>(o[s][t], vf[s], pf[t][0], pf[t][1]);
       }
     }
     __syncwarp();
@@ -641,77 +644,60 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, MT>::kWarps) paged_row
   const bool usable = P.rowinfo[b] >= 0;
   odd = __any_sync(FULL_MASK, odd);
   if (P.splits > 1 && lane == 0) P.oflag[flag] = odd;
+  // Eight query rows at a time through shared memory, so that a row is written
+  // by the whole warp.
+  float *const buf = reinterpret_cast<float *>(smem);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int t = 0; t < NT; ++t) {
+    __syncwarp();
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int rr = mt * 16 + hf * 8 + quad;
-      const int orow = __shfl_sync(FULL_MASK, my_row, rr);
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int d = E4 ? quad * (DP / 8) + 2 * s + (c >> 1) : s * 16 + quad + 8 * (c >> 1);
+        buf[(2 * j4 + (c & 1)) * C::kOPitch + d] = o[s][t][c];
+      }
+    // the rows' statistics: in the lanes of quad 0, as in all others
+    float mr[2], zr[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float a = l[t][c];
+#pragma unroll
+      for (int q = 4; q < 32; q <<= 1) a += __shfl_xor_sync(FULL_MASK, a, q);
+      mr[c] = E4 ? mv[t][c] : mx[t][c];
+      zr[c] = a != 0.f ? mx[t][c] + log2f(a) : -INFINITY;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int row = 0; row < 8; ++row) {
+      const int rr = t * 8 + row;
+      const int orow = __shfl_sync(FULL_MASK, my_row, rr), pos = __shfl_sync(FULL_MASK, my_pos, rr);
       const bool use = __shfl_sync(FULL_MASK, my_use, rr);
-      float t = l[mt][hf];
-      t += __shfl_xor_sync(FULL_MASK, t, 1);
-      t += __shfl_xor_sync(FULL_MASK, t, 2);
-      if (orow < 0) continue;
-      const bool some = usable && use && t != 0.f;
-      const float m = E4 ? mv[mt][hf] : mx[mt][hf];
-      const float z = some ? mx[mt][hf] + log2f(t) : -INFINITY;
+      const float m = __shfl_sync(FULL_MASK, row & 1 ? mr[1] : mr[0], row / 2);
+      float z = __shfl_sync(FULL_MASK, row & 1 ? zr[1] : zr[0], row / 2);
+      if (orow < 0) break;  // rows past the last
+      const bool some = usable && use && z != -INFINITY;
+      if (!some) z = -INFINITY;
+      const float4 y = *reinterpret_cast<const float4 *>(buf + row * C::kOPitch + min(lane * 4, DP - 4));
       if (P.splits > 1) {
         const long long at = static_cast<long long>(split) * P.rows + orow;
-        if (j4 == 0) P.ml[at] = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
-        if (!some) continue;
-        float *const to = P.part + at * P.D;
-        if constexpr (E4) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < kNt; i += 8) {
-              if ((2 * j4 + c) * kNt + i >= P.D) continue;
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(o[mt][i + e][2 * hf + c]);
-              st_global_v8(to + (2 * j4 + c) * kNt + i, y);
-            }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kNt; ++i)
-            if (i * 8 < P.D) *reinterpret_cast<float2 *>(to + i * 8 + 2 * j4) = make_float2(o[mt][i][2 * hf], o[mt][i][2 * hf + 1]);
-        }
+        if (lane == 0) P.ml[at] = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
+        if (some && lane * 4 < P.D) *reinterpret_cast<float4 *>(P.part + at * P.D + lane * 4) = y;
         continue;
       }
+      if (lane == 0 && P.lse) P.lse[orow] = kLn2 * z;
+      if (lane * 4 >= P.D) continue;
       const float w = some ? ex2(m - z) : 0.f;
-      if (j4 == 0 && P.lse) P.lse[orow] = kLn2 * z;
-      unsigned short *const to = static_cast<unsigned short *>(P.out) + static_cast<long long>(orow) * P.D;
-      // column d of the answer from its sum
-      auto value = [&](float y, int d) {
-        y = some ? y * w : 0.f;
-        if (some && odd) y += paged_odd_sum<CT>(P, b, qtok[mt][hf], cnt, n, qpos[mt][hf], g, d);
-        return y;
-      };
-      if constexpr (E4) {
+      float a[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int i = 0; i < kNt; i += 8) {
-            const int d = (2 * j4 + c) * kNt + i;
-            if (d >= P.D) continue;
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float lo = value(o[mt][i + 2 * e][2 * hf + c], d + 2 * e), hi = value(o[mt][i + 2 * e + 1][2 * hf + c], d + 2 * e + 1);
-              y[e] = P.qbf16 ? pack16<true>(lo, hi) : pack16<false>(lo, hi);
-            }
-            *reinterpret_cast<uint4 *>(to + d) = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kNt; ++i)
-          if (i * 8 < P.D) {
-            const int d = i * 8 + 2 * j4;
-            const float lo = value(o[mt][i][2 * hf], d), hi = value(o[mt][i][2 * hf + 1], d + 1);
-            *reinterpret_cast<uint32_t *>(to + d) = BF ? pack16<true>(lo, hi) : pack16<false>(lo, hi);
-          }
+      for (int e = 0; e < 4; ++e) {
+        a[e] = some ? a[e] * w : 0.f;
+        if (some && odd) a[e] += paged_odd_sum<CT>(P, b, min((r0 + rr) / P.G, P.N - 1), cnt, n, pos, g, lane * 4 + e);
       }
+      *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(P.out) + static_cast<long long>(orow) * P.D + lane * 4) =
+          P.qbf16 ? make_uint2(pack16<true>(a[0], a[1]), pack16<true>(a[2], a[3])) : make_uint2(pack16<false>(a[0], a[1]), pack16<false>(a[2], a[3]));
     }
+  }
 }
 
 // ------------------------------------------------------------------- join
@@ -782,27 +768,34 @@ __global__ void __launch_bounds__(kPaJoinThreads) paged_join_kernel(const __grid
 }
 
 // -------------------------------------------------------------------- host
-template <int CT, int DP, int MT>
+template <int CT, int DP, int NT>
 cudaError_t launch_rows(const PagedParams &p, cudaStream_t s) {
-  using C = PagedRowCfg<CT, DP, MT>;
+  using C = PagedRowCfg<CT, DP, NT>;
   const int blocks = (p.N * p.G + C::kM - 1) / C::kM;
   const dim3 grid(p.H * blocks, p.budget > 0 ? p.budget : p.splits, p.budget > 0 ? 1 : p.B);
-  const cudaError_t e = allow_smem<paged_rows_kernel<CT, DP, MT>>(C::kSmem);
+  const cudaError_t e = allow_smem<paged_rows_kernel<CT, DP, NT>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_after(paged_rows_kernel<CT, DP, MT>, grid, 32, C::kSmem, s, true, p);
+  return launch_after(paged_rows_kernel<CT, DP, NT>, grid, 32, C::kSmem, s, true, p);
+}
+
+template <int CT, int DP>
+cudaError_t launch_rows_n(const PagedParams &p, cudaStream_t s) {
+  if (p.oblk == 8) return launch_rows<CT, DP, 1>(p, s);
+  if (p.oblk == 16) return launch_rows<CT, DP, 2>(p, s);
+  if (p.oblk == 24) return launch_rows<CT, DP, 3>(p, s);
+  return launch_rows<CT, DP, 4>(p, s);
 }
 
 template <int CT>
 cudaError_t launch_rows_d(const PagedParams &p, cudaStream_t s) {
-  const bool two = p.oblk == 32;
-  if (p.D <= 64) return two ? launch_rows<CT, 64, 2>(p, s) : launch_rows<CT, 64, 1>(p, s);
-  return two ? launch_rows<CT, 128, 2>(p, s) : launch_rows<CT, 128, 1>(p, s);
+  return p.D <= 64 ? launch_rows_n<CT, 64>(p, s) : launch_rows_n<CT, 128>(p, s);
 }
 
 // Items of the rows kernel that run on an SM at a time.
-int rows_per_sm(int dtype, int oblk) {
-  if (dtype == SPEC_E4M3) return oblk == 16 ? PagedRowCfg<SPEC_E4M3, 128, 1>::kWarps : PagedRowCfg<SPEC_E4M3, 128, 2>::kWarps;
-  return oblk == 16 ? PagedRowCfg<SPEC_BF16, 128, 1>::kWarps : PagedRowCfg<SPEC_BF16, 128, 2>::kWarps;
+template <int CT>
+int rows_per_sm(bool small, int oblk) {
+  if (small) return oblk <= 16 ? PagedRowCfg<CT, 64, 1>::kWarps : PagedRowCfg<CT, 64, 4>::kWarps;
+  return oblk == 8 ? PagedRowCfg<CT, 128, 1>::kWarps : oblk == 16 ? PagedRowCfg<CT, 128, 2>::kWarps : PagedRowCfg<CT, 128, 4>::kWarps;
 }
 
 struct PagedPlan {
@@ -843,7 +836,7 @@ PagedPlan plan_paged(const spec_paged_attention_args *a) {
   // queries over codes go that way all the same: as bf16, which the tile kernel
   // turns codes into, they would lose three bits.)
   p.tile = rows1 > 32 && !(a->cache_dtype == SPEC_E4M3 && a->q_dtype == SPEC_F16);
-  p.oblk = p.tile ? 256 : rows1 > 16 ? 32 : 16;
+  p.oblk = p.tile ? 256 : static_cast<int>(std::min<long long>(32, (rows1 + 7) / 8 * 8));
   const long long blocks = (rows1 + p.oblk - 1) / p.oblk, items = a->B * a->heads * blocks;
   // tokens that an item may see
   long long tokens = static_cast<long long>(a->columns) * a->page_size;
@@ -862,7 +855,8 @@ PagedPlan plan_paged(const spec_paged_attention_args *a) {
     const long long want = (8LL * kPagedSms * 2 + items - 1) / items;
     p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 32})));
     // A few rows are cut by a budget of parts, all items side by side.
-    const long long budget = static_cast<long long>(rows_per_sm(a->cache_dtype, p.oblk)) * kPagedSms / a->heads;
+    const int per_sm = a->cache_dtype == SPEC_E4M3 ? rows_per_sm<SPEC_E4M3>(a->head_dim <= 64, p.oblk) : rows_per_sm<SPEC_BF16>(a->head_dim <= 64, p.oblk);
+    const long long budget = static_cast<long long>(per_sm) * kPagedSms / a->heads;
     if (blocks == 1 && a->B <= kMaxCutRows && budget > a->B) {
       p.budget = static_cast<int>(budget);
       p.splits = static_cast<int>(std::min<long long>({32, (tokens + 63) / 64, budget - a->B + 1}));
