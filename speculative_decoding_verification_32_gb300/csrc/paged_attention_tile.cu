@@ -491,74 +491,88 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
   } else if (role == 3) {
     // ------------------------------------------------- tensor-core issue
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssue));
-    if (warp == kIssueWarp && lane == 0) {
+    // All of a warp runs through this and one lane does it: with operands that the
+    // compiler knows to be the same in all lanes, an instruction is issued in half the
+    // time that it takes a lane on its own (and that bounded the whole kernel).
+    if (warp == kIssueWarp) {
       const uint32_t qk = inst_desc(BF, kBlk, false), wv = inst_desc(BF, DP, true);
-      const uint32_t base = smem_u32(smem);
+      const uint32_t base = __shfl_sync(FULL_MASK, smem_u32(smem), 0), tm = __shfl_sync(FULL_MASK, tmem, 0);
       const uint64_t qd = op_desc(base + C::kQ, 16), kd = op_desc(base + C::kK, 16), vd = op_desc(base + C::kV, 16384);
+      auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL_MASK, wait_on(c, bar, parity, limit)); };
+      auto commit = [&](uint64_t *bar) {
+        if (elect_one()) tc_commit(bar);
+      };
       auto scores = [&](int tile, int at) {
         const uint64_t a = qd + static_cast<uint32_t>(tile * C::kOp >> 4), bb = kd + static_cast<uint32_t>((at & 1) * C::kOp >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) {
-          const int off = ((d / 4) * 16384 + (d % 4) * 32) >> 4;
-          tc_mma_ss(tmem + tile * 128, a + off, bb + off, qk, d > 0);
+          for (int d = 0; d < DP / 16; ++d) {
+            const int off = ((d / 4) * 16384 + (d % 4) * 32) >> 4;
+            tc_mma_ss(tm + tile * 128, a + off, bb + off, qk, d > 0);
+          }
+          tc_commit(&c->sfull[tile]);
         }
-        tc_commit(&c->sfull[tile]);
       };
       auto values = [&](int tile, int at, bool acc) {
         const uint64_t bb = vd + static_cast<uint32_t>((at & 1) * C::kOp >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < kBlk / 16; ++j)
-          tc_mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + j * 8, bb + (j * 2048 >> 4), wv, acc || j > 0);
+          for (int j = 0; j < kBlk / 16; ++j)
+            tc_mma_ts(tm + 256 + tile * 128, tm + tile * 128 + j * 8, bb + (j * 2048 >> 4), wv, acc || j > 0);
+        }
       };
       bool live = true;
       int kb = 0, nb[2] = {0, 0}, ni[2] = {0, 0};  // blocks in all; of each tile; items of each tile
       for (int turn = 0; live; ++turn) {
         const int slot = turn % kItemSlots;
-        live = wait_on(c, &c->ifull[slot], (turn / kItemSlots) & 1, limit);
+        live = wait(&c->ifull[slot], (turn / kItemSlots) & 1);
         if (!live) break;
-        const TileItem I = c->items[slot];
-        mbar_arrive(&c->ifree[slot]);
-        if (I.item < 0) break;
-        if (I.nblk == 0) continue;
-        for (int t = 0; t < I.tiles && live; ++t) {
-          live = wait_on(c, &c->qfull[t], ni[t] & 1, limit);
-          if (live && t == 0) live = wait_on(c, &c->kfull[kb & 1], (kb >> 1) & 1, limit);
+        const int item = __shfl_sync(FULL_MASK, c->items[slot].item, 0);
+        const int nblk = __shfl_sync(FULL_MASK, c->items[slot].nblk, 0), tiles = __shfl_sync(FULL_MASK, c->items[slot].tiles, 0);
+        if (lane == 0) mbar_arrive(&c->ifree[slot]);
+        if (item < 0) break;
+        if (nblk == 0) continue;
+#pragma unroll 1
+        for (int t = 0; t < tiles && live; ++t) {
+          live = wait(&c->qfull[t], ni[t] & 1);
+          if (live && t == 0) live = wait(&c->kfull[kb & 1], (kb >> 1) & 1);
           if (!live) break;
           tc_fence_after();
           scores(t, kb);
-          if (I.nblk == 1) tc_commit(&c->qfree[t]);
+          if (nblk == 1) commit(&c->qfree[t]);
         }
-        if (live) tc_commit(&c->kfree[kb & 1]);
-        for (int k = 0; k < I.nblk && live; ++k) {
+        if (live) commit(&c->kfree[kb & 1]);
+        for (int k = 0; k < nblk && live; ++k) {
           const int at = kb + k;
-          for (int t = 0; t < I.tiles && live; ++t) {
-            live = wait_on(c, &c->pfull[t], (nb[t] + k) & 1, limit);
-            if (live && t == 0) live = wait_on(c, &c->vfull[at & 1], (at >> 1) & 1, limit);
+#pragma unroll 1
+          for (int t = 0; t < tiles && live; ++t) {
+            live = wait(&c->pfull[t], (nb[t] + k) & 1);
+            if (live && t == 0) live = wait(&c->vfull[at & 1], (at >> 1) & 1);
             // the item before's answers have to be out of the sums
-            if (live && k == 0 && ni[t] > 0) live = wait_on(c, &c->ofree[t], (ni[t] - 1) & 1, limit);
+            if (live && k == 0 && ni[t] > 0) live = wait(&c->ofree[t], (ni[t] - 1) & 1);
             if (!live) break;
             tc_fence_after();
             values(t, at, k > 0);
-            if (k + 1 < I.nblk) {
-              if (t == 0) live = wait_on(c, &c->kfull[(at + 1) & 1], ((at + 1) >> 1) & 1, limit);
+            if (k + 1 < nblk) {
+              if (t == 0) live = wait(&c->kfull[(at + 1) & 1], ((at + 1) >> 1) & 1);
               if (!live) break;
               tc_fence_after();
               scores(t, at + 1);
-              if (k + 2 == I.nblk) tc_commit(&c->qfree[t]);  // the tile's last scores
+              if (k + 2 == nblk) commit(&c->qfree[t]);  // the tile's last scores
             } else {
-              tc_commit(&c->done[t]);
+              commit(&c->done[t]);
             }
           }
           if (live) {
-            tc_commit(&c->vfree[at & 1]);
-            if (k + 1 < I.nblk) tc_commit(&c->kfree[(at + 1) & 1]);
+            commit(&c->vfree[at & 1]);
+            if (k + 1 < nblk) commit(&c->kfree[(at + 1) & 1]);
           }
         }
-        kb += I.nblk;
-        for (int t = 0; t < I.tiles; ++t) nb[t] += I.nblk, ++ni[t];
+        kb += nblk;
+        for (int t = 0; t < tiles; ++t) nb[t] += nblk, ++ni[t];
       }
       if (!live) {  // let what was issued end before tensor memory is given back
-        tc_commit(&c->drain);
+        commit(&c->drain);
         mbar_wait_bounded(&c->drain, 0, limit);
       }
     } else if (warp == kItemWarp) {

@@ -130,7 +130,8 @@ KINDS = [("bfloat16", "bfloat16"), ("float16", "float16"), ("uint8", "bfloat16")
     (1, 1, 1, 1, 64, [0], 16, 0, 0), (1, 1, 8, 2, 128, [700], 16, 0, 0), (3, 1, 4, 4, 80, [5, 100, 33], 16, 50, 4),
     (2, 1, 32, 4, 128, [1000, 2100], 16, 300, 4), (2, 6, 8, 2, 128, [300, 77], 32, 64, 1), (3, 5, 28, 4, 64, [0, 1, 200], 48, 7, 0),
     (1, 9, 8, 1, 96, [513], 128, 200, 70), (2, 3, 6, 3, 16, [40, 500], 1024, 1, 0), (4, 2, 16, 2, 112, [15, 16, 17, 31], 16, 16, 16),
-    (1, 1, 8, 8, 128, [3000], 64, 1000, 999), (2, 4, 8, 2, 128, [0, 3], 16, 2, 100)])
+    (1, 1, 8, 8, 128, [3000], 64, 1000, 999), (2, 4, 8, 2, 128, [0, 3], 16, 2, 100), (2, 1, 40, 20, 64, [300, 90], 16, 100, 4),
+    (2, 3, 33, 11, 48, [200, 31], 32, 0, 0), (1, 8, 36, 9, 128, [260], 16, 0, 0), (150, 1, 4, 2, 64, list(range(0, 450, 3)), 16, 60, 4)])
 def test_chains(sv, kind, qt, B, N, Hq, H, D, lens, page, window, sinks):
     Problem(sv, B, N, Hq, H, D, lens, page, window, sinks, kind, qt).check()
 
