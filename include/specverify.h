@@ -773,13 +773,14 @@ spec_status spec_kv_compact_pages(const spec_page_compact_args *args, int32_t *r
  *
  * The entry of slot s of page g starts at k (or v) + g * page_stride + s *
  * tok_stride bytes and is spec_kv_entry_bytes(heads, head_dim, cache_dtype) long
- * (the layouts of spec_kv_cache).  q [B, N, q_heads, head_dim] of q_dtype
- * (SPEC_BF16 or SPEC_F16) with strides in elements for row, token and head and a
- * dense last dimension; q_heads is a multiple of heads; the cache has q_dtype or
- * SPEC_E4M3.  out [B, N, q_heads, head_dim] of q_dtype and lse [B, N, q_heads]
+ * (the layouts of spec_kv_cache); all page_size entries of every page of the pool
+ * can be read.  q [B, N, q_heads, head_dim] of q_dtype (SPEC_BF16 or SPEC_F16)
+ * with strides in elements for row, token and head and a dense last dimension;
+ * q_heads is a multiple of heads; the cache has q_dtype or SPEC_E4M3.  out [B, N, q_heads, head_dim] of q_dtype and lse [B, N, q_heads]
  * fp32 (optional) are dense, 16-byte aligned.  B <= 65535, N <=
  * SPEC_MAX_TREE_NODES in a tree, B * N * q_heads < 2^31 / 256,
- * columns * page_size <= 2^31 - 4097, num_pages * page_size < 2^31, tok_stride < 2^27.
+ * columns * page_size <= 2^31 - 4097, num_pages * page_size < 2^31, tok_stride < 2^27,
+ * page_stride < 2^40 (and, of more than one page, > 0).
  *
  * row_status [B] (optional): SPEC_ROW_BAD_SLOT (kv_len[b] < 0, count[b] outside
  * [0, N], kv_len[b] + count[b] > columns * page_size, or a page that the row's

@@ -821,7 +821,7 @@ spec_status check_paged(const spec_paged_attention_args *a) {
   if (a->parent && a->N > SPEC_MAX_TREE_NODES) return SPEC_ERR_SHAPE;
   if (a->N > 0 && static_cast<long long>(a->B) * a->N >= most / 256 / a->q_heads) return SPEC_ERR_SHAPE;
   if (static_cast<long long>(a->N) * (a->q_heads / a->heads) > most / 2) return SPEC_ERR_SHAPE;
-  if (a->page_stride < 0 || a->tok_stride < static_cast<int64_t>(entry) || a->tok_stride >= 1LL << 27) return SPEC_ERR_SHAPE;
+  if (a->page_stride < (a->num_pages > 1 ? 16 : 0) || a->page_stride >= 1LL << 40 || a->tok_stride < static_cast<int64_t>(entry) || a->tok_stride >= 1LL << 27) return SPEC_ERR_SHAPE;
   for (int i = 0; i < 3; ++i)
     if (a->q_stride[i] < 0) return SPEC_ERR_SHAPE;
   if (!std::isfinite(a->scale) || a->window < 0 || a->sinks < 0) return SPEC_ERR_ARG;

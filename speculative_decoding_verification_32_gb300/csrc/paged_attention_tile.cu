@@ -8,11 +8,14 @@
 // which the weights then take the place of; sums at 256 and 384), a thread owns
 // a row, and sums are rescaled only when a row's maximum has grown by more than
 // 2^8.  What differs:
-//   - a block is eight groups of 16 keys, each from a page of its own: the
-//     producers look eight addresses up at a time;
-//   - e4m3 codes become bf16 numbers, scale and all, on their way into shared
-//     memory.  That is exact (4 bits of significand, and bf16 has fp32's
-//     exponents), so scales may lie any distance apart;
+//   - a block is eight groups of 16 keys, each from a page of its own, a box of the
+//     cache as [page][token][head][number] (a group on no page lies past the last
+//     one and comes as zeros); one warp looks the pages up, 32 at a time and ahead
+//     of use, and asks for the boxes.  (With copies by 128 threads, 16 bytes at a
+//     time, a prompt of 2 x 4096 tokens under a window of 1024 took 171 us, so 147);
+//   - e4m3 codes are brought into a place of their own, and the producers make bf16
+//     numbers of them, scale and all.  That is exact (4 bits of significand, and
+//     bf16 has fp32's exponents), so scales may lie any distance apart;
 //   - a CTA runs through many items (a prompt has hundreds of them), and the
 //     roles do not meet between them.  One warp works the items out and hands
 //     them on; the producers bring the next queries as soon as a tile's last
@@ -33,7 +36,7 @@ namespace {
 constexpr int kBlk = 128;               // keys per block
 constexpr int kBlkGroups = kBlk / kGroup;
 constexpr int kTileThreads = 512;       // softmax of tiles A and B, producers, tensor-core issue
-constexpr int kIssueWarp = 12, kItemWarp = 13;
+constexpr int kIssueWarp = 12, kItemWarp = 13, kLoadWarp = 14;
 constexpr int kLaunchRegs = 128;        // 65536 / kTileThreads
 template <bool E4>
 struct Regs {
@@ -43,15 +46,18 @@ struct Regs {
 };
 constexpr float kTileLazy = 8.f;
 
-template <int DP>
+template <int DP, bool E4>
 struct Layout {
   static constexpr int kOp = kBlk * DP * 2;  // an operand tile: 128 rows, 64-column panels of 16 KB
-  static constexpr int kQ = 0;               // tiles A and B
-  static constexpr int kK = 2 * kOp;         // two buffers
-  static constexpr int kV = 4 * kOp;         // two buffers
-  static constexpr int kCtrl = 6 * kOp;
-  static constexpr int kStage = kCtrl + 1024;        // codes: two buffers of a block's keys or values as they are
-  static constexpr int smem(bool codes) { return kStage + (codes ? kOp : 0) + 1024; }  // + alignment
+  // Queries: row tiles in turn.  With a third place an item's first tile is there
+  // before the item before is through; codes need that room for themselves.
+  static constexpr int kQs = E4 ? 2 : 3;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQs * kOp;       // two buffers
+  static constexpr int kV = kK + 2 * kOp;    // two buffers
+  static constexpr int kStage = kV + 2 * kOp;        // codes: two buffers of a block's keys or values as they are
+  static constexpr int kCtrl = 7 * kOp;
+  static constexpr int kSmem = kCtrl + 2048;         // + alignment
 };
 
 // One (row, block of 256 query rows, KV head, part of the keys), and what all
@@ -69,15 +75,17 @@ struct TileItem {
 };
 
 constexpr int kItemSlots = 4;
+constexpr int kOddSlots = 8;  // nobody is more than kItemSlots items ahead of another
 struct TileCtrl {
   uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
-  uint64_t sfull[2], pfull[2], done[2], qfull[2], qfree[2], ofree[2], drain;
+  uint64_t land[2], lfree[2];  // 16-bit values as they have come in; codes of keys and values in turn
+  uint64_t sfull[2], pfull[2], done[2], qfull[3], qfree[3], ofree[2], drain;
   uint64_t ifull[kItemSlots], ifree[kItemSlots];
   uint32_t tmem;
   int abort;
   // 1 + the item in which a value that is not finite was taken out, items with
-  // keys in turn (the producers are at most two blocks ahead of the answers)
-  int odd[kItemSlots];
+  // keys in turn
+  int odd[kOddSlots];
   TileItem items[kItemSlots];
 };
 static_assert(sizeof(TileCtrl) <= 1024, "control block");
@@ -226,9 +234,44 @@ __device__ __noinline__ void copy_eight(unsigned char *to, const unsigned short 
 
 __device__ __forceinline__ float max3f(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
+// Where a row's keys lie: lane i of a warp knows groups i of four blocks, and asks for
+// the next four blocks' pages two blocks ahead.
+struct Pages {
+  int page, token, first;  // page (one past the last: none), token in it, token of the row
+  int next_page, next_token, next_first;
+  __device__ __forceinline__ void ask(const PagedParams &P, const TileItem &I, const Keys &keys, int k, int lane) {
+    const int i = I.g0 + k * kBlkGroups + lane;
+    next_page = max(P.pages, 1);
+    next_token = 0;
+    next_first = 0x7fffff00;
+    if (i < I.g1) {
+      next_first = keys.token(i);
+      const int j = next_first / P.page, pg = __ldg(P.table + static_cast<size_t>(I.b) * P.columns + j);
+      next_token = next_first - j * P.page;
+      if (pg >= 0 && pg < P.pages) next_page = pg;
+    }
+  }
+  // before block k's groups are used
+  __device__ __forceinline__ void step(const PagedParams &P, const TileItem &I, const Keys &keys, int k, int lane) {
+    if (k % 4 == 0) {
+      if (k == 0) ask(P, I, keys, 0, lane);
+      page = next_page;
+      token = next_token;
+      first = next_first;
+    }
+    if (k % 4 == 2 && k + 2 < I.nblk) ask(P, I, keys, k + 2, lane);
+  }
+};
+
+// Keys and values as [page][token][head][number], a box being 16 tokens of one head.
+struct PagedMaps {
+  CUtensorMap k, v;
+};
+
 template <int CT, int DP>
-__global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __grid_constant__ PagedParams P, int blocks, int items) {
-  using C = Layout<DP>;
+__global__ void __launch_bounds__(kTileThreads, 1)
+    paged_tile_kernel(const __grid_constant__ PagedParams P, const __grid_constant__ PagedMaps M, int blocks, int items) {
+  using C = Layout<DP, CT == SPEC_E4M3>;
   constexpr bool E4 = CT == SPEC_E4M3, BF = CT != SPEC_F16;
   using R = Regs<E4>;
   extern __shared__ unsigned char raw[];
@@ -238,22 +281,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&c->kfull[i], 128);
+      mbar_init(&c->kfull[i], E4 ? 128 : 1);
       mbar_init(&c->vfull[i], 128);
       mbar_init(&c->kfree[i], 1);
       mbar_init(&c->vfree[i], 1);
       mbar_init(&c->sfull[i], 1);
       mbar_init(&c->pfull[i], 128);
       mbar_init(&c->done[i], 1);
+      mbar_init(&c->land[i], 1);
+      mbar_init(&c->lfree[i], 128);
+      mbar_init(&c->ofree[i], 128);
+    }
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&c->qfull[i], 128);
       mbar_init(&c->qfree[i], 1);
-      mbar_init(&c->ofree[i], 128);
     }
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(&c->ifull[i], 1);
-      mbar_init(&c->ifree[i], 4 + 1 + 8);  // warps: producers, issue, softmax
-      c->odd[i] = 0;
+      mbar_init(&c->ifree[i], 4 + 1 + 1 + 8);  // warps: producers, issue, loads, softmax
     }
+    for (int i = 0; i < kOddSlots; ++i) c->odd[i] = 0;
     mbar_init(&c->drain, 1);
     c->abort = 0;
     fence_mbar_init();
@@ -271,217 +318,185 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kProduce));
     const int pt = tid - 256;
     bool live = true;
-    // A thread brings 16-byte pieces of every kStep-th token of a block: 16-bit
-    // entries where the tensor cores want them, codes into a buffer of their own
-    // (each thread turns what it brought itself into bf16).
+    // A thread deals with 16-byte pieces of every kStep-th token of a block.
     constexpr int L = E4 ? DP / 16 : DP / 8, kStep = 128 / L, kPer = kBlk / kStep;
     static_assert(!E4 || kPer == L, "a lane's piece is the number of the token whose scale it reads");
     const int pc = pt % L, row0 = pt / L;
-    const bool col = pc * 16 < P.D * (E4 ? 1 : 2);
-    const uint32_t sbase = smem_u32(smem);
     const uint32_t put0 = E4 ? C::kStage + pt * 16 : (pc / 8) * 16384 + row0 * 128 + (((pc % 8) ^ (row0 & 7)) << 4);
     constexpr int kPut = E4 ? 2048 : kStep * 128;
-    int kb = 0, worked = 0, ni[2] = {0, 0};  // blocks and items so far, items of each tile
+    int kb = 0, worked = 0, nq = 0;  // blocks, items and row tiles so far
     const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
     TileItem I;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (live) live = wait_on(c, bar, parity, limit);
+      live = __all_sync(FULL_MASK, live);
+    };
     for (int turn = 0; live && take_item(c, turn, I, limit) && I.item >= 0; ++turn) {
       if (I.nblk == 0) continue;
       const Keys keys(P, I.p0, I.end);
-      const int32_t *const trow = P.table + static_cast<size_t>(I.b) * P.columns;
-      const long long piece = static_cast<long long>(I.g) * P.D * (E4 ? 1 : 2) + (col ? pc * 16 : 0);
-      // lane i: where group i of four blocks starts in its plane (-1: on no page), and its first token
-      long long where = -1;
-      int first = 0;
-      auto look_up = [&](int k) {
-        const int i = I.g0 + k * kBlkGroups + lane;
-        where = -1;
-        first = 0;
-        if (i < I.g1) {
-          first = keys.token(i);
-          const int j = first / P.page, pg = __ldg(trow + j);
-          if (pg >= 0 && pg < P.pages) where = pg * P.page_stride + (first - j * P.page) * P.tok_stride;
-        }
-      };
-      auto buffer_free = [&](int at, bool val) {
-        const int s = at & 1;
-        if (at >= 2 && live) live = wait_on(c, val ? &c->vfree[s] : &c->kfree[s], ((at >> 1) - 1) & 1, limit);
-        live = __all_sync(FULL_MASK, live);
-      };
-      // copies of block k's keys (it = 2 k) or values (2 k + 1); codes: the scale
-      // byte of the block's token row0 + pc kStep
-      auto issue = [&](int it) -> uint32_t {
-        uint32_t byte = 0;
-        if (it < 2 * I.nblk) {
-          const int k = it >> 1, at = kb + k, s = at & 1;
-          const bool val = it & 1;
-          if (!val && k % 4 == 0) look_up(k);
-          const int base = (k % 4) * kBlkGroups;
-          const unsigned char *const plane = val ? P.v : P.k;
-          if constexpr (E4) {
-            const int row = row0 + pc * kStep;
-            const long long w = __shfl_sync(FULL_MASK, where, base + row / 16);
-            const int t0 = __shfl_sync(FULL_MASK, first, base + row / 16);
-            if (w >= 0 && t0 + row % 16 < I.end) byte = __ldg(plane + w + row % 16 * P.tok_stride + static_cast<long long>(P.H) * P.D + I.g);
-          } else {
-            buffer_free(at, val);
-          }
-          if (live) {
-            const uint32_t dst = sbase + put0 + (E4 ? (it & 1) * (C::kOp / 2) : (val ? C::kV : C::kK) + s * C::kOp);
-            constexpr int kSame = kStep < 16 ? 16 / kStep : 1;  // neighbouring copies in one group
-#pragma unroll
-            for (int i0 = 0; i0 < kPer; i0 += kSame) {
-              const int row = row0 + i0 * kStep;
-              const long long w = __shfl_sync(FULL_MASK, where, base + row / 16);
-              const int t0 = __shfl_sync(FULL_MASK, first, base + row / 16);  // by every lane
-              const int left = w < 0 || !col ? 0 : I.end - t0;
-              const unsigned char *const src = plane + w + row % 16 * P.tok_stride + piece;
-#pragma unroll
-              for (int i = i0; i < i0 + kSame; ++i) {
-                const bool on = row % 16 + (i - i0) * kStep < left;
-                cp_async16_zfill(dst + i * kPut, on ? src + (i - i0) * kStep * P.tok_stride : plane, on);
-              }
-            }
-          }
-        }
-        cp_async_commit();
-        return byte;
-      };
-      // queries: DP / 8 lanes per row, 16 bytes each, once the scores that the
-      // item before made of the tile's are done
-      {
+      // queries of a row tile: DP / 8 lanes per row, 16 bytes each, once the scores
+      // of the place's former tile are done
+      auto queries = [&](int tile) {
         constexpr int QL = DP / 8, kRows = 128 / QL;
-        const int qc = pt % QL;
-#pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-          if (tile >= I.tiles) break;
-          if (ni[tile] > 0 && live) live = wait_on(c, &c->qfree[tile], (ni[tile] - 1) & 1, limit);
-          live = __all_sync(FULL_MASK, live);
-          if (!live) break;
-          ++ni[tile];
-          const int r = I.r0 + tile * 128 + pt / QL;
-          int t = r / P.G, h = r - t * P.G;  // the row's token and head of the group
-          const unsigned short *q = static_cast<const unsigned short *>(P.q) + I.b * P.qs[0] + t * P.qs[1] +
-                                    (static_cast<long long>(I.g) * P.G + h) * P.qs[2] + qc * 8;
-          unsigned char *to = smem + C::kQ + tile * C::kOp + (qc / 8) * 16384 + (pt / QL) * 128 + (((qc % 8) ^ (pt / QL & 7)) << 4);
-          const int dt = kRows / P.G, dh = kRows - dt * P.G;
-          const long long step = dt * P.qs[1] + dh * P.qs[2], wrap = P.qs[1] - P.G * P.qs[2];
-          const bool in = qc * 8 < P.D;
+        const int qc = pt % QL, place = nq % C::kQs;
+        if (nq >= C::kQs) wait(&c->qfree[place], (nq / C::kQs - 1) & 1);
+        ++nq;
+        if (!live) return;
+        const int r = I.r0 + tile * 128 + pt / QL;
+        int t = r / P.G, h = r - t * P.G;  // the row's token and head of the group
+        const unsigned short *q = static_cast<const unsigned short *>(P.q) + I.b * P.qs[0] + t * P.qs[1] +
+                                  (static_cast<long long>(I.g) * P.G + h) * P.qs[2] + qc * 8;
+        unsigned char *to = smem + C::kQ + place * C::kOp + (qc / 8) * 16384 + (pt / QL) * 128 + (((qc % 8) ^ (pt / QL & 7)) << 4);
+        const int dt = kRows / P.G, dh = kRows - dt * P.G;
+        const long long step = dt * P.qs[1] + dh * P.qs[2], wrap = P.qs[1] - P.G * P.qs[2];
+        const bool in = qc * 8 < P.D;
 #pragma unroll 2
-          for (int i = 0; i < 128 / kRows; ++i) {
-            const bool on = in && t < P.N;
-            if (vec)
-              cp_async16_zfill(smem_u32(to), on ? q : static_cast<const unsigned short *>(P.q), on);
-            else
-              copy_eight(to, q, on);
-            to += kRows * 128;
-            t += dt;
-            h += dh;
-            q += step;
-            if (h >= P.G) h -= P.G, ++t, q += wrap;
-          }
+        for (int i = 0; i < 128 / kRows; ++i) {
+          const bool on = in && t < P.N;
+          if (vec)
+            cp_async16_zfill(smem_u32(to), on ? q : static_cast<const unsigned short *>(P.q), on);
+          else
+            copy_eight(to, q, on);
+          to += kRows * 128;
+          t += dt;
+          h += dh;
+          q += step;
+          if (h >= P.G) h -= P.G, ++t, q += wrap;
         }
-        cp_async_commit();
-      }
-      uint32_t sc0 = 0, sc1 = 0;
-      // two turns ahead: what is issued in one is handed over in the next but one
-      for (int it = -2; it < 2 * I.nblk; ++it) {
-        if (it >= 0) {
-          cp_async_wait<1>();
-          const int k = it >> 1, at = kb + k, s = at & 1;
-          const bool val = it & 1;
-          // In groups that some query does not see whole, values that are not
-          // finite are taken out (it would get 0 * NaN) and put into the answers of
-          // the queries that see them at the end.
-          unsigned part = 0;  // such groups of the block
-          if (val) {
-            const int gi = I.g0 + k * kBlkGroups + (lane & 7);
-            part = __ballot_sync(FULL_MASK, gi < I.g1 && group_masked(P, keys.token(gi), I.n, I.p0, I.p1)) & 0xffu;
-          }
-          unsigned char *const buf = smem + (val ? C::kV : C::kK) + s * C::kOp;
-          bool odd = false;
-          if constexpr (!E4) {
-            if (part) {
-              constexpr int kRun = kPer < 8 ? kPer : 8;
-              bool some = false;
-#pragma unroll
-              for (int i0 = 0; i0 < kPer; i0 += kRun) {
-                uint4 w[kRun];
-#pragma unroll
-                for (int i = 0; i < kRun; ++i) w[i] = *reinterpret_cast<const uint4 *>(buf + put0 + (i0 + i) * kPut);
-#pragma unroll
-                for (int i = 0; i < kRun; ++i) some = some || not_finite<BF>(w[i]);
-              }
-              if (some) {
+      };
+      auto hand_queries = [&](int tiles) {
+        cp_async_wait_all();
+        fence_async_smem();
+        for (int t = nq - tiles; t < nq; ++t) mbar_arrive(&c->qfull[t % C::kQs]);
+      };
 #pragma unroll 1
-                for (int i = 0; i < kPer; ++i) {
-                  uint4 w = *reinterpret_cast<const uint4 *>(buf + put0 + i * kPut);
-                  if (!(part >> ((row0 + i * kStep) / 16) & 1u) || !not_finite<BF>(w)) continue;
-                  drop_not_finite<BF>(w);
-                  *reinterpret_cast<uint4 *>(buf + put0 + i * kPut) = w;
-                  odd = true;
-                }
-              }
-            }
-          } else {
-            buffer_free(at, val);
-            const unsigned char *const codes = smem + put0 + (it & 1) * (C::kOp / 2);
-            uint32_t nans = 0;
-            // (255 among them: a scale of NaN)
-            const bool large = __any_sync(FULL_MASK, sc0 > kTopScale);
+      for (int tile = 0; tile < I.tiles; ++tile) {
+        queries(tile);
+        if (!E4 && live) hand_queries(1);
+      }
+      // In groups that some query does not see whole, values that are not finite
+      // are taken out (it would get 0 * NaN) and put into the answers of the
+      // queries that see them at the end; what lies behind the last token was
+      // brought along, and is nobody's.
+      auto partial = [&](int k) {  // such groups of the block
+        const int gi = I.g0 + k * kBlkGroups + (lane & 7);
+        return __ballot_sync(FULL_MASK, gi < I.g1 && group_masked(P, keys.token(gi), I.n, I.p0, I.p1)) & 0xffu;
+      };
+      auto behind = [&](int k, int row) { return keys.token(I.g0 + k * kBlkGroups + row / 16) + row % 16 >= I.end; };
+      if constexpr (!E4) {
+        for (int k = 0; k < I.nblk; ++k) {
+          const int at = kb + k, s = at & 1;
+          wait(&c->land[s], (at >> 1) & 1);
+          if (!live) break;
+          const unsigned part = partial(k);
+          if (part) {
+            unsigned char *const buf = smem + C::kV + s * C::kOp + put0;
+            constexpr int kRun = kPer < 8 ? kPer : 8;
+            bool some = false, odd = false;
+#pragma unroll 1
+            for (int i0 = 0; i0 < kPer; i0 += kRun) {
+              uint4 w[kRun];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-              const int row = row0 + i * kStep;
-              const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * kPut);
-              const uint32_t f = first_factor(__shfl_sync(FULL_MASK, sc0, (lane & ~(L - 1)) + i));
-              nans |= code_nan(w.x) | code_nan(w.y) | code_nan(w.z) | code_nan(w.w);
-              const uint2 y0 = codes_to_bf16(w.x, f), y1 = codes_to_bf16(w.y, f), y2 = codes_to_bf16(w.z, f), y3 = codes_to_bf16(w.w, f);
-              // the two 16-byte halves, the upper panel's lanes in the other
-              // order: eight lanes then cover all banks
-              const int ch = (pc % 4) * 2, up = pc / 4;
-              unsigned char *const to = buf + up * 16384 + row * 128;
-              const uint4 lo = make_uint4(y0.x, y0.y, y1.x, y1.y), hi = make_uint4(y2.x, y2.y, y3.x, y3.y);
-              *reinterpret_cast<uint4 *>(to + (((ch + up) ^ (row & 7)) << 4)) = up ? hi : lo;
-              *reinterpret_cast<uint4 *>(to + (((ch + 1 - up) ^ (row & 7)) << 4)) = up ? lo : hi;
+              for (int i = 0; i < kRun; ++i) w[i] = *reinterpret_cast<const uint4 *>(buf + (i0 + i) * kPut);
+#pragma unroll
+              for (int i = 0; i < kRun; ++i) some = some || not_finite<BF>(w[i]);
             }
-            // what is rare: large scales, codes and scales of NaN
-            if (large || __any_sync(FULL_MASK, nans != 0)) {
+            if (some) {
 #pragma unroll 1
               for (int i = 0; i < kPer; ++i) {
                 const int row = row0 + i * kStep;
-                const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * kPut);
-                const uint32_t c0 = __shfl_sync(FULL_MASK, sc0, (lane & ~(L - 1)) + i);
-                const uint32_t f = first_factor(c0), f2 = second_factor(c0);
-                uint32_t cw[4] = {w.x, w.y, w.z, w.w}, y[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  uint2 z = codes_to_bf16(cw[e], f);
-                  z = with_nans(make_uint2(mul_bf16x2(z.x, f2), mul_bf16x2(z.y, f2)), code_nan(cw[e]));
-                  y[2 * e] = z.x, y[2 * e + 1] = z.y;
-                }
-                uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-                if ((part >> (row / 16) & 1u) && (not_finite<true>(lo) || not_finite<true>(hi))) {
-                  drop_not_finite<true>(lo);
-                  drop_not_finite<true>(hi);
-                  odd = true;
-                }
-                const int ch = (pc % 4) * 2, up = pc / 4;
-                unsigned char *const to = buf + up * 16384 + row * 128;
-                *reinterpret_cast<uint4 *>(to + ((ch ^ (row & 7)) << 4)) = lo;
-                *reinterpret_cast<uint4 *>(to + (((ch + 1) ^ (row & 7)) << 4)) = hi;
+                uint4 w = *reinterpret_cast<const uint4 *>(buf + i * kPut);
+                if (!(part >> (row / 16) & 1u) || !not_finite<BF>(w)) continue;
+                drop_not_finite<BF>(w);
+                *reinterpret_cast<uint4 *>(buf + i * kPut) = w;
+                odd = odd || !behind(k, row);
               }
             }
+            if (odd) c->odd[worked % kOddSlots] = I.item + 1;
+            fence_async_smem();
           }
-          if (odd) c->odd[worked % kItemSlots] = I.item + 1;
-          fence_async_smem();
-          if (!(it == 0 && (P.force_timeout == 1 || P.force_timeout == I.g + 2))) mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
+          mbar_arrive(&c->vfull[s]);
         }
-        sc0 = sc1;
-        sc1 = issue(it + 2);  // after this turn's is handed over: its buffer may be a while in coming free
-        if (it == -1) {
-          cp_async_wait<2>();  // the queries
+      } else {
+        // Blocks' keys and values in turn (it = 2 k, 2 k + 1), each thread's scale
+        // byte, of the block's token row0 + pc kStep, two turns ahead.
+        Pages where;
+        auto scale = [&](int it) -> uint32_t {
+          uint32_t byte = 0;
+          if (it < 2 * I.nblk) {
+            const int k = it >> 1, row = row0 + pc * kStep, from = (k % 4) * kBlkGroups + row / 16;
+            if (!(it & 1)) where.step(P, I, keys, k, lane);
+            const int pg = __shfl_sync(FULL_MASK, where.page, from), t = __shfl_sync(FULL_MASK, where.token, from);
+            const int first = __shfl_sync(FULL_MASK, where.first, from);
+            if (pg < P.pages && first + row % 16 < I.end)
+              byte = __ldg((it & 1 ? P.v : P.k) + pg * P.page_stride + (t + row % 16) * P.tok_stride + static_cast<long long>(P.H) * P.D + I.g);
+          }
+          return byte;
+        };
+        uint32_t sc0 = scale(0), sc1 = scale(1);
+        for (int it = 0; it < 2 * I.nblk; ++it) {
+          const int k = it >> 1, at = kb + k, s = at & 1, all = 2 * kb + it;
+          const bool val = it & 1;
+          const unsigned part = val ? partial(k) : 0;
+          const uint32_t sc2 = scale(it + 2);
+          wait(&c->land[val], at & 1);
+          if (at >= 2) wait(val ? &c->vfree[s] : &c->kfree[s], ((at >> 1) - 1) & 1);
+          if (!live) break;
+          unsigned char *const buf = smem + (val ? C::kV : C::kK) + s * C::kOp;
+          const unsigned char *const codes = smem + put0 + (all & 1) * (C::kOp / 2);
+          bool odd = false;
+          uint32_t nans = 0;
+          // (255 among them: a scale of NaN)
+          const bool large = __any_sync(FULL_MASK, sc0 > kTopScale);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int row = row0 + i * kStep;
+            const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * kPut);
+            const uint32_t f = first_factor(__shfl_sync(FULL_MASK, sc0, (lane & ~(L - 1)) + i));
+            nans |= code_nan(w.x) | code_nan(w.y) | code_nan(w.z) | code_nan(w.w);
+            const uint2 y0 = codes_to_bf16(w.x, f), y1 = codes_to_bf16(w.y, f), y2 = codes_to_bf16(w.z, f), y3 = codes_to_bf16(w.w, f);
+            // the two 16-byte halves, the upper panel's lanes in the other
+            // order: eight lanes then cover all banks
+            const int ch = (pc % 4) * 2, up = pc / 4;
+            unsigned char *const to = buf + up * 16384 + row * 128;
+            const uint4 lo = make_uint4(y0.x, y0.y, y1.x, y1.y), hi = make_uint4(y2.x, y2.y, y3.x, y3.y);
+            *reinterpret_cast<uint4 *>(to + (((ch + up) ^ (row & 7)) << 4)) = up ? hi : lo;
+            *reinterpret_cast<uint4 *>(to + (((ch + 1 - up) ^ (row & 7)) << 4)) = up ? lo : hi;
+          }
+          // what is rare: large scales, codes and scales of NaN
+          if (large || __any_sync(FULL_MASK, nans != 0)) {
+#pragma unroll 1
+            for (int i = 0; i < kPer; ++i) {
+              const int row = row0 + i * kStep;
+              const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * kPut);
+              const uint32_t c0 = __shfl_sync(FULL_MASK, sc0, (lane & ~(L - 1)) + i);
+              const uint32_t f = first_factor(c0), f2 = second_factor(c0);
+              uint32_t cw[4] = {w.x, w.y, w.z, w.w}, y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint2 z = codes_to_bf16(cw[e], f);
+                z = with_nans(make_uint2(mul_bf16x2(z.x, f2), mul_bf16x2(z.y, f2)), code_nan(cw[e]));
+                y[2 * e] = z.x, y[2 * e + 1] = z.y;
+              }
+              uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+              if ((part >> (row / 16) & 1u) && (not_finite<true>(lo) || not_finite<true>(hi))) {
+                drop_not_finite<true>(lo);
+                drop_not_finite<true>(hi);
+                odd = odd || !behind(k, row);
+              }
+              const int ch = (pc % 4) * 2, up = pc / 4;
+              unsigned char *const to = buf + up * 16384 + row * 128;
+              *reinterpret_cast<uint4 *>(to + ((ch ^ (row & 7)) << 4)) = lo;
+              *reinterpret_cast<uint4 *>(to + (((ch + 1) ^ (row & 7)) << 4)) = hi;
+            }
+          }
+          mbar_arrive(&c->lfree[val]);
+          if (odd) c->odd[worked % kOddSlots] = I.item + 1;
           fence_async_smem();
-          mbar_arrive(&c->qfull[0]);
-          if (I.tiles > 1) mbar_arrive(&c->qfull[1]);
+          mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
+          if (it == 0) hand_queries(I.tiles);
+          sc0 = sc1;
+          sc1 = sc2;
         }
       }
       kb += I.nblk;
@@ -502,8 +517,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
       auto commit = [&](uint64_t *bar) {
         if (elect_one()) tc_commit(bar);
       };
-      auto scores = [&](int tile, int at) {
-        const uint64_t a = qd + static_cast<uint32_t>(tile * C::kOp >> 4), bb = kd + static_cast<uint32_t>((at & 1) * C::kOp >> 4);
+      auto scores = [&](int tile, int place, int at) {
+        const uint64_t a = qd + static_cast<uint32_t>(place * C::kOp >> 4), bb = kd + static_cast<uint32_t>((at & 1) * C::kOp >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int d = 0; d < DP / 16; ++d) {
@@ -522,7 +537,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
         }
       };
       bool live = true;
-      int kb = 0, nb[2] = {0, 0}, ni[2] = {0, 0};  // blocks in all; of each tile; items of each tile
+      int kb = 0, nq = 0, nb[2] = {0, 0}, ni[2] = {0, 0};  // blocks and row tiles in all; of each tile, blocks and items
       for (int turn = 0; live; ++turn) {
         const int slot = turn % kItemSlots;
         live = wait(&c->ifull[slot], (turn / kItemSlots) & 1);
@@ -534,12 +549,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
         if (nblk == 0) continue;
 #pragma unroll 1
         for (int t = 0; t < tiles && live; ++t) {
-          live = wait(&c->qfull[t], ni[t] & 1);
+          const int place = (nq + t) % C::kQs;
+          live = wait(&c->qfull[place], ((nq + t) / C::kQs) & 1);
           if (live && t == 0) live = wait(&c->kfull[kb & 1], (kb >> 1) & 1);
           if (!live) break;
           tc_fence_after();
-          scores(t, kb);
-          if (nblk == 1) commit(&c->qfree[t]);
+          scores(t, place, kb);
+          if (nblk == 1) commit(&c->qfree[place]);
         }
         if (live) commit(&c->kfree[kb & 1]);
         for (int k = 0; k < nblk && live; ++k) {
@@ -557,8 +573,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
               if (t == 0) live = wait(&c->kfull[(at + 1) & 1], ((at + 1) >> 1) & 1);
               if (!live) break;
               tc_fence_after();
-              scores(t, at + 1);
-              if (k + 2 == nblk) commit(&c->qfree[t]);  // the tile's last scores
+              const int place = (nq + t) % C::kQs;
+              scores(t, place, at + 1);
+              if (k + 2 == nblk) commit(&c->qfree[place]);  // the tile's last scores
             } else {
               commit(&c->done[t]);
             }
@@ -569,11 +586,68 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
           }
         }
         kb += nblk;
+        nq += tiles;
         for (int t = 0; t < tiles; ++t) nb[t] += nblk, ++ni[t];
       }
       if (!live) {  // let what was issued end before tensor memory is given back
         commit(&c->drain);
         mbar_wait_bounded(&c->drain, 0, limit);
+      }
+    } else if (warp == kLoadWarp) {
+      // ------------------------------------------- keys and values on their way
+      bool live = true;
+      int kb = 0;
+      uint32_t brought[2] = {0, 0};  // boxes' turns so far: keys, values
+      TileItem I;
+      for (int turn = 0; live && take_item(c, turn, I, limit) && I.item >= 0; ++turn) {
+        const Keys keys(P, I.p0, I.end);
+        Pages where;
+        for (int it = 0; it < 2 * I.nblk; ++it) {
+          const int k = it >> 1, at = kb + k, s = at & 1;
+          const bool val = it & 1;
+          if (!val) where.step(P, I, keys, k, lane);
+          // codes: the places of keys and values take turns; 16-bit entries: blocks do
+          if constexpr (E4) {
+            if (at >= 1) live = __all_sync(FULL_MASK, wait_on(c, &c->lfree[val], (at - 1) & 1, limit));
+          } else {
+            if (at >= 2) live = __all_sync(FULL_MASK, wait_on(c, val ? &c->vfree[s] : &c->kfree[s], ((at >> 1) - 1) & 1, limit));
+          }
+          if (!live || (it == 0 && (P.force_timeout == 1 || P.force_timeout == I.g + 2))) {
+            live = false;
+            break;
+          }
+          uint64_t *const bar = E4 ? &c->land[val] : val ? &c->land[s] : &c->kfull[s];
+          const uint32_t to = smem_u32(smem) + (E4 ? C::kStage + val * (C::kOp / 2) : (val ? C::kV : C::kK) + s * C::kOp);
+          const CUtensorMap *const map = val ? &M.v : &M.k;
+          if (elect_one()) mbar_arrive_expect_tx(bar, E4 ? C::kOp / 2 : C::kOp);
+          __syncwarp();
+#pragma unroll 1
+          for (int j = 0; j < kBlkGroups; ++j) {
+            const int pg = __shfl_sync(FULL_MASK, where.page, (k % 4) * kBlkGroups + j), t = __shfl_sync(FULL_MASK, where.token, (k % 4) * kBlkGroups + j);
+            if (elect_one()) {
+              if constexpr (E4) {
+                tma_load_4d(to + j * kGroup * DP, map, 0, I.g, t, pg, bar);
+              } else {
+#pragma unroll
+                for (int x = 0; x < DP; x += 64) tma_load_4d(to + x / 64 * 16384 + j * kGroup * 128, map, x, I.g, t, pg, bar);
+              }
+            }
+          }
+          ++brought[val];
+        }
+        kb += I.nblk;
+      }
+      // Nothing may come in behind the block's end, if a wait of whichever warp ran
+      // out: each place's last boxes are waited for (and of no phase but a barrier's
+      // last: one before it would count as still to come).
+      for (int val = 0; val < 2; ++val) {
+        constexpr uint32_t kPlaces = E4 ? 1 : 2;
+        for (uint32_t n = brought[val] > kPlaces ? brought[val] - kPlaces : 0; n < brought[val]; ++n) {
+          if constexpr (E4)
+            mbar_wait_bounded(&c->land[val], n & 1, limit);
+          else
+            mbar_wait_bounded(val ? &c->land[n & 1] : &c->kfull[n & 1], (n >> 1) & 1, limit);
+        }
       }
     } else if (warp == kItemWarp) {
       // ------------------------------------------------------------- items
@@ -615,7 +689,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
         I = make_item(P, item, blocks);
       }
       if (I.item < 0) break;
-      const int slot = worked % kItemSlots;
+      const int slot = worked % kOddSlots;
       worked += I.nblk > 0;
       if (tile >= I.tiles) continue;
       const int r = I.r0 + rr;
@@ -832,18 +906,46 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const __gri
   }
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled f = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess || r != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiled>(nullptr);
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return f;
+}
+
 template <int CT, int DP>
 cudaError_t launch(const PagedParams &p, cudaStream_t s) {
-  using C = Layout<DP>;
+  constexpr bool E4 = CT == SPEC_E4M3;
+  using C = Layout<DP, E4>;
   const int blocks = (p.N * p.G + 255) / 256;
   const long long items = static_cast<long long>(p.B) * p.H * blocks * p.splits;
   if (items > 0x7fffffffLL - 4096) return cudaErrorInvalidValue;
-  constexpr int smem = C::smem(CT == SPEC_E4M3);
-  static_assert(smem <= 227 * 1024, "shared memory of a block");
-  const cudaError_t e = allow_smem<paged_tile_kernel<CT, DP>>(smem, kLaunchRegs);
+  static_assert(C::kSmem <= 227 * 1024, "shared memory of a block");
+  cudaError_t e = allow_smem<paged_tile_kernel<CT, DP>>(C::kSmem, kLaunchRegs);
   if (e != cudaSuccess) return e;
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return cudaErrorNotSupported;
+  PagedMaps m;
+  const cuuint64_t pages = p.pages > 0 ? p.pages : 1;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.D), static_cast<cuuint64_t>(p.H), static_cast<cuuint64_t>(p.page), pages};
+  // (the step between pages is not used where there is but one)
+  const cuuint64_t steps[3] = {static_cast<cuuint64_t>(p.D) * (E4 ? 1 : 2), static_cast<cuuint64_t>(p.tok_stride),
+                               static_cast<cuuint64_t>(pages > 1 ? p.page_stride : 16)};
+  const cuuint32_t box[4] = {E4 ? DP : 64, 1, kGroup, 1}, ones[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 2; ++i)
+    if (encode(i ? &m.v : &m.k, E4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<unsigned char *>(i ? p.v : p.k), dims,
+               steps, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, E4 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+               E4 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(items < kPagedSms ? items : kPagedSms);
-  return launch_after(paged_tile_kernel<CT, DP>, dim3(grid), kTileThreads, smem, s, true, p, blocks, static_cast<int>(items));
+  return launch_after(paged_tile_kernel<CT, DP>, dim3(grid), kTileThreads, C::kSmem, s, true, p, m, blocks, static_cast<int>(items));
 }
 
 template <int CT>

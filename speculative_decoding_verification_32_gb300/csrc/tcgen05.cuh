@@ -3,6 +3,7 @@
 // operand descriptors.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -90,6 +91,14 @@ __device__ __forceinline__ uint64_t op_desc(uint32_t addr, uint32_t panel) {
 __device__ __forceinline__ uint32_t inst_desc(bool bf16, int n, bool b_cols) {
   const uint32_t f = bf16 ? 1u : 0u;
   return 1u << 4 | f << 7 | f << 10 | (b_cols ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
+}
+
+// One box of a four-dimensional array into shared memory (at coordinates past an
+// array's end: zeros), its bytes counted on `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+               "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+               : "memory");
 }
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
