@@ -35,14 +35,21 @@ namespace {
 
 constexpr int kBlk = 128;               // keys per block
 constexpr int kBlkGroups = kBlk / kGroup;
-constexpr int kTileThreads = 512;       // softmax of tiles A and B, producers, tensor-core issue
-constexpr int kIssueWarp = 12, kItemWarp = 13, kLoadWarp = 14;
-constexpr int kLaunchRegs = 128;        // 65536 / kTileThreads
+// Warpgroups: the softmax of tiles A and B, producers, and one for the rest.  Codes
+// have two of producers, for keys and for values, at the price of registers of the
+// softmax: a prompt of 2 x 4096 tokens 230 us with one, 201 with two; in bf16, which
+// has little for them to do, 145 us with one and 157 with two.
 template <bool E4>
-struct Regs {
-  static constexpr int kSoftmax = E4 ? 176 : 184, kProduce = E4 ? 88 : 72, kIssue = 72;
-  static_assert(kSoftmax > kLaunchRegs && kProduce < kLaunchRegs && kIssue < kLaunchRegs, "softmax takes more, the others give back");
-  static_assert(2 * kSoftmax + kProduce + kIssue == 4 * kLaunchRegs, "the block's registers");
+struct Team {
+  static constexpr int kThreads = E4 ? 640 : 512;
+  static constexpr int kProducers = E4 ? 2 : 1;
+  static constexpr int kRest = 2 + kProducers;            // warpgroup of the rest:
+  static constexpr int kIssueWarp = kRest * 4;            // (two, for tile A and tile B)
+  static constexpr int kItemWarp = kRest * 4 + 2, kLoadWarp = kRest * 4 + 3;
+  static constexpr int kLaunchRegs = E4 ? 96 : 128;       // 65536 / kThreads
+  static constexpr int kSoftmaxRegs = E4 ? 144 : 184, kOtherRegs = E4 ? 64 : 72;
+  static_assert(kSoftmaxRegs > kLaunchRegs && kOtherRegs < kLaunchRegs, "softmax takes more, the others give back");
+  static_assert(2 * kSoftmaxRegs + (kProducers + 1) * kOtherRegs == kThreads / 128 * kLaunchRegs, "the block's registers");
 };
 constexpr float kTileLazy = 8.f;
 
@@ -57,7 +64,7 @@ struct Layout {
   static constexpr int kV = kK + 2 * kOp;    // two buffers
   static constexpr int kStage = kV + 2 * kOp;        // codes: two buffers of a block's keys or values as they are
   static constexpr int kCtrl = 7 * kOp;
-  static constexpr int kSmem = kCtrl + 2048;         // + alignment
+  static constexpr int kSmem = kCtrl + 1024;
 };
 
 // One (row, block of 256 query rows, KV head, part of the keys), and what all
@@ -78,8 +85,8 @@ constexpr int kItemSlots = 4;
 constexpr int kOddSlots = 8;  // nobody is more than kItemSlots items ahead of another
 struct TileCtrl {
   uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
-  uint64_t land[2], lfree[2];  // 16-bit values as they have come in; codes of keys and values in turn
-  uint64_t sfull[2], pfull[2], done[2], qfull[3], qfree[3], ofree[2], drain;
+  uint64_t land[2], lfree[2];  // 16-bit values as they have come in (two places); codes of keys and of values
+  uint64_t sfull[2], phalf[2], pfull[2], done[2], qfull[3], qfree[3], ofree[2], drain[2];
   uint64_t ifull[kItemSlots], ifree[kItemSlots];
   uint32_t tmem;
   int abort;
@@ -181,9 +188,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t factor) {
-  const uint32_t lo = __byte_perm(w, 0, 0x1404), hi = __byte_perm(w, 0, 0x3424);
-  return make_uint2(mul_bf16x2((lo & 0x80008000u) | ((lo >> 4) & 0x07f007f0u), factor),
-                    mul_bf16x2((hi & 0x80008000u) | ((hi >> 4) & 0x07f007f0u), factor));
+  // a number's two bytes: sign and the code's upper bits, the code's lower bits
+  const uint32_t up = ((w >> 4) & 0x07070707u) | (w & 0x80808080u), lo = (w * 16u) & 0xf0f0f0f0u;
+  return make_uint2(mul_bf16x2(__byte_perm(lo, up, 0x5140), factor), mul_bf16x2(__byte_perm(lo, up, 0x7362), factor));
 }
 // Nonzero in the upper bit of every byte that is a code of NaN.
 __device__ __forceinline__ uint32_t code_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
@@ -269,13 +276,12 @@ struct PagedMaps {
 };
 
 template <int CT, int DP>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
     paged_tile_kernel(const __grid_constant__ PagedParams P, const __grid_constant__ PagedMaps M, int blocks, int items) {
   using C = Layout<DP, CT == SPEC_E4M3>;
   constexpr bool E4 = CT == SPEC_E4M3, BF = CT != SPEC_F16;
-  using R = Regs<E4>;
-  extern __shared__ unsigned char raw[];
-  unsigned char *const smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  using T = Team<E4>;
+  extern __shared__ __align__(1024) unsigned char smem[];
   TileCtrl *const c = reinterpret_cast<TileCtrl *>(smem + C::kCtrl);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, role = tid / 128;
 
@@ -283,14 +289,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->kfull[i], E4 ? 128 : 1);
       mbar_init(&c->vfull[i], 128);
-      mbar_init(&c->kfree[i], 1);
-      mbar_init(&c->vfree[i], 1);
+      mbar_init(&c->kfree[i], 2);
+      mbar_init(&c->vfree[i], 2);
       mbar_init(&c->sfull[i], 1);
+      mbar_init(&c->phalf[i], 128);
       mbar_init(&c->pfull[i], 128);
       mbar_init(&c->done[i], 1);
+      mbar_init(&c->ofree[i], 128);
       mbar_init(&c->land[i], 1);
       mbar_init(&c->lfree[i], 128);
-      mbar_init(&c->ofree[i], 128);
+      mbar_init(&c->drain[i], 1);
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&c->qfull[i], 128);
@@ -298,14 +306,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(&c->ifull[i], 1);
-      mbar_init(&c->ifree[i], 4 + 1 + 1 + 8);  // warps: producers, issue, loads, softmax
+      mbar_init(&c->ifree[i], T::kProducers * 4 + 2 + 1 + 8);  // warps: producers, issue, loads, softmax
     }
     for (int i = 0; i < kOddSlots; ++i) c->odd[i] = 0;
-    mbar_init(&c->drain, 1);
     c->abort = 0;
     fence_mbar_init();
   }
-  if (warp == kIssueWarp) tc_alloc(&c->tmem);
+  if (warp == T::kIssueWarp) tc_alloc(&c->tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -313,16 +320,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint64_t limit = P.wait_limit_ns;
   const bool tree = P.W > 0;
 
-  if (role == 2) {
+  if (role >= 2 && role < T::kRest) {
     // ------------------------------------------------------------ producers
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kProduce));
-    const int pt = tid - 256;
+    // (Of two warpgroups the first has keys and queries, the second values.)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T::kOtherRegs));
+    const int val = E4 ? role - 2 : 1, pt = tid % 128;
     bool live = true;
     // A thread deals with 16-byte pieces of every kStep-th token of a block.
     constexpr int L = E4 ? DP / 16 : DP / 8, kStep = 128 / L, kPer = kBlk / kStep;
     static_assert(!E4 || kPer == L, "a lane's piece is the number of the token whose scale it reads");
     const int pc = pt % L, row0 = pt / L;
-    const uint32_t put0 = E4 ? C::kStage + pt * 16 : (pc / 8) * 16384 + row0 * 128 + (((pc % 8) ^ (row0 & 7)) << 4);
     constexpr int kPut = E4 ? 2048 : kStep * 128;
     int kb = 0, worked = 0, nq = 0;  // blocks, items and row tiles so far
     const bool vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.qs[0] % 8 == 0 && P.qs[1] % 8 == 0 && P.qs[2] % 8 == 0;
@@ -335,13 +342,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (I.nblk == 0) continue;
       const Keys keys(P, I.p0, I.end);
       // queries of a row tile: DP / 8 lanes per row, 16 bytes each, once the scores
-      // of the place's former tile are done
-      auto queries = [&](int tile) {
+      // of the place's former tile are done (all tiles' by the same warps: places are
+      // waited for in order)
+      auto hand_queries = [&]() {
+        cp_async_wait_all();
+        fence_async_smem();
+        for (int t = nq - I.tiles; t < nq; ++t) mbar_arrive(&c->qfull[t % C::kQs]);
+      };
+#pragma unroll 1
+      for (int tile = 0; tile < I.tiles && !(E4 && val); ++tile, ++nq) {
         constexpr int QL = DP / 8, kRows = 128 / QL;
         const int qc = pt % QL, place = nq % C::kQs;
         if (nq >= C::kQs) wait(&c->qfree[place], (nq / C::kQs - 1) & 1);
-        ++nq;
-        if (!live) return;
+        if (!live) break;
         const int r = I.r0 + tile * 128 + pt / QL;
         int t = r / P.G, h = r - t * P.G;  // the row's token and head of the group
         const unsigned short *q = static_cast<const unsigned short *>(P.q) + I.b * P.qs[0] + t * P.qs[1] +
@@ -363,17 +376,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           q += step;
           if (h >= P.G) h -= P.G, ++t, q += wrap;
         }
-      };
-      auto hand_queries = [&](int tiles) {
-        cp_async_wait_all();
-        fence_async_smem();
-        for (int t = nq - tiles; t < nq; ++t) mbar_arrive(&c->qfull[t % C::kQs]);
-      };
-#pragma unroll 1
-      for (int tile = 0; tile < I.tiles; ++tile) {
-        queries(tile);
-        if (!E4 && live) hand_queries(1);
+        if (!E4) {  // the second tile's place may be a while in coming free
+          cp_async_wait_all();
+          fence_async_smem();
+          mbar_arrive(&c->qfull[place]);
+        }
       }
+      if (!live) break;
       // In groups that some query does not see whole, values that are not finite
       // are taken out (it would get 0 * NaN) and put into the answers of the
       // queries that see them at the end; what lies behind the last token was
@@ -390,7 +399,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!live) break;
           const unsigned part = partial(k);
           if (part) {
-            unsigned char *const buf = smem + C::kV + s * C::kOp + put0;
+            unsigned char *const buf = smem + C::kV + s * C::kOp + (pc / 8) * 16384 + row0 * 128 + (((pc % 8) ^ (row0 & 7)) << 4);
             constexpr int kRun = kPer < 8 ? kPer : 8;
             bool some = false, odd = false;
 #pragma unroll 1
@@ -418,50 +427,50 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           mbar_arrive(&c->vfull[s]);
         }
       } else {
-        // Blocks' keys and values in turn (it = 2 k, 2 k + 1), each thread's scale
-        // byte, of the block's token row0 + pc kStep, two turns ahead.
+        // Each thread's scale byte, of the block's token row0 + pc kStep, is asked for
+        // a block ahead.
         Pages where;
-        auto scale = [&](int it) -> uint32_t {
+        auto scale = [&](int k) -> uint32_t {
           uint32_t byte = 0;
-          if (it < 2 * I.nblk) {
-            const int k = it >> 1, row = row0 + pc * kStep, from = (k % 4) * kBlkGroups + row / 16;
-            if (!(it & 1)) where.step(P, I, keys, k, lane);
+          if (k < I.nblk) {
+            const int row = row0 + pc * kStep, from = (k % 4) * kBlkGroups + row / 16;
+            where.step(P, I, keys, k, lane);
             const int pg = __shfl_sync(FULL_MASK, where.page, from), t = __shfl_sync(FULL_MASK, where.token, from);
             const int first = __shfl_sync(FULL_MASK, where.first, from);
             if (pg < P.pages && first + row % 16 < I.end)
-              byte = __ldg((it & 1 ? P.v : P.k) + pg * P.page_stride + (t + row % 16) * P.tok_stride + static_cast<long long>(P.H) * P.D + I.g);
+              byte = __ldg((val ? P.v : P.k) + pg * P.page_stride + (t + row % 16) * P.tok_stride + static_cast<long long>(P.H) * P.D + I.g);
           }
           return byte;
         };
-        uint32_t sc0 = scale(0), sc1 = scale(1);
-        for (int it = 0; it < 2 * I.nblk; ++it) {
-          const int k = it >> 1, at = kb + k, s = at & 1, all = 2 * kb + it;
-          const bool val = it & 1;
+        const unsigned char *const codes = smem + C::kStage + val * (C::kOp / 2) + pt * 16;
+        uint32_t sc0 = scale(0);
+        for (int k = 0; k < I.nblk; ++k) {
+          const int at = kb + k, s = at & 1;
           const unsigned part = val ? partial(k) : 0;
-          const uint32_t sc2 = scale(it + 2);
+          const uint32_t sc1 = scale(k + 1);
           wait(&c->land[val], at & 1);
+          if (k == 0 && live && !val) hand_queries();
           if (at >= 2) wait(val ? &c->vfree[s] : &c->kfree[s], ((at >> 1) - 1) & 1);
           if (!live) break;
           unsigned char *const buf = smem + (val ? C::kV : C::kK) + s * C::kOp;
-          const unsigned char *const codes = smem + put0 + (all & 1) * (C::kOp / 2);
           bool odd = false;
-          uint32_t nans = 0;
           // (255 among them: a scale of NaN)
           const bool large = __any_sync(FULL_MASK, sc0 > kTopScale);
-#pragma unroll
+          const int ch = (pc % 4) * 2, up = pc / 4;
+          uint32_t nans = 0;
+#pragma unroll 4
           for (int i = 0; i < kPer; ++i) {
             const int row = row0 + i * kStep;
-            const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * kPut);
+            uint4 w = *reinterpret_cast<const uint4 *>(codes + i * kPut);
             const uint32_t f = first_factor(__shfl_sync(FULL_MASK, sc0, (lane & ~(L - 1)) + i));
             nans |= code_nan(w.x) | code_nan(w.y) | code_nan(w.z) | code_nan(w.w);
-            const uint2 y0 = codes_to_bf16(w.x, f), y1 = codes_to_bf16(w.y, f), y2 = codes_to_bf16(w.z, f), y3 = codes_to_bf16(w.w, f);
             // the two 16-byte halves, the upper panel's lanes in the other
             // order: eight lanes then cover all banks
-            const int ch = (pc % 4) * 2, up = pc / 4;
+            if (up) w = make_uint4(w.z, w.w, w.x, w.y);
+            const uint2 y0 = codes_to_bf16(w.x, f), y1 = codes_to_bf16(w.y, f), y2 = codes_to_bf16(w.z, f), y3 = codes_to_bf16(w.w, f);
             unsigned char *const to = buf + up * 16384 + row * 128;
-            const uint4 lo = make_uint4(y0.x, y0.y, y1.x, y1.y), hi = make_uint4(y2.x, y2.y, y3.x, y3.y);
-            *reinterpret_cast<uint4 *>(to + (((ch + up) ^ (row & 7)) << 4)) = up ? hi : lo;
-            *reinterpret_cast<uint4 *>(to + (((ch + 1 - up) ^ (row & 7)) << 4)) = up ? lo : hi;
+            *reinterpret_cast<uint4 *>(to + (((ch + up) ^ (row & 7)) << 4)) = make_uint4(y0.x, y0.y, y1.x, y1.y);
+            *reinterpret_cast<uint4 *>(to + (((ch + 1 - up) ^ (row & 7)) << 4)) = make_uint4(y2.x, y2.y, y3.x, y3.y);
           }
           // what is rare: large scales, codes and scales of NaN
           if (large || __any_sync(FULL_MASK, nans != 0)) {
@@ -484,7 +493,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 drop_not_finite<true>(hi);
                 odd = odd || !behind(k, row);
               }
-              const int ch = (pc % 4) * 2, up = pc / 4;
               unsigned char *const to = buf + up * 16384 + row * 128;
               *reinterpret_cast<uint4 *>(to + ((ch ^ (row & 7)) << 4)) = lo;
               *reinterpret_cast<uint4 *>(to + (((ch + 1) ^ (row & 7)) << 4)) = hi;
@@ -494,110 +502,102 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (odd) c->odd[worked % kOddSlots] = I.item + 1;
           fence_async_smem();
           mbar_arrive(val ? &c->vfull[s] : &c->kfull[s]);
-          if (it == 0) hand_queries(I.tiles);
           sc0 = sc1;
-          sc1 = sc2;
         }
       }
       kb += I.nblk;
       ++worked;
     }
     cp_async_wait_all();
-  } else if (role == 3) {
+  } else if (role == T::kRest) {
     // ------------------------------------------------- tensor-core issue
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssue));
-    // All of a warp runs through this and one lane does it: with operands that the
-    // compiler knows to be the same in all lanes, an instruction is issued in half the
-    // time that it takes a lane on its own (and that bounded the whole kernel).
-    if (warp == kIssueWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T::kOtherRegs));
+    // A warp for each tile: the tensor cores take an instruction at a time from each
+    // and hardly queue any, so that with one warp for both they stood still while it
+    // waited (150 us a prompt, so 145).  All of a warp runs through this and one lane
+    // does it, with operands that the compiler knows to be the same in all lanes.
+    if (warp == T::kIssueWarp || warp == T::kIssueWarp + 1) {
+      const int t = __shfl_sync(FULL_MASK, warp == T::kIssueWarp + 1, 0);
       const uint32_t qk = inst_desc(BF, kBlk, false), wv = inst_desc(BF, DP, true);
-      const uint32_t base = __shfl_sync(FULL_MASK, smem_u32(smem), 0), tm = __shfl_sync(FULL_MASK, tmem, 0);
+      const uint32_t base = __shfl_sync(FULL_MASK, smem_u32(smem), 0), tm = __shfl_sync(FULL_MASK, tmem, 0) + t * 128;
       const uint64_t qd = op_desc(base + C::kQ, 16), kd = op_desc(base + C::kK, 16), vd = op_desc(base + C::kV, 16384);
-      auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL_MASK, wait_on(c, bar, parity, limit)); };
-      auto commit = [&](uint64_t *bar) {
-        if (elect_one()) tc_commit(bar);
-      };
-      auto scores = [&](int tile, int place, int at) {
-        const uint64_t a = qd + static_cast<uint32_t>(place * C::kOp >> 4), bb = kd + static_cast<uint32_t>((at & 1) * C::kOp >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int d = 0; d < DP / 16; ++d) {
-            const int off = ((d / 4) * 16384 + (d % 4) * 32) >> 4;
-            tc_mma_ss(tm + tile * 128, a + off, bb + off, qk, d > 0);
-          }
-          tc_commit(&c->sfull[tile]);
-        }
-      };
-      auto values = [&](int tile, int at, bool acc) {
-        const uint64_t bb = vd + static_cast<uint32_t>((at & 1) * C::kOp >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int j = 0; j < kBlk / 16; ++j)
-            tc_mma_ts(tm + 256 + tile * 128, tm + tile * 128 + j * 8, bb + (j * 2048 >> 4), wv, acc || j > 0);
-        }
-      };
       bool live = true;
-      int kb = 0, nq = 0, nb[2] = {0, 0}, ni[2] = {0, 0};  // blocks and row tiles in all; of each tile, blocks and items
+      auto wait = [&](uint64_t *bar, uint32_t parity) { live = live && __all_sync(FULL_MASK, wait_on(c, bar, parity, limit)); };
+      int kb = 0, nq = 0, ni = 0, nb = 0;  // blocks and row tiles in all; the tile's items and blocks
       for (int turn = 0; live; ++turn) {
         const int slot = turn % kItemSlots;
-        live = wait(&c->ifull[slot], (turn / kItemSlots) & 1);
+        wait(&c->ifull[slot], (turn / kItemSlots) & 1);
         if (!live) break;
         const int item = __shfl_sync(FULL_MASK, c->items[slot].item, 0);
         const int nblk = __shfl_sync(FULL_MASK, c->items[slot].nblk, 0), tiles = __shfl_sync(FULL_MASK, c->items[slot].tiles, 0);
         if (lane == 0) mbar_arrive(&c->ifree[slot]);
         if (item < 0) break;
         if (nblk == 0) continue;
-#pragma unroll 1
-        for (int t = 0; t < tiles && live; ++t) {
+        if (t < tiles) {
+          const bool both = tiles == 1;  // an item of one tile speaks for the other, too
           const int place = (nq + t) % C::kQs;
-          live = wait(&c->qfull[place], ((nq + t) / C::kQs) & 1);
-          if (live && t == 0) live = wait(&c->kfull[kb & 1], (kb >> 1) & 1);
-          if (!live) break;
-          tc_fence_after();
-          scores(t, place, kb);
-          if (nblk == 1) commit(&c->qfree[place]);
-        }
-        if (live) commit(&c->kfree[kb & 1]);
-        for (int k = 0; k < nblk && live; ++k) {
-          const int at = kb + k;
+          wait(&c->qfull[place], ((nq + t) / C::kQs) & 1);
+          // block k's weights times values, then block k + 1's scores in their place
 #pragma unroll 1
-          for (int t = 0; t < tiles && live; ++t) {
-            live = wait(&c->pfull[t], (nb[t] + k) & 1);
-            if (live && t == 0) live = wait(&c->vfull[at & 1], (at >> 1) & 1);
-            // the item before's answers have to be out of the sums
-            if (live && k == 0 && ni[t] > 0) live = wait(&c->ofree[t], (ni[t] - 1) & 1);
-            if (!live) break;
-            tc_fence_after();
-            values(t, at, k > 0);
-            if (k + 1 < nblk) {
-              if (t == 0) live = wait(&c->kfull[(at + 1) & 1], ((at + 1) >> 1) & 1);
+          for (int k = -1; k < nblk; ++k) {
+            const int at = kb + k;
+            if (k >= 0) {
+              wait(&c->vfull[at & 1], (at >> 1) & 1);
+              // the item before's answers have to be out of the sums
+              if (k == 0 && ni > 0) wait(&c->ofree[t], (ni - 1) & 1);
+              // the first half's product runs while the second half's weights are made
+              // (a prompt 148 us without, 142 with)
+              wait(&c->phalf[t], (nb + k) & 1);
+              if (!live) break;
+              const uint64_t bb = vd + static_cast<uint32_t>((at & 1) * C::kOp >> 4);
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int j = 0; j < kBlk / 32; ++j) tc_mma_ts(tm + 256, tm + j * 8, bb + (j * 2048 >> 4), wv, k > 0 || j > 0);
+              }
+              wait(&c->pfull[t], (nb + k) & 1);
               if (!live) break;
               tc_fence_after();
-              const int place = (nq + t) % C::kQs;
-              scores(t, place, at + 1);
-              if (k + 2 == nblk) commit(&c->qfree[place]);  // the tile's last scores
-            } else {
-              commit(&c->done[t]);
+              if (elect_one()) {
+#pragma unroll
+                for (int j = kBlk / 32; j < kBlk / 16; ++j) tc_mma_ts(tm + 256, tm + j * 8, bb + (j * 2048 >> 4), wv, true);
+                tc_commit(&c->vfree[at & 1]);
+                if (both) tc_commit(&c->vfree[at & 1]);
+                if (k + 1 == nblk) tc_commit(&c->done[t]);
+              }
+              if (k + 1 == nblk) break;
+            }
+            wait(&c->kfull[(at + 1) & 1], ((at + 1) >> 1) & 1);
+            if (!live) break;
+            const uint64_t a = qd + static_cast<uint32_t>(place * C::kOp >> 4), bb = kd + static_cast<uint32_t>(((at + 1) & 1) * C::kOp >> 4);
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int d = 0; d < DP / 16; ++d) {
+                const int off = ((d / 4) * 16384 + (d % 4) * 32) >> 4;
+                tc_mma_ss(tm, a + off, bb + off, qk, d > 0);
+              }
+              tc_commit(&c->sfull[t]);
+              tc_commit(&c->kfree[(at + 1) & 1]);
+              if (both) tc_commit(&c->kfree[(at + 1) & 1]);
+              if (k + 2 == nblk) tc_commit(&c->qfree[place]);  // the tile's last
             }
           }
-          if (live) {
-            commit(&c->vfree[at & 1]);
-            if (k + 1 < nblk) commit(&c->kfree[(at + 1) & 1]);
-          }
+          ++ni;
+          nb += nblk;
         }
         kb += nblk;
         nq += tiles;
-        for (int t = 0; t < tiles; ++t) nb[t] += nblk, ++ni[t];
       }
       if (!live) {  // let what was issued end before tensor memory is given back
-        commit(&c->drain);
-        mbar_wait_bounded(&c->drain, 0, limit);
+        if (elect_one()) tc_commit(&c->drain[t]);
+        mbar_wait_bounded(&c->drain[t], 0, limit);
       }
-    } else if (warp == kLoadWarp) {
+    } else if (warp == T::kLoadWarp) {
       // ------------------------------------------- keys and values on their way
       bool live = true;
       int kb = 0;
-      uint32_t brought[2] = {0, 0};  // boxes' turns so far: keys, values
+      uint32_t brought[2] = {0, 0};  // times so far: keys, values
       TileItem I;
       for (int turn = 0; live && take_item(c, turn, I, limit) && I.item >= 0; ++turn) {
         const Keys keys(P, I.p0, I.end);
@@ -606,7 +606,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int k = it >> 1, at = kb + k, s = at & 1;
           const bool val = it & 1;
           if (!val) where.step(P, I, keys, k, lane);
-          // codes: the places of keys and values take turns; 16-bit entries: blocks do
+          // codes: the place of keys or of values once it has been read; 16-bit entries:
+          // a block's
           if constexpr (E4) {
             if (at >= 1) live = __all_sync(FULL_MASK, wait_on(c, &c->lfree[val], (at - 1) & 1, limit));
           } else {
@@ -640,16 +641,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // Nothing may come in behind the block's end, if a wait of whichever warp ran
       // out: each place's last boxes are waited for (and of no phase but a barrier's
       // last: one before it would count as still to come).
-      for (int val = 0; val < 2; ++val) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
         constexpr uint32_t kPlaces = E4 ? 1 : 2;
-        for (uint32_t n = brought[val] > kPlaces ? brought[val] - kPlaces : 0; n < brought[val]; ++n) {
+        for (uint32_t n = brought[i] > kPlaces ? brought[i] - kPlaces : 0; n < brought[i]; ++n) {
           if constexpr (E4)
-            mbar_wait_bounded(&c->land[val], n & 1, limit);
+            mbar_wait_bounded(&c->land[i], n & 1, limit);
           else
-            mbar_wait_bounded(val ? &c->land[n & 1] : &c->kfull[n & 1], (n >> 1) & 1, limit);
+            mbar_wait_bounded(i ? &c->land[n & 1] : &c->kfull[n & 1], (n >> 1) & 1, limit);
         }
       }
-    } else if (warp == kItemWarp) {
+    } else if (warp == T::kItemWarp) {
       // ------------------------------------------------------------- items
       if (lane == 0) {
         bool live = true;
@@ -670,7 +672,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else {
     // --------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(T::kSoftmaxRegs));
     const int tile = role, rr = tid;  // tile and row of the block: tile * 128 + lane of tensor memory
     const int wt = tid % 128;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -678,20 +680,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const float sc = fmaxf(fabsf(P.scale), 1e-37f);  // not zero: a key that is not seen has the score -inf
     const bool minus = P.scale < 0.f, sectors = reinterpret_cast<uintptr_t>(P.out) % 32 == 0;
     bool live = true, checked = false;
-    int nb = 0, ni = 0, worked = 0;  // the tile's blocks and items; items with keys
+    int worked = 0;  // items with keys
+    uint32_t ni = 0, nb = 0;  // the tile's items and blocks so far
     if (tree) grid_dependency_wait();
-    for (int turn = 0;; ++turn) {
-      TileItem I;
-      if (live) live = take_item(c, turn, I, limit);
-      if (!live) {  // what is left is empty, too
-        const int item = blockIdx.x + turn * gridDim.x;
-        if (item >= items) break;
-        I = make_item(P, item, blocks);
-      }
-      if (I.item < 0) break;
+    TileItem next;
+    next.tiles = next.nblk = 0;
+    next.item = next.b = next.g = next.blk = next.split = next.n = next.cnt = next.r0 = next.end = next.p0 = next.p1 = next.g0 = next.g1 = 0;
+    for (int turn = -1; next.item >= 0; ++turn) {
+      const TileItem I = next;
       const int slot = worked % kOddSlots;
       worked += I.nblk > 0;
-      if (tile >= I.tiles) continue;
+      const bool here = tile < I.tiles, work = here && I.nblk > 0 && live;
       const int r = I.r0 + rr;
       int at = -1, my = 0;  // the thread's output row (-1: past the last) and token
       if (r < P.N * P.G) {
@@ -712,14 +711,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (P.lse) P.lse[at] = -INFINITY;
         if (timeout && P.row_status) P.row_status[I.b] = SPEC_ROW_TIMEOUT;
       };
-      if (I.nblk == 0 || !live) {
+      if (here && !work) {
         if (wt == 0 && tile == 0 && P.splits > 1) P.oflag[flag] = 0;
         if (!checked) grid_dependency_wait();  // the status may not come before the check's
         checked = true;
         empty(I.nblk > 0);
-        continue;
       }
-      const bool mine = use && (!tree || P.rowinfo[I.b] >= 0);
+      const bool mine = work && use && (!tree || P.rowinfo[I.b] >= 0);
       const int p = I.n + (tree ? mine ? P.depth[static_cast<size_t>(I.b) * P.N + my] : 0 : my);
       const int from = window_from(P, p);
       const uint32_t *const anc = tree ? P.anc + (static_cast<size_t>(I.b) * P.N + my) * P.W : nullptr;
@@ -728,10 +726,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int r_first = I.r0 + (rr & ~31), q_first = min(r_first / P.G, P.N - 1), q_last = min((r_first + 31) / P.G, P.N - 1);
       const int p0 = tree ? I.p0 : I.n + q_first, p1 = tree ? I.p1 : I.n + q_last;
       float m = -INFINITY, l = 0.f;
-      for (int k = 0; k < I.nblk; ++k) {
-        live = __all_sync(FULL_MASK, wait_on(c, &c->sfull[tile], (nb + k) & 1, limit));
-        if (!live) break;
-        tc_fence_after();
+      for (int k = 0; work && k < I.nblk; ++k) {
         // Groups of the block that some query of the warp does not see whole: what is
         // not seen gets the score -inf, in tensor memory and ahead of the rest, so
         // that this code, which most blocks pass by, stays out of the loop's way (the
@@ -741,6 +736,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int gi = I.g0 + k * kBlkGroups + (lane & 7);
           part = __ballot_sync(FULL_MASK, gi >= I.g1 || group_masked(P, keys.token(gi), I.n, p0, p1)) & 0xffu;
         }
+        live = __all_sync(FULL_MASK, wait_on(c, &c->sfull[tile], (nb + k) & 1, limit));
+        if (!live) break;
+        tc_fence_after();
         if (part || minus) {
 #pragma unroll 1
           for (int q = 0; q < 4; ++q, part >>= 2) {
@@ -822,6 +820,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         weights(s[0], 0);
         tc_ld32(s[0], s_addr + 64);
         weights(s[1], 1);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&c->phalf[tile]);
         tc_wait_ld();
         tc_ld32(s[1], s_addr + 96);
         weights(s[0], 2);
@@ -832,6 +833,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_fence_before();
         mbar_arrive(&c->pfull[tile]);
       }
+      // the next item, while the last product is made
+      if (live) live = take_item(c, turn + 1, next, limit);
+      if (!live) {  // what is left is empty, too
+        const int item = blockIdx.x + (turn + 1) * gridDim.x;
+        next.item = -1;
+        if (item < items) next = make_item(P, item, blocks);
+      }
+      if (!work) continue;
       nb += I.nblk;
       if (!checked) grid_dependency_wait();  // the row's check
       checked = true;
@@ -888,18 +897,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (odd && some && !split) {
-        using T = typename CacheType<BF ? SPEC_BF16 : SPEC_F16>::type;
+        using N = typename CacheType<BF ? SPEC_BF16 : SPEC_F16>::type;
 #pragma unroll 1
         for (int d = 0; d < P.D; ++d) {
-          T *const y = reinterpret_cast<T *>(answer) + d;
-          *y = T(static_cast<float>(*y) + paged_odd_sum<CT>(P, I.b, my, I.cnt, I.n, p, I.g, d));
+          N *const y = reinterpret_cast<N *>(answer) + d;
+          *y = N(static_cast<float>(*y) + paged_odd_sum<CT>(P, I.b, my, I.cnt, I.n, p, I.g, d));
         }
       }
     }
   }
   __syncthreads();
   grid_dependency_wait();
-  if (warp == kIssueWarp) {
+  if (warp == T::kIssueWarp) {
     __syncwarp();
     tc_fence_after();
     tc_dealloc(tmem);
@@ -928,7 +937,7 @@ cudaError_t launch(const PagedParams &p, cudaStream_t s) {
   const long long items = static_cast<long long>(p.B) * p.H * blocks * p.splits;
   if (items > 0x7fffffffLL - 4096) return cudaErrorInvalidValue;
   static_assert(C::kSmem <= 227 * 1024, "shared memory of a block");
-  cudaError_t e = allow_smem<paged_tile_kernel<CT, DP>>(C::kSmem, kLaunchRegs);
+  cudaError_t e = allow_smem<paged_tile_kernel<CT, DP>>(C::kSmem, Team<E4>::kLaunchRegs);
   if (e != cudaSuccess) return e;
   const EncodeTiled encode = encode_tiled();
   if (!encode) return cudaErrorNotSupported;
@@ -945,7 +954,7 @@ cudaError_t launch(const PagedParams &p, cudaStream_t s) {
                E4 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(items < kPagedSms ? items : kPagedSms);
-  return launch_after(paged_tile_kernel<CT, DP>, dim3(grid), kTileThreads, C::kSmem, s, true, p, m, blocks, static_cast<int>(items));
+  return launch_after(paged_tile_kernel<CT, DP>, dim3(grid), Team<E4>::kThreads, C::kSmem, s, true, p, m, blocks, static_cast<int>(items));
 }
 
 template <int CT>
