@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged_attention.cuh"
@@ -87,8 +88,10 @@ __global__ void __launch_bounds__(kCheckThreads) paged_check_kernel(const __grid
 // The products are made the other way round: scores as K Q^T, sums as V^T P^T, so
 // that keys fill the matrix instruction's 16 rows and query rows go in eights: 4
 // rows of a decoding token are padded to 8, 24 of a chain not at all.  (With the
-// queries as the 16 rows every item did twice to 4/3 of the work, at twice the
-// registers: 64 decoding rows in e4m3 100 us, 64 chains of 24 in bf16 97.)
+// queries as the 16 rows every item does twice to 4/3 of the work, with the
+// registers of twice the sums: 64 decoding rows of 4 in e4m3 100 us, this way 89; 64
+// chains of 24 rows 132 and 103, in bf16 105 and 101.  It is the better way for
+// just 16 rows over codes alone, 60 and 75 us for 32 rows.)
 template <int CT, int DP, int NT>
 struct PagedRowCfg {
   static constexpr bool E4 = CT == SPEC_E4M3;
@@ -104,7 +107,10 @@ struct PagedRowCfg {
   static constexpr int kOPitch = DP + 4;                    // floats: eight rows of sums at the end
   static constexpr int kLast = (kStages - 1) * kStage + (kStage > kQ ? kStage : kQ);
   static constexpr int kSmem = kLast > 8 * kOPitch * 4 ? kLast : 8 * kOPitch * 4;
-  static constexpr int kWarps = DP <= 64 ? (NT <= 2 ? 16 : 12) : NT <= 1 ? (E4 ? 14 : 12) : NT == 2 ? 12 : 8;  // items per SM
+  // Items per SM.  A multiple of four: an SM's registers lie in four parts, and what
+  // does not fit its part waits (64 decoding rows in e4m3: 89 us with 12, 112 with
+  // 14 of the 144 registers that 14 would leave).
+  static constexpr int kWarps = DP <= 64 ? (NT <= 2 ? 16 : 12) : NT == 1 ? 12 : 8;
 };
 
 // The 8 x 8 matrix of 16-bit numbers whose rows the lanes' quads hold, transposed.
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
     }
     // the values' loads, ahead of what their weights take
     constexpr int kCols = DP / 8;  // codes: columns of a quad
-    constexpr bool kEarly = E4 ? NT <= 2 : NT <= 3;
+    constexpr bool kEarly = E4 ? NT == 1 : NT <= 3;
     uint32_t vw[E4 ? kCols / 8 : 1][4][2], vf[E4 ? 1 : kSteps][4];
     auto load_codes = [&](int n0) {
       // of tokens 2 j4, 2 j4 + 1, 8 + 2 j4, 9 + 2 j4 the quad's columns
@@ -792,10 +798,13 @@ cudaError_t launch_rows_d(const PagedParams &p, cudaStream_t s) {
 }
 
 // Items of the rows kernel that run on an SM at a time.
-template <int CT>
-int rows_per_sm(bool small, int oblk) {
-  if (small) return oblk <= 16 ? PagedRowCfg<CT, 64, 1>::kWarps : PagedRowCfg<CT, 64, 4>::kWarps;
-  return oblk == 8 ? PagedRowCfg<CT, 128, 1>::kWarps : oblk == 16 ? PagedRowCfg<CT, 128, 2>::kWarps : PagedRowCfg<CT, 128, 4>::kWarps;
+int rows_per_sm(int ct, int D, int oblk) {
+  auto of = [&](auto c) {
+    constexpr int CT = decltype(c)::value;
+    if (D <= 64) return oblk <= 16 ? PagedRowCfg<CT, 64, 1>::kWarps : PagedRowCfg<CT, 64, 4>::kWarps;
+    return oblk == 8 ? PagedRowCfg<CT, 128, 1>::kWarps : PagedRowCfg<CT, 128, 2>::kWarps;
+  };
+  return ct == SPEC_E4M3 ? of(std::integral_constant<int, SPEC_E4M3>()) : of(std::integral_constant<int, SPEC_BF16>());
 }
 
 struct PagedPlan {
@@ -855,8 +864,7 @@ PagedPlan plan_paged(const spec_paged_attention_args *a) {
     const long long want = (8LL * kPagedSms * 2 + items - 1) / items;
     p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 32})));
     // A few rows are cut by a budget of parts, all items side by side.
-    const int per_sm = a->cache_dtype == SPEC_E4M3 ? rows_per_sm<SPEC_E4M3>(a->head_dim <= 64, p.oblk) : rows_per_sm<SPEC_BF16>(a->head_dim <= 64, p.oblk);
-    const long long budget = static_cast<long long>(per_sm) * kPagedSms / a->heads;
+    const long long budget = static_cast<long long>(rows_per_sm(a->cache_dtype, a->head_dim, p.oblk)) * kPagedSms / a->heads;
     if (blocks == 1 && a->B <= kMaxCutRows && budget > a->B) {
       p.budget = static_cast<int>(budget);
       p.splits = static_cast<int>(std::min<long long>({32, (tokens + 63) / 64, budget - a->B + 1}));
