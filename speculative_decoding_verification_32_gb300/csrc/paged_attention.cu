@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kCheckThreads) paged_check_kernel(const __grid
 // that keys fill the matrix instruction's 16 rows and query rows go in eights: 4
 // rows of a decoding token are padded to 8, 24 of a chain not at all.  (With the
 // queries as the 16 rows every item does twice to 4/3 of the work, with the
-// registers of twice the sums: 64 decoding rows of 4 in e4m3 100 us, this way 89; 64
+// registers of twice the sums: 64 decoding rows of 4 in e4m3 100 us, this way 86; 64
 // chains of 24 rows 132 and 103, in bf16 105 and 101.  It is the better way for
 // just 16 rows over codes alone, 60 and 75 us for 32 rows.)
 template <int CT, int DP, int NT>
@@ -97,7 +97,7 @@ struct PagedRowCfg {
   static constexpr bool E4 = CT == SPEC_E4M3;
   static constexpr int kEsz = E4 ? 1 : 2;
   static constexpr int kM = 8 * NT;                         // query rows
-  static constexpr int kStages = E4 ? 3 : 2;
+  static constexpr int kStages = 2;                         // (64 decoding rows in e4m3 86 us; with three 89)
   static constexpr int kPitch = DP * kEsz + 16;             // bytes of one token in a ring slot
   static constexpr int kPlane = kGroup * kPitch;            // K or V of a group
   static constexpr int kScales = E4 ? 2 * kGroup * 4 : 0;   // scale words, K then V
@@ -108,7 +108,7 @@ struct PagedRowCfg {
   static constexpr int kLast = (kStages - 1) * kStage + (kStage > kQ ? kStage : kQ);
   static constexpr int kSmem = kLast > 8 * kOPitch * 4 ? kLast : 8 * kOPitch * 4;
   // Items per SM.  A multiple of four: an SM's registers lie in four parts, and what
-  // does not fit its part waits (64 decoding rows in e4m3: 89 us with 12, 112 with
+  // does not fit its part waits (64 decoding rows in e4m3: 86 us with 12, 112 with
   // 14 of the 144 registers that 14 would leave).
   static constexpr int kWarps = DP <= 64 ? (NT <= 2 ? 16 : 12) : NT == 1 ? 12 : 8;
 };
