@@ -684,7 +684,8 @@ spec_status spec_token_logprobs(const spec_logprobs_args *args, const spec_logpr
  * its head and given back behind its tail, both in the order of rows, then
  * places, so the result does not depend on timing; pages given back by a call
  * are not taken by the same call.  A new ring is {0, 1, ..., num_pages - 1}
- * with free_state {0, num_pages}.
+ * with free_state {0, num_pages}.  A page is one row's: one that several rows
+ * name (a common prompt's) would come back once for each of them.
  *
  * slot_map [B, N]: the slot number of token kv_len[b] + i for i < count[b], else
  * -1.  row_status [B] (optional):
@@ -843,9 +844,10 @@ spec_status spec_paged_attention(const spec_paged_attention_args *args, void *ou
  * logits [B, V], rows row_stride elements apart (>= V), SPEC_BF16 or SPEC_F32.
  * row_status [B]: NONFINITE (a NaN or +inf logit), BAD_UNIFORM, EMPTY (no finite
  * logit), BAD_TEMPERATURE; a flagged row's token is -1 and its prob NaN.
- * Weights are fp32 with relative errors of about 2^-22, which average out in
- * the sums; sums are exact integers of 2^-44, the same in any order.  A draw
- * within about 1e-8 of a boundary of the law, or a top_p within that of a
+ * Weights are fp32: the exponent -y of a weight 2^-y is rounded (which makes up to
+ * about y 2^-23 of it) and the power is the hardware's (2^-22); sums are exact
+ * integers of 2^-44, the same in any order.  So a draw within about 2e-6 of a
+ * boundary of the law (E[y], at most log2 V, times 2^-23), or a top_p within that of a
  * group's mass, may fall to either side.  One launch, no workspace; B < 2^25.
  */
 typedef struct {

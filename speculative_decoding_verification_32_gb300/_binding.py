@@ -533,6 +533,7 @@ for _s, _t in ((_PACK_APPEND, SpecKvAppendArgs), (_PACK_READ, SpecKvReadArgs),
 _KV_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_Tensor, _int32, _empty = torch.Tensor, torch.int32, torch.empty
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 _fast = {}
 
@@ -646,6 +647,8 @@ def _i32(t, name, dev, shape):
     """The address of an int32 tensor of this shape, or 0 for None."""
     if t is None:
         return 0
+    if type(t) is _Tensor and t.dtype is _int32 and t.device == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()  # small calls take longer to check than to run
     _req(t, name, dev, torch.int32)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -844,7 +847,7 @@ def spec_token_logprobs(logits, tokens=None, temperature=None, m=0, stream=None)
 
 def _same_device(stream, t):
     """Whether a call on t's device needs no context of its own."""
-    return stream is None and t.is_cuda and t.device.index == _current_device()
+    return stream is None and t.is_cuda and t.get_device() == _current_device()
 
 
 def spec_page_plan(block_table, free_pages, free_state, kv_len, N, page_size, count=None, window=0, sinks=0,
@@ -874,8 +877,8 @@ def spec_page_plan(block_table, free_pages, free_state, kv_len, N, page_size, co
     a = _PACK_PLAN.pack(*head)
     on = None if _same_device(stream, block_table) else _enter(dev, stream, block_table, free_pages, free_state, kv_len, count)
     try:
-        slots = torch.empty(B, max(N, 0), dtype=torch.int32, device=dev)
-        status = torch.empty(B, dtype=torch.int32, device=dev)
+        slots = _empty(B, max(N, 0), dtype=_int32, device=dev)
+        status = _empty(B, dtype=_int32, device=dev)
         s = _raw_stream(dev.index)
         f, code, key = _fn("spec_page_plan", 6), SPEC_ERR_WORKSPACE, (dev.index, "scratch", s)
         with _enqueue_locks.get(key) or _enqueuing(key):
@@ -919,7 +922,7 @@ def spec_kv_compact_pages(kv, block_table, kv_len_in, accepted_len, path_nodes, 
                            _i32(path_nodes, "path_nodes", dev, (B, path_nodes.shape[1])))
     on = None if _same_device(stream, kv) else _enter(dev, stream, kv, block_table, kv_len_in, accepted_len, path_nodes)
     try:
-        status = torch.empty(B, dtype=torch.int32, device=dev)
+        status = _empty(B, dtype=_int32, device=dev)
         _check(_fn("spec_kv_compact_pages", 3)(a, status.data_ptr(), _raw_stream(dev.index)))
     finally:
         _leave(on)
@@ -967,9 +970,9 @@ def spec_paged_attention(q, cache, block_table, kv_len, parent=None, count=None,
     index = dev.index
     on = None if _same_device(stream, q) else _enter(dev, stream, q, cache, block_table, kv_len, parent, count)
     try:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-        lse = torch.empty(B, N, heads, dtype=torch.float32, device=dev)
-        status = (torch.empty if N else torch.zeros)(B, dtype=torch.int32, device=dev)
+        out = _empty(shape, dtype=dtype, device=dev)
+        lse = _empty(B, N, heads, dtype=torch.float32, device=dev)
+        status = (_empty if N else torch.zeros)(B, dtype=_int32, device=dev)
         s = _raw_stream(index)
         f, code, key = _fn("spec_paged_attention", 7), SPEC_ERR_WORKSPACE, (index, "scratch", s)
         with _enqueue_locks.get(key) or _enqueuing(key):
@@ -989,6 +992,8 @@ def _per_row(t, name, dev, dtype, B):
     """The address of a tensor of one number per row, or 0 for None."""
     if t is None:
         return 0
+    if type(t) is _Tensor and t.dtype is dtype and t.device == dev and t.shape == (B,) and t.is_contiguous():
+        return t.data_ptr()
     _req(t, name, dev, dtype)
     if t.shape != (B,):
         raise ValueError(f"{name} must be [{B}], got {list(t.shape)}")
@@ -1021,9 +1026,9 @@ def spec_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None,
                           _per_row(min_p, "min_p", dev, f32, B))
     on = None if _same_device(stream, logits) else _enter(dev, stream, logits, u, temperature, top_k, top_p, min_p)
     try:
-        out = dict(token=torch.empty(B, dtype=torch.int32, device=dev),
-                   prob=torch.empty(B, dtype=f32, device=dev),
-                   row_status=torch.empty(B, dtype=torch.int32, device=dev))
+        out = dict(token=_empty(B, dtype=_int32, device=dev),
+                   prob=_empty(B, dtype=f32, device=dev),
+                   row_status=_empty(B, dtype=_int32, device=dev))
         o = _PACK_SAMPLE_OUT.pack(out["token"].data_ptr(), out["prob"].data_ptr(), out["row_status"].data_ptr())
         _check(_fn("spec_sample", 3)(a, o, _raw_stream(dev.index)))
     finally:

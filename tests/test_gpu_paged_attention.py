@@ -145,6 +145,31 @@ def test_prompts(sv, kind, qt, N, Hq, H, D, lens, page, window, sinks):
     Problem(sv, 2, N, Hq, H, D, lens, page, window, sinks, kind, qt).check()
 
 
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("kind", ["bfloat16", "uint8"])
+def test_many_items(sv, kind, tree):
+    """More items than SMs: blocks of two row tiles, of one and of none follow one another, with few keys and
+    with many; what is not finite in one row is not another's."""
+    import torch
+    B = 44
+    p = Problem(sv, B, 130, 8, 4, 64, [(53 * b) % 400 for b in range(B)], 16, 90, 4, kind, tree=tree,
+                count=[0 if b % 11 == 3 else 1 + (37 * b) % 130 for b in range(B)])
+    clean = p.check()
+    b, t = next((b, t) for b in range(5, B) for t in range(p.lens[b]) if p.c[b] > 60 and p.see[b][0, t] and not p.see[b][:, t].all())
+    g = p.table[b, t // 16]
+    if kind == "uint8":
+        p.cache[1, g, t % 16, 64 + 5] = 0x7f  # head 1: one code
+    else:
+        p.cache[1, g, t % 16, 1, 5] = float("inf")
+    out, lse, status = p.run()
+    assert not status.any() and torch.equal(lse, clean[1])
+    want = clean[0].clone()
+    sees = torch.from_numpy(p.see[b][:, t].copy()).cuda().nonzero()[:, 0]
+    for h in (2, 3):
+        want[b, sees, h, 5] = float("nan") if kind == "uint8" else float("inf")
+    assert torch.equal(out.nan_to_num(nan=7e4), want.nan_to_num(nan=7e4))
+
+
 @pytest.mark.parametrize("kind,qt", KINDS)
 @pytest.mark.parametrize("N,Hq,H,D,lens,window,sinks", [
     (10, 16, 4, 64, [0, 40, 333], 0, 0), (60, 8, 2, 128, [500, 0, 64], 100, 4), (33, 4, 4, 128, [20, 31, 700], 3, 0),

@@ -1,10 +1,11 @@
 """spec_sample against a plain 64-bit restatement (needs a GB300).
 
-The kernel's weights are exp((l - M) / T) with a relative error of at most 2^-20 (two roundings
-of the exponent's remainder to first order and a hardware power of two, 2^-22 by its
-specification); its sums are exact but for rounding each vector's part to 2^-44 and an fp32
-sum of up to 8 terms (7 * 2^-24).  A running sum over a sum is therefore within 2^-18 of the
-law's, and so is a probability, relative.  So: the token must be the law's at some uniform within
+The kernel's weights are 2^-y with y = (M - l) log2(e) / T: three roundings of y (3 y 2^-24, of the
+weight 3 y ln 2 2^-24) and a hardware power of two (2^-22 by its specification); its sums are exact but
+for rounding each vector's part to 2^-44 and an fp32 sum of up to 8 terms (7 * 2^-24).  Over a law the
+mean of y is at most log2 V <= 17.3 here, so a running sum over a sum is within
+17.3 * 3 ln 2 2^-24 + 2^-22 + 7 * 2^-24 = 2.8e-6 < 2^-18 of the law's, and a probability, of tokens drawn
+at all (y <= 25), within twice that, relative.  So: the token must be the law's at some uniform within
 2^-18 of the given one, where a group of equal logits may be in or out of top-p's set if its
 mass is within 2^-18 of the border."""
 import numpy as np
