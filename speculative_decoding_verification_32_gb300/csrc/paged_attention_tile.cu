@@ -686,18 +686,18 @@ __global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
     TileItem next;
     next.tiles = next.nblk = 0;
     next.item = next.b = next.g = next.blk = next.split = next.n = next.cnt = next.r0 = next.end = next.p0 = next.p1 = next.g0 = next.g1 = 0;
+    struct Row {
+      int at, my;     // the thread's output row (-1: past the last) and token
+      int p, p0, p1;  // its position; the warp's rows' lie in p0 .. p1
+      bool use;
+    } row = {-1, 0, 0, 0, 0, false};
     for (int turn = -1; next.item >= 0; ++turn) {
       const TileItem I = next;
+      const int at = row.at, my = row.my, p = row.p, p0 = row.p0, p1 = row.p1;
+      const bool use = row.use;
       const int slot = worked % kOddSlots;
       worked += I.nblk > 0;
       const bool here = tile < I.tiles, work = here && I.nblk > 0 && live;
-      const int r = I.r0 + rr;
-      int at = -1, my = 0;  // the thread's output row (-1: past the last) and token
-      if (r < P.N * P.G) {
-        my = r / P.G;
-        at = (I.b * P.N + my) * P.Hq + I.g * P.G + (r - my * P.G);
-      }
-      const bool use = at >= 0 && my < I.cnt;
       const long long ml_at = static_cast<long long>(I.split) * P.rows + at;
       const long long flag = ((static_cast<long long>(I.b) * P.H + I.g) * blocks + I.blk) * P.splits + I.split;
       unsigned short *const answer = static_cast<unsigned short *>(P.out) + static_cast<long long>(at) * P.D;
@@ -717,14 +717,9 @@ __global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
         checked = true;
         empty(I.nblk > 0);
       }
-      const bool mine = work && use && (!tree || P.rowinfo[I.b] >= 0);
-      const int p = I.n + (tree ? mine ? P.depth[static_cast<size_t>(I.b) * P.N + my] : 0 : my);
       const int from = window_from(P, p);
       const uint32_t *const anc = tree ? P.anc + (static_cast<size_t>(I.b) * P.N + my) * P.W : nullptr;
       const Keys keys(P, I.p0, I.end);
-      // the warp's own positions
-      const int r_first = I.r0 + (rr & ~31), q_first = min(r_first / P.G, P.N - 1), q_last = min((r_first + 31) / P.G, P.N - 1);
-      const int p0 = tree ? I.p0 : I.n + q_first, p1 = tree ? I.p1 : I.n + q_last;
       float m = -INFINITY, l = 0.f;
       for (int k = 0; work && k < I.nblk; ++k) {
         // Groups of the block that some query of the warp does not see whole: what is
@@ -736,14 +731,12 @@ __global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
           const int gi = I.g0 + k * kBlkGroups + (lane & 7);
           part = __ballot_sync(FULL_MASK, gi >= I.g1 || group_masked(P, keys.token(gi), I.n, p0, p1)) & 0xffu;
         }
-        live = __all_sync(FULL_MASK, wait_on(c, &c->sfull[tile], (nb + k) & 1, limit));
-        if (!live) break;
-        tc_fence_after();
-        if (part || minus) {
+        uint32_t b0 = 0, b1 = 0, b2 = 0, b3 = 0;  // (made while the scores are)
+        if (part) {
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q, part >>= 2) {
+          for (int q = 0; q < 4; ++q) {
             uint32_t bits = 0xffffffffu;
-            if (part & 3u) {
+            if (part >> (2 * q) & 3u) {
               bits = 0;
 #pragma unroll 1
               for (int j = 0; j < 2; ++j) {
@@ -751,12 +744,23 @@ __global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
                 if (gi < I.g1) bits |= group_seen(P, keys.token(gi), p, from, I.n, I.end, anc) << (16 * j);
               }
             }
-            if (__all_sync(FULL_MASK, bits == 0xffffffffu) && !minus) continue;
+            b0 = b1, b1 = b2, b2 = b3, b3 = ~bits;
+          }
+        }
+        live = __all_sync(FULL_MASK, wait_on(c, &c->sfull[tile], (nb + k) & 1, limit));
+        if (!live) break;
+        tc_fence_after();
+        if (part || minus) {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t bits = b0;
+            b0 = b1, b1 = b2, b2 = b3;
+            if (__all_sync(FULL_MASK, bits == 0u) && !minus) continue;
             uint32_t x[32];
             tc_ld32(x, s_addr + q * 32);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = bits >> j & 1 ? minus ? x[j] ^ 0x80000000u : x[j] : 0xff800000u;
+            for (int j = 0; j < 32; ++j) x[j] = bits >> j & 1 ? 0xff800000u : minus ? x[j] ^ 0x80000000u : x[j];
             tc_st32(s_addr + q * 32, x);
           }
           tc_wait_st();
@@ -839,6 +843,26 @@ __global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
         const int item = blockIdx.x + (turn + 1) * gridDim.x;
         next.item = -1;
         if (item < items) next = make_item(P, item, blocks);
+      }
+      {
+        const int r = next.r0 + rr;
+        row.at = -1;
+        row.my = 0;
+        if (r < P.N * P.G) {
+          row.my = r / P.G;
+          row.at = (next.b * P.N + row.my) * P.Hq + next.g * P.G + (r - row.my * P.G);
+        }
+        row.use = next.item >= 0 && row.at >= 0 && row.my < next.cnt;
+        const int q_first = min((r & ~31) / P.G, P.N - 1), q_last = min((r | 31) / P.G, P.N - 1);
+        row.p = next.n + row.my;
+        row.p0 = next.n + q_first;
+        row.p1 = next.n + q_last;
+        if (tree) {  // (a row that cannot be used has no depths: whatever stands there is not used)
+          const int info = row.use ? P.rowinfo[next.b] : -1, d = row.use ? P.depth[static_cast<size_t>(next.b) * P.N + row.my] : 0;
+          row.p = next.n + (info >= 0 ? d : 0);
+          row.p0 = next.p0;
+          row.p1 = next.p1;
+        }
       }
       if (!work) continue;
       nb += I.nblk;
