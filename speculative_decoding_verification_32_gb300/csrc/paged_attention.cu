@@ -5,7 +5,8 @@
 //  paged_check_kernel -- one CTA per row: lengths, the pages that the row needs,
 //    and for draft trees the parents, each node's depth and which of the pass's
 //    tokens it sees.  The attention kernel runs beside it and looks at the
-//    result before it writes anything.
+//    result before it writes anything.  (Chains in parts: a few warps of the rows
+//    kernel do this, and the join looks.)
 //  paged_tile_kernel (paged_attention_tile.cu) -- many query rows.
 //  paged_rows_kernel -- 8 to 32 query rows (the query heads of one KV head and
 //    tokens of one row) against a part of their keys, one warp.
@@ -30,35 +31,43 @@ constexpr int kCheckThreads = 256;
 constexpr int kPaJoinThreads = 128;
 
 // -------------------------------------------------------------- row check
-__global__ void __launch_bounds__(kCheckThreads) paged_check_kernel(const __grid_constant__ PagedParams P, const int32_t *parent,
-                                                                    int32_t *rowinfo, uint32_t *anc, int32_t *depth) {
-  __shared__ int par[SPEC_MAX_TREE_NODES];
-  const int b = blockIdx.x, tid = threadIdx.x;
-  allow_dependents();
-  int n;
-  const int c = paged_queries(P, b, n);
-  bool tree = true, paged = true;
-  const int used = parent ? max(0, min(P.count ? P.count[b] : P.N, P.N)) : 0;
-  for (int i = tid; i < used; i += kCheckThreads) {
-    const int p = parent[static_cast<size_t>(b) * P.N + i];
-    par[i] = p;
-    tree = tree && (i == 0 ? p == -1 : p >= 0 && p < i);
-  }
+// Whether every page that the row's queries see is there: by `threads` threads, of
+// which this is the `t`-th.
+__device__ __forceinline__ bool pages_there(const PagedParams &P, int b, int n, int c, int t, int threads) {
+  bool paged = true;
   if (c > 0) {  // the pages of what the row's first query and later ones see
     const Keys keys(P, n, n + c);
     const int per = P.page / kGroup, row = keys.n;
-    for (int k = tid; k < row; k += kCheckThreads) {
+    for (int k = t; k < row; k += threads) {
       const int g = keys.token(k) / kGroup;
       if (k > 0 && k != keys.sink && g % per) continue;  // the page of the group before
       const int pg = __ldg(P.table + static_cast<size_t>(b) * P.columns + g / per);
       paged = paged && pg >= 0 && pg < P.pages;
     }
   }
+  return paged;
+}
+
+__global__ void __launch_bounds__(kCheckThreads) paged_check_kernel(const __grid_constant__ PagedParams P, const int32_t *parent,
+                                                                    uint32_t *anc, int32_t *depth) {
+  __shared__ int par[SPEC_MAX_TREE_NODES];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  allow_dependents();
+  int n;
+  const int c = paged_queries(P, b, n);
+  bool tree = true;
+  const int used = parent ? max(0, min(P.count ? P.count[b] : P.N, P.N)) : 0;
+  for (int i = tid; i < used; i += kCheckThreads) {
+    const int p = parent[static_cast<size_t>(b) * P.N + i];
+    par[i] = p;
+    tree = tree && (i == 0 ? p == -1 : p >= 0 && p < i);
+  }
+  bool paged = pages_there(P, b, n, c, tid, kCheckThreads);
   tree = __syncthreads_and(tree);
   paged = __syncthreads_and(paged);
   const int code = !tree ? kRowBadParent : !paged || c < 0 ? kRowBadSlot : c;
   if (tid == 0) {
-    rowinfo[b] = code;
+    P.rowinfo[b] = code;
     if (P.row_status) P.row_status[b] = code >= 0 ? 0 : code == kRowBadParent ? SPEC_ROW_BAD_PARENT : SPEC_ROW_BAD_SLOT;
   }
   if (code < 0) return;
@@ -89,15 +98,15 @@ __global__ void __launch_bounds__(kCheckThreads) paged_check_kernel(const __grid
 // that keys fill the matrix instruction's 16 rows and query rows go in eights: 4
 // rows of a decoding token are padded to 8, 24 of a chain not at all.  (With the
 // queries as the 16 rows every item does twice to 4/3 of the work, with the
-// registers of twice the sums: 64 decoding rows of 4 in e4m3 100 us, this way 86; 64
-// chains of 24 rows 132 and 103, in bf16 105 and 101.  It is the better way for
+// registers of twice the sums: 64 decoding rows of 4 in e4m3 100 us, this way 84; 64
+// chains of 24 rows 132 and 103, in bf16 105 and 97.  It is the better way for
 // just 16 rows over codes alone, 60 and 75 us for 32 rows.)
 template <int CT, int DP, int NT>
 struct PagedRowCfg {
   static constexpr bool E4 = CT == SPEC_E4M3;
   static constexpr int kEsz = E4 ? 1 : 2;
   static constexpr int kM = 8 * NT;                         // query rows
-  static constexpr int kStages = 2;                         // (64 decoding rows in e4m3 86 us; with three 89)
+  static constexpr int kStages = 2;                         // (64 decoding rows in e4m3 3 us more with three)
   static constexpr int kPitch = DP * kEsz + 16;             // bytes of one token in a ring slot
   static constexpr int kPlane = kGroup * kPitch;            // K or V of a group
   static constexpr int kScales = E4 ? 2 * kGroup * 4 : 0;   // scale words, K then V
@@ -108,7 +117,7 @@ struct PagedRowCfg {
   static constexpr int kLast = (kStages - 1) * kStage + (kStage > kQ ? kStage : kQ);
   static constexpr int kSmem = kLast > 8 * kOPitch * 4 ? kLast : 8 * kOPitch * 4;
   // Items per SM.  A multiple of four: an SM's registers lie in four parts, and what
-  // does not fit its part waits (64 decoding rows in e4m3: 86 us with 12, 112 with
+  // does not fit its part waits (64 decoding rows in e4m3: 84 us with 12, 112 with
   // 14 of the 144 registers that 14 would leave).
   static constexpr int kWarps = DP <= 64 ? (NT <= 2 ? 16 : 12) : NT == 1 ? 12 : 8;
 };
@@ -201,7 +210,19 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
 
   // --- the item: KV heads first (the heads of a token lie side by side in
   // memory, so the items that run together read whole entries), then parts
-  int b = blockIdx.z, split = blockIdx.y, parts = P.splits;
+  if (static_cast<int>(blockIdx.y) < P.check) {  // (a launch less: 64 decoding rows 86 -> 84 us)
+    const int r = P.budget > 0 ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x == 0 ? blockIdx.z : P.B;
+    if (r >= P.B) return;
+    int n;
+    const int c = paged_queries(P, r, n);
+    const bool fine = __all_sync(FULL_MASK, pages_there(P, r, n, c, lane, 32)) && c >= 0;
+    if (lane == 0) {
+      P.rowinfo[r] = fine ? c : kRowBadSlot;
+      if (P.row_status) P.row_status[r] = fine ? 0 : SPEC_ROW_BAD_SLOT;
+    }
+    return;
+  }
+  int b = blockIdx.z, split = blockIdx.y - P.check, parts = P.splits;
   const int blk = blockIdx.x / static_cast<unsigned>(P.H), g = blockIdx.x - blk * P.H;
   const int blocks = gridDim.x / P.H;
   if (P.budget > 0) {
@@ -647,7 +668,7 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
   cp_async_wait_all();
   allow_dependents();  // the join's blocks may take the places that come free
   grid_dependency_wait();  // the row's check
-  const bool usable = P.rowinfo[b] >= 0;
+  const bool usable = P.check > 0 || P.rowinfo[b] >= 0;  // (else the join leaves the row out)
   odd = __any_sync(FULL_MASK, odd);
   if (P.splits > 1 && lane == 0) P.oflag[flag] = odd;
   // Eight query rows at a time through shared memory, so that a row is written
@@ -778,10 +799,10 @@ template <int CT, int DP, int NT>
 cudaError_t launch_rows(const PagedParams &p, cudaStream_t s) {
   using C = PagedRowCfg<CT, DP, NT>;
   const int blocks = (p.N * p.G + C::kM - 1) / C::kM;
-  const dim3 grid(p.H * blocks, p.budget > 0 ? p.budget : p.splits, p.budget > 0 ? 1 : p.B);
+  const dim3 grid(p.H * blocks, (p.budget > 0 ? p.budget : p.splits) + p.check, p.budget > 0 ? 1 : p.B);
   const cudaError_t e = allow_smem<paged_rows_kernel<CT, DP, NT>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_after(paged_rows_kernel<CT, DP, NT>, grid, 32, C::kSmem, s, true, p);
+  return launch_after(paged_rows_kernel<CT, DP, NT>, grid, 32, C::kSmem, s, p.check == 0, p);
 }
 
 template <int CT, int DP>
@@ -862,12 +883,12 @@ PagedPlan plan_paged(const spec_paged_attention_args *a) {
     }
   } else {
     const long long want = (8LL * kPagedSms * 2 + items - 1) / items;
-    p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + 63) / 64, 32})));
+    p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + kGroup - 1) / kGroup, 32})));
     // A few rows are cut by a budget of parts, all items side by side.
     const long long budget = static_cast<long long>(rows_per_sm(a->cache_dtype, a->head_dim, p.oblk)) * kPagedSms / a->heads;
     if (blocks == 1 && a->B <= kMaxCutRows && budget > a->B) {
       p.budget = static_cast<int>(budget);
-      p.splits = static_cast<int>(std::min<long long>({32, (tokens + 63) / 64, budget - a->B + 1}));
+      p.splits = static_cast<int>(std::min<long long>({32, (tokens + kGroup - 1) / kGroup, budget - a->B + 1}));
     }
   }
   p.W = a->parent ? (a->N + 31) / 32 : 0;
@@ -946,7 +967,7 @@ spec_status spec_paged_attention(const spec_paged_attention_args *a, void *out, 
   p.splits = plan.splits;
   p.budget = plan.splits > 1 ? plan.budget : 0;
   p.nparts = reinterpret_cast<int32_t *>(w + plan.count_at);
-  p.min_groups = 4;
+  p.min_groups = 1;  // (one token under a window of 128: 14.0 us with four, 11.7 so)
   p.oblk = plan.oblk;
   p.ml = reinterpret_cast<float2 *>(w + plan.ml_at);
   p.part = reinterpret_cast<float *>(w + plan.part_at);
@@ -961,9 +982,14 @@ spec_status spec_paged_attention(const spec_paged_attention_args *a, void *out, 
   int32_t *info = reinterpret_cast<int32_t *>(w + plan.info_at);
   uint32_t *anc = reinterpret_cast<uint32_t *>(w + plan.anc_at);
   int32_t *depth = reinterpret_cast<int32_t *>(w + plan.depth_at);
-  paged_check_kernel<<<p.B, kCheckThreads, 0, s>>>(p, a->parent, info, anc, depth);
-  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
   p.rowinfo = info;
+  if (!plan.tile && !a->parent && p.splits > 1) {
+    const int across = p.H * ((p.N * p.G + p.oblk - 1) / p.oblk);  // blocks of a blockIdx.y
+    p.check = p.budget > 0 ? (p.B + across - 1) / across : 1;
+  } else {
+    paged_check_kernel<<<p.B, kCheckThreads, 0, s>>>(p, a->parent, anc, depth);
+    if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  }
   if (a->parent) p.anc = anc, p.depth = depth;
   const int ct = a->cache_dtype;
   cudaError_t e = plan.tile         ? launch_paged_tile(p, ct, s)

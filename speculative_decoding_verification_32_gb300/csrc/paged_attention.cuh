@@ -42,7 +42,8 @@ struct PagedParams {
   // from the check kernel: each row's query count (negative: the row cannot be
   // used), and for trees the words of 32 bits of the pass's tokens that a query
   // sees, and its depth
-  const int32_t *rowinfo;
+  int32_t *rowinfo;
+  int check;                   // > 0: that many of the rows kernel's first blockIdx.y make them (chains in parts)
   const uint32_t *anc;
   const int32_t *depth;
   int W;
