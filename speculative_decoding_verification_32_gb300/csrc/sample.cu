@@ -98,6 +98,7 @@ struct SampleShared {
   u64 warp[2][kSmWarps];            // this CTA's warps, two rounds in turn
   u64 warp2[2][kSmWarps];
   uint32_t tmax[kSmThreads];        // threads' largest keys, of the whole cluster
+  unsigned char pick[kSmWarps][32]; // lanes of a batch with candidates
   uint32_t cnt[kSmSegs];            // candidates of each warp, or of each CTA
   uint32_t over[kSmMaxCluster];     // CTAs with a warp that has too many to list
   uint32_t min_p_key;
@@ -482,30 +483,34 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     const i64 a = top > -INFINITY ? __float2ll_rn(mass * ex2((top - M) * weight.sc) * kSmFix) : 0;
     float c = 0.f;
     int n = 0;
-    // (only batches that hold one are looked at)
+    // Only the vectors of lanes whose batch holds one are looked at, and by all lanes:
+    // 2^width such lanes' first, second, ... vectors side by side, so that the lanes
+    // are in vocabulary order and a batch with up to four is read at once.  (Each lane
+    // looking at its own: three trips to L2 a batch, 256 rows 32 us, so 25.)
     for (int i0 = v0, turn = 0; i0 < v1 && bounded; i0 += 32 * kSmBatch, ++turn) {
       const bool here = i0 + lane < v1 && largest[turn * kSmThreads + tid] >= from;
-      if (!__any_sync(FULL_MASK, here)) continue;
-      u64 hits = 0;  // E bits for each of the batch's vectors
-#pragma unroll
-      for (int j = 0; j < kSmBatch; j += 4) {
-        uint4 q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (here && i0 + (j + i) * 32 + lane < v1) q[i] = vector_at(i0 + (j + i) * 32 + lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (here && i0 + (j + i) * 32 + lane < v1 && vector_max<BF16>(q[i]) >= from) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int e = 0; e < E; ++e) m |= element<BF16>(q[i], e) >= from ? 1u << e : 0u;
-            hits |= static_cast<u64>(m) << ((j + i) * E);
-          }
-      }
+      const unsigned those = __ballot_sync(FULL_MASK, here);
+      if (!those) continue;
+      const int found = __popc(those), width = found <= 4 ? 2 : 32 - __clz(found - 1);
+      if (here) S.pick[warp][__popc(those & ((1u << lane) - 1u))] = static_cast<unsigned char>(lane);
+      __syncwarp();
+      const int r = lane & ((1 << width) - 1), step = 32 >> width;
+      const int col = r < found ? S.pick[warp][r] : 0;
+      __syncwarp();
+      int v = i0 + (lane >> width) * 32 + col;
+      uint4 next = make_uint4(0, 0, 0, 0);
+      if (r < found && v < v1) next = vector_at(v);
 #pragma unroll 1
-      for (int i = 0; i < kSmBatch; ++i) {
-        const int mine = i0 + i * 32 + lane;
-        uint32_t bits = static_cast<uint32_t>(hits >> (i * E)) & ((1u << E) - 1u);
+      for (int j = 0; j < kSmBatch; j += step) {
+        const uint4 q = next;
+        const int mine = v;
+        v += step * 32;
+        if (j + step < kSmBatch && r < found && v < v1) next = vector_at(v);
+        uint32_t bits = 0;
+        if (r < found && mine < v1) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) bits |= element<BF16>(q, e) >= from ? 1u << e : 0u;
+        }
         const unsigned some = __ballot_sync(FULL_MASK, bits != 0);
         if (!some) continue;
         int to, all;  // the lane's first place, and places for the warp
@@ -527,15 +532,12 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
         while (bits) {
           const int e = __ffs(bits) - 1;
           bits &= bits - 1;
-          const int at = mine * E + e;
-          float l;
-          if constexpr (BF16)
-            l = __uint_as_float(static_cast<uint32_t>(KEEP ? reinterpret_cast<const unsigned short *>(data)[at]
-                                                           : __ldg(reinterpret_cast<const unsigned short *>(row) + first + at)) << 16);
-          else
-            l = KEEP ? reinterpret_cast<const float *>(data)[at] : __ldg(reinterpret_cast<const float *>(row) + first + at);
+          const int word = BF16 ? e >> 1 : e;
+          uint32_t x = word & 2 ? (word & 1 ? q.w : q.z) : (word & 1 ? q.y : q.x);
+          if (BF16) x = e & 1 ? x & 0xffff0000u : x << 16;
+          const float l = __uint_as_float(x);
           if (count_near) c += ex2((l - M) * weight.sc);
-          if (n <= seglen) st_cluster_u64(&S.cand[seg * seglen + to++], 0, static_cast<u64>(smp_key(l)) << 32 | static_cast<uint32_t>(first + at));
+          if (n <= seglen) st_cluster_u64(&S.cand[seg * seglen + to++], 0, static_cast<u64>(smp_key(l)) << 32 | static_cast<uint32_t>(first + mine * E + e));
         }
       }
     }
