@@ -12,15 +12,16 @@
 //     cache as [page][token][head][number] (a group on no page lies past the last
 //     one and comes as zeros); one warp looks the pages up, 32 at a time and ahead
 //     of use, and asks for the boxes.  (With copies by 128 threads, 16 bytes at a
-//     time, a prompt of 2 x 4096 tokens under a window of 1024 took 171 us, so 147);
+//     time, a prompt of 2 x 4096 tokens under a window of 1024 took 171 us, so 147;
+//     134 with what follows);
 //   - e4m3 codes are brought into a place of their own, and the producers make bf16
 //     numbers of them, scale and all.  That is exact (4 bits of significand, and
 //     bf16 has fp32's exponents), so scales may lie any distance apart;
 //   - a CTA runs through many items (a prompt has hundreds of them), and the
 //     roles do not meet between them.  One warp works the items out and hands
-//     them on; the producers bring the next queries as soon as a tile's last
-//     scores are made and run on through the pages, and the tensor cores start
-//     on them while the softmax writes the answers.
+//     them on; the producers bring the next queries as soon as there is room, the
+//     softmax sets the next item up while the last product is made, and the tensor
+//     cores start on it while the answers are written.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -62,7 +63,7 @@ struct Layout {
   static constexpr int kQ = 0;
   static constexpr int kK = kQs * kOp;       // two buffers
   static constexpr int kV = kK + 2 * kOp;    // two buffers
-  static constexpr int kStage = kV + 2 * kOp;        // codes: two buffers of a block's keys or values as they are
+  static constexpr int kStage = kV + 2 * kOp;        // codes: a block's keys and values as they are
   static constexpr int kCtrl = 7 * kOp;
   static constexpr int kSmem = kCtrl + 1024;
 };
@@ -82,7 +83,7 @@ struct TileItem {
 };
 
 constexpr int kItemSlots = 4;
-constexpr int kOddSlots = 8;  // nobody is more than kItemSlots items ahead of another
+constexpr int kOddSlots = 8;  // nobody is more than kItemSlots + 1 items ahead of another
 struct TileCtrl {
   uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
   uint64_t land[2], lfree[2];  // 16-bit values as they have come in (two places); codes of keys and of values
@@ -534,7 +535,6 @@ __global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
         if (item < 0) break;
         if (nblk == 0) continue;
         if (t < tiles) {
-          const bool both = tiles == 1;  // an item of one tile speaks for the other, too
           const int place = (nq + t) % C::kQs;
           wait(&c->qfull[place], ((nq + t) / C::kQs) & 1);
           // block k's weights times values, then block k + 1's scores in their place
@@ -562,7 +562,6 @@ __global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
 #pragma unroll
                 for (int j = kBlk / 32; j < kBlk / 16; ++j) tc_mma_ts(tm + 256, tm + j * 8, bb + (j * 2048 >> 4), wv, true);
                 tc_commit(&c->vfree[at & 1]);
-                if (both) tc_commit(&c->vfree[at & 1]);
                 if (k + 1 == nblk) tc_commit(&c->done[t]);
               }
               if (k + 1 == nblk) break;
@@ -579,12 +578,21 @@ __global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
               }
               tc_commit(&c->sfull[t]);
               tc_commit(&c->kfree[(at + 1) & 1]);
-              if (both) tc_commit(&c->kfree[(at + 1) & 1]);
               if (k + 2 == nblk) tc_commit(&c->qfree[place]);  // the tile's last
             }
           }
           ++ni;
           nb += nblk;
+        } else {
+          // The tile's warp goes through the blocks all the same: neither warp may be
+          // two of a buffer's turns ahead, where one turn looks like the other.
+          for (int k = 0; k < nblk && live; ++k) {
+            const int at = kb + k;
+            wait(&c->kfull[at & 1], (at >> 1) & 1);
+            if (live && lane == 0) mbar_arrive(&c->kfree[at & 1]);
+            wait(&c->vfull[at & 1], (at >> 1) & 1);
+            if (live && lane == 0) mbar_arrive(&c->vfree[at & 1]);
+          }
         }
         kb += nblk;
         nq += tiles;

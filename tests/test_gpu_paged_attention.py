@@ -145,6 +145,27 @@ def test_prompts(sv, kind, qt, N, Hq, H, D, lens, page, window, sinks):
     Problem(sv, 2, N, Hq, H, D, lens, page, window, sinks, kind, qt).check()
 
 
+@pytest.mark.parametrize("kind", ["bfloat16", "float16", "uint8"])
+@pytest.mark.parametrize("B,N,Hq,H,D,window,sinks", [(48, 130, 8, 4, 64, 0, 0), (80, 40, 32, 8, 128, 200, 4), (60, 65, 8, 4, 80, 30, 20)])
+def test_uneven_items(sv, B, N, Hq, H, D, window, sinks, kind):
+    """Items of one row tile and of two take turns on an SM, with one block of keys and with several."""
+    p = Problem(sv, B, N, Hq, H, D, [(97 * b * b) % (20 if b % 3 else 700) for b in range(B)], 16, window, sinks, kind,
+                "float16" if kind == "float16" else "bfloat16")
+    out, lse, _ = p.check(rows=range(0, B, 7))
+    for _ in range(5):
+        again = p.run()
+        assert (again[0] == out).all() and (again[1] == lse).all()
+    # a row by itself, whose keys may be cut in another way
+    for b in range(3, B, 11):
+        q = Problem.__new__(Problem)
+        q.__dict__.update(p.__dict__)
+        q.B, q.q, q.dt, q.lens, q.c = 1, p.q[b:b + 1], p.dt[b:b + 1], p.lens[b:b + 1], p.c[b:b + 1]
+        o, z, _ = q.run()
+        n = int(p.lens[b]) + N
+        check_row(o[0].cpu().double().numpy(), z[0].cpu().double().numpy(), p.qx[b], p.kx[b, :n], p.vx[b, :n], p.see[b], D**-0.5,
+                  "bfloat16" if kind == "uint8" else kind, p.out_u)
+
+
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("kind", ["bfloat16", "uint8"])
 def test_many_items(sv, kind, tree):
