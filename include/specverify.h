@@ -702,7 +702,8 @@ spec_status spec_token_logprobs(const spec_logprobs_args *args, const spec_logpr
  * block_table, free_pages and free_state are read and written; other arrays must
  * not overlap them.  0 <= N, 1 <= columns, columns * page_size < 2^31,
  * num_pages * page_size < 2^31, B * N < 2^31, B * columns < 2^31, B <= 2^20,
- * 0 <= window, 0 <= sinks (sinks without a window have no effect).  Two launches.
+ * 0 <= window, 0 <= sinks (sinks without a window have no effect).  One launch for up
+ * to 256 rows with N <= 256, else two.
  * Workspace: spec_page_plan_workspace_size(B) bytes.
  */
 typedef struct {

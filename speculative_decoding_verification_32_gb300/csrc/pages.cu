@@ -2,14 +2,16 @@
 // free pages and slot maps (spec_page_plan), and the gather of an accepted tree
 // path's entries across pages (spec_kv_compact_pages).
 //
-// The plan is two launches.  The first reads the table and counts, per row, how
-// many pages it wants and gives back; the second adds up the rows before its
-// own, moves pages between table and ring, and writes the slots.  What is taken
+// The plan first reads the table and counts, per row, how many pages it wants and
+// gives back; then it adds up the rows before each, moves pages between table and
+// ring, and writes the slots.  Up to 256 rows that is one launch, else two.  What is taken
 // (from the ring's head on) and what is given back (behind its tail) cannot
 // overlap, since taken, free and given pages are at most the whole pool, so
 // rows need not wait for one another.
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "attention.cuh"
 #include "common.cuh"
@@ -24,6 +26,9 @@ constexpr int kPlWarps = kPlThreads / 32;  // rows per CTA
 constexpr int kPlChunk = 8;                // places of a lane looked at together
 // More slots per row than this are written by a whole CTA per row.
 constexpr int kPlWide = 256;
+// Up to so many rows are dealt with in one launch.
+constexpr int kPlSmallThreads = 1024, kPlSmallCtas = 8;
+constexpr int kPlSmallRows = kPlSmallCtas * kPlSmallThreads / 32;
 
 struct PlanParams {
   int32_t *table, *free_pages, *free_state;
@@ -55,44 +60,55 @@ __device__ __forceinline__ bool row_live(const PlanParams &P, int b, int &n, int
   return true;
 }
 
+// The ring's head and free pages (negative: not a ring's).
+__device__ __forceinline__ int2 ring_state(const PlanParams &P) {
+  const int head = P.free_state[0], have = P.free_state[1];
+  const bool ok = head >= 0 && head < max(1, P.pages) && have >= 0 && have <= P.pages;
+  return make_int2(head, ok ? have : -1);
+}
+
+// Pages that a row wants and gives back, by a warp; x < 0: it cannot be used.
+__device__ __forceinline__ int2 count_row(const PlanParams &P, int b, int lane) {
+  int n, c;
+  Live live;
+  if (!row_live(P, b, n, c, live)) return make_int2(-1, 0);
+  bool ok = true;
+  int2 want = make_int2(0, 0);
+  const int32_t *const row = P.table + static_cast<size_t>(b) * P.columns;
+  for (int j0 = lane; j0 < P.columns; j0 += 32 * kPlChunk) {
+    int e[kPlChunk];
+#pragma unroll
+    for (int i = 0; i < kPlChunk; ++i) e[i] = j0 + i * 32 < P.columns ? row[j0 + i * 32] : -1;
+#pragma unroll
+    for (int i = 0; i < kPlChunk; ++i) {
+      const int j = j0 + i * 32;
+      ok = ok && e[i] < P.pages;
+      if (j < P.columns) {
+        const bool l = live(j);
+        want.x += l && e[i] < 0;
+        want.y += !l && e[i] >= 0;
+      }
+    }
+  }
+  want.x = __reduce_add_sync(FULL_MASK, want.x);
+  want.y = __reduce_add_sync(FULL_MASK, want.y);
+  return __all_sync(FULL_MASK, ok) ? want : make_int2(-1, 0);
+}
+
 __global__ void __launch_bounds__(kPlThreads) plan_count_kernel(const __grid_constant__ PlanParams P) {
   __shared__ int2 part[kPlWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, b = blockIdx.x * kPlWarps + warp;
   allow_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    const int head = P.free_state[0], have = P.free_state[1];
-    const bool ok = head >= 0 && head < max(1, P.pages) && have >= 0 && have <= P.pages;
-    P.state[0] = head;
-    P.state[1] = ok ? have : -1;
+    const int2 ring = ring_state(P);
+    P.state[0] = ring.x;
+    P.state[1] = ring.y;
   }
   int2 want = make_int2(0, 0);
   if (b < P.B) {
-    int n, c;
-    Live live;
-    bool ok = row_live(P, b, n, c, live);
-    if (ok) {
-      const int32_t *const row = P.table + static_cast<size_t>(b) * P.columns;
-      for (int j0 = lane; j0 < P.columns; j0 += 32 * kPlChunk) {
-        int e[kPlChunk];
-#pragma unroll
-        for (int i = 0; i < kPlChunk; ++i) e[i] = j0 + i * 32 < P.columns ? row[j0 + i * 32] : -1;
-#pragma unroll
-        for (int i = 0; i < kPlChunk; ++i) {
-          const int j = j0 + i * 32;
-          ok = ok && e[i] < P.pages;
-          if (j < P.columns) {
-            const bool l = live(j);
-            want.x += l && e[i] < 0;
-            want.y += !l && e[i] >= 0;
-          }
-        }
-      }
-      want.x = __reduce_add_sync(FULL_MASK, want.x);
-      want.y = __reduce_add_sync(FULL_MASK, want.y);
-      ok = __all_sync(FULL_MASK, ok);
-    }
-    if (lane == 0) P.want[b] = ok ? want : make_int2(-1, 0);
-    if (!ok) want = make_int2(0, 0);
+    want = count_row(P, b, lane);
+    if (lane == 0) P.want[b] = want;
+    if (want.x < 0) want = make_int2(0, 0);
   }
   if (lane == 0) part[warp] = want;
   __syncthreads();
@@ -101,6 +117,116 @@ __global__ void __launch_bounds__(kPlThreads) plan_count_kernel(const __grid_con
 #pragma unroll
     for (int w = 0; w < kPlWarps; ++w) s.x += part[w].x, s.y += part[w].y;
     P.sums[blockIdx.x] = s;
+  }
+}
+
+// A warp moves a row's pages, behind what the rows before it take and give back;
+// true: the ring was broken.
+__device__ __forceinline__ bool move_pages(const PlanParams &P, int32_t *row, const Live &live, int head, int have, int2 before, bool served, int lane) {
+  bool broken = false;
+  int take = before.x, give = before.y;
+  for (int j0 = 0; j0 < P.columns; j0 += 32) {
+    const int j = j0 + lane;
+    const int e = j < P.columns ? row[j] : -1;
+    const bool l = live(j);
+    const bool t = j < P.columns && l && e < 0 && served, g = j < P.columns && !l && e >= 0;
+    const unsigned ts = __ballot_sync(FULL_MASK, t), gs = __ballot_sync(FULL_MASK, g), below = (1u << lane) - 1u;
+    if (t) {
+      const long long at = static_cast<long long>(head) + take + __popc(ts & below);
+      const int page = P.free_pages[at % P.pages];
+      const bool ok = page >= 0 && page < P.pages;
+      if (ok) row[j] = page;
+      broken = broken || !ok;
+    }
+    if (g) {
+      const int rank = give + __popc(gs & below);
+      if (rank < P.pages - have)
+        P.free_pages[(static_cast<long long>(head) + have + rank) % P.pages] = e;
+      else
+        broken = true;
+      row[j] = -1;
+    }
+    take += __popc(ts);
+    give += __popc(gs);
+  }
+  return broken;
+}
+// The slots of a row's tokens i0, i0 + step, ...
+__device__ __forceinline__ void write_slots(const PlanParams &P, int b, const int32_t *row, int n, int c, bool served, int i0, int step) {
+  for (int i = i0; i < P.N; i += step) {
+    int slot = -1;
+    if (served && i < c) {
+      const int t = n + i, j = t / P.page, e = row[j];
+      if (e >= 0) slot = e * P.page + (t - j * P.page);
+    }
+    P.slot_map[static_cast<size_t>(b) * P.N + i] = slot;
+  }
+}
+
+// Up to 256 rows in one launch: a cluster of CTAs with a warp per row, which tell
+// one another what their rows want.  Bound by the host, which needs 15 us a call, 20
+// with two launches; on the GPU 64 rows of 512 places take 5.0 us and 5.3, 128 of 2048
+// 8.6 and 8.5, 200 of 512 6.7 and 5.6, 256 of 2048 11.3 and 8.5 (eight SMs' worth).
+__global__ void __launch_bounds__(kPlSmallThreads) plan_small_kernel(const __grid_constant__ PlanParams P) {
+  __shared__ int2 want[kPlSmallRows];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, b = blockIdx.x * (blockDim.x / 32) + warp;
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const int2 ring = ring_state(P);
+  const int head = ring.x, have = ring.y;
+  int2 w = make_int2(0, 0);
+  if (b < P.B) w = count_row(P, b, lane);
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the others are running
+  if (b < P.B) {
+    if (lane < static_cast<int>(cluster_nctarank()))
+      asm volatile("st.shared::cluster.v2.s32 [%0], {%1, %2};" ::"r"(dsmem_addr(&want[b], lane)), "r"(w.x), "r"(w.y) : "memory");
+  }
+  __syncwarp();
+  cluster_sync();  // (also: everyone has read the ring)
+  if (b < P.B) {
+    int2 before = make_int2(0, 0);
+    for (int i = lane; i < b; i += 32) {
+      const int2 w = want[i];
+      if (w.x >= 0) before.x += w.x, before.y += w.y;
+    }
+    before.x = __reduce_add_sync(FULL_MASK, before.x);
+    before.y = __reduce_add_sync(FULL_MASK, before.y);
+    const int2 mine = want[b];
+    const bool usable = mine.x >= 0 && have >= 0, served = usable && (mine.x == 0 || before.x + mine.x <= have);
+    int n = 0, c = 0;
+    Live live = {};
+    row_live(P, b, n, c, live);
+    int32_t *const row = P.table + static_cast<size_t>(b) * P.columns;
+    bool broken = false;
+    if (usable && (mine.x > 0 || mine.y > 0)) broken = move_pages(P, row, live, head, have, before, served, lane);
+    broken = __any_sync(FULL_MASK, broken);
+    __syncwarp();
+    if (lane == 0 && P.row_status) P.row_status[b] = !usable || broken ? SPEC_ROW_BAD_SLOT : !served ? SPEC_ROW_NO_PAGES : 0;
+    write_slots(P, b, row, n, c, served, lane, 32);
+  }
+  // the ring after the call: what the rows up to the first that got nothing took
+  if (blockIdx.x == 0 && warp == 0 && have >= 0 && P.pages > 0) {
+    int taken = 0, given = 0;
+    bool over = false;
+    for (int i0 = 0; i0 < P.B; i0 += 32) {
+      const int2 w = i0 + lane < P.B ? want[i0 + lane] : make_int2(0, 0);
+      given += __reduce_add_sync(FULL_MASK, w.x >= 0 ? w.y : 0);
+      int x = max(w.x, 0);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(FULL_MASK, x, o);
+        if (lane >= o) x += y;
+      }
+      if (over) continue;
+      const unsigned beyond = __ballot_sync(FULL_MASK, taken + x > have);
+      over = beyond != 0;
+      const int k = over ? __ffs(beyond) - 2 : 31;  // the last that was served
+      if (k >= 0) taken += __shfl_sync(FULL_MASK, x, k);
+    }
+    if (lane == 0) {
+      P.free_state[0] = static_cast<int>((static_cast<long long>(head) + taken) % P.pages);
+      P.free_state[1] = have - taken + min(given, P.pages - have);
+    }
   }
 }
 
@@ -148,33 +274,7 @@ __global__ void __launch_bounds__(kPlThreads) plan_apply_kernel(const __grid_con
   Live live = {};
   if (b < P.B) row_live(P, b, n, c, live);
   int32_t *const row = P.table + static_cast<size_t>(b) * P.columns;
-  if (usable && (mine.x > 0 || mine.y > 0) && (!WIDE || warp == 0)) {
-    int take = before.x, give = before.y;
-    for (int j0 = 0; j0 < P.columns; j0 += 32) {
-      const int j = j0 + lane;
-      const int e = j < P.columns ? row[j] : -1;
-      const bool l = live(j);
-      const bool t = j < P.columns && l && e < 0 && served, g = j < P.columns && !l && e >= 0;
-      const unsigned ts = __ballot_sync(FULL_MASK, t), gs = __ballot_sync(FULL_MASK, g), below = (1u << lane) - 1u;
-      if (t) {
-        const long long at = static_cast<long long>(head) + take + __popc(ts & below);
-        const int page = P.free_pages[at % P.pages];
-        const bool ok = page >= 0 && page < P.pages;
-        if (ok) row[j] = page;
-        broken = broken || !ok;
-      }
-      if (g) {
-        const int rank = give + __popc(gs & below);
-        if (rank < P.pages - have)
-          P.free_pages[(static_cast<long long>(head) + have + rank) % P.pages] = e;
-        else
-          broken = true;
-        row[j] = -1;
-      }
-      take += __popc(ts);
-      give += __popc(gs);
-    }
-  }
+  if (usable && (mine.x > 0 || mine.y > 0) && (!WIDE || warp == 0)) broken = move_pages(P, row, live, head, have, before, served, lane);
   if (WIDE) {
     broken = __syncthreads_or(broken);  // also: the table's changes are seen by the whole CTA
   } else {
@@ -185,14 +285,7 @@ __global__ void __launch_bounds__(kPlThreads) plan_apply_kernel(const __grid_con
     const bool lead = WIDE ? tid == 0 : lane == 0;
     if (lead && P.row_status)
       P.row_status[b] = !usable || broken ? SPEC_ROW_BAD_SLOT : !served ? SPEC_ROW_NO_PAGES : 0;
-    for (int i = WIDE ? tid : lane; i < P.N; i += WIDE ? kPlThreads : 32) {
-      int slot = -1;
-      if (served && i < c) {
-        const int t = n + i, j = t / P.page, e = row[j];
-        if (e >= 0) slot = e * P.page + (t - j * P.page);
-      }
-      P.slot_map[static_cast<size_t>(b) * P.N + i] = slot;
-    }
+    write_slots(P, b, row, n, c, served, WIDE ? tid : lane, WIDE ? kPlThreads : 32);
   }
   // --- the ring after the call, by the CTA of the last row: all that was wanted,
   // or where that is too much what the rows up to the first that got nothing took
@@ -364,6 +457,19 @@ spec_status spec_page_plan(const spec_page_plan_args *a, int32_t *slot_map, int3
   p.window = a->window;
   p.sinks = a->sinks;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->B <= kPlSmallRows && a->N <= kPlWide) {
+    const int ctas = std::min(a->B, kPlSmallCtas), rows = (a->B + ctas - 1) / ctas;  // spread over as many SMs as go
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(32 * rows);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, plan_small_kernel, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  }
   const int groups = groups_of(a->B);
   plan_count_kernel<<<groups, kPlThreads, 0, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;

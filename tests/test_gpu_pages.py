@@ -149,11 +149,27 @@ def test_bad_rows(sv):
     assert status.tolist() == [8, 0, 8, 8, 8, 0, 0, 8]
 
 
+@pytest.mark.parametrize("N", [3, 300])
+def test_bad_rows_among_many(sv, N):
+    """The same where the rows are too many for one launch, or their slots."""
+    B = 300
+    table = np.full((B, 20), -1, np.int32)
+    table[250] = [2000] + 19 * [-1]
+    table[270, 3] = 1
+    free, ring = np.roll(np.arange(2, 1202, dtype=np.int32), 7), np.array([7, 1190], np.int32)
+    kv_len, count = np.arange(B) % 19, np.arange(B) % (N + 1)
+    kv_len[5], count[9], kv_len[10] = -1, N + 1, 20 * 16
+    count[10] = 1
+    _, status = agree(sv, table, free, ring, kv_len, count, N, 16)
+    assert [b for b in range(B) if status[b] == 8] == [5, 9, 10, 250]
+
+
+@pytest.mark.parametrize("B", [3, 300])
 @pytest.mark.parametrize("ring", [(-1, 3), (10, 3), (0, -1), (0, 11)])
-def test_bad_ring(sv, ring):
-    table = np.full((3, 4), -1, np.int32)
-    _, status = agree(sv, table, np.arange(10, dtype=np.int32), np.array(ring, np.int32), np.full(3, 5), None, 3, 16)
-    assert status.tolist() == [8, 8, 8]
+def test_bad_ring(sv, ring, B):
+    table = np.full((B, 4), -1, np.int32)
+    _, status = agree(sv, table, np.arange(10, dtype=np.int32), np.array(ring, np.int32), np.full(B, 5), None, 3, 16)
+    assert status.tolist() == [8] * B
 
 
 def test_broken_ring(sv):
