@@ -764,11 +764,8 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   i64 w[kSmPer];
   bool low[kSmPer];  // out by min-p
 #pragma unroll
-  for (int i = 0; i < kSmPer; ++i) {
-    low[i] = false;
-    key[i] = 0;
-    id[i] = -1;
-    w[i] = 0;
+  for (int i = 0; i < kSmPer; ++i) low[i] = false, key[i] = 0, id[i] = -1, w[i] = 0;
+  auto take = [&](int i) {
     const int at = tid * each + i;
     if (i < each && at < total) {
       int seg = 0;  // the last segment that starts at or before `at`
@@ -788,6 +785,11 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
         low[i] = out;
       }
     }
+  };
+  take(0);
+  if (each > 1) {  // (passed by at once: what is skipped piece by piece is fetched all the same)
+#pragma unroll
+    for (int i = 1; i < kSmPer; ++i) take(i);
   }
   uint32_t floor = floor_key;
   if (total <= kSmPairs) {
@@ -797,6 +799,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     i64 above = 0;
     int larger = 0;
     if (tid < total)
+#pragma unroll 4
       for (int j = 0; j < total; ++j) {
         const bool gt = S.tmax[j] > key[0];
         larger += gt;
@@ -875,14 +878,17 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     all += x;
   }
   const i64 target = fraction_of(u, all, false);
+  int token = -1;
+  i64 its = 0;
 #pragma unroll
   for (int i = 0; i < kSmPer; ++i) {
-    if (run <= target && run + w[i] > target) {
-      P.token[b] = id[i];
-      if (P.prob) P.prob[b] = static_cast<float>(w[i]) / static_cast<float>(all);
-      P.row_status[b] = 0;
-    }
+    if (run <= target && run + w[i] > target) token = id[i], its = w[i];
     run += w[i];
+  }
+  if (token >= 0) {
+    P.token[b] = token;
+    if (P.prob) P.prob[b] = static_cast<float>(its) / static_cast<float>(all);
+    P.row_status[b] = 0;
   }
 }
 
