@@ -112,9 +112,14 @@ struct PagedRowCfg {
   static constexpr int kScales = E4 ? 2 * kGroup * 4 : 0;   // scale words, K then V
   static constexpr int kStage = 2 * kPlane + kScales;
   static constexpr int kQPitch = DP * 2 + 16;
-  static constexpr int kQ = kM * kQPitch + kM * 4;          // queries and factors, in the last slot before it is used
+  static constexpr int kQ = kM * kQPitch + kM * 4;          // queries and factors, in the last slot before it is used, or by themselves
   static constexpr int kOPitch = DP + 4;                    // floats: eight rows of sums at the end
-  static constexpr int kLast = (kStages - 1) * kStage + (kStage > kQ ? kStage : kQ);
+  // 32 rows' queries stay in shared memory, behind the ring: their fragments and sums
+  // together do not fit in registers (64 chains of 8 over codes 174 us, so 133; bf16
+  // 116 and 109.  24 rows' fit: no difference).
+  static constexpr bool kHeld = NT <= 3;
+  static constexpr int kQAt = (kHeld ? kStages - 1 : kStages) * kStage;
+  static constexpr int kLast = kHeld && kStage > kQ ? kStages * kStage : kQAt + kQ;
   static constexpr int kSmem = kLast > 8 * kOPitch * 4 ? kLast : 8 * kOPitch * 4;
   // Items per SM.  A multiple of four: an SM's registers lie in four parts, and what
   // does not fit its part waits (64 decoding rows in e4m3: 84 us with 12, 112 with
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
   constexpr bool BF = CT == SPEC_BF16;
   constexpr int kSteps = DP / 16;  // steps of the scores' contraction, tiles of the sums' rows
   extern __shared__ __align__(16) unsigned char smem[];
-  unsigned char *const qsm = smem + (C::kStages - 1) * C::kStage;
+  unsigned char *const qsm = smem + C::kQAt;
   float *const qfac = reinterpret_cast<float *>(qsm + C::kM * C::kQPitch);
   const int lane = threadIdx.x, quad = lane / 4, j4 = lane % 4;
 
@@ -376,9 +381,9 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
   // Fragments.  The contraction over d may run in any order as long as Q and
   // K agree: for codes a thread takes DP/4 consecutive d (a few 16-byte
   // reads), for 16-bit entries the order ldmatrix gives.
-  uint32_t qf[NT][kSteps][2];
+  uint32_t qf[C::kHeld ? NT : 1][kSteps][2];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int t = 0; t < (C::kHeld ? NT : 0); ++t)
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int d0 = E4 ? j4 * (DP / 4) + s * 4 : s * 16 + j4 * 2, d1 = E4 ? d0 + 2 : d0 + 8;
@@ -400,7 +405,20 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
       qpos[t][c] = __shfl_sync(FULL_MASK, my_pos, rr);
     }
   scaled = E4 && __any_sync(FULL_MASK, scaled);
-  if (P.D < DP) {  // the slot's padding columns were queries
+  auto fragment = [&](int t, int s, uint32_t (&f)[2]) {
+    if constexpr (C::kHeld) {
+      f[0] = qf[t][s][0], f[1] = qf[t][s][1];
+    } else {
+      const uint32_t at = smem_u32(qsm) + (t * 8 + quad) * C::kQPitch + (E4 ? j4 * (DP / 4) + s * 4 : s * 16 + j4 * 2) * 2;
+      if constexpr (E4) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(f[0]), "=r"(f[1]) : "r"(at) : "memory");
+      } else {
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(f[0]) : "r"(at) : "memory");
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(f[1]) : "r"(at + 16) : "memory");
+      }
+    }
+  };
+  if (C::kHeld && P.D < DP) {  // the slot's padding columns were queries
     __syncwarp();
     for (int i = lane; i < C::kStage / 16; i += 32) *reinterpret_cast<uint4 *>(qsm + i * 16) = make_uint4(0, 0, 0, 0);
   }
@@ -500,7 +518,11 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
         for (int s = 0; s < 4; ++s) {
           const uint32_t kf[4] = {e4m3x2_to_f16x2(w[0][s]), e4m3x2_to_f16x2(w[1][s]), e4m3x2_to_f16x2_hi(w[0][s]), e4m3x2_to_f16x2_hi(w[1][s])};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816<false>(s & 1 ? x2[t] : x[t], kf, qf[t][s0 + s][0], qf[t][s0 + s][1]);
+          for (int t = 0; t < NT; ++t) {
+            uint32_t f[2];
+            fragment(t, s0 + s, f);
+            mma16816<false>(s & 1 ? x2[t] : x[t], kf, f[0], f[1]);
+          }
         }
       }
     } else {
@@ -511,7 +533,11 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
         uint32_t kf[4];
         ldmatrix_x4(kf, at + s * 32);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816<BF>(s & 1 ? x2[t] : x[t], kf, qf[t][s][0], qf[t][s][1]);
+        for (int t = 0; t < NT; ++t) {
+          uint32_t f[2];
+          fragment(t, s, f);
+          mma16816<BF>(s & 1 ? x2[t] : x[t], kf, f[0], f[1]);
+        }
       }
     }
     // the values' loads, ahead of what their weights take
