@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kCheckThreads) paged_check_kernel(const __grid
 // queries as the 16 rows every item does twice to 4/3 of the work, with the
 // registers of twice the sums: 64 decoding rows of 4 in e4m3 100 us, this way 84; 64
 // chains of 24 rows 132 and 103, in bf16 105 and 97.  It is the better way for
-// just 16 rows over codes alone, 60 and 75 us for 32 rows.)
+// just 16 rows over codes alone, 60 and 68 us for 32 rows.)
 template <int CT, int DP, int NT>
 struct PagedRowCfg {
   static constexpr bool E4 = CT == SPEC_E4M3;
@@ -114,17 +114,19 @@ struct PagedRowCfg {
   static constexpr int kQPitch = DP * 2 + 16;
   static constexpr int kQ = kM * kQPitch + kM * 4;          // queries and factors, in the last slot before it is used, or by themselves
   static constexpr int kOPitch = DP + 4;                    // floats: eight rows of sums at the end
-  // 32 rows' queries stay in shared memory, behind the ring: their fragments and sums
-  // together do not fit in registers (64 chains of 8 over codes 174 us, so 133; bf16
-  // 116 and 109.  24 rows' fit: no difference).
-  static constexpr bool kHeld = NT <= 3;
+  // 32 rows' queries stay in shared memory, behind the ring, and are not held in
+  // registers: these do not take their fragments beside the sums (64 chains of 8 over
+  // codes 174 us, so 133; bf16 116 and 109; 24 rows' fit: no difference).  16 rows' over
+  // codes make room for 12 items (32 decoding rows of 16 73 us, so 68; 24 rows' sums
+  // would spill then: 107 and 145).
+  static constexpr bool kHeld = E4 ? NT % 2 == 1 : NT <= 3;
   static constexpr int kQAt = (kHeld ? kStages - 1 : kStages) * kStage;
   static constexpr int kLast = kHeld && kStage > kQ ? kStages * kStage : kQAt + kQ;
   static constexpr int kSmem = kLast > 8 * kOPitch * 4 ? kLast : 8 * kOPitch * 4;
   // Items per SM.  A multiple of four: an SM's registers lie in four parts, and what
   // does not fit its part waits (64 decoding rows in e4m3: 84 us with 12, 112 with
   // 14 of the 144 registers that 14 would leave).
-  static constexpr int kWarps = DP <= 64 ? (NT <= 2 ? 16 : 12) : NT == 1 ? 12 : 8;
+  static constexpr int kWarps = DP <= 64 ? (NT <= 2 ? 16 : 12) : NT == 1 || (E4 && NT == 2) ? 12 : 8;
 };
 
 // The 8 x 8 matrix of 16-bit numbers whose rows the lanes' quads hold, transposed.
@@ -849,7 +851,7 @@ int rows_per_sm(int ct, int D, int oblk) {
   auto of = [&](auto c) {
     constexpr int CT = decltype(c)::value;
     if (D <= 64) return oblk <= 16 ? PagedRowCfg<CT, 64, 1>::kWarps : PagedRowCfg<CT, 64, 4>::kWarps;
-    return oblk == 8 ? PagedRowCfg<CT, 128, 1>::kWarps : PagedRowCfg<CT, 128, 2>::kWarps;
+    return oblk == 8 ? PagedRowCfg<CT, 128, 1>::kWarps : oblk == 16 ? PagedRowCfg<CT, 128, 2>::kWarps : PagedRowCfg<CT, 128, 4>::kWarps;
   };
   return ct == SPEC_E4M3 ? of(std::integral_constant<int, SPEC_E4M3>()) : of(std::integral_constant<int, SPEC_BF16>());
 }
