@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
           const bool large = __any_sync(FULL_MASK, sc0 > kTopScale);
           const int ch = (pc % 4) * 2, up = pc / 4;
           uint32_t nans = 0;
-#pragma unroll 4
+#pragma unroll 2
           for (int i = 0; i < kPer; ++i) {
             const int row = row0 + i * kStep;
             uint4 w = *reinterpret_cast<const uint4 *>(codes + i * kPut);
