@@ -398,6 +398,33 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       part = k;
       if (before + x > target) break;
     }
+    if (part < 0) {
+      // the threads' sums weigh something, but no vector of theirs does by itself: the first
+      // token with a weight at all
+      if (warp != 0) return;
+      for (int v = lo; v < hi; v += 32) {
+        const int mine = v + lane;
+        int e = E;
+        float y = 0.f;
+        if (mine < hi) {
+          const uint4 q = vector_at(mine);
+#pragma unroll
+          for (int i = E - 1; i >= 0; --i) {
+            const float l = element<BF16>(q, i), z = l >= floor ? weight(l) : 0.f;
+            if (z > 0.f) e = i, y = z;
+          }
+        }
+        const unsigned some = __ballot_sync(FULL_MASK, e < E);
+        if (!some) continue;
+        if (lane == __ffs(some) - 1) {
+          P.token[b] = first + mine * E + e;
+          if (P.prob) P.prob[b] = y * kSmFix / static_cast<float>(Z);
+          P.row_status[b] = 0;
+        }
+        break;
+      }
+      return;
+    }
     if (part != warp) return;
     // (what is added up again may round to a little less than that warp's sum, which
     // was made against the threads' own maxima: the last kept token, then)
