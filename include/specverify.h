@@ -845,11 +845,12 @@ spec_status spec_paged_attention(const spec_paged_attention_args *args, void *ou
  * logits [B, V], rows row_stride elements apart (>= V), SPEC_BF16 or SPEC_F32.
  * row_status [B]: NONFINITE (a NaN or +inf logit), BAD_UNIFORM, EMPTY (no finite
  * logit), BAD_TEMPERATURE; a flagged row's token is -1 and its prob NaN.
- * Weights are fp32: the exponent -y of a weight 2^-y is rounded (which makes up to
- * about y 2^-23 of it) and the power is the hardware's (2^-22); sums are exact
- * integers of 2^-44, the same in any order.  So a draw within about 2e-6 of a
- * boundary of the law (E[y], at most log2 V, times 2^-23), or a top_p within that of a
- * group's mass, may fall to either side.  One launch, no workspace; B < 2^25.
+ * The token is this law's, whatever batch the row is in: weights are fp32 where
+ * their errors cannot change it, and good to 2^-36 of themselves where they could, so
+ * that only a u within 2^-35 of a boundary of the law, or a top_p within that of a
+ * group's mass, may fall to either side.  (Weights of 2^-126 of the largest and less
+ * count as none.)  prob is off by 2^-17 of itself at most.  One launch, no
+ * workspace; B < 2^25.
  */
 typedef struct {
   int32_t B, V;

@@ -11,8 +11,7 @@
 //
 // One cluster of CTAs per row.  The pass over memory finds the threads' largest
 // logits and their masses against these; a slice stays in shared memory or is read
-// again from L2.  Sums over threads are integers (w 2^44, at most 2^18 of them):
-// they do not depend on the order in which they are made.  The floors are found among few candidates: a bound
+// again from L2.  The floors are found among few candidates: a bound
 // below the floor that is cheap (the k-th largest of the threads' own maxima;
 // for top-p some octaves below the largest weight) leaves not many more logits
 // than the law keeps.  A second pass sends these to the first CTA, in vocabulary
@@ -21,6 +20,15 @@
 // not hold enough mass or too many logits, a histogram of the weights by their
 // leading bits gives a nearer bound; and where more are left than the first CTA
 // can list, all CTAs search together.
+//
+// The token is the definition's.  Sums are made of fp32 weights and rounded to
+// integers (w 2^44), and every decision that hangs on one (where u falls, which side of
+// top-p's border a logit is on) is held against a bound on the sums' errors (Slack).
+// One that lies nearer is made again from weights in two words (exact_weight.cuh), which
+// takes the row 6 us (2048 tokens) to 13 (131072, eight CTAs; 25 with two).  How often
+// depends on the law: its tokens' borders, 2 slack wide each.  Of rows of 128256
+// tokens drawn from whole 4% (standard deviation 3, and some tokens 9 above) and 27%
+// (1), of 32000 under top-p 0.95 8%, under min-p 0.02 as well or top-k 50 0 to 0.2%.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -28,6 +36,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "exact_weight.cuh"
 #include "internal.h"
 #include "specverify.h"
 
@@ -87,7 +96,11 @@ __device__ __forceinline__ void max_cluster_u32(const void *p, uint32_t rank, ui
 // own (the aligned form wants whole warps).
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-__device__ __forceinline__ void cluster_meet() {
+__device__ __forceinline__ void cluster_meet(uint32_t ranks) {
+  if (ranks == 1) {  // (the cluster's takes 1000 cycles all the same)
+    __syncthreads();
+    return;
+  }
   cluster_arrive();
   cluster_wait();
 }
@@ -103,6 +116,10 @@ struct SampleShared {
   uint32_t over[kSmMaxCluster];     // CTAs with a warp that has too many to list
   uint32_t min_p_key;
   float floor;                      // what top-p's histogram says
+  uint32_t sure;                    // what was decided by fp32 weights holds
+  float M;                          // the row's largest logit
+  Words dpart[2][kSmMaxCluster];    // exact sums: of the CTAs, two in turn, and of this CTA's warps
+  Words dwarp[kSmWarps];
   union {
     struct {
       u64 hist[kSmBins];            // first CTA: the cluster's
@@ -150,11 +167,11 @@ __device__ __forceinline__ i64 fraction_of(float f, i64 n, bool up) {
   return static_cast<i64>(r + (up && rest ? 1 : 0));
 }
 
-// The weights of a row: w(l) = 2^((l - M) log2(e) / T).  The exponent is rounded
-// to fp32 like its factors, so a weight of 2^-y is off by about y 2^-24, and by the
-// hardware's 2^-22 at most: each on its own, so that in the sums it evens out.
-// (Exponents to twice the bits, as first-order corrections, took twice the
-// instructions of the pass and left the hardware's error.)
+// The weights of a row: w(l) = 2^((l - M) log2(e) / T), in fp32.  A weight of 2^-y is
+// off by less than 3.25 ln 2 2^-24 y of itself (the difference, the product, the
+// division by T, log2(e): the latter two alike for all of a row) and the hardware's
+// 2^-22 for the power.  (In two words all along the passes would take ten times the
+// instructions.)
 struct Weight {
   float M, sc;
   __device__ __forceinline__ float operator()(float l) const { return ex2((l - M) * sc); }
@@ -200,15 +217,444 @@ __device__ __forceinline__ uint4 load_vector(const char *row, int at, int last, 
   }
 }
 
+// How far a sum of fp32 weights (an integer's worth) may lie from the true one, with a
+// tenth to spare.  The exponents' part: sum w y <= s log2(V / s), most where all
+// weights are alike.  Powers: the weight's own, the row's, and one for each time that a
+// thread's largest logit grew (with every batch but the first at most).  Sums: 8
+// roundings in a batch, one a batch.  And an integer's half for each vector or thread.
+struct Slack {
+  float V, powers;
+  __device__ __forceinline__ explicit Slack(const SampleParams &P)
+      : V(static_cast<float>(P.V)), powers(1.1f * ((P.batches + 1) * 0x1.4p-22f + (8 + P.batches) * 0x1p-24f)) {}
+  __device__ __forceinline__ float operator()(i64 sum) const {
+    const float s = fmaxf(static_cast<float>(sum) / kSmFix, 0x1p-60f);
+    return (s * (1.1f * 1.35e-7f * __log2f(V / s) + powers)) * kSmFix + 0x1p16f;
+  }
+};
+
+// ------------------------------------------------------------ exact decisions
+// What is done for few rows stays out of line and asks for little, so that the rest
+// is not slower for it.
+
+// Dynamic shared memory: kPower32, the largest logit of every batch of vectors of every
+// thread, and the slice where it is kept.
+extern __shared__ __align__(16) unsigned char smp_raw[];
+constexpr int kSmTable = 32 * 8;
+__device__ __forceinline__ const float2 *power_table() { return reinterpret_cast<const float2 *>(smp_raw); }
+__device__ __forceinline__ float *batch_largest() { return reinterpret_cast<float *>(smp_raw + kSmTable); }
+__device__ __forceinline__ uint4 *kept_slice(const SampleParams &P) { return reinterpret_cast<uint4 *>(smp_raw + kSmTable + P.batches * kSmThreads * 4); }
+
+// A CTA's part of a row, a run of vectors for each thread.
+template <bool BF16, bool VEC, bool KEEP>
+struct RowSlice {
+  static constexpr int E = BF16 ? 8 : 4;
+  const char *row;
+  const uint4 *data;
+  uint64_t policy;
+  int first, last, vecs, per;
+  __device__ __forceinline__ RowSlice(const SampleParams &P) {
+    row = static_cast<const char *>(P.logits) + static_cast<size_t>(blockIdx.x / cluster_nctarank()) * P.row_stride * (BF16 ? 2 : 4);
+    data = kept_slice(P);
+    policy = l2_policy_evict_normal();
+    first = cluster_ctarank() * P.slice;
+    last = min(P.V, first + P.slice);
+    vecs = last > first ? (last - first + E - 1) / E : 0;
+    per = (vecs + kSmThreads - 1) / kSmThreads;
+  }
+  __device__ __forceinline__ uint4 operator()(int v) const { return KEEP ? data[v] : load_vector<BF16, VEC>(row, first + v * E, last, policy); }
+};
+__device__ __forceinline__ ExactWeight exact_weight(const SampleParams &P, const SampleShared &S) {
+  return ExactWeight(S.M, P.temperature ? __ldg(P.temperature + blockIdx.x / cluster_nctarank()) : 1.f, power_table());
+}
+
+// The weights that reach `floor` in vectors from .. to - 1, by one thread.
+template <bool BF16, bool VEC, bool KEEP>
+__device__ __noinline__ Words lane_sum(const SampleParams &P, const SampleShared &S, float floor, int from, int to) {
+  const RowSlice<BF16, VEC, KEEP> row(P);
+  const ExactWeight weight = exact_weight(P, S);
+  ExactSum<2> sum;
+  uint4 q[3];  // the next ones are on their way
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (from + i < to) q[i] = row(from + i);
+#pragma unroll 1
+  for (int v = from; v < to; ++v) {
+    if (v + 2 < to) q[2] = row(v + 2);
+    if (vector_max<BF16>(q[0]) >= floor) {
+#pragma unroll
+      for (int e = 0; e < row.E; e += 4) {
+        const float2 l[2] = {make_float2(element<BF16>(q[0], e), element<BF16>(q[0], e + 1)), make_float2(element<BF16>(q[0], e + 2), element<BF16>(q[0], e + 3))};
+        float2 w[2], wl[2];
+        weight(l, floor, w, wl);
+        sum.add(w, wl);
+      }
+    }
+    q[0] = q[1];
+    q[1] = q[2];
+  }
+  return sum.all();
+}
+
+// Of the lanes' shares, one after the other from `run` on: the first that passes
+// `target`, or (hit: 0) the last that is not empty; -1: all are.  What lies before it,
+// and where all of them end.
+struct Found {
+  int lane, hit;
+  Words before, end;
+};
+// (the first `width` lanes have some)
+__device__ __noinline__ Found find_lane(Words x, int width, Words run, Words target) {
+  const int lane = threadIdx.x % 32;
+  if (lane >= width) x = {0.f, 0.f};
+  Words inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    if (o >= width) break;
+    const Words y = {__shfl_up_sync(FULL_MASK, inc.hi, o), __shfl_up_sync(FULL_MASK, inc.lo, o)};
+    if (lane >= o) inc = add_words(inc, y);
+  }
+  const Words upto = add_words(run, inc);
+  const unsigned some = __ballot_sync(FULL_MASK, x.hi > 0.f), hit = some & __ballot_sync(FULL_MASK, exceeds(upto, target));
+  Found f;
+  f.hit = hit != 0;
+  f.lane = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : -1;
+  f.before = {__shfl_sync(FULL_MASK, upto.hi, max(f.lane - 1, 0)), __shfl_sync(FULL_MASK, upto.lo, max(f.lane - 1, 0))};
+  if (f.lane < 1) f.before = run;
+  f.end = {__shfl_sync(FULL_MASK, upto.hi, width - 1), __shfl_sync(FULL_MASK, upto.lo, width - 1)};
+  return f;
+}
+// The shares' sum.
+__device__ __forceinline__ Words sum_lanes(Words x, int width) { return find_lane(x, width, {0.f, 0.f}, {INFINITY, 0.f}).end; }
+
+// The exact mass of the row's logits that reach `floor`, by the whole cluster, the
+// same in every thread; the shares of the CTAs are in S.dpart[turn] (another one's with
+// each call), of the warps in S.dwarp, and a lane's is `mine`.
+template <bool BF16, bool VEC, bool KEEP>
+__device__ __noinline__ Words exact_sum(const SampleParams &P, SampleShared &S, float floor, int turn, Words &mine) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const uint32_t ranks = cluster_nctarank();
+  const RowSlice<BF16, VEC, KEEP> row(P);
+  const int v = min(row.vecs, tid * row.per);
+  mine = lane_sum<BF16, VEC, KEEP>(P, S, floor, v, min(row.vecs, v + row.per));
+  const Words part = sum_lanes(mine, 32);
+  if (lane == 0) S.dwarp[warp] = part;
+  __syncthreads();
+  if (warp == 0) {
+    const Words all = sum_lanes(S.dwarp[lane % kSmWarps], kSmWarps);
+    if (lane < static_cast<int>(ranks))
+      st_cluster_u64(&S.dpart[turn][cluster_ctarank()], lane, static_cast<u64>(__float_as_uint(all.lo)) << 32 | __float_as_uint(all.hi));
+  }
+  cluster_meet(ranks);
+  return sum_lanes(S.dpart[turn][lane % kSmMaxCluster], ranks);
+}
+template <bool BF16, bool VEC, bool KEEP>
+__device__ __forceinline__ Words exact_mass(const SampleParams &P, SampleShared &S, float floor, int turn) {
+  Words mine;
+  return exact_sum<BF16, VEC, KEEP>(P, S, floor, turn, mine);
+}
+
+// The row's token from exact weights, by the whole cluster: the smallest that
+// reaches `floor` and whose running sum passes u times the whole.
+template <bool BF16, bool VEC, bool KEEP>
+__device__ __noinline__ void draw_exact(const SampleParams &P, SampleShared &S, float floor, int turn) {
+  constexpr int E = BF16 ? 8 : 4;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  Words mine;
+  const Words Z = exact_sum<BF16, VEC, KEEP>(P, S, floor, turn, mine);
+  const int b = blockIdx.x / cluster_nctarank();
+  const RowSlice<BF16, VEC, KEEP> row(P);
+  const Words target = times(__ldg(P.u + b), Z);
+  // (Sums made in another order round another way: where nothing passes the target, the
+  // last share that is not empty has it.)
+  Found f = find_lane(S.dpart[turn][lane % kSmMaxCluster], cluster_nctarank(), {0.f, 0.f}, target);
+  if (f.lane != static_cast<int>(cluster_ctarank())) return;
+  f = find_lane(S.dwarp[lane % kSmWarps], kSmWarps, f.before, target);
+  if (f.lane != warp) return;
+  f = find_lane(mine, 32, f.before, target);
+  // the lane's vectors, side by side
+  const int a0 = min(row.vecs, (warp * 32 + f.lane) * row.per), a1 = min(row.vecs, a0 + row.per);
+  int vec = -1;
+  Words run = f.before;
+  for (int v = a0; v < a1; v += 32) {
+    const Found g = find_lane(lane_sum<BF16, VEC, KEEP>(P, S, floor, v + lane, min(a1, v + lane + 1)), 32, run, target);
+    if (g.lane >= 0) vec = v + g.lane, f = g;
+    if (g.hit) break;
+    run = g.end;
+  }
+  if (vec < 0) return;  // (only where another stream writes the row meanwhile)
+  // its elements, a lane each
+  const uint4 q = row(vec);
+  float l = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (lane == e) l = element<BF16>(q, e);
+  const Words x = exact_weight(P, S)(l, floor);
+  if (lane == find_lane(x, E, f.before, target).lane) {
+    P.token[b] = row.first + vec * E + lane;
+    if (P.prob) P.prob[b] = x.hi / Z.hi;
+    P.row_status[b] = 0;
+  }
+}
+
+// Place `at` of the list of the segments one after the other.
+__device__ __forceinline__ int listed_at(const SampleShared &S, int nseg, int seglen, int at) {
+  int seg = 0;  // the last segment that starts at or before `at`
+#pragma unroll
+  for (int step = kSmSegs / 2; step > 0; step >>= 1)
+    if (seg + step < nseg && S.at[seg + step] <= at) seg += step;
+  return seg * seglen + at - S.at[seg];
+}
+
+// The token of a list (key 0: not in the law), by the first CTA, for u next to 0: among
+// weights that an integer holds few bits of, or none.
+__device__ __noinline__ void draw_small(const SampleParams &P, SampleShared &S, int b, int nseg, int seglen, int total) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const ExactWeight weight = exact_weight(P, S);
+  // a warp's places lie side by side
+  const int each = (total + kSmThreads - 1) / kSmThreads * 32, a0 = min(total, warp * each), a1 = min(total, a0 + each);
+  auto weigh = [&](int at) {
+    const uint32_t key = at < a1 ? static_cast<uint32_t>(S.cand[listed_at(S, nseg, seglen, at)] >> 32) : 0u;
+    const float l = key ? smp_from_key(key) : -INFINITY;
+    return weight(l, -INFINITY);
+  };
+  Words mine = {0.f, 0.f};
+#pragma unroll 1
+  for (int at = a0; at < a1; at += 32) mine = add_words(mine, weigh(at + lane));
+  mine = sum_lanes(mine, 32);
+  if (lane == 0) S.dwarp[warp] = mine;
+  __syncthreads();
+  const Words share = S.dwarp[lane % kSmWarps], Z = sum_lanes(share, kSmWarps), target = times(__ldg(P.u + b), Z);
+  Found f = find_lane(share, kSmWarps, {0.f, 0.f}, target);
+  if (f.lane != warp) return;
+  int place = -1;
+  float prob = 0.f;
+  Words run = f.before;
+#pragma unroll 1
+  for (int at = a0; at < a1; at += 32) {
+    const Words x = weigh(at + lane);
+    f = find_lane(x, 32, run, target);
+    if (f.lane == lane) place = at + lane, prob = x.hi / Z.hi;
+    else if (f.lane >= 0) place = -1;
+    if (f.hit) break;
+    run = f.end;
+  }
+  if (place >= 0) {
+    P.token[b] = static_cast<int>(static_cast<uint32_t>(S.cand[listed_at(S, nseg, seglen, place)]));
+    if (P.prob) P.prob[b] = prob;
+    P.row_status[b] = 0;
+  }
+}
+
+// What a list's members are held against.
+struct ListLaw {
+  int nseg, seglen, total, round;  // segments, places in each, members in all; of the exchange
+  int top_k;                       // 0: off
+  uint32_t floor_key, top_key;     // min-p's floor, where members are not asked themselves; the largest logit's
+  bool use_p, ask;
+  float top_p, min_p, u, M, T;
+  i64 need;                        // top-p's share of the whole row's mass (without top-k)
+};
+
+// The token of a list, by the first CTA.  By fp32 weights nothing is written, and the
+// answer is true, where a decision lies nearer than their errors (open: top-p's, where
+// it goes by the whole row); by exact ones (EXACT) all is decided, but for tokens
+// next to u = 0.
+template <bool BF16, bool EXACT>
+__device__ __forceinline__ bool list_token(const SampleParams &P, SampleShared &S, int b, const ListLaw &L, const Weight &weight, const Slack &slack, float open) {
+  constexpr int kLow = BF16 ? 16 : 0;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, total = L.total;
+  int round = L.round;
+  auto block_sum64 = [&](i64 a) {
+    const int r = round & 1;
+    ++round;
+    a = warp_sum64(a);
+    if (lane == 0) S.warp[r][warp] = static_cast<u64>(a);
+    __syncthreads();
+    u64 x = 0;
+#pragma unroll
+    for (int k = 0; k < kSmWarps; ++k) x += S.warp[r][k];
+    return static_cast<i64>(x);
+  };
+  const int each = (total + kSmThreads - 1) / kSmThreads;  // neighbours in a thread, at most kSmPer
+  uint32_t key[kSmPer];
+  int id[kSmPer];
+  i64 w[kSmPer];
+  bool low[kSmPer];  // out by min-p
+#pragma unroll
+  for (int i = 0; i < kSmPer; ++i) low[i] = false, key[i] = 0, id[i] = -1, w[i] = 0;
+  auto take = [&](int i) {
+    const int at = tid * each + i;
+    if (i < each && at < total) {
+      const u64 c = S.cand[listed_at(S, L.nseg, L.seglen, at)];
+      key[i] = static_cast<uint32_t>(c >> 32);
+      id[i] = static_cast<int>(static_cast<uint32_t>(c));
+      const float l = smp_from_key(key[i]);
+      float y;
+      if constexpr (EXACT) {
+        const Words x = ExactWeight(L.M, L.T, power_table())(l, -INFINITY);
+        y = x.hi;
+        w[i] = __float2ll_rn(y * kSmFix) + __float2ll_rn(x.lo * kSmFix);
+      } else {
+        y = weight(l);
+        w[i] = __float2ll_rn(y * kSmFix);
+      }
+      // min-p: by the weight, or in fp64 where that is too near to say
+      if (L.ask) {
+        bool out = y < L.min_p;
+        if (fabsf(y - L.min_p) <= 1e-5f * L.min_p)
+          out = static_cast<double>(l) - static_cast<double>(L.M) < static_cast<double>(L.T) * log(static_cast<double>(L.min_p));
+        low[i] = out;
+      }
+    }
+  };
+  take(0);
+  if (each > 1) {  // (passed by at once: what is skipped piece by piece is fetched all the same)
+#pragma unroll
+    for (int i = 1; i < kSmPer; ++i) take(i);
+  }
+  bool unsure = false;
+  i64 need = L.need;
+  if (total <= kSmPairs) {
+    // --- few: each thread holds its candidate (each = 1) against all of them
+    if (tid < total) S.mass[tid] = static_cast<u64>(w[0]), S.tmax[tid] = key[0];
+    __syncthreads();
+    i64 above = 0;
+    int larger = 0;
+    if (tid < total)
+#pragma unroll 4
+      for (int j = 0; j < total; ++j) {
+        const bool gt = S.tmax[j] > key[0];
+        larger += gt;
+        above += gt ? static_cast<i64>(S.mass[j]) : 0;
+      }
+    bool keep = tid < total && key[0] >= L.floor_key && !low[0] && (!L.top_k || larger < L.top_k);
+    if (L.top_k && L.use_p) {
+      const i64 mass = block_sum64(tid < total && larger < L.top_k ? w[0] : 0);
+      need = fraction_of(L.top_p, mass, true);
+      open = 2.f * slack(mass);
+    }
+    if (L.use_p) {
+      if (!EXACT) unsure = keep && fabsf(static_cast<float>(above - need)) <= open;
+      keep = keep && above < need;
+    }
+    if (!keep) w[0] = 0, id[0] = -1;
+  } else {
+    uint32_t floor = L.floor_key, least = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < kSmPer; ++i)
+      if (id[i] >= 0) least = min(least, key[i]);
+    {
+      const int r = round & 1;
+      ++round;
+      least = __reduce_min_sync(FULL_MASK, least);
+      if (lane == 0) S.warp[r][warp] = least;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kSmWarps; ++k) least = min(least, static_cast<uint32_t>(S.warp[r][k]));
+    }
+    if (L.top_k) {
+      uint32_t lo = least >> kLow, hi = L.top_key >> kLow;
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kSmPer; ++i) n += id[i] >= 0 && key[i] >= mid << kLow;
+        if (block_sum64(n) >= L.top_k) lo = mid;
+        else hi = mid - 1;
+      }
+      floor = max(floor, lo << kLow);
+      if (L.use_p) {
+        i64 a = 0;
+#pragma unroll
+        for (int i = 0; i < kSmPer; ++i)
+          if (key[i] >= lo << kLow) a += w[i];
+        a = block_sum64(a);
+        need = fraction_of(L.top_p, a, true);
+        open = 2.f * slack(a);
+        least = max(least, lo << kLow);
+      }
+    }
+    if (L.use_p) {
+      uint32_t lo = least >> kLow, hi = L.top_key >> kLow;
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        i64 a = 0;
+#pragma unroll
+        for (int i = 0; i < kSmPer; ++i)
+          if (key[i] >= mid << kLow) a += w[i];
+        a = block_sum64(a);
+        if (!EXACT) unsure = unsure || fabsf(static_cast<float>(a - need)) <= open;
+        if (a >= need) lo = mid;
+        else hi = mid - 1;
+      }
+      floor = max(floor, lo << kLow);
+    }
+#pragma unroll
+    for (int i = 0; i < kSmPer; ++i)
+      if (key[i] < floor || low[i]) w[i] = 0, id[i] = -1;
+  }
+  // --- running sums in vocabulary order
+  i64 mine = 0;
+#pragma unroll
+  for (int i = 0; i < kSmPer; ++i) mine += w[i];
+  const i64 inc = warp_scan64(mine, lane);
+  const int r = round & 1;
+  if (lane == 31) S.warp[r][warp] = static_cast<u64>(inc);
+  unsure = __syncthreads_or(unsure);
+  if (unsure) return true;
+  i64 run = inc - mine, all = 0;
+#pragma unroll
+  for (int k = 0; k < kSmWarps; ++k) {
+    const i64 x = static_cast<i64>(S.warp[r][k]);
+    if (k < warp) run += x;
+    all += x;
+  }
+  const i64 target = fraction_of(L.u, all, false);
+  if (EXACT && target < 1 << 20) {
+#pragma unroll
+    for (int i = 0; i < kSmPer; ++i)
+      if (id[i] < 0 && i < each && tid * each + i < total) S.cand[listed_at(S, L.nseg, L.seglen, tid * each + i)] = 0;
+    __syncthreads();
+    draw_small(P, S, b, L.nseg, L.seglen, total);
+    return false;
+  }
+  int token = -1;
+  i64 its = 0, low_end = 0;
+#pragma unroll
+  for (int i = 0; i < kSmPer; ++i) {
+    if (run <= target && run + w[i] > target) token = id[i], its = w[i], low_end = run;
+    run += w[i];
+  }
+  bool sure = false;
+  if (token >= 0) {
+    const float off = slack(all);
+    sure = EXACT || (static_cast<float>(target - low_end) > off && static_cast<float>(low_end + its - target) > off);
+    if (sure) {
+      P.token[b] = token;
+      if (P.prob) P.prob[b] = static_cast<float>(its) / static_cast<float>(all);
+      P.row_status[b] = 0;
+    }
+  }
+  return EXACT ? false : !__syncthreads_or(sure);
+}
+template <bool BF16, bool VEC, bool KEEP>
+__device__ __noinline__ void list_token_exact(const SampleParams &P, SampleShared &S, int b, const ListLaw &law) {
+  ListLaw L = law;
+  if (L.use_p && !L.top_k) {
+    const Words share = times(L.top_p, exact_mass<BF16, VEC, KEEP>(P, S, -INFINITY, 0));
+    L.need = __float2ll_rn(share.hi * kSmFix) + __float2ll_ru(share.lo * kSmFix);
+  }
+  __syncthreads();  // (the exchange's buffers start anew)
+  list_token<BF16, true>(P, S, b, L, Weight{L.M, 0.f}, Slack(P), 0.f);
+}
+
 // KEEP: slices stay in shared memory; else later passes read them again, from L2.
 template <bool BF16, bool VEC, bool KEEP>
 __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_constant__ SampleParams P) {
   constexpr int E = BF16 ? 8 : 4;
   __shared__ SampleShared S;
-  extern __shared__ __align__(16) unsigned char smp_raw[];
-  // the largest logit of every batch of vectors of every thread, then the slice
-  float *const largest = reinterpret_cast<float *>(smp_raw);
-  uint4 *const data = reinterpret_cast<uint4 *>(smp_raw + P.batches * kSmThreads * 4);
+  float *const largest = batch_largest();
+  uint4 *const data = kept_slice(P);
   const uint32_t ranks = cluster_nctarank(), rank = cluster_ctarank();
   const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const char *row = static_cast<const char *>(P.logits) + static_cast<size_t>(b) * P.row_stride * (BF16 ? 2 : 4);
@@ -219,6 +665,8 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   const int v0 = min(vecs, warp * per), v1 = min(vecs, v0 + per);
 
   S.tmax[tid] = 0;
+  if (tid < 32) reinterpret_cast<float2 *>(smp_raw)[tid] = kPower32[tid];
+  if (tid == 0) S.sure = 0;
   cluster_arrive();  // the others must be running before anything is stored into their memory
   // --- the slice, and its largest logit
   const uint64_t policy = KEEP ? l2_policy_evict_first() : l2_policy_evict_normal();
@@ -257,12 +705,16 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
     if (top > -INFINITY) {
       weight.M = top;
-      float2 s = make_float2(0.f, 0.f);
+      float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int i = 0; i < kSmBatch; ++i)
-#pragma unroll
-        for (int e = 0; e < E; e += 2) s = fadd2(s, weight(make_float2(element<BF16>(q[i], e), element<BF16>(q[i], e + 1))));
-      mass += s.x + s.y;
+      for (int i = 0; i < kSmBatch; ++i) {
+        auto pair = [&](int e) { return weight(make_float2(element<BF16>(q[i], e), element<BF16>(q[i], e + 1))); };
+        float2 x = fadd2(pair(0), pair(2));
+        if constexpr (BF16) x = fadd2(x, fadd2(pair(4), pair(6)));
+        s[i % 2] = fadd2(s[i % 2], x);
+      }
+      s[0] = fadd2(s[0], s[1]);
+      mass += s[0].x + s[0].y;
     }
   }
   const uint32_t my_top = smp_key(top);
@@ -286,7 +738,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   // (every CTA's columns have been cleared: it has arrived)
   if (top_k && top_k <= kSmThreads)
     for (uint32_t k = 0; k < ranks; ++k) max_cluster_u32(&S.tmax[tid], k, my_top);
-  cluster_meet();
+  cluster_meet(ranks);
   uint32_t top_key = 0;
   flags = 0;
   for (uint32_t k = 0; k < ranks; ++k) {
@@ -307,6 +759,10 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     return;
   }
   weight.M = M;
+  if (tid == 0) S.M = M;
+  // temperatures whose reciprocals or differences leave fp32's range: exact weights alone
+  const bool far = !(T >= 0x1p-64f && T <= 0x1p64f);
+  const Slack slack(P);
   // min-p's floor in fp32, put below it by more than what that rounds
   const float min_p_low = use_m ? M + log2f(min_p) / weight.sc - (1e-5f - 1e-5f * log2f(min_p)) / weight.sc - 0x1p-21f * fabsf(M) : -INFINITY;
 
@@ -336,7 +792,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       st_cluster_u64(&S.part[r][rank], tid, x);
       st_cluster_u64(&S.part2[r][rank], tid, y);
     }
-    cluster_meet();
+    cluster_meet(ranks);
     A = C = 0;
     for (uint32_t k = 0; k < ranks; ++k) A += static_cast<i64>(S.part[r][k]), C += static_cast<i64>(S.part2[r][k]);
     return r;
@@ -355,8 +811,9 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
     return exchange(a, n, mass, count);
   };
-  // the token at u: all CTAs together, from the sums that exchange number r left.
-  // A running sum of integers passes u Z where it passes floor(u Z).
+  // The token at u: all CTAs together, from the sums that exchange number r left.
+  // A running sum of integers passes u Z where it passes floor(u Z).  Nothing is
+  // written, and S.sure left 0, where the sums' errors leave the token open.
   auto choose = [&](float floor, int r, i64 Z) {
     const i64 target = fraction_of(u, Z, false);  // less than Z, so it is passed
     int owner = 0;
@@ -374,6 +831,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       if (before + x > target) break;
       before += x;
     }
+    const i64 start = before;
     // that warp's part of the slice, an eighth to each warp
     const int lo = min(vecs, w * per), hi = min(vecs, lo + per), each = (per / 32 + kSmWarps - 1) / kSmWarps * 32;
     const int a0 = min(hi, lo + warp * each), a1 = min(hi, a0 + each);
@@ -398,40 +856,8 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       part = k;
       if (before + x > target) break;
     }
-    if (part < 0) {
-      // the threads' sums weigh something, but no vector of theirs does by itself: the first
-      // token with a weight at all
-      if (warp != 0) return;
-      for (int v = lo; v < hi; v += 32) {
-        const int mine = v + lane;
-        int e = E;
-        float y = 0.f;
-        if (mine < hi) {
-          const uint4 q = vector_at(mine);
-#pragma unroll
-          for (int i = E - 1; i >= 0; --i) {
-            const float l = element<BF16>(q, i), z = l >= floor ? weight(l) : 0.f;
-            if (z > 0.f) e = i, y = z;
-          }
-        }
-        const unsigned some = __ballot_sync(FULL_MASK, e < E);
-        if (!some) continue;
-        if (lane == __ffs(some) - 1) {
-          P.token[b] = first + mine * E + e;
-          if (P.prob) P.prob[b] = y * kSmFix / static_cast<float>(Z);
-          P.row_status[b] = 0;
-        }
-        break;
-      }
-      return;
-    }
     if (part != warp) return;
-    // (what is added up again may round to a little less than that warp's sum, which
-    // was made against the threads' own maxima: the last kept token, then)
-    int tok = -1;
-    float prob = 0.f;
-    bool done = false;
-    for (int v = a0; v < a1 && !done; v += 32) {
+    for (int v = a0; v < a1; v += 32) {
       const int mine = v + lane;
       uint4 q = make_uint4(0, 0, 0, 0);
       i64 x = 0;
@@ -440,36 +866,51 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
         x = vector_mass(q, floor);
       }
       const i64 inc = warp_scan64(x, lane);
-      const unsigned hit = __ballot_sync(FULL_MASK, before + inc > target), some = __ballot_sync(FULL_MASK, x > 0);
-      const int who = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : -1;
-      if (who >= 0) {
-        int mine_tok = -1;
-        float mine_prob = 0.f;
-        if (lane == who) {  // its sums up to each element
-          float s = 0.f;
-          bool found = false;
+      const unsigned hit = __ballot_sync(FULL_MASK, before + inc > target);
+      if (!hit) {
+        before += __shfl_sync(FULL_MASK, inc, 31);
+        continue;
+      }
+      if (lane == __ffs(hit) - 1) {  // its sums up to each element
+        const i64 base = before + inc - x;
+        float s = 0.f, prob = 0.f;
+        i64 low = base, high = base;
+        int tok = -1;
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float l = element<BF16>(q, e), y = l >= floor ? weight(l) : 0.f;
-            s += y;
-            if (!found && y > 0.f) {
-              mine_tok = first + mine * E + e;
-              mine_prob = y;
-              found = before + inc - x + __float2ll_rn(s * kSmFix) > target;
-            }
+        for (int e = 0; e < E; ++e) {
+          const float l = element<BF16>(q, e), y = l >= floor ? weight(l) : 0.f;
+          s += y;
+          if (high <= target && y > 0.f) {
+            tok = first + mine * E + e;
+            prob = y;
+            low = high;
+            high = base + __float2ll_rn(s * kSmFix);
           }
         }
-        tok = __shfl_sync(FULL_MASK, mine_tok, who);
-        prob = __shfl_sync(FULL_MASK, mine_prob, who);
+        // The token is right if low (1 - u) <= u (Z - low) and high (1 - u) > u (Z - high)
+        // for the true sums.  (What lies behind the token is the whole less what lies
+        // before it, of which the warp's own part has been added up twice.)
+        const float below = (1.f - u) * slack(low) + u * (slack(Z - low) + 2.f * slack(low - start));
+        const float above = (1.f - u) * slack(high) + u * (slack(Z - high) + 2.f * slack(high - start));
+        if (tok >= 0 && static_cast<float>(target - low) > below && static_cast<float>(high - target) > above) {
+          P.token[b] = tok;
+          if (P.prob) P.prob[b] = prob * kSmFix / static_cast<float>(Z);
+          P.row_status[b] = 0;
+          for (uint32_t k = 0; k < ranks; ++k) st_cluster_u32(&S.sure, k, 1);
+        }
       }
-      done = hit != 0;
-      before += __shfl_sync(FULL_MASK, inc, 31);
+      return;
     }
-    if (lane == 0) {
-      P.token[b] = tok;
-      if (P.prob) P.prob[b] = prob * kSmFix / static_cast<float>(Z);
-      P.row_status[b] = 0;
+  };
+  // the token by fp32 weights, and where these leave it open by exact ones
+  int turn = 0;
+  auto draw = [&](float floor, int r, i64 Z) {
+    if (!far) {
+      choose(floor, r, Z);
+      cluster_meet(ranks);
+      if (S.sure) return;
     }
+    draw_exact<BF16, VEC, KEEP>(P, S, floor, turn);
   };
 
   // --- a bound that the law's floor does not lie below: the k-th largest of the
@@ -477,7 +918,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   // below the largest weight, which holds if the mass within them, found in the
   // same pass, is enough.  (Where top-p goes by the mass that top-k leaves, what
   // reaches top-k's floor has to be listed whole.)
-  const bool near = use_p && !top_k;
+  const bool near = use_p && !top_k && !far;
   const float near_floor = near ? M - (5.f - log2f(1.f - top_p)) / weight.sc : -INFINITY;
   float from = top_k && use_p ? -INFINITY : fmaxf(min_p_low, near_floor);
   if (top_k && top_k <= kSmThreads) {
@@ -499,7 +940,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
     from = fmaxf(from, smp_from_key(max(t << 16, kSmMinusInf)));
   }
-  const bool plain = !top_k && !use_p && !use_m, bounded = from > -INFINITY;
+  const bool plain = !top_k && !use_p && !use_m, bounded = from > -INFINITY && !far;
   // --- the logits from the bound on into the first CTA's list, warp by warp and so
   // in vocabulary order; and the row's mass
   int nseg = kSmWarps * ranks, seglen = kSmCands / nseg;
@@ -574,17 +1015,19 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     // (the second sum is a bound: cut by more than its rounding)
     const int r = exchange(a, __float2ll_rn(c * (kSmFix * (1.f - 0x1p-14f))), Z, within);
     if (plain) {
-      choose(-INFINITY, r, Z);
+      draw(-INFINITY, r, Z);
       return;
     }
     if (!count_near) within = Z;  // the bound holds as it is
   }
   const i64 want = use_p ? fraction_of(top_p, Z, true) : 0;  // of the whole row's mass
-  bool listed = bounded && within >= want;
+  // ... and a share of it that is more than top-p's, whatever the sums' errors
+  const i64 ample = use_p ? want + static_cast<i64>(2.f * slack(Z)) : 0;
+  bool listed = bounded && within >= ample;
   for (uint32_t k = 0; k < ranks; ++k) listed = listed && !S.over[k];
   uint32_t floor_key = kSmMinusInf;  // min-p's, where the list's members are not asked themselves
   bool ask = use_m;
-  uint32_t bound = smp_key(near && within < want ? min_p_low : from);
+  uint32_t bound = smp_key(far ? -INFINITY : near && within < ample ? min_p_low : from);
   if (!listed) {
     ask = false;
     // min-p's floor: the least logit with l - M >= T ln(min_p)
@@ -598,7 +1041,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       }
       S.min_p_key = k;
     }
-    cluster_meet();  // (the list is read by no one, and may be written over)
+    cluster_meet(ranks);  // (the list is read by no one, and may be written over)
     floor_key = S.min_p_key;
     if (!(top_k && use_p)) bound = max(bound, floor_key);
   }
@@ -609,7 +1052,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     if (!binned) {
       binned = true;
       for (int i = tid; i < kSmBins; i += kSmThreads) S.hist[i] = 0, S.mine[i] = 0;
-      cluster_meet();
+      cluster_meet(ranks);
       // What is dropped weighs less than (1 - top_p) Z, so a token of less than a
       // V-th of that cannot be the last one kept: such tokens are not looked at.
       const float least = (1.f - top_p) * 0.999f * (static_cast<float>(Z) / kSmFix) / P.V;
@@ -633,7 +1076,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       __syncthreads();  // (a slice has at most 2^16 logits: its sums stay below 2^32)
       for (int i = tid; i < kSmBins; i += kSmThreads)
         if (S.mine[i]) add_cluster_u64(&S.hist[i], 0, S.mine[i]);
-      cluster_meet();
+      cluster_meet(ranks);
       if (rank == 0) {
         // running sums from the largest weights down, in the sums' unit; bin i
         // holds weights of exponent -ceil(i / 8), 16 bits of each
@@ -653,7 +1096,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
         for (int w = 0; w < warp; ++w) run += static_cast<i64>(S.warp[r][w]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          if (run < want && run + x[j] >= want)  // one bin only: its least weight, as a logit
+          if (run < ample && run + x[j] >= ample)  // one bin only: its least weight, as a logit
             S.floor = fmaxf(from, M + (log2f(__uint_as_float(static_cast<uint32_t>((127 << 3) - i0 - j) << 20)) - 0.001f) / weight.sc);
           run += x[j];
         }
@@ -661,7 +1104,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
         if (tid > 0 && tid < static_cast<int>(ranks)) st_cluster_u32(&S.floor, tid, __float_as_uint(S.floor));
       }
       ++round;
-      cluster_meet();
+      cluster_meet(ranks);
       bound = max(bound, smp_key(S.floor));
     }
     // --- the candidates, in vocabulary order
@@ -717,7 +1160,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
         at += __shfl_sync(FULL_MASK, inc, 31);
       }
     }
-    cluster_meet();
+    cluster_meet(ranks);
     listed = true;
     for (uint32_t k = 0; k < ranks; ++k) listed = listed && static_cast<int>(S.cnt[k]) <= share;
     nseg = ranks, seglen = share;
@@ -729,6 +1172,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     // first key reaches what the unit's logit does.)
     i64 mass = 0, count = 0, need = want;
     uint32_t floor = floor_key;
+    float of = -INFINITY, open = use_p ? top_p * slack(Z) : 0.f;  // whose share is needed, and how far that may be off
     if (top_k) {
       uint32_t lo = bound >> kLow, hi = top_key >> kLow;
       while (lo < hi) {
@@ -739,37 +1183,51 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       }
       floor = max(floor_key, lo << kLow);
       if (use_p) {
+        of = smp_from_key(max(lo << kLow, kSmMinusInf));
         reach(max(lo << kLow, kSmMinusInf), mass, count);
         need = fraction_of(top_p, mass, true);
+        open = top_p * slack(mass);
         bound = max(bound, lo << kLow);
       }
     }
     if (use_p) {
+      // Of sets whose mass is too near to say, by their sizes (each holds the smaller ones):
+      // the smallest that is known to be enough, the largest that is known not to be.
+      Words whole = {-1.f, 0.f};
+      i64 ample_n = 1LL << 40, short_n = -1;
       uint32_t lo = bound >> kLow, hi = top_key >> kLow;
       while (lo < hi) {
         const uint32_t mid = lo + (hi - lo + 1) / 2;
         reach(mid << kLow, mass, count);
-        if (mass >= need) lo = mid;
+        bool enough = mass >= need;
+        if (far || fabsf(static_cast<float>(mass - need)) <= open + slack(mass)) {
+          if (count < ample_n && count > short_n) {
+            if (whole.hi < 0.f) whole = exact_mass<BF16, VEC, KEEP>(P, S, of, turn), turn ^= 1;
+            if (exceeds(times(top_p, whole), exact_mass<BF16, VEC, KEEP>(P, S, smp_from_key(mid << kLow), turn))) short_n = count;
+            else ample_n = count;
+            turn ^= 1;
+          }
+          enough = count >= ample_n;
+        }
+        if (enough) lo = mid;
         else hi = mid - 1;
       }
       floor = max(floor, lo << kLow);
     }
     const int r = reach(floor, mass, count);
-    choose(smp_from_key(floor), r, mass);
+    draw(smp_from_key(floor), r, mass);
     return;
   }
-  if (rank != 0) return;
-  auto block_sum64 = [&](i64 a) {
-    const int r = round & 1;
-    ++round;
-    a = warp_sum64(a);
-    if (lane == 0) S.warp[r][warp] = static_cast<u64>(a);
-    __syncthreads();
-    u64 x = 0;
-#pragma unroll
-    for (int k = 0; k < kSmWarps; ++k) x += S.warp[r][k];
-    return static_cast<i64>(x);
-  };
+  // top-p's border goes by the whole row's mass: where fp32 weights leave something open,
+  // by the exact one, to which all CTAs add their part
+  const bool whole_row = use_p && !top_k;
+  if (rank != 0) {
+    if (whole_row) {
+      cluster_meet(ranks);
+      if (!S.sure) exact_mass<BF16, VEC, KEEP>(P, S, -INFINITY, 0);
+    }
+    return;
+  }
   // the list's segments, one after the other
   int total = 0;
   {
@@ -785,138 +1243,15 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     if (warp == 0) S.at[2 * lane] = inc - c0 - c1, S.at[2 * lane + 1] = inc - c1;
   }
   __syncthreads();
-  const int each = (total + kSmThreads - 1) / kSmThreads;  // neighbours in a thread, at most kSmPer
-  uint32_t key[kSmPer];
-  int id[kSmPer];
-  i64 w[kSmPer];
-  bool low[kSmPer];  // out by min-p
-#pragma unroll
-  for (int i = 0; i < kSmPer; ++i) low[i] = false, key[i] = 0, id[i] = -1, w[i] = 0;
-  auto take = [&](int i) {
-    const int at = tid * each + i;
-    if (i < each && at < total) {
-      int seg = 0;  // the last segment that starts at or before `at`
-#pragma unroll
-      for (int step = kSmSegs / 2; step > 0; step >>= 1)
-        if (seg + step < nseg && S.at[seg + step] <= at) seg += step;
-      const u64 c = S.cand[seg * seglen + at - S.at[seg]];
-      key[i] = static_cast<uint32_t>(c >> 32);
-      id[i] = static_cast<int>(static_cast<uint32_t>(c));
-      const float l = smp_from_key(key[i]), y = weight(l);
-      w[i] = __float2ll_rn(y * kSmFix);
-      // min-p: by the weight, or in fp64 where that is too near to say
-      if (ask) {
-        bool out = y < min_p;
-        if (fabsf(y - min_p) <= 1e-5f * min_p)
-          out = static_cast<double>(l) - static_cast<double>(M) < static_cast<double>(T) * log(static_cast<double>(min_p));
-        low[i] = out;
-      }
-    }
-  };
-  take(0);
-  if (each > 1) {  // (passed by at once: what is skipped piece by piece is fetched all the same)
-#pragma unroll
-    for (int i = 1; i < kSmPer; ++i) take(i);
+  const ListLaw law = {nseg, seglen, total, round, top_k, floor_key, top_key, use_p, ask, top_p, min_p, u, M, T, want};
+  bool unsure = far;
+  // (both sides of the comparison may be off)
+  if (!far) unsure = list_token<BF16, false>(P, S, b, law, weight, slack, whole_row ? 2.f * slack(Z) : 0.f);
+  if (whole_row) {
+    if (tid < static_cast<int>(ranks)) st_cluster_u32(&S.sure, tid, !unsure);
+    cluster_meet(ranks);
   }
-  uint32_t floor = floor_key;
-  if (total <= kSmPairs) {
-    // --- few: each thread holds its candidate (each = 1) against all of them
-    if (tid < total) S.mass[tid] = static_cast<u64>(w[0]), S.tmax[tid] = key[0];
-    __syncthreads();
-    i64 above = 0;
-    int larger = 0;
-    if (tid < total)
-#pragma unroll 4
-      for (int j = 0; j < total; ++j) {
-        const bool gt = S.tmax[j] > key[0];
-        larger += gt;
-        above += gt ? static_cast<i64>(S.mass[j]) : 0;
-      }
-    bool keep = tid < total && key[0] >= floor && !low[0] && (!top_k || larger < top_k);
-    i64 need = want;
-    if (top_k && use_p) need = fraction_of(top_p, block_sum64(tid < total && larger < top_k ? w[0] : 0), true);
-    if (use_p) keep = keep && above < need;
-    if (!keep) w[0] = 0;
-  } else {
-    uint32_t least = 0xffffffffu;
-#pragma unroll
-    for (int i = 0; i < kSmPer; ++i)
-      if (id[i] >= 0) least = min(least, key[i]);
-    {
-      const int r = round & 1;
-      ++round;
-      least = __reduce_min_sync(FULL_MASK, least);
-      if (lane == 0) S.warp[r][warp] = least;
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < kSmWarps; ++k) least = min(least, static_cast<uint32_t>(S.warp[r][k]));
-    }
-    i64 need = want;
-    if (top_k) {
-      uint32_t lo = least >> kLow, hi = top_key >> kLow;
-      while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo + 1) / 2;
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < kSmPer; ++i) n += id[i] >= 0 && key[i] >= mid << kLow;
-        if (block_sum64(n) >= top_k) lo = mid;
-        else hi = mid - 1;
-      }
-      floor = max(floor, lo << kLow);
-      if (use_p) {
-        i64 a = 0;
-#pragma unroll
-        for (int i = 0; i < kSmPer; ++i)
-          if (key[i] >= lo << kLow) a += w[i];
-        need = fraction_of(top_p, block_sum64(a), true);
-        least = max(least, lo << kLow);
-      }
-    }
-    if (use_p) {
-      uint32_t lo = least >> kLow, hi = top_key >> kLow;
-      while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo + 1) / 2;
-        i64 a = 0;
-#pragma unroll
-        for (int i = 0; i < kSmPer; ++i)
-          if (key[i] >= mid << kLow) a += w[i];
-        if (block_sum64(a) >= need) lo = mid;
-        else hi = mid - 1;
-      }
-      floor = max(floor, lo << kLow);
-    }
-#pragma unroll
-    for (int i = 0; i < kSmPer; ++i)
-      if (key[i] < floor || low[i]) w[i] = 0;
-  }
-  // --- running sums in vocabulary order
-  i64 mine = 0;
-#pragma unroll
-  for (int i = 0; i < kSmPer; ++i) mine += w[i];
-  const i64 inc = warp_scan64(mine, lane);
-  const int r = round & 1;
-  if (lane == 31) S.warp[r][warp] = static_cast<u64>(inc);
-  __syncthreads();
-  i64 run = inc - mine, all = 0;
-#pragma unroll
-  for (int k = 0; k < kSmWarps; ++k) {
-    const i64 x = static_cast<i64>(S.warp[r][k]);
-    if (k < warp) run += x;
-    all += x;
-  }
-  const i64 target = fraction_of(u, all, false);
-  int token = -1;
-  i64 its = 0;
-#pragma unroll
-  for (int i = 0; i < kSmPer; ++i) {
-    if (run <= target && run + w[i] > target) token = id[i], its = w[i];
-    run += w[i];
-  }
-  if (token >= 0) {
-    P.token[b] = token;
-    if (P.prob) P.prob[b] = static_cast<float>(its) / static_cast<float>(all);
-    P.row_status[b] = 0;
-  }
+  if (unsure) list_token_exact<BF16, VEC, KEEP>(P, S, b, law);
 }
 
 bool smp_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -939,7 +1274,7 @@ cudaError_t launch_sample(const SampleParams &p, int ranks, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * ranks);
   cfg.blockDim = dim3(kSmThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.batches) * kSmThreads * 4 + (KEEP ? static_cast<size_t>(p.slice) * (BF16 ? 2 : 4) : 0);
+  cfg.dynamicSmemBytes = kSmTable + static_cast<size_t>(p.batches) * kSmThreads * 4 + (KEEP ? static_cast<size_t>(p.slice) * (BF16 ? 2 : 4) : 0);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
