@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
     }
     return;
   }
-  int b = blockIdx.z, split = blockIdx.y - P.check, parts = P.splits;
+  const int item = blockIdx.y - P.check;
+  int b = blockIdx.z, split = item, parts = P.splits;
   const int blk = blockIdx.x / static_cast<unsigned>(P.H), g = blockIdx.x - blk * P.H;
   const int blocks = gridDim.x / P.H;
   if (P.budget > 0) {
@@ -238,10 +239,11 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
       grid_dependency_wait();
       return;
     }
-    if (split == 0 && blk == 0 && g == 0 && lane == 0) P.nparts[b] = parts;
+    if (split == 0 && g == 0 && lane == 0) P.parts_of[b] = make_int2(item, parts);  // (one block of query rows)
   }
   const int r0 = blk * C::kM, nrows = P.N * P.G;
-  const long long flag = ((static_cast<long long>(b) * P.H + g) * blocks + blk) * P.splits + split;
+  const bool cut = P.budget > 0;
+  const long long flag = cut ? static_cast<long long>(item) * P.H + g : ((static_cast<long long>(b) * P.H + g) * blocks + blk) * P.splits + split;
   int n;
   const int cnt = paged_queries(P, b, n);
   const bool tree = P.anc != nullptr;
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
   }
   if (g0 >= g1 && P.splits > 1) {  // nothing here
     if (lane == 0) P.oflag[flag] = 0;
-    if (my_row >= 0) P.ml[static_cast<long long>(split) * P.rows + my_row] = make_float2(-INFINITY, -INFINITY);
+    if (my_row >= 0) P.ml[cut ? flag * C::kM + lane : static_cast<long long>(split) * P.rows + my_row] = make_float2(-INFINITY, -INFINITY);
     grid_dependency_wait();
     return;
   }
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(32, PagedRowCfg<CT, DP, NT>::kWarps) paged_row
       if (!some) z = -INFINITY;
       const float4 y = *reinterpret_cast<const float4 *>(buf + row * C::kOPitch + min(lane * 4, DP - 4));
       if (P.splits > 1) {
-        const long long at = static_cast<long long>(split) * P.rows + orow;
+        const long long at = cut ? flag * C::kM + rr : static_cast<long long>(split) * P.rows + orow;
         if (lane == 0) P.ml[at] = some ? make_float2(m, z) : make_float2(-INFINITY, -INFINITY);
         if (some && lane * 4 < P.D) *reinterpret_cast<float4 *>(P.part + at * P.D + lane * 4) = y;
         continue;
@@ -771,8 +773,20 @@ __global__ void __launch_bounds__(kPaJoinThreads) paged_join_kernel(const __grid
   float Z = -INFINITY;
   bool gone = false;  // a part's kernel gave up waiting: the row is flagged and its answer left empty
   float2 ml = make_float2(-INFINITY, -INFINITY);  // this lane's part (there are 32 at most)
-  const int parts = P.budget > 0 ? P.nparts[b] : P.splits;
-  if (on && lane < parts) ml = P.ml[static_cast<long long>(lane) * P.rows + r];
+  const int g = h / P.G, row = qt * P.G + h % P.G;  // the row among its KV head's
+  int parts = P.splits;
+  long long at0 = r, step = P.rows, flag0, fstep = 1;  // the first part, and from one to the next; so with the flags
+  if (P.budget > 0) {
+    const int2 of = P.parts_of[b];
+    parts = of.y;
+    flag0 = static_cast<long long>(of.x) * P.H + g;
+    fstep = P.H;
+    at0 = flag0 * P.oblk + row;
+    step = static_cast<long long>(P.H) * P.oblk;
+  } else {
+    flag0 = ((static_cast<long long>(b) * P.H + g) * ((P.N * P.G + P.oblk - 1) / P.oblk) + row / P.oblk) * P.splits;
+  }
+  if (on && lane < parts) ml = P.ml[at0 + lane * step];
   gone = __any_sync(FULL_MASK, __float_as_uint(ml.y) == kTimeoutBits);
   if (gone && lane == 0 && P.row_status) P.row_status[b] = SPEC_ROW_TIMEOUT;
   Z = ml.y;
@@ -797,7 +811,7 @@ __global__ void __launch_bounds__(kPaJoinThreads) paged_join_kernel(const __grid
         if (k < 0)
           w[j] = 0.f;
         else if (lane * 4 < P.D)
-          x[j] = *reinterpret_cast<const float4 *>(P.part + (static_cast<long long>(k) * P.rows + r) * P.D + lane * 4);
+          x[j] = *reinterpret_cast<const float4 *>(P.part + (at0 + k * step) * P.D + lane * 4);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -807,9 +821,7 @@ __global__ void __launch_bounds__(kPaJoinThreads) paged_join_kernel(const __grid
         acc[3] = fmaf(w[j], x[j].w, acc[3]);
       }
     }
-    const int g = h / P.G, blocks = (P.N * P.G + P.oblk - 1) / P.oblk;
-    const int32_t *flag = P.oflag + ((static_cast<long long>(b) * P.H + g) * blocks + (qt * P.G + h % P.G) / P.oblk) * P.splits;
-    if (__any_sync(FULL_MASK, lane < parts && flag[lane])) {
+    if (__any_sync(FULL_MASK, lane < parts && P.oflag[flag0 + lane * fstep])) {
       const int n = P.kv_len[b], p = n + (P.anc ? P.depth[static_cast<size_t>(b) * P.N + qt] : qt);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -925,17 +937,23 @@ PagedPlan plan_paged(const spec_paged_attention_args *a) {
   p.info_at = at;
   at += pa_round(static_cast<size_t>(a->B) * 4);
   p.count_at = at;
-  at += pa_round(static_cast<size_t>(a->B) * 4);
+  at += pa_round(static_cast<size_t>(a->B) * 8);
   p.anc_at = at;
   at += pa_round(q * p.W * 4);
   p.depth_at = at;
   at += pa_round(a->parent ? q * 4 : 0);
+  // parts times what each has: rows of answers, or (by a budget) of a block
+  size_t flags = static_cast<size_t>(items) * p.splits, part_rows = p.splits * p.rows;
+  if (p.budget > 0) {
+    flags = static_cast<size_t>(std::min<long long>(p.budget, static_cast<long long>(a->B) * p.splits)) * a->heads;
+    part_rows = flags * p.oblk;
+  }
   p.flag_at = at;
-  if (p.splits > 1) at += pa_round(static_cast<size_t>(items) * p.splits * 4);
+  if (p.splits > 1) at += pa_round(flags * 4);
   p.ml_at = at;
-  if (p.splits > 1) at += pa_round(p.splits * p.rows * sizeof(float2));
+  if (p.splits > 1) at += pa_round(part_rows * sizeof(float2));
   p.part_at = at;
-  if (p.splits > 1) at += pa_round(p.splits * p.rows * a->head_dim * 4);
+  if (p.splits > 1) at += pa_round(part_rows * a->head_dim * 4);
   p.bytes = at + 256;
   return p;
 }
@@ -994,7 +1012,7 @@ spec_status spec_paged_attention(const spec_paged_attention_args *a, void *out, 
   p.rows = static_cast<int>(plan.rows);
   p.splits = plan.splits;
   p.budget = plan.splits > 1 ? plan.budget : 0;
-  p.nparts = reinterpret_cast<int32_t *>(w + plan.count_at);
+  p.parts_of = reinterpret_cast<int2 *>(w + plan.count_at);
   p.min_groups = 1;  // (one token under a window of 128: 14.0 us with four, 11.7 so)
   p.oblk = plan.oblk;
   p.ml = reinterpret_cast<float2 *>(w + plan.ml_at);

@@ -47,17 +47,19 @@ struct PagedParams {
   const uint32_t *anc;
   const int32_t *depth;
   int W;
-  // partial sums: part s of output row r has O at part[(s * rows + r) * D] and
-  // (m, z) at ml[s * rows + r]; z = -inf: an empty part, O not written
+  // partial sums: part s of output row r has O at part[at * D] and (m, z) at ml[at],
+  // at = s * rows + r, and where rows are cut by a budget, so that there are no more
+  // parts than run side by side, at = (item * H + KV head) * oblk + row of the block;
+  // z = -inf: an empty part, O not written
   float *part;
   float2 *ml;
   int rows;                    // B * N * Hq
   int splits;                  // parts of an item's keys, at most; 1: the answers are written at once
   int budget;                  // > 0: the rows are cut into at most this many parts (cut_groups) ...
-  int32_t *nparts;             // ... each into this many
+  int2 *parts_of;              // ... each into y parts, items x, x + 1, ..
   int min_groups;              // groups in a part, at least
   int oblk;                    // query rows per item
-  int32_t *oflag;              // per item and part: a value that is not finite was left out of its sums
+  int32_t *oflag;              // per item and part (by a budget: [item][KV head]): a value that is not finite was left out of its sums
   void *out;
   float *lse;
   int32_t *row_status;
