@@ -123,7 +123,7 @@ __device__ __forceinline__ bool paged_sees(const PagedParams &P, int b, int i, i
 template <int CT>
 __device__ __noinline__ float paged_odd_sum(const PagedParams &P, int b, int i, int c, int n, int p, int g, int d) {
   float y = 0.f;
-  const Keys keys(P, p, P.anc ? n + c : p + 1);
+  const Keys keys(P, P.anc ? n : p, P.anc ? n + c : p + 1);  // (in a tree a sink's slot may be anywhere behind n)
   for (int k = 0; k < keys.n; ++k) {
     const int t0 = keys.token(k);
     for (int t = t0; t < t0 + kGroup; ++t)
