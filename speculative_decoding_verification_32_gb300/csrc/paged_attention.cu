@@ -29,6 +29,9 @@ namespace {
 constexpr float kPaLazy = 8.f;
 constexpr int kCheckThreads = 256;
 constexpr int kPaJoinThreads = 128;
+// Rows of more tokens are not cut by a budget: cut_groups counts groups of 16 of them
+// in fp32 and adds up 128 rows' in 32 bits.  (What its own few queries bring may be above.)
+constexpr long long kMaxCutTokens = (1LL << 28) - 4096;
 
 // -------------------------------------------------------------- row check
 // Whether every page that the row's queries see is there: by `threads` threads, of
@@ -152,7 +155,7 @@ __device__ __forceinline__ void cut_groups(const PagedParams &P, int idx, int &b
     if (r < P.B) {
       int n;
       const int c = paged_queries(P, r, n);
-      if (c > 0) w[q] = Keys(P, n, n + c).n;  // < 2^24 (checked by the caller)
+      if (c > 0) w[q] = Keys(P, n, n + c).n;  // < 2^24, and the sum < 2^31 (kMaxCutTokens)
     }
     sum += w[q];
     top = max(top, w[q]);
@@ -926,7 +929,7 @@ PagedPlan plan_paged(const spec_paged_attention_args *a) {
     p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>({want, (tokens + kGroup - 1) / kGroup, 32})));
     // A few rows are cut by a budget of parts, all items side by side.
     const long long budget = static_cast<long long>(rows_per_sm(a->cache_dtype, a->head_dim, p.oblk)) * kPagedSms / a->heads;
-    if (blocks == 1 && a->B <= kMaxCutRows && budget > a->B) {
+    if (blocks == 1 && a->B <= kMaxCutRows && budget > a->B && tokens <= kMaxCutTokens) {
       p.budget = static_cast<int>(budget);
       p.splits = static_cast<int>(std::min<long long>({32, (tokens + kGroup - 1) / kGroup, budget - a->B + 1}));
     }
