@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(Team<CT == SPEC_E4M3>::kThreads, 1)
     const int wt = tid % 128;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp & 3) << 21);
     const uint32_t s_addr = lane_addr + tile * 128, o_addr = lane_addr + 256 + tile * 128;
-    const float sc = fmaxf(fabsf(P.scale), 1e-37f);  // not zero: a key that is not seen has the score -inf
+    const float sc = fmaxf(fabsf(P.scale), 0x1p-149f);  // not zero: a key that is not seen has the score -inf (what is seen stays below 2^-21)
     const bool minus = P.scale < 0.f, sectors = reinterpret_cast<uintptr_t>(P.out) % 32 == 0;
     bool live = true, checked = false;
     int worked = 0;  // items with keys
