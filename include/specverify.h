@@ -807,7 +807,7 @@ typedef struct {
   int32_t columns;             /* places per row in block_table */
   int32_t page_size, num_pages;
   int32_t window, sinks;
-  float scale;                 /* finite */
+  float scale;                 /* finite, as scale * log2(e) is in fp32 */
   int32_t pad;
   int64_t page_stride, tok_stride;  /* bytes */
   int64_t q_stride[3];         /* elements: row, token, head */

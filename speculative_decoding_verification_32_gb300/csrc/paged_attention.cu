@@ -27,6 +27,7 @@ namespace sv {
 namespace {
 
 constexpr float kPaLazy = 8.f;
+constexpr float kLog2e = 1.442695040888963407f;
 constexpr int kCheckThreads = 256;
 constexpr int kPaJoinThreads = 128;
 // Rows of more tokens are not cut by a budget: cut_groups counts groups of 16 of them
@@ -897,7 +898,7 @@ spec_status check_paged(const spec_paged_attention_args *a) {
   if (a->page_stride < (a->num_pages > 1 ? 16 : 0) || a->page_stride >= 1LL << 40 || a->tok_stride < static_cast<int64_t>(entry) || a->tok_stride >= 1LL << 27) return SPEC_ERR_SHAPE;
   for (int i = 0; i < 3; ++i)
     if (a->q_stride[i] < 0) return SPEC_ERR_SHAPE;
-  if (!std::isfinite(a->scale) || a->window < 0 || a->sinks < 0) return SPEC_ERR_ARG;
+  if (!std::isfinite(a->scale * kLog2e) || a->window < 0 || a->sinks < 0) return SPEC_ERR_ARG;
   return SPEC_OK;
 }
 
@@ -1000,7 +1001,7 @@ spec_status spec_paged_attention(const spec_paged_attention_args *a, void *out, 
   p.table = a->block_table;
   p.q = a->q;
   for (int i = 0; i < 3; ++i) p.qs[i] = a->q_stride[i];
-  p.scale = a->scale * 1.442695040888963407f;
+  p.scale = a->scale * kLog2e;
   p.B = a->B;
   p.N = a->N;
   p.Hq = a->q_heads;
