@@ -33,6 +33,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -1321,15 +1322,19 @@ spec_status spec_sample(const spec_sample_args *a, const spec_sample_out *o, voi
   p.row_stride = a->row_stride;
   p.B = a->B;
   p.V = a->V;
-  // CTAs per row: slices of at most 32 KB, as far as eight go, which stay in shared
-  // memory.  More rows than run side by side that way are cut into fewer slices
-  // (of 2^16 logits at most), which are read a second time: from L2, since what runs
-  // at a time fits (256 rows of 128256 bf16 logits 35 us, and 43 with slices kept;
-  // 64 rows 16 and 15).
+  // CTAs per row: slices of at most 32 KB, as far as eight go.  They stay in shared memory
+  // where they all run at once: with three quarters of what the SMs' memory has room
+  // for, since clusters of eight leave some of it.  Else slices are read again from L2,
+  // which holds what runs at a time, and more rows than run side by side so are cut into
+  // fewer slices (of 2^16 logits at most).  Kept and read again, us: 19 rows of 128256 fp32
+  // logits under min-p 11.7 and 11.8, searched under top-p 0.9 181 and 209; 38 rows
+  // 15.8 and 12.8, 297 and 253; 19 of 200000 16.7 and 12.4, 386 and 310; of bf16 38 rows
+  // 12.2 and 12.0, 97 and 114; 76 16.2 and 14.5, 147 and 174.
   const long long bytes = static_cast<long long>(a->V) * esz;
   int ranks = 1;
   while (ranks < kSmMaxCluster && bytes > ranks * (32LL << 10)) ranks *= 2;
-  const bool keep = static_cast<long long>(a->B) * ranks <= kSmResident;
+  const long long cta = sizeof(SampleShared) + kSmTable + 4096 + (bytes + ranks - 1) / ranks;  // its shared memory, about
+  const bool keep = static_cast<long long>(a->B) * ranks * 4 <= 152 * std::min(4LL, (227LL << 10) / cta) * 3;
   if (!keep) {
     while (ranks > 1 && static_cast<long long>(a->B) * ranks > kSmResident && (a->V + ranks / 2 - 1) / (ranks / 2) <= 1 << 16) ranks /= 2;
   }
