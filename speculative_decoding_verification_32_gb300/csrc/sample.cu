@@ -643,7 +643,7 @@ __device__ __noinline__ void list_token_exact(const SampleParams &P, SampleShare
   ListLaw L = law;
   if (L.use_p && !L.top_k) {
     const Words share = times(L.top_p, exact_mass<BF16, VEC, KEEP>(P, S, -INFINITY, 0));
-    L.need = __float2ll_rn(share.hi * kSmFix) + __float2ll_ru(share.lo * kSmFix);
+    L.need = max(1LL, __float2ll_rn(share.hi * kSmFix) + __float2ll_ru(share.lo * kSmFix));  // (the largest logits stay)
   }
   __syncthreads();  // (the exchange's buffers start anew)
   list_token<BF16, true>(P, S, b, L, Weight{L.M, 0.f}, Slack(P), 0.f);

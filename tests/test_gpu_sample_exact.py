@@ -200,3 +200,28 @@ def test_temperatures_out_of_range(sv, T, mix, V):
     assert not got["row_status"].any() and near.sum() <= 1
     assert torch.equal(got["token"][~near], token[~near])
     assert ((got["prob"].double() - prob).abs() <= 2.0**-17 * prob)[~near].all()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("V", [5, 300, 60000])
+@pytest.mark.parametrize("p", [1e-5, 1e-7, 1e-12, 1e-16, 1e-30, 1e-45])
+def test_top_p_next_to_zero(sv, p, V, dtype):
+    """The largest logits alone are kept, however small top_p is."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(6)
+    B = 6
+    for spread in (0.1, 2.0):
+        x = (spread * torch.randn(B, V, generator=g, device="cuda")).to(getattr(torch, dtype))
+        top = x.amax(1, keepdim=True)
+        at = torch.randint(0, V, (B, 3), generator=g, device="cuda")
+        x.scatter_(1, at, top.expand(B, 3) + (2 if dtype == "bfloat16" else 2.0**-10))
+        u = torch.rand(B, generator=g, device="cuda")
+        for kw in (dict(p=p), dict(p=p, m=0.9), dict(p=p, k=min(4, V - 1))):
+            got = sample(sv, x, u, None, **kw)
+            assert not got["row_status"].any()
+            best = x == x.amax(1, keepdim=True)
+            n = best.sum(1)
+            want = torch.stack([best[b].nonzero()[min(int(float(u[b]) * int(n[b])), int(n[b]) - 1), 0] for b in range(B)])
+            if p < 1e-6 or V < 1000:  # (a larger share of a flat law is more than these)
+                assert torch.equal(got["token"].long(), want)
+                assert (got["prob"] * n - 1).abs().max() <= 2.0**-17
