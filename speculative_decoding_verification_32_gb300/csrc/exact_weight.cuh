@@ -82,6 +82,7 @@ struct ExactWeight {
   float c, cl;          // log2(e) / T, in two words
   const float2 *power;  // kPower32, where lanes read it side by side
 
+  ExactWeight() = default;
   // T finite and > 0, M finite
   __device__ __forceinline__ ExactWeight(float m, float T, const float2 *p) {
     before = T > 0x1p64f ? 0x1p-64f : 1.f;

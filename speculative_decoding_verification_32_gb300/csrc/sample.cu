@@ -118,7 +118,7 @@ struct SampleShared {
   uint32_t min_p_key;
   float floor;                      // what top-p's histogram says
   uint32_t sure;                    // what was decided by fp32 weights holds
-  float M;                          // the row's largest logit
+  ExactWeight exact;                // the row's weights in two words
   Words dpart[2][kSmMaxCluster];    // exact sums: of the CTAs, two in turn, and of this CTA's warps
   Words dwarp[kSmWarps];
   union {
@@ -264,15 +264,17 @@ struct RowSlice {
   }
   __device__ __forceinline__ uint4 operator()(int v) const { return KEEP ? data[v] : load_vector<BF16, VEC>(row, first + v * E, last, policy); }
 };
-__device__ __forceinline__ ExactWeight exact_weight(const SampleParams &P, const SampleShared &S) {
-  return ExactWeight(S.M, P.temperature ? __ldg(P.temperature + blockIdx.x / cluster_nctarank()) : 1.f, power_table());
+__device__ __forceinline__ ExactWeight exact_weight(const SampleShared &S) {
+  ExactWeight w = S.exact;
+  w.power = power_table();  // (known to be shared memory)
+  return w;
 }
 
 // The weights that reach `floor` in vectors from .. to - 1, by one thread.
 template <bool BF16, bool VEC, bool KEEP>
 __device__ __noinline__ Words lane_sum(const SampleParams &P, const SampleShared &S, float floor, int from, int to) {
   const RowSlice<BF16, VEC, KEEP> row(P);
-  const ExactWeight weight = exact_weight(P, S);
+  const ExactWeight weight = exact_weight(S);
   ExactSum<2> sum;
   uint4 q[3];  // the next ones are on their way
 #pragma unroll
@@ -389,7 +391,7 @@ __device__ __noinline__ void draw_exact(const SampleParams &P, SampleShared &S, 
 #pragma unroll
   for (int e = 0; e < E; ++e)
     if (lane == e) l = element<BF16>(q, e);
-  const Words x = exact_weight(P, S)(l, floor);
+  const Words x = exact_weight(S)(l, floor);
   if (lane == find_lane(x, E, f.before, target).lane) {
     P.token[b] = row.first + vec * E + lane;
     if (P.prob) P.prob[b] = x.hi / Z.hi;
@@ -410,7 +412,7 @@ __device__ __forceinline__ int listed_at(const SampleShared &S, int nseg, int se
 // weights that an integer holds few bits of, or none.
 __device__ __noinline__ void draw_small(const SampleParams &P, SampleShared &S, int b, int nseg, int seglen, int total) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const ExactWeight weight = exact_weight(P, S);
+  const ExactWeight weight = exact_weight(S);
   // a warp's places lie side by side
   const int each = (total + kSmThreads - 1) / kSmThreads * 32, a0 = min(total, warp * each), a1 = min(total, a0 + each);
   auto weigh = [&](int at) {
@@ -492,7 +494,7 @@ __device__ __forceinline__ bool list_token(const SampleParams &P, SampleShared &
       const float l = smp_from_key(key[i]);
       float y;
       if constexpr (EXACT) {
-        const Words x = ExactWeight(L.M, L.T, power_table())(l, -INFINITY);
+        const Words x = exact_weight(S)(l, -INFINITY);
         y = x.hi;
         w[i] = __float2ll_rn(y * kSmFix) + __float2ll_rn(x.lo * kSmFix);
       } else {
@@ -760,7 +762,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     return;
   }
   weight.M = M;
-  if (tid == 0) S.M = M;
+  if (tid == kSmThreads - 1) S.exact = ExactWeight(M, T, power_table());  // (800 cycles, which whoever needs it would wait for)
   // temperatures whose reciprocals or differences leave fp32's range: exact weights alone
   const bool far = !(T >= 0x1p-64f && T <= 0x1p64f);
   const Slack slack(P);
