@@ -665,7 +665,7 @@ spec_status spec_token_logprobs(const spec_logprobs_args *args, const spec_logpr
  * pool described as a spec_kv_cache of one row of pages * page_size slots,
  * rows = B * N, row_stride = 0 and kv_len = the slot map, spec_kv_append with
  * N = 1 writes each token of the pass to its slot (and leaves those whose slot is
- * -1 alone, as SPEC_ROW_BAD_SLOT).
+ * -1 alone, as SPEC_ROW_BAD_SLOT); more than 65535 tokens are appended in pieces.
  *
  * spec_page_plan -- block tables and slot maps from the rows' lengths, on the
  * device, once per pass ("Speculative Decoding: Draft, Verify, and Correct",

@@ -25,10 +25,10 @@
 // integers (w 2^44), and every decision that hangs on one (where u falls, which side of
 // top-p's border a logit is on) is held against a bound on the sums' errors (Slack).
 // One that lies nearer is made again from weights in two words (exact_weight.cuh), which
-// takes the row 6 us (2048 tokens) to 13 (131072, eight CTAs; 25 with two).  How often
+// takes the row 6 us (2048 tokens) to 12 (131072, eight CTAs; 23 with two).  How often
 // depends on the law: its tokens' borders, 2 slack wide each.  Of rows of 128256
 // tokens drawn from whole 4% (standard deviation 3, and some tokens 9 above) and 27%
-// (1), of 32000 under top-p 0.95 8%, under min-p 0.02 as well or top-k 50 0 to 0.2%.
+// (1), of 32000 under top-p 0.95 10%, under min-p 0.02 as well or top-k 50 0 to 0.2%.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
