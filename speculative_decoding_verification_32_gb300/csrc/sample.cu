@@ -1328,7 +1328,10 @@ spec_status spec_sample(const spec_sample_args *a, const spec_sample_out *o, voi
   // where they all run at once: with three quarters of what the SMs' memory has room
   // for, since clusters of eight leave some of it.  Else slices are read again from L2,
   // which holds what runs at a time, and more rows than run side by side so are cut into
-  // fewer slices (of 2^16 logits at most).  Kept and read again, us: 19 rows of 128256 fp32
+  // fewer slices: of 2^16 logits at most (256 rows of 128256 under top-p and min-p 26 us,
+  // with 2^15 32), and of 2^15 where there is no truncation, since some of many rows'
+  // sums have to be made again (256 rows of bf16 45 us, with 2^16 53; 300 of fp32 63 and
+  // 77).  Kept and read again, us: 19 rows of 128256 fp32
   // logits under min-p 11.7 and 11.8, searched under top-p 0.9 181 and 209; 38 rows
   // 15.8 and 12.8, 297 and 253; 19 of 200000 16.7 and 12.4, 386 and 310; of bf16 38 rows
   // 12.2 and 12.0, 97 and 114; 76 16.2 and 14.5, 147 and 174.
@@ -1338,7 +1341,8 @@ spec_status spec_sample(const spec_sample_args *a, const spec_sample_out *o, voi
   const long long cta = sizeof(SampleShared) + kSmTable + 4096 + (bytes + ranks - 1) / ranks;  // its shared memory, about
   const bool keep = static_cast<long long>(a->B) * ranks * 4 <= 152 * std::min(4LL, (227LL << 10) / cta) * 3;
   if (!keep) {
-    while (ranks > 1 && static_cast<long long>(a->B) * ranks > kSmResident && (a->V + ranks / 2 - 1) / (ranks / 2) <= 1 << 16) ranks /= 2;
+    const int most = a->top_k || a->top_p || a->min_p ? 1 << 16 : 1 << 15;
+    while (ranks > 1 && static_cast<long long>(a->B) * ranks > kSmResident && (a->V + ranks / 2 - 1) / (ranks / 2) <= most) ranks /= 2;
   }
   const int unit = 16 / esz;
   p.slice = ((a->V + ranks - 1) / ranks + unit - 1) / unit * unit;
