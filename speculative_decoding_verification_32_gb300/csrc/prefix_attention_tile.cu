@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(Roles<CT == SPEC_E4M3>::kThreads, 1) attn_tile
           grow = En - E;
           E = En;
         }
-        sc = fmaxf(sc, 1e-37f);  // not zero: a token that is not seen has the score -inf
+        sc = fmaxf(sc, 0x1p-149f);  // not zero: a token that is not seen has the score -inf (what is seen stays below 2^-21)
         live = __all_sync(FULL_MASK, live);
         if (!live) break;
         tc_fence_after();
